@@ -506,6 +506,126 @@ TREE_ATTN_API unsigned long long tree_attn_set_wait_limit_ns(unsigned long long 
  */
 TREE_ATTN_API int tree_attn_set_early_prefix_loads(int enable);
 
+/*
+ * The 8-bit paged cache.  A row (one token, one KV head) of d bf16 values x is
+ * held as d e4m3 codes c and one exponent s, x ~ c * 2^s:
+ *   s      the smallest integer with max|x| <= 448 * 2^s over the row's finite
+ *          values, held within [-56, 40] (-56 for a row without finite
+ *          non-zero values); stored as the byte s + 127.
+ *   c      x * 2^-s rounded to e4m3, nearest even; NaN stays NaN, values
+ *          beyond +-448 * 2^s (infinities) become +-448.
+ * Pools: k_pages, v_pages uint8 [num_pages][Hkv][page_size][d] (codes) and
+ * k_scales, v_scales uint8 [num_pages][Hkv][page_size]; block_table as for
+ * tree_attn_verify.  Reading back (c * 2^s in bf16) adds no rounding.
+ * (Counterpart of the paged, persistent KV handling the review's Referee
+ * Report summary names; the pages give no 8-bit form.)
+ *
+ * Shapes for all entries below: Hkv <= 65535, d in {64, 128}, page_size in
+ * {16, 32, 64, 128}, max_pages_per_seq >= 1, num_pages >= 1 and
+ * num_pages*Hkv*page_size < 2^31; pools and bf16 tensors 16-byte aligned.
+ * Slots that no call writes keep their bytes.
+ *
+ * tree_kv_append_fp8 -- quantise new tokens' K/V as they are written.
+ *   k, v         bf16 [N][Hkv][d], packed: sequence b's new tokens are rows
+ *                cu_seqlens[b] .. cu_seqlens[b+1] - 1.  Token and head strides
+ *                are in elements, multiples of 8 (slices of a fused
+ *                projection's output are fine); the d values are contiguous.
+ *   cu_seqlens   int32 [B+1], 0 <= ascending <= N; rows outside
+ *                [cu_seqlens[0], cu_seqlens[B]) are ignored.
+ *   seq_lens     int32 [B]: tokens held already; new token j of sequence b
+ *                goes to logical position seq_lens[b] + j, through pages the
+ *                caller mapped and that no other sequence of the call writes.
+ *   seq_lens_out nullable int32 [B]: seq_lens[b] + the new tokens; must not
+ *                be seq_lens itself (-2)
+ *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN (cu_seqlens out of
+ *                order or range, a negative length, a position past the block
+ *                table), _BAD_PAGE; rows that fail are skipped.
+ * Returns 0, -1, -2, -3, -5.
+ */
+TREE_ATTN_API int tree_kv_append_fp8(
+    uint8_t *k_pages, uint8_t *v_pages, uint8_t *k_scales, uint8_t *v_scales,
+    const int32_t *block_table, int max_pages_per_seq, const int32_t *seq_lens,
+    const int32_t *cu_seqlens, const uint16_t *k, const uint16_t *v, long long k_token_stride,
+    long long k_head_stride, long long v_token_stride, long long v_head_stride,
+    int32_t *seq_lens_out, int B, int N, int Hkv, int d, int page_size, int num_pages,
+    int32_t *status, void *stream);
+
+/*
+ * tree_kv_commit_fp8 -- tree_kv_commit into the 8-bit cache: path node
+ * accept_path[b][k] (k < accept_len[b]) of the tree buffers tree_k, tree_v
+ * (bf16 [B][T][Hkv][d]) is quantised into logical position seq_lens[b] + k.
+ * seq_lens_out, status and return codes as tree_kv_commit.
+ */
+TREE_ATTN_API int tree_kv_commit_fp8(uint8_t *k_pages, uint8_t *v_pages, uint8_t *k_scales,
+                                     uint8_t *v_scales, const int32_t *block_table,
+                                     int max_pages_per_seq, const int32_t *seq_lens,
+                                     const int32_t *accept_path, const int32_t *accept_len,
+                                     const uint16_t *tree_k, const uint16_t *tree_v,
+                                     int32_t *seq_lens_out, int B, int Hkv, int d, int T,
+                                     int page_size, int num_pages, int32_t *status, void *stream);
+
+/*
+ * tree_kv_read_fp8 -- read a stretch of every sequence back as bf16.
+ *   starts       nullable int32 [B] (NULL: 0): first position of sequence b
+ *   cu_seqlens   int32 [B+1]: output row cu_seqlens[b] + j is position
+ *                starts[b] + j of sequence b
+ *   k_out, v_out bf16 [N][Hkv][d]; rows outside every sequence's range, and
+ *                rows that fail, keep what they held
+ *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN, _BAD_PAGE.
+ * Returns 0, -1, -2, -3, -5.
+ */
+TREE_ATTN_API int tree_kv_read_fp8(const uint8_t *k_pages, const uint8_t *v_pages,
+                                   const uint8_t *k_scales, const uint8_t *v_scales,
+                                   const int32_t *block_table, int max_pages_per_seq,
+                                   const int32_t *starts, const int32_t *cu_seqlens,
+                                   uint16_t *k_out, uint16_t *v_out, int B, int N, int Hkv, int d,
+                                   int page_size, int num_pages, int32_t *status, void *stream);
+
+/*
+ * tree_attn_verify_fp8 -- split tree attention over the 8-bit cache: as
+ * tree_attn_verify with every committed row c * 2^s (the tree tokens stay
+ * bf16), T = 1 being plain decoding.  Scale bytes of committed rows must lie
+ * in [71, 167] (what the entries above write).
+ *   mask         uint64 [T] (mask_stride 0) or [B][T] (mask_stride T), or NULL:
+ *   parents      int32 [T] (parents_stride 0) or [B][T] (parents_stride T), from
+ *                which the masks are built on the device and written to
+ *                mask_out when that is not NULL.  Exactly one of mask and
+ *                parents is given (both: -2, neither: -1).
+ *   workspace    tree_attn_workspace_size(...) bytes, as for tree_attn_verify.
+ * tree_attn_set_early_prefix_loads does not apply; the wait limit does.
+ * Other arguments, statuses and return codes as tree_attn_verify.
+ */
+TREE_ATTN_API int tree_attn_verify_fp8(
+    const uint16_t *q, const uint8_t *k_pages, const uint8_t *v_pages, const uint8_t *k_scales,
+    const uint8_t *v_scales, const int32_t *block_table, int max_pages_per_seq,
+    const int32_t *seq_lens, const uint16_t *tree_k, const uint16_t *tree_v, const uint64_t *mask,
+    int mask_stride, const int32_t *parents, int parents_stride, uint64_t *mask_out, uint16_t *out,
+    float *lse, int B, int Hq, int Hkv, int d, int T, int page_size, int num_pages,
+    float softmax_scale, void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * tree_attn_prefill -- causal attention over whole prompts, packed:
+ * for token i of sequence b (rows cu_seqlens[b] .. cu_seqlens[b+1] - 1) and
+ * query head h (KV head h / (Hq / Hkv)), the keys are the sequence's tokens up
+ * to and including i.  This is the pass that fills a cache before drafts are
+ * verified against it.
+ *   q            bf16 [N][Hq][d], k, v bf16 [N][Hkv][d]; token and head strides
+ *                in elements, multiples of 8; the d values are contiguous
+ *   cu_seqlens   int32 [B+1], 0 <= ascending <= N; empty sequences are fine
+ *   out          bf16 [N][Hq][d], lse fp32 [N][Hq] (natural log), dense; rows
+ *                outside every sequence keep what they held
+ *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN (cu_seqlens out of order
+ *                or range: that sequence's rows are not written), _TIMEOUT
+ * d in {64, 128}, Hq % Hkv == 0.  No workspace.  Returns 0, -1, -2, -3, -5.
+ */
+TREE_ATTN_API int tree_attn_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                    long long q_token_stride, long long q_head_stride,
+                                    long long k_token_stride, long long k_head_stride,
+                                    long long v_token_stride, long long v_head_stride,
+                                    const int32_t *cu_seqlens, uint16_t *out, float *lse, int B,
+                                    int N, int Hq, int Hkv, int d, float softmax_scale,
+                                    int32_t *status, void *stream);
+
 /* Library version, as major*10000 + minor*100 + patch. */
 TREE_ATTN_API int tree_attn_version(void);
 

@@ -42,3 +42,10 @@ from ._lib import (  # noqa: F401
     set_early_prefix_loads,
     DEFAULT_WAIT_NS,
 )
+from ._serving import (  # noqa: F401
+    kv_append_fp8,
+    kv_commit_fp8,
+    kv_read_fp8,
+    verify_fp8,
+    prefill,
+)

@@ -56,6 +56,11 @@ EXPORTED = (
     "tree_accept_commit",
     "tree_attn_set_wait_limit_ns",
     "tree_attn_set_early_prefix_loads",
+    "tree_kv_append_fp8",
+    "tree_kv_commit_fp8",
+    "tree_kv_read_fp8",
+    "tree_attn_verify_fp8",
+    "tree_attn_prefill",
 )
 
 
@@ -142,6 +147,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tree_attn_set_wait_limit_ns.restype = ctypes.c_ulonglong
     lib.tree_attn_set_early_prefix_loads.argtypes = [i32]
     lib.tree_attn_set_early_prefix_loads.restype = i32
+    i64 = ctypes.c_longlong
+    lib.tree_kv_append_fp8.argtypes = [vp] * 5 + [i32] + [vp] * 4 + [i64] * 4 + [vp] + [i32] * 6 + [vp, vp]
+    lib.tree_kv_append_fp8.restype = i32
+    lib.tree_kv_commit_fp8.argtypes = [vp] * 5 + [i32] + [vp] * 6 + [i32] * 6 + [vp, vp]
+    lib.tree_kv_commit_fp8.restype = i32
+    lib.tree_kv_read_fp8.argtypes = [vp] * 5 + [i32] + [vp] * 4 + [i32] * 6 + [vp, vp]
+    lib.tree_kv_read_fp8.restype = i32
+    lib.tree_attn_verify_fp8.argtypes = ([vp] * 6 + [i32] + [vp] * 4 + [i32, vp, i32] + [vp] * 3
+                                         + [i32] * 7 + [f32, vp, sz, vp, vp])
+    lib.tree_attn_verify_fp8.restype = i32
+    lib.tree_attn_prefill.argtypes = [vp] * 3 + [i64] * 6 + [vp] * 3 + [i32] * 5 + [f32, vp, vp]
+    lib.tree_attn_prefill.restype = i32
     if path == LIB_PATH:
         _lib = lib
     return lib

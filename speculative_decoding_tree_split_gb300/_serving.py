@@ -1,0 +1,306 @@
+"""Python calls around verification: the 8-bit paged cache (write, commit, read
+back), verification over it, and causal attention over whole prompts.
+
+As in ``_lib``: arguments are checked, then handed to the library; there is no
+fallback.  Every call runs on the device its tensors are on (all on one), on
+``stream`` or that device's current stream.  Results and workspaces that a call
+makes itself belong to the stream it runs on.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from ._lib import _BITS64, TreeAttnError, load
+
+_BF16 = torch.bfloat16
+_I32 = torch.int32
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _tensor(t, name: str, dtypes, ndim: int, dev, dense: bool = True):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+
+
+def _status(status, dev):
+    if status is None:
+        return None
+    _tensor(status, "status", (_I32,), status.dim() if isinstance(status, torch.Tensor) else 1, dev)
+    if status.numel() < 1:
+        raise ValueError("status must hold one int32")
+    return status.data_ptr()
+
+
+class _Place:
+    """The device and stream of one call, and what is allocated there."""
+
+    def __init__(self, dev: torch.device, stream):
+        self.dev = dev
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        self.current = torch.cuda.current_stream(dev)
+        self.stream = self.current if stream is None else stream
+        self.foreign = self.stream != self.current
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        if not self.foreign:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        # Taken from the pool of the stream that writes it, so that it cannot
+        # be memory that work queued on the current stream still reads; the
+        # caller goes on to use it on the current stream.
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=self.dev)
+        t.record_stream(self.current)
+        return t
+
+    def call(self, name: str, *args) -> int:
+        fn = getattr(load(), name)
+        if self.dev.index == torch.cuda.current_device():
+            return fn(*args)
+        with torch.cuda.device(self.dev):
+            return fn(*args)
+
+    def run(self, name: str, *args) -> None:
+        rc = self.call(name, *args, self.stream.cuda_stream)
+        if rc != 0:
+            raise TreeAttnError(name, rc)
+
+
+def _pools(k_pages, v_pages, k_scales, v_scales, block_table):
+    """Checks the cache's tensors; returns (device, num_pages, Hkv, P, d)."""
+    dev = k_pages.device if isinstance(k_pages, torch.Tensor) else None
+    _tensor(k_pages, "k_pages", _CODES, 4, dev)
+    _tensor(v_pages, "v_pages", _CODES, 4, dev)
+    _tensor(k_scales, "k_scales", (torch.uint8,), 3, dev)
+    _tensor(v_scales, "v_scales", (torch.uint8,), 3, dev)
+    _tensor(block_table, "block_table", (_I32,), 2, dev)
+    shape = k_pages.shape
+    if v_pages.shape != shape or k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
+        raise ValueError("k_pages, v_pages, k_scales and v_scales disagree on their sizes")
+    return dev, shape[0], shape[1], shape[2], shape[3]
+
+
+def _rows(t, name: str, dev, heads: Optional[int], d: Optional[int]):
+    """Checks packed rows [N][H][d] with d contiguous; returns (token, head)
+    strides, 0 where there is one row of that kind."""
+    _tensor(t, name, (_BF16,), 3, dev, dense=False)
+    n, h, e = t.shape
+    if (heads is not None and h != heads) or (d is not None and e != d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [N, {heads}, {d}]")
+    ts, hs, es = t.stride()
+    if es != 1 and e > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return (ts if n > 1 else 0), (hs if h > 1 else 0)
+
+
+def _vector(t, name: str, n: int, dev):
+    _tensor(t, name, (_I32,), 1, dev)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+
+
+def kv_append_fp8(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_seqlens, k, v, *,
+                  seq_lens_out=None, status=None, stream=None) -> torch.Tensor:
+    """Quantise new tokens' K/V into the 8-bit paged cache.
+
+    k_pages / v_pages uint8 or float8_e4m3fn [num_pages][Hkv][P][d], k_scales /
+    v_scales uint8 [num_pages][Hkv][P]; k, v bf16 [N][Hkv][d] packed by
+    cu_seqlens int32 [B + 1] (token and head strides free, e.g. slices of a
+    fused projection); token j of sequence b goes to position seq_lens[b] + j.
+    Returns seq_lens_out (seq_lens plus the new tokens).
+    """
+    dev, num_pages, Hkv, P, d = _pools(k_pages, v_pages, k_scales, v_scales, block_table)
+    B = block_table.shape[0]
+    _vector(seq_lens, "seq_lens", B, dev)
+    _vector(cu_seqlens, "cu_seqlens", B + 1, dev)
+    k_ts, k_hs = _rows(k, "k", dev, Hkv, d)
+    v_ts, v_hs = _rows(v, "v", dev, Hkv, d)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v disagree on the number of rows")
+    at = _Place(dev, stream)
+    if seq_lens_out is None:
+        seq_lens_out = at.empty(B, _I32)
+    else:
+        _vector(seq_lens_out, "seq_lens_out", B, dev)
+    at.run("tree_kv_append_fp8", k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+           v_scales.data_ptr(), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
+           cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), k_ts, k_hs, v_ts, v_hs,
+           seq_lens_out.data_ptr(), B, k.shape[0], Hkv, d, P, num_pages, _status(status, dev))
+    return seq_lens_out
+
+
+def kv_commit_fp8(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, accept_path,
+                  accept_len, tree_k, tree_v, *, seq_lens_out=None, status=None,
+                  stream=None) -> torch.Tensor:
+    """Quantise each sequence's accepted path (``greedy_accept``) into the 8-bit
+    cache at positions seq_lens[b] + k.  tree_k / tree_v bf16 [B][T][Hkv][d].
+    Returns seq_lens_out (seq_lens + accept_len)."""
+    dev, num_pages, Hkv, P, d = _pools(k_pages, v_pages, k_scales, v_scales, block_table)
+    B = block_table.shape[0]
+    _vector(seq_lens, "seq_lens", B, dev)
+    _vector(accept_len, "accept_len", B, dev)
+    _tensor(accept_path, "accept_path", (_I32,), 2, dev)
+    _tensor(tree_k, "tree_k", (_BF16,), 4, dev)
+    _tensor(tree_v, "tree_v", (_BF16,), 4, dev)
+    T = accept_path.shape[1]
+    if (accept_path.shape[0] != B or tuple(tree_k.shape) != (B, T, Hkv, d)
+            or tree_v.shape != tree_k.shape):
+        raise ValueError("accept_path, tree_k, tree_v and the cache disagree on their sizes")
+    at = _Place(dev, stream)
+    if seq_lens_out is None:
+        seq_lens_out = at.empty(B, _I32)
+    else:
+        _vector(seq_lens_out, "seq_lens_out", B, dev)
+    at.run("tree_kv_commit_fp8", k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+           v_scales.data_ptr(), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
+           accept_path.data_ptr(), accept_len.data_ptr(), tree_k.data_ptr(), tree_v.data_ptr(),
+           seq_lens_out.data_ptr(), B, Hkv, d, T, P, num_pages, _status(status, dev))
+    return seq_lens_out
+
+
+def kv_read_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens, n_tokens: int, *,
+                starts=None, k_out=None, v_out=None, status=None,
+                stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Read cached rows back as bf16 (exactly the values they stand for): output
+    row cu_seqlens[b] + j is position starts[b] + j (starts None: 0) of
+    sequence b.  Returns (k, v), bf16 [n_tokens][Hkv][d]; rows outside every
+    sequence's range keep what k_out / v_out held (are uninitialised when the
+    call makes them)."""
+    dev, num_pages, Hkv, P, d = _pools(k_pages, v_pages, k_scales, v_scales, block_table)
+    B, n = block_table.shape[0], int(n_tokens)
+    if n < 0:
+        raise ValueError("n_tokens must not be negative")
+    _vector(cu_seqlens, "cu_seqlens", B + 1, dev)
+    if starts is not None:
+        _vector(starts, "starts", B, dev)
+    at = _Place(dev, stream)
+    outs = []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = at.empty((n, Hkv, d), _BF16)
+        else:
+            _tensor(t, name, (_BF16,), 3, dev)
+            if tuple(t.shape) != (n, Hkv, d):
+                raise ValueError(f"{name} must have shape {(n, Hkv, d)}")
+        outs.append(t)
+    at.run("tree_kv_read_fp8", k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+           v_scales.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+           None if starts is None else starts.data_ptr(), cu_seqlens.data_ptr(),
+           outs[0].data_ptr(), outs[1].data_ptr(), B, n, Hkv, d, P, num_pages,
+           _status(status, dev))
+    return outs[0], outs[1]
+
+
+def verify_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, tree_k, tree_v, *,
+               mask=None, parents=None, mask_out=None, out=None, lse=None, workspace=None,
+               status=None, softmax_scale: Optional[float] = None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Split tree attention over the 8-bit paged cache (T = 1: plain decoding).
+
+    As ``verify`` / ``verify_tree`` with the committed rows in 8 bits and the
+    tree tokens in bf16; give the tree either as ``mask`` (int64 / uint64 bits,
+    [T] or [B][T]) or as ``parents`` (int32, [T] or [B][T]).  Returns (out, lse).
+    """
+    dev, num_pages, Hkv, P, d = _pools(k_pages, v_pages, k_scales, v_scales, block_table)
+    for t, name in ((q, "q"), (tree_k, "tree_k"), (tree_v, "tree_v")):
+        _tensor(t, name, (_BF16,), 4, dev)
+    B, T, Hq, _ = q.shape
+    _vector(seq_lens, "seq_lens", B, dev)
+    if (q.shape[3] != d or tuple(tree_k.shape) != (B, T, Hkv, d) or tree_v.shape != tree_k.shape
+            or block_table.shape[0] != B):
+        raise ValueError("inconsistent tensor shapes")
+    if (mask is None) == (parents is None):
+        raise ValueError("give exactly one of mask and parents")
+    tree, dtypes, name = (mask, _BITS64, "mask") if parents is None else (parents, (_I32,), "parents")
+    _tensor(tree, name, dtypes, tree.dim() if isinstance(tree, torch.Tensor) else 1, dev)
+    if tuple(tree.shape) not in ((T,), (B, T)):
+        raise ValueError(f"{name} must have shape [T] or [B][T]")
+    stride = T if tree.dim() == 2 else 0
+    if mask_out is not None:
+        if parents is None:
+            raise ValueError("mask_out goes with parents")
+        _tensor(mask_out, "mask_out", _BITS64, tree.dim(), dev)
+        if mask_out.shape != tree.shape:
+            raise ValueError("mask_out must have the shape of parents")
+    at = _Place(dev, stream)
+    if out is None:
+        out = at.empty(q.shape, _BF16)
+    else:
+        _tensor(out, "out", (_BF16,), 4, dev)
+    if lse is None:
+        lse = at.empty((B, T, Hq), torch.float32)
+    else:
+        _tensor(lse, "lse", (torch.float32,), 3, dev)
+    if out.shape != q.shape or tuple(lse.shape) != (B, T, Hq):
+        raise ValueError("out and lse must have shapes [B][T][Hq][d] and [B][T][Hq]")
+    if workspace is None:
+        need = at.call("tree_attn_workspace_size", B, Hq, Hkv, d, T, 0, P)
+        workspace = at.empty(max(need, 256), torch.uint8)
+    else:
+        _tensor(workspace, "workspace", (torch.uint8,), 1, dev)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    at.run("tree_attn_verify_fp8", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+           k_scales.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+           seq_lens.data_ptr(), tree_k.data_ptr(), tree_v.data_ptr(),
+           None if mask is None else mask.data_ptr(), stride if parents is None else 0,
+           None if parents is None else parents.data_ptr(), 0 if parents is None else stride,
+           None if mask_out is None else mask_out.data_ptr(), out.data_ptr(), lse.data_ptr(), B,
+           Hq, Hkv, d, T, P, num_pages, float(softmax_scale), workspace.data_ptr(),
+           workspace.numel(), _status(status, dev))
+    return out, lse
+
+
+def prefill(q, k, v, cu_seqlens, *, out=None, lse=None, status=None,
+            softmax_scale: Optional[float] = None,
+            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention over packed prompts of different lengths.
+
+    q bf16 [N][Hq][d], k and v bf16 [N][Hkv][d] (token and head strides free),
+    cu_seqlens int32 [B + 1]: sequence b is rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1.  Returns (out [N][Hq][d] bf16, lse [N][Hq] fp32);
+    rows outside every sequence keep what out / lse held (are uninitialised
+    when the call makes them).
+    """
+    dev = q.device if isinstance(q, torch.Tensor) else None
+    q_ts, q_hs = _rows(q, "q", dev, None, None)
+    N, Hq, d = q.shape
+    k_ts, k_hs = _rows(k, "k", dev, None, d)
+    Hkv = k.shape[1]
+    v_ts, v_hs = _rows(v, "v", dev, Hkv, d)
+    if k.shape[0] != N or v.shape[0] != N:
+        raise ValueError("q, k and v disagree on the number of rows")
+    _tensor(cu_seqlens, "cu_seqlens", (_I32,), 1, dev)
+    if cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must have B + 1 entries")
+    at = _Place(dev, stream)
+    if out is None:
+        out = at.empty((N, Hq, d), _BF16)
+    else:
+        _tensor(out, "out", (_BF16,), 3, dev)
+    if lse is None:
+        lse = at.empty((N, Hq), torch.float32)
+    else:
+        _tensor(lse, "lse", (torch.float32,), 2, dev)
+    if tuple(out.shape) != (N, Hq, d) or tuple(lse.shape) != (N, Hq):
+        raise ValueError("out and lse must have shapes [N][Hq][d] and [N][Hq]")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    at.run("tree_attn_prefill", q.data_ptr(), k.data_ptr(), v.data_ptr(), q_ts, q_hs, k_ts, k_hs,
+           v_ts, v_hs, cu_seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+           cu_seqlens.shape[0] - 1, N, Hq, Hkv, d, float(softmax_scale), _status(status, dev))
+    return out, lse
