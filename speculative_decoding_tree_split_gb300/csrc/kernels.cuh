@@ -43,6 +43,7 @@ struct VerifyArgs {
     int ovh;  // overhead slots per unit on the work line (the kernel selector's)
     unsigned long long wait_ns;  // limit of a pipeline wait in the prefix pass
     int early;  // plan and first committed-prefix loads before the dependency wait
+    int copies; // row copies per partial the merge finds; 0: the kernel selector's
 };
 
 // Enqueue the explicit-mask builder: dense[b][t][p] for p < dense_cols and
@@ -69,5 +70,8 @@ cudaError_t launch_prefix_early(const VerifyArgs& a, const void* tmap_k, const v
 
 // Enqueue the suffix pass + merge (reads the partials in a.ws).
 cudaError_t launch_merge(const VerifyArgs& a, cudaStream_t stream);
+
+// The host's limit of a pipeline wait (tree_attn_set_wait_limit_ns).
+unsigned long long wait_limit_ns();
 
 }  // namespace treeattn

@@ -155,6 +155,8 @@ int prefix_impl(VerifyArgs& a, const uint16_t* k_pages, const uint16_t* v_pages,
 
 }  // namespace
 
+unsigned long long treeattn::wait_limit_ns() { return g_wait_ns.load(); }
+
 extern "C" {
 
 int tree_attn_version(void) { return 10200; }

@@ -1,7 +1,33 @@
-// verify_fp8.cu -- split tree attention over the 8-bit paged cache.
+// verify_fp8.cu -- split tree attention over the 8-bit paged cache: the prefix
+// pass over committed rows (this file), then the tree pass and log-sum-exp
+// merge of kernels.cu on the partials it leaves.
+//
+// For a unit (sequence, KV head) with R query rows (tree nodes x grouped heads)
+// and keys j held as codes with scales:
+//   x_rj = c F_j <q_r, k_j>,  F_j = 2^(scale of k_j),  c = softmax scale log2(e)
+//   out_r = sum_j 2^x_rj 2^(scale of v_j) v_j / sum_j 2^x_rj.
+// The 8-bit codes go to the tensor cores as they are, so the other operand has
+// to be 8 bits as well, and both products are turned round to make that cheap:
+//   S^T = K Q^T     (128 keys x rows; A = K tile, B = Q)
+//   O^T += V^T P^T  (d x rows;        A = V tile, B = P)
+// * A query row and a row of probabilities enter as two e4m3 rows each, the
+//   rounded value and sixteen times what is left of it: together nine
+//   significant bits, as much as bf16 has.  Both halves are columns of the same
+//   B operand, so a product is still four instructions (d = 128).
+// * A TMEM lane is a key, so a key's scales are scalars of the thread that
+//   holds it, and the softmax has no idle lanes however few rows there are.
+// * The value scale joins the exponent: e = x + scale of v_j, p = 2^(e - ref),
+//   O sums p v, and the row's sum takes p 2^-(scale of v_j).
+// * A row's maximum would need the 128 lanes to meet; instead each block only
+//   asks whether any e exceeds its row's reference by more than 8 (p must stay
+//   below 448).  If one does, the references move and O is rescaled (the first
+//   block of a segment always does).
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -11,11 +37,22 @@
 #include "launch.cuh"
 #include "layout.h"
 #include "ptx.cuh"
+#include "tma_host.h"
 
 namespace treeattn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kKeys = 2 * kChunk;    // keys of a block
+constexpr int kSoftWarps = 8;        // two warpgroups, half of the rows each
+constexpr int kWarpTma = 8, kWarpMma = 9;
+constexpr int kThreads = 32 * 10;
+// References sit 2^kRoom below what p may reach without the row moving them:
+// a moved reference puts its row's largest p at 2^4, and p may grow to 2^8.
+constexpr float kTop = 4.f, kMost = 8.f;
+// Work-line slots that stand for a segment's fixed cost.
+constexpr int kOverhead = 6;
 
 __device__ __forceinline__ void report(int32_t* status, int code) {
     if (status != nullptr) atomicCAS(status, 0, code);
@@ -23,121 +60,830 @@ __device__ __forceinline__ void report(int32_t* status, int code) {
 
 struct Fp8Args {
     const uint16_t* q;
-    const uint8_t* k_pages;
-    const uint8_t* v_pages;
     const uint8_t* k_scales;
     const uint8_t* v_scales;
     const int32_t* block_table;
     const int32_t* seq_lens;
-    const uint16_t* tree_k;
-    const uint16_t* tree_v;
-    const uint64_t* mask;
-    int mask_stride;
-    const int32_t* parents;
-    int parents_stride;
-    uint64_t* mask_out;
-    uint16_t* out;
-    float* lse;
+    float* ws;
     int32_t* status;
-    int B, Hq, Hkv, G, T, P, max_pages, num_pages;
+    int B, Hq, Hkv, G, T, M, RB, P, max_pages, num_pages, n_ctas, ovh;
     float scale_log2;
+    unsigned long long wait_ns;
 };
 
-// One warp per (sequence, tree node, query head): a running softmax over the
-// committed rows and then the tree rows.
+// Shared memory and TMEM of a CTA for D-wide heads and tiles of up to R rows.
+template <int D, int R>
+struct Shape {
+    static constexpr int N = 2 * R;                   // columns: both halves of each row
+    static constexpr int HALF = R / 2;                // rows of a warpgroup
+    static constexpr int TILE = kKeys * D;            // K (or V) codes of a block
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int Q_BYTES = N * D < 1024 ? 1024 : N * D;
+    static constexpr int P_ATOMS = N > 128 ? 2 : 1;   // 128-byte columns of the P tile
+    static constexpr int P_ATOM = kKeys * 128;
+    static constexpr int P_BYTES = P_ATOMS * P_ATOM;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_P = OFF_Q + (Q_BYTES + 1023) / 1024 * 1024;
+    static constexpr int OFF_STAGE = OFF_P + 2 * P_BYTES;
+    static constexpr int SMALL = 8 * 1024;            // scales, references, barriers
+    static constexpr int FIT = (227 * 1024 - 1024 - SMALL - OFF_STAGE) / STAGE;
+    static constexpr int NS = FIT > 6 ? 6 : FIT;      // ring depth
+    static constexpr int OFF_SCALE = OFF_STAGE + NS * STAGE;  // [NS][K, V][128]
+    static constexpr int OFF_REF = OFF_SCALE + NS * 2 * kKeys;  // reference of each row
+    static constexpr int OFF_ALPHA = OFF_REF + R * 4;           // its last change, as a factor
+    static constexpr int OFF_WMAX = OFF_ALPHA + R * 4;          // [4][R]: maxima / sums by warp
+    static constexpr int OFF_MISC = OFF_WMAX + 4 * R * 4;
+    static constexpr int OFF_BAR = OFF_MISC + 64;
+    // barriers
+    static constexpr int KV_FULL = 0;
+    static constexpr int KV_EMPTY = NS;
+    static constexpr int S_FULL = 2 * NS;
+    static constexpr int S_FREE = S_FULL + 2;
+    static constexpr int P_FULL = S_FULL + 4;
+    static constexpr int P_FREE = S_FULL + 6;
+    static constexpr int O_FULL = S_FULL + 8;
+    static constexpr int O_FREE = S_FULL + 9;
+    static constexpr int Q_FULL = S_FULL + 10;
+    static constexpr int CHECK = S_FULL + 11;  // the softmax warps' vote on each block
+    static constexpr int MEET = S_FULL + 12;   // the softmax warps meet
+    static constexpr int DRAIN = S_FULL + 13;
+    static constexpr int NBAR = S_FULL + 14;
+    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
+    // TMEM columns: S in two buffers where they fit, then O.
+    static constexpr int NB = 3 * N <= 512 ? 2 : 1;
+    static constexpr int TM_S = 0;
+    static constexpr int TM_O = NB * N;
+    static_assert(R % 16 == 0 && R <= kRows, "rows of a tile");
+    static_assert((NB + 1) * N <= 512, "TMEM budget");
+    static_assert(NS >= 3 && SMEM <= 227 * 1024, "shared memory budget");
+    static_assert(SMEM > 114 * 1024, "one CTA per SM keeps TMEM allocation uncontended");
+    static_assert(OFF_BAR + NBAR * 8 - OFF_SCALE <= SMALL, "small arrays fit their room");
+};
+
+struct Misc {
+    uint32_t tmem_base;
+    int abort;
+    uint32_t qmax[kSoftWarps];  // largest |q| bits seen by each warp
+    uint64_t vote[2];           // a byte per warp: an exponent left its range
+};
+static_assert(sizeof(Misc) <= 64, "Misc fits its slot");
+
+// tcgen05 instruction descriptor of kind::f8f6f4, e4m3 A and B, fp32 D.
+TA_HD uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
+    return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+           ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+// Shared-memory descriptor of a tile whose rows are D bytes: 128-byte swizzle
+// (mode 2) for D = 128, 64-byte swizzle (mode 4) for D = 64; 8-row groups are
+// 8 * D bytes apart (the stride dimension for K-major and MN-major alike: a
+// row holds every M/N element of an MN-major tile).
 template <int D>
-__global__ void __launch_bounds__(128) verify_fp8_rows_kernel(const Fp8Args a) {
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>((8 * D) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(D == 128 ? 2 : 4) << 61);
+}
+
+// Byte offset of 16-byte chunk c of row r in such a tile.
+template <int D>
+__device__ __forceinline__ uint32_t tile_offset(uint32_t r, uint32_t c) {
+    return D == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+}
+
+struct Range {
+    long long x0, x1, base0;
+    int b0;
+    int32_t lraw0;
+};
+
+// This CTA's stretch of the work line (one warp; every lane gets it).
+__device__ Range plan_range(const Fp8Args& a, int lane) {
+    const int upb = a.Hkv * a.RB;
+    auto len_of = [&](int b) -> int {
+        if (b >= a.B) return 0;
+        bool bad;
+        const int n = unit_len(unit_chunks(a.seq_lens[b], a.P, a.max_pages, kTreeNone, 0, bad),
+                               a.ovh);
+        if (bad && blockIdx.x == 0) report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
+        return n;
+    };
+    const int n0 = len_of(lane), n1 = len_of(lane + 32);  // both loads in flight
+    long long tot = __reduce_add_sync(kFull, n0) + __reduce_add_sync(kFull, n1);
+    for (int b = 64; b < a.B; b += 32) tot += __reduce_add_sync(kFull, len_of(b + lane));
+    const long long W = tot * upb;
+    Range r;
+    r.x0 = cta_start(blockIdx.x, W, a.n_ctas);
+    r.x1 = cta_start(blockIdx.x + 1, W, a.n_ctas);
+    r.b0 = 0;
+    r.base0 = 0;
+    r.lraw0 = 0;
+    if (r.x0 >= r.x1) return r;
+    long long run = 0;
+    for (int b = 0; b < a.B; b += 32) {
+        const long long n =
+            static_cast<long long>(upb) * (b == 0 ? n0 : (b == 32 ? n1 : len_of(b + lane)));
+        long long incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(kFull, incl, off);
+            if (lane >= off) incl += v;
+        }
+        const bool hit = run + incl - n <= r.x0 && r.x0 < run + incl;
+        const unsigned m = __ballot_sync(kFull, hit);
+        if (m != 0) {
+            const int src = __ffs(m) - 1;
+            r.b0 = b + src;
+            r.base0 = run + __shfl_sync(kFull, incl - n, src);
+            r.lraw0 = a.seq_lens[r.b0];
+            break;
+        }
+        run += __shfl_sync(kFull, incl, 31);
+    }
+    return r;
+}
+
+// Sums over the 32 lanes of NC columns held one value per lane and column.
+// Afterwards v[i] of lane l is the sum of column 32 i + l (NC = 32 k), or, with
+// fewer than 32 columns, of column l % NC.  Each exchange halves the columns a
+// lane still holds.
+template <int NC>
+__device__ __forceinline__ void column_sums(float* v, int lane) {
+    if constexpr (NC > 32) {
+        column_sums<32>(v, lane);
+        column_sums<NC - 32>(v + 32, lane);
+        v[1] = v[32];
+    } else if constexpr (NC == 24) {
+        column_sums<16>(v, lane);
+        column_sums<8>(v + 16, lane);
+        if ((lane & 31) >= 16) v[0] = v[16];
+    } else {
+        static_assert(NC == 8 || NC == 16 || NC == 32, "columns");
+#pragma unroll
+        for (int w = NC / 2; w >= 1; w >>= 1) {
+            const bool up = (lane & w) != 0;
+#pragma unroll
+            for (int i = 0; i < w; ++i) {
+                const float send = up ? v[i] : v[i + w];
+                const float keep = up ? v[i + w] : v[i];
+                v[i] = keep + __shfl_xor_sync(kFull, send, w);
+            }
+        }
+#pragma unroll
+        for (int w = NC; w < 32; w <<= 1) v[0] += __shfl_xor_sync(kFull, v[0], w);
+    }
+}
+
+// fp32 to an int that orders the same way, NaN lowest; and back.
+__device__ __forceinline__ int ordered(float x) {
+    const int b = __float_as_int(x == x ? x : kNegInf);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int o) {
+    return __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
+}
+
+__device__ __forceinline__ int blocks_of(const Segment& sg) {
+    return (sg.chunk_end - sg.chunk_begin + 1) / 2;
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_fp8_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Fp8Args a) {
+    using S = Shape<D, R>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = ptx::smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sb = raw_addr + pad;
+    Misc* misc = reinterpret_cast<Misc*>(smem + S::OFF_MISC);
+    volatile int* abort_flag = &misc->abort;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    auto bar = [&](int i) -> uint32_t { return sb + S::OFF_BAR + 8u * i; };
+
+    if (warp == kWarpTma && lane == 0) {
+        for (int s = 0; s < S::NS; ++s) {
+            ptx::mbar_init(bar(S::KV_FULL + s), 1);
+            ptx::mbar_init(bar(S::KV_EMPTY + s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(S::S_FULL + i), 1);
+            ptx::mbar_init(bar(S::S_FREE + i), kSoftWarps);
+            ptx::mbar_init(bar(S::P_FULL + i), kSoftWarps);
+            ptx::mbar_init(bar(S::P_FREE + i), 1);
+        }
+        ptx::mbar_init(bar(S::O_FULL), 1);
+        ptx::mbar_init(bar(S::O_FREE), kSoftWarps);
+        ptx::mbar_init(bar(S::Q_FULL), kSoftWarps);
+        ptx::mbar_init(bar(S::CHECK), kSoftWarps);
+        ptx::mbar_init(bar(S::MEET), kSoftWarps);
+        ptx::mbar_init(bar(S::DRAIN), 1);
+        misc->abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_v);
+    }
+    if (warp == kWarpMma) {
+        ptx::tmem_alloc(ptx::smem_u32(&misc->tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    const uint64_t pol = ptx::policy_evict_first();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = misc->tmem_base;
+    // Everything below reads inputs that the kernel before may write.  Only
+    // after that wait may the next kernel start (see tree_mask_kernel).
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (w >= static_cast<long long>(a.B) * a.T * a.Hq) return;
-    const int h = static_cast<int>(w % a.Hq);
-    const int t = static_cast<int>(w / a.Hq % a.T);
-    const int b = static_cast<int>(w / a.Hq / a.T);
-    const int hk = h / a.G;
-    bool bad;
-    const int L = clamp_seq_len(a.seq_lens[b], a.P, a.max_pages, bad);
-    if (bad && lane == 0) report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
-    uint64_t bits = 0;
-    if (a.parents != nullptr) {
-        const int32_t* par = a.parents + static_cast<size_t>(b) * a.parents_stride;
-        for (int node = t; node >= 0;) {
-            bits |= 1ull << node;
-            const int up = par[node];
-            if (up < -1 || up >= node) {
-                report(a.status, TREE_ATTN_STATUS_BAD_PARENT);
+    const Range rg = plan_range(a, lane);
+    Walker w;
+    w.init_known(a.seq_lens, a.B, a.P, a.max_pages, a.Hkv * a.RB, a.RB, rg.b0, rg.base0, rg.x0,
+                 rg.x1, kTreeNone, 0, a.ovh, rg.lraw0);
+    auto fail = [&]() {
+        *abort_flag = 1;
+        report(a.status, TREE_ATTN_STATUS_TIMEOUT);
+    };
+
+    if (warp == kWarpTma) {
+        // ================= copies (one thread)
+        if (lane == 0) {
+            const int Pb = a.P < kChunk ? a.P : kChunk;  // tokens per box
+            const int nsub = kChunk / Pb;
+            const int pshift = __ffs(a.P) - 1;
+            uint32_t jj = 0;
+            bool ok = true;
+            Segment sg;
+            while (ok && w.next(sg)) {
+                bool bad;
+                const int L = clamp_seq_len(sg.len_raw, a.P, a.max_pages, bad);
+                const int npages = (L + a.P - 1) / a.P;
+                const int32_t* table = a.block_table + static_cast<size_t>(sg.b) * a.max_pages;
+#pragma unroll 1
+                for (int ch = sg.chunk_begin; ch < sg.chunk_end; ch += 2, ++jj) {
+                    // All page lookups of the block go out before the wait for
+                    // its stage.
+                    const int nh = min(2, sg.chunk_end - ch);
+                    int pid[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int hh = k >> 2, i = k & 3;
+                        const int lp = ((ch + hh) * kChunk + i * Pb) >> pshift;
+                        const bool use = hh < nh && i < nsub && lp < npages;
+                        pid[k] = use ? table[lp] : -2;
+                    }
+                    const int s = jj % S::NS;
+                    if (jj >= S::NS &&
+                        !ptx::mbar_wait(bar(S::KV_EMPTY + s), ((jj / S::NS) - 1) & 1, a.wait_ns)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    if (*abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    int nl = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (pid[k] == -2) continue;
+                        if (pid[k] < 0 || pid[k] >= a.num_pages) {
+                            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                            pid[k] = -2;
+                        } else {
+                            ++nl;
+                        }
+                    }
+                    const uint32_t fb = bar(S::KV_FULL + s);
+                    if (nl > 0)
+                        ptx::mbar_arrive_expect_tx(fb, static_cast<uint32_t>(nl * Pb * 2 * (D + 1)));
+                    else
+                        ptx::mbar_arrive(fb);
+                    const uint32_t kst = sb + S::OFF_STAGE + s * S::STAGE;
+                    const uint32_t sst = sb + S::OFF_SCALE + s * 2 * kKeys;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (pid[k] == -2) continue;
+                        const int hh = k >> 2, i = k & 3;
+                        const int tok = (ch + hh) * kChunk + i * Pb;
+                        const int y = (pid[k] * a.Hkv + sg.hk) * a.P + (tok & (a.P - 1));
+                        const int row = hh * kChunk + i * Pb;
+                        ptx::tma_load_2d(kst + row * D, &tm_k, 0, y, fb, pol);
+                        ptx::tma_load_2d(kst + S::TILE + row * D, &tm_v, 0, y, fb, pol);
+                        ptx::bulk_load(sst + row, a.k_scales + y, Pb, fb);
+                        ptx::bulk_load(sst + kKeys + row, a.v_scales + y, Pb, fb);
+                    }
+                }
+            }
+            if (!ok) {
+                const uint32_t first = jj > S::NS ? jj - S::NS : 0;
+                for (uint32_t j = first; j < jj; ++j)
+                    (void)ptx::mbar_wait(bar(S::KV_FULL + j % S::NS), (j / S::NS) & 1,
+                                         ptx::kDrainLimitNs);
+            }
+        }
+    } else if (warp == kWarpMma) {
+        // ================= MMA issuer: the whole warp walks, one lane issues
+        const bool lead = ptx::elect_one();
+        const uint32_t id_s = idesc_e4m3_f32(kKeys, S::N, false, false);
+        const uint32_t id_o = idesc_e4m3_f32(D, S::N, true, true);
+        uint32_t jj = 0, kk = 0;
+        bool ok = true;
+        Segment sg;
+        while (ok && w.next(sg)) {
+            if (!__all_sync(kFull, ptx::mbar_wait(bar(S::Q_FULL), kk & 1, a.wait_ns))) {
+                fail();
                 break;
             }
-            node = up;
+            ptx::tc_fence_after();
+            const int n = blocks_of(sg);
+            int nq = 0, np = 0;
+            uint64_t t0 = 0;
+            while (np < n) {
+                bool progress = false;
+                if (np < nq) {
+                    const uint32_t j = jj + np;
+                    const bool go =
+                        ptx::mbar_try_wait(bar(S::P_FULL + (j & 1)), (j >> 1) & 1) &&
+                        (np > 0 || kk == 0 || ptx::mbar_try_wait(bar(S::O_FREE), (kk - 1) & 1));
+                    if (__all_sync(kFull, go)) {
+                        ptx::tc_fence_after();
+                        const uint32_t vst =
+                            sb + S::OFF_STAGE + (j % S::NS) * S::STAGE + S::TILE;
+                        const uint32_t pst = sb + S::OFF_P + (j & 1) * S::P_BYTES;
+                        // A block of one 64-token step has nothing in its second half.
+                        const int nk = sg.chunk_end - sg.chunk_begin - 2 * np >= 2 ? 4 : 2;
+                        if (lead) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (k >= nk) break;
+                                ptx::mma_f8(tmem + S::TM_O, tile_desc<D>(vst + k * 32 * D),
+                                            smem_desc_sw128(pst + k * 32 * 128, S::P_ATOM, 1024),
+                                            id_o, (np == 0 && k == 0) ? 0u : 1u);
+                            }
+                            ptx::mma_commit(bar(S::KV_EMPTY + j % S::NS));
+                            ptx::mma_commit(bar(S::P_FREE + (j & 1)));
+                        }
+                        __syncwarp();
+                        ++np;
+                        progress = true;
+                    }
+                }
+                if (nq < n) {
+                    const uint32_t j = jj + nq;
+                    const int s = j % S::NS;
+                    const int sbuf = j % S::NB;
+                    const bool go =
+                        ptx::mbar_try_wait(bar(S::KV_FULL + s), (j / S::NS) & 1) &&
+                        (j < S::NB ||
+                         ptx::mbar_try_wait(bar(S::S_FREE + sbuf), ((j / S::NB) - 1) & 1));
+                    if (__all_sync(kFull, go)) {
+                        ptx::tc_fence_after();
+                        const uint32_t kst = sb + S::OFF_STAGE + s * S::STAGE;
+                        if (lead) {
+#pragma unroll
+                            for (int k = 0; k < D / 32; ++k)
+                                ptx::mma_f8(tmem + S::TM_S + sbuf * S::N,
+                                            tile_desc<D>(kst + k * 32),
+                                            tile_desc<D>(sb + S::OFF_Q + k * 32), id_s,
+                                            k > 0 ? 1u : 0u);
+                            ptx::mma_commit(bar(S::S_FULL + sbuf));
+                        }
+                        __syncwarp();
+                        ++nq;
+                        progress = true;
+                    }
+                }
+                if (progress) {
+                    t0 = 0;
+                } else {
+                    const uint64_t now = ptx::globaltimer();
+                    if (t0 == 0) t0 = now;
+                    if (__any_sync(kFull, now - t0 > a.wait_ns || *abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                }
+            }
+            if (!ok) {
+                fail();
+                break;
+            }
+            if (lead) ptx::mma_commit(bar(S::O_FULL));
+            __syncwarp();
+            jj += n;
+            ++kk;
         }
-        if (h == 0 && lane == 0 && a.mask_out != nullptr && (a.parents_stride != 0 || b == 0))
-            a.mask_out[static_cast<size_t>(b) * a.parents_stride + t] = bits;
+        if (lead) ptx::mma_commit(bar(S::DRAIN));
+        __syncwarp();
+        (void)ptx::mbar_wait(bar(S::DRAIN), 0, ptx::kDrainLimitNs);
     } else {
-        bits = a.mask[static_cast<size_t>(b) * a.mask_stride + t];
-        if (a.T < 64) bits &= (1ull << a.T) - 1ull;
-    }
-    auto bf = [](const uint16_t* p, int e) { return __uint_as_float(uint32_t(p[e]) << 16); };
-    float q[E], acc[E], kv[E], vv[E];
+        // ================= softmax and epilogue (two warpgroups)
+        constexpr int H = S::HALF;  // this warpgroup's rows
+        const int wg = warp >> 2;
+        const int quad = warp & 3;  // the TMEM lanes this warp reaches
+        const int key = quad * 32 + lane;
+        const int row0 = wg * H;    // first row of the tile taken here
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        float* ref = reinterpret_cast<float*>(smem + S::OFF_REF);
+        float* alpha = reinterpret_cast<float*>(smem + S::OFF_ALPHA);
+        float* wmax = reinterpret_cast<float*>(smem + S::OFF_WMAX);  // [4][R]
+        auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
+            const bool ok = ptx::mbar_wait(b, parity, a.wait_ns);
+            const bool all = __all_sync(kFull, ok && !*abort_flag);
+            if (!ok) fail();
+            return all;
+        };
+        uint32_t met = 0;  // meetings of the softmax warps so far
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(S::MEET));
+            const uint32_t parity = met & 1;
+            ++met;
+            return wait_all(bar(S::MEET), parity);
+        };
+
+        uint32_t jj = 0, kk = 0;
+        bool ok = true;
+        Segment cur;
+        while (ok && w.next(cur)) {
+            bool bad;
+            const int L = clamp_seq_len(cur.len_raw, a.P, a.max_pages, bad);
+            const int Mrb = min(kRows, a.M - cur.rb * kRows);  // query rows of the tile
+            // ---- the tile's queries: a common power of two brings the largest
+            // |q| into [128, 256); each value is held as hi (e4m3) and
+            // lo = 16 (value - hi), which is exact down to 2^-9 / 16.
+            float c_scale;
+            {
+                constexpr int LPR = D / 8;                   // lanes per row
+                constexpr int STEP = kSoftWarps * 32 / LPR;  // rows per pass
+                constexpr int NP = (R + STEP - 1) / STEP;
+                const int r0 = threadIdx.x / LPR, gl = threadIdx.x % LPR;
+                uint4 x[NP];
+                uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = bf(a.q + w * D, lane * E + e);
-        acc[e] = 0.f;
-    }
-    float m = -__builtin_huge_valf(), l = 0.f;
-    auto add_key = [&]() {
-        float x = 0.f;
+                for (int i = 0; i < NP; ++i) {
+                    const int r = r0 + i * STEP;
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < Mrb) {
+                        const int rr = cur.rb * kRows + r;
+                        const int t = rr / a.G, h = cur.hk * a.G + rr % a.G;
+                        x[i] = __ldg(reinterpret_cast<const uint4*>(
+                            a.q + ((static_cast<size_t>(cur.b) * a.T + t) * a.Hq + h) * D +
+                            gl * 8));
+                    }
+                    const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-        for (int e = 0; e < E; ++e) x = fmaf(q[e], kv[e], x);
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
-        x *= a.scale_log2;
-        const float mn = fmaxf(m, x);
-        if (mn == -__builtin_huge_valf()) return;
-        const float al = exp2f(m - mn), p = exp2f(x - mn);
-        l = l * al + p;
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t lo = (wd[u] << 16) & 0x7fff0000u, hi = wd[u] & 0x7fff0000u;
+                        if (lo < 0x7f800000u) m = max(m, lo);
+                        if (hi < 0x7f800000u) m = max(m, hi);
+                    }
+                }
+                m = __reduce_max_sync(kFull, m);
+                if (lane == 0) misc->qmax[warp] = m;
+                if (!meet()) {
+                    ok = false;
+                    break;
+                }
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * al + p * vv[e];
-        m = mn;
-    };
-    auto code = [](uint32_t c) {
-        const uint32_t h2 = f16x2_of_e4m3x2(c);
-        float f;
-        asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.f32.f16 %0, lo;}" : "=f"(f) : "r"(h2));
-        return f;
-    };
-    for (int p = 0; p < L; ++p) {
-        const int page = a.block_table[static_cast<size_t>(b) * a.max_pages + p / a.P];
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-            continue;
+                for (int i = 0; i < kSoftWarps; ++i) m = max(m, misc->qmax[i]);
+                int kq = m == 0 ? 0 : 134 - static_cast<int>(m >> 23);
+                kq = kq > 100 ? 100 : kq;
+                const float up = __int_as_float((127 + kq) << 23);
+                c_scale = a.scale_log2 * __int_as_float((127 - kq) << 23);
+                uint8_t* qs = smem + S::OFF_Q;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int r = r0 + i * STEP;
+                    if (r >= R) continue;
+                    const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        float v0 = __uint_as_float(wd[u] << 16) * up;
+                        float v1 = __uint_as_float(wd[u] & 0xffff0000u) * up;
+                        // an infinite query has no finite scores: NaN, as its softmax
+                        v0 = fabsf(v0) < 1e30f ? v0 : __int_as_float(0x7fffffff);
+                        v1 = fabsf(v1) < 1e30f ? v1 : __int_as_float(0x7fffffff);
+                        hi[u] = e4m3x2(v0, v1);
+                        const uint32_t hh = f16x2_of_e4m3x2(hi[u]);
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+                        lo[u] = e4m3x2((v0 - b.x) * 16.f, (v1 - b.y) * 16.f);
+                    }
+                    // tile rows: the hi halves of a warpgroup's rows, then the lo halves
+                    const int n = (r / H) * R + r % H;
+                    *reinterpret_cast<uint2*>(qs + tile_offset<D>(n, gl >> 1) + (gl & 1) * 8) =
+                        make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                    *reinterpret_cast<uint2*>(qs + tile_offset<D>(n + H, gl >> 1) +
+                                              (gl & 1) * 8) =
+                        make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(S::Q_FULL));
+            }
+
+            float l[H];
+#pragma unroll
+            for (int i = 0; i < H; ++i) l[i] = 0.f;
+            for (int ch = cur.chunk_begin; ch < cur.chunk_end; ch += 2, ++jj) {
+                const bool first = ch == cur.chunk_begin;
+                const int nh = min(2, cur.chunk_end - ch);
+                // Keys of this block, and whether this thread's is one of them.
+                const int keys = min(nh * kChunk, L - ch * kChunk);
+                const bool valid = key < keys;
+                const uint32_t sbuf = jj % S::NB;
+                if (!wait_all(bar(S::S_FULL + sbuf), (jj / S::NB) & 1)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                // x = hi + lo / 16 for this thread's key and rows
+                float x[H];
+                {
+                    const uint32_t ta = lanes + S::TM_S + sbuf * S::N + wg * R;
+                    const uint64_t sixteenth = ptx::f2_pack(0.0625f, 0.0625f);
+                    constexpr int CH = H > 40 ? 32 : H;  // columns in flight
+#pragma unroll
+                    for (int c0 = 0; c0 < H; c0 += CH) {
+                        float y[CH];
+#pragma unroll
+                        for (int c = 0; c < CH; c += 8) {
+                            ptx::tmem_ld8(ta + c0 + c, x + c0 + c);
+                            ptx::tmem_ld8(ta + H + c0 + c, y + c);
+                        }
+                        ptx::tmem_wait_ld();
+                        if (c0 + CH == H) {
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(bar(S::S_FREE + sbuf));
+                        }
+#pragma unroll
+                        for (int i = 0; i < CH; i += 2)
+                            ptx::f2_unpack(
+                                ptx::f2_fma(ptx::f2_pack(y[i], y[i + 1]), sixteenth,
+                                            ptx::f2_pack(x[c0 + i], x[c0 + i + 1])),
+                                x[c0 + i], x[c0 + i + 1]);
+                    }
+                }
+                // The key's scales.  The S product was made from this stage, so
+                // its copies have landed; this wait makes them visible here.
+                if (!wait_all(bar(S::KV_FULL + jj % S::NS), (jj / S::NS) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* sc = smem + S::OFF_SCALE + (jj % S::NS) * 2 * kKeys;
+                const int vbyte = sc[kKeys + key];
+                const float F = scale_of(sc[key]) * c_scale;
+                const float vs = static_cast<float>(vbyte - 127);
+                const float wkey = inv_scale_of(vbyte);
+                const uint64_t F2 = ptx::f2_pack(F, F);
+                const uint64_t vs2 = ptx::f2_pack(vs, vs);
+                // e = F x + scale of v: once more where the references moved
+                bool redo = first;
+                if (!first) {
+                    float top = kNegInf;
+#pragma unroll
+                    for (int i = 0; i < H; i += 2) {
+                        const float2 rf = *reinterpret_cast<const float2*>(ref + row0 + i);
+                        float e0, e1;
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), F2,
+                                                   ptx::f2_add(vs2, ptx::f2_pack(-rf.x, -rf.y))),
+                                       e0, e1);
+                        top = ptx::fmax3(top, e0, e1);
+                    }
+                    const bool over = __any_sync(kFull, valid && top > kMost);
+                    if (lane == 0)
+                        reinterpret_cast<volatile uint8_t*>(&misc->vote[jj & 1])[warp] = over;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(S::CHECK));
+                }
+                // (the vote of block j of a segment is its j-th; first blocks hold none)
+                if (!first) {
+                    if (!wait_all(bar(S::CHECK), (jj - kk - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    redo = *reinterpret_cast<volatile uint64_t*>(&misc->vote[jj & 1]) != 0;
+                }
+                if (redo) {
+                    // Largest e of every row, by warp, then by tile.
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const float e = valid ? fmaf(x[i], F, vs) : kNegInf;
+                        const int o = __reduce_max_sync(kFull, ordered(e));
+                        if (lane == (i & 31)) wmax[quad * R + row0 + i] = unordered(o);
+                    }
+                    if (!meet()) {
+                        ok = false;
+                        break;
+                    }
+                    const int r = threadIdx.x;
+                    if (r < R) {
+                        const float top = fmaxf(fmaxf(wmax[r], wmax[R + r]),
+                                                fmaxf(wmax[2 * R + r], wmax[3 * R + r]));
+                        const float old = first ? kNegInf : ref[r];
+                        const bool move = first || top > old + kMost;
+                        // a row of NaN scores has no largest: any finite reference
+                        const float now = move ? (top == kNegInf ? 0.f : top - kTop) : old;
+                        ref[r] = now;
+                        alpha[r] = move ? ptx::ex2(old - now) : 1.f;
+                    }
+                    if (!meet()) {
+                        ok = false;
+                        break;
+                    }
+                    if (!first) {
+#pragma unroll
+                        for (int i = 0; i < H; ++i) l[i] *= alpha[row0 + i];
+                        // O holds the blocks before once P.V of the last has completed.
+                        if (!wait_all(bar(S::P_FREE + ((jj - 1) & 1)), ((jj - 1) >> 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                            for (int c = 0; c < H; c += 8) {
+                                const uint32_t to = lanes + S::TM_O + wg * R + half * H + c;
+                                float o[8];
+                                ptx::tmem_ld8(to, o);
+                                ptx::tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] *= alpha[row0 + c + i];
+                                ptx::tmem_st8(to, o);
+                            }
+                        }
+                        ptx::tmem_wait_st();
+                    }
+                }
+                // P buffer (jj & 1) is free once P.V of block jj - 2 has completed.
+                if (jj >= 2 && !wait_all(bar(S::P_FREE + (jj & 1)), ((jj >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (key < nh * kChunk) {
+                    // p = 2^(e - ref) as hi and lo; a key past the data has none.
+                    const uint32_t pst = sb + S::OFF_P + (jj & 1) * S::P_BYTES;
+                    const uint64_t w2 = ptx::f2_pack(wkey, wkey);
+                    uint32_t code[R / 4];
+                    uint16_t* c16 = reinterpret_cast<uint16_t*>(code);
+                    const uint64_t sixteen = ptx::f2_pack(16.f, 16.f);
+#pragma unroll
+                    for (int i = 0; i < H; i += 2) {
+                        const float2 rf = *reinterpret_cast<const float2*>(ref + row0 + i);
+                        float e0, e1;
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), F2,
+                                                   ptx::f2_add(vs2, ptx::f2_pack(-rf.x, -rf.y))),
+                                       e0, e1);
+                        const float p0 = valid ? ptx::ex2(e0) : 0.f;
+                        const float p1 = valid ? ptx::ex2(e1) : 0.f;
+                        if (valid)
+                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(p0, p1), w2,
+                                                       ptx::f2_pack(l[i], l[i + 1])),
+                                           l[i], l[i + 1]);
+                        const uint32_t hi = e4m3x2(p0, p1);
+                        const uint32_t back = f16x2_of_e4m3x2(hi);
+                        const __half2 neg = __hmul2(*reinterpret_cast<const __half2*>(&back),
+                                                    __float2half2_rn(-16.f));
+                        const float2 b = __half22float2(neg);
+                        float r0, r1;
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(p0, p1), sixteen,
+                                                   ptx::f2_pack(b.x, b.y)),
+                                       r0, r1);
+                        c16[i / 2] = static_cast<uint16_t>(hi);
+                        c16[(H + i) / 2] = static_cast<uint16_t>(e4m3x2(r0, r1));
+                    }
+#pragma unroll
+                    for (int c = 0; c < R / 16; ++c) {
+                        const int n = wg * (R / 16) + c;  // 16-byte chunk of the key's row
+                        const uint32_t at = pst + (n >> 3) * S::P_ATOM +
+                                            sw128_offset(key, n & 7);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                                     "r"(code[4 * c]), "r"(code[4 * c + 1]), "r"(code[4 * c + 2]),
+                                     "r"(code[4 * c + 3])
+                                     : "memory");
+                    }
+                    if (!valid && wg == 0) {
+                        // 0 * NaN is not 0: the value rows past the data are cleared.
+                        const uint32_t vrow = sb + S::OFF_STAGE + (jj % S::NS) * S::STAGE +
+                                              S::TILE + key * D;
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow +
+                                                                                      c * 16),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(S::P_FULL + (jj & 1)));
+            }
+            if (!ok) break;
+            // ---- epilogue: the rows' sums over the key lanes, then O.
+            column_sums<H>(l, lane);
+#pragma unroll
+            for (int i = 0; i < (H + 31) / 32; ++i)
+                if (i * 32 + lane < H) wmax[quad * R + row0 + i * 32 + lane] = l[i];
+            if (!meet()) {
+                ok = false;
+                break;
+            }
+            float* slot = a.ws + static_cast<size_t>(cur.unit + blockIdx.x) * slot_floats(D);
+            {
+                const int r = threadIdx.x;
+                if (r < Mrb) {
+                    slot[r] = ref[r];
+                    slot[kRows + r] = (wmax[r] + wmax[R + r]) + (wmax[2 * R + r] + wmax[3 * R + r]);
+                }
+            }
+            if (!wait_all(bar(S::O_FULL), kk & 1)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            // An M = 64 accumulator (D = 64) keeps its rows in the first 16
+            // lanes of each warp's 32.
+            const int dim = D == 128 ? key : quad * 16 + lane;
+            float* acc = slot + 2 * kRows + dim;
+#pragma unroll
+            for (int c = 0; c < H; c += 8) {
+                float o[8], o2[8];
+                ptx::tmem_ld8(lanes + S::TM_O + wg * R + c, o);
+                ptx::tmem_ld8(lanes + S::TM_O + wg * R + H + c, o2);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = row0 + c + i;
+                    if (r < Mrb && (D == 128 || lane < 16))
+                        acc[static_cast<size_t>(r) * D] = fmaf(o2[i], 0.0625f, o[i]);
+                }
+            }
+            ptx::tc_fence_before();
+            // wmax, ref and Q of this segment have been read when all are here
+            if (!meet()) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) ptx::mbar_arrive(bar(S::O_FREE));
+            ++kk;
         }
-        const long long row = (static_cast<long long>(page) * a.Hkv + hk) * a.P + p % a.P;
-        const float fk = scale_of(a.k_scales[row]), fv = scale_of(a.v_scales[row]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            kv[e] = code(a.k_pages[row * D + lane * E + e]) * fk;
-            vv[e] = code(a.v_pages[row * D + lane * E + e]) * fv;
-        }
-        add_key();
     }
-    for (int j = 0; j < a.T; ++j) {
-        if (((bits >> j) & 1ull) == 0) continue;
-        const long long row = (static_cast<long long>(b) * a.T + j) * a.Hkv + hk;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            kv[e] = bf(a.tree_k + row * D, lane * E + e);
-            vv[e] = bf(a.tree_v + row * D, lane * E + e);
-        }
-        add_key();
+
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
     }
-    const bool none = m == -__builtin_huge_valf();
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const __nv_bfloat16 o = __float2bfloat16_rn(none ? 0.f : acc[e] / l);
-        a.out[w * D + lane * E + e] = *reinterpret_cast<const uint16_t*>(&o);
+}
+
+template <int D, int R>
+cudaError_t launch_prefix_fp8(const Fp8Args& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                              int dev, cudaStream_t stream) {
+    using S = Shape<D, R>;
+    // Devices on which the shared-memory opt-in has been applied.
+    static std::atomic<unsigned long long> configured{0};
+    const unsigned long long bit = 1ull << (dev & 63);
+    if ((configured.load() & bit) == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            prefix_fp8_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit);
     }
-    if (lane == 0) a.lse[w] = none ? m : (m + log2f(l)) * 0.69314718055994530942f;
+    return launch_dependent(prefix_fp8_kernel<D, R>, dim3(a.n_ctas), dim3(kThreads), S::SMEM,
+                            stream, tk, tv, a);
+}
+
+// The smallest tile that holds a unit's rows: every lane of the softmax works
+// on each of them, so idle rows cost as much as used ones.
+template <int D>
+cudaError_t launch_prefix_fp8_rows(const Fp8Args& a, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, int dev, cudaStream_t stream) {
+    const int rows = a.M < kRows ? a.M : kRows;
+    if (rows <= 16) return launch_prefix_fp8<D, 16>(a, tk, tv, dev, stream);
+    if (rows <= 32) return launch_prefix_fp8<D, 32>(a, tk, tv, dev, stream);
+    if (rows <= 48) return launch_prefix_fp8<D, 48>(a, tk, tv, dev, stream);
+    if (rows <= 64) return launch_prefix_fp8<D, 64>(a, tk, tv, dev, stream);
+    if (rows <= 80) return launch_prefix_fp8<D, 80>(a, tk, tv, dev, stream);
+    return launch_prefix_fp8<D, 128>(a, tk, tv, dev, stream);
+}
+
+// The [num_pages * Hkv * P][d] codes of a pool in boxes of up to 64 tokens.
+bool encode_codes(CUtensorMap* map, const void* base, long long rows, int d, int P) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(d),
+                               static_cast<cuuint32_t>(P < kChunk ? P : kChunk)};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box,
+                        d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace
@@ -172,37 +918,69 @@ extern "C" int tree_attn_verify_fp8(
     if (need == 0) return TREE_ATTN_ERR_CUDA;
     if (workspace == nullptr || !ptr_aligned(workspace, 256) || workspace_bytes < need)
         return TREE_ATTN_ERR_WORKSPACE;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return TREE_ATTN_ERR_CUDA;
+    const Plan plan = make_plan(B, Hq, Hkv, T, page_size, max_pages_per_seq, sms, 0, kTreeNone);
+    const long long rows = static_cast<long long>(num_pages) * Hkv * page_size;
+    CUtensorMap tk, tv;
+    if (!encode_codes(&tk, k_pages, rows, d, page_size) ||
+        !encode_codes(&tv, v_pages, rows, d, page_size))
+        return TREE_ATTN_ERR_CUDA;
     Fp8Args a;
     a.q = q;
-    a.k_pages = k_pages;
-    a.v_pages = v_pages;
     a.k_scales = k_scales;
     a.v_scales = v_scales;
     a.block_table = block_table;
     a.seq_lens = seq_lens;
-    a.tree_k = tree_k;
-    a.tree_v = tree_v;
-    a.mask = mask;
-    a.mask_stride = mask_stride;
-    a.parents = parents;
-    a.parents_stride = parents_stride;
-    a.mask_out = mask_out;
-    a.out = out;
-    a.lse = lse;
+    a.ws = static_cast<float*>(workspace);
     a.status = status;
     a.B = B;
     a.Hq = Hq;
     a.Hkv = Hkv;
-    a.G = Hq / Hkv;
+    a.G = plan.G;
     a.T = T;
+    a.M = plan.M;
+    a.RB = plan.RB;
     a.P = page_size;
     a.max_pages = max_pages_per_seq;
     a.num_pages = num_pages;
+    a.n_ctas = plan.n_ctas;
+    a.ovh = kOverhead;
     a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
-    const long long rows = static_cast<long long>(B) * T * Hq;
-    const cudaError_t e = launch_dependent(
-        d == 128 ? verify_fp8_rows_kernel<128> : verify_fp8_rows_kernel<64>,
-        dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0,
-        static_cast<cudaStream_t>(stream), a);
-    return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
+    a.wait_ns = wait_limit_ns();
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((d == 128 ? launch_prefix_fp8_rows<128>(a, tk, tv, dev, st)
+                  : launch_prefix_fp8_rows<64>(a, tk, tv, dev, st)) != cudaSuccess)
+        return TREE_ATTN_ERR_CUDA;
+    // The tree pass and the merge, on one partial per CTA and unit.
+    VerifyArgs v = {};
+    v.q = q;
+    v.block_table = block_table;
+    v.seq_lens = seq_lens;
+    v.tree_k = tree_k;
+    v.tree_v = tree_v;
+    v.mask = mask;
+    v.mask_stride = mask_stride;
+    v.parents = parents;
+    v.parents_stride = parents_stride;
+    v.mask_out = mask_out;
+    v.out = out;
+    v.lse = lse;
+    v.ws = a.ws;
+    v.status = status;
+    v.B = B;
+    v.Hq = Hq;
+    v.Hkv = Hkv;
+    v.d = d;
+    v.T = T;
+    v.P = page_size;
+    v.max_pages = max_pages_per_seq;
+    v.num_pages = num_pages;
+    v.n_ctas = a.n_ctas;
+    v.ovh = a.ovh;
+    v.scale_log2 = a.scale_log2;
+    v.copies = 1;
+    return launch_merge(v, st) == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }
