@@ -20,8 +20,9 @@
 //   O sums p v, and the row's sum takes p 2^-(scale of v_j).
 // * A row's maximum would need the 128 lanes to meet; instead each block only
 //   asks whether any e exceeds its row's reference by more than 8 (p must stay
-//   below 448).  If one does, the references move and O is rescaled (the first
-//   block of a segment always does).
+//   below 448), and goes on while the warps' answers come in.  If one does, the
+//   references move and O is rescaled (the first block of a segment always
+//   does that).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,13 +45,14 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr int kKeys = 2 * kChunk;    // keys of a block
-constexpr int kSoftWarps = 8;        // two warpgroups, half of the rows each
-constexpr int kWarpTma = 8, kWarpMma = 9;
-constexpr int kThreads = 32 * 10;
-// References sit 2^kRoom below what p may reach without the row moving them:
-// a moved reference puts its row's largest p at 2^4, and p may grow to 2^8.
-constexpr float kTop = 4.f, kMost = 8.f;
+constexpr int kKeys = 2 * kChunk;  // keys of a block
+// p = 2^(e - reference) may reach 2^kMost (e4m3 ends at 448).  When a block
+// passes that, the references of all rows whose maximum stands above 2^kNear
+// move up to it, so that rows close to their limit do not stop a later block:
+// with scores of a spread of about 2.3 binades, 80 rows and 7000 keys 8 % of
+// the blocks move references (moving only the rows past their limit, to 2^4:
+// 53 %).
+constexpr float kMost = 8.f, kNear = 2.f;
 // Work-line slots that stand for a segment's fixed cost.
 constexpr int kOverhead = 6;
 
@@ -71,11 +73,14 @@ struct Fp8Args {
     unsigned long long wait_ns;
 };
 
-// Shared memory and TMEM of a CTA for D-wide heads and tiles of up to R rows.
-template <int D, int R>
+// Shared memory and TMEM of a CTA for D-wide heads and tiles of up to R rows,
+// split over WG softmax warpgroups.
+template <int D, int R, int WG>
 struct Shape {
     static constexpr int N = 2 * R;                   // columns: both halves of each row
-    static constexpr int HALF = R / 2;                // rows of a warpgroup
+    static constexpr int H = R / WG;                  // rows of a warpgroup
+    static constexpr int WARPS = 4 * WG;              // softmax warps
+    static constexpr int THREADS = 32 * (WARPS + 2);  // and the copy and MMA warps
     static constexpr int TILE = kKeys * D;            // K (or V) codes of a block
     static constexpr int STAGE = 2 * TILE;
     static constexpr int Q_BYTES = N * D < 1024 ? 1024 : N * D;
@@ -93,7 +98,7 @@ struct Shape {
     static constexpr int OFF_ALPHA = OFF_REF + R * 4;           // its last change, as a factor
     static constexpr int OFF_WMAX = OFF_ALPHA + R * 4;          // [4][R]: maxima / sums by warp
     static constexpr int OFF_MISC = OFF_WMAX + 4 * R * 4;
-    static constexpr int OFF_BAR = OFF_MISC + 64;
+    static constexpr int OFF_BAR = OFF_MISC + 256;
     // barriers
     static constexpr int KV_FULL = 0;
     static constexpr int KV_EMPTY = NS;
@@ -113,7 +118,7 @@ struct Shape {
     static constexpr int NB = 3 * N <= 512 ? 2 : 1;
     static constexpr int TM_S = 0;
     static constexpr int TM_O = NB * N;
-    static_assert(R % 16 == 0 && R <= kRows, "rows of a tile");
+    static_assert(R % WG == 0 && H % 8 == 0 && R <= kRows, "rows of a tile");
     static_assert((NB + 1) * N <= 512, "TMEM budget");
     static_assert(NS >= 3 && SMEM <= 227 * 1024, "shared memory budget");
     static_assert(SMEM > 114 * 1024, "one CTA per SM keeps TMEM allocation uncontended");
@@ -123,10 +128,11 @@ struct Shape {
 struct Misc {
     uint32_t tmem_base;
     int abort;
-    uint32_t qmax[kSoftWarps];  // largest |q| bits seen by each warp
-    uint64_t vote[2];           // a byte per warp: an exponent left its range
+    int pad[2];
+    uint8_t vote[2][32];  // by warp: an exponent left its range
+    uint32_t qmax[32];    // by warp: the largest |q| bits seen
 };
-static_assert(sizeof(Misc) <= 64, "Misc fits its slot");
+static_assert(sizeof(Misc) <= 256, "Misc fits its slot");
 
 // tcgen05 instruction descriptor of kind::f8f6f4, e4m3 A and B, fp32 D.
 TA_HD uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
@@ -204,9 +210,8 @@ __device__ Range plan_range(const Fp8Args& a, int lane) {
 }
 
 // Sums over the 32 lanes of NC columns held one value per lane and column.
-// Afterwards v[i] of lane l is the sum of column 32 i + l (NC = 32 k), or, with
-// fewer than 32 columns, of column l % NC.  Each exchange halves the columns a
-// lane still holds.
+// Afterwards v[i] of lane l is the sum of column 32 i + l, for columns below NC.
+// Each exchange halves the columns a lane still holds.
 template <int NC>
 __device__ __forceinline__ void column_sums(float* v, int lane) {
     if constexpr (NC > 32) {
@@ -216,7 +221,7 @@ __device__ __forceinline__ void column_sums(float* v, int lane) {
     } else if constexpr (NC == 24) {
         column_sums<16>(v, lane);
         column_sums<8>(v + 16, lane);
-        if ((lane & 31) >= 16) v[0] = v[16];
+        if (lane >= 16) v[0] = v[16];
     } else {
         static_assert(NC == 8 || NC == 16 || NC == 32, "columns");
 #pragma unroll
@@ -234,6 +239,29 @@ __device__ __forceinline__ void column_sums(float* v, int lane) {
     }
 }
 
+// x = hi + lo / 16 for one key and the H rows of a warpgroup: 2 H columns, the
+// hi halves first.
+template <int H>
+__device__ __forceinline__ void load_scores(uint32_t ta, float* x) {
+    const uint64_t sixteenth = ptx::f2_pack(0.0625f, 0.0625f);
+    constexpr int CH = H > 40 ? 32 : H;  // columns in flight
+#pragma unroll
+    for (int c0 = 0; c0 < H; c0 += CH) {
+        float y[CH];
+#pragma unroll
+        for (int c = 0; c < CH; c += 8) {
+            ptx::tmem_ld8(ta + c0 + c, x + c0 + c);
+            ptx::tmem_ld8(ta + H + c0 + c, y + c);
+        }
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < CH; i += 2)
+            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(y[i], y[i + 1]), sixteenth,
+                                       ptx::f2_pack(x[c0 + i], x[c0 + i + 1])),
+                           x[c0 + i], x[c0 + i + 1]);
+    }
+}
+
 // fp32 to an int that orders the same way, NaN lowest; and back.
 __device__ __forceinline__ int ordered(float x) {
     const int b = __float_as_int(x == x ? x : kNegInf);
@@ -247,11 +275,12 @@ __device__ __forceinline__ int blocks_of(const Segment& sg) {
     return (sg.chunk_end - sg.chunk_begin + 1) / 2;
 }
 
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int R, int WG>
+__global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
     prefix_fp8_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Fp8Args a) {
-    using S = Shape<D, R>;
+    using S = Shape<D, R, WG>;
+    constexpr int kWarpTma = S::WARPS, kWarpMma = S::WARPS + 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -270,17 +299,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(S::S_FULL + i), 1);
-            ptx::mbar_init(bar(S::S_FREE + i), kSoftWarps);
-            ptx::mbar_init(bar(S::P_FULL + i), kSoftWarps);
+            ptx::mbar_init(bar(S::S_FREE + i), S::WARPS);
+            ptx::mbar_init(bar(S::P_FULL + i), S::WARPS);
             ptx::mbar_init(bar(S::P_FREE + i), 1);
         }
         ptx::mbar_init(bar(S::O_FULL), 1);
-        ptx::mbar_init(bar(S::O_FREE), kSoftWarps);
-        ptx::mbar_init(bar(S::Q_FULL), kSoftWarps);
-        ptx::mbar_init(bar(S::CHECK), kSoftWarps);
-        ptx::mbar_init(bar(S::MEET), kSoftWarps);
+        ptx::mbar_init(bar(S::O_FREE), S::WARPS);
+        ptx::mbar_init(bar(S::Q_FULL), S::WARPS);
+        ptx::mbar_init(bar(S::CHECK), S::WARPS);
+        ptx::mbar_init(bar(S::MEET), S::WARPS);
         ptx::mbar_init(bar(S::DRAIN), 1);
         misc->abort = 0;
+        for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(misc->vote)[i] = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tm_k);
         ptx::prefetch_tmap(&tm_v);
@@ -308,84 +338,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp == kWarpTma) {
-        // ================= copies (one thread)
-        if (lane == 0) {
-            const int Pb = a.P < kChunk ? a.P : kChunk;  // tokens per box
-            const int nsub = kChunk / Pb;
-            const int pshift = __ffs(a.P) - 1;
-            uint32_t jj = 0;
-            bool ok = true;
-            Segment sg;
-            while (ok && w.next(sg)) {
-                bool bad;
-                const int L = clamp_seq_len(sg.len_raw, a.P, a.max_pages, bad);
-                const int npages = (L + a.P - 1) / a.P;
-                const int32_t* table = a.block_table + static_cast<size_t>(sg.b) * a.max_pages;
+        // ================= copies: lane k < 8 takes box k of a block
+        const int Pb = a.P < kChunk ? a.P : kChunk;  // tokens per box
+        const int nsub = kChunk / Pb;                // boxes per 64-token step
+        const int pshift = __ffs(a.P) - 1;
+        const int hh = (lane >> 2) & 1, sub = lane & 3;
+        uint32_t jj = 0;
+        bool ok = true;
+        Segment sg;
+        while (ok && w.next(sg)) {
+            bool bad;
+            const int L = clamp_seq_len(sg.len_raw, a.P, a.max_pages, bad);
+            const int npages = (L + a.P - 1) >> pshift;
+            const int32_t* table = a.block_table + static_cast<size_t>(sg.b) * a.max_pages;
+            // 64 table entries from `base` on, two to a lane: looked up long
+            // before the block that uses them.
+            int base = (sg.chunk_begin * kChunk) >> pshift;
+            auto look = [&](int i) -> int { return i < npages ? table[i] : -1; };
+            int near_ = look(base + lane), far_ = look(base + 32 + lane);
 #pragma unroll 1
-                for (int ch = sg.chunk_begin; ch < sg.chunk_end; ch += 2, ++jj) {
-                    // All page lookups of the block go out before the wait for
-                    // its stage.
-                    const int nh = min(2, sg.chunk_end - ch);
-                    int pid[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int hh = k >> 2, i = k & 3;
-                        const int lp = ((ch + hh) * kChunk + i * Pb) >> pshift;
-                        const bool use = hh < nh && i < nsub && lp < npages;
-                        pid[k] = use ? table[lp] : -2;
-                    }
-                    const int s = jj % S::NS;
-                    if (jj >= S::NS &&
-                        !ptx::mbar_wait(bar(S::KV_EMPTY + s), ((jj / S::NS) - 1) & 1, a.wait_ns)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    if (*abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    int nl = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (pid[k] == -2) continue;
-                        if (pid[k] < 0 || pid[k] >= a.num_pages) {
-                            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-                            pid[k] = -2;
-                        } else {
-                            ++nl;
-                        }
-                    }
-                    const uint32_t fb = bar(S::KV_FULL + s);
-                    if (nl > 0)
-                        ptx::mbar_arrive_expect_tx(fb, static_cast<uint32_t>(nl * Pb * 2 * (D + 1)));
+            for (int ch = sg.chunk_begin; ch < sg.chunk_end; ch += 2, ++jj) {
+                if (((ch * kChunk) >> pshift) - base >= 32) {
+                    base += 32;
+                    near_ = far_;
+                    far_ = look(base + 32 + lane);
+                }
+                const int tok = (ch + hh) * kChunk + sub * Pb;
+                const int lp = tok >> pshift;
+                const int at = lp - base;
+                const int p0 = __shfl_sync(kFull, near_, at & 31);
+                const int p1 = __shfl_sync(kFull, far_, at & 31);
+                const int pid = at < 32 ? p0 : p1;
+                bool use = lane < 8 && ch + hh < sg.chunk_end && sub < nsub && lp < npages;
+                if (use && (pid < 0 || pid >= a.num_pages)) {
+                    report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                    use = false;
+                }
+                const int n = __popc(__ballot_sync(kFull, use));
+                const int s = jj % S::NS;
+                if (jj >= S::NS &&
+                    !__all_sync(kFull, ptx::mbar_wait(bar(S::KV_EMPTY + s), ((jj / S::NS) - 1) & 1,
+                                                      a.wait_ns))) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                if (__any_sync(kFull, *abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = bar(S::KV_FULL + s);
+                if (lane == 0) {
+                    if (n > 0)
+                        ptx::mbar_arrive_expect_tx(fb, static_cast<uint32_t>(n * Pb * 2 * (D + 1)));
                     else
                         ptx::mbar_arrive(fb);
+                }
+                __syncwarp();
+                if (use) {
                     const uint32_t kst = sb + S::OFF_STAGE + s * S::STAGE;
                     const uint32_t sst = sb + S::OFF_SCALE + s * 2 * kKeys;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (pid[k] == -2) continue;
-                        const int hh = k >> 2, i = k & 3;
-                        const int tok = (ch + hh) * kChunk + i * Pb;
-                        const int y = (pid[k] * a.Hkv + sg.hk) * a.P + (tok & (a.P - 1));
-                        const int row = hh * kChunk + i * Pb;
-                        ptx::tma_load_2d(kst + row * D, &tm_k, 0, y, fb, pol);
-                        ptx::tma_load_2d(kst + S::TILE + row * D, &tm_v, 0, y, fb, pol);
-                        ptx::bulk_load(sst + row, a.k_scales + y, Pb, fb);
-                        ptx::bulk_load(sst + kKeys + row, a.v_scales + y, Pb, fb);
-                    }
+                    const int y = (pid * a.Hkv + sg.hk) * a.P + (tok & (a.P - 1));
+                    const int row = hh * kChunk + sub * Pb;
+                    ptx::tma_load_2d(kst + row * D, &tm_k, 0, y, fb, pol);
+                    ptx::bulk_load(sst + row, a.k_scales + y, Pb, fb);
+                    ptx::bulk_load(sst + kKeys + row, a.v_scales + y, Pb, fb);
+                    ptx::tma_load_2d(kst + S::TILE + row * D, &tm_v, 0, y, fb, pol);
                 }
-            }
-            if (!ok) {
-                const uint32_t first = jj > S::NS ? jj - S::NS : 0;
-                for (uint32_t j = first; j < jj; ++j)
-                    (void)ptx::mbar_wait(bar(S::KV_FULL + j % S::NS), (j / S::NS) & 1,
-                                         ptx::kDrainLimitNs);
+                __syncwarp();
             }
         }
+        if (!ok) {
+            const uint32_t first = jj > S::NS ? jj - S::NS : 0;
+            for (uint32_t j = first; j < jj; ++j)
+                (void)ptx::mbar_wait(bar(S::KV_FULL + j % S::NS), (j / S::NS) & 1,
+                                     ptx::kDrainLimitNs);
+        }
     } else if (warp == kWarpMma) {
-        // ================= MMA issuer: the whole warp walks, one lane issues
+        // ================= MMA issuer: the whole warp walks, one lane issues.
+        // It polls without waiting: a suspended poll for P would hold up the
+        // scores of the next block.
         const bool lead = ptx::elect_one();
         const uint32_t id_s = idesc_e4m3_f32(kKeys, S::N, false, false);
         const uint32_t id_o = idesc_e4m3_f32(D, S::N, true, true);
@@ -406,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (np < nq) {
                     const uint32_t j = jj + np;
                     const bool go =
-                        ptx::mbar_try_wait(bar(S::P_FULL + (j & 1)), (j >> 1) & 1) &&
-                        (np > 0 || kk == 0 || ptx::mbar_try_wait(bar(S::O_FREE), (kk - 1) & 1));
+                        ptx::mbar_test(bar(S::P_FULL + (j & 1)), (j >> 1) & 1) &&
+                        (np > 0 || kk == 0 || ptx::mbar_test(bar(S::O_FREE), (kk - 1) & 1));
                     if (__all_sync(kFull, go)) {
                         ptx::tc_fence_after();
                         const uint32_t vst =
@@ -436,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int s = j % S::NS;
                     const int sbuf = j % S::NB;
                     const bool go =
-                        ptx::mbar_try_wait(bar(S::KV_FULL + s), (j / S::NS) & 1) &&
+                        ptx::mbar_test(bar(S::KV_FULL + s), (j / S::NS) & 1) &&
                         (j < S::NB ||
-                         ptx::mbar_try_wait(bar(S::S_FREE + sbuf), ((j / S::NB) - 1) & 1));
+                         ptx::mbar_test(bar(S::S_FREE + sbuf), ((j / S::NB) - 1) & 1));
                     if (__all_sync(kFull, go)) {
                         ptx::tc_fence_after();
                         const uint32_t kst = sb + S::OFF_STAGE + s * S::STAGE;
@@ -480,20 +512,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         (void)ptx::mbar_wait(bar(S::DRAIN), 0, ptx::kDrainLimitNs);
     } else {
-        // ================= softmax and epilogue (two warpgroups)
-        constexpr int H = S::HALF;  // this warpgroup's rows
+        // ================= softmax and epilogue
+        constexpr int H = S::H;     // this warpgroup's rows
         const int wg = warp >> 2;
         const int quad = warp & 3;  // the TMEM lanes this warp reaches
         const int key = quad * 32 + lane;
         const int row0 = wg * H;    // first row of the tile taken here
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        float* ref = reinterpret_cast<float*>(smem + S::OFF_REF);
+        float* nref = reinterpret_cast<float*>(smem + S::OFF_REF);  // minus each row's reference
         float* alpha = reinterpret_cast<float*>(smem + S::OFF_ALPHA);
         float* wmax = reinterpret_cast<float*>(smem + S::OFF_WMAX);  // [4][R]
         auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
-            const bool ok = ptx::mbar_wait(b, parity, a.wait_ns);
-            const bool all = __all_sync(kFull, ok && !*abort_flag);
-            if (!ok) fail();
+            // A role that gave up leaves its barriers unfinished, so those who
+            // wait for it give up within the limit too.
+            const bool all = __all_sync(kFull, ptx::mbar_wait(b, parity, a.wait_ns));
+            if (!all) fail();
             return all;
         };
         uint32_t met = 0;  // meetings of the softmax warps so far
@@ -518,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float c_scale;
             {
                 constexpr int LPR = D / 8;                   // lanes per row
-                constexpr int STEP = kSoftWarps * 32 / LPR;  // rows per pass
+                constexpr int STEP = S::WARPS * 32 / LPR;    // rows per pass
                 constexpr int NP = (R + STEP - 1) / STEP;
                 const int r0 = threadIdx.x / LPR, gl = threadIdx.x % LPR;
                 uint4 x[NP];
@@ -549,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
 #pragma unroll
-                for (int i = 0; i < kSoftWarps; ++i) m = max(m, misc->qmax[i]);
+                for (int i = 0; i < S::WARPS; ++i) m = max(m, misc->qmax[i]);
                 int kq = m == 0 ? 0 : 134 - static_cast<int>(m >> 23);
                 kq = kq > 100 ? 100 : kq;
                 const float up = __int_as_float((127 + kq) << 23);
@@ -574,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lo[u] = e4m3x2((v0 - b.x) * 16.f, (v1 - b.y) * 16.f);
                     }
                     // tile rows: the hi halves of a warpgroup's rows, then the lo halves
-                    const int n = (r / H) * R + r % H;
+                    const int n = (r / H) * 2 * H + r % H;
                     *reinterpret_cast<uint2*>(qs + tile_offset<D>(n, gl >> 1) + (gl & 1) * 8) =
                         make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
                     *reinterpret_cast<uint2*>(qs + tile_offset<D>(n + H, gl >> 1) +
@@ -596,41 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int keys = min(nh * kChunk, L - ch * kChunk);
                 const bool valid = key < keys;
                 const uint32_t sbuf = jj % S::NB;
-                if (!wait_all(bar(S::S_FULL + sbuf), (jj / S::NB) & 1)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                // x = hi + lo / 16 for this thread's key and rows
-                float x[H];
-                {
-                    const uint32_t ta = lanes + S::TM_S + sbuf * S::N + wg * R;
-                    const uint64_t sixteenth = ptx::f2_pack(0.0625f, 0.0625f);
-                    constexpr int CH = H > 40 ? 32 : H;  // columns in flight
-#pragma unroll
-                    for (int c0 = 0; c0 < H; c0 += CH) {
-                        float y[CH];
-#pragma unroll
-                        for (int c = 0; c < CH; c += 8) {
-                            ptx::tmem_ld8(ta + c0 + c, x + c0 + c);
-                            ptx::tmem_ld8(ta + H + c0 + c, y + c);
-                        }
-                        ptx::tmem_wait_ld();
-                        if (c0 + CH == H) {
-                            ptx::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(bar(S::S_FREE + sbuf));
-                        }
-#pragma unroll
-                        for (int i = 0; i < CH; i += 2)
-                            ptx::f2_unpack(
-                                ptx::f2_fma(ptx::f2_pack(y[i], y[i + 1]), sixteenth,
-                                            ptx::f2_pack(x[c0 + i], x[c0 + i + 1])),
-                                x[c0 + i], x[c0 + i + 1]);
-                    }
-                }
-                // The key's scales.  The S product was made from this stage, so
-                // its copies have landed; this wait makes them visible here.
+                // The key's scales (landed well before the scores are made).
                 if (!wait_all(bar(S::KV_FULL + jj % S::NS), (jj / S::NS) & 1)) {
                     ok = false;
                     break;
@@ -642,143 +641,185 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float wkey = inv_scale_of(vbyte);
                 const uint64_t F2 = ptx::f2_pack(F, F);
                 const uint64_t vs2 = ptx::f2_pack(vs, vs);
-                // e = F x + scale of v: once more where the references moved
-                bool redo = first;
-                if (!first) {
-                    float top = kNegInf;
-#pragma unroll
-                    for (int i = 0; i < H; i += 2) {
-                        const float2 rf = *reinterpret_cast<const float2*>(ref + row0 + i);
-                        float e0, e1;
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), F2,
-                                                   ptx::f2_add(vs2, ptx::f2_pack(-rf.x, -rf.y))),
-                                       e0, e1);
-                        top = ptx::fmax3(top, e0, e1);
-                    }
-                    const bool over = __any_sync(kFull, valid && top > kMost);
-                    if (lane == 0)
-                        reinterpret_cast<volatile uint8_t*>(&misc->vote[jj & 1])[warp] = over;
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(S::CHECK));
+                const uint64_t sixteen = ptx::f2_pack(16.f, 16.f);
+                const uint32_t ta = lanes + S::TM_S + sbuf * S::N + wg * 2 * H;
+                if (!wait_all(bar(S::S_FULL + sbuf), (jj / S::NB) & 1)) {
+                    ok = false;
+                    break;
                 }
-                // (the vote of block j of a segment is its j-th; first blocks hold none)
-                if (!first) {
-                    if (!wait_all(bar(S::CHECK), (jj - kk - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    redo = *reinterpret_cast<volatile uint64_t*>(&misc->vote[jj & 1]) != 0;
-                }
-                if (redo) {
-                    // Largest e of every row, by warp, then by tile.
-#pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const float e = valid ? fmaf(x[i], F, vs) : kNegInf;
-                        const int o = __reduce_max_sync(kFull, ordered(e));
-                        if (lane == (i & 31)) wmax[quad * R + row0 + i] = unordered(o);
-                    }
-                    if (!meet()) {
-                        ok = false;
-                        break;
-                    }
-                    const int r = threadIdx.x;
-                    if (r < R) {
-                        const float top = fmaxf(fmaxf(wmax[r], wmax[R + r]),
-                                                fmaxf(wmax[2 * R + r], wmax[3 * R + r]));
-                        const float old = first ? kNegInf : ref[r];
-                        const bool move = first || top > old + kMost;
-                        // a row of NaN scores has no largest: any finite reference
-                        const float now = move ? (top == kNegInf ? 0.f : top - kTop) : old;
-                        ref[r] = now;
-                        alpha[r] = move ? ptx::ex2(old - now) : 1.f;
-                    }
-                    if (!meet()) {
-                        ok = false;
-                        break;
-                    }
-                    if (!first) {
-#pragma unroll
-                        for (int i = 0; i < H; ++i) l[i] *= alpha[row0 + i];
-                        // O holds the blocks before once P.V of the last has completed.
-                        if (!wait_all(bar(S::P_FREE + ((jj - 1) & 1)), ((jj - 1) >> 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        ptx::tc_fence_after();
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                            for (int c = 0; c < H; c += 8) {
-                                const uint32_t to = lanes + S::TM_O + wg * R + half * H + c;
-                                float o[8];
-                                ptx::tmem_ld8(to, o);
-                                ptx::tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) o[i] *= alpha[row0 + c + i];
-                                ptx::tmem_st8(to, o);
-                            }
-                        }
-                        ptx::tmem_wait_st();
-                    }
-                }
+                ptx::tc_fence_after();
                 // P buffer (jj & 1) is free once P.V of block jj - 2 has completed.
                 if (jj >= 2 && !wait_all(bar(S::P_FREE + (jj & 1)), ((jj >> 1) - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                if (key < nh * kChunk) {
-                    // p = 2^(e - ref) as hi and lo; a key past the data has none.
-                    const uint32_t pst = sb + S::OFF_P + (jj & 1) * S::P_BYTES;
-                    const uint64_t w2 = ptx::f2_pack(wkey, wkey);
-                    uint32_t code[R / 4];
-                    uint16_t* c16 = reinterpret_cast<uint16_t*>(code);
-                    const uint64_t sixteen = ptx::f2_pack(16.f, 16.f);
+                const uint32_t prow = sb + S::OFF_P + (jj & 1) * S::P_BYTES;
+                float x[H];  // this key's scores, e, then p
+                // Once, and once more when the references had to move.
+                bool move = first;
+#pragma unroll 1
+                while (true) {
+                    load_scores<H>(ta, x);
+                    const bool moved = move;
+                    if (move) {
+                        // Largest e of every row that stands near its limit, by
+                        // warp, then by tile.
 #pragma unroll
-                    for (int i = 0; i < H; i += 2) {
-                        const float2 rf = *reinterpret_cast<const float2*>(ref + row0 + i);
-                        float e0, e1;
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), F2,
-                                                   ptx::f2_add(vs2, ptx::f2_pack(-rf.x, -rf.y))),
-                                       e0, e1);
-                        const float p0 = valid ? ptx::ex2(e0) : 0.f;
-                        const float p1 = valid ? ptx::ex2(e1) : 0.f;
-                        if (valid)
-                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(p0, p1), w2,
-                                                       ptx::f2_pack(l[i], l[i + 1])),
-                                           l[i], l[i + 1]);
-                        const uint32_t hi = e4m3x2(p0, p1);
-                        const uint32_t back = f16x2_of_e4m3x2(hi);
-                        const __half2 neg = __hmul2(*reinterpret_cast<const __half2*>(&back),
-                                                    __float2half2_rn(-16.f));
-                        const float2 b = __half22float2(neg);
-                        float r0, r1;
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(p0, p1), sixteen,
-                                                   ptx::f2_pack(b.x, b.y)),
-                                       r0, r1);
-                        c16[i / 2] = static_cast<uint16_t>(hi);
-                        c16[(H + i) / 2] = static_cast<uint16_t>(e4m3x2(r0, r1));
+                        for (int i = 0; i < H; ++i) {
+                            const float e = valid ? fmaf(x[i], F, vs) : kNegInf;
+                            const float old = first ? kNegInf : -nref[row0 + i];
+                            float m = kNegInf;
+                            if (__any_sync(kFull, e > old + kNear))
+                                m = unordered(__reduce_max_sync(kFull, ordered(e)));
+                            if (lane == (i & 31)) wmax[quad * R + row0 + i] = m;
+                        }
+                        if (!meet()) {
+                            ok = false;
+                            break;
+                        }
+                        const int r = threadIdx.x;
+                        if (r < R) {
+                            const float top = fmaxf(fmaxf(wmax[r], wmax[R + r]),
+                                                    fmaxf(wmax[2 * R + r], wmax[3 * R + r]));
+                            // (a first block of NaN scores has no largest: any
+                            // finite reference)
+                            const float old = first ? kNegInf : -nref[r];
+                            const float now =
+                                top > old + kNear ? top : (first ? 0.f : old);
+                            nref[r] = -now;
+                            alpha[r] = ptx::ex2(old - now);
+                        }
+                        if (!meet()) {
+                            ok = false;
+                            break;
+                        }
+                        if (!first) {
+                            // O holds the blocks before once P.V of the last has
+                            // completed.
+                            if (!wait_all(bar(S::P_FREE + ((jj - 1) & 1)), ((jj - 1) >> 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            ptx::tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < H; c += 8) {
+                                float al[8];
+                                bool any = false;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    al[i] = alpha[row0 + c + i];
+                                    any |= al[i] != 1.f;
+                                }
+                                if (!any) continue;  // the same for the whole warpgroup
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) l[c + i] *= al[i];
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    const uint32_t to =
+                                        lanes + S::TM_O + wg * 2 * H + half * H + c;
+                                    float o[8];
+                                    ptx::tmem_ld8(to, o);
+                                    ptx::tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) o[i] *= al[i];
+                                    ptx::tmem_st8(to, o);
+                                }
+                            }
+                            ptx::tmem_wait_st();
+                        }
                     }
+                    // e = F x + scale of v - reference
+                    float top = kNegInf;
 #pragma unroll
-                    for (int c = 0; c < R / 16; ++c) {
-                        const int n = wg * (R / 16) + c;  // 16-byte chunk of the key's row
-                        const uint32_t at = pst + (n >> 3) * S::P_ATOM +
-                                            sw128_offset(key, n & 7);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                                     "r"(code[4 * c]), "r"(code[4 * c + 1]), "r"(code[4 * c + 2]),
-                                     "r"(code[4 * c + 3])
-                                     : "memory");
+                    for (int i = 0; i < H; i += 4) {
+                        const float4 nr = *reinterpret_cast<const float4*>(nref + row0 + i);
+#pragma unroll
+                        for (int u = 0; u < 4; u += 2) {
+                            const uint64_t bias =
+                                ptx::f2_add(vs2, u == 0 ? ptx::f2_pack(nr.x, nr.y)
+                                                        : ptx::f2_pack(nr.z, nr.w));
+                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i + u], x[i + u + 1]), F2, bias),
+                                           x[i + u], x[i + u + 1]);
+                            top = ptx::fmax3(top, x[i + u], x[i + u + 1]);
+                        }
                     }
-                    if (!valid && wg == 0) {
-                        // 0 * NaN is not 0: the value rows past the data are cleared.
-                        const uint32_t vrow = sb + S::OFF_STAGE + (jj % S::NS) * S::STAGE +
-                                              S::TILE + key * D;
+                    if (!moved) {
+                        const bool over = __any_sync(kFull, valid && top > kMost);
+                        if (lane == 0) {
+                            *reinterpret_cast<volatile uint8_t*>(&misc->vote[jj & 1][warp]) = over;
+                            ptx::mbar_arrive(bar(S::CHECK));
+                        }
+                    }
+                    // p = 2^e as hi, and lo = 16 (p - hi), into the key's row of the
+                    // P tile; a key past the data has no probability.
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow +
-                                                                                      c * 16),
-                                         "r"(0)
+                    for (int i = 0; i < H; i += 8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int k = i + 2 * u;
+                            x[k] = ptx::ex2(x[k]);
+                            x[k + 1] = ptx::ex2(x[k + 1]);
+                            hi[u] = e4m3x2(x[k], x[k + 1]);
+                            const uint32_t back = f16x2_of_e4m3x2(hi[u]);
+                            const __half2 neg = __hmul2(*reinterpret_cast<const __half2*>(&back),
+                                                        __float2half2_rn(-16.f));
+                            const float2 b = __half22float2(neg);
+                            float r0, r1;
+                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[k], x[k + 1]), sixteen,
+                                                       ptx::f2_pack(b.x, b.y)),
+                                           r0, r1);
+                            lo[u] = e4m3x2(r0, r1);
+                        }
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t* c = half == 0 ? hi : lo;
+                            const int n = wg * 2 * H + half * H + i;  // byte of the key's row
+                            const uint32_t at = prow + (n >> 7) * S::P_ATOM +
+                                                sw128_offset(key, (n >> 4) & 7) + (n & 8);
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
+                                         "r"(valid ? c[0] | (c[1] << 16) : 0u),
+                                         "r"(valid ? c[2] | (c[3] << 16) : 0u)
                                          : "memory");
+                        }
                     }
+                    if (moved) break;
+                    // (the vote of a block is one per block but the first of each segment)
+                    if (!wait_all(bar(S::CHECK), (jj - kk - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint4* v4 = reinterpret_cast<const uint4*>(misc->vote[jj & 1]);
+                    uint32_t votes = 0;
+#pragma unroll
+                    for (int i = 0; i < (S::WARPS + 15) / 16; ++i) {
+                        const uint4 v = v4[i];
+                        votes |= v.x | v.y | v.z | v.w;
+                    }
+                    if (votes == 0) break;
+                    move = true;
+                }
+                if (!ok) break;
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(S::S_FREE + sbuf));
+                if (valid) {
+                    const uint64_t w2 = ptx::f2_pack(wkey, wkey);
+#pragma unroll
+                    for (int i = 0; i < H; i += 2)
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), w2,
+                                                   ptx::f2_pack(l[i], l[i + 1])),
+                                       l[i], l[i + 1]);
+                } else if (wg == 0 && key < nh * kChunk) {
+                    // 0 * NaN is not 0: the value rows past the data are cleared.
+                    const uint32_t vrow = sb + S::OFF_STAGE + (jj % S::NS) * S::STAGE + S::TILE +
+                                          key * D;
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow +
+                                                                                  c * 16),
+                                     "r"(0)
+                                     : "memory");
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
@@ -799,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             {
                 const int r = threadIdx.x;
                 if (r < Mrb) {
-                    slot[r] = ref[r];
+                    slot[r] = -nref[r];
                     slot[kRows + r] = (wmax[r] + wmax[R + r]) + (wmax[2 * R + r] + wmax[3 * R + r]);
                 }
             }
@@ -815,8 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < H; c += 8) {
                 float o[8], o2[8];
-                ptx::tmem_ld8(lanes + S::TM_O + wg * R + c, o);
-                ptx::tmem_ld8(lanes + S::TM_O + wg * R + H + c, o2);
+                ptx::tmem_ld8(lanes + S::TM_O + wg * 2 * H + c, o);
+                ptx::tmem_ld8(lanes + S::TM_O + wg * 2 * H + H + c, o2);
                 ptx::tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -826,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ptx::tc_fence_before();
-            // wmax, ref and Q of this segment have been read when all are here
+            // wmax, nref and Q of this segment have been read when all are here
             if (!meet()) {
                 ok = false;
                 break;
@@ -845,20 +886,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, int R>
+template <int D, int R, int WG>
 cudaError_t launch_prefix_fp8(const Fp8Args& a, const CUtensorMap& tk, const CUtensorMap& tv,
                               int dev, cudaStream_t stream) {
-    using S = Shape<D, R>;
+    using S = Shape<D, R, WG>;
     // Devices on which the shared-memory opt-in has been applied.
     static std::atomic<unsigned long long> configured{0};
     const unsigned long long bit = 1ull << (dev & 63);
     if ((configured.load() & bit) == 0) {
         const cudaError_t e = cudaFuncSetAttribute(
-            prefix_fp8_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+            prefix_fp8_kernel<D, R, WG>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    return launch_dependent(prefix_fp8_kernel<D, R>, dim3(a.n_ctas), dim3(kThreads), S::SMEM,
+    return launch_dependent(prefix_fp8_kernel<D, R, WG>, dim3(a.n_ctas), dim3(S::THREADS), S::SMEM,
                             stream, tk, tv, a);
 }
 
@@ -868,12 +909,12 @@ template <int D>
 cudaError_t launch_prefix_fp8_rows(const Fp8Args& a, const CUtensorMap& tk,
                                    const CUtensorMap& tv, int dev, cudaStream_t stream) {
     const int rows = a.M < kRows ? a.M : kRows;
-    if (rows <= 16) return launch_prefix_fp8<D, 16>(a, tk, tv, dev, stream);
-    if (rows <= 32) return launch_prefix_fp8<D, 32>(a, tk, tv, dev, stream);
-    if (rows <= 48) return launch_prefix_fp8<D, 48>(a, tk, tv, dev, stream);
-    if (rows <= 64) return launch_prefix_fp8<D, 64>(a, tk, tv, dev, stream);
-    if (rows <= 80) return launch_prefix_fp8<D, 80>(a, tk, tv, dev, stream);
-    return launch_prefix_fp8<D, 128>(a, tk, tv, dev, stream);
+    if (rows <= 16) return launch_prefix_fp8<D, 16, 2>(a, tk, tv, dev, stream);
+    if (rows <= 32) return launch_prefix_fp8<D, 32, 2>(a, tk, tv, dev, stream);
+    if (rows <= 48) return launch_prefix_fp8<D, 48, 2>(a, tk, tv, dev, stream);
+    if (rows <= 64) return launch_prefix_fp8<D, 64, 2>(a, tk, tv, dev, stream);
+    if (rows <= 80) return launch_prefix_fp8<D, 80, 2>(a, tk, tv, dev, stream);
+    return launch_prefix_fp8<D, 128, 2>(a, tk, tv, dev, stream);
 }
 
 // The [num_pages * Hkv * P][d] codes of a pool in boxes of up to 64 tokens.
