@@ -41,6 +41,13 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
+// The same from an fp16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+
 // Two e4m3 codes as fp16 pairs (exact): the low code in the low half.
 __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t codes) {
     uint32_t r;

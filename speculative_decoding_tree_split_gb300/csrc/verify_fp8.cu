@@ -11,9 +11,10 @@
 //   S^T = K Q^T     (128 keys x rows; A = K tile, B = Q)
 //   O^T += V^T P^T  (d x rows;        A = V tile, B = P)
 // * A query row and a row of probabilities enter as two e4m3 rows each, the
-//   rounded value and sixteen times what is left of it: together nine
-//   significant bits, as much as bf16 has.  Both halves are columns of the same
-//   B operand, so a product is still four instructions (d = 128).
+//   rounded value (hi) and what is left of it (lo): together nine significant
+//   bits, as much as bf16 has.  Scores sum both halves in one accumulator; the
+//   lo half of the probabilities is held sixteenfold, for four more binades,
+//   and has columns of its own.
 // * A TMEM lane is a key, so a key's scales are scalars of the thread that
 //   holds it, and the softmax has no idle lanes however few rows there are.
 // * The value scale joins the exponent: e = x + scale of v_j, p = 2^(e - ref),
@@ -77,7 +78,7 @@ struct Fp8Args {
 // split over WG softmax warpgroups.
 template <int D, int R, int WG>
 struct Shape {
-    static constexpr int N = 2 * R;                   // columns: both halves of each row
+    static constexpr int N = 2 * R;                   // both halves of each row
     static constexpr int H = R / WG;                  // rows of a warpgroup
     static constexpr int WARPS = 4 * WG;              // softmax warps
     static constexpr int THREADS = 32 * (WARPS + 2);  // and the copy and MMA warps
@@ -114,12 +115,12 @@ struct Shape {
     static constexpr int DRAIN = S_FULL + 13;
     static constexpr int NBAR = S_FULL + 14;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
-    // TMEM columns: S in two buffers where they fit, then O.
-    static constexpr int NB = 3 * N <= 512 ? 2 : 1;
+    // TMEM columns: S in two buffers, then O.
+    static constexpr int NB = 2;
     static constexpr int TM_S = 0;
-    static constexpr int TM_O = NB * N;
+    static constexpr int TM_O = NB * R;
     static_assert(R % WG == 0 && H % 8 == 0 && R <= kRows, "rows of a tile");
-    static_assert((NB + 1) * N <= 512, "TMEM budget");
+    static_assert(NB * R + N <= 512, "TMEM budget");
     static_assert(NS >= 3 && SMEM <= 227 * 1024, "shared memory budget");
     static_assert(SMEM > 114 * 1024, "one CTA per SM keeps TMEM allocation uncontended");
     static_assert(OFF_BAR + NBAR * 8 - OFF_SCALE <= SMALL, "small arrays fit their room");
@@ -209,18 +210,18 @@ __device__ Range plan_range(const Fp8Args& a, int lane) {
     return r;
 }
 
-// Sums over the 32 lanes of NC columns held one value per lane and column.
-// Afterwards v[i] of lane l is the sum of column 32 i + l, for columns below NC.
-// Each exchange halves the columns a lane still holds.
-template <int NC>
-__device__ __forceinline__ void column_sums(float* v, int lane) {
+// Reduces NC columns, held one value per lane and column, over the 32 lanes
+// (op: of two values).  Afterwards v[i] of lane l is that of column 32 i + l, for
+// columns below NC.  Each exchange halves the columns a lane still holds.
+template <int NC, typename Op>
+__device__ __forceinline__ void reduce_columns(float* v, int lane, Op op) {
     if constexpr (NC > 32) {
-        column_sums<32>(v, lane);
-        column_sums<NC - 32>(v + 32, lane);
+        reduce_columns<32>(v, lane, op);
+        reduce_columns<NC - 32>(v + 32, lane, op);
         v[1] = v[32];
     } else if constexpr (NC == 24) {
-        column_sums<16>(v, lane);
-        column_sums<8>(v + 16, lane);
+        reduce_columns<16>(v, lane, op);
+        reduce_columns<8>(v + 16, lane, op);
         if (lane >= 16) v[0] = v[16];
     } else {
         static_assert(NC == 8 || NC == 16 || NC == 32, "columns");
@@ -231,44 +232,25 @@ __device__ __forceinline__ void column_sums(float* v, int lane) {
             for (int i = 0; i < w; ++i) {
                 const float send = up ? v[i] : v[i + w];
                 const float keep = up ? v[i + w] : v[i];
-                v[i] = keep + __shfl_xor_sync(kFull, send, w);
+                v[i] = op(keep, __shfl_xor_sync(kFull, send, w));
             }
         }
 #pragma unroll
-        for (int w = NC; w < 32; w <<= 1) v[0] += __shfl_xor_sync(kFull, v[0], w);
+        for (int w = NC; w < 32; w <<= 1) v[0] = op(v[0], __shfl_xor_sync(kFull, v[0], w));
     }
 }
 
-// x = hi + lo / 16 for one key and the H rows of a warpgroup: 2 H columns, the
-// hi halves first.
+// The scores of one key and H rows.
 template <int H>
 __device__ __forceinline__ void load_scores(uint32_t ta, float* x) {
-    const uint64_t sixteenth = ptx::f2_pack(0.0625f, 0.0625f);
-    constexpr int CH = H > 40 ? 32 : H;  // columns in flight
+    static_assert(H % 8 == 0, "columns");
 #pragma unroll
-    for (int c0 = 0; c0 < H; c0 += CH) {
-        float y[CH];
-#pragma unroll
-        for (int c = 0; c < CH; c += 8) {
-            ptx::tmem_ld8(ta + c0 + c, x + c0 + c);
-            ptx::tmem_ld8(ta + H + c0 + c, y + c);
-        }
-        ptx::tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < CH; i += 2)
-            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(y[i], y[i + 1]), sixteenth,
-                                       ptx::f2_pack(x[c0 + i], x[c0 + i + 1])),
-                           x[c0 + i], x[c0 + i + 1]);
-    }
-}
-
-// fp32 to an int that orders the same way, NaN lowest; and back.
-__device__ __forceinline__ int ordered(float x) {
-    const int b = __float_as_int(x == x ? x : kNegInf);
-    return b ^ ((b >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float unordered(int o) {
-    return __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
+    for (int c = 0; c < H / 32; ++c) ptx::tmem_ld32(ta + 32 * c, x + 32 * c);
+    constexpr int c16 = H / 32 * 32;
+    if constexpr (H % 32 >= 16) ptx::tmem_ld16(ta + c16, x + c16);
+    constexpr int c8 = H / 16 * 16;
+    if constexpr (H % 16 == 8) ptx::tmem_ld8(ta + c8, x + c8);
+    ptx::tmem_wait_ld();
 }
 
 __device__ __forceinline__ int blocks_of(const Segment& sg) {
@@ -419,7 +401,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         // It polls without waiting: a suspended poll for P would hold up the
         // scores of the next block.
         const bool lead = ptx::elect_one();
-        const uint32_t id_s = idesc_e4m3_f32(kKeys, S::N, false, false);
+        const uint32_t id_s = idesc_e4m3_f32(kKeys, R, false, false);
         const uint32_t id_o = idesc_e4m3_f32(D, S::N, true, true);
         uint32_t jj = 0, kk = 0;
         bool ok = true;
@@ -476,11 +458,13 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                         const uint32_t kst = sb + S::OFF_STAGE + s * S::STAGE;
                         if (lead) {
 #pragma unroll
-                            for (int k = 0; k < D / 32; ++k)
-                                ptx::mma_f8(tmem + S::TM_S + sbuf * S::N,
-                                            tile_desc<D>(kst + k * 32),
-                                            tile_desc<D>(sb + S::OFF_Q + k * 32), id_s,
-                                            k > 0 ? 1u : 0u);
+                            for (int k = 0; k < 2 * D / 32; ++k) {
+                                const int kd = k % (D / 32);  // the hi rows, then the lo rows
+                                ptx::mma_f8(tmem + S::TM_S + sbuf * R, tile_desc<D>(kst + kd * 32),
+                                            tile_desc<D>(sb + S::OFF_Q + (k / (D / 32)) * R * D +
+                                                         kd * 32),
+                                            id_s, k > 0 ? 1u : 0u);
+                            }
                             ptx::mma_commit(bar(S::S_FULL + sbuf));
                         }
                         __syncwarp();
@@ -546,8 +530,8 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             const int L = clamp_seq_len(cur.len_raw, a.P, a.max_pages, bad);
             const int Mrb = min(kRows, a.M - cur.rb * kRows);  // query rows of the tile
             // ---- the tile's queries: a common power of two brings the largest
-            // |q| into [128, 256); each value is held as hi (e4m3) and
-            // lo = 16 (value - hi), which is exact down to 2^-9 / 16.
+            // |q| into [128, 256); each value is held as hi + lo, exactly down to
+            // 2^-2 and to 2^-10 below (2^-17 of the largest).
             float c_scale;
             {
                 constexpr int LPR = D / 8;                   // lanes per row
@@ -604,14 +588,13 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                         hi[u] = e4m3x2(v0, v1);
                         const uint32_t hh = f16x2_of_e4m3x2(hi[u]);
                         const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-                        lo[u] = e4m3x2((v0 - b.x) * 16.f, (v1 - b.y) * 16.f);
+                        lo[u] = e4m3x2(v0 - b.x, v1 - b.y);
                     }
-                    // tile rows: the hi halves of a warpgroup's rows, then the lo halves
-                    const int n = (r / H) * 2 * H + r % H;
-                    *reinterpret_cast<uint2*>(qs + tile_offset<D>(n, gl >> 1) + (gl & 1) * 8) =
+                    // tile rows: all hi halves, then all lo halves
+                    uint8_t* at = qs + tile_offset<D>(r, gl >> 1) + (gl & 1) * 8;
+                    *reinterpret_cast<uint2*>(at) =
                         make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-                    *reinterpret_cast<uint2*>(qs + tile_offset<D>(n + H, gl >> 1) +
-                                              (gl & 1) * 8) =
+                    *reinterpret_cast<uint2*>(at + R * D) =
                         make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
                 }
                 ptx::fence_proxy_async_smem();
@@ -641,8 +624,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 const float wkey = inv_scale_of(vbyte);
                 const uint64_t F2 = ptx::f2_pack(F, F);
                 const uint64_t vs2 = ptx::f2_pack(vs, vs);
-                const uint64_t sixteen = ptx::f2_pack(16.f, 16.f);
-                const uint32_t ta = lanes + S::TM_S + sbuf * S::N + wg * 2 * H;
+                const uint32_t ta = lanes + S::TM_S + sbuf * R + row0;
                 if (!wait_all(bar(S::S_FULL + sbuf), (jj / S::NB) & 1)) {
                     ok = false;
                     break;
@@ -662,17 +644,15 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                     load_scores<H>(ta, x);
                     const bool moved = move;
                     if (move) {
-                        // Largest e of every row that stands near its limit, by
-                        // warp, then by tile.
+                        // Largest e of every row, by warp, then by tile (fmaxf
+                        // passes over NaN).
 #pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            const float e = valid ? fmaf(x[i], F, vs) : kNegInf;
-                            const float old = first ? kNegInf : -nref[row0 + i];
-                            float m = kNegInf;
-                            if (__any_sync(kFull, e > old + kNear))
-                                m = unordered(__reduce_max_sync(kFull, ordered(e)));
-                            if (lane == (i & 31)) wmax[quad * R + row0 + i] = m;
-                        }
+                        for (int i = 0; i < H; ++i) x[i] = valid ? fmaf(x[i], F, vs) : kNegInf;
+                        reduce_columns<H>(x, lane, [](float p, float q) { return fmaxf(p, q); });
+#pragma unroll
+                        for (int i = 0; i < (H + 31) / 32; ++i)
+                            if (i * 32 + lane < H) wmax[quad * R + row0 + i * 32 + lane] = x[i];
+                        load_scores<H>(ta, x);
                         if (!meet()) {
                             ok = false;
                             break;
@@ -760,16 +740,13 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                             const int k = i + 2 * u;
                             x[k] = ptx::ex2(x[k]);
                             x[k + 1] = ptx::ex2(x[k + 1]);
-                            hi[u] = e4m3x2(x[k], x[k + 1]);
+                            const __half2 ph = __floats2half2_rn(x[k], x[k + 1]);
+                            hi[u] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&ph));
                             const uint32_t back = f16x2_of_e4m3x2(hi[u]);
-                            const __half2 neg = __hmul2(*reinterpret_cast<const __half2*>(&back),
-                                                        __float2half2_rn(-16.f));
-                            const float2 b = __half22float2(neg);
-                            float r0, r1;
-                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[k], x[k + 1]), sixteen,
-                                                       ptx::f2_pack(b.x, b.y)),
-                                           r0, r1);
-                            lo[u] = e4m3x2(r0, r1);
+                            const __half2 rest =
+                                __hfma2(*reinterpret_cast<const __half2*>(&back),
+                                        __float2half2_rn(-16.f), __hmul2(ph, __float2half2_rn(16.f)));
+                            lo[u] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rest));
                         }
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -828,7 +805,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             }
             if (!ok) break;
             // ---- epilogue: the rows' sums over the key lanes, then O.
-            column_sums<H>(l, lane);
+            reduce_columns<H>(l, lane, [](float p, float q) { return p + q; });
 #pragma unroll
             for (int i = 0; i < (H + 31) / 32; ++i)
                 if (i * 32 + lane < H) wmax[quad * R + row0 + i * 32 + lane] = l[i];
@@ -911,10 +888,10 @@ cudaError_t launch_prefix_fp8_rows(const Fp8Args& a, const CUtensorMap& tk,
     const int rows = a.M < kRows ? a.M : kRows;
     if (rows <= 16) return launch_prefix_fp8<D, 16, 2>(a, tk, tv, dev, stream);
     if (rows <= 32) return launch_prefix_fp8<D, 32, 2>(a, tk, tv, dev, stream);
-    if (rows <= 48) return launch_prefix_fp8<D, 48, 2>(a, tk, tv, dev, stream);
-    if (rows <= 64) return launch_prefix_fp8<D, 64, 2>(a, tk, tv, dev, stream);
-    if (rows <= 80) return launch_prefix_fp8<D, 80, 2>(a, tk, tv, dev, stream);
-    return launch_prefix_fp8<D, 128, 2>(a, tk, tv, dev, stream);
+    if (rows <= 48) return launch_prefix_fp8<D, 48, 3>(a, tk, tv, dev, stream);
+    if (rows <= 64) return launch_prefix_fp8<D, 64, 4>(a, tk, tv, dev, stream);
+    if (rows <= 80) return launch_prefix_fp8<D, 80, 5>(a, tk, tv, dev, stream);
+    return launch_prefix_fp8<D, 128, 4>(a, tk, tv, dev, stream);
 }
 
 // The [num_pages * Hkv * P][d] codes of a pool in boxes of up to 64 tokens.
