@@ -523,6 +523,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         };
 
         uint32_t jj = 0, kk = 0;
+        uint32_t stage = 0, phase = 0;  // jj % NS, (jj / NS) & 1
         bool ok = true;
         Segment cur;
         while (ok && w.next(cur)) {
@@ -611,13 +612,22 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 // Keys of this block, and whether this thread's is one of them.
                 const int keys = min(nh * kChunk, L - ch * kChunk);
                 const bool valid = key < keys;
-                const uint32_t sbuf = jj % S::NB;
-                // The key's scales (landed well before the scores are made).
-                if (!wait_all(bar(S::KV_FULL + jj % S::NS), (jj / S::NS) & 1)) {
-                    ok = false;
-                    break;
+                const uint32_t sbuf = jj & 1;
+                // The block's scales have landed, P buffer (jj & 1) is free (P.V of
+                // block jj - 2 has completed), the scores are there.
+                {
+                    bool in = ptx::mbar_wait(bar(S::KV_FULL + stage), phase, a.wait_ns);
+                    if (jj >= 2)
+                        in &= ptx::mbar_wait(bar(S::P_FREE + sbuf), ((jj >> 1) - 1) & 1, a.wait_ns);
+                    in &= ptx::mbar_wait(bar(S::S_FULL + sbuf), (jj >> 1) & 1, a.wait_ns);
+                    if (!__all_sync(kFull, in)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
                 }
-                const uint8_t* sc = smem + S::OFF_SCALE + (jj % S::NS) * 2 * kKeys;
+                ptx::tc_fence_after();
+                const uint8_t* sc = smem + S::OFF_SCALE + stage * 2 * kKeys;
                 const int vbyte = sc[kKeys + key];
                 const float F = scale_of(sc[key]) * c_scale;
                 const float vs = static_cast<float>(vbyte - 127);
@@ -625,17 +635,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 const uint64_t F2 = ptx::f2_pack(F, F);
                 const uint64_t vs2 = ptx::f2_pack(vs, vs);
                 const uint32_t ta = lanes + S::TM_S + sbuf * R + row0;
-                if (!wait_all(bar(S::S_FULL + sbuf), (jj / S::NB) & 1)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                // P buffer (jj & 1) is free once P.V of block jj - 2 has completed.
-                if (jj >= 2 && !wait_all(bar(S::P_FREE + (jj & 1)), ((jj >> 1) - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t prow = sb + S::OFF_P + (jj & 1) * S::P_BYTES;
+                const uint32_t prow = sb + S::OFF_P + sbuf * S::P_BYTES;
                 float x[H];  // this key's scores, e, then p
                 // Once, and once more when the references had to move.
                 bool move = first;
@@ -789,8 +789,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                                        l[i], l[i + 1]);
                 } else if (wg == 0 && key < nh * kChunk) {
                     // 0 * NaN is not 0: the value rows past the data are cleared.
-                    const uint32_t vrow = sb + S::OFF_STAGE + (jj % S::NS) * S::STAGE + S::TILE +
-                                          key * D;
+                    const uint32_t vrow = sb + S::OFF_STAGE + stage * S::STAGE + S::TILE + key * D;
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow +
@@ -802,6 +801,10 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(S::P_FULL + (jj & 1)));
+                if (++stage == S::NS) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
             if (!ok) break;
             // ---- epilogue: the rows' sums over the key lanes, then O.
@@ -890,7 +893,7 @@ cudaError_t launch_prefix_fp8_rows(const Fp8Args& a, const CUtensorMap& tk,
     if (rows <= 32) return launch_prefix_fp8<D, 32, 2>(a, tk, tv, dev, stream);
     if (rows <= 48) return launch_prefix_fp8<D, 48, 3>(a, tk, tv, dev, stream);
     if (rows <= 64) return launch_prefix_fp8<D, 64, 4>(a, tk, tv, dev, stream);
-    if (rows <= 80) return launch_prefix_fp8<D, 80, 5>(a, tk, tv, dev, stream);
+    if (rows <= 80) return launch_prefix_fp8<D, 80, 2>(a, tk, tv, dev, stream);
     return launch_prefix_fp8<D, 128, 4>(a, tk, tv, dev, stream);
 }
 
