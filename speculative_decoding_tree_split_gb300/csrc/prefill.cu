@@ -86,13 +86,14 @@ struct Shape {
     static constexpr int FULL = 0;
     static constexpr int EMPTY = NS;
     static constexpr int S_FULL = 2 * NS;      // [2] by tile
-    static constexpr int P_FULL = S_FULL + 2;  // [2]
+    static constexpr int P_FULL = S_FULL + 2;  // [2]: all of P
     static constexpr int O_FULL = S_FULL + 4;  // [2]
     static constexpr int Q_FULL = S_FULL + 6;  // [2]
     static constexpr int ASK = S_FULL + 8;    // V of an edge block has landed: clean it
     static constexpr int CLEAN = S_FULL + 9;  // it is clean
-    static constexpr int DRAIN = S_FULL + 10;
-    static constexpr int NBAR = S_FULL + 11;
+    static constexpr int P_HALF = S_FULL + 10;  // [2]: P of the first 64 keys
+    static constexpr int DRAIN = S_FULL + 12;
+    static constexpr int NBAR = S_FULL + 13;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
     // TMEM: S of both tiles (P over them), then O of both.
     static constexpr int TM_S = 0;
@@ -130,32 +131,32 @@ __device__ bool find_unit(const PrefillArgs& a, int lane, Unit& u) {
     const int id = static_cast<int>(blockIdx.x) / a.Hkv;
     u.hk = static_cast<int>(blockIdx.x) % a.Hkv;
     const int n0 = row_blocks(a, lane);  // the first 32 sequences stay here
-    auto count = [&](int r) -> long long {
-        long long n = max(0, n0 - r);
+    auto count = [&](int r) -> int {
+        int n = max(0, n0 - r);
         for (int b = 32; b < a.B; b += 32) n += max(0, row_blocks(a, b + lane) - r);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(kFull, n, off);
-        return n;
+        return __reduce_add_sync(kFull, n);
     };
     if (id >= count(0)) return false;
     int lo = 0, hi = n0;  // the largest r with count(r) > id
     for (int b = 32; b < a.B; b += 32) hi = max(hi, row_blocks(a, b + lane));
     hi = __reduce_max_sync(kFull, hi);
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (count(mid) > id)
-            lo = mid;
-        else
-            hi = mid;
-    }
+    if (a.B == 1) lo = hi - 1 - id;
+    else
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (count(mid) > id)
+                lo = mid;
+            else
+                hi = mid;
+        }
     u.rb = lo;
-    long long rest = id - count(lo + 1);  // which of the sequences with n_b > lo
+    int rest = id - count(lo + 1);  // which of the sequences with n_b > lo
     for (int b = 0; b < a.B; b += 32) {
         const int n = b == 0 ? n0 : row_blocks(a, b + lane);
         const unsigned m = __ballot_sync(kFull, n > lo);
         const int c = __popc(m);
         if (rest < c) {
-            const int at = __fns(m, 0, static_cast<int>(rest) + 1);
+            const int at = __fns(m, 0, rest + 1);
             u.b = b + at;
             u.first = a.cu[u.b];
             u.len = a.cu[u.b + 1] - u.first;
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(S::S_FULL + i), 1);
             ptx::mbar_init(bar(S::P_FULL + i), 4);
+            ptx::mbar_init(bar(S::P_HALF + i), 4);
             ptx::mbar_init(bar(S::O_FULL + i), 1);
             ptx::mbar_init(bar(S::Q_FULL + i), 4);
         }
@@ -315,15 +317,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            auto values = [&](int x, int j) {  // O_x += P_x V_j
+            auto values = [&](int x, int j, int half) {  // O_x += P_x V_j, 64 keys
                 const uint32_t vst = sb + S::OFF_RING + ((2 * j + 1) % S::NS) * S::TILE;
                 if (lead) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
+                    for (int i = 0; i < kKeys / 32; ++i) {
+                        const int k = half * (kKeys / 32) + i;
                         ptx::mma_bf16_ts(tmem + S::TM_O + x * D,
                                          tmem + S::TM_S + x * kKeys + k * 8,
                                          smem_desc_sw128(vst + k * 16 * 128, S::ATOM, 1024), id_o,
                                          (j > 0 || k > 0) ? 1u : 0u);
+                    }
                 }
                 __syncwarp();
             };
@@ -355,9 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 if (j < nA) {
-                    if (!wait(S::P_FULL, j & 1) || !cleaned(j)) break;
+                    if (!wait(S::P_HALF, j & 1) || !cleaned(j)) break;
                     ptx::tc_fence_after();
-                    values(0, j);
+                    values(0, j, 0);
+                    if (!wait(S::P_FULL, j & 1)) break;
+                    ptx::tc_fence_after();
+                    values(0, j, 1);
                     if (j + 1 >= nA) {
                         done(S::O_FULL);
                     } else {
@@ -366,9 +373,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (j < nB) {
-                    if (!wait(S::P_FULL + 1, j & 1) || (j >= nA && !cleaned(j))) break;
+                    if (!wait(S::P_HALF + 1, j & 1) || (j >= nA && !cleaned(j))) break;
                     ptx::tc_fence_after();
-                    values(1, j);
+                    values(1, j, 0);
+                    if (!wait(S::P_FULL + 1, j & 1)) break;
+                    ptx::tc_fence_after();
+                    values(1, j, 1);
                 }
                 done(S::EMPTY + (2 * j + 1) % S::NS);
                 if (j < nB) {
@@ -400,26 +410,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 uint8_t* tile = smem + S::OFF_RING + (t % S::NS) * S::TILE;
-#pragma unroll 4
+                // x * 0 is NaN for just the values looked for.
+                __nv_bfloat162 sum[4];
+                const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[k] = zero;
+#pragma unroll 8
                 for (int i = part * 32 + lane; i < S::TILE / 16; i += 64) {
                     const uint4 v = *reinterpret_cast<const uint4*>(tile + i * 16);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t bad = 0;
+                    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        bad |= ((w[k] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
-                    if (bad == 0) continue;
-                    // 16-byte chunk i: atom column, row (key), swizzled chunk
-                    const int key = (i % (S::ATOM / 16)) / 8;
-                    const int c0 = (i / (S::ATOM / 16)) * 64 + ((i & 7) ^ (key & 7)) * 8;
-                    uint16_t* e = reinterpret_cast<uint16_t*>(tile + i * 16);
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t x = (w[k >> 1] >> (16 * (k & 1))) & 0xffffu;
-                        if ((x & 0x7f80u) != 0x7f80u) continue;
-                        const int kind = (x & 0x7fu) != 0 ? 0 : ((x >> 15) ? 2 : 1);
-                        atomicMin(first_bad + kind * D + c0 + k, j * kKeys + key);
-                        e[k] = 0;
-                        misc->dirty = 1;
+                    for (int k = 0; k < 4; ++k) sum[k] = __hfma2(w[k], zero, sum[k]);
+                }
+                const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]),
+                                                   __hadd2(sum[2], sum[3]));
+                if (__hisnan(__low2bfloat16(all)) || __hisnan(__high2bfloat16(all))) {
+                    for (int i = part * 32 + lane; i < S::TILE / 16; i += 64) {
+                        // 16-byte chunk i: atom column, row (key), swizzled chunk
+                        const int key = (i % (S::ATOM / 16)) / 8;
+                        const int c0 = (i / (S::ATOM / 16)) * 64 + ((i & 7) ^ (key & 7)) * 8;
+                        uint16_t* e = reinterpret_cast<uint16_t*>(tile + i * 16);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t x = e[k];
+                            if ((x & 0x7f80u) != 0x7f80u) continue;
+                            const int kind = (x & 0x7fu) != 0 ? 0 : ((x >> 15) ? 2 : 1);
+                            atomicMin(first_bad + kind * D + c0 + k, j * kKeys + key);
+                            e[k] = 0;
+                            misc->dirty = 1;
+                        }
                     }
                 }
                 ptx::fence_proxy_async_smem();
@@ -440,20 +458,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_ok = row < rows;
         const int tok = row_ok ? row / a.G : 0;
         const int head = u.hk * a.G + (row_ok ? row % a.G : 0);
-        // ---- queries into the K-major tile
+        constexpr int LPR = D / 8;  // lanes that move a row, 16 bytes each
+        // ---- queries into the K-major tile, this warp's 32 rows
         if (nx > 0) {
             uint8_t* qs = smem + S::OFF_Q + x * S::Q_TILE;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + static_cast<long long>(u.first + tok) * a.q_ts + head * a.q_hs);
+            const long long at = static_cast<long long>(u.first + tok) * a.q_ts + head * a.q_hs;
+            const int c = lane % LPR;
+            uint4 v[LPR];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (row_ok) v = __ldg(src + c);
-                v.x = (v.x ^ a.q_sign) & a.q_keep;
-                v.y = (v.y ^ a.q_sign) & a.q_keep;
-                v.z = (v.z ^ a.q_sign) & a.q_keep;
-                v.w = (v.w ^ a.q_sign) & a.q_keep;
-                *reinterpret_cast<uint4*>(qs + (c >> 3) * S::Q_ATOM + sw128_offset(r, c & 7)) = v;
+            for (int i = 0; i < LPR; ++i) {
+                const int rr = i * (32 / LPR) + lane / LPR;  // row of the warp
+                const long long src = __shfl_sync(kFull, at, rr);
+                const bool in = __shfl_sync(kFull, row_ok, rr);
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (in) v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + src) + c);
+            }
+#pragma unroll
+            for (int i = 0; i < LPR; ++i) {
+                const int rr = (warp & 3) * 32 + i * (32 / LPR) + lane / LPR;
+                v[i].x = (v[i].x ^ a.q_sign) & a.q_keep;
+                v[i].y = (v[i].y ^ a.q_sign) & a.q_keep;
+                v[i].z = (v[i].z ^ a.q_sign) & a.q_keep;
+                v[i].w = (v[i].w ^ a.q_sign) & a.q_keep;
+                *reinterpret_cast<uint4*>(qs + (c >> 3) * S::Q_ATOM + sw128_offset(rr, c & 7)) =
+                    v[i];
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -476,23 +504,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             ptx::tc_fence_after();
+            float s[kKeys];
             if (warp_any) {
-                float s[kKeys];
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 32) ptx::tmem_ld32(ts + c, s + c);
+                ptx::tmem_ld32(ts, s);
+                ptx::tmem_ld32(ts + 32, s + 32);
                 ptx::tmem_wait_ld();
-                if (j >= edge_x) {
-                    const int lim = tok - j * kKeys;  // the last key this row sees
-#pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
-                        if (i > lim) s[i] = kNegInf;
-                }
+                ptx::tmem_ld32(ts + 64, s + 64);
+                ptx::tmem_ld32(ts + 96, s + 96);
+                const int lim = j >= edge_x ? tok - j * kKeys : kKeys;  // last key seen
                 float mp[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) mp[i] = kNegInf;
+                // the first half's maxima while the second half is on its way
 #pragma unroll
-                for (int i = 0; i < kKeys; i += 2)
-                    mp[(i >> 1) & 7] = ptx::fmax3(mp[(i >> 1) & 7], s[i], s[i + 1]);
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1) ptx::tmem_wait_ld();
+                    if (j >= edge_x) {
+#pragma unroll
+                        for (int i = 64 * h; i < 64 * h + 64; ++i)
+                            if (i > lim) s[i] = kNegInf;
+                    }
+#pragma unroll
+                    for (int i = 64 * h; i < 64 * h + 64; i += 2)
+                        mp[(i >> 1) & 7] = ptx::fmax3(mp[(i >> 1) & 7], s[i], s[i + 1]);
+                }
                 const float mx = ptx::fmax3(ptx::fmax3(mp[0], mp[1], mp[2]),
                                             ptx::fmax3(mp[3], mp[4], mp[5]),
                                             fmaxf(mp[6], mp[7])) *
@@ -522,33 +557,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float neg_m = m_ref == kNegInf ? 0.f : -m_ref;
                 const uint64_t nm2 = ptx::f2_pack(neg_m, neg_m);
-                uint64_t sp2[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sp2[i] = ptx::f2_pack(0.f, 0.f);
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) {
                     uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = c; i < c + 32; i += 2) {
                         float e0, e1;
-                        ptx::f2_unpack(
-                            ptx::f2_fma(ptx::f2_pack(s[c + i], s[c + i + 1]), sc2, nm2), e0, e1);
-                        e0 = ptx::ex2(e0);
-                        e1 = ptx::ex2(e1);
-                        sp2[(i >> 1) & 3] = ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(e0, e1));
-                        pk[i / 2] = pack_bf16(e0, e1);
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[i], s[i + 1]), sc2, nm2), e0,
+                                       e1);
+                        s[i] = ptx::ex2(e0);
+                        s[i + 1] = ptx::ex2(e1);
+                        pk[(i - c) / 2] = pack_bf16(s[i], s[i + 1]);
                     }
                     ptx::tmem_st16(ts + c / 2, pk);
+                    if (c == 32) {
+                        // the tensor cores may start on these 64 keys
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(S::P_HALF + x));
+                    }
                 }
                 ptx::tmem_wait_st();
+            } else if (lane == 0) {
+                ptx::mbar_arrive(bar(S::P_HALF + x));
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(S::P_FULL + x));
+            if (warp_any) {  // the row's sum, off the tensor cores' path
+                uint64_t sp2[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sp2[i] = ptx::f2_pack(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+                for (int i = 8; i < kKeys; i += 2)
+                    sp2[(i >> 1) & 3] =
+                        ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(s[i], s[i + 1]));
                 float p[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ptx::f2_unpack(sp2[i], p[2 * i], p[2 * i + 1]);
                 l_sum += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(S::P_FULL + x));
         }
         // ---- epilogue: rows out through this warp's part of the query tile (all
         // its score products have completed)
@@ -591,22 +640,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.lse[static_cast<long long>(u.first + tok) * a.Hq + head] =
                         (m_ref + log2f(l_sum)) * kLn2;
                 __syncwarp();
-                // a row by D / 8 lanes, 16 bytes each
-                constexpr int LPR = D / 8;
-                const int wrow = row0 + x * kRows + (warp & 3) * 32;
+                const long long at =
+                    (static_cast<long long>(u.first + tok) * a.Hq + head) * D;
 #pragma unroll
-                for (int i = lane / LPR; i < 32; i += 32 / LPR) {
-                    const int rr = wrow + i;
+                for (int i = 0; i < LPR; ++i) {
+                    const int rr = i * (32 / LPR) + lane / LPR;
                     const int ch = lane % LPR;
-                    if (rr < rows) {
-                        const long long at =
-                            (static_cast<long long>(u.first + rr / a.G) * a.Hq + u.hk * a.G +
-                             rr % a.G) *
-                                D +
-                            ch * 8;
-                        *reinterpret_cast<uint4*>(a.out + at) = *reinterpret_cast<const uint4*>(
-                            stg + i * (D * 2) + ((ch ^ (i & 7)) << 4));
-                    }
+                    const long long dst = __shfl_sync(kFull, at, rr);
+                    if (__shfl_sync(kFull, row_ok, rr))
+                        *reinterpret_cast<uint4*>(a.out + dst + ch * 8) =
+                            *reinterpret_cast<const uint4*>(stg + rr * (D * 2) +
+                                                            ((ch ^ (rr & 7)) << 4));
                 }
             }
         }
