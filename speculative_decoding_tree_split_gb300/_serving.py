@@ -21,7 +21,11 @@ _I32 = torch.int32
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _tensor(t, name: str, dtypes, ndim: int, dev, dense: bool = True):
+def _tensor(t, name: str, dtypes, ndim: int, dev: int, dense: bool = True):
+    """Checks one argument; dev: the index of the device the others are on."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev
+            and t.dim() == ndim and (not dense or t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -30,13 +34,20 @@ def _tensor(t, name: str, dtypes, ndim: int, dev, dense: bool = True):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the other tensors on cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _status(status, dev):
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return t.get_device()
+
+
+def _status(status, dev: int):
     if status is None:
         return None
     _tensor(status, "status", (_I32,), status.dim() if isinstance(status, torch.Tensor) else 1, dev)
@@ -48,50 +59,67 @@ def _status(status, dev):
 class _Place:
     """The device and stream of one call, and what is allocated there."""
 
-    def __init__(self, dev: torch.device, stream):
+    __slots__ = ("dev", "current", "stream", "handle")
+
+    def __init__(self, dev: int, stream):
         self.dev = dev
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        self.current = torch.cuda.current_stream(dev)
-        self.stream = self.current if stream is None else stream
-        self.foreign = self.stream != self.current
+        self.current = self.stream = None
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(dev)
+            return
+        if stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+        self.handle = stream.cuda_stream
+        current = torch.cuda.current_stream(dev)
+        if stream != current:
+            self.current, self.stream = current, stream
 
     def empty(self, shape, dtype) -> torch.Tensor:
-        if not self.foreign:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=_DEVICES[self.dev])
         # Taken from the pool of the stream that writes it, so that it cannot
         # be memory that work queued on the current stream still reads; the
         # caller goes on to use it on the current stream.
         with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=self.dev)
+            t = torch.empty(shape, dtype=dtype, device=_DEVICES[self.dev])
         t.record_stream(self.current)
         return t
 
     def call(self, name: str, *args) -> int:
         fn = getattr(load(), name)
-        if self.dev.index == torch.cuda.current_device():
+        if self.dev == torch.cuda.current_device():
             return fn(*args)
         with torch.cuda.device(self.dev):
             return fn(*args)
 
     def run(self, name: str, *args) -> None:
-        rc = self.call(name, *args, self.stream.cuda_stream)
+        rc = self.call(name, *args, self.handle)
         if rc != 0:
             raise TreeAttnError(name, rc)
 
 
+class _Devices(dict):
+    def __missing__(self, index: int) -> torch.device:
+        self[index] = torch.device("cuda", index)
+        return self[index]
+
+
+_DEVICES = _Devices()
+_WORKSPACE: dict = {}  # bytes, by sizes and device
+
+
 def _pools(k_pages, v_pages, k_scales, v_scales, block_table):
-    """Checks the cache's tensors; returns (device, num_pages, Hkv, P, d)."""
-    dev = k_pages.device if isinstance(k_pages, torch.Tensor) else None
+    """Checks the cache's tensors; returns (device index, num_pages, Hkv, P, d)."""
+    dev = _device_of(k_pages, "k_pages")
     _tensor(k_pages, "k_pages", _CODES, 4, dev)
     _tensor(v_pages, "v_pages", _CODES, 4, dev)
     _tensor(k_scales, "k_scales", (torch.uint8,), 3, dev)
     _tensor(v_scales, "v_scales", (torch.uint8,), 3, dev)
     _tensor(block_table, "block_table", (_I32,), 2, dev)
-    shape = k_pages.shape
-    if v_pages.shape != shape or k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
+    n, h, P, d = shape = k_pages.shape
+    if v_pages.shape != shape or k_scales.shape != (n, h, P) or v_scales.shape != (n, h, P):
         raise ValueError("k_pages, v_pages, k_scales and v_scales disagree on their sizes")
-    return dev, shape[0], shape[1], shape[2], shape[3]
+    return dev, n, h, P, d
 
 
 def _rows(t, name: str, dev, heads: Optional[int], d: Optional[int]):
@@ -248,7 +276,11 @@ def verify_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, t
     if out.shape != q.shape or tuple(lse.shape) != (B, T, Hq):
         raise ValueError("out and lse must have shapes [B][T][Hq][d] and [B][T][Hq]")
     if workspace is None:
-        need = at.call("tree_attn_workspace_size", B, Hq, Hkv, d, T, 0, P)
+        sizes = (B, Hq, Hkv, d, T, P, dev)
+        need = _WORKSPACE.get(sizes)
+        if need is None:
+            need = at.call("tree_attn_workspace_size", B, Hq, Hkv, d, T, 0, P)
+            _WORKSPACE[sizes] = need
         workspace = at.empty(max(need, 256), torch.uint8)
     else:
         _tensor(workspace, "workspace", (torch.uint8,), 1, dev)
@@ -276,7 +308,7 @@ def prefill(q, k, v, cu_seqlens, *, out=None, lse=None, status=None,
     rows outside every sequence keep what out / lse held (are uninitialised
     when the call makes them).
     """
-    dev = q.device if isinstance(q, torch.Tensor) else None
+    dev = _device_of(q, "q")
     q_ts, q_hs = _rows(q, "q", dev, None, None)
     N, Hq, d = q.shape
     k_ts, k_hs = _rows(k, "k", dev, None, d)

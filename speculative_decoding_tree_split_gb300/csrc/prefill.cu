@@ -469,13 +469,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < LPR; ++i) {
                 const int rr = i * (32 / LPR) + lane / LPR;  // row of the warp
                 const long long src = __shfl_sync(kFull, at, rr);
-                const bool in = __shfl_sync(kFull, row_ok, rr);
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (in) v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + src) + c);
+                v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + src) + c);
             }
 #pragma unroll
             for (int i = 0; i < LPR; ++i) {
                 const int rr = (warp & 3) * 32 + i * (32 / LPR) + lane / LPR;
+                // (rows past the sequence hold its first query: never stored)
                 v[i].x = (v[i].x ^ a.q_sign) & a.q_keep;
                 v[i].y = (v[i].y ^ a.q_sign) & a.q_keep;
                 v[i].z = (v[i].z ^ a.q_sign) & a.q_keep;

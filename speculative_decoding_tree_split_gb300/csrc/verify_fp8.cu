@@ -543,15 +543,16 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 uint32_t m = 0;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
+                    // (loads that no branch surrounds are all in flight at once)
                     const int r = r0 + i * STEP;
-                    x[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < Mrb) {
-                        const int rr = cur.rb * kRows + r;
-                        const int t = rr / a.G, h = cur.hk * a.G + rr % a.G;
-                        x[i] = __ldg(reinterpret_cast<const uint4*>(
-                            a.q + ((static_cast<size_t>(cur.b) * a.T + t) * a.Hq + h) * D +
-                            gl * 8));
-                    }
+                    const int rr = cur.rb * kRows + min(r, Mrb - 1);
+                    const int t = rr / a.G, h = cur.hk * a.G + rr % a.G;
+                    x[i] = __ldg(reinterpret_cast<const uint4*>(
+                        a.q + ((static_cast<size_t>(cur.b) * a.T + t) * a.Hq + h) * D + gl * 8));
+                }
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    if (r0 + i * STEP >= Mrb) x[i] = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
