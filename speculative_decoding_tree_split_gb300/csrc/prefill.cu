@@ -18,15 +18,15 @@
 // * Keys a row may not see get a score of -inf by index, whatever K holds.
 //   V of such keys still meets P = 0 in the tensor cores, and 0 * NaN is not 0:
 //   in blocks that some row does not see whole, two warps clear the non-finite
-//   values of the V tile and note where they stood; the epilogue puts them back
-//   into the rows that see them.
-// * Units are taken longest first (the grid is one CTA per unit).
+//   values of the V tile, and the epilogue adds them to the rows that see them.
+// * The grid is one CTA per unit, longest first, but a CTA that has started goes
+//   on with units whose CTAs have not (cluster launch control): their loads
+//   and queries are under way while the unit before ends.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -48,8 +48,8 @@ constexpr int kUnit = 2 * kRows;     // rows of a unit
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpClean = 10;
 constexpr int kThreads = 384;        // two softmax warpgroups and one of helpers
 // Registers: 168 a thread at launch; the helpers give theirs to the softmax,
-// which holds a row's 128 scores.  256 * 208 + 128 * 56 <= 384 * 168.
-constexpr int kSoftRegs = 208, kHelpRegs = 56;
+// which holds a row's 128 scores.  256 * 232 + 128 * 40 = 384 * 168.
+constexpr int kSoftRegs = 232, kHelpRegs = 40;
 
 __device__ __forceinline__ void report(int32_t* status, int code) {
     if (status != nullptr) atomicCAS(status, 0, code);
@@ -57,14 +57,15 @@ __device__ __forceinline__ void report(int32_t* status, int code) {
 
 struct PrefillArgs {
     const uint16_t* q;
-    long long q_ts, q_hs;  // token and head strides (elements)
+    const uint16_t* v;
+    long long q_ts, q_hs, v_ts, v_hs;  // token and head strides (elements)
     int k_heads, v_heads;  // 0: one head stands for all (stride 0)
     const int32_t* cu;
     uint16_t* out;
     float* lse;
     int32_t* status;
     int B, N, Hq, Hkv, G;
-    float scale_log2;      // >= 0
+    float scale_log2;      // > 0
     uint32_t q_sign;       // flips the queries' signs where the scale is negative
     uint32_t q_keep;       // 0 clears the queries (scale 0)
     unsigned long long wait_ns;
@@ -80,9 +81,8 @@ struct Shape {
     static constexpr int NS = D == 128 ? 5 : 8;    // ring slots, K and V in turn
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + 2 * Q_TILE;
-    static constexpr int OFF_FIRST = OFF_RING + NS * TILE;  // int [3][D]: see clean()
-    static constexpr int OFF_MISC = OFF_FIRST + 3 * D * 4;
-    static constexpr int OFF_BAR = OFF_MISC + 64;
+    static constexpr int OFF_MISC = OFF_RING + NS * TILE;
+    static constexpr int OFF_BAR = OFF_MISC + 128;
     static constexpr int FULL = 0;
     static constexpr int EMPTY = NS;
     static constexpr int S_FULL = 2 * NS;      // [2] by tile
@@ -92,8 +92,11 @@ struct Shape {
     static constexpr int ASK = S_FULL + 8;    // V of an edge block has landed: clean it
     static constexpr int CLEAN = S_FULL + 9;  // it is clean
     static constexpr int P_HALF = S_FULL + 10;  // [2]: P of the first 64 keys
-    static constexpr int DRAIN = S_FULL + 12;
-    static constexpr int NBAR = S_FULL + 13;
+    static constexpr int UNIT_FULL = S_FULL + 12;   // [2]: a unit has been announced
+    static constexpr int UNIT_EMPTY = S_FULL + 14;  // [2]: every warp has read it
+    static constexpr int ANSWER = S_FULL + 16;      // the launch control has answered
+    static constexpr int DRAIN = S_FULL + 17;
+    static constexpr int NBAR = S_FULL + 18;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
     // TMEM: S of both tiles (P over them), then O of both.
     static constexpr int TM_S = 0;
@@ -103,16 +106,20 @@ struct Shape {
     static_assert(SMEM > 114 * 1024, "one CTA per SM keeps TMEM allocation uncontended");
 };
 
-struct Misc {
-    uint32_t tmem_base;
-    int abort;
-    int dirty;  // clean() found something
+struct Unit {
+    int first, len;  // packed rows of the sequence
+    int hk, rb;      // KV head; row block, -1: no more units
 };
 
-struct Unit {
-    int b, hk, rb;
-    int first, len;  // packed rows of the sequence
+struct Misc {
+    ulonglong2 answer;  // of the launch control
+    Unit unit[2];       // announced units, in turn
+    uint32_t tmem_base;
+    int abort;
+    int dirty[4][2];    // by unit, in turn, and cleaning warp: V held something
 };
+static_assert(sizeof(Misc) <= 128, "Misc fits its slot");
+constexpr int kReaders = 11;  // warps that read announced units: all but the copies'
 
 // Row blocks of sequence b (0 where its range is out of order or empty).
 __device__ __forceinline__ int row_blocks(const PrefillArgs& a, int b) {
@@ -123,20 +130,23 @@ __device__ __forceinline__ int row_blocks(const PrefillArgs& a, int b) {
     return static_cast<int>((rows + kUnit - 1) / kUnit);
 }
 
-// Unit blockIdx.x in the order of falling row-block index (so of falling work),
-// KV heads innermost; false past the last.  One warp, every lane gets it.  With
+// Unit `index` in the order of falling row-block index (so of falling work), KV
+// heads innermost; rb = -1 past the last.  One warp, every lane gets it.  With
 // n_b row blocks in sequence b, the units of index >= r number
 // sum_b max(0, n_b - r), so the index of unit u is found by halving.
-__device__ bool find_unit(const PrefillArgs& a, int lane, Unit& u) {
-    const int id = static_cast<int>(blockIdx.x) / a.Hkv;
-    u.hk = static_cast<int>(blockIdx.x) % a.Hkv;
+__device__ Unit find_unit(const PrefillArgs& a, int lane, int index) {
+    const int id = index / a.Hkv;
+    Unit u;
+    u.hk = index % a.Hkv;
+    u.rb = -1;
+    u.first = u.len = 0;
     const int n0 = row_blocks(a, lane);  // the first 32 sequences stay here
     auto count = [&](int r) -> int {
         int n = max(0, n0 - r);
         for (int b = 32; b < a.B; b += 32) n += max(0, row_blocks(a, b + lane) - r);
         return __reduce_add_sync(kFull, n);
     };
-    if (id >= count(0)) return false;
+    if (id >= count(0)) return u;
     int lo = 0, hi = n0;  // the largest r with count(r) > id
     for (int b = 32; b < a.B; b += 32) hi = max(hi, row_blocks(a, b + lane));
     hi = __reduce_max_sync(kFull, hi);
@@ -157,14 +167,14 @@ __device__ bool find_unit(const PrefillArgs& a, int lane, Unit& u) {
         const int c = __popc(m);
         if (rest < c) {
             const int at = __fns(m, 0, rest + 1);
-            u.b = b + at;
-            u.first = a.cu[u.b];
-            u.len = a.cu[u.b + 1] - u.first;
-            return true;
+            u.first = a.cu[b + at];
+            u.len = a.cu[b + at + 1] - u.first;
+            return u;
         }
         rest -= c;
     }
-    return false;
+    u.rb = -1;
+    return u;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -184,19 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sb = raw_addr + pad;
     Misc* misc = reinterpret_cast<Misc*>(smem + S::OFF_MISC);
     volatile int* abort_flag = &misc->abort;
-    int* first_bad = reinterpret_cast<int*>(smem + S::OFF_FIRST);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     auto bar = [&](int i) -> uint32_t { return sb + S::OFF_BAR + 8u * i; };
-
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < a.B; b += kThreads)
-            if (a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.N)
-                report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
-    Unit u;
-    if (!find_unit(a, lane, u)) return;  // the same in every warp
 
     if (warp == kWarpTma && lane == 0) {
         for (int s = 0; s < S::NS; ++s) {
@@ -212,9 +212,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mbar_init(bar(S::ASK), 1);
         ptx::mbar_init(bar(S::CLEAN), 2);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(S::UNIT_FULL + i), 1);
+            ptx::mbar_init(bar(S::UNIT_EMPTY + i), kReaders);
+        }
+        ptx::mbar_init(bar(S::ANSWER), 1);
         ptx::mbar_init(bar(S::DRAIN), 1);
         misc->abort = 0;
-        misc->dirty = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tm_k);
         ptx::prefetch_tmap(&tm_v);
@@ -223,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(ptx::smem_u32(&misc->tmem_base), 512);
         ptx::tmem_relinquish();
     }
-    for (int i = threadIdx.x; i < 3 * D; i += kThreads) first_bad[i] = INT_MAX;
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -233,75 +236,128 @@ __global__ void __launch_bounds__(kThreads, 1)
         report(a.status, TREE_ATTN_STATUS_TIMEOUT);
     };
 
-    // Rows of the unit: row r of the sequence is token r / G, head r % G of the
-    // group.  Tile x holds rows [row0 + 128 x, ...); its keys end with its last
-    // row's token.
-    const int rows = u.len * a.G;  // fits: N * G < 2^31 (checked on the host)
-    const int row0 = u.rb * kUnit;
-    auto blocks_of = [&](int x) -> int {
-        const int lo = row0 + x * kRows;
-        if (lo >= rows) return 0;
-        return (min(lo + kRows, rows) - 1) / a.G / kKeys + 1;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < a.B; b += kThreads)
+            if (a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.N)
+                report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
+
+    // Rows of a unit: row r of the sequence is token r / G, head r % G of the
+    // group (N * G < 2^31: the host checks).  Tile x holds rows [row0 + 128 x, ...);
+    // its blocks end with its last row's token.  Blocks from `edge` on hold keys
+    // that some row of the unit does not see.
+    struct Span {
+        int rows, row0, nA, nB, n, edge;
     };
-    const int nA = blocks_of(0), nB = blocks_of(1);
-    const int n = max(nA, nB);
-    // Blocks from this one on hold keys that some row of the unit does not see.
-    const int edge = (row0 / a.G + 1) / kKeys;
+    auto span_of = [&](const Unit& u) -> Span {
+        Span s;
+        s.rows = u.len * a.G;
+        s.row0 = u.rb * kUnit;
+        s.nA = (min(s.row0 + kRows, s.rows) - 1) / a.G / kKeys + 1;
+        s.nB = s.row0 + kRows < s.rows ? (min(s.row0 + kUnit, s.rows) - 1) / a.G / kKeys + 1 : 0;
+        s.n = max(s.nA, s.nB);
+        s.edge = (s.row0 / a.G + 1) / kKeys;
+        return s;
+    };
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        const bool all = __all_sync(kFull, ptx::mbar_wait(bar(i), parity & 1, a.wait_ns));
+        if (!all) fail();
+        return all;
+    };
+    // Announced unit number k (every warp but the copies' reads each in turn);
+    // false: no more, or a wait ran out.
+    auto next_unit = [&](uint32_t k, Unit& u) -> bool {
+        if (!wait(S::UNIT_FULL + (k & 1), k >> 1)) return false;
+        u = misc->unit[k & 1];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(S::UNIT_EMPTY + (k & 1)));
+        return u.rb >= 0;
+    };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kHelpRegs));
         if (warp == kWarpTma) {
-            // ================= copies (one lane): K0, V0, K1, V1, ...
+            // ================= units and copies: K0, V0, K1, V1, ... of each
+            Unit u = find_unit(a, lane, blockIdx.x);
             if (lane == 0) {
-                bool ok = true;
-                int t = 0;
-                const int hk_k = a.k_heads ? u.hk : 0, hk_v = a.v_heads ? u.hk : 0;
+                misc->unit[0] = u;
+                ptx::mbar_arrive(bar(S::UNIT_FULL));
+            }
+            __syncwarp();
+            uint32_t t = 0;  // tiles loaded so far
+            bool ok = true, asked = false;
 #pragma unroll 1
-                for (; t < 2 * n; ++t) {
-                    const int s = t % S::NS;
-                    if (t >= S::NS &&
-                        !ptx::mbar_wait(bar(S::EMPTY + s), (t / S::NS - 1) & 1, a.wait_ns)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    if (*abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    const bool is_v = t & 1;
-                    const int tok = u.first + (t >> 1) * kKeys;
-                    const int y = is_v ? hk_v : hk_k;
-                    const uint32_t dst = sb + S::OFF_RING + s * S::TILE;
-                    ptx::mbar_arrive_expect_tx(bar(S::FULL + s), S::TILE);
+            for (uint32_t k = 0; u.rb >= 0; ++k) {
+                // One unit ahead: the answer comes in while this one is loaded.
+                if (lane == 0) {
+                    ptx::fence_proxy_async_smem();  // the last answer has been read
+                    ptx::mbar_arrive_expect_tx(bar(S::ANSWER), 16);
+                    ptx::try_cancel(ptx::smem_u32(&misc->answer), bar(S::ANSWER));
+                }
+                __syncwarp();
+                asked = true;
+                const int n2 = 2 * span_of(u).n;
+                if (lane == 0) {
+                    const int hk_k = a.k_heads ? u.hk : 0, hk_v = a.v_heads ? u.hk : 0;
+#pragma unroll 1
+                    for (int i = 0; i < n2; ++i, ++t) {
+                        const uint32_t s = t % S::NS;
+                        if (t >= S::NS &&
+                            !ptx::mbar_wait(bar(S::EMPTY + s), (t / S::NS - 1) & 1, a.wait_ns)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        if (*abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                        const bool is_v = i & 1;
+                        const int tok = u.first + (i >> 1) * kKeys;
+                        const uint32_t dst = sb + S::OFF_RING + s * S::TILE;
+                        ptx::mbar_arrive_expect_tx(bar(S::FULL + s), S::TILE);
 #pragma unroll
-                    for (int h = 0; h < S::DH; ++h)
-                        ptx::tma_load_3d_keep(dst + h * S::ATOM, is_v ? &tm_v : &tm_k, h * 64, y,
-                                              tok, bar(S::FULL + s));
+                        for (int h = 0; h < S::DH; ++h)
+                            ptx::tma_load_3d_keep(dst + h * S::ATOM, is_v ? &tm_v : &tm_k, h * 64,
+                                                  is_v ? hk_v : hk_k, tok, bar(S::FULL + s));
+                    }
                 }
-                if (!ok) {
-                    for (int k = t > S::NS ? t - S::NS : 0; k < t; ++k)
-                        (void)ptx::mbar_wait(bar(S::FULL + k % S::NS), (k / S::NS) & 1,
-                                             ptx::kDrainLimitNs);
+                ok = __shfl_sync(kFull, ok, 0);
+                if (!ok || !wait(S::ANSWER, k)) break;
+                asked = false;
+                int index;
+                u.rb = -1;
+                if (ptx::cancelled(misc->answer.x, misc->answer.y, index))
+                    u = find_unit(a, lane, index);
+                const uint32_t m = k + 1;
+                if (m >= 2 && !wait(S::UNIT_EMPTY + (m & 1), (m >> 1) - 1)) break;
+                __syncwarp();
+                if (lane == 0) {
+                    misc->unit[m & 1] = u;
+                    ptx::mbar_arrive(bar(S::UNIT_FULL + (m & 1)));
                 }
+                __syncwarp();
+            }
+            // Copies and an answer in flight land before the CTA exits.
+            if (*abort_flag && lane == 0) {
+                for (uint32_t i = t > S::NS ? t - S::NS : 0; i < t; ++i)
+                    (void)ptx::mbar_wait(bar(S::FULL + i % S::NS), (i / S::NS) & 1,
+                                         ptx::kDrainLimitNs);
+                // (an answer asked for at the last unit: its phase is odd or even)
+                if (asked && !ptx::mbar_wait(bar(S::ANSWER), 0, ptx::kDrainLimitNs / 16))
+                    (void)ptx::mbar_wait(bar(S::ANSWER), 1, ptx::kDrainLimitNs);
             }
         } else if (warp == kWarpMma) {
             // ================= MMA issuer (the whole warp walks, one lane issues)
             const bool lead = ptx::elect_one();
             const uint32_t id_s = idesc_bf16_f32(kRows, kKeys, false, false);
             const uint32_t id_o = idesc_bf16_f32(kRows, D, false, true);
-            bool ok = true;
-            auto wait = [&](int i, int parity) -> bool {
-                const bool all =
-                    __all_sync(kFull, ptx::mbar_wait(bar(i), parity, a.wait_ns));
-                if (!all) fail();
-                return all;
+            auto slot_full = [&](uint32_t t) -> bool {
+                return wait(S::FULL + t % S::NS, t / S::NS);
             };
-            auto slot_full = [&](int t) -> bool {
-                return wait(S::FULL + t % S::NS, (t / S::NS) & 1);
-            };
-            auto scores = [&](int x, int j) {  // S_x = Q_x K_j^T
-                const uint32_t kst = sb + S::OFF_RING + (2 * j % S::NS) * S::TILE;
+            auto scores = [&](int x, uint32_t t) {  // S_x = Q_x K^T, K in tile t
+                const uint32_t kst = sb + S::OFF_RING + (t % S::NS) * S::TILE;
                 if (lead) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
@@ -317,8 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            auto values = [&](int x, int j, int half) {  // O_x += P_x V_j, 64 keys
-                const uint32_t vst = sb + S::OFF_RING + ((2 * j + 1) % S::NS) * S::TILE;
+            // O_x += P_x V (or O_x = P_x V), V in tile t, 64 of the keys
+            auto values = [&](int x, uint32_t t, int half, bool add) {
+                const uint32_t vst = sb + S::OFF_RING + (t % S::NS) * S::TILE;
                 if (lead) {
 #pragma unroll
                     for (int i = 0; i < kKeys / 32; ++i) {
@@ -326,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::mma_bf16_ts(tmem + S::TM_O + x * D,
                                          tmem + S::TM_S + x * kKeys + k * 8,
                                          smem_desc_sw128(vst + k * 16 * 128, S::ATOM, 1024), id_o,
-                                         (j > 0 || k > 0) ? 1u : 0u);
+                                         (add || half > 0 || i > 0) ? 1u : 0u);
                     }
                 }
                 __syncwarp();
@@ -335,114 +392,130 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lead) ptx::mma_commit(bar(i));
                 __syncwarp();
             };
-            auto cleaned = [&](int j) -> bool {
-                return j < edge || wait(S::CLEAN, (j - edge) & 1);
-            };
-            ok = slot_full(0) && wait(S::Q_FULL, 0);
-            if (ok) {
-                ptx::tc_fence_after();
-                scores(0, 0);
-                if (nB > 0) {
-                    ok = wait(S::Q_FULL + 1, 0);
-                    if (ok) {
-                        ptx::tc_fence_after();
-                        scores(1, 0);
-                    }
-                }
-                done(S::EMPTY + 0);
-            }
+            uint32_t base = 0, cA = 0, cB = 0, ce = 0;  // tiles, blocks of A and B, edge blocks
+            Unit u;
+            bool ok = true;
 #pragma unroll 1
-            for (int j = 0; ok && j < n; ++j) {
-                if (!slot_full(2 * j + 1)) break;
-                if (j >= edge) {
-                    if (lead) ptx::mbar_arrive(bar(S::ASK));
-                    __syncwarp();
-                }
-                if (j < nA) {
-                    if (!wait(S::P_HALF, j & 1) || !cleaned(j)) break;
-                    ptx::tc_fence_after();
-                    values(0, j, 0);
-                    if (!wait(S::P_FULL, j & 1)) break;
-                    ptx::tc_fence_after();
-                    values(0, j, 1);
-                    if (j + 1 >= nA) {
-                        done(S::O_FULL);
-                    } else {
-                        if (!slot_full(2 * j + 2)) break;
-                        scores(0, j + 1);
+            for (uint32_t k = 0; ok && next_unit(k, u); ++k) {
+                const Span s = span_of(u);
+                ok = false;
+                if (!slot_full(base) || !wait(S::Q_FULL, k)) break;
+                ptx::tc_fence_after();
+                scores(0, base);
+                if (!wait(S::Q_FULL + 1, k)) break;
+                ptx::tc_fence_after();
+                if (s.nB > 0) scores(1, base);
+                done(S::EMPTY + base % S::NS);
+                int j = 0;
+#pragma unroll 1
+                for (; j < s.n; ++j) {
+                    const uint32_t tv = base + 2 * j + 1, tk = tv + 1;
+                    if (!slot_full(tv)) break;
+                    if (j >= s.edge) {
+                        if (lead) ptx::mbar_arrive(bar(S::ASK));
+                        __syncwarp();
                     }
-                }
-                if (j < nB) {
-                    if (!wait(S::P_HALF + 1, j & 1) || (j >= nA && !cleaned(j))) break;
-                    ptx::tc_fence_after();
-                    values(1, j, 0);
-                    if (!wait(S::P_FULL + 1, j & 1)) break;
-                    ptx::tc_fence_after();
-                    values(1, j, 1);
-                }
-                done(S::EMPTY + (2 * j + 1) % S::NS);
-                if (j < nB) {
-                    if (j + 1 >= nB) {
-                        done(S::O_FULL + 1);
-                    } else {
-                        if (!slot_full(2 * j + 2)) break;
-                        scores(1, j + 1);
+                    auto cleaned = [&]() -> bool {
+                        return j < s.edge || wait(S::CLEAN, ce + (j - s.edge));
+                    };
+                    if (j < s.nA) {
+                        if (!wait(S::P_HALF, cA + j) || !cleaned()) break;
+                        ptx::tc_fence_after();
+                        values(0, tv, 0, j > 0);
+                        if (!wait(S::P_FULL, cA + j)) break;
+                        ptx::tc_fence_after();
+                        values(0, tv, 1, true);
+                        if (j + 1 >= s.nA) {
+                            done(S::O_FULL);
+                        } else {
+                            if (!slot_full(tk)) break;
+                            scores(0, tk);
+                        }
                     }
+                    if (j < s.nB) {
+                        if (!wait(S::P_HALF + 1, cB + j) || (j >= s.nA && !cleaned())) break;
+                        ptx::tc_fence_after();
+                        values(1, tv, 0, j > 0);
+                        if (!wait(S::P_FULL + 1, cB + j)) break;
+                        ptx::tc_fence_after();
+                        values(1, tv, 1, true);
+                    }
+                    done(S::EMPTY + tv % S::NS);
+                    if (j < s.nB) {
+                        if (j + 1 >= s.nB) {
+                            done(S::O_FULL + 1);
+                        } else {
+                            if (!slot_full(tk)) break;
+                            scores(1, tk);
+                        }
+                    }
+                    if (j + 1 < s.n) done(S::EMPTY + tk % S::NS);
                 }
-                if (j + 1 < n) done(S::EMPTY + (2 * j + 2) % S::NS);
+                if (j < s.n) break;
+                ok = true;
+                base += 2 * s.n;
+                cA += s.nA;
+                cB += s.nB;
+                ce += max(0, s.n - s.edge);
             }
             done(S::DRAIN);
             (void)ptx::mbar_wait(bar(S::DRAIN), 0, ptx::kDrainLimitNs);
         } else {
-            // ================= clean(): V tiles of the edge blocks.  For each
-            // column the first key that holds NaN, +inf, -inf is noted.
+            // ================= V tiles of edge blocks: values that are not finite
+            // become 0 and are noted.  A warp takes half of the columns.
+            constexpr int CPL = D / 16;  // 16-byte chunks of a row taken here
             const int part = warp - kWarpClean;
+            const int chunk = part * CPL + lane % CPL;
+            uint32_t base = 0, ce = 0;
+            Unit u;
+            bool ok = true;
 #pragma unroll 1
-            for (int j = edge; j < n; ++j) {
-                // The MMA warp has seen the tile land when it asks; the second
-                // wait makes the copy visible here.
-                const int t = 2 * j + 1;
-                if (!__all_sync(kFull,
-                                ptx::mbar_wait(bar(S::ASK), (j - edge) & 1, a.wait_ns) &&
-                                    ptx::mbar_wait(bar(S::FULL + t % S::NS), (t / S::NS) & 1,
-                                                   a.wait_ns))) {
-                    fail();
-                    break;
-                }
-                uint8_t* tile = smem + S::OFF_RING + (t % S::NS) * S::TILE;
-                // x * 0 is NaN for just the values looked for.
-                __nv_bfloat162 sum[4];
-                const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sum[k] = zero;
-#pragma unroll 8
-                for (int i = part * 32 + lane; i < S::TILE / 16; i += 64) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(tile + i * 16);
-                    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sum[k] = __hfma2(w[k], zero, sum[k]);
-                }
-                const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]),
-                                                   __hadd2(sum[2], sum[3]));
-                if (__hisnan(__low2bfloat16(all)) || __hisnan(__high2bfloat16(all))) {
-                    for (int i = part * 32 + lane; i < S::TILE / 16; i += 64) {
-                        // 16-byte chunk i: atom column, row (key), swizzled chunk
-                        const int key = (i % (S::ATOM / 16)) / 8;
-                        const int c0 = (i / (S::ATOM / 16)) * 64 + ((i & 7) ^ (key & 7)) * 8;
-                        uint16_t* e = reinterpret_cast<uint16_t*>(tile + i * 16);
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t x = e[k];
-                            if ((x & 0x7f80u) != 0x7f80u) continue;
-                            const int kind = (x & 0x7fu) != 0 ? 0 : ((x >> 15) ? 2 : 1);
-                            atomicMin(first_bad + kind * D + c0 + k, j * kKeys + key);
-                            e[k] = 0;
-                            misc->dirty = 1;
-                        }
-                    }
-                }
-                ptx::fence_proxy_async_smem();
+            for (uint32_t k = 0; ok && next_unit(k, u); ++k) {
+                const Span s = span_of(u);
+                volatile int* dirty = &misc->dirty[k & 3][part];
+                if (lane == 0) *dirty = 0;
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(S::CLEAN));
+#pragma unroll 1
+                for (int j = s.edge; j < s.n; ++j, ++ce) {
+                    // The MMA warp has seen the tile land when it asks; the second
+                    // wait makes the copy visible here.
+                    const uint32_t t = base + 2 * j + 1;
+                    if (!wait(S::ASK, ce) || !wait(S::FULL + t % S::NS, t / S::NS)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* tile = smem + S::OFF_RING + (t % S::NS) * S::TILE +
+                                    (chunk >> 3) * S::ATOM;
+                    auto at = [&](int key) -> uint8_t* {
+                        return tile + key * 128 + (((chunk & 7) ^ (key & 7)) << 4);
+                    };
+                    // x * 0 is NaN for just the values looked for.
+                    __nv_bfloat162 sum[4];
+                    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[i] = zero;
+#pragma unroll 8
+                    for (int key = lane / CPL; key < kKeys; key += 32 / CPL) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(at(key));
+                        const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum[i] = __hfma2(w[i], zero, sum[i]);
+                    }
+                    const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]),
+                                                       __hadd2(sum[2], sum[3]));
+                    if (__hisnan(__low2bfloat16(all)) || __hisnan(__high2bfloat16(all))) {
+                        for (int key = lane / CPL; key < kKeys; key += 32 / CPL) {
+                            uint16_t* e = reinterpret_cast<uint16_t*>(at(key));
+                            for (int i = 0; i < 8; ++i)
+                                if ((e[i] & 0x7f80u) == 0x7f80u) e[i] = 0;
+                        }
+                        *dirty = 1;
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(S::CLEAN));
+                }
+                base += 2 * s.n;
             }
         }
     } else {
@@ -453,205 +526,227 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t ts = lanes + S::TM_S + x * kKeys;
         const uint32_t to = lanes + S::TM_O + x * D;
-        const int nx = x == 0 ? nA : nB;
-        const int row = row0 + x * kRows + r;
-        const bool row_ok = row < rows;
-        const int tok = row_ok ? row / a.G : 0;
-        const int head = u.hk * a.G + (row_ok ? row % a.G : 0);
-        constexpr int LPR = D / 8;  // lanes that move a row, 16 bytes each
-        // ---- queries into the K-major tile, this warp's 32 rows
-        if (nx > 0) {
-            uint8_t* qs = smem + S::OFF_Q + x * S::Q_TILE;
-            const long long at = static_cast<long long>(u.first + tok) * a.q_ts + head * a.q_hs;
-            const int c = lane % LPR;
-            uint4 v[LPR];
+        const uint64_t sc2 = ptx::f2_pack(a.scale_log2, a.scale_log2);
+        struct Row {  // this thread's row of a unit
+            int nx, edge_x, tok, head, first, edge, hk;
+            bool ok;
+        };
+        auto row_of = [&](const Unit& u) -> Row {
+            const Span s = span_of(u);
+            Row w;
+            w.nx = x == 0 ? s.nA : s.nB;
+            w.edge = s.edge;
+            w.edge_x = ((s.row0 + x * kRows) / a.G + 1) / kKeys;  // first block to mask
+            const int row = s.row0 + x * kRows + r;
+            w.ok = row < s.rows;
+            w.tok = w.ok ? row / a.G : 0;
+            w.head = u.hk * a.G + (w.ok ? row % a.G : 0);
+            w.first = u.first;
+            w.hk = u.hk;
+            return w;
+        };
+        // Queries of a unit into the K-major tile, this warp's 32 rows; every
+        // score product of the unit before has completed.
+        auto load_q = [&](const Row& w) {
+            if (w.nx > 0) {
+                constexpr int LPR = D / 8;  // lanes that move a row, 16 bytes each
+                uint8_t* qs = smem + S::OFF_Q + x * S::Q_TILE;
+                const long long at =
+                    static_cast<long long>(w.first + w.tok) * a.q_ts + w.head * a.q_hs;
+                const int c = lane % LPR;
+                uint4 v[LPR];
 #pragma unroll
-            for (int i = 0; i < LPR; ++i) {
-                const int rr = i * (32 / LPR) + lane / LPR;  // row of the warp
-                const long long src = __shfl_sync(kFull, at, rr);
-                v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + src) + c);
-            }
+                for (int i = 0; i < LPR; ++i) {
+                    const int rr = i * (32 / LPR) + lane / LPR;  // row of the warp
+                    const long long src = __shfl_sync(kFull, at, rr);
+                    v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + src) + c);
+                }
 #pragma unroll
-            for (int i = 0; i < LPR; ++i) {
-                const int rr = (warp & 3) * 32 + i * (32 / LPR) + lane / LPR;
-                // (rows past the sequence hold its first query: never stored)
-                v[i].x = (v[i].x ^ a.q_sign) & a.q_keep;
-                v[i].y = (v[i].y ^ a.q_sign) & a.q_keep;
-                v[i].z = (v[i].z ^ a.q_sign) & a.q_keep;
-                v[i].w = (v[i].w ^ a.q_sign) & a.q_keep;
-                *reinterpret_cast<uint4*>(qs + (c >> 3) * S::Q_ATOM + sw128_offset(rr, c & 7)) =
-                    v[i];
+                for (int i = 0; i < LPR; ++i) {
+                    const int rr = (warp & 3) * 32 + i * (32 / LPR) + lane / LPR;
+                    // (rows past the sequence hold its first query: never stored)
+                    v[i].x = (v[i].x ^ a.q_sign) & a.q_keep;
+                    v[i].y = (v[i].y ^ a.q_sign) & a.q_keep;
+                    v[i].z = (v[i].z ^ a.q_sign) & a.q_keep;
+                    v[i].w = (v[i].w ^ a.q_sign) & a.q_keep;
+                    *reinterpret_cast<uint4*>(qs + (c >> 3) * S::Q_ATOM +
+                                              sw128_offset(rr, c & 7)) = v[i];
+                }
+                ptx::fence_proxy_async_smem();
             }
-            ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(S::Q_FULL + x));
-        }
-        auto wait = [&](int i, int parity) -> bool {
-            const bool all = __all_sync(kFull, ptx::mbar_wait(bar(i), parity, a.wait_ns));
-            if (!all) fail();
-            return all;
         };
-        const bool warp_any = __any_sync(kFull, row_ok);
-        const int edge_x = ((row0 + x * kRows) / a.G + 1) / kKeys;  // first block to mask
-        float m_ref = kNegInf, l_sum = 0.f;
-        bool ok = true;
-        const uint64_t sc2 = ptx::f2_pack(a.scale_log2, a.scale_log2);
-#pragma unroll 1
-        for (int j = 0; j < nx; ++j) {
-            if (!wait(S::S_FULL + x, j & 1)) {
-                ok = false;
-                break;
-            }
-            ptx::tc_fence_after();
-            float s[kKeys];
-            if (warp_any) {
-                ptx::tmem_ld32(ts, s);
-                ptx::tmem_ld32(ts + 32, s + 32);
-                ptx::tmem_wait_ld();
-                ptx::tmem_ld32(ts + 64, s + 64);
-                ptx::tmem_ld32(ts + 96, s + 96);
-                const int lim = j >= edge_x ? tok - j * kKeys : kKeys;  // last key seen
-                float mp[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mp[i] = kNegInf;
-                // the first half's maxima while the second half is on its way
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1) ptx::tmem_wait_ld();
-                    if (j >= edge_x) {
-#pragma unroll
-                        for (int i = 64 * h; i < 64 * h + 64; ++i)
-                            if (i > lim) s[i] = kNegInf;
-                    }
-#pragma unroll
-                    for (int i = 64 * h; i < 64 * h + 64; i += 2)
-                        mp[(i >> 1) & 7] = ptx::fmax3(mp[(i >> 1) & 7], s[i], s[i + 1]);
-                }
-                const float mx = ptx::fmax3(ptx::fmax3(mp[0], mp[1], mp[2]),
-                                            ptx::fmax3(mp[3], mp[4], mp[5]),
-                                            fmaxf(mp[6], mp[7])) *
-                                 a.scale_log2;
-                float alpha = 1.f;
-                bool rescale = false;
-                if (j == 0) {
-                    m_ref = mx;
-                } else if (mx > m_ref + 8.f) {
-                    alpha = ptx::ex2(m_ref - mx);
-                    m_ref = mx;
-                    l_sum *= alpha;
-                    rescale = true;
-                }
-                // S_x(j) was issued behind O_x += P V of block j - 1 and has
-                // completed, so O is at rest until this block's P is handed over.
-                if (__any_sync(kFull, rescale)) {
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        ptx::tmem_ld32(to + c, o);
-                        ptx::tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                        ptx::tmem_st32(to + c, o);
-                    }
-                }
-                const float neg_m = m_ref == kNegInf ? 0.f : -m_ref;
-                const uint64_t nm2 = ptx::f2_pack(neg_m, neg_m);
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = c; i < c + 32; i += 2) {
-                        float e0, e1;
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[i], s[i + 1]), sc2, nm2), e0,
-                                       e1);
-                        s[i] = ptx::ex2(e0);
-                        s[i + 1] = ptx::ex2(e1);
-                        pk[(i - c) / 2] = pack_bf16(s[i], s[i + 1]);
-                    }
-                    ptx::tmem_st16(ts + c / 2, pk);
-                    if (c == 32) {
-                        // the tensor cores may start on these 64 keys
-                        ptx::tmem_wait_st();
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bar(S::P_HALF + x));
-                    }
-                }
-                ptx::tmem_wait_st();
-            } else if (lane == 0) {
-                ptx::mbar_arrive(bar(S::P_HALF + x));
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(S::P_FULL + x));
-            if (warp_any) {  // the row's sum, off the tensor cores' path
-                uint64_t sp2[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sp2[i] = ptx::f2_pack(s[2 * i], s[2 * i + 1]);
-#pragma unroll
-                for (int i = 8; i < kKeys; i += 2)
-                    sp2[(i >> 1) & 3] =
-                        ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(s[i], s[i + 1]));
-                float p[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ptx::f2_unpack(sp2[i], p[2 * i], p[2 * i + 1]);
-                l_sum += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-            }
+        uint32_t blocks = 0, ends = 0;  // blocks and units of this tile so far
+        Unit u;
+        bool have = next_unit(0, u);
+        Row w = {};
+        if (have) {
+            w = row_of(u);
+            load_q(w);
         }
-        // ---- epilogue: rows out through this warp's part of the query tile (all
-        // its score products have completed)
-        if (ok && nx > 0 && wait(S::O_FULL + x, 0)) {
-            ptx::tc_fence_after();
-            if (warp_any) {
-                const float inv = 1.f / l_sum;
-                const bool dirty = *reinterpret_cast<volatile int*>(&misc->dirty) != 0;
-                uint8_t* stg = smem + S::OFF_Q + x * S::Q_TILE + (warp & 3) * 32 * D * 2;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    ptx::tmem_ld32(to + c, o);
+#pragma unroll 1
+        for (uint32_t k = 0; have; ++k) {
+            const bool warp_any = __any_sync(kFull, w.ok);
+            float m_ref = kNegInf, l_sum = 0.f;
+            bool ok = true;
+#pragma unroll 1
+            for (int j = 0; j < w.nx; ++j) {
+                if (!wait(S::S_FULL + x, blocks + j)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                float s[kKeys];
+                if (warp_any) {
+                    ptx::tmem_ld32(ts, s);
+                    ptx::tmem_ld32(ts + 32, s + 32);
                     ptx::tmem_wait_ld();
+                    ptx::tmem_ld32(ts + 64, s + 64);
+                    ptx::tmem_ld32(ts + 96, s + 96);
+                    const int lim = j >= w.edge_x ? w.tok - j * kKeys : kKeys;  // last key seen
+                    float mp[8];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] *= inv;
-                    if (dirty) {
+                    for (int i = 0; i < 8; ++i) mp[i] = kNegInf;
+                    // the first half's maxima while the second half is on its way
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const bool nan = first_bad[c + i] <= tok;
-                            const bool up = first_bad[D + c + i] <= tok;
-                            const bool dn = first_bad[2 * D + c + i] <= tok;
-                            if (up) o[i] += __builtin_huge_valf();
-                            if (dn) o[i] -= __builtin_huge_valf();
-                            if (nan) o[i] = __int_as_float(0x7fffffff);
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1) ptx::tmem_wait_ld();
+                        if (j >= w.edge_x) {
+#pragma unroll
+                            for (int i = 64 * h; i < 64 * h + 64; ++i)
+                                if (i > lim) s[i] = kNegInf;
+                        }
+#pragma unroll
+                        for (int i = 64 * h; i < 64 * h + 64; i += 2)
+                            mp[(i >> 1) & 7] = ptx::fmax3(mp[(i >> 1) & 7], s[i], s[i + 1]);
+                    }
+                    const float mx = ptx::fmax3(ptx::fmax3(mp[0], mp[1], mp[2]),
+                                                ptx::fmax3(mp[3], mp[4], mp[5]),
+                                                fmaxf(mp[6], mp[7])) *
+                                     a.scale_log2;
+                    float alpha = 1.f;
+                    bool rescale = false;
+                    if (j == 0) {
+                        m_ref = mx;
+                    } else if (mx > m_ref + 8.f) {
+                        alpha = ptx::ex2(m_ref - mx);
+                        m_ref = mx;
+                        l_sum *= alpha;
+                        rescale = true;
+                    }
+                    // S_x(j) was issued behind O_x += P V of block j - 1 and has
+                    // completed, so O is at rest until this block's P is handed over.
+                    if (__any_sync(kFull, rescale)) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            ptx::tmem_ld32(to + c, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            ptx::tmem_st32(to + c, o);
                         }
                     }
+                    const float neg_m = m_ref == kNegInf ? 0.f : -m_ref;
+                    const uint64_t nm2 = ptx::f2_pack(neg_m, neg_m);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ch = c / 8 + i;  // 16-byte chunk of the row
-                        *reinterpret_cast<uint4*>(stg + lane * (D * 2) +
-                                                  ((ch ^ (lane & 7)) << 4)) =
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = c; i < c + 32; i += 2) {
+                            float e0, e1;
+                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[i], s[i + 1]), sc2, nm2), e0,
+                                           e1);
+                            s[i] = ptx::ex2(e0);
+                            s[i + 1] = ptx::ex2(e1);
+                            pk[(i - c) / 2] = pack_bf16(s[i], s[i + 1]);
+                        }
+                        ptx::tmem_st16(ts + c / 2, pk);
+                        if (c == 32) {
+                            // the tensor cores may start on these 64 keys
+                            ptx::tmem_wait_st();
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(bar(S::P_HALF + x));
+                        }
+                    }
+                    ptx::tmem_wait_st();
+                } else if (lane == 0) {
+                    ptx::mbar_arrive(bar(S::P_HALF + x));
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(S::P_FULL + x));
+                if (warp_any) {  // the row's sum, off the tensor cores' path
+                    uint64_t sp2[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sp2[i] = ptx::f2_pack(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+                    for (int i = 8; i < kKeys; i += 2)
+                        sp2[(i >> 1) & 3] =
+                            ptx::f2_add(sp2[(i >> 1) & 3], ptx::f2_pack(s[i], s[i + 1]));
+                    float p[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ptx::f2_unpack(sp2[i], p[2 * i], p[2 * i + 1]);
+                    l_sum += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+                }
+            }
+            if (!ok) break;
+            blocks += w.nx;
+            // ---- the next unit's queries, so that its first scores are made beside
+            // this epilogue
+            const Row end = w;
+            have = next_unit(k + 1, u);
+            if (have) {
+                w = row_of(u);
+                load_q(w);
+            }
+            // ---- epilogue
+            if (end.nx == 0) continue;
+            if (!wait(S::O_FULL + x, ends)) break;
+            ++ends;
+            ptx::tc_fence_after();
+            if (!warp_any) continue;
+            const float inv = 1.f / l_sum;
+            const volatile int* d3 = misc->dirty[k & 3];
+            const bool dirty = (d3[0] | d3[1]) != 0;
+            const long long row =
+                static_cast<long long>(end.first + end.tok) * a.Hq + end.head;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                ptx::tmem_ld32(to + c, o);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= inv;
+                if (dirty) {
+                    // (rare) what was cleared, for the rows that see it: a
+                    // probability times NaN or an infinity is that again
+#pragma unroll 1
+                    for (int key = end.edge * kKeys; key <= end.tok; ++key) {
+                        const uint16_t* vr =
+                            a.v + static_cast<long long>(end.first + key) * a.v_ts +
+                            end.hk * a.v_hs + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const uint32_t b = __ldg(vr + i);
+                            if ((b & 0x7f80u) == 0x7f80u) o[i] += __uint_as_float(b << 16);
+                        }
+                    }
+                }
+                if (end.ok) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(a.out + row * D + c + 8 * i) =
                             make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]),
                                        pack_bf16(o[8 * i + 2], o[8 * i + 3]),
                                        pack_bf16(o[8 * i + 4], o[8 * i + 5]),
                                        pack_bf16(o[8 * i + 6], o[8 * i + 7]));
-                    }
-                }
-                if (row_ok)
-                    a.lse[static_cast<long long>(u.first + tok) * a.Hq + head] =
-                        (m_ref + log2f(l_sum)) * kLn2;
-                __syncwarp();
-                const long long at =
-                    (static_cast<long long>(u.first + tok) * a.Hq + head) * D;
-#pragma unroll
-                for (int i = 0; i < LPR; ++i) {
-                    const int rr = i * (32 / LPR) + lane / LPR;
-                    const int ch = lane % LPR;
-                    const long long dst = __shfl_sync(kFull, at, rr);
-                    if (__shfl_sync(kFull, row_ok, rr))
-                        *reinterpret_cast<uint4*>(a.out + dst + ch * 8) =
-                            *reinterpret_cast<const uint4*>(stg + rr * (D * 2) +
-                                                            ((ch ^ (rr & 7)) << 4));
                 }
             }
+            if (end.ok) a.lse[row] = (m_ref + log2f(l_sum)) * kLn2;
+            ptx::tc_fence_before();
         }
     }
 
@@ -715,7 +810,7 @@ extern "C" int tree_attn_prefill(const uint16_t* q, const uint16_t* k, const uin
         static_cast<long long>(N) * (Hq / Hkv) >= (1LL << 31) - kUnit)
         return TREE_ATTN_ERR_SHAPE;
     // One CTA per 256 rows of a sequence and KV head; the lengths are on the
-    // device, so the grid is the largest it can be and the rest return at once.
+    // device, so the grid is the largest it can be and the rest end at once.
     const long long ctas =
         (static_cast<long long>(N) * (Hq / Hkv) / kUnit + B) * static_cast<long long>(Hkv);
     if (ctas > 0x7fffffffLL) return TREE_ATTN_ERR_SHAPE;
@@ -733,6 +828,9 @@ extern "C" int tree_attn_prefill(const uint16_t* q, const uint16_t* k, const uin
         return TREE_ATTN_ERR_CUDA;
     PrefillArgs a;
     a.q = q;
+    a.v = v;
+    a.v_ts = v_token_stride;
+    a.v_hs = v_head_stride;
     a.q_ts = q_token_stride;
     a.q_hs = q_head_stride;
     a.k_heads = k_head_stride != 0;

@@ -160,6 +160,38 @@ __device__ __forceinline__ void grid_dep_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- launch control
+// Ask for a CTA of this grid that has not started yet: 16 bytes of answer at
+// `dst` (shared memory), completing on `bar`.  Not to be asked again after a "no".
+__device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+        " [%0], [%1];" ::"r"(dst),
+        "r"(bar)
+        : "memory");
+}
+
+// The answer: whether a CTA was taken over, and its blockIdx.x.
+__device__ __forceinline__ bool cancelled(uint64_t lo, uint64_t hi, int& x) {
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "mov.b128 r, {%1, %2};\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes)
+        : "l"(lo), "l"(hi));
+    x = 0;
+    if (yes != 0)
+        asm volatile(
+            "{\n\t.reg .b128 r;\n\t"
+            "mov.b128 r, {%1, %2};\n\t"
+            "clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+            : "=r"(x)
+            : "l"(lo), "l"(hi));
+    return yes != 0;
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Allocate `ncols` TMEM columns (whole warp); the base address is written to
 // shared memory at `dst`.
