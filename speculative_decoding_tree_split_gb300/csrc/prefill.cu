@@ -78,10 +78,11 @@ struct Shape {
     static constexpr int Q_ATOM = kRows * 128;
     static constexpr int TILE = kKeys * D * 2;     // K or V of one block
     static constexpr int ATOM = kKeys * 128;
-    static constexpr int NS = D == 128 ? 5 : 8;    // ring slots, K and V in turn
+    static constexpr int NS = D == 128 ? 4 : 8;    // ring slots, K and V in turn
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + 2 * Q_TILE;
-    static constexpr int OFF_MISC = OFF_RING + NS * TILE;
+    static constexpr int OFF_OUT = OFF_RING + NS * TILE;  // [8 warps][32 rows][64 columns]
+    static constexpr int OFF_MISC = OFF_OUT + 8 * 32 * 128;
     static constexpr int OFF_BAR = OFF_MISC + 128;
     static constexpr int FULL = 0;
     static constexpr int EMPTY = NS;
@@ -330,6 +331,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 u.rb = -1;
                 if (ptx::cancelled(misc->answer.x, misc->answer.y, index))
                     u = find_unit(a, lane, index);
+                if (u.rb >= 0) {
+                    // its queries on their way to L2: a row's G heads in one piece
+                    const Span s = span_of(u);
+                    const int r1 = min(s.row0 + kUnit, s.rows);
+                    for (int row = s.row0 + lane; row < r1; row += 32) {
+                        const uint16_t* p =
+                            a.q + static_cast<long long>(u.first + row / a.G) * a.q_ts +
+                            static_cast<long long>(u.hk * a.G + row % a.G) * a.q_hs;
+                        ptx::prefetch_l2(p);
+                        if (D == 128) ptx::prefetch_l2(p + 64);
+                    }
+                }
                 const uint32_t m = k + 1;
                 if (m >= 2 && !wait(S::UNIT_EMPTY + (m & 1), (m >> 1) - 1)) break;
                 __syncwarp();
@@ -709,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             if (!warp_any) continue;
             const float inv = 1.f / l_sum;
+            uint8_t* stg = smem + S::OFF_OUT + warp * (32 * 128);
             const volatile int* d3 = misc->dirty[k & 3];
             const bool dirty = (d3[0] | d3[1]) != 0;
             const long long row =
@@ -735,14 +749,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (end.ok) {
+                // 64 columns at a time through this warp's staging rows, so that a
+                // store instruction covers whole 128-byte pieces of four rows.
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(a.out + row * D + c + 8 * i) =
-                            make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]),
-                                       pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                                       pack_bf16(o[8 * i + 4], o[8 * i + 5]),
-                                       pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+                for (int i = 0; i < 4; ++i) {
+                    const int ch = (c % 64) / 8 + i;
+                    *reinterpret_cast<uint4*>(stg + lane * 128 + ((ch ^ (lane & 7)) << 4)) =
+                        make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]),
+                                   pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                   pack_bf16(o[8 * i + 4], o[8 * i + 5]),
+                                   pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+                }
+                if (c % 64 == 32) {
+                    __syncwarp();
+                    const int ch = lane & 7;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + (lane >> 3);
+                        const long long dst = __shfl_sync(kFull, row, rr) * D + c - 32 + ch * 8;
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            stg + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                        if (__shfl_sync(kFull, end.ok, rr))
+                            *reinterpret_cast<uint4*>(a.out + dst) = v;
+                    }
+                    __syncwarp();
                 }
             }
             if (end.ok) a.lse[row] = (m_ref + log2f(l_sum)) * kLn2;
