@@ -298,59 +298,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 asked = true;
+                // A ring's worth of tiles first, then the next unit is looked up and
+                // announced, then the rest.
                 const int n2 = 2 * span_of(u).n;
-                if (lane == 0) {
-                    const int hk_k = a.k_heads ? u.hk : 0, hk_v = a.v_heads ? u.hk : 0;
+                const int hk_k = a.k_heads ? u.hk : 0, hk_v = a.v_heads ? u.hk : 0;
+                auto load = [&](int from, int to) -> bool {
+                    if (lane == 0) {
 #pragma unroll 1
-                    for (int i = 0; i < n2; ++i, ++t) {
-                        const uint32_t s = t % S::NS;
-                        if (t >= S::NS &&
-                            !ptx::mbar_wait(bar(S::EMPTY + s), (t / S::NS - 1) & 1, a.wait_ns)) {
-                            fail();
-                            ok = false;
-                            break;
-                        }
-                        if (*abort_flag) {
-                            ok = false;
-                            break;
-                        }
-                        const bool is_v = i & 1;
-                        const int tok = u.first + (i >> 1) * kKeys;
-                        const uint32_t dst = sb + S::OFF_RING + s * S::TILE;
-                        ptx::mbar_arrive_expect_tx(bar(S::FULL + s), S::TILE);
+                        for (int i = from; i < to; ++i, ++t) {
+                            const uint32_t s = t % S::NS;
+                            if (t >= S::NS && !ptx::mbar_wait(bar(S::EMPTY + s),
+                                                              (t / S::NS - 1) & 1, a.wait_ns)) {
+                                fail();
+                                ok = false;
+                                break;
+                            }
+                            if (*abort_flag) {
+                                ok = false;
+                                break;
+                            }
+                            const bool is_v = i & 1;
+                            const int tok = u.first + (i >> 1) * kKeys;
+                            const uint32_t dst = sb + S::OFF_RING + s * S::TILE;
+                            ptx::mbar_arrive_expect_tx(bar(S::FULL + s), S::TILE);
 #pragma unroll
-                        for (int h = 0; h < S::DH; ++h)
-                            ptx::tma_load_3d_keep(dst + h * S::ATOM, is_v ? &tm_v : &tm_k, h * 64,
-                                                  is_v ? hk_v : hk_k, tok, bar(S::FULL + s));
+                            for (int h = 0; h < S::DH; ++h)
+                                ptx::tma_load_3d_keep(dst + h * S::ATOM, is_v ? &tm_v : &tm_k,
+                                                      h * 64, is_v ? hk_v : hk_k, tok,
+                                                      bar(S::FULL + s));
+                        }
                     }
-                }
-                ok = __shfl_sync(kFull, ok, 0);
-                if (!ok || !wait(S::ANSWER, k)) break;
+                    ok = __shfl_sync(kFull, ok, 0);
+                    return ok;
+                };
+                if (!load(0, min(n2, S::NS)) || !wait(S::ANSWER, k)) break;
                 asked = false;
                 int index;
-                u.rb = -1;
+                Unit nxt;
+                nxt.rb = -1;
                 if (ptx::cancelled(misc->answer.x, misc->answer.y, index))
-                    u = find_unit(a, lane, index);
-                if (u.rb >= 0) {
-                    // its queries on their way to L2: a row's G heads in one piece
-                    const Span s = span_of(u);
-                    const int r1 = min(s.row0 + kUnit, s.rows);
-                    for (int row = s.row0 + lane; row < r1; row += 32) {
-                        const uint16_t* p =
-                            a.q + static_cast<long long>(u.first + row / a.G) * a.q_ts +
-                            static_cast<long long>(u.hk * a.G + row % a.G) * a.q_hs;
-                        ptx::prefetch_l2(p);
-                        if (D == 128) ptx::prefetch_l2(p + 64);
-                    }
-                }
+                    nxt = find_unit(a, lane, index);
                 const uint32_t m = k + 1;
                 if (m >= 2 && !wait(S::UNIT_EMPTY + (m & 1), (m >> 1) - 1)) break;
                 __syncwarp();
                 if (lane == 0) {
-                    misc->unit[m & 1] = u;
+                    misc->unit[m & 1] = nxt;
                     ptx::mbar_arrive(bar(S::UNIT_FULL + (m & 1)));
                 }
                 __syncwarp();
+                if (nxt.rb >= 0) {
+                    // its queries on their way to L2
+                    const Span s = span_of(nxt);
+                    const int r1 = min(s.row0 + kUnit, s.rows);
+                    for (int row = s.row0 + lane; row < r1; row += 32) {
+                        const uint16_t* p =
+                            a.q + static_cast<long long>(nxt.first + row / a.G) * a.q_ts +
+                            static_cast<long long>(nxt.hk * a.G + row % a.G) * a.q_hs;
+                        ptx::prefetch_l2(p);
+                        if (D == 128) ptx::prefetch_l2(p + 64);
+                    }
+                }
+                if (!load(min(n2, S::NS), n2)) break;
+                u = nxt;
             }
             // Copies and an answer in flight land before the CTA exits.
             if (*abort_flag && lane == 0) {
