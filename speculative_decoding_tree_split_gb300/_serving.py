@@ -5,6 +5,11 @@ As in ``_lib``: arguments are checked, then handed to the library; there is no
 fallback.  Every call runs on the device its tensors are on (all on one), on
 ``stream`` or that device's current stream.  Results and workspaces that a call
 makes itself belong to the stream it runs on.
+
+A step of a server makes these calls for every layer, and a small one takes the
+GPU less time than the host, so each call first asks in one expression whether
+its arguments are all as they should be; only if not does it go through them one
+by one to say what is wrong.
 """
 from __future__ import annotations
 
@@ -18,7 +23,11 @@ from ._lib import _BITS64, TreeAttnError, load
 
 _BF16 = torch.bfloat16
 _I32 = torch.int32
+_U8 = torch.uint8
+_F32 = torch.float32
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+# What a question about something that is no such tensor raises.
+_NOT_SO = (AttributeError, TypeError, ValueError)
 
 
 def _tensor(t, name: str, dtypes, ndim: int, dev: int, dense: bool = True):
@@ -93,7 +102,12 @@ class _Place:
             return fn(*args)
 
     def run(self, name: str, *args) -> None:
-        rc = self.call(name, *args, self.handle)
+        fn = getattr(load(), name)
+        if self.dev == torch.cuda.current_device():
+            rc = fn(*args, self.handle)
+        else:
+            with torch.cuda.device(self.dev):
+                rc = fn(*args, self.handle)
         if rc != 0:
             raise TreeAttnError(name, rc)
 
@@ -110,21 +124,42 @@ _WORKSPACE: dict = {}  # bytes, by sizes and device
 
 def _pools(k_pages, v_pages, k_scales, v_scales, block_table):
     """Checks the cache's tensors; returns (device index, num_pages, Hkv, P, d)."""
+    try:
+        dev = k_pages.get_device()
+        n, h, P, d = shape = k_pages.shape
+        if (dev >= 0 and k_pages.dtype in _CODES and v_pages.dtype in _CODES
+                and k_scales.dtype is _U8 and v_scales.dtype is _U8 and block_table.dtype is _I32
+                and v_pages.shape == shape and k_scales.shape == (n, h, P)
+                and v_scales.shape == (n, h, P) and block_table.dim() == 2
+                and v_pages.get_device() == dev and k_scales.get_device() == dev
+                and v_scales.get_device() == dev and block_table.get_device() == dev
+                and k_pages.is_contiguous() and v_pages.is_contiguous()
+                and k_scales.is_contiguous() and v_scales.is_contiguous()
+                and block_table.is_contiguous()):
+            return dev, n, h, P, d
+    except _NOT_SO:
+        pass
     dev = _device_of(k_pages, "k_pages")
     _tensor(k_pages, "k_pages", _CODES, 4, dev)
     _tensor(v_pages, "v_pages", _CODES, 4, dev)
-    _tensor(k_scales, "k_scales", (torch.uint8,), 3, dev)
-    _tensor(v_scales, "v_scales", (torch.uint8,), 3, dev)
+    _tensor(k_scales, "k_scales", (_U8,), 3, dev)
+    _tensor(v_scales, "v_scales", (_U8,), 3, dev)
     _tensor(block_table, "block_table", (_I32,), 2, dev)
-    n, h, P, d = shape = k_pages.shape
-    if v_pages.shape != shape or k_scales.shape != (n, h, P) or v_scales.shape != (n, h, P):
-        raise ValueError("k_pages, v_pages, k_scales and v_scales disagree on their sizes")
-    return dev, n, h, P, d
+    raise ValueError("k_pages, v_pages, k_scales and v_scales disagree on their sizes")
 
 
 def _rows(t, name: str, dev, heads: Optional[int], d: Optional[int]):
     """Checks packed rows [N][H][d] with d contiguous; returns (token, head)
     strides, 0 where there is one row of that kind."""
+    try:
+        n, h, e = t.shape
+        if (t.dtype is _BF16 and t.get_device() == dev and (heads is None or h == heads)
+                and (d is None or e == d)):
+            ts, hs, es = t.stride()
+            if es == 1:
+                return (ts if n > 1 else 0), (hs if h > 1 else 0)
+    except _NOT_SO:
+        pass
     _tensor(t, name, (_BF16,), 3, dev, dense=False)
     n, h, e = t.shape
     if (heads is not None and h != heads) or (d is not None and e != d):
@@ -136,6 +171,12 @@ def _rows(t, name: str, dev, heads: Optional[int], d: Optional[int]):
 
 
 def _vector(t, name: str, n: int, dev):
+    try:
+        if (t.dtype is _I32 and t.shape == (n,) and t.get_device() == dev
+                and t.is_contiguous()):
+            return
+    except _NOT_SO:
+        pass
     _tensor(t, name, (_I32,), 1, dev)
     if t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
@@ -233,6 +274,29 @@ def kv_read_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens, n
     return outs[0], outs[1]
 
 
+def _check_verify(q, tree_k, tree_v, seq_lens, block_table, mask, parents, mask_out, dev, Hkv, d):
+    """verify_fp8's arguments one by one."""
+    for t, name in ((q, "q"), (tree_k, "tree_k"), (tree_v, "tree_v")):
+        _tensor(t, name, (_BF16,), 4, dev)
+    B, T = q.shape[:2]
+    _vector(seq_lens, "seq_lens", B, dev)
+    if (q.shape[3] != d or tuple(tree_k.shape) != (B, T, Hkv, d) or tree_v.shape != tree_k.shape
+            or block_table.shape[0] != B):
+        raise ValueError("inconsistent tensor shapes")
+    if (mask is None) == (parents is None):
+        raise ValueError("give exactly one of mask and parents")
+    tree, dtypes, name = (mask, _BITS64, "mask") if parents is None else (parents, (_I32,), "parents")
+    _tensor(tree, name, dtypes, tree.dim() if isinstance(tree, torch.Tensor) else 1, dev)
+    if tuple(tree.shape) not in ((T,), (B, T)):
+        raise ValueError(f"{name} must have shape [T] or [B][T]")
+    if mask_out is not None:
+        if parents is None:
+            raise ValueError("mask_out goes with parents")
+        _tensor(mask_out, "mask_out", _BITS64, tree.dim(), dev)
+        if mask_out.shape != tree.shape:
+            raise ValueError("mask_out must have the shape of parents")
+
+
 def verify_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, tree_k, tree_v, *,
                mask=None, parents=None, mask_out=None, out=None, lse=None, workspace=None,
                status=None, softmax_scale: Optional[float] = None,
@@ -244,26 +308,26 @@ def verify_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, t
     [T] or [B][T]) or as ``parents`` (int32, [T] or [B][T]).  Returns (out, lse).
     """
     dev, num_pages, Hkv, P, d = _pools(k_pages, v_pages, k_scales, v_scales, block_table)
-    for t, name in ((q, "q"), (tree_k, "tree_k"), (tree_v, "tree_v")):
-        _tensor(t, name, (_BF16,), 4, dev)
-    B, T, Hq, _ = q.shape
-    _vector(seq_lens, "seq_lens", B, dev)
-    if (q.shape[3] != d or tuple(tree_k.shape) != (B, T, Hkv, d) or tree_v.shape != tree_k.shape
-            or block_table.shape[0] != B):
-        raise ValueError("inconsistent tensor shapes")
-    if (mask is None) == (parents is None):
-        raise ValueError("give exactly one of mask and parents")
-    tree, dtypes, name = (mask, _BITS64, "mask") if parents is None else (parents, (_I32,), "parents")
-    _tensor(tree, name, dtypes, tree.dim() if isinstance(tree, torch.Tensor) else 1, dev)
-    if tuple(tree.shape) not in ((T,), (B, T)):
-        raise ValueError(f"{name} must have shape [T] or [B][T]")
+    tree = mask if parents is None else parents
+    try:
+        B, T, Hq, _ = q.shape
+        sound = (q.dtype is _BF16 and tree_k.dtype is _BF16 and tree_v.dtype is _BF16
+                 and seq_lens.dtype is _I32 and q.shape[3] == d
+                 and tree_k.shape == (B, T, Hkv, d) and tree_v.shape == (B, T, Hkv, d)
+                 and seq_lens.shape == (B,) and block_table.shape[0] == B
+                 and (parents is None or mask is None) and tree.shape in ((T,), (B, T))
+                 and (tree.dtype is _I32 if mask is None else tree.dtype in _BITS64)
+                 and q.get_device() == dev and tree_k.get_device() == dev
+                 and tree_v.get_device() == dev and seq_lens.get_device() == dev
+                 and tree.get_device() == dev and q.is_contiguous() and tree_k.is_contiguous()
+                 and tree_v.is_contiguous() and seq_lens.is_contiguous()
+                 and tree.is_contiguous() and mask_out is None)
+    except _NOT_SO:
+        sound = False
+    if not sound:
+        _check_verify(q, tree_k, tree_v, seq_lens, block_table, mask, parents, mask_out, dev, Hkv,
+                      d)
     stride = T if tree.dim() == 2 else 0
-    if mask_out is not None:
-        if parents is None:
-            raise ValueError("mask_out goes with parents")
-        _tensor(mask_out, "mask_out", _BITS64, tree.dim(), dev)
-        if mask_out.shape != tree.shape:
-            raise ValueError("mask_out must have the shape of parents")
     at = _Place(dev, stream)
     if out is None:
         out = at.empty(q.shape, _BF16)
