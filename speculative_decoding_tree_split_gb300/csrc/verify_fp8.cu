@@ -99,7 +99,7 @@ struct Shape {
     static constexpr int OFF_ALPHA = OFF_REF + R * 4;           // its last change, as a factor
     static constexpr int OFF_WMAX = OFF_ALPHA + R * 4;          // [4][R]: maxima / sums by warp
     static constexpr int OFF_MISC = OFF_WMAX + 4 * R * 4;
-    static constexpr int OFF_BAR = OFF_MISC + 256;
+    static constexpr int OFF_BAR = OFF_MISC + 320;
     // barriers
     static constexpr int KV_FULL = 0;
     static constexpr int KV_EMPTY = NS;
@@ -112,8 +112,10 @@ struct Shape {
     static constexpr int Q_FULL = S_FULL + 10;
     static constexpr int CHECK = S_FULL + 11;  // the softmax warps' vote on each block
     static constexpr int MEET = S_FULL + 12;   // the softmax warps meet
-    static constexpr int DRAIN = S_FULL + 13;
-    static constexpr int NBAR = S_FULL + 14;
+    static constexpr int SEG_FULL = S_FULL + 13;   // [2]: a segment has been announced
+    static constexpr int SEG_EMPTY = S_FULL + 15;  // [2]: every reader has it
+    static constexpr int DRAIN = S_FULL + 17;
+    static constexpr int NBAR = S_FULL + 18;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
     // TMEM columns: S in two buffers, then O.
     static constexpr int NB = 2;
@@ -126,14 +128,22 @@ struct Shape {
     static_assert(OFF_BAR + NBAR * 8 - OFF_SCALE <= SMALL, "small arrays fit their room");
 };
 
+// A piece of a unit's keys that this CTA takes, as the copies' warp announces it.
+struct Piece {
+    int b, hk, rb, slot;         // slot of its partial; -1: no more pieces
+    int chunk_begin, chunk_end;  // 64-token steps of the sequence
+    int L, pad;                  // committed tokens
+};
+
 struct Misc {
     uint32_t tmem_base;
     int abort;
     int pad[2];
+    Piece piece[2];
     uint8_t vote[2][32];  // by warp: an exponent left its range
     uint32_t qmax[32];    // by warp: the largest |q| bits seen
 };
-static_assert(sizeof(Misc) <= 256, "Misc fits its slot");
+static_assert(sizeof(Misc) <= 320, "Misc fits its slot");
 
 // tcgen05 instruction descriptor of kind::f8f6f4, e4m3 A and B, fp32 D.
 TA_HD uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
@@ -253,7 +263,7 @@ __device__ __forceinline__ void load_scores(uint32_t ta, float* x) {
     ptx::tmem_wait_ld();
 }
 
-__device__ __forceinline__ int blocks_of(const Segment& sg) {
+__device__ __forceinline__ int blocks_of(const Piece& sg) {
     return (sg.chunk_end - sg.chunk_begin + 1) / 2;
 }
 
@@ -290,6 +300,10 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         ptx::mbar_init(bar(S::Q_FULL), S::WARPS);
         ptx::mbar_init(bar(S::CHECK), S::WARPS);
         ptx::mbar_init(bar(S::MEET), S::WARPS);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(S::SEG_FULL + i), 1);
+            ptx::mbar_init(bar(S::SEG_EMPTY + i), S::WARPS + 1);
+        }
         ptx::mbar_init(bar(S::DRAIN), 1);
         misc->abort = 0;
         for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(misc->vote)[i] = 0;
@@ -310,27 +324,65 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
     // after that wait may the next kernel start (see tree_mask_kernel).
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const Range rg = plan_range(a, lane);
-    Walker w;
-    w.init_known(a.seq_lens, a.B, a.P, a.max_pages, a.Hkv * a.RB, a.RB, rg.b0, rg.base0, rg.x0,
-                 rg.x1, kTreeNone, 0, a.ovh, rg.lraw0);
     auto fail = [&]() {
         *abort_flag = 1;
         report(a.status, TREE_ATTN_STATUS_TIMEOUT);
     };
 
+    // Announced piece number k, for the MMA and softmax warps; false: no more, or
+    // a wait ran out.
+    auto next_piece = [&](uint32_t k, Piece& pc) -> bool {
+        if (!__all_sync(kFull, ptx::mbar_wait(bar(S::SEG_FULL + (k & 1)), (k >> 1) & 1,
+                                              a.wait_ns))) {
+            fail();
+            return false;
+        }
+        pc = misc->piece[k & 1];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(S::SEG_EMPTY + (k & 1)));
+        return pc.slot >= 0;
+    };
+
     if (warp == kWarpTma) {
-        // ================= copies: lane k < 8 takes box k of a block
+        // ================= this CTA's pieces and their copies: lane k < 8 takes
+        // box k of a block
+        const Range rg = plan_range(a, lane);
+        Walker w;
+        w.init_known(a.seq_lens, a.B, a.P, a.max_pages, a.Hkv * a.RB, a.RB, rg.b0, rg.base0, rg.x0,
+                     rg.x1, kTreeNone, 0, a.ovh, rg.lraw0);
         const int Pb = a.P < kChunk ? a.P : kChunk;  // tokens per box
         const int nsub = kChunk / Pb;                // boxes per 64-token step
         const int pshift = __ffs(a.P) - 1;
         const int hh = (lane >> 2) & 1, sub = lane & 3;
         uint32_t jj = 0;
         bool ok = true;
-        Segment sg;
-        while (ok && w.next(sg)) {
+        Segment sg = {};
+#pragma unroll 1
+        for (uint32_t k = 0; ok; ++k) {
+            const bool more = w.next(sg);
             bool bad;
             const int L = clamp_seq_len(sg.len_raw, a.P, a.max_pages, bad);
+            if (k >= 2 && !__all_sync(kFull, ptx::mbar_wait(bar(S::SEG_EMPTY + (k & 1)),
+                                                            ((k >> 1) - 1) & 1, a.wait_ns))) {
+                fail();
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                Piece pc;
+                pc.b = sg.b;
+                pc.hk = sg.hk;
+                pc.rb = sg.rb;
+                pc.slot = more ? sg.unit + static_cast<int>(blockIdx.x) : -1;
+                pc.chunk_begin = sg.chunk_begin;
+                pc.chunk_end = sg.chunk_end;
+                pc.L = L;
+                pc.pad = 0;
+                misc->piece[k & 1] = pc;
+                ptx::mbar_arrive(bar(S::SEG_FULL + (k & 1)));
+            }
+            __syncwarp();
+            if (!more) break;
             const int npages = (L + a.P - 1) >> pshift;
             const int32_t* table = a.block_table + static_cast<size_t>(sg.b) * a.max_pages;
             // 64 table entries from `base` on, two to a lane: looked up long
@@ -405,8 +457,8 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         const uint32_t id_o = idesc_e4m3_f32(D, S::N, true, true);
         uint32_t jj = 0, kk = 0;
         bool ok = true;
-        Segment sg;
-        while (ok && w.next(sg)) {
+        Piece sg;
+        while (ok && next_piece(kk, sg)) {
             if (!__all_sync(kFull, ptx::mbar_wait(bar(S::Q_FULL), kk & 1, a.wait_ns))) {
                 fail();
                 break;
@@ -525,10 +577,9 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         uint32_t jj = 0, kk = 0;
         uint32_t stage = 0, phase = 0;  // jj % NS, (jj / NS) & 1
         bool ok = true;
-        Segment cur;
-        while (ok && w.next(cur)) {
-            bool bad;
-            const int L = clamp_seq_len(cur.len_raw, a.P, a.max_pages, bad);
+        Piece cur;
+        while (ok && next_piece(kk, cur)) {
+            const int L = cur.L;
             const int Mrb = min(kRows, a.M - cur.rb * kRows);  // query rows of the tile
             // ---- the tile's queries: a common power of two brings the largest
             // |q| into [128, 256); each value is held as hi + lo, exactly down to
@@ -817,7 +868,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 ok = false;
                 break;
             }
-            float* slot = a.ws + static_cast<size_t>(cur.unit + blockIdx.x) * slot_floats(D);
+            float* slot = a.ws + static_cast<size_t>(cur.slot) * slot_floats(D);
             {
                 const int r = threadIdx.x;
                 if (r < Mrb) {
