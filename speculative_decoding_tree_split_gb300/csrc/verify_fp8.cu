@@ -85,15 +85,16 @@ struct Shape {
     static constexpr int TILE = kKeys * D;            // K (or V) codes of a block
     static constexpr int STAGE = 2 * TILE;
     static constexpr int Q_BYTES = N * D < 1024 ? 1024 : N * D;
-    static constexpr int P_ATOMS = N > 128 ? 2 : 1;   // 128-byte columns of the P tile
-    static constexpr int P_ATOM = kKeys * 128;
-    static constexpr int P_BYTES = P_ATOMS * P_ATOM;
+    static constexpr int PW = N <= 32 ? 32 : (N <= 64 ? 64 : 128);  // row bytes of a P tile
+    static constexpr int P_ATOM = kKeys * PW;
+    static constexpr int P_BYTES = (N > 128 ? 2 : 1) * P_ATOM;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + (Q_BYTES + 1023) / 1024 * 1024;
     static constexpr int OFF_STAGE = OFF_P + 2 * P_BYTES;
     static constexpr int SMALL = 8 * 1024;            // scales, references, barriers
     static constexpr int FIT = (227 * 1024 - 1024 - SMALL - OFF_STAGE) / STAGE;
-    static constexpr int NS = FIT > 6 ? 6 : FIT;      // ring depth
+    static constexpr int MOST = D == 128 ? 6 : 8;
+    static constexpr int NS = FIT > MOST ? MOST : FIT;  // ring depth
     static constexpr int OFF_SCALE = OFF_STAGE + NS * STAGE;  // [NS][K, V][128]
     static constexpr int OFF_REF = OFF_SCALE + NS * 2 * kKeys;  // reference of each row
     static constexpr int OFF_ALPHA = OFF_REF + R * 4;           // its last change, as a factor
@@ -151,21 +152,23 @@ TA_HD uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
            ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
-// Shared-memory descriptor of a tile whose rows are D bytes: 128-byte swizzle
-// (mode 2) for D = 128, 64-byte swizzle (mode 4) for D = 64; 8-row groups are
-// 8 * D bytes apart (the stride dimension for K-major and MN-major alike: a
-// row holds every M/N element of an MN-major tile).
-template <int D>
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
-           (static_cast<uint64_t>((8 * D) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(D == 128 ? 2 : 4) << 61);
+// Shared-memory descriptor of a tile whose rows are W = 128, 64 or 32 bytes, with
+// the swizzle of that width (modes 2, 4, 6).  8-row groups are 8 * W bytes apart
+// (the stride dimension for K-major and MN-major alike: a row holds W elements
+// of K, or of M/N); `lbo`: bytes between W-element columns of an MN-major tile.
+template <int W>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lbo = 16) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
+           (static_cast<uint64_t>(lbo >> 4) << 16) |
+           (static_cast<uint64_t>((8 * W) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(W == 128 ? 2 : (W == 64 ? 4 : 6)) << 61);
 }
 
 // Byte offset of 16-byte chunk c of row r in such a tile.
-template <int D>
+template <int W>
 __device__ __forceinline__ uint32_t tile_offset(uint32_t r, uint32_t c) {
-    return D == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+    const uint32_t x = W == 128 ? (r & 7u) : (W == 64 ? ((r >> 1) & 3u) : ((r >> 2) & 1u));
+    return r * W + ((c ^ x) << 4);
 }
 
 struct Range {
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                             for (int k = 0; k < 4; ++k) {
                                 if (k >= nk) break;
                                 ptx::mma_f8(tmem + S::TM_O, tile_desc<D>(vst + k * 32 * D),
-                                            smem_desc_sw128(pst + k * 32 * 128, S::P_ATOM, 1024),
+                                            tile_desc<S::PW>(pst + k * 32 * S::PW, S::P_ATOM),
                                             id_o, (np == 0 && k == 0) ? 0u : 1u);
                             }
                             ptx::mma_commit(bar(S::KV_EMPTY + j % S::NS));
@@ -655,9 +658,108 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 if (lane == 0) ptx::mbar_arrive(bar(S::Q_FULL));
             }
 
-            float l[H];
+            float l[H];  // the rows' sums over this thread's keys
 #pragma unroll
             for (int i = 0; i < H; ++i) l[i] = 0.f;
+            float x[H];  // scores of this thread's key, then its probabilities
+            // Moves the references up to block q's largest e where that stands near
+            // the limit (all rows' in a first block), and rescales l and O.
+            auto move_refs = [&](uint32_t q, bool first, bool valid, float F, float vs) -> bool {
+                load_scores<H>(lanes + S::TM_S + (q & 1) * R + row0, x);
+                // largest e of every row, by warp, then by tile (fmaxf passes over NaN)
+#pragma unroll
+                for (int i = 0; i < H; ++i) x[i] = valid ? fmaf(x[i], F, vs) : kNegInf;
+                reduce_columns<H>(x, lane, [](float u, float v) { return fmaxf(u, v); });
+#pragma unroll
+                for (int i = 0; i < (H + 31) / 32; ++i)
+                    if (i * 32 + lane < H) wmax[quad * R + row0 + i * 32 + lane] = x[i];
+                if (!meet()) return false;
+                const int r = threadIdx.x;
+                if (r < R) {
+                    const float top = fmaxf(fmaxf(wmax[r], wmax[R + r]),
+                                            fmaxf(wmax[2 * R + r], wmax[3 * R + r]));
+                    // (a first block of NaN scores has no largest: any finite reference)
+                    const float old = first ? kNegInf : -nref[r];
+                    const float now = top > old + kNear ? top : (first ? 0.f : old);
+                    nref[r] = -now;
+                    alpha[r] = ptx::ex2(old - now);
+                }
+                if (!meet()) return false;
+                if (first) return true;
+                // O holds the blocks before once P.V of the last has completed.
+                if (!wait_all(bar(S::P_FREE + ((q - 1) & 1)), ((q - 1) >> 1) & 1)) return false;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < H; c += 8) {
+                    float al[8];
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        al[i] = alpha[row0 + c + i];
+                        any |= al[i] != 1.f;
+                    }
+                    if (!any) continue;  // the same for the whole warpgroup
+                    const uint32_t to = lanes + S::TM_O + wg * 2 * H + 2 * c;
+                    float o[16];
+                    ptx::tmem_ld16(to, o);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        l[c + i] *= al[i];
+                        o[i] *= al[i];
+                        o[8 + i] *= al[i];
+                    }
+                    ptx::tmem_st8(to, o);
+                    ptx::tmem_st8(to + 8, o + 8);
+                }
+                ptx::tmem_wait_st();
+                return true;
+            };
+            // Block q's probabilities p = 2^(F s + scale of v - reference), into x and,
+            // as hi and lo = 16 (p - hi), into the key's row of the P tile (eight
+            // rows' hi codes beside their lo codes, 16 bytes); a key past the data has
+            // none.  Returns whether a p has passed 2^kMost (NaN has not).
+            auto probabilities = [&](uint32_t q, bool valid, float F, float vs) -> bool {
+                const uint64_t F2 = ptx::f2_pack(F, F), vs2 = ptx::f2_pack(vs, vs);
+                const uint32_t prow = sb + S::OFF_P + (q & 1) * S::P_BYTES;
+                load_scores<H>(lanes + S::TM_S + (q & 1) * R + row0, x);
+                __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+                for (int i = 0; i < H; i += 8) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int k = i + 2 * u;
+                        const float2 nr = *reinterpret_cast<const float2*>(nref + row0 + k);
+                        float e0, e1;
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[k], x[k + 1]), F2,
+                                                   ptx::f2_add(vs2, ptx::f2_pack(nr.x, nr.y))),
+                                       e0, e1);
+                        x[k] = ptx::ex2(e0);
+                        x[k + 1] = ptx::ex2(e1);
+                        const __half2 ph = __floats2half2_rn(x[k], x[k + 1]);
+                        top = __hmax2(top, ph);
+                        hi[u] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&ph));
+                        const uint32_t back = f16x2_of_e4m3x2(hi[u]);
+                        const __half2 rest =
+                            __hfma2(*reinterpret_cast<const __half2*>(&back),
+                                    __float2half2_rn(-16.f), __hmul2(ph, __float2half2_rn(16.f)));
+                        lo[u] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rest));
+                    }
+                    const int c = wg * (H / 8) + i / 8;  // 16-byte chunk of the key's row
+                    const uint32_t at = prow + (c * 16 / S::PW) * S::P_ATOM +
+                                        tile_offset<S::PW>(key, c % (S::PW / 16));
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                                 "r"(valid ? hi[0] | (hi[1] << 16) : 0u),
+                                 "r"(valid ? hi[2] | (hi[3] << 16) : 0u),
+                                 "r"(valid ? lo[0] | (lo[1] << 16) : 0u),
+                                 "r"(valid ? lo[2] | (lo[3] << 16) : 0u)
+                                 : "memory");
+                }
+                const float2 m = __half22float2(top);
+                return valid && fmaxf(m.x, m.y) > 256.f;
+            };
+            static_assert(kMost == 8.f, "the limit of p above");
             for (int ch = cur.chunk_begin; ch < cur.chunk_end; ch += 2, ++jj) {
                 const bool first = ch == cur.chunk_begin;
                 const int nh = min(2, cur.chunk_end - ch);
@@ -683,163 +785,12 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 const int vbyte = sc[kKeys + key];
                 const float F = scale_of(sc[key]) * c_scale;
                 const float vs = static_cast<float>(vbyte - 127);
-                const float wkey = inv_scale_of(vbyte);
-                const uint64_t F2 = ptx::f2_pack(F, F);
-                const uint64_t vs2 = ptx::f2_pack(vs, vs);
-                const uint32_t ta = lanes + S::TM_S + sbuf * R + row0;
-                const uint32_t prow = sb + S::OFF_P + sbuf * S::P_BYTES;
-                float x[H];  // this key's scores, e, then p
-                // Once, and once more when the references had to move.
-                bool move = first;
-#pragma unroll 1
-                while (true) {
-                    load_scores<H>(ta, x);
-                    const bool moved = move;
-                    if (move) {
-                        // Largest e of every row, by warp, then by tile (fmaxf
-                        // passes over NaN).
-#pragma unroll
-                        for (int i = 0; i < H; ++i) x[i] = valid ? fmaf(x[i], F, vs) : kNegInf;
-                        reduce_columns<H>(x, lane, [](float p, float q) { return fmaxf(p, q); });
-#pragma unroll
-                        for (int i = 0; i < (H + 31) / 32; ++i)
-                            if (i * 32 + lane < H) wmax[quad * R + row0 + i * 32 + lane] = x[i];
-                        load_scores<H>(ta, x);
-                        if (!meet()) {
-                            ok = false;
-                            break;
-                        }
-                        const int r = threadIdx.x;
-                        if (r < R) {
-                            const float top = fmaxf(fmaxf(wmax[r], wmax[R + r]),
-                                                    fmaxf(wmax[2 * R + r], wmax[3 * R + r]));
-                            // (a first block of NaN scores has no largest: any
-                            // finite reference)
-                            const float old = first ? kNegInf : -nref[r];
-                            const float now =
-                                top > old + kNear ? top : (first ? 0.f : old);
-                            nref[r] = -now;
-                            alpha[r] = ptx::ex2(old - now);
-                        }
-                        if (!meet()) {
-                            ok = false;
-                            break;
-                        }
-                        if (!first) {
-                            // O holds the blocks before once P.V of the last has
-                            // completed.
-                            if (!wait_all(bar(S::P_FREE + ((jj - 1) & 1)), ((jj - 1) >> 1) & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            ptx::tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < H; c += 8) {
-                                float al[8];
-                                bool any = false;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    al[i] = alpha[row0 + c + i];
-                                    any |= al[i] != 1.f;
-                                }
-                                if (!any) continue;  // the same for the whole warpgroup
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) l[c + i] *= al[i];
-#pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    const uint32_t to =
-                                        lanes + S::TM_O + wg * 2 * H + half * H + c;
-                                    float o[8];
-                                    ptx::tmem_ld8(to, o);
-                                    ptx::tmem_wait_ld();
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) o[i] *= al[i];
-                                    ptx::tmem_st8(to, o);
-                                }
-                            }
-                            ptx::tmem_wait_st();
-                        }
-                    }
-                    // e = F x + scale of v - reference
-                    float top = kNegInf;
-#pragma unroll
-                    for (int i = 0; i < H; i += 4) {
-                        const float4 nr = *reinterpret_cast<const float4*>(nref + row0 + i);
-#pragma unroll
-                        for (int u = 0; u < 4; u += 2) {
-                            const uint64_t bias =
-                                ptx::f2_add(vs2, u == 0 ? ptx::f2_pack(nr.x, nr.y)
-                                                        : ptx::f2_pack(nr.z, nr.w));
-                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i + u], x[i + u + 1]), F2, bias),
-                                           x[i + u], x[i + u + 1]);
-                            top = ptx::fmax3(top, x[i + u], x[i + u + 1]);
-                        }
-                    }
-                    if (!moved) {
-                        const bool over = __any_sync(kFull, valid && top > kMost);
-                        if (lane == 0) {
-                            *reinterpret_cast<volatile uint8_t*>(&misc->vote[jj & 1][warp]) = over;
-                            ptx::mbar_arrive(bar(S::CHECK));
-                        }
-                    }
-                    // p = 2^e as hi, and lo = 16 (p - hi), into the key's row of the
-                    // P tile; a key past the data has no probability.
-#pragma unroll
-                    for (int i = 0; i < H; i += 8) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int k = i + 2 * u;
-                            x[k] = ptx::ex2(x[k]);
-                            x[k + 1] = ptx::ex2(x[k + 1]);
-                            const __half2 ph = __floats2half2_rn(x[k], x[k + 1]);
-                            hi[u] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&ph));
-                            const uint32_t back = f16x2_of_e4m3x2(hi[u]);
-                            const __half2 rest =
-                                __hfma2(*reinterpret_cast<const __half2*>(&back),
-                                        __float2half2_rn(-16.f), __hmul2(ph, __float2half2_rn(16.f)));
-                            lo[u] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rest));
-                        }
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint32_t* c = half == 0 ? hi : lo;
-                            const int n = wg * 2 * H + half * H + i;  // byte of the key's row
-                            const uint32_t at = prow + (n >> 7) * S::P_ATOM +
-                                                sw128_offset(key, (n >> 4) & 7) + (n & 8);
-                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
-                                         "r"(valid ? c[0] | (c[1] << 16) : 0u),
-                                         "r"(valid ? c[2] | (c[3] << 16) : 0u)
-                                         : "memory");
-                        }
-                    }
-                    if (moved) break;
-                    // (the vote of a block is one per block but the first of each segment)
-                    if (!wait_all(bar(S::CHECK), (jj - kk - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint4* v4 = reinterpret_cast<const uint4*>(misc->vote[jj & 1]);
-                    uint32_t votes = 0;
-#pragma unroll
-                    for (int i = 0; i < (S::WARPS + 15) / 16; ++i) {
-                        const uint4 v = v4[i];
-                        votes |= v.x | v.y | v.z | v.w;
-                    }
-                    if (votes == 0) break;
-                    move = true;
+                if (first && !move_refs(jj, true, valid, F, vs)) {
+                    ok = false;
+                    break;
                 }
-                if (!ok) break;
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(S::S_FREE + sbuf));
-                if (valid) {
-                    const uint64_t w2 = ptx::f2_pack(wkey, wkey);
-#pragma unroll
-                    for (int i = 0; i < H; i += 2)
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), w2,
-                                                   ptx::f2_pack(l[i], l[i + 1])),
-                                       l[i], l[i + 1]);
-                } else if (wg == 0 && key < nh * kChunk) {
+                const bool over = probabilities(jj, valid, F, vs);
+                if (!valid && wg == 0 && key < nh * kChunk) {
                     // 0 * NaN is not 0: the value rows past the data are cleared.
                     const uint32_t vrow = sb + S::OFF_STAGE + stage * S::STAGE + S::TILE + key * D;
 #pragma unroll
@@ -850,9 +801,49 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                                      : "memory");
                 }
                 ptx::fence_proxy_async_smem();
+                if (!first) {
+                    // P is handed over only when every warp has found its p in
+                    // range (one vote per block but the first of each piece).
+                    const bool any = __any_sync(kFull, over);
+                    if (lane == 0) {
+                        *reinterpret_cast<volatile uint8_t*>(&misc->vote[sbuf][warp]) = any;
+                        ptx::mbar_arrive(bar(S::CHECK));
+                    }
+                    if (!wait_all(bar(S::CHECK), (jj - kk - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint4* v4 = reinterpret_cast<const uint4*>(misc->vote[sbuf]);
+                    uint32_t votes = 0;
+#pragma unroll
+                    for (int i = 0; i < (S::WARPS + 15) / 16; ++i) {
+                        const uint4 v = v4[i];
+                        votes |= v.x | v.y | v.z | v.w;
+                    }
+                    if (votes != 0) {
+                        if (!move_refs(jj, false, valid, F, vs)) {
+                            ok = false;
+                            break;
+                        }
+                        (void)probabilities(jj, valid, F, vs);
+                        ptx::fence_proxy_async_smem();
+                    }
+                }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(S::P_FULL + (jj & 1)));
+                if (lane == 0) {
+                    ptx::mbar_arrive(bar(S::P_FULL + sbuf));
+                    ptx::mbar_arrive(bar(S::S_FREE + sbuf));
+                }
+                if (valid) {
+                    const float wkey = inv_scale_of(vbyte);
+                    const uint64_t w2 = ptx::f2_pack(wkey, wkey);
+#pragma unroll
+                    for (int i = 0; i < H; i += 2)
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[i], x[i + 1]), w2,
+                                                   ptx::f2_pack(l[i], l[i + 1])),
+                                       l[i], l[i + 1]);
+                }
                 if (++stage == S::NS) {
                     stage = 0;
                     phase ^= 1;
@@ -887,15 +878,14 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             float* acc = slot + 2 * kRows + dim;
 #pragma unroll
             for (int c = 0; c < H; c += 8) {
-                float o[8], o2[8];
-                ptx::tmem_ld8(lanes + S::TM_O + wg * 2 * H + c, o);
-                ptx::tmem_ld8(lanes + S::TM_O + wg * 2 * H + H + c, o2);
+                float o[16];  // eight rows' hi sums, then their lo sums
+                ptx::tmem_ld16(lanes + S::TM_O + wg * 2 * H + 2 * c, o);
                 ptx::tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = row0 + c + i;
                     if (r < Mrb && (D == 128 || lane < 16))
-                        acc[static_cast<size_t>(r) * D] = fmaf(o2[i], 0.0625f, o[i]);
+                        acc[static_cast<size_t>(r) * D] = fmaf(o[8 + i], 0.0625f, o[i]);
                 }
             }
             ptx::tc_fence_before();
@@ -946,7 +936,7 @@ cudaError_t launch_prefix_fp8_rows(const Fp8Args& a, const CUtensorMap& tk,
     if (rows <= 48) return launch_prefix_fp8<D, 48, 3>(a, tk, tv, dev, stream);
     if (rows <= 64) return launch_prefix_fp8<D, 64, 4>(a, tk, tv, dev, stream);
     if (rows <= 80) return launch_prefix_fp8<D, 80, 2>(a, tk, tv, dev, stream);
-    return launch_prefix_fp8<D, 128, 4>(a, tk, tv, dev, stream);
+    return launch_prefix_fp8<D, 128, 2>(a, tk, tv, dev, stream);
 }
 
 // The [num_pages * Hkv * P][d] codes of a pool in boxes of up to 64 tokens.
