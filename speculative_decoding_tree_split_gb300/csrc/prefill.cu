@@ -288,8 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             uint32_t t = 0;  // tiles loaded so far
             bool ok = true, asked = false;
+            uint32_t k = 0;
 #pragma unroll 1
-            for (uint32_t k = 0; u.rb >= 0; ++k) {
+            for (; u.rb >= 0; ++k) {
                 // One unit ahead: the answer comes in while this one is loaded.
                 if (lane == 0) {
                     ptx::fence_proxy_async_smem();  // the last answer has been read
@@ -361,15 +362,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!load(min(n2, S::NS), n2)) break;
                 u = nxt;
             }
-            // Copies and an answer in flight land before the CTA exits.
-            if (*abort_flag && lane == 0) {
+            // Copies and an answer in flight land before the CTA exits, whoever has
+            // given up.
+            if (lane == 0) {
                 for (uint32_t i = t > S::NS ? t - S::NS : 0; i < t; ++i)
                     (void)ptx::mbar_wait(bar(S::FULL + i % S::NS), (i / S::NS) & 1,
                                          ptx::kDrainLimitNs);
-                // (an answer asked for at the last unit: its phase is odd or even)
-                if (asked && !ptx::mbar_wait(bar(S::ANSWER), 0, ptx::kDrainLimitNs / 16))
-                    (void)ptx::mbar_wait(bar(S::ANSWER), 1, ptx::kDrainLimitNs);
+                if (asked) (void)ptx::mbar_wait(bar(S::ANSWER), k & 1, ptx::kDrainLimitNs);
             }
+            __syncwarp();
         } else if (warp == kWarpMma) {
             // ================= MMA issuer (the whole warp walks, one lane issues)
             const bool lead = ptx::elect_one();

@@ -445,12 +445,10 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 __syncwarp();
             }
         }
-        if (!ok) {
-            const uint32_t first = jj > S::NS ? jj - S::NS : 0;
-            for (uint32_t j = first; j < jj; ++j)
-                (void)ptx::mbar_wait(bar(S::KV_FULL + j % S::NS), (j / S::NS) & 1,
-                                     ptx::kDrainLimitNs);
-        }
+        // Every copy lands before the CTA exits, whoever has given up.
+        const uint32_t first = jj > S::NS ? jj - S::NS : 0;
+        for (uint32_t j = first; j < jj; ++j)
+            (void)ptx::mbar_wait(bar(S::KV_FULL + j % S::NS), (j / S::NS) & 1, ptx::kDrainLimitNs);
     } else if (warp == kWarpMma) {
         // ================= MMA issuer: the whole warp walks, one lane issues.
         // It polls without waiting: a suspended poll for P would hold up the

@@ -130,6 +130,34 @@ def test_append_is_bit_exact_and_writes_nothing_else(lens, starts, Hkv, d, P, la
     assert_same(got, cache[:4])
 
 
+@pytest.mark.parametrize("Hkv,d,P", [(1, 128, 64), (2, 64, 16)])
+def test_append_and_read_of_many_tokens(Hkv, d, P):
+    # enough tokens that the larger tile of the two kernels is used on any GPU
+    # of up to 160 SMs, none of the ranges a multiple of it
+    lens, starts = [9001, 0, 1, 2003, 17], [5, 0, 63, 1, P]
+    N = sum(lens)
+    assert N // 16 >= 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    cache = make_cache([s + n for s, n in zip(starts, lens)], Hkv, d, P)
+    k, v = edge_rows(rows(N, Hkv, d, 21)), edge_rows(rows(N, Hkv, d, 22))
+    got, status = dev(cache), ints([0])
+    cu = cumulate(lens)
+    ta.kv_append_fp8(*got, ints(starts), ints(cu), k.cuda(), v.cuda(), status=status)
+    seq = torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(lens))
+    pos = torch.arange(N) - torch.tensor(cu)[seq] + torch.tensor(starts)[seq]
+    page, off = cache[4][seq, pos // P].long(), pos % P
+    values = []
+    for w, x in enumerate((k, v)):
+        codes, scale = fp8_rows.encode(x.double().numpy())
+        values.append(fp8_rows.decode(codes, scale))
+        cache[w][page, :, off] = torch.from_numpy(codes)
+        cache[2 + w][page, :, off] = torch.from_numpy(scale)
+    assert_same(got, cache[:4])
+    back = ta.kv_read_fp8(*got, ints(cu), N, starts=ints(starts), status=status)
+    assert int(status) == 0
+    for x, want in zip(back, values):
+        assert np.array_equal(x.double().cpu().numpy(), want, equal_nan=True)
+
+
 def test_append_takes_float8_pools():
     cache = make_cache([9], 1, 64, 16)
     x = rows(9, 1, 64, 3)

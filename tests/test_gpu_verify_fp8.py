@@ -111,6 +111,14 @@ CASES = [
     (cfg(1, 16, 2, 64, 16, 64), [130]),                # 512 rows
     (cfg(5, 2, 2, 64, 128, 7), [5, 0, 256, 128, 511]),
     (cfg(1, 3, 1, 128, 64, 64, "chain"), [2000]),
+    (cfg(2, 8, 1, 128, 32, 4), [77, 900]),             # 32 rows
+    (cfg(2, 8, 2, 64, 64, 8), [64, 391]),              # 32 rows
+    (cfg(1, 12, 1, 64, 16, 4), [700]),                 # 48 rows
+    (cfg(2, 16, 2, 128, 64, 8), [1, 555]),             # 64 rows
+    (cfg(2, 8, 1, 64, 128, 8), [200, 333]),            # 64 rows
+    (cfg(1, 10, 2, 64, 32, 16), [1023]),               # 80 rows
+    (cfg(70, 4, 1, 64, 16, 2), [(37 * i) % 90 for i in range(70)]),  # many short sequences
+    (cfg(300, 1, 1, 128, 64, 1), [(29 * i) % 150 for i in range(300)]),
 ]
 
 
