@@ -1840,7 +1840,7 @@ cudaError_t launch_merge_d(const VerifyArgs& v, cudaStream_t stream) {
     const Plan plan =
         make_plan(v.B, v.Hq, v.Hkv, v.T, v.P, v.max_pages, v.n_ctas, v.n_ctas, v.tmode);
     const long long units = plan.units;
-    const int F = v.copies > 0 ? v.copies : plan.F;
+    const int F = plan.F;
     ma.wpr = plan.merge_wpr;
     ma.rpw = plan.merge_rpw;
     const int rows = M < kRows ? M : kRows;

@@ -43,7 +43,6 @@ struct VerifyArgs {
     int ovh;  // overhead slots per unit on the work line (the kernel selector's)
     unsigned long long wait_ns;  // limit of a pipeline wait in the prefix pass
     int early;  // plan and first committed-prefix loads before the dependency wait
-    int copies; // row copies per partial the merge finds; 0: the kernel selector's
 };
 
 // Enqueue the explicit-mask builder: dense[b][t][p] for p < dense_cols and

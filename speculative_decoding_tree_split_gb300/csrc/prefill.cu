@@ -34,7 +34,7 @@
 #include "kernels.cuh"
 #include "launch.cuh"
 #include "layout.h"
-#include "ptx.cuh"
+#include "ptx_serving.cuh"
 #include "tma_host.h"
 
 namespace treeattn {

@@ -1,8 +1,8 @@
-// verify_fp8.cu -- split tree attention over the 8-bit paged cache: the prefix
-// pass over committed rows (this file), then the tree pass and log-sum-exp
-// merge of kernels.cu on the partials it leaves.
+// verify_fp8.cu -- split tree attention over the 8-bit paged cache: a prefix pass
+// over the committed rows, which leaves partial results, then a kernel that
+// attends the tree tokens and merges everything by log-sum-exp.
 //
-// For a unit (sequence, KV head) with R query rows (tree nodes x grouped heads)
+// Prefix pass.  For a unit (sequence, KV head) with R query rows (tree nodes x grouped heads)
 // and keys j held as codes with scales:
 //   x_rj = c F_j <q_r, k_j>,  F_j = 2^(scale of k_j),  c = softmax scale log2(e)
 //   out_r = sum_j 2^x_rj 2^(scale of v_j) v_j / sum_j 2^x_rj.
@@ -38,7 +38,7 @@
 #include "kernels.cuh"
 #include "launch.cuh"
 #include "layout.h"
-#include "ptx.cuh"
+#include "ptx_serving.cuh"
 #include "tma_host.h"
 
 namespace treeattn {
@@ -46,6 +46,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kKeys = 2 * kChunk;  // keys of a block
 // p = 2^(e - reference) may reach 2^kMost (e4m3 ends at 448).  When a block
 // passes that, the references of all rows whose maximum stands above 2^kNear
@@ -906,6 +907,492 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
     }
 }
 
+// ---------------------------------------------------------------------------
+// Tree pass and merge.  A CTA takes 4 RW query rows of a unit, a warp RW of them.
+//
+// Tree pass (reads only this call's inputs, so it runs before the wait for the
+// prefix pass): S = Q K^T and O = P V over at most 64 tree tokens with bf16
+// mma.sync, whose tile is 16 rows; P enters as two bf16 rows (value and
+// remainder), because a row may see only a few tree tokens.  Scores of hidden
+// tokens become -inf whatever K holds; a non-finite V value is left out of the
+// product and added to the rows that see it.
+//
+// Merge: a warp reads whole rows of the partials, eight loads of 16 bytes to a lane
+// in flight together with the references and sums.  It is bound by round trips:
+// with few rows a CTA takes four, so that every warp has one row and its
+// partials come in one or two trips.
+// ---------------------------------------------------------------------------
+constexpr int kTileRows = 16;
+constexpr int kMergeCtaWarps = 4;
+constexpr int kMergeThreads = 32 * kMergeCtaWarps;
+
+struct TreeMergeArgs {
+    const uint16_t* q;
+    const uint16_t* tree_k;
+    const uint16_t* tree_v;
+    const uint64_t* mask;
+    int mask_stride;
+    const int32_t* parents;
+    int parents_stride;
+    uint64_t* mask_out;
+    const int32_t* seq_lens;
+    const float* ws;
+    uint16_t* out;
+    float* lse;
+    int32_t* status;
+    int B, Hq, Hkv, G, T, M, RB, P, max_pages, n_ctas, ovh;
+    float scale_log2;
+};
+
+// D += A B for one 16 x 8 tile, 16 deep, bf16 in, fp32 out.
+__device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Ancestor-or-self bits of nodes lane and lane + 32 by following parents six
+// doublings deep; an invalid parent makes its node a root and is told of.
+__device__ bool ancestor_bits(const int32_t* parents, int T, int lane, uint64_t bits[2]) {
+    int jump[2];
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h;
+        int p = i < T ? parents[i] : -1;
+        if (p < -1 || p >= i) {
+            bad = bad || i < T;
+            p = -1;
+        }
+        jump[h] = p;
+        bits[h] = i < T ? 1ull << i : 0ull;
+    }
+#pragma unroll
+    for (int round = 0; round < 6; ++round) {
+        uint64_t nb[2];
+        int nj[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = max(jump[h], 0);
+            const uint64_t b0 = __shfl_sync(kFull, bits[0], j & 31);
+            const uint64_t b1 = __shfl_sync(kFull, bits[1], j & 31);
+            const int j0 = __shfl_sync(kFull, jump[0], j & 31);
+            const int j1 = __shfl_sync(kFull, jump[1], j & 31);
+            const bool on = jump[h] >= 0;
+            nb[h] = on ? bits[h] | (j < 32 ? b0 : b1) : bits[h];
+            nj[h] = on ? (j < 32 ? j0 : j1) : -1;
+        }
+        bits[0] = nb[0];
+        bits[1] = nb[1];
+        jump[0] = nj[0];
+        jump[1] = nj[1];
+    }
+    return __any_sync(kFull, bad);
+}
+
+// A pair of bf16 halves with those that are not finite set to zero.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    return w;
+}
+
+template <int D, int RW>
+__global__ void __launch_bounds__(kMergeThreads, 6) tree_merge_fp8_kernel(const TreeMergeArgs a) {
+    constexpr int ROWS = RW * kMergeCtaWarps;  // of this CTA: 4 or 16
+    constexpr int NT = D / 8 / kMergeCtaWarps;  // 8-wide accumulator tiles of a warp
+    __shared__ float s_score[kTileRows][TREE_ATTN_MAX_T + 4];  // then P, hi | lo << 16
+    __shared__ uint64_t s_bits[TREE_ATTN_MAX_T];
+    __shared__ float s_m[ROWS], s_l[ROWS];  // the tree's share: reference, sum,
+    __shared__ __align__(16) float s_o[ROWS][D + 4];  // accumulator
+    __shared__ int s_first, s_count, s_all;
+    __shared__ uint32_t s_has;  // which of the first 32 partials there are
+    __shared__ long long s_W;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x;
+    const int rb = unit % a.RB;
+    const int hk = (unit / a.RB) % a.Hkv;
+    const int b = unit / (a.RB * a.Hkv);
+    const int r0 = blockIdx.y * ROWS;  // first row of the row block taken here
+    // The next kernel waits for this grid before it writes anything read here.
+    ptx::grid_dep_launch();
+
+    auto row_at = [&](int r) -> int { return rb * kRows + r0 + r; };  // row of the unit
+    auto row_ok = [&](int r) -> bool {
+        return r < ROWS && r0 + r < kRows && row_at(r) < a.M;
+    };
+    // Element offset of row r's d values in q and out; lse has one per d.
+    auto row_offset = [&](int r) -> long long {
+        const int rr = row_at(r);
+        return ((static_cast<long long>(b) * a.T + rr / a.G) * a.Hq + hk * a.G + rr % a.G) * D;
+    };
+    const int g = lane >> 2, t = lane & 3;  // lane of an accumulator: rows g, g + 8
+
+    // ---- tree scores: 16 tokens to a warp
+    {
+        const int key0 = warp * 16;
+        float c[2][4] = {};
+        if (key0 < a.T) {
+            // A lane holds eight consecutive elements of rows g and g + 8 and of
+            // token g of each 8-token tile: a dot product does not mind which of
+            // the 16 places of a step an element takes.
+            const uint16_t* q0 = a.q + row_offset(row_ok(g) ? g : 0) + t * 8;
+            const uint16_t* q1 = a.q + row_offset(row_ok(g + 8) ? g + 8 : 0) + t * 8;
+            auto token = [&](int j) -> const uint16_t* {
+                return a.tree_k +
+                       ((static_cast<long long>(b) * a.T + min(j, a.T - 1)) * a.Hkv + hk) * D +
+                       t * 8;
+            };
+            const uint16_t* k0 = token(key0 + g);
+            const uint16_t* k1 = token(key0 + 8 + g);
+            uint4 x[4][D / 32];
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s) {
+                x[0][s] = __ldg(reinterpret_cast<const uint4*>(q0 + s * 32));
+                x[1][s] = __ldg(reinterpret_cast<const uint4*>(q1 + s * 32));
+                x[2][s] = __ldg(reinterpret_cast<const uint4*>(k0 + s * 32));
+                x[3][s] = __ldg(reinterpret_cast<const uint4*>(k1 + s * 32));
+            }
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s) {
+                const uint32_t a0[4] = {x[0][s].x, x[1][s].x, x[0][s].y, x[1][s].y};
+                const uint32_t a1[4] = {x[0][s].z, x[1][s].z, x[0][s].w, x[1][s].w};
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    mma_16816(c[n], a0, x[2 + n][s].x, x[2 + n][s].y);
+                    mma_16816(c[n], a1, x[2 + n][s].z, x[2 + n][s].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s_score[g + 8 * (i >> 1)][key0 + 8 * n + 2 * t + (i & 1)] = c[n][i] * a.scale_log2;
+    }
+    // ---- masks (warp 3: the one least likely to have had tokens)
+    if (warp == 3) {
+        uint64_t bits[2] = {0ull, 0ull};
+        if (a.parents != nullptr) {
+            const bool bad = ancestor_bits(
+                a.parents + static_cast<size_t>(b) * a.parents_stride, a.T, lane, bits);
+            // One CTA per tree reports and writes the masks out.
+            const bool writer = unit == b * a.Hkv * a.RB && blockIdx.y == 0 &&
+                                (a.parents_stride != 0 || b == 0);
+            if (writer && bad && lane == 0) report(a.status, TREE_ATTN_STATUS_BAD_PARENT);
+            if (writer && a.mask_out != nullptr) {
+                uint64_t* mo = a.mask_out + static_cast<size_t>(b) * a.parents_stride;
+                if (lane < a.T) mo[lane] = bits[0];
+                if (lane + 32 < a.T) mo[lane + 32] = bits[1];
+            }
+        } else {
+            const uint64_t live = a.T < 64 ? (1ull << a.T) - 1ull : ~0ull;
+            const uint64_t* m = a.mask + static_cast<size_t>(b) * a.mask_stride;
+            if (lane < a.T) bits[0] = m[lane] & live;
+            if (lane + 32 < a.T) bits[1] = m[lane + 32] & live;
+        }
+        s_bits[lane] = bits[0];
+        s_bits[lane + 32] = bits[1];
+    }
+    // ---- the prefix CTAs that hold this unit's partials (warp 2): s_first and the
+    // s_count - 1 behind it
+    if (warp == 2) {
+        long long W = 0, base = 0;
+        int nch = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int bi = b0 + lane;
+            bool bad;
+            const int n =
+                bi < a.B ? unit_chunks(a.seq_lens[bi], a.P, a.max_pages, kTreeNone, 0, bad) : 0;
+            const int len = unit_len(n, a.ovh);
+            W += __reduce_add_sync(kFull, len);
+            base += __reduce_add_sync(kFull, bi < b ? len : 0);
+            nch += __reduce_add_sync(kFull, bi == b ? n : 0);
+        }
+        const int upb = a.Hkv * a.RB;
+        W *= upb;
+        base *= upb;
+        int first = 0, count = 0;
+        if (nch > 0) {
+            const long long start =
+                base + static_cast<long long>(unit - b * upb) * unit_len(nch, a.ovh);
+            first = cta_of(start, W, a.n_ctas);
+            count = cta_of(start + nch - 1, W, a.n_ctas) - first + 1;
+        }
+        // With a step or more to every CTA each of them has a partial.
+        const bool all = W >= a.n_ctas;
+        const uint32_t some = __ballot_sync(
+            kFull, lane < count && (all || cta_has_work(first + lane, W, a.n_ctas)));
+        if (lane == 0) {
+            s_first = first;
+            s_count = count;
+            s_all = all;
+            s_has = some;
+            s_W = W;
+        }
+    }
+    __syncthreads();
+
+    // ---- softmax of the tree scores, RW rows to a warp (the tile's other rows are
+    // never looked at)
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const int r = warp * RW + i;
+        const uint64_t bits = row_ok(r) ? s_bits[row_at(r) / a.G] : 0ull;
+        const bool see0 = (bits >> lane) & 1ull, see1 = (bits >> (lane + 32)) & 1ull;
+        const float x0 = see0 ? s_score[r][lane] : kNegInf;
+        const float x1 = see1 ? s_score[r][lane + 32] : kNegInf;
+        float m = fmaxf(x0, x1);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+        const float ref = m == kNegInf ? 0.f : m;
+        const float p0 = see0 ? ptx::ex2(x0 - ref) : 0.f;
+        const float p1 = see1 ? ptx::ex2(x1 - ref) : 0.f;
+        float l = p0 + p1;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+        if (lane == 0) {
+            // (a row of NaN scores has no largest; its sum is NaN all the same)
+            s_m[r] = bits != 0 && m == kNegInf ? 0.f : m;
+            s_l[r] = l;
+        }
+        auto split = [](float p) -> float {
+            const uint32_t hi = pack_bf16(p, 0.f) & 0xffffu;
+            const uint32_t lo = pack_bf16(p - __uint_as_float(hi << 16), 0.f) & 0xffffu;
+            return __uint_as_float(hi | (lo << 16));
+        };
+        s_score[r][lane] = split(p0);
+        s_score[r][lane + 32] = split(p1);
+    }
+    __syncthreads();
+
+    // ---- O = P V: this thread's dimensions are dim .. dim + 2 NT - 1.  Column c of
+    // tile n stands for dimension dim0 + NT c + n, so that a lane's B elements of all
+    // tiles (columns g) and its accumulator's (columns 2t, 2t + 1) lie side by side.
+    {
+    const int dim0 = warp * NT * 8;
+    const int dim = dim0 + 2 * t * NT;
+    float o[NT][4] = {};
+    {
+        const uint16_t* v0 = a.tree_v + (static_cast<long long>(b) * a.T * a.Hkv + hk) * D;
+        const long long vs = static_cast<long long>(a.Hkv) * D;  // from token to token
+        bool odd = false;  // a value that is not finite
+        static_assert(NT == 4 || NT == 2, "columns of a lane");
+        constexpr int NW = NT / 2;  // 32-bit words of a lane's NT columns
+#pragma unroll 2
+        for (int k0 = 0; k0 < a.T; k0 += 16) {
+            uint32_t vw[4][NW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = min(k0 + 2 * t + (i & 1) + 8 * (i >> 1), a.T - 1);
+                const uint16_t* p = v0 + j * vs + dim0 + NT * g;
+                if constexpr (NT == 4) {
+                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+                    vw[i][0] = w.x;
+                    vw[i][NW - 1] = w.y;
+                } else {
+                    vw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+                }
+            }
+            bool here = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+                    here |= (((vw[i][w] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u) != 0;
+            if (__any_sync(kFull, here)) {
+                odd = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) vw[i][w] = finite_pair(vw[i][w]);
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = g + 8 * (i & 1), k = k0 + 2 * t + 8 * (i >> 1);
+                const uint32_t u0 = __float_as_uint(s_score[r][k]);
+                const uint32_t u1 = __float_as_uint(s_score[r][k + 1]);
+                hi[i] = __byte_perm(u0, u1, 0x5410);
+                lo[i] = __byte_perm(u0, u1, 0x7632);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint32_t pick_half = n & 1 ? 0x7632 : 0x5410;
+                const uint32_t b0 = __byte_perm(vw[0][n / 2], vw[1][n / 2], pick_half);
+                const uint32_t b1 = __byte_perm(vw[2][n / 2], vw[3][n / 2], pick_half);
+                mma_16816(o[n], hi, b0, b1);
+                mma_16816(o[n], lo, b0, b1);
+            }
+        }
+        if (odd) {
+#pragma unroll 1
+            for (int j = 0; j < a.T; ++j)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = g + 8 * (i >> 1);
+                        const uint32_t v = __ldg(v0 + j * vs + dim + (i & 1) * NT + n);
+                        if ((v & 0x7f80u) == 0x7f80u && row_ok(r) &&
+                            ((s_bits[row_at(r) / a.G] >> j) & 1ull))
+                            o[n][i] += __uint_as_float(v << 16);
+                    }
+        }
+    }
+
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = g + 8 * i;
+            if (r >= ROWS) continue;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                s_o[r][dim + n] = o[n][2 * i];
+                s_o[r][dim + NT + n] = o[n][2 * i + 1];
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- merge with the prefix pass's partials (read through L2: the prefix grid
+    // writes them while this one is resident)
+    ptx::grid_dep_wait();
+    constexpr int E = D / 32;    // dimensions of a lane
+    constexpr int PF = 8 / RW;   // partials of a row in flight
+    const int count = s_count;
+    const uint32_t some = s_has;
+    const size_t sf = static_cast<size_t>(slot_floats(D));
+    const float* slots = a.ws + static_cast<size_t>(unit + s_first) * sf;
+    auto has = [&](int v) -> bool {
+        if (v < 32) return (some >> v) & 1u;
+        return v < count && (s_all || cta_has_work(s_first + v, s_W, a.n_ctas));
+    };
+    // E accumulator values of row r in partial v; a partial that is not there has
+    // weight 0 and is read as slot 0, so that no branch stands between loads.
+    auto fetch = [&](int v, int r, float* x) {
+        const float* p = slots + static_cast<size_t>(has(v) ? v : 0) * sf + 2 * kRows +
+                         static_cast<size_t>(r) * D + lane * E;
+        if constexpr (E == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(p));
+            x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+        } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(p));
+            x[0] = f.x, x[1] = f.y;
+        }
+    };
+    int at[RW];  // rows of the slots; a row that is not there reads the first
+    bool live[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        live[i] = row_ok(warp * RW + i);
+        at[i] = r0 + (live[i] ? warp * RW + i : 0);
+    }
+    float x[RW][PF][E], m[RW], l[RW];
+    if (count > 0) {
+        // One round trip: references and sums (lane v: partial v) and the first
+        // partials' accumulators.
+        const float* mine = slots + static_cast<size_t>(has(lane) ? lane : 0) * sf;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            m[i] = __ldcg(mine + at[i]);
+            l[i] = __ldcg(mine + kRows + at[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < PF; ++k)
+#pragma unroll
+            for (int i = 0; i < RW; ++i) fetch(k, at[i], x[i][k]);
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const int r = warp * RW + i;
+        if (count == 0 || !has(lane)) {
+            m[i] = kNegInf;
+            l[i] = 0.f;
+        }
+        float top = m[i];
+        for (int v0 = 32; v0 < count; v0 += 32)  // (rare)
+            if (has(v0 + lane))
+                top = fmaxf(top, __ldcg(slots + static_cast<size_t>(v0 + lane) * sf + at[i]));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+        top = fmaxf(top, s_m[r]);
+        const float ref = top == kNegInf ? 0.f : top;
+        float w = ptx::ex2(m[i] - ref);  // lane v: weight of partial v
+        float sum = m[i] == kNegInf ? 0.f : w * l[i];
+        const float ws = ptx::ex2(s_m[r] - ref);
+        float o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = ws * s_o[r][lane * E + e];
+        for (int v0 = 0; v0 < count; v0 += 32) {
+            if (v0 > 0) {
+                float lv = 0.f;
+                w = 0.f;
+                if (has(v0 + lane)) {
+                    const float* p = slots + static_cast<size_t>(v0 + lane) * sf + at[i];
+                    w = ptx::ex2(__ldcg(p) - ref);
+                    lv = __ldcg(p + kRows);
+                }
+                sum = fmaf(w, lv, sum);
+            }
+            const int here = min(32, count - v0);
+            for (int k0 = 0; k0 < here; k0 += PF) {
+                if (v0 + k0 > 0) {
+#pragma unroll
+                    for (int k = 0; k < PF; ++k) fetch(v0 + k0 + k, at[i], x[i][k]);
+                }
+#pragma unroll
+                for (int k = 0; k < PF; ++k) {
+                    const float wk = __shfl_sync(kFull, w, (k0 + k) & 31);
+                    if (k0 + k >= here) continue;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] = fmaf(wk, x[i][k][e], o[e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+        sum = fmaf(ws, s_l[r], sum);
+        if (!live[i]) continue;
+        const bool none = top == kNegInf;  // no key at all
+        const float inv = none ? 0.f : 1.f / sum;
+        const long long to = row_offset(r);
+        uint32_t word[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            word[e / 2] = none ? 0u : pack_bf16(o[e] * inv, o[e + 1] * inv);
+        uint16_t* dst = a.out + to + lane * E;
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(word[0], word[1]);
+        else
+            *reinterpret_cast<uint32_t*>(dst) = word[0];
+        if (lane == 0) a.lse[to / D] = none ? kNegInf : (top + log2f(sum)) * kLn2;
+    }
+}
+
+// Four rows to a CTA as long as all CTAs run at once (six to an SM), else sixteen:
+// the tree's scores are then made for fewer CTAs.
+template <int D>
+cudaError_t launch_tree_merge(const TreeMergeArgs& v, int units, int sms, cudaStream_t stream) {
+    const int rows = v.M < kRows ? v.M : kRows;
+    const unsigned fours = static_cast<unsigned>((rows + 3) / 4);
+    if (static_cast<long long>(units) * fours <= 6LL * sms)
+        return launch_dependent(tree_merge_fp8_kernel<D, 1>,
+                                dim3(static_cast<unsigned>(units), fours), dim3(kMergeThreads), 0,
+                                stream, v);
+    return launch_dependent(
+        tree_merge_fp8_kernel<D, 4>,
+        dim3(static_cast<unsigned>(units), static_cast<unsigned>((rows + 15) / 16)),
+        dim3(kMergeThreads), 0, stream, v);
+}
+
 template <int D, int R, int WG>
 cudaError_t launch_prefix_fp8(const Fp8Args& a, const CUtensorMap& tk, const CUtensorMap& tv,
                               int dev, cudaStream_t stream) {
@@ -1015,11 +1502,8 @@ extern "C" int tree_attn_verify_fp8(
     if ((d == 128 ? launch_prefix_fp8_rows<128>(a, tk, tv, dev, st)
                   : launch_prefix_fp8_rows<64>(a, tk, tv, dev, st)) != cudaSuccess)
         return TREE_ATTN_ERR_CUDA;
-    // The tree pass and the merge, on one partial per CTA and unit.
-    VerifyArgs v = {};
+    TreeMergeArgs v;
     v.q = q;
-    v.block_table = block_table;
-    v.seq_lens = seq_lens;
     v.tree_k = tree_k;
     v.tree_v = tree_v;
     v.mask = mask;
@@ -1027,21 +1511,24 @@ extern "C" int tree_attn_verify_fp8(
     v.parents = parents;
     v.parents_stride = parents_stride;
     v.mask_out = mask_out;
+    v.seq_lens = seq_lens;
+    v.ws = a.ws;
     v.out = out;
     v.lse = lse;
-    v.ws = a.ws;
     v.status = status;
     v.B = B;
     v.Hq = Hq;
     v.Hkv = Hkv;
-    v.d = d;
+    v.G = a.G;
     v.T = T;
+    v.M = a.M;
+    v.RB = a.RB;
     v.P = page_size;
     v.max_pages = max_pages_per_seq;
-    v.num_pages = num_pages;
     v.n_ctas = a.n_ctas;
     v.ovh = a.ovh;
     v.scale_log2 = a.scale_log2;
-    v.copies = 1;
-    return launch_merge(v, st) == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
+    const cudaError_t e = d == 128 ? launch_tree_merge<128>(v, plan.units, sms, st)
+                                   : launch_tree_merge<64>(v, plan.units, sms, st);
+    return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }

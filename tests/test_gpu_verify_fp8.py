@@ -215,6 +215,36 @@ def test_nan_of_a_committed_row_reaches_only_its_sequence_and_head():
     assert bool(out[1, :, 2:].isnan().all()) and bool(lse[1, :, 2:].isnan().all())
 
 
+@pytest.mark.parametrize("T,G,d", [(5, 2, 64), (40, 3, 128)])
+def test_nan_and_infinity_of_a_tree_token_reach_only_rows_that_see_it(T, G, d):
+    c = cfg(2, 2 * G, 2, d, 16, T)
+    wl = make_workload(c, seq_lens=[0, 50])
+    pools, wl = quantised(wl)
+    clean, clean_l = run(wl, pools)
+    masks = [int(m) for m in ta.mask_build(wl.parents.cuda()).cpu()]
+    # a leaf's key is NaN, a leaf's value infinite in one place, another's NaN
+    leaves = [j for j in range(T) if sum((m >> j) & 1 for m in masks) == 1]
+    k_bad, v_inf, v_nan = leaves[0], leaves[-1], leaves[len(leaves) // 2]
+    tk, tv = wl.tree_k.clone(), wl.tree_v.clone()
+    tk[:, k_bad, :, 3] = float("nan")
+    tv[:, v_inf, :, 7] = -float("inf")
+    tv[:, v_nan, :, 9] = float("nan")
+    out, lse = run(dataclasses.replace(wl, tree_k=tk, tree_v=tv), pools)
+    for t in range(T):
+        if (masks[t] >> k_bad) & 1:
+            assert bool(out[:, t].isnan().all()) and bool(lse[:, t].isnan().all())
+            continue
+        assert torch.equal(lse[:, t], clean_l[:, t])
+        want = clean[:, t].clone()
+        if (masks[t] >> v_inf) & 1:
+            want[..., 7] = -math.inf
+        if (masks[t] >> v_nan) & 1:
+            want[..., 9] = math.nan
+        assert torch.equal(out[:, t].isnan(), want.isnan()), t
+        ok = ~want.isnan()
+        assert torch.equal(out[:, t][ok], want[ok]), t
+
+
 def test_bad_data_is_reported():
     c = cfg(2, 4, 2, 64, 16, 2)
     wl = make_workload(c, seq_lens=[100, 40])
