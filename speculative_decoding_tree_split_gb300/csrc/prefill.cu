@@ -45,6 +45,9 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kKeys = 128;           // keys of a block
 constexpr int kUnit = 2 * kRows;     // rows of a unit
+// Keys of a block whose probabilities are handed over before the rest (16384 tokens,
+// 32 heads: 32 keys 1457 us, 64 keys 1439 us, 96 keys 1463 us).
+constexpr int kFirstKeys = 64;
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpClean = 10;
 constexpr int kThreads = 384;        // two softmax warpgroups and one of helpers
 // Registers: 168 a thread at launch; the helpers give theirs to the softmax,
@@ -92,7 +95,7 @@ struct Shape {
     static constexpr int Q_FULL = S_FULL + 6;  // [2]
     static constexpr int ASK = S_FULL + 8;    // V of an edge block has landed: clean it
     static constexpr int CLEAN = S_FULL + 9;  // it is clean
-    static constexpr int P_HALF = S_FULL + 10;  // [2]: P of the first 64 keys
+    static constexpr int P_HALF = S_FULL + 10;  // [2]: P of the first keys
     static constexpr int UNIT_FULL = S_FULL + 12;   // [2]: a unit has been announced
     static constexpr int UNIT_EMPTY = S_FULL + 14;  // [2]: every warp has read it
     static constexpr int ANSWER = S_FULL + 16;      // the launch control has answered
@@ -287,10 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             uint32_t t = 0;  // tiles loaded so far
-            bool ok = true, asked = false;
-            uint32_t k = 0;
+            bool ok = true;
 #pragma unroll 1
-            for (; u.rb >= 0; ++k) {
+            for (uint32_t k = 0; u.rb >= 0; ++k) {
                 // One unit ahead: the answer comes in while this one is loaded.
                 if (lane == 0) {
                     ptx::fence_proxy_async_smem();  // the last answer has been read
@@ -298,7 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::try_cancel(ptx::smem_u32(&misc->answer), bar(S::ANSWER));
                 }
                 __syncwarp();
-                asked = true;
                 // A ring's worth of tiles first, then the next unit is looked up and
                 // announced, then the rest.
                 const int n2 = 2 * span_of(u).n;
@@ -332,8 +333,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __shfl_sync(kFull, ok, 0);
                     return ok;
                 };
-                if (!load(0, min(n2, S::NS)) || !wait(S::ANSWER, k)) break;
-                asked = false;
+                if (!load(0, min(n2, S::NS)) || !wait(S::ANSWER, k)) {
+                    // an answer in flight lands before the CTA exits
+                    (void)ptx::mbar_wait(bar(S::ANSWER), k & 1, ptx::kDrainLimitNs);
+                    break;
+                }
                 int index;
                 Unit nxt;
                 nxt.rb = -1;
@@ -362,14 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!load(min(n2, S::NS), n2)) break;
                 u = nxt;
             }
-            // Copies and an answer in flight land before the CTA exits, whoever has
-            // given up.
-            if (lane == 0) {
+            // Copies in flight land before the CTA exits, whoever has given up.
+            if (lane == 0)
                 for (uint32_t i = t > S::NS ? t - S::NS : 0; i < t; ++i)
                     (void)ptx::mbar_wait(bar(S::FULL + i % S::NS), (i / S::NS) & 1,
                                          ptx::kDrainLimitNs);
-                if (asked) (void)ptx::mbar_wait(bar(S::ANSWER), k & 1, ptx::kDrainLimitNs);
-            }
             __syncwarp();
         } else if (warp == kWarpMma) {
             // ================= MMA issuer (the whole warp walks, one lane issues)
@@ -396,17 +397,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            // O_x += P_x V (or O_x = P_x V), V in tile t, 64 of the keys
+            // O_x += P_x V (or O_x = P_x V), V in tile t, the first keys or the rest
             auto values = [&](int x, uint32_t t, int half, bool add) {
                 const uint32_t vst = sb + S::OFF_RING + (t % S::NS) * S::TILE;
                 if (lead) {
 #pragma unroll
-                    for (int i = 0; i < kKeys / 32; ++i) {
-                        const int k = half * (kKeys / 32) + i;
+                    for (int k = 0; k < kKeys / 16; ++k) {
+                        if ((k >= kFirstKeys / 16) != (half > 0)) continue;
                         ptx::mma_bf16_ts(tmem + S::TM_O + x * D,
                                          tmem + S::TM_S + x * kKeys + k * 8,
                                          smem_desc_sw128(vst + k * 16 * 128, S::ATOM, 1024), id_o,
-                                         (add || half > 0 || i > 0) ? 1u : 0u);
+                                         (add || k > 0) ? 1u : 0u);
                     }
                 }
                 __syncwarp();
@@ -686,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pk[(i - c) / 2] = pack_bf16(s[i], s[i + 1]);
                         }
                         ptx::tmem_st16(ts + c / 2, pk);
-                        if (c == 32) {
-                            // the tensor cores may start on these 64 keys
+                        if (c + 32 == kFirstKeys) {
+                            // the tensor cores may start on these keys
                             ptx::tmem_wait_st();
                             ptx::tc_fence_before();
                             __syncwarp();
