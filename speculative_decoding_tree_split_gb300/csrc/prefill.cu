@@ -50,9 +50,6 @@ constexpr int kUnit = 2 * kRows;     // rows of a unit
 constexpr int kFirstKeys = 64;
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpClean = 10;
 constexpr int kThreads = 384;        // two softmax warpgroups and one of helpers
-// Registers: 168 a thread at launch; the helpers give theirs to the softmax,
-// which holds a row's 128 scores.  256 * 232 + 128 * 40 = 384 * 168.
-constexpr int kSoftRegs = 232, kHelpRegs = 40;
 
 __device__ __forceinline__ void report(int32_t* status, int code) {
     if (status != nullptr) atomicCAS(status, 0, code);
@@ -69,6 +66,7 @@ struct PrefillArgs {
     int32_t* status;
     int B, N, Hq, Hkv, G;
     float scale_log2;      // > 0
+    float inv_g;           // 1 / G
     uint32_t q_sign;       // flips the queries' signs where the scale is negative
     uint32_t q_keep;       // 0 clears the queries (scale 0)
     unsigned long long wait_ns;
@@ -82,11 +80,17 @@ struct Shape {
     static constexpr int TILE = kKeys * D * 2;     // K or V of one block
     static constexpr int ATOM = kKeys * 128;
     static constexpr int NS = D == 128 ? 4 : 8;    // ring slots, K and V in turn
+    // Registers: 168 a thread at launch; the helpers give theirs to the softmax, which
+    // holds a row's 128 scores.  The split leaves neither side with spills (which
+    // cost the copies' warp 20 % of a ragged batch).
+    static constexpr int SOFT_REGS = D == 128 ? 232 : 224;
+    static constexpr int HELP_REGS = D == 128 ? 40 : 56;
+    static_assert(256 * SOFT_REGS + 128 * HELP_REGS <= kThreads * 168, "registers at launch");
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + 2 * Q_TILE;
     static constexpr int OFF_OUT = OFF_RING + NS * TILE;  // [8 warps][32 rows][64 columns]
     static constexpr int OFF_MISC = OFF_OUT + 8 * 32 * 128;
-    static constexpr int OFF_BAR = OFF_MISC + 128;
+    static constexpr int OFF_BAR = OFF_MISC + 192;
     static constexpr int FULL = 0;
     static constexpr int EMPTY = NS;
     static constexpr int S_FULL = 2 * NS;      // [2] by tile
@@ -110,9 +114,13 @@ struct Shape {
     static_assert(SMEM > 114 * 1024, "one CTA per SM keeps TMEM allocation uncontended");
 };
 
+// Row r of a sequence is token r / G, head r % G of the group (N * G < 2^31: the
+// host checks).
 struct Unit {
     int first, len;  // packed rows of the sequence
     int hk, rb;      // KV head; row block, -1: no more units
+    int tok0, rem0;  // token and head of its first row
+    int nA, nB;      // blocks of its two tiles: they end with the last row's token
 };
 
 struct Misc {
@@ -122,8 +130,14 @@ struct Misc {
     int abort;
     int dirty[4][2];    // by unit, in turn, and cleaning warp: V held something
 };
-static_assert(sizeof(Misc) <= 128, "Misc fits its slot");
+static_assert(sizeof(Misc) <= 192, "Misc fits its slot");
 constexpr int kReaders = 11;  // warps that read announced units: all but the copies'
+
+// n / G for n < 2^17: (n + 1/2) / G is at least 1 / (2 G) away from an integer, and
+// its two roundings move it by less than (n + 1/2) / G * 2^-22.
+__device__ __forceinline__ int by_group(const PrefillArgs& a, int n) {
+    return static_cast<int>((static_cast<float>(n) + 0.5f) * a.inv_g);
+}
 
 // Row blocks of sequence b (0 where its range is out of order or empty).
 __device__ __forceinline__ int row_blocks(const PrefillArgs& a, int b) {
@@ -143,7 +157,7 @@ __device__ Unit find_unit(const PrefillArgs& a, int lane, int index) {
     Unit u;
     u.hk = index % a.Hkv;
     u.rb = -1;
-    u.first = u.len = 0;
+    u.first = u.len = u.tok0 = u.rem0 = u.nA = u.nB = 0;
     const int n0 = row_blocks(a, lane);  // the first 32 sequences stay here
     auto count = [&](int r) -> int {
         int n = max(0, n0 - r);
@@ -173,6 +187,14 @@ __device__ Unit find_unit(const PrefillArgs& a, int lane, int index) {
             const int at = __fns(m, 0, rest + 1);
             u.first = a.cu[b + at];
             u.len = a.cu[b + at + 1] - u.first;
+            const int left = u.len * a.G - u.rb * kUnit;  // rows from the first on
+            u.tok0 = u.rb * kUnit / a.G;
+            u.rem0 = u.rb * kUnit - u.tok0 * a.G;
+            auto blocks = [&](int n) -> int {  // for the first n rows
+                return (u.tok0 + by_group(a, u.rem0 + min(n, left) - 1)) / kKeys + 1;
+            };
+            u.nA = blocks(kRows);
+            u.nB = left > kRows ? blocks(kUnit) : 0;
             return u;
         }
         rest -= c;
@@ -247,22 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.N)
                 report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
 
-    // Rows of a unit: row r of the sequence is token r / G, head r % G of the
-    // group (N * G < 2^31: the host checks).  Tile x holds rows [row0 + 128 x, ...);
-    // its blocks end with its last row's token.  Blocks from `edge` on hold keys
-    // that some row of the unit does not see.
+    // Blocks from `edge` on hold keys that some row of the unit does not see.
     struct Span {
-        int rows, row0, nA, nB, n, edge;
+        int nA, nB, n, edge;
     };
     auto span_of = [&](const Unit& u) -> Span {
-        Span s;
-        s.rows = u.len * a.G;
-        s.row0 = u.rb * kUnit;
-        s.nA = (min(s.row0 + kRows, s.rows) - 1) / a.G / kKeys + 1;
-        s.nB = s.row0 + kRows < s.rows ? (min(s.row0 + kUnit, s.rows) - 1) / a.G / kKeys + 1 : 0;
-        s.n = max(s.nA, s.nB);
-        s.edge = (s.row0 / a.G + 1) / kKeys;
-        return s;
+        return {u.nA, u.nB, max(u.nA, u.nB), (u.tok0 + 1) / kKeys};
     };
     auto wait = [&](int i, uint32_t parity) -> bool {
         const bool all = __all_sync(kFull, ptx::mbar_wait(bar(i), parity & 1, a.wait_ns));
@@ -280,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kHelpRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::HELP_REGS));
         if (warp == kWarpTma) {
             // ================= units and copies: K0, V0, K1, V1, ... of each
             Unit u = find_unit(a, lane, blockIdx.x);
@@ -353,12 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (nxt.rb >= 0) {
                     // its queries on their way to L2
-                    const Span s = span_of(nxt);
-                    const int r1 = min(s.row0 + kUnit, s.rows);
-                    for (int row = s.row0 + lane; row < r1; row += 32) {
+                    const int rows = min(kUnit, nxt.len * a.G - nxt.rb * kUnit);
+                    for (int r = lane; r < rows; r += 32) {
+                        const int t = by_group(a, nxt.rem0 + r);
+                        const int h = nxt.rem0 + r - t * a.G;
                         const uint16_t* p =
-                            a.q + static_cast<long long>(nxt.first + row / a.G) * a.q_ts +
-                            static_cast<long long>(nxt.hk * a.G + row % a.G) * a.q_hs;
+                            a.q + static_cast<long long>(nxt.first + nxt.tok0 + t) * a.q_ts +
+                            static_cast<long long>(nxt.hk * a.G + h) * a.q_hs;
                         ptx::prefetch_l2(p);
                         if (D == 128) ptx::prefetch_l2(p + 64);
                     }
@@ -544,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ================= softmax and epilogue: warpgroup x takes tile x
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFT_REGS));
         const int x = warp >> 2;
         const int r = threadIdx.x & 127;  // row of the tile, TMEM lane
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -556,15 +569,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok;
         };
         auto row_of = [&](const Unit& u) -> Row {
-            const Span s = span_of(u);
             Row w;
-            w.nx = x == 0 ? s.nA : s.nB;
-            w.edge = s.edge;
-            w.edge_x = ((s.row0 + x * kRows) / a.G + 1) / kKeys;  // first block to mask
-            const int row = s.row0 + x * kRows + r;
-            w.ok = row < s.rows;
-            w.tok = w.ok ? row / a.G : 0;
-            w.head = u.hk * a.G + (w.ok ? row % a.G : 0);
+            w.nx = x == 0 ? u.nA : u.nB;
+            w.edge = (u.tok0 + 1) / kKeys;
+            const int rem = u.rem0 + x * kRows;
+            // first block to mask
+            w.edge_x = (u.tok0 + by_group(a, rem) + 1) / kKeys;
+            w.ok = u.rb * kUnit + x * kRows + r < u.len * a.G;
+            const int t = by_group(a, rem + r);
+            w.tok = w.ok ? u.tok0 + t : 0;
+            w.head = u.hk * a.G + (w.ok ? rem + r - t * a.G : 0);
             w.first = u.first;
             w.hk = u.hk;
             return w;
@@ -738,52 +752,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool dirty = (d3[0] | d3[1]) != 0;
             const long long row =
                 static_cast<long long>(end.first + end.tok) * a.Hq + end.head;
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
+            // where the row goes, from the warp's first row on (which exists); -1: nowhere
+            const long long row_0 = __shfl_sync(kFull, row, 0);
+            const int rel = end.ok ? static_cast<int>(row - row_0) : -1;
+            // 64 columns at a time through this warp's staging rows, so that a store
+            // instruction covers whole 128-byte pieces of four rows.
+#pragma unroll 1
+            for (int c = 0; c < D; c += 64) {
+                float o[64];
                 ptx::tmem_ld32(to + c, o);
+                ptx::tmem_ld32(to + c + 32, o + 32);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= inv;
-                if (dirty) {
-                    // (rare) what was cleared, for the rows that see it: a
-                    // probability times NaN or an infinity is that again
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        pk[e] = pack_bf16(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
+                    *reinterpret_cast<uint4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+                __syncwarp();
+                const int ch = lane & 7;
+                uint16_t* dst = a.out + row_0 * D + c + ch * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = 4 * i + (lane >> 3);
+                    const int to_row = __shfl_sync(kFull, rel, rr);
+                    const uint4 v = *reinterpret_cast<const uint4*>(
+                        stg + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                    if (to_row >= 0)
+                        *reinterpret_cast<uint4*>(dst + static_cast<long long>(to_row) * D) = v;
+                }
+                __syncwarp();
+            }
+            if (dirty && end.ok) {
+                // (rare) what was cleared, for the rows that see it: a probability
+                // times NaN or an infinity is that again, whatever it is added to
+#pragma unroll 1
+                for (int c = 0; c < D; ++c) {
+                    float odd = 0.f;
 #pragma unroll 1
                     for (int key = end.edge * kKeys; key <= end.tok; ++key) {
-                        const uint16_t* vr =
+                        const uint32_t b = __ldg(
                             a.v + static_cast<long long>(end.first + key) * a.v_ts +
-                            end.hk * a.v_hs + c;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const uint32_t b = __ldg(vr + i);
-                            if ((b & 0x7f80u) == 0x7f80u) o[i] += __uint_as_float(b << 16);
-                        }
+                            end.hk * a.v_hs + c);
+                        if ((b & 0x7f80u) == 0x7f80u) odd += __uint_as_float(b << 16);
                     }
-                }
-                // 64 columns at a time through this warp's staging rows, so that a
-                // store instruction covers whole 128-byte pieces of four rows.
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int ch = (c % 64) / 8 + i;
-                    *reinterpret_cast<uint4*>(stg + lane * 128 + ((ch ^ (lane & 7)) << 4)) =
-                        make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]),
-                                   pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                                   pack_bf16(o[8 * i + 4], o[8 * i + 5]),
-                                   pack_bf16(o[8 * i + 6], o[8 * i + 7]));
-                }
-                if (c % 64 == 32) {
-                    __syncwarp();
-                    const int ch = lane & 7;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = 4 * i + (lane >> 3);
-                        const long long dst = __shfl_sync(kFull, row, rr) * D + c - 32 + ch * 8;
-                        const uint4 v = *reinterpret_cast<const uint4*>(
-                            stg + rr * 128 + ((ch ^ (rr & 7)) << 4));
-                        if (__shfl_sync(kFull, end.ok, rr))
-                            *reinterpret_cast<uint4*>(a.out + dst) = v;
-                    }
-                    __syncwarp();
+                    uint16_t* at = a.out + row * D + c;
+                    if (odd != 0.f)
+                        *at = static_cast<uint16_t>(pack_bf16(
+                            __uint_as_float(static_cast<uint32_t>(*at) << 16) + odd, 0.f));
                 }
             }
             if (end.ok) a.lse[row] = (m_ref + log2f(l_sum)) * kLn2;
@@ -885,6 +904,7 @@ extern "C" int tree_attn_prefill(const uint16_t* q, const uint16_t* k, const uin
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.G = Hq / Hkv;
+    a.inv_g = 1.f / static_cast<float>(a.G);
     // The kernel looks for the largest raw score, so a negative scale turns the
     // queries round instead, and a scale of zero clears them.
     a.q_sign = softmax_scale < 0.f ? 0x80008000u : 0u;
