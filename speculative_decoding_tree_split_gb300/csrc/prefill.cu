@@ -60,6 +60,7 @@ struct PrefillArgs {
     const uint16_t* v;
     long long q_ts, q_hs, v_ts, v_hs;  // token and head strides (elements)
     int k_heads, v_heads;  // 0: one head stands for all (stride 0)
+    int q_tiles, o_tiles;  // queries (results) move as boxes of the tensor maps
     const int32_t* cu;
     uint16_t* out;
     float* lse;
@@ -81,10 +82,9 @@ struct Shape {
     static constexpr int ATOM = kKeys * 128;
     static constexpr int NS = D == 128 ? 4 : 8;    // ring slots, K and V in turn
     // Registers: 168 a thread at launch; the helpers give theirs to the softmax, which
-    // holds a row's 128 scores.  The split leaves neither side with spills (which
-    // cost the copies' warp 20 % of a ragged batch).
-    static constexpr int SOFT_REGS = D == 128 ? 232 : 224;
-    static constexpr int HELP_REGS = D == 128 ? 40 : 56;
+    // holds a row's 128 scores.  The split leaves neither side with spills (114 bytes
+    // in the copies' warp cost a ragged batch 20 %).
+    static constexpr int SOFT_REGS = 232, HELP_REGS = 40;
     static_assert(256 * SOFT_REGS + 128 * HELP_REGS <= kThreads * 168, "registers at launch");
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + 2 * Q_TILE;
@@ -104,7 +104,8 @@ struct Shape {
     static constexpr int UNIT_EMPTY = S_FULL + 14;  // [2]: every warp has read it
     static constexpr int ANSWER = S_FULL + 16;      // the launch control has answered
     static constexpr int DRAIN = S_FULL + 17;
-    static constexpr int NBAR = S_FULL + 18;
+    static constexpr int Q_FREE = S_FULL + 18;  // [2]: a unit's last scores have been made
+    static constexpr int NBAR = S_FULL + 20;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
     // TMEM: S of both tiles (P over them), then O of both.
     static constexpr int TM_S = 0;
@@ -128,6 +129,7 @@ struct Misc {
     Unit unit[2];       // announced units, in turn
     uint32_t tmem_base;
     int abort;
+    uint32_t q_loads;   // query tiles that the copies' warp has loaded
     int dirty[4][2];    // by unit, in turn, and cleaning warp: V held something
 };
 static_assert(sizeof(Misc) <= 192, "Misc fits its slot");
@@ -211,7 +213,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a) {
+                   const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_o, const PrefillArgs a) {
     using S = Shape<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_u32(smem_raw);
@@ -234,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar(S::P_FULL + i), 4);
             ptx::mbar_init(bar(S::P_HALF + i), 4);
             ptx::mbar_init(bar(S::O_FULL + i), 1);
-            ptx::mbar_init(bar(S::Q_FULL + i), 4);
+            ptx::mbar_init(bar(S::Q_FULL + i), a.q_tiles ? 1 : 4);
+            ptx::mbar_init(bar(S::Q_FREE + i), 1);
         }
         ptx::mbar_init(bar(S::ASK), 1);
         ptx::mbar_init(bar(S::CLEAN), 2);
@@ -245,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(bar(S::ANSWER), 1);
         ptx::mbar_init(bar(S::DRAIN), 1);
         misc->abort = 0;
+        misc->q_loads = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tm_k);
         ptx::prefetch_tmap(&tm_v);
@@ -345,7 +351,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __shfl_sync(kFull, ok, 0);
                     return ok;
                 };
-                if (!load(0, min(n2, S::NS)) || !wait(S::ANSWER, k)) {
+                // Queries as boxes, once the unit before has made its last scores: of the
+                // tiles that the ring has room for by then, the last two are behind them.
+                auto queries = [&]() -> bool {
+                    if (lane == 0 && a.q_tiles) {
+#pragma unroll 1
+                        for (int x = 0; x < 2; ++x) {
+                            if (k > 0 &&
+                                !ptx::mbar_wait(bar(S::Q_FREE + x), (k - 1) & 1, a.wait_ns)) {
+                                fail();
+                                ok = false;
+                                break;
+                            }
+                            const uint32_t fb = bar(S::Q_FULL + x);
+                            misc->q_loads = 2 * k + x + 1;
+                            if (x == 1 && u.nB == 0) {
+                                ptx::mbar_arrive(fb);
+                                continue;
+                            }
+                            ptx::mbar_arrive_expect_tx(fb, S::Q_TILE);
+                            const int tok = u.first + u.tok0 + x * (kRows / a.G);
+#pragma unroll
+                            for (int h = 0; h < S::DH; ++h)
+                                ptx::tma_load_3d_keep(
+                                    sb + S::OFF_Q + x * S::Q_TILE + h * S::Q_ATOM, &tm_q, h * 64,
+                                    u.hk * a.G, tok, fb);
+                        }
+                    }
+                    ok = __shfl_sync(kFull, ok, 0);
+                    return ok;
+                };
+                const int q_at = min(n2, S::NS - 2);
+                if (!load(0, q_at) || !queries() || !load(q_at, min(n2, S::NS)) ||
+                    !wait(S::ANSWER, k)) {
                     // an answer in flight lands before the CTA exits
                     (void)ptx::mbar_wait(bar(S::ANSWER), k & 1, ptx::kDrainLimitNs);
                     break;
@@ -380,10 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 u = nxt;
             }
             // Copies in flight land before the CTA exits, whoever has given up.
-            if (lane == 0)
+            if (lane == 0) {
                 for (uint32_t i = t > S::NS ? t - S::NS : 0; i < t; ++i)
                     (void)ptx::mbar_wait(bar(S::FULL + i % S::NS), (i / S::NS) & 1,
                                          ptx::kDrainLimitNs);
+                const uint32_t nq = misc->q_loads;
+                for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i)
+                    (void)ptx::mbar_wait(bar(S::Q_FULL + (i & 1)), (i >> 1) & 1,
+                                         ptx::kDrainLimitNs);
+            }
             __syncwarp();
         } else if (warp == kWarpMma) {
             // ================= MMA issuer (the whole warp walks, one lane issues)
@@ -442,6 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(S::Q_FULL + 1, k)) break;
                 ptx::tc_fence_after();
                 if (s.nB > 0) scores(1, base);
+                if (s.nA == 1) done(S::Q_FREE);
+                if (s.nB <= 1) done(S::Q_FREE + 1);
                 done(S::EMPTY + base % S::NS);
                 int j = 0;
 #pragma unroll 1
@@ -467,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             if (!slot_full(tk)) break;
                             scores(0, tk);
+                            if (j + 2 == s.nA) done(S::Q_FREE);
                         }
                     }
                     if (j < s.nB) {
@@ -484,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             if (!slot_full(tk)) break;
                             scores(1, tk);
+                            if (j + 2 == s.nB) done(S::Q_FREE + 1);
                         }
                     }
                     if (j + 1 < s.n) done(S::EMPTY + tk % S::NS);
@@ -586,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Queries of a unit into the K-major tile, this warp's 32 rows; every
         // score product of the unit before has completed.
         auto load_q = [&](const Row& w) {
+            if (a.q_tiles) return;
             if (w.nx > 0) {
                 constexpr int LPR = D / 8;  // lanes that move a row, 16 bytes each
                 uint8_t* qs = smem + S::OFF_Q + x * S::Q_TILE;
@@ -755,6 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // where the row goes, from the warp's first row on (which exists); -1: nowhere
             const long long row_0 = __shfl_sync(kFull, row, 0);
             const int rel = end.ok ? static_cast<int>(row - row_0) : -1;
+            const bool box = a.o_tiles && !dirty && __all_sync(kFull, end.ok);
             // 64 columns at a time through this warp's staging rows, so that a store
             // instruction covers whole 128-byte pieces of four rows.
 #pragma unroll 1
@@ -763,6 +812,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tmem_ld32(to + c, o);
                 ptx::tmem_ld32(to + c + 32, o + 32);
                 ptx::tmem_wait_ld();
+                if (lane == 0) ptx::bulk_wait_read();  // the staging rows' last box
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint32_t pk[4];
@@ -771,6 +822,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[e] = pack_bf16(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
                     *reinterpret_cast<uint4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
                         make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+                if (box) {
+                    // (32 rows are whole tokens, and the first row's head is the group's)
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::tma_store_3d(&tm_o, c, end.head, end.first + end.tok,
+                                          sb + S::OFF_OUT + warp * (32 * 128));
+                    continue;
                 }
                 __syncwarp();
                 const int ch = lane & 7;
@@ -808,6 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (end.ok) a.lse[row] = (m_ref + log2f(l_sum)) * kLn2;
             ptx::tc_fence_before();
         }
+        if (lane == 0) ptx::bulk_wait();
     }
 
     __syncwarp();
@@ -833,9 +894,24 @@ bool encode_rows(CUtensorMap* map, const void* base, int N, int H, int d, long l
                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The same rows in boxes of `tokens` tokens x G heads x 64 columns, in which a
+// row is token * G + head.
+bool encode_groups(CUtensorMap* map, const void* base, int N, int H, int d, long long ts,
+                   long long hs, int G, int tokens) {
+    if ((N > 1 && ts == 0) || (H > 1 && hs == 0)) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H),
+                                static_cast<cuuint64_t>(N)};
+    const cuuint64_t strides[2] = {H > 1 ? static_cast<cuuint64_t>(hs) * 2 : 16,
+                                   N > 1 ? static_cast<cuuint64_t>(ts) * 2 : 16};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 template <int D>
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
-                           long long ctas, cudaStream_t stream) {
+                           const CUtensorMap& tq, const CUtensorMap& to, long long ctas,
+                           cudaStream_t stream) {
     static std::atomic<unsigned long long> configured{0};  // by device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -848,7 +924,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tk, const CU
         configured.fetch_or(bit);
     }
     return launch_dependent(prefill_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads),
-                            Shape<D>::SMEM, stream, tk, tv, a);
+                            Shape<D>::SMEM, stream, tk, tv, tq, to, a);
 }
 
 }  // namespace
@@ -914,8 +990,17 @@ extern "C" int tree_attn_prefill(const uint16_t* q, const uint16_t* k, const uin
                        : static_cast<float>(std::fabs(static_cast<double>(softmax_scale)) *
                                             1.4426950408889634);
     a.wait_ns = wait_limit_ns();
+    // Queries and results move as whole boxes where a warp's 32 rows are whole
+    // tokens and the queries go in as they are (16 sequences of up to 2048 tokens, 8
+    // heads to a KV head: 377 us); else row by row through registers (405 us).
+    CUtensorMap tq = tk, to = tk;
+    const bool whole = 32 % a.G == 0;
+    a.q_tiles = whole && softmax_scale > 0.f &&
+                encode_groups(&tq, q, N, Hq, d, q_token_stride, q_head_stride, a.G, kRows / a.G);
+    a.o_tiles = whole && encode_groups(&to, out, N, Hq, d, static_cast<long long>(Hq) * d, d, a.G,
+                                       32 / a.G);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = d == 128 ? launch_prefill<128>(a, tk, tv, ctas, st)
-                                   : launch_prefill<64>(a, tk, tv, ctas, st);
+    const cudaError_t e = d == 128 ? launch_prefill<128>(a, tk, tv, tq, to, ctas, st)
+                                   : launch_prefill<64>(a, tk, tv, tq, to, ctas, st);
     return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA;
 }
