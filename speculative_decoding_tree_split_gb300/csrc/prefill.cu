@@ -472,6 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lead) ptx::mma_commit(bar(i));
                 __syncwarp();
             };
+            // The tensor cores' queue is short, and each question asked while it runs dry
+            // costs them time: a tile's questions are asked at once, and those that
+            // have a "no" for an answer are waited for one by one.
+            auto test = [&](int i, uint32_t parity) -> bool {
+                return ptx::mbar_test(bar(i), parity & 1);
+            };
             uint32_t base = 0, cA = 0, cB = 0, ce = 0;  // tiles, blocks of A and B, edge blocks
             Unit u;
             bool ok = true;
@@ -492,8 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (; j < s.n; ++j) {
                     const uint32_t tv = base + 2 * j + 1, tk = tv + 1;
-                    if (!slot_full(tv)) break;
+                    const int fv = S::FULL + tv % S::NS, fk = S::FULL + tk % S::NS;
+                    const uint32_t pv = tv / S::NS, pk = tk / S::NS;
                     if (j >= s.edge) {
+                        if (!wait(fv, pv)) break;
                         if (lead) ptx::mbar_arrive(bar(S::ASK));
                         __syncwarp();
                     }
@@ -501,38 +509,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                         return j < s.edge || wait(S::CLEAN, ce + (j - s.edge));
                     };
                     if (j < s.nA) {
-                        if (!wait(S::P_HALF, cA + j) || !cleaned()) break;
+                        const bool last = j + 1 >= s.nA;
+                        const bool v = test(fv, pv), h = test(S::P_HALF, cA + j);
+                        const bool f = test(S::P_FULL, cA + j), n = last || test(fk, pk);
+                        const bool first = __all_sync(kFull, v && h);
+                        const bool rest = __all_sync(kFull, f && n);
+                        if (!first && !(wait(fv, pv) && wait(S::P_HALF, cA + j))) break;
+                        if (!cleaned()) break;
                         ptx::tc_fence_after();
                         values(0, tv, 0, j > 0);
-                        if (!wait(S::P_FULL, cA + j)) break;
-                        ptx::tc_fence_after();
+                        if (!rest) {
+                            if (!wait(S::P_FULL, cA + j) || !(last || wait(fk, pk))) break;
+                            ptx::tc_fence_after();
+                        }
                         values(0, tv, 1, true);
-                        if (j + 1 >= s.nA) {
+                        if (last) {
                             done(S::O_FULL);
                         } else {
-                            if (!slot_full(tk)) break;
                             scores(0, tk);
                             if (j + 2 == s.nA) done(S::Q_FREE);
                         }
                     }
                     if (j < s.nB) {
-                        if (!wait(S::P_HALF + 1, cB + j) || (j >= s.nA && !cleaned())) break;
+                        const bool h = test(S::P_HALF + 1, cB + j);
+                        const bool f = test(S::P_FULL + 1, cB + j);
+                        const bool first = __all_sync(kFull, h);
+                        const bool rest = __all_sync(kFull, f);
+                        if (!first && !wait(S::P_HALF + 1, cB + j)) break;
+                        if (j >= s.nA && (!wait(fv, pv) || !cleaned())) break;
                         ptx::tc_fence_after();
                         values(1, tv, 0, j > 0);
-                        if (!wait(S::P_FULL + 1, cB + j)) break;
-                        ptx::tc_fence_after();
+                        if (!rest) {
+                            if (!wait(S::P_FULL + 1, cB + j)) break;
+                            ptx::tc_fence_after();
+                        }
                         values(1, tv, 1, true);
                     }
-                    done(S::EMPTY + tv % S::NS);
                     if (j < s.nB) {
                         if (j + 1 >= s.nB) {
                             done(S::O_FULL + 1);
                         } else {
-                            if (!slot_full(tk)) break;
+                            if (j + 1 >= s.nA && !wait(fk, pk)) break;
                             scores(1, tk);
                             if (j + 2 == s.nB) done(S::Q_FREE + 1);
                         }
                     }
+                    done(S::EMPTY + tv % S::NS);
                     if (j + 1 < s.n) done(S::EMPTY + tk % S::NS);
                 }
                 if (j < s.n) break;
