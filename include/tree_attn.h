@@ -610,13 +610,18 @@ TREE_ATTN_API int tree_attn_verify_fp8(
  * to and including i.  This is the pass that fills a cache before drafts are
  * verified against it.
  *   q            bf16 [N][Hq][d], k, v bf16 [N][Hkv][d]; token and head strides
- *                in elements, multiples of 8; the d values are contiguous
+ *                in elements, multiples of 8 and not negative (a head stride of 0
+ *                is one head standing for all; k and v have a token stride
+ *                other than 0 where N > 1); the d values are contiguous
  *   cu_seqlens   int32 [B+1], 0 <= ascending <= N; empty sequences are fine
  *   out          bf16 [N][Hq][d], lse fp32 [N][Hq] (natural log), dense; rows
  *                outside every sequence keep what they held
  *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN (cu_seqlens out of order
- *                or range: that sequence's rows are not written), _TIMEOUT
- * d in {64, 128}, Hq % Hkv == 0.  No workspace.  Returns 0, -1, -2, -3, -5.
+ *                or range: that sequence's rows are not written, and where
+ *                entries out of order make sound ranges overlap, theirs need
+ *                not be), _TIMEOUT
+ * d in {64, 128}, Hq % Hkv == 0, Hq <= 65535, N * (Hq / Hkv) < 2^31 - 256.  No
+ * workspace; out and lse may not overlap q, k or v.  Returns 0, -1, -2, -3, -5.
  */
 TREE_ATTN_API int tree_attn_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                     long long q_token_stride, long long q_head_stride,

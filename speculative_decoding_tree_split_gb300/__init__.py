@@ -7,6 +7,10 @@ C ABI in ``include/tree_attn.h``); this package is its thin Python binding.
     out, lse = verify(q, k_pages, v_pages, block_table, seq_lens,
                       tree_k, tree_v, mask, workspace=ws)
 
+Around verification: ``prefill`` (causal attention over packed prompts),
+``kv_append_fp8`` / ``kv_commit_fp8`` / ``kv_read_fp8`` (the 8-bit paged cache)
+and ``verify_fp8`` (verification, or with T = 1 decoding, over that cache).
+
 ``build()`` compiles the library in place with nvcc.
 """
 from ._build import build, LIB as LIB_PATH  # noqa: F401
