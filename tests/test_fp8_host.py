@@ -169,6 +169,18 @@ def test_prefill_refusals(lib):
     assert _prefill(lib, N=0, q=None) == 0
 
 
+def test_prefill_refuses_strides_it_cannot_walk(lib):
+    for i in range(6):  # negative ones, of q, k and v
+        st = [16] * 6
+        st[i] = -16
+        assert _prefill(lib, st=tuple(st)) == -2, i
+    for i in (2, 4):    # one key or value for all tokens
+        st = [16] * 6
+        st[i] = 0
+        assert _prefill(lib, st=tuple(st)) == -2, i
+    assert _prefill(lib, N=1 << 30, Hq=16, Hkv=2) == -2  # rows past 32 bits
+
+
 def test_the_binding_refuses_cpu_tensors():
     z = torch.zeros
     pools = (z(2, 1, 16, 64, dtype=torch.uint8), z(2, 1, 16, 64, dtype=torch.uint8),
