@@ -41,10 +41,15 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// The same from an fp16 pair.
-__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+// The same from two fp16 pairs: four codes.
+__device__ __forceinline__ uint32_t e4m3x4_of_f16x2(uint32_t h0, uint32_t h1) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(r)
+        : "r"(h0), "r"(h1));
     return r;
 }
 
@@ -53,6 +58,16 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t codes) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
     return r;
+}
+
+// Four codes as two fp16 pairs.
+__device__ __forceinline__ void f16x2_of_e4m3x4(uint32_t codes, uint32_t& h0, uint32_t& h1) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(h0), "=r"(h1)
+        : "r"(codes));
 }
 
 }  // namespace treeattn

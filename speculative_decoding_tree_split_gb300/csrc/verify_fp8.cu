@@ -84,7 +84,14 @@ struct Shape {
     static constexpr int N = 2 * R;                   // both halves of each row
     static constexpr int H = R / WG;                  // rows of a warpgroup
     static constexpr int WARPS = 4 * WG;              // softmax warps
-    static constexpr int THREADS = 32 * (WARPS + 2);  // and the copy and MMA warps
+    // And the copies' and MMA warps; with many rows to a thread these make a
+    // warpgroup with two idle ones, which gives its registers to the softmax.
+    // (Tiles of 128 rows: 125 -> 110 us for 4 x 32768 tokens, of 80: 88.9 -> 85.5.)
+    static constexpr bool SHIFT = H > 32;
+    static constexpr int THREADS = 32 * (WARPS + (SHIFT ? 4 : 2));
+    static constexpr int SOFT_REGS = 200, HELP_REGS = 104;
+    static_assert(!SHIFT || (WG == 2 && 256 * SOFT_REGS + 128 * HELP_REGS <= 384 * 168),
+                  "registers at launch");
     static constexpr int TILE = kKeys * D;            // K (or V) codes of a block
     static constexpr int STAGE = 2 * TILE;
     static constexpr int Q_BYTES = N * D < 1024 ? 1024 : N * D;
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         return pc.slot >= 0;
     };
 
-    if (warp == kWarpTma) {
+    auto copies = [&]() {
         // ================= this CTA's pieces and their copies: lane k < 8 takes
         // box k of a block
         const Range rg = plan_range(a, lane);
@@ -452,7 +459,8 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         const uint32_t first = jj > S::NS ? jj - S::NS : 0;
         for (uint32_t j = first; j < jj; ++j)
             (void)ptx::mbar_wait(bar(S::KV_FULL + j % S::NS), (j / S::NS) & 1, ptx::kDrainLimitNs);
-    } else if (warp == kWarpMma) {
+    };
+    auto products = [&]() {
         // ================= MMA issuer: the whole warp walks, one lane issues.
         // It polls without waiting: a suspended poll for P would hold up the
         // scores of the next block.
@@ -551,8 +559,18 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         if (lead) ptx::mma_commit(bar(S::DRAIN));
         __syncwarp();
         (void)ptx::mbar_wait(bar(S::DRAIN), 0, ptx::kDrainLimitNs);
+    };
+    if (warp >= S::WARPS) {
+        if constexpr (S::SHIFT)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::HELP_REGS));
+        if (warp == kWarpTma)
+            copies();
+        else if (warp == kWarpMma)
+            products();
     } else {
         // ================= softmax and epilogue
+        if constexpr (S::SHIFT)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFT_REGS));
         constexpr int H = S::H;     // this warpgroup's rows
         const int wg = warp >> 2;
         const int quad = warp & 3;  // the TMEM lanes this warp reaches
@@ -723,11 +741,17 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             auto probabilities = [&](uint32_t q, bool valid, float F, float vs) -> bool {
                 const uint64_t F2 = ptx::f2_pack(F, F), vs2 = ptx::f2_pack(vs, vs);
                 const uint32_t prow = sb + S::OFF_P + (q & 1) * S::P_BYTES;
+                // 16-byte chunk of the key's row for rows i .. i + 7
+                auto p_at = [&](int i) -> uint32_t {
+                    const int c = wg * (H / 8) + i / 8;
+                    return prow + (c * 16 / S::PW) * S::P_ATOM +
+                           tile_offset<S::PW>(key, c % (S::PW / 16));
+                };
                 load_scores<H>(lanes + S::TM_S + (q & 1) * R + row0, x);
                 __half2 top = __float2half2_rn(0.f);
 #pragma unroll
                 for (int i = 0; i < H; i += 8) {
-                    uint32_t hi[4], lo[4];
+                    uint32_t ph[4], hi[2], lo[2];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const int k = i + 2 * u;
@@ -738,24 +762,37 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                                        e0, e1);
                         x[k] = ptx::ex2(e0);
                         x[k + 1] = ptx::ex2(e1);
-                        const __half2 ph = __floats2half2_rn(x[k], x[k + 1]);
-                        top = __hmax2(top, ph);
-                        hi[u] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&ph));
-                        const uint32_t back = f16x2_of_e4m3x2(hi[u]);
-                        const __half2 rest =
-                            __hfma2(*reinterpret_cast<const __half2*>(&back),
-                                    __float2half2_rn(-16.f), __hmul2(ph, __float2half2_rn(16.f)));
-                        lo[u] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&rest));
+                        const __half2 h = __floats2half2_rn(x[k], x[k + 1]);
+                        top = __hmax2(top, h);
+                        ph[u] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-                    const int c = wg * (H / 8) + i / 8;  // 16-byte chunk of the key's row
-                    const uint32_t at = prow + (c * 16 / S::PW) * S::P_ATOM +
-                                        tile_offset<S::PW>(key, c % (S::PW / 16));
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                                 "r"(valid ? hi[0] | (hi[1] << 16) : 0u),
-                                 "r"(valid ? hi[2] | (hi[3] << 16) : 0u),
-                                 "r"(valid ? lo[0] | (lo[1] << 16) : 0u),
-                                 "r"(valid ? lo[2] | (lo[3] << 16) : 0u)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        hi[u] = e4m3x4_of_f16x2(ph[2 * u], ph[2 * u + 1]);
+                        uint32_t back[2], rest[2];
+                        f16x2_of_e4m3x4(hi[u], back[0], back[1]);
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const __half2 v =
+                                __hfma2(*reinterpret_cast<const __half2*>(&back[w]),
+                                        __float2half2_rn(-16.f),
+                                        __hmul2(*reinterpret_cast<const __half2*>(&ph[2 * u + w]),
+                                                __float2half2_rn(16.f)));
+                            rest[w] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        lo[u] = e4m3x4_of_f16x2(rest[0], rest[1]);
+                    }
+                    const uint32_t at = p_at(i);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]),
+                                 "r"(hi[1]), "r"(lo[0]), "r"(lo[1])
                                  : "memory");
+                }
+                if (!valid) {
+#pragma unroll
+                    for (int i = 0; i < H; i += 8)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(p_at(i)),
+                                     "r"(0)
+                                     : "memory");
                 }
                 const float2 m = __half22float2(top);
                 return valid && fmaxf(m.x, m.y) > 256.f;
@@ -1413,7 +1450,10 @@ cudaError_t launch_prefix_fp8(const Fp8Args& a, const CUtensorMap& tk, const CUt
 }
 
 // The smallest tile that holds a unit's rows: every lane of the softmax works
-// on each of them, so idle rows cost as much as used ones.
+// on each of them, so idle rows cost as much as used ones.  8 x 16384 tokens, 8 KV
+// heads, d = 128: 16 rows 48 us, 32: 52, 48: 59, 64: 71, 80: 79, 128: 107.  Other
+// numbers of warpgroups: two for 48 rows 60 us, two for 64 rows 75, four for 32 rows
+// 53; five for 80 rows 3 % slower.
 template <int D>
 cudaError_t launch_prefix_fp8_rows(const Fp8Args& a, const CUtensorMap& tk,
                                    const CUtensorMap& tv, int dev, cudaStream_t stream) {
