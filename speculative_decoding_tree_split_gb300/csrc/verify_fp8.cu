@@ -21,9 +21,8 @@
 //   O sums p v, and the row's sum takes p 2^-(scale of v_j).
 // * A row's maximum would need the 128 lanes to meet; instead each block only
 //   asks whether any e exceeds its row's reference by more than 8 (p must stay
-//   below 448), and goes on while the warps' answers come in.  If one does, the
-//   references move and O is rescaled (the first block of a segment always
-//   does that).
+//   below 448): each warpgroup asks for its own rows.  If one does, its references
+//   move and O is rescaled (the first block of a segment always does that).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -86,10 +85,12 @@ struct Shape {
     static constexpr int WARPS = 4 * WG;              // softmax warps
     // And the copies' and MMA warps; with many rows to a thread these make a
     // warpgroup with two idle ones, which gives its registers to the softmax.
-    // (Tiles of 128 rows: 125 -> 110 us for 4 x 32768 tokens, of 80: 88.9 -> 85.5.)
+    // 4 x 32768 tokens, 128 rows: 125 us without, 110 with; 80 rows: 88.9 and 87.0.
     static constexpr bool SHIFT = H > 32;
     static constexpr int THREADS = 32 * (WARPS + (SHIFT ? 4 : 2));
-    static constexpr int SOFT_REGS = 200, HELP_REGS = 104;
+    // (80 rows: 184 registers 80.5 us, 200: 81.2, 208: 82.5; 128 rows, 8 x 16384
+    // tokens: 114, 114, 111.)
+    static constexpr int SOFT_REGS = H > 48 ? 208 : 184, HELP_REGS = H > 48 ? 88 : 136;
     static_assert(!SHIFT || (WG == 2 && 256 * SOFT_REGS + 128 * HELP_REGS <= 384 * 168),
                   "registers at launch");
     static constexpr int TILE = kKeys * D;            // K (or V) codes of a block
@@ -121,12 +122,13 @@ struct Shape {
     static constexpr int O_FULL = S_FULL + 8;
     static constexpr int O_FREE = S_FULL + 9;
     static constexpr int Q_FULL = S_FULL + 10;
-    static constexpr int CHECK = S_FULL + 11;  // the softmax warps' vote on each block
-    static constexpr int MEET = S_FULL + 12;   // the softmax warps meet
-    static constexpr int SEG_FULL = S_FULL + 13;   // [2]: a segment has been announced
-    static constexpr int SEG_EMPTY = S_FULL + 15;  // [2]: every reader has it
-    static constexpr int DRAIN = S_FULL + 17;
-    static constexpr int NBAR = S_FULL + 18;
+    static constexpr int MEET = S_FULL + 11;   // the softmax warps meet
+    static constexpr int SEG_FULL = S_FULL + 12;   // [2]: a segment has been announced
+    static constexpr int SEG_EMPTY = S_FULL + 14;  // [2]: every reader has it
+    static constexpr int DRAIN = S_FULL + 16;
+    static constexpr int CHECK = S_FULL + 17;       // [WG]: a warpgroup's vote on a block
+    static constexpr int MEET_WG = CHECK + WG;      // [WG]: a warpgroup meets
+    static constexpr int NBAR = MEET_WG + WG;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
     // TMEM columns: S in two buffers, then O.
     static constexpr int NB = 2;
@@ -311,7 +313,10 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         ptx::mbar_init(bar(S::O_FULL), 1);
         ptx::mbar_init(bar(S::O_FREE), S::WARPS);
         ptx::mbar_init(bar(S::Q_FULL), S::WARPS);
-        ptx::mbar_init(bar(S::CHECK), S::WARPS);
+        for (int i = 0; i < WG; ++i) {
+            ptx::mbar_init(bar(S::CHECK + i), 4);
+            ptx::mbar_init(bar(S::MEET_WG + i), 4);
+        }
         ptx::mbar_init(bar(S::MEET), S::WARPS);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(S::SEG_FULL + i), 1);
@@ -596,6 +601,15 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             return wait_all(bar(S::MEET), parity);
         };
 
+        uint32_t met_wg = 0;
+        auto meet_wg = [&]() -> bool {  // the same of a warpgroup, whose rows are its own
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(S::MEET_WG + wg));
+            const uint32_t parity = met_wg & 1;
+            ++met_wg;
+            return wait_all(bar(S::MEET_WG + wg), parity);
+        };
+
         uint32_t jj = 0, kk = 0;
         uint32_t stage = 0, phase = 0;  // jj % NS, (jj / NS) & 1
         bool ok = true;
@@ -685,16 +699,16 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             // the limit (all rows' in a first block), and rescales l and O.
             auto move_refs = [&](uint32_t q, bool first, bool valid, float F, float vs) -> bool {
                 load_scores<H>(lanes + S::TM_S + (q & 1) * R + row0, x);
-                // largest e of every row, by warp, then by tile (fmaxf passes over NaN)
+                // largest e of every row, by warp, then by warpgroup (fmaxf passes over NaN)
 #pragma unroll
                 for (int i = 0; i < H; ++i) x[i] = valid ? fmaf(x[i], F, vs) : kNegInf;
                 reduce_columns<H>(x, lane, [](float u, float v) { return fmaxf(u, v); });
 #pragma unroll
                 for (int i = 0; i < (H + 31) / 32; ++i)
                     if (i * 32 + lane < H) wmax[quad * R + row0 + i * 32 + lane] = x[i];
-                if (!meet()) return false;
-                const int r = threadIdx.x;
-                if (r < R) {
+                if (!meet_wg()) return false;
+                const int r = row0 + (threadIdx.x & 127);
+                if (r < row0 + H) {
                     const float top = fmaxf(fmaxf(wmax[r], wmax[R + r]),
                                             fmaxf(wmax[2 * R + r], wmax[3 * R + r]));
                     // (a first block of NaN scores has no largest: any finite reference)
@@ -703,7 +717,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                     nref[r] = -now;
                     alpha[r] = ptx::ex2(old - now);
                 }
-                if (!meet()) return false;
+                if (!meet_wg()) return false;
                 if (first) return true;
                 // O holds the blocks before once P.V of the last has completed.
                 if (!wait_all(bar(S::P_FREE + ((q - 1) & 1)), ((q - 1) >> 1) & 1)) return false;
@@ -840,25 +854,18 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 }
                 ptx::fence_proxy_async_smem();
                 if (!first) {
-                    // P is handed over only when every warp has found its p in
+                    // P is handed over only when the warpgroup has found its rows' p in
                     // range (one vote per block but the first of each piece).
                     const bool any = __any_sync(kFull, over);
                     if (lane == 0) {
                         *reinterpret_cast<volatile uint8_t*>(&misc->vote[sbuf][warp]) = any;
-                        ptx::mbar_arrive(bar(S::CHECK));
+                        ptx::mbar_arrive(bar(S::CHECK + wg));
                     }
-                    if (!wait_all(bar(S::CHECK), (jj - kk - 1) & 1)) {
+                    if (!wait_all(bar(S::CHECK + wg), (jj - kk - 1) & 1)) {
                         ok = false;
                         break;
                     }
-                    const uint4* v4 = reinterpret_cast<const uint4*>(misc->vote[sbuf]);
-                    uint32_t votes = 0;
-#pragma unroll
-                    for (int i = 0; i < (S::WARPS + 15) / 16; ++i) {
-                        const uint4 v = v4[i];
-                        votes |= v.x | v.y | v.z | v.w;
-                    }
-                    if (votes != 0) {
+                    if (*reinterpret_cast<const uint32_t*>(&misc->vote[sbuf][4 * wg]) != 0) {
                         if (!move_refs(jj, false, valid, F, vs)) {
                             ok = false;
                             break;
@@ -1451,9 +1458,9 @@ cudaError_t launch_prefix_fp8(const Fp8Args& a, const CUtensorMap& tk, const CUt
 
 // The smallest tile that holds a unit's rows: every lane of the softmax works
 // on each of them, so idle rows cost as much as used ones.  8 x 16384 tokens, 8 KV
-// heads, d = 128: 16 rows 48 us, 32: 52, 48: 59, 64: 71, 80: 79, 128: 107.  Other
-// numbers of warpgroups: two for 48 rows 60 us, two for 64 rows 75, four for 32 rows
-// 53; five for 80 rows 3 % slower.
+// heads, d = 128: 16 rows 48 us, 32: 51, 48: 56, 64: 68, 80: 80, 128: 111.  Other
+// numbers of warpgroups, against what it was then: two for 48 rows 60 us for 59, two
+// for 64 rows 75 for 72, four for 32 rows 53 for 52; five for 80 rows 3 % slower.
 template <int D>
 cudaError_t launch_prefix_fp8_rows(const Fp8Args& a, const CUtensorMap& tk,
                                    const CUtensorMap& tv, int dev, cudaStream_t stream) {
