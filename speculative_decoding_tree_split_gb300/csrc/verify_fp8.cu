@@ -618,8 +618,8 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             const int L = cur.L;
             const int Mrb = min(kRows, a.M - cur.rb * kRows);  // query rows of the tile
             // ---- the tile's queries: a common power of two brings the largest
-            // |q| into [128, 256); each value is held as hi + lo, exactly down to
-            // 2^-2 and to 2^-10 below (2^-17 of the largest).
+            // |q| into (224, 448]; each value is held as hi + lo, exactly down to
+            // 2^-2 and to 2^-10 below (2^-17 of the largest at the most).
             float c_scale;
             {
                 constexpr int LPR = D / 8;                   // lanes per row
@@ -656,7 +656,9 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 }
 #pragma unroll
                 for (int i = 0; i < S::WARPS; ++i) m = max(m, misc->qmax[i]);
-                int kq = m == 0 ? 0 : 134 - static_cast<int>(m >> 23);
+                int kq = m == 0 ? 0
+                                : 134 - static_cast<int>(m >> 23) +
+                                      ((m & 0x7fffffu) <= 0x600000u ? 1 : 0);
                 kq = kq > 100 ? 100 : kq;
                 const float up = __int_as_float((127 + kq) << 23);
                 c_scale = a.scale_log2 * __int_as_float((127 - kq) << 23);
