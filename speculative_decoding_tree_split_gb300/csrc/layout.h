@@ -294,6 +294,23 @@ TA_HD int replicas_of(int M) { return M <= 32 ? 4 : (M <= 64 ? 2 : 1); }
 // Partial-result slot layout: m[kRows] | l[kRows] | acc[kRows][d] (fp32).
 TA_HD long long slot_floats(int d) { return 2LL * kRows + static_cast<long long>(kRows) * d; }
 
+// Tree pass and merge over the 8-bit cache: a CTA takes `rows` rows of a row
+// block (from r0 = blockIdx.y * rows on).  The grid is the same for every row
+// block of a unit, so in the last one a CTA may have no row at all.
+TA_HD int merge_groups(int M, int rows) { return ((M < kRows ? M : kRows) + rows - 1) / rows; }
+
+// Whether row r of such a CTA is one of the unit's M rows.
+TA_HD bool merge_has_row(int rb, int r0, int r, int rows, int M) {
+    return r < rows && r0 + r < kRows && rb * kRows + r0 + r < M;
+}
+
+// The row of the unit that is read for it: its own, or one that exists.
+TA_HD int merge_reads_row(int rb, int r0, int r, int rows, int M) {
+    const int first = rb * kRows + r0;
+    const int at = merge_has_row(rb, r0, r, rows, M) ? first + r : first;
+    return at < M ? at : M - 1;
+}
+
 // The kernel selector: every launch choice of a call, from the shapes alone
 // (the sequence lengths live on the device and are not read by the host).
 // Split-count heuristics pick a number of KV splits that fills the SMs from

@@ -1073,13 +1073,14 @@ __global__ void __launch_bounds__(kMergeThreads, 6) tree_merge_fp8_kernel(const 
     ptx::grid_dep_launch();
 
     auto row_at = [&](int r) -> int { return rb * kRows + r0 + r; };  // row of the unit
-    auto row_ok = [&](int r) -> bool {
-        return r < ROWS && r0 + r < kRows && row_at(r) < a.M;
-    };
-    // Element offset of row r's d values in q and out; lse has one per d.
-    auto row_offset = [&](int r) -> long long {
-        const int rr = row_at(r);
+    auto row_ok = [&](int r) -> bool { return merge_has_row(rb, r0, r, ROWS, a.M); };
+    // Element offset in q and out of the d values of row rr of the unit; lse has
+    // one per d.
+    auto row_offset = [&](int rr) -> long long {
         return ((static_cast<long long>(b) * a.T + rr / a.G) * a.Hq + hk * a.G + rr % a.G) * D;
+    };
+    auto q_row = [&](int r) -> const uint16_t* {
+        return a.q + row_offset(merge_reads_row(rb, r0, r, ROWS, a.M));
     };
     const int g = lane >> 2, t = lane & 3;  // lane of an accumulator: rows g, g + 8
 
@@ -1091,8 +1092,8 @@ __global__ void __launch_bounds__(kMergeThreads, 6) tree_merge_fp8_kernel(const 
             // A lane holds eight consecutive elements of rows g and g + 8 and of
             // token g of each 8-token tile: a dot product does not mind which of
             // the 16 places of a step an element takes.
-            const uint16_t* q0 = a.q + row_offset(row_ok(g) ? g : 0) + t * 8;
-            const uint16_t* q1 = a.q + row_offset(row_ok(g + 8) ? g + 8 : 0) + t * 8;
+            const uint16_t* q0 = q_row(g) + t * 8;
+            const uint16_t* q1 = q_row(g + 8) + t * 8;
             auto token = [&](int j) -> const uint16_t* {
                 return a.tree_k +
                        ((static_cast<long long>(b) * a.T + min(j, a.T - 1)) * a.Hkv + hk) * D +
@@ -1411,7 +1412,7 @@ __global__ void __launch_bounds__(kMergeThreads, 6) tree_merge_fp8_kernel(const 
         if (!live[i]) continue;
         const bool none = top == kNegInf;  // no key at all
         const float inv = none ? 0.f : 1.f / sum;
-        const long long to = row_offset(r);
+        const long long to = row_offset(row_at(r));
         uint32_t word[E / 2];
 #pragma unroll
         for (int e = 0; e < E; e += 2)
@@ -1429,15 +1430,14 @@ __global__ void __launch_bounds__(kMergeThreads, 6) tree_merge_fp8_kernel(const 
 // the tree's scores are then made for fewer CTAs.
 template <int D>
 cudaError_t launch_tree_merge(const TreeMergeArgs& v, int units, int sms, cudaStream_t stream) {
-    const int rows = v.M < kRows ? v.M : kRows;
-    const unsigned fours = static_cast<unsigned>((rows + 3) / 4);
+    const unsigned fours = static_cast<unsigned>(merge_groups(v.M, 4));
     if (static_cast<long long>(units) * fours <= 6LL * sms)
         return launch_dependent(tree_merge_fp8_kernel<D, 1>,
                                 dim3(static_cast<unsigned>(units), fours), dim3(kMergeThreads), 0,
                                 stream, v);
     return launch_dependent(
         tree_merge_fp8_kernel<D, 4>,
-        dim3(static_cast<unsigned>(units), static_cast<unsigned>((rows + 15) / 16)),
+        dim3(static_cast<unsigned>(units), static_cast<unsigned>(merge_groups(v.M, 16))),
         dim3(kMergeThreads), 0, stream, v);
 }
 
