@@ -41,18 +41,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// The same from two fp16 pairs: four codes.
-__device__ __forceinline__ uint32_t e4m3x4_of_f16x2(uint32_t h0, uint32_t h1) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 a, b;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
-        "mov.b32 %0, {a, b};\n\t}"
-        : "=r"(r)
-        : "r"(h0), "r"(h1));
-    return r;
-}
-
 // Two e4m3 codes as fp16 pairs (exact): the low code in the low half.
 __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t codes) {
     uint32_t r;

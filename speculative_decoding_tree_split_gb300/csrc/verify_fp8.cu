@@ -5,24 +5,31 @@
 // Prefix pass.  For a unit (sequence, KV head) with R query rows (tree nodes x grouped heads)
 // and keys j held as codes with scales:
 //   x_rj = c F_j <q_r, k_j>,  F_j = 2^(scale of k_j),  c = softmax scale log2(e)
-//   out_r = sum_j 2^x_rj 2^(scale of v_j) v_j / sum_j 2^x_rj.
-// The 8-bit codes go to the tensor cores as they are, so the other operand has
-// to be 8 bits as well, and both products are turned round to make that cheap:
+//   out_r = sum_j 2^x_rj v_j / sum_j 2^x_rj.
+// Both products are turned round:
 //   S^T = K Q^T     (128 keys x rows; A = K tile, B = Q)
 //   O^T += V^T P^T  (d x rows;        A = V tile, B = P)
-// * A query row and a row of probabilities enter as two e4m3 rows each, the
-//   rounded value (hi) and what is left of it (lo): together nine significant
-//   bits, as much as bf16 has.  Scores sum both halves in one accumulator; the
-//   lo half of the probabilities is held sixteenfold, for four more binades,
-//   and has columns of its own.
+// * The key codes go to the tensor cores as they are, so the queries have to be
+//   8 bits as well: a query row enters as two e4m3 rows, the rounded value (hi)
+//   and what is left of it (lo), summed in one accumulator.
+// * A probability may be any fraction of its row's largest, and thousands of
+//   small ones may make up half of the row (8-bit halves, with a step of 2^-13 of
+//   the reference, lost up to 30 % of such a result).  So P is fp16, and warps of
+//   their own widen a block's value codes to fp16, which is exact.
 // * A TMEM lane is a key, so a key's scales are scalars of the thread that
 //   holds it, and the softmax has no idle lanes however few rows there are.
 // * The value scale joins the exponent: e = x + scale of v_j, p = 2^(e - ref),
-//   O sums p v, and the row's sum takes p 2^-(scale of v_j).
+//   O sums p v, and the row's sum takes p 2^-(scale of v_j) in fp32.
 // * A row's maximum would need the 128 lanes to meet; instead each block only
-//   asks whether any e exceeds its row's reference by more than 8 (p must stay
-//   below 448): each warpgroup asks for its own rows.  If one does, its references
+//   asks whether any e exceeds its row's reference by more than 15 (p must stay
+//   below 2^16): each warpgroup asks for its own rows.  If one does, its references
 //   move and O is rescaled (the first block of a segment always does that).
+// * A new reference leaves the largest p at 2^7.  fp16 rounds to 11 bits down to
+//   2^-14 and to half of 2^-24 below, and a code is at most 448, so with n keys the
+//   result is off by
+//     2^-11 sum_j p_j |v_j| / l + n 2^-31 max_j (p_j max|v_j|) / l
+//   at most: the second term, of keys whose p leaves fp16's normal range, is 2^-17
+//   of max|v| for 16384 keys and 2^-11 for a million.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,13 +54,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kKeys = 2 * kChunk;  // keys of a block
-// p = 2^(e - reference) may reach 2^kMost (e4m3 ends at 448).  When a block
-// passes that, the references of all rows whose maximum stands above 2^kNear
-// move up to it, so that rows close to their limit do not stop a later block (moving
-// only the rows past their limit: 53 % of the blocks did so with 80 rows and scores
-// of a spread of 2.3 binades, about 8 % now).  4 x 32768 tokens, 80 rows: 0: 80.0 us,
-// 1: 80.1, 2: 80.7, 3: 81.6, 4: 83.5.
-constexpr float kMost = 8.f, kNear = 0.f;
+// p = 2^(e - reference) may reach 2^kMost.  When a block passes that, the references
+// of all rows whose largest p stands above 2^kFresh move up until it is that, so that
+// rows close to their limit do not stop a later block.
+constexpr float kMost = 15.f, kFresh = 7.f;
 // Work-line slots (64-token steps) that stand for a segment's fixed cost.  Measured, 64
 // sequences of up to 16384 tokens, 4 rows a head: 4: 181 us, 6: 169, 8: 167, 12: 169;
 // 4 x 32768 tokens, 80 rows: 91.3, 89.6, 89.0, 88.5 us.
@@ -80,28 +84,35 @@ struct Fp8Args {
 // split over WG softmax warpgroups.
 template <int D, int R, int WG>
 struct Shape {
-    static constexpr int N = 2 * R;                   // both halves of each row
     static constexpr int H = R / WG;                  // rows of a warpgroup
     static constexpr int WARPS = 4 * WG;              // softmax warps
-    // And the copies' and MMA warps; with many rows to a thread these make a
-    // warpgroup with two idle ones, which gives its registers to the softmax.
-    // 4 x 32768 tokens, 128 rows: 125 us without, 110 with; 80 rows: 88.9 and 87.0.
+    // And the warps for copies, MMAs and values; with many rows to a thread these
+    // make one warpgroup, which gives its registers to the softmax.
     static constexpr bool SHIFT = H > 32;
-    static constexpr int THREADS = 32 * (WARPS + (SHIFT ? 4 : 2));
-    // (80 rows: 184 registers 80.5 us, 200: 81.2, 208: 82.5; 128 rows, 8 x 16384
-    // tokens: 114, 114, 111.)
+    // Warps that widen values: 64 sequences of up to 16384 tokens, 16 rows: 4: 177 us,
+    // 8: 180; where registers are short, two (64 rows, 8 x 16384 tokens: 4, with
+    // spills: 79 us, 2: 76).
+    static constexpr int WIDEN = SHIFT || WG == 4 ? 2 : 4;
+    static constexpr int THREADS = 32 * (WARPS + 2 + WIDEN);
     static constexpr int SOFT_REGS = H > 48 ? 208 : 184, HELP_REGS = H > 48 ? 88 : 136;
     static_assert(!SHIFT || (WG == 2 && 256 * SOFT_REGS + 128 * HELP_REGS <= 384 * 168),
                   "registers at launch");
     static constexpr int TILE = kKeys * D;            // K (or V) codes of a block
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int Q_BYTES = N * D < 1024 ? 1024 : N * D;
-    static constexpr int PW = N <= 32 ? 32 : (N <= 64 ? 64 : 128);  // row bytes of a P tile
+    static constexpr int Q_BYTES = 2 * R * D;         // both halves of each row
+    static constexpr int PB = 2 * R;                  // bytes of a key's row of P
+    static constexpr int PW = PB <= 32 ? 32 : (PB <= 64 ? 64 : 128);  // row bytes of a P tile
     static constexpr int P_ATOM = kKeys * PW;
-    static constexpr int P_BYTES = (N > 128 ? 2 : 1) * P_ATOM;
+    static constexpr int P_BYTES = (PB > 128 ? 2 : 1) * P_ATOM;
+    static constexpr int V_ATOM = kKeys * 128;        // 64 columns of the fp16 values
+    static constexpr int V_BYTES = D / 64 * V_ATOM;
+    // Buffers of fp16 values: with many rows at d = 128 there is room for one, filled
+    // between the P.V products of two blocks.
+    static constexpr int NV = D == 128 && R > 64 ? 1 : 2;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + (Q_BYTES + 1023) / 1024 * 1024;
-    static constexpr int OFF_STAGE = OFF_P + 2 * P_BYTES;
+    static constexpr int OFF_V = OFF_P + 2 * P_BYTES;
+    static constexpr int OFF_STAGE = OFF_V + NV * V_BYTES;
     static constexpr int SMALL = 8 * 1024;            // scales, references, barriers
     static constexpr int FIT = (227 * 1024 - 1024 - SMALL - OFF_STAGE) / STAGE;
     static constexpr int MOST = D == 128 ? 6 : 8;
@@ -128,15 +139,16 @@ struct Shape {
     static constexpr int DRAIN = S_FULL + 16;
     static constexpr int CHECK = S_FULL + 17;       // [WG]: a warpgroup's vote on a block
     static constexpr int MEET_WG = CHECK + WG;      // [WG]: a warpgroup meets
-    static constexpr int NBAR = MEET_WG + WG;
+    static constexpr int V_FULL = MEET_WG + WG;     // [NV]: a block's values are fp16
+    static constexpr int NBAR = V_FULL + NV;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;  // + alignment slack
     // TMEM columns: S in two buffers, then O.
     static constexpr int NB = 2;
     static constexpr int TM_S = 0;
     static constexpr int TM_O = NB * R;
     static_assert(R % WG == 0 && H % 8 == 0 && R <= kRows, "rows of a tile");
-    static_assert(NB * R + N <= 512, "TMEM budget");
-    static_assert(NS >= 3 && SMEM <= 227 * 1024, "shared memory budget");
+    static_assert(NB * R + R <= 512, "TMEM budget");
+    static_assert(NS >= 2 && SMEM <= 227 * 1024, "shared memory budget");
     static_assert(SMEM > 114 * 1024, "one CTA per SM keeps TMEM allocation uncontended");
     static_assert(OFF_BAR + NBAR * 8 - OFF_SCALE <= SMALL, "small arrays fit their room");
 };
@@ -153,21 +165,22 @@ struct Misc {
     int abort;
     int pad[2];
     Piece piece[2];
-    uint8_t vote[2][32];  // by warp: an exponent left its range
+    uint8_t vote[2][32];  // by warp: a probability left its range
     uint32_t qmax[32];    // by warp: the largest |q| bits seen
 };
 static_assert(sizeof(Misc) <= 320, "Misc fits its slot");
 
-// tcgen05 instruction descriptor of kind::f8f6f4, e4m3 A and B, fp32 D.
-TA_HD uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
+// tcgen05 instruction descriptor for fp32 D and A and B of format 0: e4m3 in
+// kind::f8f6f4, fp16 in kind::f16.
+TA_HD uint32_t idesc_0_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
     return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
            ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
 // Shared-memory descriptor of a tile whose rows are W = 128, 64 or 32 bytes, with
 // the swizzle of that width (modes 2, 4, 6).  8-row groups are 8 * W bytes apart
-// (the stride dimension for K-major and MN-major alike: a row holds W elements
-// of K, or of M/N); `lbo`: bytes between W-element columns of an MN-major tile.
+// (the stride dimension for K-major and MN-major alike: a row holds W bytes of K,
+// or of M/N); `lbo`: bytes between W-byte columns of an MN-major tile.
 template <int W>
 __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lbo = 16) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
@@ -302,7 +315,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
     if (warp == kWarpTma && lane == 0) {
         for (int s = 0; s < S::NS; ++s) {
             ptx::mbar_init(bar(S::KV_FULL + s), 1);
-            ptx::mbar_init(bar(S::KV_EMPTY + s), 1);
+            ptx::mbar_init(bar(S::KV_EMPTY + s), S::WARPS + S::WIDEN);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(S::S_FULL + i), 1);
@@ -320,8 +333,9 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         ptx::mbar_init(bar(S::MEET), S::WARPS);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(S::SEG_FULL + i), 1);
-            ptx::mbar_init(bar(S::SEG_EMPTY + i), S::WARPS + 1);
+            ptx::mbar_init(bar(S::SEG_EMPTY + i), S::WARPS + 1 + S::WIDEN);
         }
+        for (int i = 0; i < S::NV; ++i) ptx::mbar_init(bar(S::V_FULL + i), S::WIDEN);
         ptx::mbar_init(bar(S::DRAIN), 1);
         misc->abort = 0;
         for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(misc->vote)[i] = 0;
@@ -347,8 +361,8 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         report(a.status, TREE_ATTN_STATUS_TIMEOUT);
     };
 
-    // Announced piece number k, for the MMA and softmax warps; false: no more, or
-    // a wait ran out.
+    // Announced piece number k, for all warps but the copies'; false: no more, or a
+    // wait ran out.
     auto next_piece = [&](uint32_t k, Piece& pc) -> bool {
         if (!__all_sync(kFull, ptx::mbar_wait(bar(S::SEG_FULL + (k & 1)), (k >> 1) & 1,
                                               a.wait_ns))) {
@@ -470,8 +484,8 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         // It polls without waiting: a suspended poll for P would hold up the
         // scores of the next block.
         const bool lead = ptx::elect_one();
-        const uint32_t id_s = idesc_e4m3_f32(kKeys, R, false, false);
-        const uint32_t id_o = idesc_e4m3_f32(D, S::N, true, true);
+        const uint32_t id_s = idesc_0_f32(kKeys, R, false, false);
+        const uint32_t id_o = idesc_0_f32(D, R, true, true);
         uint32_t jj = 0, kk = 0;
         bool ok = true;
         Piece sg;
@@ -490,23 +504,23 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                     const uint32_t j = jj + np;
                     const bool go =
                         ptx::mbar_test(bar(S::P_FULL + (j & 1)), (j >> 1) & 1) &&
+                        ptx::mbar_test(bar(S::V_FULL + j % S::NV), (j / S::NV) & 1) &&
                         (np > 0 || kk == 0 || ptx::mbar_test(bar(S::O_FREE), (kk - 1) & 1));
                     if (__all_sync(kFull, go)) {
                         ptx::tc_fence_after();
-                        const uint32_t vst =
-                            sb + S::OFF_STAGE + (j % S::NS) * S::STAGE + S::TILE;
+                        const uint32_t vst = sb + S::OFF_V + (j % S::NV) * S::V_BYTES;
                         const uint32_t pst = sb + S::OFF_P + (j & 1) * S::P_BYTES;
                         // A block of one 64-token step has nothing in its second half.
-                        const int nk = sg.chunk_end - sg.chunk_begin - 2 * np >= 2 ? 4 : 2;
+                        const int nk = sg.chunk_end - sg.chunk_begin - 2 * np >= 2 ? 8 : 4;
                         if (lead) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int k = 0; k < 8; ++k) {
                                 if (k >= nk) break;
-                                ptx::mma_f8(tmem + S::TM_O, tile_desc<D>(vst + k * 32 * D),
-                                            tile_desc<S::PW>(pst + k * 32 * S::PW, S::P_ATOM),
-                                            id_o, (np == 0 && k == 0) ? 0u : 1u);
+                                ptx::mma_f16(tmem + S::TM_O,
+                                             tile_desc<128>(vst + k * 16 * 128, S::V_ATOM),
+                                             tile_desc<S::PW>(pst + k * 16 * S::PW, S::P_ATOM),
+                                             id_o, (np == 0 && k == 0) ? 0u : 1u);
                             }
-                            ptx::mma_commit(bar(S::KV_EMPTY + j % S::NS));
                             ptx::mma_commit(bar(S::P_FREE + (j & 1)));
                         }
                         __syncwarp();
@@ -565,6 +579,68 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         __syncwarp();
         (void)ptx::mbar_wait(bar(S::DRAIN), 0, ptx::kDrainLimitNs);
     };
+    auto values = [&]() {
+        // ================= values: a lane widens the codes of a key to fp16.
+        // A key past the data gets zeros, as 0 * NaN is not 0.
+        uint32_t jj = 0, kk = 0;
+        uint32_t stage = 0, phase = 0;  // jj % NS, (jj / NS) & 1
+        bool ok = true;
+        Piece sg;
+        while (ok && next_piece(kk, sg)) {
+#pragma unroll 1
+            for (int ch = sg.chunk_begin; ch < sg.chunk_end; ch += 2, ++jj) {
+                const int rows = min(2, sg.chunk_end - ch) * kChunk;
+                const int keys = min(rows, sg.L - ch * kChunk);
+                // The codes have landed; P.V of the block before in this buffer has
+                // completed.
+                bool in = ptx::mbar_wait(bar(S::KV_FULL + stage), phase, a.wait_ns);
+                if (jj >= S::NV)
+                    in &= ptx::mbar_wait(bar(S::P_FREE + ((jj - S::NV) & 1)),
+                                         ((jj - S::NV) >> 1) & 1, a.wait_ns);
+                if (!__all_sync(kFull, in)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                const uint32_t src = sb + S::OFF_STAGE + stage * S::STAGE + S::TILE;
+                const uint32_t dst = sb + S::OFF_V + (jj % S::NV) * S::V_BYTES;
+#pragma unroll 1
+                for (int key = (warp - kWarpMma - 1) * 32 + lane; key < rows;
+                     key += S::WIDEN * 32) {
+                    uint4 v[D / 16];
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        v[c] = ptx::ld_shared_v4(src + tile_offset<D>(key, c));
+                        if (key >= keys) v[c] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t w[8];
+                        f16x2_of_e4m3x4(v[c].x, w[0], w[1]);
+                        f16x2_of_e4m3x4(v[c].y, w[2], w[3]);
+                        f16x2_of_e4m3x4(v[c].z, w[4], w[5]);
+                        f16x2_of_e4m3x4(v[c].w, w[6], w[7]);
+                        const uint32_t at = dst + (c >> 2) * S::V_ATOM;
+                        ptx::st_shared_v4(at + tile_offset<128>(key, (2 * c) & 7), w[0], w[1],
+                                          w[2], w[3]);
+                        ptx::st_shared_v4(at + tile_offset<128>(key, (2 * c + 1) & 7), w[4], w[5],
+                                          w[6], w[7]);
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(bar(S::V_FULL + jj % S::NV));
+                    ptx::mbar_arrive(bar(S::KV_EMPTY + stage));
+                }
+                if (++stage == S::NS) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            ++kk;
+        }
+    };
     if (warp >= S::WARPS) {
         if constexpr (S::SHIFT)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::HELP_REGS));
@@ -572,6 +648,8 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             copies();
         else if (warp == kWarpMma)
             products();
+        else
+            values();
     } else {
         // ================= softmax and epilogue
         if constexpr (S::SHIFT)
@@ -697,8 +775,8 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
 #pragma unroll
             for (int i = 0; i < H; ++i) l[i] = 0.f;
             float x[H];  // scores of this thread's key, then its probabilities
-            // Moves the references up to block q's largest e where that stands near
-            // the limit (all rows' in a first block), and rescales l and O.
+            // Moves the references up to 2^kFresh below block q's largest e where that
+            // stands above (all rows' in a first block), and rescales l and O.
             auto move_refs = [&](uint32_t q, bool first, bool valid, float F, float vs) -> bool {
                 load_scores<H>(lanes + S::TM_S + (q & 1) * R + row0, x);
                 // largest e of every row, by warp, then by warpgroup (fmaxf passes over NaN)
@@ -712,10 +790,11 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 const int r = row0 + (threadIdx.x & 127);
                 if (r < row0 + H) {
                     const float top = fmaxf(fmaxf(wmax[r], wmax[R + r]),
-                                            fmaxf(wmax[2 * R + r], wmax[3 * R + r]));
+                                            fmaxf(wmax[2 * R + r], wmax[3 * R + r])) -
+                                      kFresh;
                     // (a first block of NaN scores has no largest: any finite reference)
                     const float old = first ? kNegInf : -nref[r];
-                    const float now = top > old + kNear ? top : (first ? 0.f : old);
+                    const float now = top > old ? top : (first ? 0.f : old);
                     nref[r] = -now;
                     alpha[r] = ptx::ex2(old - now);
                 }
@@ -734,26 +813,23 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                         any |= al[i] != 1.f;
                     }
                     if (!any) continue;  // the same for the whole warpgroup
-                    const uint32_t to = lanes + S::TM_O + wg * 2 * H + 2 * c;
-                    float o[16];
-                    ptx::tmem_ld16(to, o);
+                    const uint32_t to = lanes + S::TM_O + row0 + c;
+                    float o[8];
+                    ptx::tmem_ld8(to, o);
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         l[c + i] *= al[i];
                         o[i] *= al[i];
-                        o[8 + i] *= al[i];
                     }
                     ptx::tmem_st8(to, o);
-                    ptx::tmem_st8(to + 8, o + 8);
                 }
                 ptx::tmem_wait_st();
                 return true;
             };
-            // Block q's probabilities p = 2^(F s + scale of v - reference), into x and,
-            // as hi and lo = 16 (p - hi), into the key's row of the P tile (eight
-            // rows' hi codes beside their lo codes, 16 bytes); a key past the data has
-            // none.  Returns whether a p has passed 2^kMost (NaN has not).
+            // Block q's probabilities p = 2^(F s + vs - reference), into x and, as fp16,
+            // into the key's row of the P tile; a key past the data has none.  Returns
+            // whether a p has passed 2^kMost (NaN has not).
             auto probabilities = [&](uint32_t q, bool valid, float F, float vs) -> bool {
                 const uint64_t F2 = ptx::f2_pack(F, F), vs2 = ptx::f2_pack(vs, vs);
                 const uint32_t prow = sb + S::OFF_P + (q & 1) * S::P_BYTES;
@@ -767,7 +843,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 __half2 top = __float2half2_rn(0.f);
 #pragma unroll
                 for (int i = 0; i < H; i += 8) {
-                    uint32_t ph[4], hi[2], lo[2];
+                    uint32_t ph[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const int k = i + 2 * u;
@@ -782,38 +858,16 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                         top = __hmax2(top, h);
                         ph[u] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        hi[u] = e4m3x4_of_f16x2(ph[2 * u], ph[2 * u + 1]);
-                        uint32_t back[2], rest[2];
-                        f16x2_of_e4m3x4(hi[u], back[0], back[1]);
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            const __half2 v =
-                                __hfma2(*reinterpret_cast<const __half2*>(&back[w]),
-                                        __float2half2_rn(-16.f),
-                                        __hmul2(*reinterpret_cast<const __half2*>(&ph[2 * u + w]),
-                                                __float2half2_rn(16.f)));
-                            rest[w] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
-                        lo[u] = e4m3x4_of_f16x2(rest[0], rest[1]);
-                    }
-                    const uint32_t at = p_at(i);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]),
-                                 "r"(hi[1]), "r"(lo[0]), "r"(lo[1])
-                                 : "memory");
+                    ptx::st_shared_v4(p_at(i), ph[0], ph[1], ph[2], ph[3]);
                 }
                 if (!valid) {
 #pragma unroll
-                    for (int i = 0; i < H; i += 8)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(p_at(i)),
-                                     "r"(0)
-                                     : "memory");
+                    for (int i = 0; i < H; i += 8) ptx::st_shared_v4(p_at(i), 0u, 0u, 0u, 0u);
                 }
                 const float2 m = __half22float2(top);
-                return valid && fmaxf(m.x, m.y) > 256.f;
+                return valid && fmaxf(m.x, m.y) > 32768.f;
             };
-            static_assert(kMost == 8.f, "the limit of p above");
+            static_assert(kMost == 15.f, "the limit of p above");
             for (int ch = cur.chunk_begin; ch < cur.chunk_end; ch += 2, ++jj) {
                 const bool first = ch == cur.chunk_begin;
                 const int nh = min(2, cur.chunk_end - ch);
@@ -839,21 +893,14 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 const int vbyte = sc[kKeys + key];
                 const float F = scale_of(sc[key]) * c_scale;
                 const float vs = static_cast<float>(vbyte - 127);
+                __syncwarp();
+                // (the score product has read the keys, this warp their scales)
+                if (lane == 0) ptx::mbar_arrive(bar(S::KV_EMPTY + stage));
                 if (first && !move_refs(jj, true, valid, F, vs)) {
                     ok = false;
                     break;
                 }
                 const bool over = probabilities(jj, valid, F, vs);
-                if (!valid && wg == 0 && key < nh * kChunk) {
-                    // 0 * NaN is not 0: the value rows past the data are cleared.
-                    const uint32_t vrow = sb + S::OFF_STAGE + stage * S::STAGE + S::TILE + key * D;
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vrow +
-                                                                                  c * 16),
-                                     "r"(0)
-                                     : "memory");
-                }
                 ptx::fence_proxy_async_smem();
                 if (!first) {
                     // P is handed over only when the warpgroup has found its rows' p in
@@ -925,14 +972,14 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             float* acc = slot + 2 * kRows + dim;
 #pragma unroll
             for (int c = 0; c < H; c += 8) {
-                float o[16];  // eight rows' hi sums, then their lo sums
-                ptx::tmem_ld16(lanes + S::TM_O + wg * 2 * H + 2 * c, o);
+                float o[8];
+                ptx::tmem_ld8(lanes + S::TM_O + row0 + c, o);
                 ptx::tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = row0 + c + i;
                     if (r < Mrb && (D == 128 || lane < 16))
-                        acc[static_cast<size_t>(r) * D] = fmaf(o[8 + i], 0.0625f, o[i]);
+                        acc[static_cast<size_t>(r) * D] = o[i];
                 }
             }
             ptx::tc_fence_before();
