@@ -122,6 +122,13 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y
                  : "memory");
 }
 
+// Packed pair of fp32 products.
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // mma_bf16 with fp16 operands: the same instruction, the descriptor names the type.
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                         uint32_t idesc, uint32_t accumulate) {

@@ -4,14 +4,16 @@
 //
 // Prefix pass.  For a unit (sequence, KV head) with R query rows (tree nodes x grouped heads)
 // and keys j held as codes with scales:
-//   x_rj = c F_j <q_r, k_j>,  F_j = 2^(scale of k_j),  c = softmax scale log2(e)
+//   x_rj = c_r F_j <2^u_r q_r, k_j>,  F_j = 2^(scale of k_j),
+//   c_r = softmax scale log2(e) 2^-u_r
 //   out_r = sum_j 2^x_rj v_j / sum_j 2^x_rj.
 // Both products are turned round:
 //   S^T = K Q^T     (128 keys x rows; A = K tile, B = Q)
 //   O^T += V^T P^T  (d x rows;        A = V tile, B = P)
 // * The key codes go to the tensor cores as they are, so the queries have to be
 //   8 bits as well: a query row enters as two e4m3 rows, the rounded value (hi)
-//   and what is left of it (lo), summed in one accumulator.
+//   and what is left of it (lo), summed in one accumulator.  Each row has a power of
+//   two 2^u of its own, so that a large query costs the other rows nothing.
 // * A probability may be any fraction of its row's largest, and thousands of
 //   small ones may make up half of the row (8-bit halves, with a step of 2^-13 of
 //   the reference, lost up to 30 % of such a result).  So P is fp16, and warps of
@@ -118,11 +120,11 @@ struct Shape {
     static constexpr int MOST = D == 128 ? 6 : 8;
     static constexpr int NS = FIT > MOST ? MOST : FIT;  // ring depth
     static constexpr int OFF_SCALE = OFF_STAGE + NS * STAGE;  // [NS][K, V][128]
-    static constexpr int OFF_REF = OFF_SCALE + NS * 2 * kKeys;  // reference of each row
-    static constexpr int OFF_ALPHA = OFF_REF + R * 4;           // its last change, as a factor
+    static constexpr int OFF_REF = OFF_SCALE + NS * 2 * kKeys;  // reference, factor of each row
+    static constexpr int OFF_ALPHA = OFF_REF + R * 8;           // its last change, as a factor
     static constexpr int OFF_WMAX = OFF_ALPHA + R * 4;          // [4][R]: maxima / sums by warp
     static constexpr int OFF_MISC = OFF_WMAX + 4 * R * 4;
-    static constexpr int OFF_BAR = OFF_MISC + 320;
+    static constexpr int OFF_BAR = OFF_MISC + 192;
     // barriers
     static constexpr int KV_FULL = 0;
     static constexpr int KV_EMPTY = NS;
@@ -166,9 +168,8 @@ struct Misc {
     int pad[2];
     Piece piece[2];
     uint8_t vote[2][32];  // by warp: a probability left its range
-    uint32_t qmax[32];    // by warp: the largest |q| bits seen
 };
-static_assert(sizeof(Misc) <= 320, "Misc fits its slot");
+static_assert(sizeof(Misc) <= 192, "Misc fits its slot");
 
 // tcgen05 instruction descriptor for fp32 D and A and B of format 0: e4m3 in
 // kind::f8f6f4, fp16 in kind::f16.
@@ -660,7 +661,14 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         const int key = quad * 32 + lane;
         const int row0 = wg * H;    // first row of the tile taken here
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        float* nref = reinterpret_cast<float*>(smem + S::OFF_REF);  // minus each row's reference
+        // By pairs of rows: minus their references, then their factors c_r.
+        float4* row_pair = reinterpret_cast<float4*>(smem + S::OFF_REF);
+        auto nref = [&](int r) -> float& {
+            return reinterpret_cast<float*>(row_pair)[(r >> 1) * 4 + (r & 1)];
+        };
+        auto factor = [&](int r) -> float& {
+            return reinterpret_cast<float*>(row_pair)[(r >> 1) * 4 + 2 + (r & 1)];
+        };
         float* alpha = reinterpret_cast<float*>(smem + S::OFF_ALPHA);
         float* wmax = reinterpret_cast<float*>(smem + S::OFF_WMAX);  // [4][R]
         auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
@@ -695,17 +703,15 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
         while (ok && next_piece(kk, cur)) {
             const int L = cur.L;
             const int Mrb = min(kRows, a.M - cur.rb * kRows);  // query rows of the tile
-            // ---- the tile's queries: a common power of two brings the largest
-            // |q| into (224, 448]; each value is held as hi + lo, exactly down to
-            // 2^-2 and to 2^-10 below (2^-17 of the largest at the most).
-            float c_scale;
+            // ---- the tile's queries: a row's power of two brings its largest |q| into
+            // (224, 448]; each value is held as hi + lo, exactly down to 2^-2 and to
+            // 2^-10 below (2^-17 of the row's largest at the most).
             {
                 constexpr int LPR = D / 8;                   // lanes per row
                 constexpr int STEP = S::WARPS * 32 / LPR;    // rows per pass
                 constexpr int NP = (R + STEP - 1) / STEP;
                 const int r0 = threadIdx.x / LPR, gl = threadIdx.x % LPR;
                 uint4 x[NP];
-                uint32_t m = 0;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     // (loads that no branch surrounds are all in flight at once)
@@ -715,37 +721,29 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                     x[i] = __ldg(reinterpret_cast<const uint4*>(
                         a.q + ((static_cast<size_t>(cur.b) * a.T + t) * a.Hq + h) * D + gl * 8));
                 }
+                uint8_t* qs = smem + S::OFF_Q;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    if (r0 + i * STEP >= Mrb) x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    const int r = r0 + i * STEP;
+                    if (r >= Mrb) x[i] = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t m = 0;
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const uint32_t lo = (wd[u] << 16) & 0x7fff0000u, hi = wd[u] & 0x7fff0000u;
                         if (lo < 0x7f800000u) m = max(m, lo);
                         if (hi < 0x7f800000u) m = max(m, hi);
                     }
-                }
-                m = __reduce_max_sync(kFull, m);
-                if (lane == 0) misc->qmax[warp] = m;
-                if (!meet()) {
-                    ok = false;
-                    break;
-                }
 #pragma unroll
-                for (int i = 0; i < S::WARPS; ++i) m = max(m, misc->qmax[i]);
-                int kq = m == 0 ? 0
-                                : 134 - static_cast<int>(m >> 23) +
-                                      ((m & 0x7fffffu) <= 0x600000u ? 1 : 0);
-                kq = kq > 100 ? 100 : kq;
-                const float up = __int_as_float((127 + kq) << 23);
-                c_scale = a.scale_log2 * __int_as_float((127 - kq) << 23);
-                uint8_t* qs = smem + S::OFF_Q;
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int r = r0 + i * STEP;
+                    for (int off = LPR / 2; off > 0; off >>= 1)
+                        m = max(m, __shfl_xor_sync(kFull, m, off));
                     if (r >= R) continue;
-                    const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    int kq = m == 0 ? 0
+                                    : 134 - static_cast<int>(m >> 23) +
+                                          ((m & 0x7fffffu) <= 0x600000u ? 1 : 0);
+                    kq = kq > 100 ? 100 : kq;
+                    const float up = __int_as_float((127 + kq) << 23);
+                    if (gl == 0) factor(r) = a.scale_log2 * __int_as_float((127 - kq) << 23);
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
@@ -769,6 +767,10 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(S::Q_FULL));
+                if (!meet()) {  // the factors, beside the first score product
+                    ok = false;
+                    break;
+                }
             }
 
             float l[H];  // the rows' sums over this thread's keys
@@ -781,7 +783,11 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 load_scores<H>(lanes + S::TM_S + (q & 1) * R + row0, x);
                 // largest e of every row, by warp, then by warpgroup (fmaxf passes over NaN)
 #pragma unroll
-                for (int i = 0; i < H; ++i) x[i] = valid ? fmaf(x[i], F, vs) : kNegInf;
+                for (int i = 0; i < H; i += 2) {
+                    const float4 rp = row_pair[(row0 + i) >> 1];
+                    x[i] = valid ? fmaf(x[i] * F, rp.z, vs) : kNegInf;
+                    x[i + 1] = valid ? fmaf(x[i + 1] * F, rp.w, vs) : kNegInf;
+                }
                 reduce_columns<H>(x, lane, [](float u, float v) { return fmaxf(u, v); });
 #pragma unroll
                 for (int i = 0; i < (H + 31) / 32; ++i)
@@ -793,9 +799,9 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                                             fmaxf(wmax[2 * R + r], wmax[3 * R + r])) -
                                       kFresh;
                     // (a first block of NaN scores has no largest: any finite reference)
-                    const float old = first ? kNegInf : -nref[r];
+                    const float old = first ? kNegInf : -nref(r);
                     const float now = top > old ? top : (first ? 0.f : old);
-                    nref[r] = -now;
+                    nref(r) = -now;
                     alpha[r] = ptx::ex2(old - now);
                 }
                 if (!meet_wg()) return false;
@@ -827,7 +833,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 ptx::tmem_wait_st();
                 return true;
             };
-            // Block q's probabilities p = 2^(F s + vs - reference), into x and, as fp16,
+            // Block q's probabilities p = 2^(c F s + vs - reference), into x and, as fp16,
             // into the key's row of the P tile; a key past the data has none.  Returns
             // whether a p has passed 2^kMost (NaN has not).
             auto probabilities = [&](uint32_t q, bool valid, float F, float vs) -> bool {
@@ -847,10 +853,11 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const int k = i + 2 * u;
-                        const float2 nr = *reinterpret_cast<const float2*>(nref + row0 + k);
+                        const float4 rp = row_pair[(row0 + k) >> 1];
                         float e0, e1;
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x[k], x[k + 1]), F2,
-                                                   ptx::f2_add(vs2, ptx::f2_pack(nr.x, nr.y))),
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_mul(ptx::f2_pack(x[k], x[k + 1]), F2),
+                                                   ptx::f2_pack(rp.z, rp.w),
+                                                   ptx::f2_add(vs2, ptx::f2_pack(rp.x, rp.y))),
                                        e0, e1);
                         x[k] = ptx::ex2(e0);
                         x[k + 1] = ptx::ex2(e1);
@@ -891,7 +898,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
                 ptx::tc_fence_after();
                 const uint8_t* sc = smem + S::OFF_SCALE + stage * 2 * kKeys;
                 const int vbyte = sc[kKeys + key];
-                const float F = scale_of(sc[key]) * c_scale;
+                const float F = scale_of(sc[key]);
                 const float vs = static_cast<float>(vbyte - 127);
                 __syncwarp();
                 // (the score product has read the keys, this warp their scales)
@@ -957,7 +964,7 @@ __global__ void __launch_bounds__((Shape<D, R, WG>::THREADS), 1)
             {
                 const int r = threadIdx.x;
                 if (r < Mrb) {
-                    slot[r] = -nref[r];
+                    slot[r] = -nref(r);
                     slot[kRows + r] = (wmax[r] + wmax[R + r]) + (wmax[2 * R + r] + wmax[3 * R + r]);
                 }
             }
