@@ -122,6 +122,16 @@ _DEVICES = _Devices()
 _WORKSPACE: dict = {}  # bytes, by sizes and device
 
 
+def _workspace_bytes(at: _Place, B: int, Hq: int, Hkv: int, d: int, T: int, P: int) -> int:
+    sizes = (B, Hq, Hkv, d, T, P, at.dev)
+    need = _WORKSPACE.get(sizes)
+    if need is None:
+        need = at.call("tree_attn_workspace_size", B, Hq, Hkv, d, T, 0, P)
+        if need > 0:  # 0: the library could not say, this time (the call itself says why)
+            _WORKSPACE[sizes] = need
+    return need
+
+
 def _pools(k_pages, v_pages, k_scales, v_scales, block_table):
     """Checks the cache's tensors; returns (device index, num_pages, Hkv, P, d)."""
     try:
@@ -340,12 +350,7 @@ def verify_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, t
     if out.shape != q.shape or tuple(lse.shape) != (B, T, Hq):
         raise ValueError("out and lse must have shapes [B][T][Hq][d] and [B][T][Hq]")
     if workspace is None:
-        sizes = (B, Hq, Hkv, d, T, P, dev)
-        need = _WORKSPACE.get(sizes)
-        if need is None:
-            need = at.call("tree_attn_workspace_size", B, Hq, Hkv, d, T, 0, P)
-            _WORKSPACE[sizes] = need
-        workspace = at.empty(max(need, 256), torch.uint8)
+        workspace = at.empty(max(_workspace_bytes(at, B, Hq, Hkv, d, T, P), 256), torch.uint8)
     else:
         _tensor(workspace, "workspace", (torch.uint8,), 1, dev)
     if softmax_scale is None:
