@@ -58,11 +58,13 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kKeys = 2 * kChunk;  // keys of a block
 // p = 2^(e - reference) may reach 2^kMost.  When a block passes that, the references
 // of all rows whose largest p stands above 2^kFresh move up until it is that, so that
-// rows close to their limit do not stop a later block.
+// rows close to their limit do not stop a later block.  kFresh 5 would leave fewer
+// blocks to be done twice (4 x 32768 tokens, 80 rows: 86 us for 89), but four times
+// the fixed error of small p.
 constexpr float kMost = 15.f, kFresh = 7.f;
 // Work-line slots (64-token steps) that stand for a segment's fixed cost.  Measured, 64
-// sequences of up to 16384 tokens, 4 rows a head: 4: 181 us, 6: 169, 8: 167, 12: 169;
-// 4 x 32768 tokens, 80 rows: 91.3, 89.6, 89.0, 88.5 us.
+// sequences of up to 16384 tokens, 4 rows a head: 4: 185 us, 6: 178.5, 8: 178.8, 12: 181;
+// 4 x 32768 tokens, 80 rows: 90.5, 89.3, 89.0, 89.4 us.
 constexpr int kOverhead = 8;
 
 __device__ __forceinline__ void report(int32_t* status, int code) {
@@ -91,11 +93,12 @@ struct Shape {
     // And the warps for copies, MMAs and values; with many rows to a thread these
     // make one warpgroup, which gives its registers to the softmax.
     static constexpr bool SHIFT = H > 32;
-    // Warps that widen values: 64 sequences of up to 16384 tokens, 16 rows: 4: 177 us,
-    // 8: 180; where registers are short, two (64 rows, 8 x 16384 tokens: 4, with
-    // spills: 79 us, 2: 76).
-    static constexpr int WIDEN = SHIFT || WG == 4 ? 2 : 4;
+    // Warps that widen values (64 sequences of up to 16384 tokens, 16 rows: 2: 176 us,
+    // 4: 179, 8: 183; one of 8192 tokens, 48 rows: 17.6, 18.1, 18.3).
+    static constexpr int WIDEN = 2;
     static constexpr int THREADS = 32 * (WARPS + 2 + WIDEN);
+    // (8 x 16384 tokens, 80 rows: 184 registers 97.8 us, 200: 98.1, 208: 98.9; 128 rows:
+    // 145, 145, 137.)
     static constexpr int SOFT_REGS = H > 48 ? 208 : 184, HELP_REGS = H > 48 ? 88 : 136;
     static_assert(!SHIFT || (WG == 2 && 256 * SOFT_REGS + 128 * HELP_REGS <= 384 * 168),
                   "registers at launch");
@@ -1514,9 +1517,10 @@ cudaError_t launch_prefix_fp8(const Fp8Args& a, const CUtensorMap& tk, const CUt
 
 // The smallest tile that holds a unit's rows: every lane of the softmax works
 // on each of them, so idle rows cost as much as used ones.  8 x 16384 tokens, 8 KV
-// heads, d = 128: 16 rows 48 us, 32: 51, 48: 56, 64: 68, 80: 80, 128: 111.  Other
-// numbers of warpgroups, against what it was then: two for 48 rows 60 us for 59, two
-// for 64 rows 75 for 72, four for 32 rows 53 for 52; five for 80 rows 3 % slower.
+// heads, d = 128: 16 rows 52 us, 32: 60, 48: 66, 64: 80, 80: 98, 128: 137.  (Other
+// numbers of warpgroups, measured with P in two 8-bit halves: two for 48 rows 60 us
+// for 59, two for 64 rows 75 for 72, four for 32 rows 53 for 52; five for 80 rows 3 %
+// slower.)
 template <int D>
 cudaError_t launch_prefix_fp8_rows(const Fp8Args& a, const CUtensorMap& tk,
                                    const CUtensorMap& tv, int dev, cudaStream_t stream) {
