@@ -592,6 +592,10 @@ TREE_ATTN_API int tree_kv_read_fp8(const uint8_t *k_pages, const uint8_t *v_page
  *                mask_out when that is not NULL.  Exactly one of mask and
  *                parents is given (both: -2, neither: -1).
  *   workspace    tree_attn_workspace_size(...) bytes, as for tree_attn_verify.
+ * A query element is held to 2^-17 of its row's largest.  Probabilities over the
+ * committed rows enter the product as fp16, the largest at 2^7 or above: beyond the
+ * relative 2^-11, a result is off by 2^-31 of the largest p_j max|v_j| per
+ * committed row at most.
  * tree_attn_set_early_prefix_loads does not apply; the wait limit does.
  * Other arguments, statuses and return codes as tree_attn_verify.
  */

@@ -15,6 +15,10 @@
 // * One thread per row: 128 scores from TMEM, maximum, exponentials, P back to
 //   TMEM over its own scores.  The reference moves only when a maximum exceeds
 //   it by 8 binades, so O is seldom rescaled.
+// * P is bf16 because V is: an MMA's operands have one type, and fp16 does not hold
+//   every V.  The row's sum takes p in fp32, so that lse has all its bits; a
+//   row whose probabilities all round the same way is then off by half a bf16 step
+//   (2^-8 of it at the most), as in the pass over the bf16 cache.
 // * Keys a row may not see get a score of -inf by index, whatever K holds.
 //   V of such keys still meets P = 0 in the tensor cores, and 0 * NaN is not 0:
 //   in blocks that some row does not see whole, two warps clear the non-finite
