@@ -60,6 +60,8 @@ extern "C" {
 #define TREE_ATTN_STATUS_TIMEOUT 4      /* an internal pipeline wait gave up           */
 #define TREE_ATTN_STATUS_BAD_PATH 5     /* accept_len outside [0, T] or a path node     */
                                         /* outside [0, T) (tree_kv_commit)              */
+#define TREE_ATTN_STATUS_NO_PAGE 6      /* no free page left (tree_kv_fork)             */
+#define TREE_ATTN_STATUS_BAD_ROW 7      /* src outside [-1, rows_in) (tree_kv_fork)     */
 
 /* Limits. */
 #define TREE_ATTN_MAX_T 64
@@ -634,6 +636,191 @@ TREE_ATTN_API int tree_attn_prefill(const uint16_t *q, const uint16_t *k, const 
                                     const int32_t *cu_seqlens, uint16_t *out, float *lse, int B,
                                     int N, int Hq, int Hkv, int d, float softmax_scale,
                                     int32_t *status, void *stream);
+
+/*
+ * The pages of a cache.  A server keeps one block table and, for every page, a
+ * count of the table entries (and whatever else of its own) that refer to it;
+ * 0 is a free page.  Tables handed to these entries hold -1 where a row has no
+ * page.  Pools are all the arrays that a page is a row of: K and V of every
+ * layer, scale bytes, block bounds (page i at pool + i * page_bytes).
+ *
+ * tree_kv_copy_pages -- page src[k] of every pool to its page dst[k].
+ *   pools        HOST array of n_pools device pointers, page_bytes (host) the
+ *                bytes of one page of each, 1 .. 2^31 (fastest where pool and
+ *                size are multiples of 16)
+ *   src, dst     int32 [n]; a pair with a -1 is skipped.  No page may be a dst
+ *                twice, or a src and a dst.
+ *   count        nullable device int32: only the first min(*count, n) pairs
+ *   status       nullable: TREE_ATTN_STATUS_BAD_PAGE (that pair is skipped).
+ * Returns 0, -1, -2, -3, -5.
+ */
+TREE_ATTN_API int tree_kv_copy_pages(void *const *pools, const size_t *page_bytes, int n_pools,
+                                     const int32_t *src, const int32_t *dst,
+                                     const int32_t *count, int n, int num_pages, int32_t *status,
+                                     void *stream);
+
+/*
+ * tree_kv_fork -- the rows of the next step from the rows of this one: beams or
+ * samples that go on from the same row, rows that end, rows that grow, new rows.
+ * Row i of the outputs continues row p = src[i] with its L = seq_lens[p] tokens
+ * (src[i] = -1: a row without tokens), mapped for L + reserve positions:
+ *   - pages of whole committed blocks are shared with p;
+ *   - a page behind them is kept by the first row that continues p, if
+ *     page_refs counts nobody else for it; other rows get pages of their own,
+ *     and the one that holds L's last tokens is copied in every pool;
+ *   - new pages are the lowest free ones, in the order of rows and positions;
+ *     pages that this call sets free are not handed out by it.
+ * page_refs_out = page_refs - (entries of block_table) + (entries of
+ * block_table_out), so rows that nobody continues give their pages back.
+ *   block_table  int32 [rows_in][max_pages_per_seq], seq_lens int32 [rows_in],
+ *   page_refs    int32 [num_pages], src int32 [rows_out]
+ *   reserve      nullable int32 [rows_out] (negative: 0); NULL: reserve_all
+ *   outputs      block_table_out [rows_out][max_pages_per_seq], seq_lens_out
+ *                [rows_out], page_refs_out [num_pages], none of them the input
+ *                of its kind (-2)
+ *   workspace    tree_kv_fork_workspace_size(...) bytes, 256-byte aligned
+ *   status       nullable: TREE_ATTN_STATUS_NO_PAGE (entries without a page are
+ *                -1; a row whose copied page is among them ends at that page:
+ *                seq_lens_out says where), _BAD_SEQ_LEN (a length, or a length
+ *                and reserve, outside the table), _BAD_PAGE, _BAD_ROW.
+ * rows_in and rows_out below 2^24, num_pages and max_pages_per_seq below 2^30.
+ * n_pools = 0 makes the tables only.  Returns 0, -1, -2, -3, -4, -5.
+ */
+TREE_ATTN_API size_t tree_kv_fork_workspace_size(int rows_in, int rows_out, int num_pages);
+
+TREE_ATTN_API int tree_kv_fork(void *const *pools, const size_t *page_bytes, int n_pools,
+                               const int32_t *block_table, int max_pages_per_seq,
+                               const int32_t *seq_lens, const int32_t *page_refs,
+                               const int32_t *src, const int32_t *reserve, int reserve_all,
+                               int32_t *block_table_out, int32_t *seq_lens_out,
+                               int32_t *page_refs_out, int rows_in, int rows_out, int page_size,
+                               int num_pages, void *workspace, size_t workspace_bytes,
+                               int32_t *status, void *stream);
+
+/*
+ * tree_kv_compact -- the used pages (page_refs > 0) moved to the front of every
+ * pool: with n of them, the k-th used page at or past n goes to the k-th free
+ * page before n, and all others stay.
+ *   block_table_out  the table with the pages' new places (may be block_table)
+ *   page_refs_out    their counts (not page_refs: -2)
+ *   n_used           int32 [1]: n; pages n .. num_pages - 1 are free
+ *   workspace        tree_kv_compact_workspace_size(...) bytes, 256-byte aligned
+ *   status           nullable: TREE_ATTN_STATUS_BAD_PAGE (an entry without a used
+ *                    page becomes -1).
+ * Sizes, n_pools = 0 and return codes as tree_kv_fork.
+ */
+TREE_ATTN_API size_t tree_kv_compact_workspace_size(int num_pages);
+
+TREE_ATTN_API int tree_kv_compact(void *const *pools, const size_t *page_bytes, int n_pools,
+                                  const int32_t *block_table, int max_pages_per_seq,
+                                  const int32_t *page_refs, int32_t *block_table_out,
+                                  int32_t *page_refs_out, int32_t *n_used, int rows,
+                                  int num_pages, void *workspace, size_t workspace_bytes,
+                                  int32_t *status, void *stream);
+
+/*
+ * tree_beam_select -- beam search's selection.  Candidate (w, v) of sequence b
+ * scores scores[b][w] + ln softmax(logits[b][w])[v]; the K highest of all beams
+ * and tokens are taken, in descending order, ties to the lowest (w, v).
+ *   logits       [B][W][V] of type `dtype` (0 bf16, 1 fp16, 2 fp32); batch and
+ *                beam strides in elements, not negative, the V logits contiguous.
+ *                NaN and -inf are no candidates, +inf is the largest number.
+ *   scores       fp32 [B][W]; a beam at -inf or NaN has no candidates
+ *   finished     nullable uint8 [B][W]: a non-zero beam's only candidate is (w,
+ *                eos) with its score unchanged (its logits are not read)
+ *   scores_out   fp32 [B][K];  rows_out int32 [B][K]: b * W + w;  tokens_out int32
+ *                [B][K].  Where there are fewer than K candidates: -inf, -1, -1.
+ *   workspace    tree_beam_workspace_size(...) bytes, 256-byte aligned
+ * 1 <= W, K <= 64, B * W <= 65535, V <= 2^30, W * K * ceil((V + 7) / 8192) <=
+ * 32768.  Scores are summed in fp64 over fp32 sums of exponentials.
+ * Returns 0, -1, -2, -3, -4, -5.
+ */
+TREE_ATTN_API size_t tree_beam_workspace_size(int B, int W, int V, int K);
+
+TREE_ATTN_API int tree_beam_select(const void *logits, int dtype, long long batch_stride,
+                                   long long beam_stride, const float *scores,
+                                   const uint8_t *finished, int eos, float *scores_out,
+                                   int32_t *rows_out, int32_t *tokens_out, int B, int W, int V,
+                                   int K, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Attention over selected pages of a long cache.  Three steps: bounds of every
+ * page's keys (written as tokens arrive), the pages whose bounds allow a query
+ * the largest scores, attention over those.
+ *
+ * Bounds of a page with n committed tokens, for each KV head: hi and lo, the
+ * largest and smallest key of every channel (NaN skipped, infinities as the
+ * largest finite bf16 number; 0 where there is nothing), held as codes
+ * ceil(hi * 2^-e) and floor(lo * 2^-e) in [-127, 127], e the smallest integer of
+ * [-100, 100] with max(|hi|, |lo|) <= 127 * 2^e; the byte is e + 127.
+ *   bounds       int8 [num_pages][Hkv][2][d] (hi, then lo)
+ *   bounds_exp   uint8 [num_pages][Hkv]
+ *
+ * tree_kv_block_bounds -- bounds of the pages that hold positions starts[b] ..
+ * seq_lens[b] - 1 of each sequence, over their committed tokens.
+ *   k_pages      the cache's keys: bf16 (k_scales NULL) or e4m3 codes with
+ *                k_scales as for the 8-bit cache
+ *   starts       nullable int32 [B] (NULL: 0): the lengths before the tokens came
+ *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN, _BAD_PAGE.
+ * A page that two sequences of the call share gets the bounds of one of them.
+ * Sizes as for the 8-bit cache; bounds and k_pages 16-byte aligned.  Returns 0,
+ * -1, -2, -3, -5.
+ */
+TREE_ATTN_API int tree_kv_block_bounds(const void *k_pages, const uint8_t *k_scales,
+                                       const int32_t *block_table, int max_pages_per_seq,
+                                       const int32_t *starts, const int32_t *seq_lens,
+                                       int8_t *bounds, uint8_t *bounds_exp, int B, int Hkv, int d,
+                                       int page_size, int num_pages, int32_t *status,
+                                       void *stream);
+
+/*
+ * tree_select_blocks -- for every query the n_select pages of highest score.
+ * The queries of a (sequence, token, KV head) group choose together: with
+ * codes c = rint(q * 2^-f) in [-127, 127], f the smallest integer of [-100, 100] with
+ * max|q| <= 127 * 2^f over the group's finite values (NaN is 0), a page scores
+ *   2^e * max over the group's heads of sum_i max(c_i * hi_i, c_i * lo_i),
+ * a whole number times a power of two, so that the choice is exact.  The first
+ * n_first and the last n_last pages of a sequence are always taken; ties go to
+ * the lowest page.
+ *   q            bf16 [B][T][Hq][d]; bounds, bounds_exp as above
+ *   blocks       int32 [B][T][Hkv][n_select]: pages of the sequence (logical),
+ *                ascending, then -1
+ *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN, _BAD_PAGE (such a page
+ *                scores nothing).
+ * 1 <= T <= 64, 1 <= n_select <= 4096, n_first, n_last >= 0 and n_first + n_last
+ * <= n_select, max_pages_per_seq <= 262144, Hq / Hkv <= 128.  Returns 0, -1, -2, -3, -5.
+ */
+TREE_ATTN_API int tree_select_blocks(const uint16_t *q, const int8_t *bounds,
+                                     const uint8_t *bounds_exp, const int32_t *block_table,
+                                     int max_pages_per_seq, const int32_t *seq_lens,
+                                     int32_t *blocks, int B, int Hq, int Hkv, int d, int T,
+                                     int page_size, int num_pages, int n_select, int n_first,
+                                     int n_last, int32_t *status, void *stream);
+
+/*
+ * tree_attn_verify_blocks -- split tree attention over selected pages: as
+ * tree_attn_verify (bf16 cache, k_scales and v_scales NULL) or
+ * tree_attn_verify_fp8, where token t of sequence b sees, through KV head h,
+ * the committed tokens of the pages blocks[b][t][h] instead of all, and the
+ * tree tokens as before.
+ *   blocks       int32 [B][T][Hkv][n_blocks] logical pages, -1 none; a page that
+ *                is listed twice counts twice
+ *   mask, mask_stride, parents, parents_stride   as tree_attn_verify_fp8
+ *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN, _BAD_PAGE (a block outside
+ *                the sequence, or a page outside the pool: it is skipped),
+ *                _BAD_PARENT.
+ * 0 <= n_blocks <= 4096.  In the 8-bit form a query element is held to 2^-38 of its row's
+ * largest or to bf16's precision, probabilities as for tree_attn_verify_fp8; with
+ * a bf16 cache they enter the product as two bf16 numbers.  No workspace.
+ * Returns 0, -1, -2, -3, -5.
+ */
+TREE_ATTN_API int tree_attn_verify_blocks(
+    const uint16_t *q, const void *k_pages, const void *v_pages, const uint8_t *k_scales,
+    const uint8_t *v_scales, const int32_t *block_table, int max_pages_per_seq,
+    const int32_t *seq_lens, const int32_t *blocks, int n_blocks, const uint16_t *tree_k,
+    const uint16_t *tree_v, const uint64_t *mask, int mask_stride, const int32_t *parents,
+    int parents_stride, uint16_t *out, float *lse, int B, int Hq, int Hkv, int d, int T,
+    int page_size, int num_pages, float softmax_scale, int32_t *status, void *stream);
 
 /* Library version, as major*10000 + minor*100 + patch. */
 TREE_ATTN_API int tree_attn_version(void);

@@ -9,7 +9,10 @@ C ABI in ``include/tree_attn.h``); this package is its thin Python binding.
 
 Around verification: ``prefill`` (causal attention over packed prompts),
 ``kv_append_fp8`` / ``kv_commit_fp8`` / ``kv_read_fp8`` (the 8-bit paged cache)
-and ``verify_fp8`` (verification, or with T = 1 decoding, over that cache).
+and ``verify_fp8`` (verification, or with T = 1 decoding, over that cache).  For
+several hypotheses and long contexts: ``beam_select``, ``kv_fork`` / ``kv_compact`` /
+``kv_copy_pages`` (the pages of either cache), and ``kv_block_bounds`` /
+``select_blocks`` / ``verify_blocks`` (attention over selected pages).
 
 ``build()`` compiles the library in place with nvcc.
 """
@@ -23,6 +26,8 @@ from ._lib import (  # noqa: F401
     STATUS_BAD_SEQ_LEN,
     STATUS_TIMEOUT,
     STATUS_BAD_PATH,
+    STATUS_NO_PAGE,
+    STATUS_BAD_ROW,
     TreeAttnError,
     load,
     mask_build,
@@ -52,4 +57,15 @@ from ._serving import (  # noqa: F401
     kv_read_fp8,
     verify_fp8,
     prefill,
+)
+from ._pages import (  # noqa: F401
+    kv_copy_pages,
+    kv_fork,
+    kv_compact,
+)
+from ._beam import beam_select  # noqa: F401
+from ._blocks import (  # noqa: F401
+    kv_block_bounds,
+    select_blocks,
+    verify_blocks,
 )

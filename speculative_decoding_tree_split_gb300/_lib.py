@@ -32,6 +32,8 @@ STATUS_BAD_PAGE = 2
 STATUS_BAD_SEQ_LEN = 3
 STATUS_TIMEOUT = 4
 STATUS_BAD_PATH = 5
+STATUS_NO_PAGE = 6
+STATUS_BAD_ROW = 7
 MAX_T = 64
 
 EXPORTED = (
@@ -61,6 +63,16 @@ EXPORTED = (
     "tree_kv_read_fp8",
     "tree_attn_verify_fp8",
     "tree_attn_prefill",
+    "tree_kv_copy_pages",
+    "tree_kv_fork_workspace_size",
+    "tree_kv_fork",
+    "tree_kv_compact_workspace_size",
+    "tree_kv_compact",
+    "tree_beam_workspace_size",
+    "tree_beam_select",
+    "tree_kv_block_bounds",
+    "tree_select_blocks",
+    "tree_attn_verify_blocks",
 )
 
 
@@ -159,6 +171,29 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tree_attn_verify_fp8.restype = i32
     lib.tree_attn_prefill.argtypes = [vp] * 3 + [i64] * 6 + [vp] * 3 + [i32] * 5 + [f32, vp, vp]
     lib.tree_attn_prefill.restype = i32
+    lib.tree_kv_copy_pages.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, vp, vp]
+    lib.tree_kv_copy_pages.restype = i32
+    lib.tree_kv_fork_workspace_size.argtypes = [i32] * 3
+    lib.tree_kv_fork_workspace_size.restype = sz
+    lib.tree_kv_fork.argtypes = ([vp, vp, i32, vp, i32] + [vp] * 4 + [i32] + [vp] * 3 + [i32] * 4
+                                 + [vp, sz, vp, vp])
+    lib.tree_kv_fork.restype = i32
+    lib.tree_kv_compact_workspace_size.argtypes = [i32]
+    lib.tree_kv_compact_workspace_size.restype = sz
+    lib.tree_kv_compact.argtypes = [vp, vp, i32, vp, i32] + [vp] * 4 + [i32, i32, vp, sz, vp, vp]
+    lib.tree_kv_compact.restype = i32
+    lib.tree_beam_workspace_size.argtypes = [i32] * 4
+    lib.tree_beam_workspace_size.restype = sz
+    lib.tree_beam_select.argtypes = ([vp, i32, i64, i64, vp, vp, i32, vp, vp, vp] + [i32] * 4
+                                     + [vp, sz, vp])
+    lib.tree_beam_select.restype = i32
+    lib.tree_kv_block_bounds.argtypes = [vp] * 3 + [i32] + [vp] * 4 + [i32] * 5 + [vp, vp]
+    lib.tree_kv_block_bounds.restype = i32
+    lib.tree_select_blocks.argtypes = [vp] * 4 + [i32] + [vp] * 2 + [i32] * 10 + [vp, vp]
+    lib.tree_select_blocks.restype = i32
+    lib.tree_attn_verify_blocks.argtypes = ([vp] * 6 + [i32, vp, vp, i32] + [vp] * 3
+                                            + [i32, vp, i32, vp, vp] + [i32] * 7 + [f32, vp, vp])
+    lib.tree_attn_verify_blocks.restype = i32
     if path == LIB_PATH:
         _lib = lib
     return lib

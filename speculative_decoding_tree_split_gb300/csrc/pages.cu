@@ -1,0 +1,711 @@
+// pages.cu -- the pages of a paged cache as managed things: copied, forked
+// (rows of the next step made from rows of this one: sharing, copy on write,
+// growth, release) and compacted.
+//
+// A page's reference count is the only state: 0 is free, and a page handed out
+// is always the lowest free one not yet handed out, in order of (row, slot), so
+// that results do not depend on timing.  Counts and tables go from inputs to
+// outputs; what this call frees is not handed out by it, so no page is read
+// and written by the copies.
+//
+// A plan is a few KB to a few MB of integers with four dependent phases: one
+// cluster of CTAs runs them with hardware barriers in between, in one launch.
+// The copies are bound by memory traffic.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/tree_attn.h"
+#include "cluster.cuh"
+#include "launch.cuh"
+#include "layout.h"
+#include "ptx.cuh"
+
+namespace treeattn {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kMaxCtas = 8;
+
+__device__ __forceinline__ void report(int32_t* status, int code) {
+    if (status != nullptr) atomicCAS(status, 0, code);
+}
+
+// ---------------------------------------------------------------------------
+// Copies: page src[k] of every pool to its page dst[k].  A warp moves 4 KB at a
+// time, eight 16-byte vectors to a lane, all loaded before the first is stored.
+// ---------------------------------------------------------------------------
+constexpr int kPoolsMost = 120;  // of one launch
+constexpr int kPiece = 4096;     // bytes a warp moves at a time
+constexpr int kCopyThreads = 256;
+
+struct CopyArgs {
+    uint8_t* pool[kPoolsMost];
+    long long bytes[kPoolsMost];  // of one page
+    int first[kPoolsMost + 1];    // first piece of each pool within a page's
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* count;  // nullable: n
+    int n, n_pools, num_pages;
+    int32_t* status;
+};
+
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    const int n = a.count != nullptr ? min(max(*a.count, 0), a.n) : a.n;
+    const int per = a.first[a.n_pools];
+    const int warps = gridDim.x * (kCopyThreads / 32);
+    const int step_k = warps / per, step_c = warps % per;
+    const int w0 = blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32;
+    int k = w0 / per, c = w0 % per;
+    while (k < n) {
+        const int s = a.src[k], d = a.dst[k];
+        if (s >= 0 && d >= 0 && s < a.num_pages && d < a.num_pages) {
+            int lo = 0, hi = a.n_pools - 1;  // the pool that piece c belongs to
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (a.first[mid] <= c)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const long long page = a.bytes[lo];
+            const long long at = static_cast<long long>(c - a.first[lo]) * kPiece;
+            const int m = static_cast<int>(min(page - at, static_cast<long long>(kPiece)));
+            const uint8_t* from = a.pool[lo] + s * page + at;
+            uint8_t* to = a.pool[lo] + d * page + at;
+            if (((page | reinterpret_cast<uintptr_t>(a.pool[lo])) & 15) == 0) {
+                uint4 v[kPiece / 512];
+#pragma unroll
+                for (int i = 0; i < kPiece / 512; ++i)
+                    if (i * 512 + lane * 16 < m) v[i] = ld_once(from + i * 512 + lane * 16);
+#pragma unroll
+                for (int i = 0; i < kPiece / 512; ++i)
+                    if (i * 512 + lane * 16 < m)
+                        *reinterpret_cast<uint4*>(to + i * 512 + lane * 16) = v[i];
+            } else {
+                for (int i = lane; i < m; i += 32) to[i] = from[i];
+            }
+        } else if (lane == 0 && (s < -1 || d < -1 || s >= a.num_pages || d >= a.num_pages)) {
+            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+        }
+        k += step_k;
+        c += step_c;
+        if (c >= per) {
+            c -= per;
+            ++k;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// What both plans use: prefix sums of one CTA, and runs over the page counts.
+// ---------------------------------------------------------------------------
+
+// Exclusive prefix of v over the CTA's threads; the sum in `total`.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, off);
+        if (lane >= off) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w) {
+        const int s = warp_sums[w];
+        before += w < warp ? s : 0;
+        all += s;
+    }
+    total = all;
+    return before + x - v;
+}
+
+// The part [lo, hi) of the pages that a CTA of the cluster looks after.
+__device__ __forceinline__ void my_pages(int num_pages, int& lo, int& hi) {
+    const long long ctas = ptx::cluster_size(), r = ptx::cluster_rank();
+    lo = static_cast<int>(num_pages * r / ctas);
+    hi = static_cast<int>(num_pages * (r + 1) / ctas);
+}
+
+// ---------------------------------------------------------------------------
+// Fork.  Row i continues row p = src[i] with its L = seq_lens[p] tokens:
+//   slots before floor(L / P)   p's pages, shared;
+//   slots up to (L + reserve)   p's own page where i is p's first row and no
+//                               other reference to that page exists, else a new
+//                               page; the one that holds tokens is copied;
+//   behind                      none.
+// counts' = counts - (entries of the old table) + (entries of the new one).
+// ---------------------------------------------------------------------------
+struct ForkArgs {
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* refs;
+    const int32_t* src;
+    const int32_t* reserve;  // nullable: reserve_all for every row
+    int reserve_all;
+    int32_t* table_out;
+    int32_t* lens_out;
+    int32_t* refs_out;
+    int rows_in, rows_out, max_pages, P, num_pages;
+    // workspace
+    int32_t* copy_src;  // [rows_out]
+    int32_t* copy_dst;  // [rows_out]
+    int32_t* count;     // [1]
+    int32_t* free_of;   // [kMaxCtas] free pages of each CTA's part
+    int32_t* children;  // [rows_in]
+    int32_t* eldest;    // [rows_in]
+    int32_t* wants;     // [rows_out] new pages, 2^30 added if one is a copy
+    int32_t* base;      // [rows_out] new pages of the rows before
+    int32_t* copies;    // [rows_out] copies of the rows before
+    int32_t* list;      // [num_pages] free pages in order
+    int32_t* status;
+};
+
+struct Row {
+    int parent;  // -1: an empty row
+    int L, full, need;
+    bool eldest;
+};
+
+__device__ __forceinline__ bool entry_ok(int e, int num_pages) { return e >= 0 && e < num_pages; }
+
+__device__ __forceinline__ Row row_of(const ForkArgs& a, int i) {
+    Row r;
+    r.parent = a.src[i];
+    if (r.parent < 0 || r.parent >= a.rows_in) {
+        if (r.parent != -1) report(a.status, TREE_ATTN_STATUS_BAD_ROW);
+        r.parent = -1;
+        r.L = r.full = r.need = 0;
+        r.eldest = false;
+        return r;
+    }
+    bool bad;
+    r.L = clamp_seq_len(a.lens[r.parent], a.P, a.max_pages, bad);
+    if (bad) {
+        report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
+        r.L = 0;
+    }
+    const int more = a.reserve != nullptr ? a.reserve[i] : a.reserve_all;
+    const long long end = static_cast<long long>(r.L) + max(more, 0);
+    const long long need = (end + a.P - 1) / a.P;
+    if (need > a.max_pages) report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
+    r.full = r.L / a.P;
+    r.need = static_cast<int>(min(need, static_cast<long long>(a.max_pages)));
+    r.eldest = __ldcg(a.eldest + r.parent) == i;
+    return r;
+}
+
+// Whether row r keeps its parent's entry e behind the full pages.
+__device__ __forceinline__ bool keeps(const ForkArgs& a, const Row& r, int e) {
+    return r.eldest && entry_ok(e, a.num_pages) && a.refs[e] == 1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    __shared__ int sums[kPlanWarps];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int ctas = static_cast<int>(ptx::cluster_size());
+    const int rank = static_cast<int>(ptx::cluster_rank());
+    const int gtid = rank * kPlanThreads + tid, gthreads = ctas * kPlanThreads;
+    const int gwarp = gtid >> 5, gwarps = gthreads >> 5;
+    int lo, hi;
+    my_pages(a.num_pages, lo, hi);
+
+    // Counts carried over, free pages counted, rows' children reset.
+    int mine = 0;
+    for (int p = lo + tid; p < hi; p += kPlanThreads) {
+        const int c = a.refs[p];
+        a.refs_out[p] = c;
+        mine += c == 0;
+    }
+    int free_here;
+    block_scan(mine, sums, free_here);
+    if (tid == 0) a.free_of[rank] = free_here;
+    for (int p = gtid; p < a.rows_in; p += gthreads) {
+        a.children[p] = 0;
+        a.eldest[p] = 0x7fffffff;
+    }
+    ptx::cluster_sync();
+
+    for (int i = gtid; i < a.rows_out; i += gthreads) {
+        const int p = a.src[i];
+        if (p >= 0 && p < a.rows_in) {
+            atomicAdd(a.children + p, 1);
+            atomicMin(a.eldest + p, i);
+        }
+    }
+    ptx::cluster_sync();
+
+    // New pages that each row wants.
+    for (int i = gwarp; i < a.rows_out; i += gwarps) {
+        const Row r = row_of(a, i);
+        int n = 0;
+        bool copy = false;
+        for (int s0 = r.full; s0 < r.need; s0 += 32) {
+            const int s = s0 + lane;
+            bool fresh = false;
+            if (s < r.need) {
+                const int e = a.table[static_cast<size_t>(r.parent) * a.max_pages + s];
+                fresh = !keeps(a, r, e);
+                copy |= fresh && s == r.full && r.L % a.P != 0;
+            }
+            n += __popc(__ballot_sync(kFull, fresh));
+        }
+        copy = __any_sync(kFull, copy);
+        if (lane == 0) a.wants[i] = n | (copy ? 1 << 30 : 0);
+    }
+    ptx::cluster_sync();
+
+    // Where each row's new pages begin, and the free pages themselves.
+    int total = 0, copies = 0;
+    for (int i0 = 0; i0 < a.rows_out; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        const int w = i < a.rows_out ? __ldcg(a.wants + i) : 0;
+        int sum, sum_c;
+        const int before = block_scan(w & 0x3fffffff, sums, sum);
+        const int before_c = block_scan(w >> 30, sums, sum_c);
+        if (rank == 0 && i < a.rows_out) {
+            a.base[i] = total + before;
+            a.copies[i] = copies + before_c;
+        }
+        total += sum;
+        copies += sum_c;
+    }
+    int at = 0, free_all = 0;
+    for (int r = 0; r < ctas; ++r) {
+        const int f = __ldcg(a.free_of + r);
+        at += r < rank ? f : 0;
+        free_all += f;
+    }
+    constexpr int kEach = 4;
+    for (int p0 = lo; p0 < hi && at < total; p0 += kEach * kPlanThreads) {
+        bool is[kEach];
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int p = p0 + tid * kEach + j;
+            is[j] = p < hi && a.refs[p] == 0;
+            n += is[j];
+        }
+        int sum;
+        int k = at + block_scan(n, sums, sum);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            if (is[j] && k < total) a.list[k] = p0 + tid * kEach + j;
+            k += is[j];
+        }
+        at += sum;
+    }
+    if (gtid == 0) {
+        *a.count = copies;
+        if (total > free_all) report(a.status, TREE_ATTN_STATUS_NO_PAGE);
+    }
+    ptx::cluster_sync();
+
+    // The new table, and the counts of entries that come and go.
+    for (int i = gwarp; i < a.rows_out; i += gwarps) {
+        const Row r = row_of(a, i);
+        const int32_t* from = a.table + static_cast<size_t>(max(r.parent, 0)) * a.max_pages;
+        int32_t* to = a.table_out + static_cast<size_t>(i) * a.max_pages;
+        int next = __ldcg(a.base + i);
+        int L = r.L;
+        for (int s0 = 0; s0 < a.max_pages; s0 += 32) {
+            const int s = s0 + lane;
+            int e = -1;
+            bool fresh = false;
+            if (s < r.need) {
+                e = from[s];
+                if (s < r.full) {
+                    if (!entry_ok(e, a.num_pages)) {
+                        report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                        e = -1;
+                    }
+                } else {
+                    fresh = !keeps(a, r, e);
+                }
+            }
+            const unsigned who = __ballot_sync(kFull, fresh);
+            if (fresh) {
+                const int k = next + __popc(who & ((1u << lane) - 1u));
+                const int page = k < free_all ? __ldcg(a.list + k) : -1;
+                if (s == r.full && r.L % a.P != 0) {
+                    const int c = __ldcg(a.copies + i);
+                    if (!entry_ok(e, a.num_pages)) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                    a.copy_src[c] = page >= 0 && entry_ok(e, a.num_pages) ? e : -1;
+                    a.copy_dst[c] = page;
+                    if (page < 0) L = r.full * a.P;  // the tokens that found no page
+                }
+                e = page;
+            }
+            if (s >= r.full && e >= 0) atomicAdd(a.refs_out + e, 1);
+            if (s < a.max_pages) to[s] = e;
+            next += __popc(who);
+        }
+        L = __reduce_min_sync(kFull, L);
+        if (lane == 0) a.lens_out[i] = L;
+    }
+    for (int p = gwarp; p < a.rows_in; p += gwarps) {
+        bool bad;
+        const int L = clamp_seq_len(a.lens[p], a.P, a.max_pages, bad);
+        const int full = bad ? 0 : L / a.P;
+        const int kept = __ldcg(a.children + p) - 1;  // for shared pages
+        const int32_t* from = a.table + static_cast<size_t>(p) * a.max_pages;
+        for (int s = (kept == 0 ? full : 0) + lane; s < a.max_pages; s += 32) {
+            const int e = from[s];
+            const int more = s < full ? kept : -1;
+            if (entry_ok(e, a.num_pages))
+                atomicAdd(a.refs_out + e, more);
+            else if (e != -1)
+                report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Compact.  With u(p) = used pages before p and n the used pages in all, the
+// k-th used page at or past n goes to the k-th free page before n:
+//   page p >= n is mover u(p) - u(n), page p < n is hole p - u(p).
+// ---------------------------------------------------------------------------
+struct CompactArgs {
+    const int32_t* table;
+    const int32_t* refs;
+    int32_t* table_out;
+    int32_t* refs_out;
+    int32_t* n_used;  // [1]
+    long long entries;
+    int num_pages;
+    // workspace
+    int32_t* copy_src;  // [num_pages]
+    int32_t* copy_dst;  // [num_pages]
+    int32_t* count;     // [1]
+    int32_t* used_of;   // [kMaxCtas]
+    int32_t* before_n;  // [1] u(n)
+    int32_t* movers;    // [num_pages], at u(p)
+    int32_t* to;        // [num_pages] new place of a page that moves
+    int32_t* status;
+};
+
+__global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    __shared__ int sums[kPlanWarps];
+    const int tid = threadIdx.x;
+    const int ctas = static_cast<int>(ptx::cluster_size());
+    const int rank = static_cast<int>(ptx::cluster_rank());
+    const int gtid = rank * kPlanThreads + tid, gthreads = ctas * kPlanThreads;
+    int lo, hi;
+    my_pages(a.num_pages, lo, hi);
+
+    int mine = 0;
+    for (int p = lo + tid; p < hi; p += kPlanThreads) mine += a.refs[p] > 0;
+    int used_here;
+    block_scan(mine, sums, used_here);
+    if (tid == 0) a.used_of[rank] = used_here;
+    ptx::cluster_sync();
+
+    int u0 = 0, n = 0;
+    for (int r = 0; r < ctas; ++r) {
+        const int c = __ldcg(a.used_of + r);
+        u0 += r < rank ? c : 0;
+        n += c;
+    }
+    if (gtid == 0 && n == a.num_pages) *a.before_n = n;
+    constexpr int kEach = 4;
+    for (int p0 = lo; p0 < hi; p0 += kEach * kPlanThreads) {
+        int c[kEach], m = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int p = p0 + tid * kEach + j;
+            c[j] = p < hi ? a.refs[p] : 0;
+            m += c[j] > 0;
+        }
+        int sum;
+        int u = u0 + block_scan(m, sums, sum);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int p = p0 + tid * kEach + j;
+            if (p >= hi) break;
+            if (p == n) *a.before_n = u;
+            if (p < n) {
+                if (c[j] > 0)
+                    a.refs_out[p] = c[j];
+                else
+                    a.copy_dst[p - u] = p;
+            } else {
+                a.refs_out[p] = 0;
+                if (c[j] > 0) a.movers[u] = p;
+            }
+            u += c[j] > 0;
+        }
+        u0 += sum;
+    }
+    ptx::cluster_sync();
+
+    const int un = __ldcg(a.before_n);
+    const int moves = n - un;
+    for (int k = gtid; k < moves; k += gthreads) {
+        const int from = __ldcg(a.movers + un + k), to = __ldcg(a.copy_dst + k);
+        a.copy_src[k] = from;
+        a.to[from] = to;
+        a.refs_out[to] = a.refs[from];
+    }
+    if (gtid == 0) {
+        *a.count = moves;
+        *a.n_used = n;
+    }
+    ptx::cluster_sync();
+
+    for (long long i = gtid; i < a.entries; i += gthreads) {
+        int e = a.table[i];
+        if (e != -1) {
+            if (!entry_ok(e, a.num_pages) || a.refs[e] <= 0) {
+                report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                e = -1;
+            } else if (e >= n) {
+                e = __ldcg(a.to + e);
+            }
+        }
+        a.table_out[i] = e;
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+int check_pools(void* const* pools, const size_t* page_bytes, int n_pools) {
+    if (n_pools < 0) return TREE_ATTN_ERR_SHAPE;
+    if (n_pools == 0) return TREE_ATTN_OK;
+    if (!pools || !page_bytes) return TREE_ATTN_ERR_NULL;
+    for (int i = 0; i < n_pools; ++i) {
+        if (!pools[i]) return TREE_ATTN_ERR_NULL;
+        if (page_bytes[i] < 1 || page_bytes[i] > (static_cast<size_t>(1) << 31))
+            return TREE_ATTN_ERR_SHAPE;
+    }
+    return TREE_ATTN_OK;
+}
+
+// Pools in launches of at most kPoolsMost.
+int enqueue_copies(void* const* pools, const size_t* page_bytes, int n_pools, const int32_t* src,
+                   const int32_t* dst, const int32_t* count, int n, int num_pages,
+                   int32_t* status, cudaStream_t stream) {
+    if (n == 0) return TREE_ATTN_OK;
+    const int sms = sm_count();
+    if (sms == 0) return TREE_ATTN_ERR_CUDA;
+    CopyArgs a;
+    a.src = src;
+    a.dst = dst;
+    a.count = count;
+    a.n = n;
+    a.num_pages = num_pages;
+    a.status = status;
+    for (int i = 0; i < n_pools;) {
+        long long pieces = 0;
+        int m = 0;
+        for (; i < n_pools && m < kPoolsMost; ++i, ++m) {
+            const long long more = (static_cast<long long>(page_bytes[i]) + kPiece - 1) / kPiece;
+            if (m > 0 && pieces + more > (1LL << 30)) break;
+            a.pool[m] = static_cast<uint8_t*>(pools[i]);
+            a.bytes[m] = static_cast<long long>(page_bytes[i]);
+            a.first[m] = static_cast<int>(pieces);
+            pieces += more;
+        }
+        a.first[m] = static_cast<int>(pieces);
+        a.n_pools = m;
+        // As many CTAs as the SMs hold at once: they take the pieces in turn.
+        const long long warps = pieces * n;
+        const long long ctas = (warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+        const int grid = static_cast<int>(ctas < 8LL * sms ? ctas : 8LL * sms);
+        const int rc = rc_of(launch_dependent(copy_kernel, dim3(grid), dim3(kCopyThreads), 0,
+                                              stream, a));
+        if (rc != TREE_ATTN_OK) return rc;
+    }
+    return TREE_ATTN_OK;
+}
+
+// One CTA where the whole plan is little work, else a cluster.
+int plan_ctas(long long work) { return work <= 8192 ? 1 : kMaxCtas; }
+
+bool pages_shape_ok(int rows, int max_pages, int num_pages) {
+    return rows >= 0 && rows < (1 << 24) && max_pages >= 1 && num_pages >= 1 &&
+           max_pages < (1 << 30) && num_pages < (1 << 30) &&
+           static_cast<long long>(rows) * max_pages < (1LL << 40);
+}
+
+size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+size_t fork_bytes(int rows_in, int rows_out, int num_pages) {
+    return padded((64 + 2 * static_cast<size_t>(rows_in) + 5 * static_cast<size_t>(rows_out) +
+                   static_cast<size_t>(num_pages)) * 4);
+}
+size_t compact_bytes(int num_pages) { return padded((64 + 4 * static_cast<size_t>(num_pages)) * 4); }
+
+}  // namespace
+}  // namespace treeattn
+
+using namespace treeattn;
+
+extern "C" {
+
+int tree_kv_copy_pages(void* const* pools, const size_t* page_bytes, int n_pools,
+                       const int32_t* src, const int32_t* dst, const int32_t* count, int n,
+                       int num_pages, int32_t* status, void* stream) {
+    if (n < 0 || num_pages < 1) return TREE_ATTN_ERR_SHAPE;
+    const int rc = check_pools(pools, page_bytes, n_pools);
+    if (rc != TREE_ATTN_OK) return rc;
+    if (n == 0 || n_pools == 0) return TREE_ATTN_OK;
+    if (!src || !dst) return TREE_ATTN_ERR_NULL;
+    if (!ptr_aligned(src, 4) || !ptr_aligned(dst, 4) || !ptr_aligned(count, 4) ||
+        !ptr_aligned(status, 4))
+        return TREE_ATTN_ERR_ALIGN;
+    return enqueue_copies(pools, page_bytes, n_pools, src, dst, count, n, num_pages, status,
+                          static_cast<cudaStream_t>(stream));
+}
+
+size_t tree_kv_fork_workspace_size(int rows_in, int rows_out, int num_pages) {
+    if (rows_in < 0 || rows_out < 0 || num_pages < 1) return 0;
+    return fork_bytes(rows_in, rows_out, num_pages);
+}
+
+int tree_kv_fork(void* const* pools, const size_t* page_bytes, int n_pools,
+                 const int32_t* block_table, int max_pages_per_seq, const int32_t* seq_lens,
+                 const int32_t* page_refs, const int32_t* src, const int32_t* reserve,
+                 int reserve_all, int32_t* block_table_out, int32_t* seq_lens_out,
+                 int32_t* page_refs_out, int rows_in, int rows_out, int page_size, int num_pages,
+                 void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    if (!pages_shape_ok(rows_in, max_pages_per_seq, num_pages) ||
+        !pages_shape_ok(rows_out, max_pages_per_seq, num_pages) || !page_size_ok(page_size) ||
+        reserve_all < 0)
+        return TREE_ATTN_ERR_SHAPE;
+    const int rc = check_pools(pools, page_bytes, n_pools);
+    if (rc != TREE_ATTN_OK) return rc;
+    if (!page_refs || !page_refs_out || (rows_in > 0 && (!block_table || !seq_lens)) ||
+        (rows_out > 0 && (!src || !block_table_out || !seq_lens_out)))
+        return TREE_ATTN_ERR_NULL;
+    if (page_refs_out == page_refs || (rows_out > 0 && block_table_out == block_table) ||
+        (rows_out > 0 && seq_lens_out == seq_lens))
+        return TREE_ATTN_ERR_SHAPE;
+    const void* ints[] = {block_table, seq_lens,     page_refs,     src,   reserve,
+                          status,      seq_lens_out, page_refs_out, block_table_out};
+    for (const void* p : ints)
+        if (!ptr_aligned(p, 4)) return TREE_ATTN_ERR_ALIGN;
+    if (!workspace || !ptr_aligned(workspace, 256) ||
+        workspace_bytes < fork_bytes(rows_in, rows_out, num_pages))
+        return TREE_ATTN_ERR_WORKSPACE;
+    ForkArgs a;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.refs = page_refs;
+    a.src = src;
+    a.reserve = reserve;
+    a.reserve_all = reserve_all;
+    a.table_out = block_table_out;
+    a.lens_out = seq_lens_out;
+    a.refs_out = page_refs_out;
+    a.rows_in = rows_in;
+    a.rows_out = rows_out;
+    a.max_pages = max_pages_per_seq;
+    a.P = page_size;
+    a.num_pages = num_pages;
+    int32_t* w = static_cast<int32_t*>(workspace);
+    a.count = w;
+    a.free_of = w + 32;
+    w += 64;
+    a.children = w;
+    a.eldest = w + rows_in;
+    w += 2 * static_cast<size_t>(rows_in);
+    a.copy_src = w;
+    a.copy_dst = w + rows_out;
+    w += 2 * static_cast<size_t>(rows_out);
+    a.wants = w;
+    a.base = w + rows_out;
+    w += 2 * static_cast<size_t>(rows_out);
+    a.copies = w;
+    a.list = w + rows_out;
+    a.status = status;
+    const long long work =
+        num_pages + static_cast<long long>(rows_in + rows_out) * max_pages_per_seq;
+    const int ctas = plan_ctas(work);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int rp = rc_of(launch_cluster(fork_kernel, dim3(ctas), dim3(kPlanThreads), 0, ctas, s, a));
+    if (rp != TREE_ATTN_OK || n_pools == 0) return rp;
+    return enqueue_copies(pools, page_bytes, n_pools, a.copy_src, a.copy_dst, a.count, rows_out,
+                          num_pages, status, s);
+}
+
+size_t tree_kv_compact_workspace_size(int num_pages) {
+    return num_pages < 1 ? 0 : compact_bytes(num_pages);
+}
+
+int tree_kv_compact(void* const* pools, const size_t* page_bytes, int n_pools,
+                    const int32_t* block_table, int max_pages_per_seq, const int32_t* page_refs,
+                    int32_t* block_table_out, int32_t* page_refs_out, int32_t* n_used, int rows,
+                    int num_pages, void* workspace, size_t workspace_bytes, int32_t* status,
+                    void* stream) {
+    if (!pages_shape_ok(rows, max_pages_per_seq, num_pages)) return TREE_ATTN_ERR_SHAPE;
+    const int rc = check_pools(pools, page_bytes, n_pools);
+    if (rc != TREE_ATTN_OK) return rc;
+    if (!page_refs || !page_refs_out || !n_used ||
+        (rows > 0 && (!block_table || !block_table_out)))
+        return TREE_ATTN_ERR_NULL;
+    if (page_refs_out == page_refs) return TREE_ATTN_ERR_SHAPE;
+    const void* ints[] = {block_table, page_refs, block_table_out, page_refs_out, n_used, status};
+    for (const void* p : ints)
+        if (!ptr_aligned(p, 4)) return TREE_ATTN_ERR_ALIGN;
+    if (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < compact_bytes(num_pages))
+        return TREE_ATTN_ERR_WORKSPACE;
+    CompactArgs a;
+    a.table = block_table;
+    a.refs = page_refs;
+    a.table_out = block_table_out;
+    a.refs_out = page_refs_out;
+    a.n_used = n_used;
+    a.entries = static_cast<long long>(rows) * max_pages_per_seq;
+    a.num_pages = num_pages;
+    int32_t* w = static_cast<int32_t*>(workspace);
+    a.count = w;
+    a.before_n = w + 1;
+    a.used_of = w + 32;
+    w += 64;
+    a.copy_src = w;
+    a.copy_dst = w + num_pages;
+    w += 2 * static_cast<size_t>(num_pages);
+    a.movers = w;
+    a.to = w + num_pages;
+    a.status = status;
+    const int ctas = plan_ctas(num_pages + a.entries);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int rp =
+        rc_of(launch_cluster(compact_kernel, dim3(ctas), dim3(kPlanThreads), 0, ctas, s, a));
+    if (rp != TREE_ATTN_OK || n_pools == 0) return rp;
+    return enqueue_copies(pools, page_bytes, n_pools, a.copy_src, a.copy_dst, a.count,
+                          num_pages / 2, num_pages, status, s);
+}
+
+}  // extern "C"
