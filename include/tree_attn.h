@@ -61,7 +61,7 @@ extern "C" {
 #define TREE_ATTN_STATUS_BAD_PATH 5     /* accept_len outside [0, T] or a path node     */
                                         /* outside [0, T) (tree_kv_commit)              */
 #define TREE_ATTN_STATUS_NO_PAGE 6      /* no free page left (tree_kv_fork)             */
-#define TREE_ATTN_STATUS_BAD_ROW 7      /* src outside [-1, rows_in) (tree_kv_fork)     */
+#define TREE_ATTN_STATUS_BAD_ROW 7      /* src outside [-2, rows_in) (tree_kv_fork)     */
 
 /* Limits. */
 #define TREE_ATTN_MAX_T 64
@@ -663,7 +663,8 @@ TREE_ATTN_API int tree_kv_copy_pages(void *const *pools, const size_t *page_byte
  * tree_kv_fork -- the rows of the next step from the rows of this one: beams or
  * samples that go on from the same row, rows that end, rows that grow, new rows.
  * Row i of the outputs continues row p = src[i] with its L = seq_lens[p] tokens
- * (src[i] = -1: a row without tokens), mapped for L + reserve positions:
+ * (src[i] = -2: a new row, L = 0; -1: no row, no pages), mapped for L + reserve
+ * positions:
  *   - pages of whole committed blocks are shared with p;
  *   - a page behind them is kept by the first row that continues p, if
  *     page_refs counts nobody else for it; other rows get pages of their own,
@@ -724,7 +725,8 @@ TREE_ATTN_API int tree_kv_compact(void *const *pools, const size_t *page_bytes, 
  * and tokens are taken, in descending order, ties to the lowest (w, v).
  *   logits       [B][W][V] of type `dtype` (0 bf16, 1 fp16, 2 fp32); batch and
  *                beam strides in elements, not negative, the V logits contiguous.
- *                NaN and -inf are no candidates, +inf is the largest number.
+ *                NaN and -inf are no candidates; where some are +inf, those share
+                the beam's whole probability.
  *   scores       fp32 [B][W]; a beam at -inf or NaN has no candidates
  *   finished     nullable uint8 [B][W]: a non-zero beam's only candidate is (w,
  *                eos) with its score unchanged (its logits are not read)

@@ -88,8 +88,8 @@ def kv_fork(pools, block_table, seq_lens, page_refs, src, page_size: int, *, res
     """The rows of the next step from the rows of this one.
 
     Row i of the results continues row src[i] of block_table int32 [rows][max_pages]
-    (-1 where there is no page) and seq_lens int32 [rows]; src int32 [rows_out], -1: a
-    new row without tokens.  Whole pages are shared; the last one stays with the
+    (-1 where there is no page) and seq_lens int32 [rows]; src int32 [rows_out], -2: a
+    new row without tokens, -1: no row.  Whole pages are shared; the last one stays with the
     first row that continues a row and is copied, in every pool, for the others;
     every row is mapped for ``reserve`` more tokens (a number, or int32
     [rows_out]).  page_refs int32 [num_pages] counts the table entries (and other

@@ -34,11 +34,8 @@ constexpr int kEach = 32;                  // logits of one thread
 constexpr int kPiece = kThreads * kEach;   // logits of one CTA
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Order-preserving bits of a logit; 0 for what is no candidate (NaN, -inf).
-// +inf counts as the largest finite number; -0 as +0.
-__device__ __forceinline__ float clean(float x) {
-    return fminf(x + 0.0f, 3.402823466e38f);  // (NaN becomes the number)
-}
+// Order-preserving bits of a logit (-0 as +0, NaN as -inf: no candidate).
+__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : x + 0.0f; }
 __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t b = __float_as_uint(x);
     return (b >> 31) != 0 ? ~b : b | 0x80000000u;
@@ -111,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) piece_kernel(const PieceArgs a) {
     int at = 0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        v[e] = v[e] != v[e] ? -INFINITY : clean(v[e]);
+        v[e] = clean(v[e]);
         if (v[e] > top) {
             top = v[e];
             at = e;
@@ -157,7 +154,10 @@ __global__ void __launch_bounds__(kThreads) piece_kernel(const PieceArgs a) {
         if (t != 0 && above == a.K - 1) bound = t;
     }
     float sum = 0.0f;
-    if (m > -INFINITY) {
+    if (m == INFINITY) {  // such logits share all of the probability
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) sum += v[e] == INFINITY ? 1.0f : 0.0f;
+    } else if (m > -INFINITY) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) sum += exp2f((v[e] - m) * kLog2e);
     }
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a) {
         if (!done && m > -INFINITY)
             for (int i = lane; i < a.pieces; i += 32)
                 if (s[i].x > -INFINITY)
-                    sum += static_cast<double>(s[i].y) * exp2f((s[i].x - m) * kLog2e);
+                    sum += s[i].x == m ? s[i].y
+                                       : static_cast<double>(s[i].y) * exp2f((s[i].x - m) * kLog2e);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
         if (lane == 0) {
@@ -285,7 +286,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a) {
         const unsigned long long k = a.keys[(row0 + w) * per_row + j];
         if (k != 0) {
             const double x = logit_of(static_cast<uint32_t>(k >> 32));
-            c.s = bits_of(start + ((x - static_cast<double>(row_max[w])) - log_sum[w]));
+            const double top = row_max[w];
+            c.s = bits_of(start + ((x == top ? 0.0 : x - top) - log_sum[w]));
             c.place = ~(static_cast<unsigned long long>(w) * a.V +
                         (0xffffffffu - static_cast<uint32_t>(k)));
         }

@@ -145,7 +145,8 @@ __device__ __forceinline__ void my_pages(int num_pages, int& lo, int& hi) {
 }
 
 // ---------------------------------------------------------------------------
-// Fork.  Row i continues row p = src[i] with its L = seq_lens[p] tokens:
+// Fork.  Row i continues row p = src[i] with its L = seq_lens[p] tokens (p = -2: a
+// new row, L = 0; p = -1: no row, no pages):
 //   slots before floor(L / P)   p's pages, shared;
 //   slots up to (L + reserve)   p's own page where i is p's first row and no
 //                               other reference to that page exists, else a new
@@ -179,7 +180,7 @@ struct ForkArgs {
 };
 
 struct Row {
-    int parent;  // -1: an empty row
+    int parent;  // -1: no row, -2: a new one
     int L, full, need;
     bool eldest;
 };
@@ -189,15 +190,18 @@ __device__ __forceinline__ bool entry_ok(int e, int num_pages) { return e >= 0 &
 __device__ __forceinline__ Row row_of(const ForkArgs& a, int i) {
     Row r;
     r.parent = a.src[i];
-    if (r.parent < 0 || r.parent >= a.rows_in) {
-        if (r.parent != -1) report(a.status, TREE_ATTN_STATUS_BAD_ROW);
+    r.L = r.full = r.need = 0;
+    r.eldest = false;
+    if (r.parent < -2 || r.parent >= a.rows_in) {
+        report(a.status, TREE_ATTN_STATUS_BAD_ROW);
         r.parent = -1;
-        r.L = r.full = r.need = 0;
-        r.eldest = false;
-        return r;
     }
-    bool bad;
-    r.L = clamp_seq_len(a.lens[r.parent], a.P, a.max_pages, bad);
+    if (r.parent == -1) return r;
+    bool bad = false;
+    if (r.parent >= 0) {
+        r.L = clamp_seq_len(a.lens[r.parent], a.P, a.max_pages, bad);
+        r.eldest = __ldcg(a.eldest + r.parent) == i;
+    }
     if (bad) {
         report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
         r.L = 0;
@@ -208,7 +212,6 @@ __device__ __forceinline__ Row row_of(const ForkArgs& a, int i) {
     if (need > a.max_pages) report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
     r.full = r.L / a.P;
     r.need = static_cast<int>(min(need, static_cast<long long>(a.max_pages)));
-    r.eldest = __ldcg(a.eldest + r.parent) == i;
     return r;
 }
 
@@ -263,7 +266,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
             const int s = s0 + lane;
             bool fresh = false;
             if (s < r.need) {
-                const int e = a.table[static_cast<size_t>(r.parent) * a.max_pages + s];
+                const int e = r.parent >= 0
+                                  ? a.table[static_cast<size_t>(r.parent) * a.max_pages + s]
+                                  : -1;
                 fresh = !keeps(a, r, e);
                 copy |= fresh && s == r.full && r.L % a.P != 0;
             }
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
             int e = -1;
             bool fresh = false;
             if (s < r.need) {
-                e = from[s];
+                e = r.parent >= 0 ? from[s] : -1;
                 if (s < r.full) {
                     if (!entry_ok(e, a.num_pages)) {
                         report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
