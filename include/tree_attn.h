@@ -733,8 +733,8 @@ TREE_ATTN_API int tree_kv_compact(void *const *pools, const size_t *page_bytes, 
  *   scores_out   fp32 [B][K];  rows_out int32 [B][K]: b * W + w;  tokens_out int32
  *                [B][K].  Where there are fewer than K candidates: -inf, -1, -1.
  *   workspace    tree_beam_workspace_size(...) bytes, 256-byte aligned
- * 1 <= W, K <= 64, B * W <= 65535, V <= 2^30, W * K * ceil((V + 7) / 8192) <=
- * 32768.  Scores are summed in fp64 over fp32 sums of exponentials.
+ * 1 <= W, K <= 64, B * W <= 65535, V <= 2^30, W * K * ceil((V + 7) / 4096) <=
+ * 131072.  Scores are summed in fp64 over fp32 sums of exponentials.
  * Returns 0, -1, -2, -3, -4, -5.
  */
 TREE_ATTN_API size_t tree_beam_workspace_size(int B, int W, int V, int K);

@@ -4,16 +4,19 @@
 // With x the logits of beam w and s_w its score, candidate (w, v) scores
 //   s_w + (x_v - m) - ln sum_u exp(x_u - m),   m = max x,
 // and the K highest are taken, ties to the lowest (w, v).  Within a beam that
-// is the order of x itself, so one pass over the logits suffices: a CTA takes a
-// piece of a row, keeps it in registers, and leaves the piece's maximum, its
-// sum of exponentials (fp32) and its K largest logits.  A second, small kernel
-// joins the sums, scores the few candidates in fp64 (so that the order of two
-// beams' candidates is not that of a rounding) and takes the best K.
+// is the order of x itself, so one pass over the logits suffices: a CTA streams a
+// piece of a row and leaves the piece's maximum, its sum of exponentials (fp32)
+// and its K largest logits.  A second, small kernel joins the sums, scores the few
+// candidates in fp64 (so that the order of two beams' candidates is not that of a
+// rounding) and takes the best K.
 //
-// The K largest of a piece: the largest logit of every group of four lanes is
-// known after the maximum; the K-th largest of those 64 is a bound that at least
-// K logits reach and few exceed, and only logits at or above it are looked at
-// again.  Keys (logit, -index) are all different, so ties need no extra rule.
+// The K largest of a piece: of its first tile the largest logit of every group of
+// four lanes is known after the maximum; the K-th largest of those 64 is a bound
+// that at least K logits reach and few exceed.  Only logits above it are kept from
+// then on (one comparison per tile and thread as a rule).  Where more are kept than
+// there is room for -- logits that ascend, a first tile of -inf -- the piece is read
+// again with the bound of all its threads' largest logits, under which there is
+// always room.  Keys (logit, -index) are all different, so ties need no extra rule.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,8 +33,9 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kEach = 32;                  // logits of one thread
-constexpr int kPiece = kThreads * kEach;   // logits of one CTA
+constexpr int kEach = 16;                  // logits of one thread in a tile
+constexpr int kTile = kThreads * kEach;
+constexpr int kMostTiles = 8;              // of a piece
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Order-preserving bits of a logit (-0 as +0, NaN as -inf: no candidate).
@@ -42,6 +46,12 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 __device__ __forceinline__ float logit_of(uint32_t key) {
     return __uint_as_float((key >> 31) != 0 ? key & 0x7fffffffu : ~key);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <typename T>
@@ -65,132 +75,254 @@ struct PieceArgs {
     const uint8_t* finished;              // nullable [B][W]
     unsigned long long* keys;             // [rows][pieces][K]
     float2* sums;                         // [rows][pieces] (max, sum)
-    int W, V, K, pieces;
+    int W, V, K, pieces, tiles, room;
 };
 
+// Sorting key of a logit: 0 for what is no candidate.
+__device__ __forceinline__ unsigned long long full_key(float x, uint32_t index) {
+    return x == -INFINITY
+               ? 0ull
+               : (static_cast<unsigned long long>(key_of(x)) << 32) | (0xffffffffu - index);
+}
+
+// The K-th largest of the CTA's NT keys (0: none) in `tops`, 1 where there are
+// fewer; to be called by all threads, kThreads / NT of which look at one key.
+template <int NT>
+__device__ __forceinline__ void find_bound(const unsigned long long* tops, int K,
+                                           unsigned long long* bound) {
+    constexpr int P = kThreads / NT;
+    const int tid = threadIdx.x;
+    if (tid == 0) *bound = 1;
+    __syncthreads();
+    const unsigned long long t = tops[tid / P];
+    int above = 0;
+#pragma unroll 16
+    for (int i = tid % P; i < NT; i += P) above += tops[i] > t;
+#pragma unroll
+    for (int off = 1; off < P; off <<= 1) above += __shfl_xor_sync(kFull, above, off);
+    if (t != 0 && above == K - 1) *bound = t;  // (one of P threads' equal stores)
+    __syncthreads();
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) piece_kernel(const PieceArgs a) {
+struct Row {
+    const T* x;
+    int V, skew;  // `skew` logits before the row's first share its first vector, unread
+    static constexpr int N = 16 / sizeof(T);
+
+    // Index of logit e of a thread in the tile that begins at `first`.
+    __device__ __forceinline__ int index(int first, int e) const {
+        return first + ((e / N) * kThreads + static_cast<int>(threadIdx.x)) * N - skew + e % N;
+    }
+    static constexpr int kVecs = kEach / N;
+
+    // Whether a tile lies inside the row, so that its vectors can be read whole.
+    __device__ __forceinline__ bool inside(int first) const {
+        return first >= skew && first + kTile - skew <= V;
+    }
+    __device__ __forceinline__ void fetch(int first, uint4 (&raw)[kVecs]) const {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+            raw[u] = __ldcs(reinterpret_cast<const uint4*>(x + index(first, u * N)));
+    }
+    __device__ __forceinline__ void unpack(const uint4 (&raw)[kVecs], float (&v)[kEach]) const {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            const T* t = reinterpret_cast<const T*>(&raw[u]);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[u * N + j] = as_float<T>(t[j]);
+        }
+    }
+    // Any tile; -inf for what is not in the row.
+    __device__ __forceinline__ void load(int first, float (&v)[kEach]) const {
+        if (inside(first)) {
+            uint4 raw[kVecs];
+            fetch(first, raw);
+            unpack(raw, v);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = index(first, e);
+            v[e] = i >= 0 && i < V ? as_float<T>(x[i]) : -INFINITY;
+        }
+    }
+    // The largest of a thread's logits; of equal ones the first.
+    __device__ __forceinline__ unsigned long long largest(int first, const float (&v)[kEach]) const {
+        float top = -INFINITY;
+        int at = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const float y = clean(v[e]);
+            if (y > top) {
+                top = y;
+                at = e;
+            }
+        }
+        return full_key(top, static_cast<uint32_t>(index(first, at)));
+    }
+};
+
+// Sum of exp(v - m) with m >= every v; no number where m log2(e) overflows.
+__device__ __forceinline__ float exp_sum(const float (&v)[kEach], float m) {
+    // 2^(v log2(e) - r), r being m log2(e) rounded, and what the rounding took.
+    const float r = m * kLog2e;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) s[e & 3] += ex2(fmaf(v[e], kLog2e, -r));
+    return ((s[0] + s[1]) + (s[2] + s[3])) * ex2(fmaf(-m, kLog2e, r));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    extern __shared__ unsigned long long piece_found[];  // K * 4 * kEach at most
+    extern __shared__ unsigned long long kept[];  // [room]
     __shared__ unsigned long long tops[kThreads];
-    __shared__ float red[kWarps];
+    __shared__ float red[2][kWarps];
     __shared__ unsigned long long bound;
-    __shared__ int n_found;
+    __shared__ int n_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.y, piece = blockIdx.x;
     const int b = row / a.W, w = row % a.W;
     if (a.finished != nullptr && a.finished[row] != 0) return;  // (not read for it either)
-    const T* x = static_cast<const T*>(a.logits) + b * a.batch_stride + w * a.beam_stride;
-    const int first = piece * kPiece;
-    constexpr int N = 16 / sizeof(T);  // logits of a vector
-    constexpr int U = kEach / N;
-    // Vectors start on 16-byte boundaries: `skew` logits before the row's first
-    // belong to the first one, and are not read.
-    const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    float v[kEach];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int i = first + (u * kThreads + tid) * N - skew;
-        if (i >= 0 && i + N <= a.V) {
-            const uint4 raw = *reinterpret_cast<const uint4*>(x + i);
-            const T* t = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[u * N + j] = as_float<T>(t[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                v[u * N + j] = i + j >= 0 && i + j < a.V ? as_float<T>(x[i + j]) : -INFINITY;
+    Row<T> r;
+    r.x = static_cast<const T*>(a.logits) + b * a.batch_stride + w * a.beam_stride;
+    r.V = a.V;
+    r.skew = static_cast<int>((reinterpret_cast<uintptr_t>(r.x) & 15) / sizeof(T));
+    const int first = piece * a.tiles * kTile;
+    if (tid == 0) n_kept = 0;
+    // Keeps those of a thread's logits (bits of `which`) that reach `least`: few, read
+    // again rather than held for it.
+    auto keep = [&](unsigned which, int at, unsigned long long least) {
+        while (which != 0) {
+            const int i = r.index(at, __ffs(which) - 1);
+            which &= which - 1;
+            const unsigned long long k =
+                full_key(clean(as_float<T>(r.x[i])), static_cast<uint32_t>(i));
+            if (k >= least) {
+                const int place = atomicAdd(&n_kept, 1);
+                if (place < a.room) kept[place] = k;
+            }
         }
-    }
-    // The largest of each thread; of two equal ones the first.
-    float top = -INFINITY;
-    int at = 0;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        v[e] = clean(v[e]);
-        if (v[e] > top) {
-            top = v[e];
-            at = e;
-        }
-    }
-    auto index_of = [&](int e) {
-        return static_cast<uint32_t>(first + ((e / N) * kThreads + tid) * N - skew + e % N);
     };
-    unsigned long long mine =
-        top == -INFINITY
-            ? 0ull
-            : (static_cast<unsigned long long>(key_of(top)) << 32) | (0xffffffffu - index_of(at));
-    float m = top;
+    float m = -INFINITY, s = 0.0f, lim = INFINITY;
+    uint4 raw[Row<T>::kVecs];
+    if (r.inside(first)) r.fetch(first, raw);
+    for (int t = 0; t < a.tiles; ++t) {
+        const int at = first + t * kTile;
+        if (at - r.skew >= a.V) break;
+        float v[kEach];
+        if (r.inside(at))
+            r.unpack(raw, v);
+        else
+            r.load(at, v);
+        // The next tile is on its way while this one is looked at.
+        if (t + 1 < a.tiles && r.inside(at + kTile)) r.fetch(at + kTile, raw);
+        float top = -INFINITY;  // (the number, of a number and a NaN)
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-    if (lane == 0) red[warp] = m;
-    // Groups of four lanes where 64 tops are enough, else every lane its own.
-    const int group = a.K <= 16 ? 4 : 1;
-    if (group == 4) {
+        for (int e = 0; e < kEach; ++e) top = fmaxf(top, v[e]);
+        unsigned long long least = 1;
+        bool some;
+        if (t == 0) {
+            unsigned long long mine = r.largest(at, v);
+            // Groups of four lanes where 64 of them are enough, else every lane its own.
+            if (a.K <= 16) {
 #pragma unroll
-        for (int off = 1; off < 4; off <<= 1) {
-            const unsigned long long o = __shfl_xor_sync(kFull, mine, off);
-            mine = o > mine ? o : mine;
+                for (int off = 1; off < 4; off <<= 1) {
+                    const unsigned long long o = __shfl_xor_sync(kFull, mine, off);
+                    mine = o > mine ? o : mine;
+                }
+                if ((lane & 3) == 0) tops[tid >> 2] = mine;
+                find_bound<kThreads / 4>(tops, a.K, &bound);
+            } else {
+                tops[tid] = mine;
+                find_bound<kThreads>(tops, a.K, &bound);
+            }
+            least = bound;
+            lim = least == 1 ? -INFINITY : logit_of(static_cast<uint32_t>(least >> 32));
+            some = top >= lim;
+        } else {
+            some = top > lim;  // (an equal one further on is worse than K others)
         }
-        if ((lane & 3) == 0) tops[tid >> 2] = mine;
-    } else {
-        tops[tid] = mine;
-    }
-    if (tid == 0) {
-        n_found = 0;
-        bound = 1;  // any candidate, unless there are K tops
-    }
-    __syncthreads();
-    m = red[0];
+        if (some) {
+            unsigned which = 0;  // (never what lies outside the row: that is -inf)
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) m = fmaxf(m, red[i]);
-    const int n_tops = kThreads / group;
-    if (tid < n_tops) {
-        const unsigned long long t = tops[tid];
-        int above = 0;
-#pragma unroll 8
-        for (int i = 0; i < n_tops; ++i) above += tops[i] > t;
-        if (t != 0 && above == a.K - 1) bound = t;
-    }
-    float sum = 0.0f;
-    if (m == INFINITY) {  // such logits share all of the probability
+            for (int e = 0; e < kEach; ++e)
+                if (v[e] > lim || (least != 1 && v[e] == lim)) which |= 1u << e;
+            keep(which, at, least);
+        }
+        if (top > m) {
+            s = m == -INFINITY ? 0.0f : s * ex2((m - top) * kLog2e);
+            m = top;
+        }
+        if (m > -INFINITY) {
+            float sum = exp_sum(v, m);
+            if (!(sum < INFINITY)) {  // NaN among them, or +inf: such share all of the probability
+                sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) sum += v[e] == INFINITY ? 1.0f : 0.0f;
-    } else if (m > -INFINITY) {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) sum += exp2f((v[e] - m) * kLog2e);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    __syncthreads();
-    if (lane == 0) red[warp] = sum;
-    const unsigned long long lim = bound;
-    const float least = logit_of(static_cast<uint32_t>(lim >> 32));
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        if (lim == 1 ? v[e] > -INFINITY : v[e] >= least) {
-            const unsigned long long k = (static_cast<unsigned long long>(key_of(v[e])) << 32) |
-                                         (0xffffffffu - index_of(e));
-            if (k >= lim) piece_found[atomicAdd(&n_found, 1)] = k;
+                for (int e = 0; e < kEach; ++e) {
+                    const float y = clean(v[e]);
+                    sum += y == m ? 1.0f : m == INFINITY ? 0.0f : ex2((y - m) * kLog2e);
+                }
+            }
+            s += sum;
         }
     }
+    // The piece's maximum and sum.
+    float all = m;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, off));
+    if (lane == 0) red[0][warp] = all;
     __syncthreads();
-    const int n = n_found;
+    all = red[0][0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) all = fmaxf(all, red[0][i]);
+    s = m == all ? s : m == -INFINITY || all == INFINITY ? 0.0f : s * ex2((m - all) * kLog2e);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+    if (lane == 0) red[1][warp] = s;
+    __syncthreads();
     const size_t out = static_cast<size_t>(row) * a.pieces + piece;
+    if (tid == 0) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) sum += red[1][i];
+        a.sums[out] = make_float2(all, sum);
+    }
+    int n = n_kept;
+    if (n > a.room) {  // (rare) the piece again
+        unsigned long long mine = 0;
+        for (int t = 0; t < a.tiles; ++t) {
+            float v[kEach];
+            r.load(first + t * kTile, v);
+            const unsigned long long k = r.largest(first + t * kTile, v);
+            mine = k > mine ? k : mine;
+        }
+        tops[tid] = mine;
+        find_bound<kThreads>(tops, a.K, &bound);
+        const unsigned long long least = bound;
+        if (tid == 0) n_kept = 0;
+        __syncthreads();
+        for (int t = 0; t < a.tiles; ++t) {
+            float v[kEach];
+            r.load(first + t * kTile, v);
+            unsigned which = 0;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                if (v[e] > -INFINITY) which |= 1u << e;
+            keep(which, first + t * kTile, least);
+        }
+        __syncthreads();
+        n = n_kept;
+    }
     for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long k = piece_found[i];
+        const unsigned long long k = kept[i];
         int above = 0;
-        for (int j = 0; j < n; ++j) above += piece_found[j] > k;
+        for (int j = 0; j < n; ++j) above += kept[j] > k;
         if (above < a.K) a.keys[out * a.K + above] = k;
     }
     for (int i = n + tid; i < a.K; i += kThreads) a.keys[out * a.K + i] = 0;
-    if (tid == 0) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) s += red[i];
-        a.sums[out] = make_float2(m, s);
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -204,10 +336,9 @@ struct JoinArgs {
     float* scores_out;        // [B][K]
     int32_t* rows_out;        // [B][K]
     int32_t* tokens_out;      // [B][K]
-    int W, V, K, pieces, eos;
+    int W, V, K, pieces, eos, group;
 };
 
-constexpr int kJoinThreads = 256;
 constexpr int kMaxBeams = 64;
 
 // A candidate: order-preserving bits of its fp64 score (0: none), then the
@@ -229,106 +360,168 @@ __device__ __forceinline__ double score_of(unsigned long long b) {
         static_cast<long long>((b >> 63) != 0 ? b & ~(1ull << 63) : ~b));
 }
 
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a) {
+// ln x for x in [1, 2^126) to 2^-24 absolute: the power of two apart, its logarithm in
+// fp64.  (fp32 would hold ln 128000 to 2^-21 only, and fp64 throughout is slow.)
+__device__ __forceinline__ double log_of(float x) {
+    const int e = static_cast<int>(__float_as_uint(x) >> 23) - 127;
+    const float f = __uint_as_float((__float_as_uint(x) & 0x7fffffu) | 0x3f800000u);  // [1, 2)
+    return static_cast<double>(e) * 0.693147180559945309 + static_cast<double>(logf(f));
+}
+
+// How many of n candidates are better than each of them: n_of(i) is told for
+// candidate i by one thread, where as many threads as there are for each share it.
+template <int NT, typename F>
+__device__ __forceinline__ void rank_all(const Cand* c, int n, F n_of) {
+    const int tid = threadIdx.x;
+    int P = 1;  // threads to a candidate
+    while (P < 32 && 2 * P * n <= NT) P *= 2;
+    for (int i0 = 0; i0 < n; i0 += NT / P) {
+        const int i = i0 + tid / P;
+        const Cand mine = c[min(i, n - 1)];
+        int above = 0;
+#pragma unroll 4
+        for (int j = tid % P; j < n; j += P) above += better(c[j], mine);
+        for (int off = 1; off < P; off <<= 1) above += __shfl_xor_sync(kFull, above, off);
+        if (i < n && tid % P == 0) n_of(i, mine, above);
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    extern __shared__ Cand join_found[];  // K * (candidates per thread) at most
-    __shared__ Cand tops[kJoinThreads];
-    __shared__ double log_sum[kMaxBeams];
-    __shared__ float row_max[kMaxBeams];
+    extern __shared__ Cand kept_of[];     // join_smem
+    __shared__ Cand tops[NT];
+    __shared__ double less[kMaxBeams];    // what is taken off a beam's logits, after its maximum
+    __shared__ float row_max[kMaxBeams], start[kMaxBeams];
+    __shared__ uint8_t done[kMaxBeams];
     __shared__ Cand bound;
-    __shared__ int n_found;
+    __shared__ int n_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x;
-    const size_t row0 = static_cast<size_t>(b) * a.W;
-    for (int w = warp; w < a.W; w += kJoinThreads / 32) {
-        float m = -INFINITY;
-        const bool done = a.finished != nullptr && a.finished[row0 + w] != 0;
-        const float2* s = a.sums + (row0 + w) * a.pieces;
-        if (!done)
-            for (int i = lane; i < a.pieces; i += 32) m = fmaxf(m, s[i].x);
+    const int row0 = b * a.W;
+    const int per_row = a.pieces * a.K;
+    const int all = a.W * per_row;
+    const unsigned long long* keys = a.keys + static_cast<size_t>(row0) * per_row;
+    // The first few candidates of a thread stay with it; their loads come first.
+    constexpr int kHeld = 4;
+    unsigned long long key[kHeld];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-        double sum = 0.0;
-        if (!done && m > -INFINITY)
-            for (int i = lane; i < a.pieces; i += 32)
-                if (s[i].x > -INFINITY)
-                    sum += s[i].x == m ? s[i].y
-                                       : static_cast<double>(s[i].y) * exp2f((s[i].x - m) * kLog2e);
+    for (int h = 0; h < kHeld; ++h) key[h] = tid + h * NT < all ? keys[tid + h * NT] : 0ull;
+    for (int w = warp; w < a.W; w += NT / 32) {
+        const bool over = a.finished != nullptr && a.finished[row0 + w] != 0;
+        const float2* s = a.sums + static_cast<size_t>(row0 + w) * a.pieces;
+        float m = -INFINITY, sum = 0.0f;
+        for (int i = lane; i < a.pieces; i += 32) {
+            const float2 y = s[i];
+            if (over || y.x == -INFINITY) continue;
+            if (y.x > m) {
+                sum = m == -INFINITY ? 0.0f : sum * ex2((m - y.x) * kLog2e);
+                m = y.x;
+            }
+            sum += y.x == m ? y.y : y.y * ex2((y.x - m) * kLog2e);
+        }
+        float top = m;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+        sum = m == top ? sum : m == -INFINITY ? 0.0f : sum * ex2((m - top) * kLog2e);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
         if (lane == 0) {
-            row_max[w] = m;
-            log_sum[w] = done ? 0.0 : log(sum);
+            row_max[w] = top;
+            start[w] = a.scores[row0 + w];
+            done[w] = over;
+            less[w] = over || top == -INFINITY ? 0.0 : log_of(sum);
         }
     }
-    if (tid == 0) {
-        n_found = 0;
-        bound.s = 1;
-        bound.place = 0;
-    }
+    if (tid == 0) n_kept = 0;
     __syncthreads();
-    const int per_row = a.pieces * a.K;
-    const int all = a.W * per_row;
-    auto cand = [&](int i) {
+    const float per_inv = 1.0f / static_cast<float>(per_row);
+    auto cand = [&](int i, unsigned long long k) {
         Cand c;
         c.s = 0;
         c.place = 0;
-        const int w = i / per_row, j = i - w * per_row;
-        const double start = a.scores[row0 + w];
-        if (a.finished != nullptr && a.finished[row0 + w] != 0) {  // stands for itself alone
-            if (j == 0) {
-                c.s = bits_of(start);
+        // Exact: (i + 1/2) / per_row lies 1 / (2 per_row) >= W 2^-18 from a whole number
+        // (131072 candidates at most), and its error is below W 2^-22.
+        const int w = min(static_cast<int>((static_cast<float>(i) + 0.5f) * per_inv), a.W - 1);
+        if (done[w]) {  // stands for itself alone
+            if (i == w * per_row) {
+                c.s = bits_of(start[w]);
                 c.place = ~(static_cast<unsigned long long>(w) * a.V + a.eos);
             }
-            return c;
-        }
-        const unsigned long long k = a.keys[(row0 + w) * per_row + j];
-        if (k != 0) {
-            const double x = logit_of(static_cast<uint32_t>(k >> 32));
-            const double top = row_max[w];
-            c.s = bits_of(start + ((x == top ? 0.0 : x - top) - log_sum[w]));
+        } else if (k != 0) {
+            const float x = logit_of(static_cast<uint32_t>(k >> 32)), top = row_max[w];
+            const double y = x == top ? 0.0 : static_cast<double>(x) - static_cast<double>(top);
+            c.s = bits_of(static_cast<double>(start[w]) + (y - less[w]));
             c.place = ~(static_cast<unsigned long long>(w) * a.V +
                         (0xffffffffu - static_cast<uint32_t>(k)));
         }
         return c;
     };
-    Cand mine;
-    mine.s = mine.place = 0;
-    for (int i = tid; i < all; i += kJoinThreads) {
-        const Cand c = cand(i);
-        if (better(c, mine)) mine = c;
-    }
-    tops[tid] = mine;
-    __syncthreads();
-    if (mine.s != 0) {
-        int above = 0;
-        for (int i = 0; i < kJoinThreads; ++i) above += better(tops[i], mine);
-        if (above == a.K - 1) bound = mine;
-    }
-    __syncthreads();
-    const Cand lim = bound;
-    for (int i = tid; i < all; i += kJoinThreads) {
-        const Cand c = cand(i);
-        if (!better(lim, c)) join_found[atomicAdd(&n_found, 1)] = c;
-    }
-    __syncthreads();
-    const int n = n_found;
     const size_t out = static_cast<size_t>(b) * a.K;
-    for (int i = tid; i < n; i += kJoinThreads) {
-        const Cand c = join_found[i];
-        int above = 0;
-        for (int j = 0; j < n; ++j) above += better(join_found[j], c);
-        if (above < a.K) {
-            const unsigned long long flat = ~c.place;
-            const int w = static_cast<int>(flat / a.V);
-            a.scores_out[out + above] = static_cast<float>(score_of(c.s));
-            a.rows_out[out + above] = static_cast<int>(row0) + w;
-            a.tokens_out[out + above] =
-                static_cast<int>(flat - static_cast<unsigned long long>(w) * a.V);
-        }
+    auto put = [&](int, const Cand& c, int above) {
+        if (above >= a.K) return;
+        const unsigned long long flat = ~c.place;
+        const int w = static_cast<int>(flat / a.V);
+        a.scores_out[out + above] = static_cast<float>(score_of(c.s));
+        a.rows_out[out + above] = row0 + w;
+        a.tokens_out[out + above] =
+            static_cast<int>(flat - static_cast<unsigned long long>(w) * a.V);
+    };
+    Cand held[kHeld];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        held[h].s = held[h].place = 0;
+        if (tid + h * NT < all) held[h] = cand(tid + h * NT, key[h]);
     }
-    for (int i = n + tid; i < a.K; i += kJoinThreads) {
+    Cand lim;
+    lim.s = 1;
+    lim.place = 0;
+    if (all > 64) {
+        // The K-th best of the best ones of groups of four threads (of threads, where
+        // that might keep too many) is a bound.
+        Cand mine = held[0];
+#pragma unroll
+        for (int h = 1; h < kHeld; ++h)
+            if (better(held[h], mine)) mine = held[h];
+        for (int i = tid + kHeld * NT; i < all; i += NT) {
+            const Cand c = cand(i, keys[i]);
+            if (better(c, mine)) mine = c;
+        }
+        int n_tops = NT;
+        if (a.group == 4) {
+            n_tops = NT / 4;
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) {
+                Cand o;
+                o.s = __shfl_xor_sync(kFull, mine.s, off);
+                o.place = __shfl_xor_sync(kFull, mine.place, off);
+                if (better(o, mine)) mine = o;
+            }
+            if (lane % 4 == 0) tops[tid / 4] = mine;
+        } else {
+            tops[tid] = mine;
+        }
+        if (tid == 0) bound = lim;
+        __syncthreads();
+        rank_all<NT>(tops, n_tops, [&](int, const Cand& c, int above) {
+            if (c.s != 0 && above == a.K - 1) bound = c;
+        });
+        __syncthreads();
+        lim = bound;
+    }
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+        if (held[h].s != 0 && !better(lim, held[h])) kept_of[atomicAdd(&n_kept, 1)] = held[h];
+    for (int i = tid + kHeld * NT; i < all; i += NT) {
+        const Cand c = cand(i, keys[i]);
+        if (c.s != 0 && !better(lim, c)) kept_of[atomicAdd(&n_kept, 1)] = c;
+    }
+    __syncthreads();
+    const int n = n_kept;
+    rank_all<NT>(kept_of, n, put);
+    for (int i = n + tid; i < a.K; i += NT) {
         a.scores_out[out + i] = -INFINITY;
         a.rows_out[out + i] = -1;
         a.tokens_out[out + i] = -1;
@@ -337,26 +530,53 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a) {
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
 
-// Pieces of a row: one more than V asks for, for rows that start inside a vector.
-int pieces_of(int V) { return (V + 7 + kPiece - 1) / kPiece; }
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+// Tiles of a row (one more than V asks for, for rows that start inside a vector).
+int tiles_of(int V) { return (V + 7 + kTile - 1) / kTile; }
+
+// Tiles of a piece: one where the tiles do not fill the SMs with the twelve CTAs
+// that they have at work or waiting, more where they do, since every piece costs a
+// bound, two reductions and K candidates for the join.
+int piece_tiles(long long rows, int V, int sms) {
+    const long long n = rows * tiles_of(V) / (12LL * sms);
+    return n < 1 ? 1 : n > kMostTiles ? kMostTiles : static_cast<int>(n);
+}
 
 bool beam_shape_ok(int B, int W, int V, int K) {
     return B >= 0 && W >= 1 && W <= kMaxBeams && V >= 1 && K >= 1 && K <= kMaxBeams &&
            V <= (1 << 30) && static_cast<long long>(B) * W <= 65535 &&
-           static_cast<long long>(W) * pieces_of(V) * K <= 32768;
+           static_cast<long long>(W) * tiles_of(V) * K <= 131072;
 }
 
-// Candidates the join may have to keep: K threads' worth of them.
-size_t join_smem(int W, int V, int K) {
-    const int all = W * pieces_of(V) * K;
-    return static_cast<size_t>(K) * ((all + kJoinThreads - 1) / kJoinThreads) * sizeof(Cand);
-}
-size_t piece_smem(int K) {
-    return static_cast<size_t>(K) * (K <= 16 ? 4 : 1) * kEach * sizeof(unsigned long long);
+// Threads of the join: sixteen candidates to each at most, as far as that goes.
+int join_threads(int all) { return all <= 4096 ? 256 : 1024; }
+
+// Threads of a group whose best candidate counts: four, unless K groups' candidates
+// would not fit.
+int join_group(int all, int K) {
+    const int n = join_threads(all);
+    return static_cast<size_t>(K) * ((all + n - 1) / n) * 4 * sizeof(Cand) <= 128 * 1024 ? 4 : 1;
 }
 
+// Candidates the join may have to keep: all where they are few, else K groups'.
+size_t join_smem(int all, int K) {
+    const int n = join_threads(all);
+    const int most = all <= 64 ? all : K * ((all + n - 1) / n) * join_group(all, K);
+    return static_cast<size_t>(most) * sizeof(Cand);
+}
+// Logits a piece keeps: K groups' worth of its first tile, or K threads' of all.
+int piece_room(int K, int tiles) { return K * kEach * (tiles > 4 ? tiles : 4); }
+
+// (For pieces of one tile, the most that there can be, whatever the device.)
 size_t beam_bytes(int B, int W, int V, int K) {
-    const size_t n = static_cast<size_t>(B) * W * pieces_of(V);
+    const size_t n = static_cast<size_t>(B) * W * tiles_of(V);
     return (n * K * 8 + n * 8 + 255) / 256 * 256;
 }
 
@@ -391,7 +611,11 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
         return TREE_ATTN_ERR_ALIGN;
     if (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < beam_bytes(B, W, V, K))
         return TREE_ATTN_ERR_WORKSPACE;
-    const int pieces = pieces_of(V);
+    const int sms = sm_count();
+    if (sms == 0) return TREE_ATTN_ERR_CUDA;
+    const int tiles = piece_tiles(static_cast<long long>(B) * W, V, sms);
+    const int pieces = (tiles_of(V) + tiles - 1) / tiles;
+    const size_t smem = static_cast<size_t>(piece_room(K, tiles)) * sizeof(unsigned long long);
     PieceArgs p;
     p.logits = logits;
     p.batch_stride = batch_stride;
@@ -403,16 +627,21 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     p.V = V;
     p.K = K;
     p.pieces = pieces;
+    p.tiles = tiles;
+    p.room = piece_room(K, tiles);
     using Kernel = void (*)(PieceArgs);
     const Kernel kernel = dtype == 2   ? piece_kernel<float>
                           : dtype == 1 ? piece_kernel<__half>
                                        : piece_kernel<__nv_bfloat16>;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), piece_smem(K)) ||
-        !allow_smem(reinterpret_cast<const void*>(join_kernel), join_smem(W, V, K)))
+    const int all = W * pieces * K;
+    using Join = void (*)(JoinArgs);
+    const Join join = join_threads(all) == 256 ? join_kernel<256> : join_kernel<1024>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), smem) ||
+        !allow_smem(reinterpret_cast<const void*>(join), join_smem(all, K)))
         return TREE_ATTN_ERR_CUDA;
     const int rc = rc_of(launch_dependent(kernel, dim3(pieces, B * W), dim3(kThreads),
-                                          piece_smem(K), s, p));
+                                          smem, s, p));
     if (rc != TREE_ATTN_OK) return rc;
     JoinArgs j;
     j.keys = p.keys;
@@ -427,8 +656,8 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     j.K = K;
     j.pieces = pieces;
     j.eos = eos;
-    return rc_of(launch_dependent(join_kernel, dim3(B), dim3(kJoinThreads), join_smem(W, V, K), s,
-                                  j));
+    j.group = join_group(all, K);
+    return rc_of(launch_dependent(join, dim3(B), dim3(join_threads(all)), join_smem(all, K), s, j));
 }
 
 }  // extern "C"
