@@ -805,8 +805,8 @@ TREE_ATTN_API int tree_select_blocks(const uint16_t *q, const int8_t *bounds,
  * tree_attn_verify_fp8, where token t of sequence b sees, through KV head h,
  * the committed tokens of the pages blocks[b][t][h] instead of all, and the
  * tree tokens as before.
- *   blocks       int32 [B][T][Hkv][n_blocks] logical pages, -1 none; a page that
- *                is listed twice counts twice
+ *   blocks       int32 [B][T][Hkv][n_blocks] logical pages in any order (fastest
+ *                ascending), -1 none; a page that is listed twice counts once
  *   mask, mask_stride, parents, parents_stride   as tree_attn_verify_fp8
  *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN, _BAD_PAGE (a block outside
  *                the sequence, or a page outside the pool: it is skipped),

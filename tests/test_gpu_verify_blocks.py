@@ -102,7 +102,7 @@ class Case:
                 for h in range(self.Hkv):
                     ks = [self.tk[b, tree, h].double().cpu()]
                     vs = [self.tv[b, tree, h].double().cpu()]
-                    for j in self.blocks[b, t, h].tolist():
+                    for j in sorted(set(self.blocks[b, t, h].tolist())):  # twice counts once
                         if j >= 0:
                             n, page = min(self.P, L - j * self.P), self.rows[b][j]
                             ks.append(self.values(self.k, self.ks, page, h, n))
@@ -209,8 +209,58 @@ def test_a_value_that_is_no_number_reaches_the_rows_that_list_its_page():
     assert torch.equal(before[1, 0][:, keep], after[1, 0][:, keep])
 
 
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_all_pages_are_the_whole_cache_and_twice_counts_twice(fp8):
+def test_a_value_that_is_no_number_stays_with_the_tokens_that_see_it(fp8, d):
+    """Tokens that are worked on together, of which some list a page (see a tree token)
+    with such a value."""
+    c = Case([64], 1, 4, d, 16, 4, 2, fp8, seed=15)
+    c.parents = ints([-1, 0, 0, 2])
+    for t, pages in enumerate(([0, 1], [1, 2], [0, 2], [1, 3])):
+        c.blocks[0, t, 0] = ints(pages)
+    before, _ = c.call()
+    page = c.rows[0][2]
+    if fp8:
+        c.v[page, 0, 5, 3] = 0x7f
+    else:
+        c.v[page, 0, 5, 3] = math.nan
+        c.v[page, 0, 7, 9] = math.inf
+    after, _ = c.call()
+    bad = {1, 2}
+    for t in range(4):
+        assert torch.equal(before[0, t], after[0, t]) == (t not in bad)
+    assert bool(after[0, 1:3, :, 3].isnan().all()) and int(after[0, :, :, 3].isnan().sum()) == 8
+    keep = [i for i in range(d) if i not in (3, 9)]
+    assert torch.equal(before[0, 1:3][..., keep], after[0, 1:3][..., keep])
+    c.v[page, 0] = 0
+    before, _ = c.call()
+    c.tv[0, 2, 0, 11] = math.nan  # tokens 2 and 3 see it
+    after, _ = c.call()
+    assert torch.equal(before[0, :2], after[0, :2])
+    assert bool(after[0, 2:, :, 11].isnan().all())
+    keep = [i for i in range(d) if i != 11]
+    assert torch.equal(before[0, 2:][..., keep], after[0, 2:][..., keep])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_lists_over_many_pages_and_cache_rows_off_32_byte_boundaries(fp8):
+    P, L = 16, 20000 * 16 - 5  # pages of a sequence in more than one stretch
+    c = Case([L, 70], 1, 2, 64, P, 3, 6, fp8, seed=16)
+    c.blocks[0, :, 0] = ints([[0, 8191, 8192, 16383, 16384, 19999], [19999, 4, 8192, -1, 4, 12000],
+                              [7, 8, 9, 16384, 16385, 16386]])
+    c.check()
+    for name in "kv":  # the same pools 16 bytes further on
+        x = getattr(c, name)
+        room = torch.empty(x.nbytes + 16, dtype=torch.uint8, device="cuda")
+        y = room[16:].view(x.dtype).view(x.shape)
+        y.copy_(x)
+        setattr(c, name, y)
+    assert c.k.data_ptr() % 32 == 16
+    c.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_all_pages_are_the_whole_cache_and_twice_counts_once(fp8):
     c = Case([300, 17], 2, 4, 128, 16, 5, 19, fp8, seed=10)
     for b, L in enumerate(c.lens):
         nb = -(-L // 16)
@@ -223,6 +273,9 @@ def test_all_pages_are_the_whole_cache_and_twice_counts_twice(fp8):
     assert float((lse - want[1]).abs().max()) <= 1e-3
     c.blocks[0, :, :, 1] = 0
     c.blocks[1, :, :, 1] = 0
+    c.check()
+    c = Case([300], 2, 4, 128, 16, 1, 19, fp8, seed=20)
+    c.blocks[0, 0, 0, :4] = ints([3, 3, -1, 3])
     c.check()
 
 
