@@ -10,12 +10,13 @@
 // which the CTA joins through shared memory and the cluster through one another's, so
 // there is one launch and no workspace.
 //
-// K and V go from memory straight into the registers of the product: with
-// S^T = K Q^T and O^T = V^T P^T the keys (channels) are the 16-row side and the
-// query rows the 8-column side, so no half of a tile is padding for 8 rows, and
-// since the order of channels within the product is free, it is chosen so that 32 (K)
-// or 16 (V) contiguous bytes of a row are a lane's operands.  V's pairs of keys are put
-// together by byte permutes, P turns from result to operand by movmatrix.
+// K and V tiles come by asynchronous copies into a ring of each warp's own, K and V
+// apart, so that the next ones are on their way while one is worked on and no register
+// waits for them.  With S^T = K Q^T and O^T = V^T P^T the keys (channels) are the 16-row
+// side and the query rows the 8-column side, so no half of a tile is padding for 8 rows,
+// and since the order of channels within the product is free, it is chosen so that 32
+// (K) or 16 (V) contiguous bytes of a row are a lane's operands.  V's pairs of keys are
+// put together by byte permutes, P turns from result to operand by movmatrix.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,19 +31,26 @@
 #include "layout.h"
 #include "mma_sync.cuh"
 #include "ptx.cuh"
+#include "ptx_serving.cuh"
 
 namespace treeattn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kResident = 2;  // CTAs of an SM: 128 registers, and half of the shared memory
 constexpr int kTile = 16;        // keys
 constexpr int kWindow = 8192;    // pages of a sequence that are marked at a time
 constexpr int kMostEntries = 4096;
+constexpr int kFixed = 4;
 constexpr float kMove = 8.0f;    // binades a score may exceed its row's reference by
 // 8-bit cache: P's largest at a fresh reference is 2^kLift (2^8 above it is still
 // below fp16's 2^16).
 constexpr int kLift = 6;
 constexpr int kNoScale = -1000;  // no key has been seen
+constexpr float kLeast = 1.17549435e-38f;  // of a score unit: never 0, which would lose -inf
+constexpr float kLow = -3.0e38f; // a reference before the first key
 
 __device__ __forceinline__ void report(int32_t* status, int code) {
     if (status != nullptr) atomicCAS(status, 0, code);
@@ -62,7 +70,6 @@ struct Args {
     float* lse;
     int n_blocks, max_pages, mask_stride, parents_stride, Hq, Hkv, T, P, num_pages, row_blocks;
     int tokens, groups;  // of a unit, and units of a sequence's tokens
-    bool wide;           // K's rows begin on 32-byte boundaries
     float scale_log2;
     int32_t* status;
 };
@@ -86,68 +93,89 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 // One warp's running state for NT * 8 query rows; a lane holds columns 2c and
-// 2c + 1 of every column tile.
-template <int D, int NT>
+// 2c + 1 of every column tile.  Scores x come in units that make a logarithm to base 2
+// of them by a factor (> 0), a column's own (8-bit cache) or one for all.
+template <int D, bool FP8, int NT>
 struct State {
-    float m[NT][2];           // references, in units of log2
+    float unit[FP8 ? NT : 1][FP8 ? 2 : 1];
+    float m[NT][2];           // references, logarithms to base 2
     float l[NT][2];           // this lane's part of the sums
     float o[NT][D / 16][4];   // [column tile][channel tile]
+
+    __device__ __forceinline__ float factor(int n, int i) const {
+        return FP8 ? unit[FP8 ? n : 0][FP8 ? i : 0] : unit[0][0];
+    }
+    // Logarithms above the references.
+    __device__ __forceinline__ void above(float (&y)[NT][4], const float (&x)[NT][4]) const {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[n][i] = fmaf(x[n][i], factor(n, i & 1), -m[n][i & 1]);
+    }
 };
 
-// Moves the references where a score exceeds one by more than kMove.
-template <int D, int NT>
-__device__ __forceinline__ void follow(State<D, NT>& st, const float (&x)[NT][4]) {
-    bool move = false;
+// Scores to probabilities (in place), summed; the references are moved where a score
+// exceeds one by more than kMove.
+template <int D, bool FP8, int NT>
+__device__ __forceinline__ void exponents(State<D, FP8, NT>& st, float (&x)[NT][4]) {
+    float y[NT][4];
+    st.above(y, x);
+    float top = -INFINITY;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) move |= x[n][i] > st.m[n][i & 1] + kMove;
-    if (!__any_sync(kFull, move)) return;
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, y[n][i]);
+    if (__any_sync(kFull, top > kMove)) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float f[2];
+        for (int n = 0; n < NT; ++n) {
+            float f[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float t = fmaxf(x[n][i], x[n][i + 2]);
+            for (int i = 0; i < 2; ++i) {
+                float t = fmaxf(x[n][i], x[n][i + 2]);
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1)
-                t = fmaxf(t, __shfl_xor_sync(kFull, t, off));
-            t = fmaxf(t, st.m[n][i]);
-            f[i] = st.m[n][i] == -INFINITY ? 0.0f : ex2(st.m[n][i] - t);
-            st.m[n][i] = t;
-            st.l[n][i] *= f[i];
+                for (int off = 4; off < 32; off <<= 1)
+                    t = fmaxf(t, __shfl_xor_sync(kFull, t, off));
+                t = fmaxf(t * st.factor(n, i), st.m[n][i]);
+                f[i] = ex2(st.m[n][i] - t);
+                st.m[n][i] = t;
+                st.l[n][i] *= f[i];
+            }
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st.o[n][d][i] *= f[i & 1];
         }
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st.o[n][d][i] *= f[i & 1];
+        st.above(y, x);
     }
-}
-
-// Scores to probabilities (in place), summed.
-template <int D, int NT>
-__device__ __forceinline__ void exponents(State<D, NT>& st, float (&x)[NT][4]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float m = st.m[n][i & 1];
-            x[n][i] = ex2(x[n][i] - (m == -INFINITY ? 0.0f : m));
+            x[n][i] = ex2(y[n][i]);
             st.l[n][i & 1] += x[n][i];
         }
 }
 
 // O^T += V^T P^T for one tile of channels: an accumulator that takes all, or (columns
 // whose `mine` is false keep what they have) one apart that is added where it belongs.
-template <typename Mma>
-__device__ __forceinline__ void add_tile(float (&o)[4], const bool (&mine)[2], bool careful,
-                                         Mma mma) {
-    if (!careful) {
+template <bool CAREFUL, typename Mma>
+__device__ __forceinline__ void add_tile(float (&o)[4], const bool (&mine)[2], Mma mma) {
+    if (!CAREFUL) {
         mma(o);
     } else {
         float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -156,43 +184,6 @@ __device__ __forceinline__ void add_tile(float (&o)[4], const bool (&mine)[2], b
         for (int i = 0; i < 4; ++i)
             if (mine[i & 1]) o[i] += y[i];
     }
-}
-
-// O^T += V^T P^T for 16 keys of bf16 values, the probabilities (times f) as two
-// bf16 numbers: what one leaves out (2^-9) would be the largest error before the
-// result is rounded, and the product is not what bounds the kernel.
-template <int D, int NT>
-__device__ __forceinline__ void add_values_bf16(State<D, NT>& st, const float (&p)[NT][4],
-                                                const uint4 (&v)[4][D / 64], float f,
-                                                const bool (&mine)[NT][2], bool careful) {
-    uint32_t b[NT][2][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float y0 = p[n][2 * h] * f, y1 = p[n][2 * h + 1] * f;
-            const uint32_t hi = pack_bf16(y0, y1);
-            const uint32_t lo =
-                pack_bf16(y0 - __uint_as_float(hi << 16), y1 - __uint_as_float(hi & 0xffff0000u));
-            b[n][0][h] = ptx::transpose8(hi);
-            b[n][1][h] = ptx::transpose8(lo);
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t k0 = word(v[0][h], w), k1 = word(v[1][h], w);
-            const uint32_t k2 = word(v[2][h], w), k3 = word(v[3][h], w);
-            const uint32_t a0 = __byte_perm(k0, k1, 0x5410), a1 = __byte_perm(k0, k1, 0x7632);
-            const uint32_t a2 = __byte_perm(k2, k3, 0x5410), a3 = __byte_perm(k2, k3, 0x7632);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                add_tile(st.o[n][h * 4 + w], mine[n], careful, [&](float (&o)[4]) {
-                    ptx::mma_sync_bf16(o, a0, a1, a2, a3, b[n][0][0], b[n][0][1]);
-                    ptx::mma_sync_bf16(o, a0, a1, a2, a3, b[n][1][0], b[n][1][1]);
-                });
-        }
 }
 
 // Channel of o[.][t][0 or 1] (the next one for 2 and 3) of lane g.
@@ -217,58 +208,121 @@ __device__ __forceinline__ uint4 query(const uint8_t* q, int row, int j, int c) 
     return *reinterpret_cast<const uint4*>(q + query_at<D>(row, j, c));
 }
 
-// 32 bytes of a row (`wide`: on a 32-byte boundary).
-__device__ __forceinline__ void load32(uint4& lo, uint4& hi, const void* p, bool wide) {
-    if (wide) {
-        asm volatile(
-            "ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-            : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z),
-              "=r"(hi.w)
-            : "l"(p));
-    } else {
-        lo = ptx::ld_stream(p);
-        hi = ptx::ld_stream(static_cast<const uint8_t*>(p) + 16);
+// ---- tiles of 16 rows of RB bytes in shared memory, 16-byte chunks of a row moved
+// about so that a warp's reads of operands meet no bank twice
+
+// Where chunk ch of a row lies: for K a lane reads two next to one another, eight lanes
+// two rows; for V one of each of four even rows.
+template <int RB, bool V>
+__device__ __forceinline__ int chunk_at(int row, int ch) {
+    if (RB < 128) return row * RB + (V ? ch ^ ((row >> 1) & 3) : ch) * 16;
+    const int turn = V ? (row >> 1 & 3) << 1 : row & 1;
+    return row * RB + (ch & ~7) * 16 + ((ch & 7) ^ turn) * 16;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All of this thread's copies but the last N groups have arrived; then all lanes'.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    __syncwarp();
+}
+
+// One warp copies a tile, row r from row(r).
+template <int RB, bool V, typename Row>
+__device__ __forceinline__ void copy_tile(uint32_t dst, Row row) {
+    constexpr int kChunks = RB / 16;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kChunks * kTile / 32; ++i) {
+        const int id = lane + 32 * i, r = id / kChunks, ch = id % kChunks;
+        copy16(dst + chunk_at<RB, V>(r, ch), reinterpret_cast<const uint8_t*>(row(r)) + ch * 16);
     }
 }
 
-// 16 bf16 keys: the lane's vectors of rows g and g + 8 (16 channels of every 64), and
-// of the values of rows 2c, 2c + 1, 2c + 8, 2c + 9, by a function from row to address.
-template <int D, typename Row>
-__device__ __forceinline__ void load_keys_bf16(uint4 (&k)[2][D / 32], Row row, int g, int c,
-                                               bool wide) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-            load32(k[r][2 * j], k[r][2 * j + 1], row(g + 8 * r) + j * 64 + c * 16, wide);
-}
-template <int D, typename Row>
-__device__ __forceinline__ void load_values_bf16(uint4 (&v)[4][D / 64], Row row, int g, int c) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-            v[r][h] = ptx::ld_stream(row(2 * c + (r & 1) + 8 * (r >> 1)) + h * 64 + g * 8);
-}
-
-// The query operand in shared memory: [row][channels in the order of K's vectors].
+// S^T += K Q^T for 16 bf16 keys; the query operand in shared memory: [row][channels in
+// the order of K's chunks].
 template <int D, int NT>
-__device__ __forceinline__ void scores_bf16(float (&x)[NT][4], const uint4 (&k)[2][D / 32],
-                                            const uint8_t* q, int g, int c) {
+__device__ __forceinline__ void scores_bf16(float (&x)[NT][4], uint32_t k, const uint8_t* q, int g,
+                                            int c) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[n][i] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
+    for (int j = 0; j < D / 32; ++j) {
+        const int ch = j / 2 * 8 + 2 * c + (j & 1);
+        const uint4 k0 = ptx::ld_shared_v4(k + chunk_at<2 * D, false>(g, ch));
+        const uint4 k1 = ptx::ld_shared_v4(k + chunk_at<2 * D, false>(g + 8, ch));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             const uint4 y = query<D>(q, n * 8 + g, j, c);
-            ptx::mma_sync_bf16(x[n], k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y, y.x, y.y);
-            ptx::mma_sync_bf16(x[n], k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w, y.z, y.w);
+            ptx::mma_sync_bf16(x[n], k0.x, k1.x, k0.y, k1.y, y.x, y.y);
+            ptx::mma_sync_bf16(x[n], k0.z, k1.z, k0.w, k1.w, y.z, y.w);
         }
     }
 }
 
-// Keys past `live` seen by nobody.
+// A lane's 16 bytes of the values of rows 2c, 2c + 1, 2c + 8 and 2c + 9; those of keys
+// that are not there are cleared: a probability of 0 times a value that is no number is
+// no number.
+template <int RB>
+__device__ __forceinline__ void load_values(uint4 (&v)[4], uint32_t at, int ch, int c, int live) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+        v[r] = ptx::ld_shared_v4(at + chunk_at<RB, true>(row, ch));
+        if (row >= live) v[r] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// O^T += V^T P^T for 16 keys of bf16 values, the probabilities (times f) as two
+// bf16 numbers: what one leaves out (2^-9) would be the largest error before the
+// result is rounded, and the product is not what bounds the kernel.  SPREAD: a lane's
+// channels are 8 of every 64, else D / 8 in a row.
+template <bool CAREFUL, bool SPREAD, int D, bool FP8, int NT>
+__device__ __forceinline__ void add_values_bf16(State<D, FP8, NT>& st, const float (&p)[NT][4],
+                                                uint32_t v_at, int live, float f,
+                                                const bool (&mine)[NT][2], int g, int c) {
+    uint32_t b[NT][2][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float y0 = p[n][2 * h] * f, y1 = p[n][2 * h + 1] * f;
+            const uint32_t hi = pack_bf16(y0, y1);
+            const uint32_t lo =
+                pack_bf16(y0 - __uint_as_float(hi << 16), y1 - __uint_as_float(hi & 0xffff0000u));
+            b[n][0][h] = ptx::transpose8(hi);
+            b[n][1][h] = ptx::transpose8(lo);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+        uint4 v[4];
+        load_values<2 * D>(v, v_at, SPREAD ? 8 * h + g : g * (D / 64) + h, c, live);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t k0 = word(v[0], w), k1 = word(v[1], w);
+            const uint32_t k2 = word(v[2], w), k3 = word(v[3], w);
+            const uint32_t a0 = __byte_perm(k0, k1, 0x5410), a1 = __byte_perm(k0, k1, 0x7632);
+            const uint32_t a2 = __byte_perm(k2, k3, 0x5410), a3 = __byte_perm(k2, k3, 0x7632);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                add_tile<CAREFUL>(st.o[n][h * 4 + w], mine[n], [&](float (&o)[4]) {
+                    ptx::mma_sync_bf16(o, a0, a1, a2, a3, b[n][0][0], b[n][0][1]);
+                    ptx::mma_sync_bf16(o, a0, a1, a2, a3, b[n][1][0], b[n][1][1]);
+                });
+        }
+    }
+}
+
 template <int NT>
 __device__ __forceinline__ void hide(float (&x)[NT][4], int live, int g) {
 #pragma unroll
@@ -287,36 +341,20 @@ __device__ __forceinline__ void hide_others(float (&x)[NT][4], const bool (&mine
             if (!mine[n][i & 1]) x[n][i] = -INFINITY;
 }
 
-// A probability of 0 times a value that is no number is no number, so values of
-// keys that are not there are cleared.
-template <int N>
-__device__ __forceinline__ void clear_values(uint4 (&v)[4][N], int live, int c) {
+// Whether some accumulator of the warp is no finite number.
+template <int D, bool FP8, int NT>
+__device__ __forceinline__ bool not_finite(const State<D, FP8, NT>& st) {
+    float y = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (2 * c + (r & 1) + 8 * (r >> 1) >= live)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < N; ++h) v[r][h] = make_uint4(0u, 0u, 0u, 0u);
-}
-
-// Whether some value of the tile is no finite number.
-template <bool FP8, int N>
-__device__ __forceinline__ bool not_finite(const uint4 (&v)[4][N]) {
-    uint32_t bad = 0;
+        for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int h = 0; h < N; ++h)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t x = word(v[r][h], w);
-                bad |= FP8 ? ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u
-                           : ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
-            }
-    return __any_sync(kFull, bad != 0);
+            for (int i = 0; i < 4; ++i) y = fmaf(st.o[n][d][i], 0.0f, y);
+    return __any_sync(kFull, y != 0.0f);
 }
 
 // Exclusive prefix of v over the CTA; the sum in `total`.
-template <int W>
 __device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -331,22 +369,13 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
     int before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         const int s = sums[w];
         before += w < warp ? s : 0;
         total += s;
     }
     return before + x - v;
 }
-
-// Warps of a CTA and CTAs of an SM: as many registers as two column tiles need leave
-// room for twelve warps, one for sixteen.
-template <int NT>
-struct Shape {
-    static constexpr int kWarps = NT == 1 ? 8 : 4;
-    static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kResident = NT == 1 ? 2 : 3;
-};
 
 // One page of a unit's list: its row of the pools, its committed tokens, and (from
 // bit 8 on) the tokens of the unit that list it.
@@ -355,39 +384,319 @@ struct Entry {
     uint32_t live_who;
 };
 
-template <int D, int NT>
+template <int D, bool FP8, int NT>
 struct Smem {
-    static constexpr int kWarps = Shape<NT>::kWarps;
     static constexpr int R = 8 * NT;         // query rows
     static constexpr int kStride = D + 4;    // floats of a partial row
-    float part[kWarps][R][kStride];
+    static constexpr int RB = FP8 ? D : 2 * D;       // bytes of a cache row
+    static constexpr int kSlot = kTile * RB + (FP8 ? 16 : 0);  // K or V of a tile, and its scales
+    // Slots of a warp's ring: 8 and 12 KB (d = 128), which also hold a tile of tree tokens.
+    static constexpr int kSlots = FP8 ? 4 : 3;
+    union alignas(16) Warp {
+        uint8_t ring[kSlots * kSlot];
+        float rows[R][kStride];              // the warp's own, in the end
+    };
+    Warp warp[kWarps];
     float part_m[kWarps][R], part_l[kWarps][R];
-    float mine[R][kStride];                  // the CTA's own rows
+    alignas(16) float mine[R][kStride];      // the CTA's own rows
     float mine_m[R], mine_l[R];
-    float unit[R];                           // of a row's scores
-    uint8_t q[2][R * (2 * D + 64)];          // queries for the pages, and (8-bit) for the tree
+    float unit[R], inv[R];                   // 8-bit cache: a row's score unit, and its factor
+    alignas(16) uint8_t q[FP8 ? 2 : 1][R * (2 * D + 64)];  // queries for the pages, and (8-bit) for the tree
     int8_t seen[R][TREE_ATTN_MAX_T];         // tree tokens that each token sees
     int n_seen[R];
     int sums[kWarps];
-    Entry entries[1];                        // [tokens * n_blocks]
+    alignas(16) Entry entries[1];            // [tokens * n_blocks]
 
-    // Tokens that list a page, 16 bits each, while the list is made (`part` is used last).
+    // Tokens that list a page, 16 bits each, while the list is made.
     __device__ __forceinline__ uint32_t* marks() {
-        static_assert(sizeof(part) >= kWindow * 2, "a window's marks");
-        return reinterpret_cast<uint32_t*>(&part[0][0][0]);
+        static_assert(sizeof(warp) >= kWindow * 2, "a window's marks");
+        static_assert(sizeof(Warp::ring) >= 2 * kTile * 2 * D, "a tile of tree tokens");
+        return reinterpret_cast<uint32_t*>(&warp[0]);
     }
 };
 
+// What a warp has to know of its unit.
+struct Unit {
+    int b, hk, nt, per_token, rows, n_entries;
+    int turn, step;  // of the tiles it takes
+};
+
+// One warp's tiles, its rows left in shared memory.  A value that is no number must not
+// reach tokens that do not see it, but a product gives it to all.  So that the tiles need
+// not look, the warp looks at what it has in the end: if that is no number, it leaves
+// nothing (false) and takes its tiles again, CAREFUL.
+template <int D, bool FP8, int NT, bool CAREFUL>
+__device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, const Unit& u) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const unsigned everyone = (1u << u.nt) - 1u;
+    unsigned token[NT][2];  // of this lane's columns, as a bit
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = n * 8 + 2 * c + i;
+            token[n][i] = r < u.rows ? 1u << (r / u.per_token) : 0u;
+        }
+    State<D, FP8, NT> st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (FP8) st.unit[FP8 ? n : 0][FP8 ? i : 0] = sm.unit[n * 8 + 2 * c + i];
+    if (!FP8) st.unit[0][0] = fmaxf(fabsf(a.scale_log2), kLeast);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            st.m[n][i] = kLow;
+            st.l[n][i] = 0.0f;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st.o[n][d][i] = 0.0f;
+    }
+    int sref = kNoScale;  // 8-bit cache: accumulators are in units of 2^(sref - kLift)
+
+    // ---- pages
+    const int per_page = a.P / kTile, shift = __ffs(per_page) - 1;
+    const int tiles = u.n_entries << shift;
+    // Tile i: its first row in the pools, its keys, and who sees them.
+    using Sm = Smem<D, FP8, NT>;
+    constexpr int RB = Sm::RB;
+    const uint32_t ring = ptx::smem_u32(sm.warp[warp].ring);
+    // Tiles without keys are passed over.
+    auto live_at = [&](int i) {
+        return min(static_cast<int>(sm.entries[i >> shift].live_who & 255u) -
+                       (i & (per_page - 1)) * kTile,
+                   kTile);
+    };
+    auto skip = [&](int i) {
+        while (i < tiles && live_at(i) <= 0) i += u.step;
+        return i;
+    };
+    // The copies run ahead by the ring's slots: K of a tile, V of it, K of the next.
+    int ahead = skip(u.turn);
+    bool values = false;
+    auto copy_next = [&](uint32_t slot) {
+        if (ahead < tiles) {
+            const int page = sm.entries[ahead >> shift].page;
+            const size_t first = (static_cast<size_t>(page) * a.Hkv + u.hk) * a.P +
+                                 (ahead & (per_page - 1)) * kTile;
+            const uint8_t* base = static_cast<const uint8_t*>(a.kv[values]) + first * RB;
+            if (values)
+                copy_tile<RB, true>(slot, [&](int r) { return base + r * RB; });
+            else
+                copy_tile<RB, false>(slot, [&](int r) { return base + r * RB; });
+            if (FP8 && lane == 0) copy16(slot + kTile * RB, a.scales[values] + first);
+            if (values) ahead = skip(ahead + u.step);
+            values = !values;
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < Sm::kSlots; ++i) copy_next(ring + i * Sm::kSlot);
+    uint32_t slot = ring;
+    // The slot's copies have arrived; it has been read and is filled again.
+    auto arrive = [&] { copies_wait<Sm::kSlots - 1>(); };
+    auto refill = [&] {
+        __syncwarp();
+        copy_next(slot);
+        slot += Sm::kSlot;
+        if (slot == ring + Sm::kSlots * Sm::kSlot) slot = ring;
+    };
+    for (int i = skip(u.turn); i < tiles; i = skip(i + u.step)) {
+        const int live = live_at(i);
+        const unsigned seers = sm.entries[i >> shift].live_who >> 8;
+        float x[NT][4];
+        arrive();
+        if (!FP8) {
+            scores_bf16<D, NT>(x, slot, sm.q[0], g, c);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[n][j] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {  // 16 codes of a lane
+                const int ch = D / 64 * c + j;
+                const uint4 k0 = ptx::ld_shared_v4(slot + chunk_at<RB, false>(g, ch));
+                const uint4 k1 = ptx::ld_shared_v4(slot + chunk_at<RB, false>(g + 8, ch));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        f16x2_of_e4m3x4(word(k0, 2 * h + w), f[w][0], f[w][2]);
+                        f16x2_of_e4m3x4(word(k1, 2 * h + w), f[w][1], f[w][3]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const uint4 y = query<D>(sm.q[0], n * 8 + g, 2 * j + h, c);
+                        ptx::mma_sync_f16(x[n], f[0][0], f[0][1], f[0][2], f[0][3], y.x, y.y);
+                        ptx::mma_sync_f16(x[n], f[1][0], f[1][1], f[1][2], f[1][3], y.z, y.w);
+                    }
+                }
+            }
+            const float f0 = scale_of(ld_shared_u8(slot + kTile * RB + g));
+            const float f1 = scale_of(ld_shared_u8(slot + kTile * RB + g + 8));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[n][j] *= j < 2 ? f0 : f1;
+        }
+        refill();
+        if (live < kTile) hide<NT>(x, live, g);
+        bool mine[NT][2];
+        if (CAREFUL || seers != everyone) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) mine[n][j] = (token[n][j] & seers) != 0;
+            hide_others<NT>(x, mine);
+        }
+        exponents(st, x);
+        arrive();
+        if (!FP8) {
+            add_values_bf16<CAREFUL, true>(st, x, slot, live, 1.0f, mine, g, c);
+        } else {
+            const uint32_t s = slot + kTile * RB;
+            const int sv0 = g < live ? static_cast<int>(ld_shared_u8(s + g)) - 127 : kNoScale;
+            const int sv1 = g + 8 < live ? static_cast<int>(ld_shared_u8(s + g + 8)) - 127 : kNoScale;
+            // The unit of the accumulators follows the largest value scale.
+            const int top = __reduce_max_sync(kFull, max(sv0, sv1));
+            if (top > sref) {
+                const float f = sref == kNoScale ? 1.0f : pow2(sref - top);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) st.o[n][d][j] *= f;
+                sref = top;
+            }
+            const float pf0 = pow2(sv0 - sref + kLift), pf1 = pow2(sv1 - sref + kLift);
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                p[n][0] = ptx::transpose8(pack_f16(x[n][0] * pf0, x[n][1] * pf0));
+                p[n][1] = ptx::transpose8(pack_f16(x[n][2] * pf1, x[n][3] * pf1));
+            }
+            uint4 v[4];
+            if (D == 128) {
+                load_values<RB>(v, slot, g, c, live);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                    const uint2 y =
+                        ld_shared_v2(slot + chunk_at<RB, true>(row, g >> 1) + (g & 1) * 8);
+                    v[r] = row < live ? make_uint4(y.x, y.y, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                const uint32_t k0 = word(v[0], w), k1 = word(v[1], w);
+                const uint32_t k2 = word(v[2], w), k3 = word(v[3], w);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // channels 4w + 2h and the next
+                    uint32_t a0, a1, a2, a3;
+                    f16x2_of_e4m3x4(__byte_perm(k0, k1, h ? 0x7362 : 0x5140), a0, a1);
+                    f16x2_of_e4m3x4(__byte_perm(k2, k3, h ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        add_tile<CAREFUL>(st.o[n][2 * w + h], mine[n], [&](float (&o)[4]) {
+                            ptx::mma_sync_f16(o, a0, a1, a2, a3, p[n][0], p[n][1]);
+                        });
+                }
+            }
+        }
+        refill();
+    }
+
+    // ---- tree tokens (bf16 in either cache): tiles of one token each, behind the pages'
+    {
+        const size_t stride = static_cast<size_t>(a.Hkv) * D;
+        const size_t base = (static_cast<size_t>(u.b) * a.T * a.Hkv + u.hk) * D;
+        int turn = tiles;
+        for (int t = 0; t < u.nt; ++t) {
+            for (int i = 0; i < sm.n_seen[t]; i += kTile, ++turn) {
+                if (turn % u.step != u.turn) continue;
+                const int here = min(sm.n_seen[t] - i, kTile);
+                auto from = [&](const uint16_t* p, int r) {
+                    return p + base + sm.seen[t][i + min(r, here - 1)] * stride;
+                };
+                const uint32_t v_at = ring + kTile * 2 * D;
+                __syncwarp();  // (the ring has been read)
+                copy_tile<2 * D, false>(ring, [&](int r) { return from(a.tree[0], r); });
+                copy_tile<2 * D, true>(v_at, [&](int r) { return from(a.tree[1], r); });
+                copies_commit();
+                copies_wait<0>();
+                float x[NT][4];
+                scores_bf16<D, NT>(x, ring, sm.q[FP8 ? 1 : 0], g, c);
+                bool mine[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) mine[n][j] = (token[n][j] >> t & 1u) != 0;
+                    if (FP8) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[n][j] *= sm.inv[n * 8 + 2 * c + (j & 1)];
+                    }
+                }
+                hide<NT>(x, here, g);
+                hide_others<NT>(x, mine);
+                exponents(st, x);
+                if (FP8 && sref == kNoScale) sref = 0;
+                // (the accumulators' order of channels)
+                add_values_bf16<CAREFUL, !FP8>(st, x, v_at, here, FP8 ? pow2(kLift - sref) : 1.0f,
+                                               mine, g, c);
+            }
+        }
+    }
+    if (!CAREFUL && u.nt > 1 && not_finite(st)) return false;
+
+    // ---- this warp's rows to shared memory, where its ring was
+    copies_wait<0>();
+    const float unit_of = FP8 && sref != kNoScale ? pow2(sref - kLift) : 1.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float l = st.l[n][i];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(kFull, l, off);
+            const int r = n * 8 + 2 * c + i;
+            if (g == 0) {
+                sm.part_m[warp][r] = st.m[n][i];
+                sm.part_l[warp][r] = l;
+            }
+#pragma unroll
+            for (int d = 0; d < D / 16; d += 2) {
+                const int ch = FP8 ? channel_fp8<D>(d, g) : channel_bf16<D>(d, g);
+                *reinterpret_cast<float4*>(&sm.warp[warp].rows[r][ch]) =
+                    make_float4(st.o[n][d][i] * unit_of, st.o[n][d][i + 2] * unit_of,
+                                st.o[n][d + 1][i] * unit_of, st.o[n][d + 1][i + 2] * unit_of);
+            }
+        }
+    return true;
+}
+
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kResident)
-    blocks_kernel(const Args a) {
+__device__ __noinline__ void warp_rows_again(const Args& a, Smem<D, FP8, NT>& sm, const Unit& u) {
+    warp_rows<D, FP8, NT, true>(a, sm, u);
+}
+
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(kThreads, kResident)
+    blocks_kernel(const __grid_constant__ Args a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads, R = 8 * NT;
-    Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(smem_raw);
+    constexpr int R = 8 * NT;
+    Smem<D, FP8, NT>& sm = *reinterpret_cast<Smem<D, FP8, NT>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, c = lane & 3;
     const int S = static_cast<int>(ptx::cluster_size());
     const int rank = static_cast<int>(ptx::cluster_rank());
     // Units in the order (sequence, KV head, tokens, rows of a wide group).
@@ -401,7 +710,6 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kResident)
     const int nt = min(a.tokens, a.T - t0);
     const int per_token = min(G - rb * R, R);  // rows
     const int rows = nt * per_token;
-    const unsigned everyone = (1u << nt) - 1u;
     // Row r: head rb * R + r % per_token of token t0 + r / per_token.
     auto row_of = [&](int r) {
         return (static_cast<size_t>(b) * a.T + t0 + r / per_token) * a.Hq +
@@ -445,7 +753,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kResident)
             n += ok;
         }
         as_is = __syncthreads_and(ascends);
-        block_scan<kWarps>(n, sm.sums, n_entries);
+        block_scan(n, sm.sums, n_entries);
     }
     if (!as_is) {
         n_entries = 0;
@@ -469,7 +777,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kResident)
                 const uint32_t m = i0 + tid < (width + 1) / 2 ? marks[i0 + tid] : 0u;
                 const unsigned lo = m & 0xffffu, hi = m >> 16;
                 int total;
-                int at = n_entries + block_scan<kWarps>((lo != 0) + (hi != 0), sm.sums, total);
+                int at = n_entries + block_scan((lo != 0) + (hi != 0), sm.sums, total);
                 const int j = w0 + 2 * (i0 + tid);
                 if (lo != 0) sm.entries[at++] = entry(j, lo);
                 if (hi != 0) sm.entries[at] = entry(j + 1, hi);
@@ -513,8 +821,14 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kResident)
     constexpr int kVecs = D / 8;  // 16-byte vectors of a row, one to a lane
     for (int r = tid / kVecs; r < R; r += kThreads / kVecs) {
         const int i = tid % kVecs;
-        const uint4 x = r < rows ? *reinterpret_cast<const uint4*>(a.q + row_of(r) * D + i * 8)
-                                 : make_uint4(0u, 0u, 0u, 0u);
+        uint4 x = r < rows ? *reinterpret_cast<const uint4*>(a.q + row_of(r) * D + i * 8)
+                           : make_uint4(0u, 0u, 0u, 0u);
+        if (a.scale_log2 < 0.0f) {  // score units are positive
+            x.x ^= 0x80008000u;
+            x.y ^= 0x80008000u;
+            x.z ^= 0x80008000u;
+            x.w ^= 0x80008000u;
+        }
         // Vector i holds channels 8 i: in 64 channels 16 to a lane, or D / 4 to a lane.
         const int bf = query_at<D>(r, i / 8 * 2 + (i & 1), i % 8 / 2);
         if (FP8) {
@@ -537,311 +851,41 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kResident)
             *reinterpret_cast<uint4*>(sm.q[0] + query_at<D>(r, i % (D / 32), i / (D / 32))) =
                 make_uint4(y[0], y[1], y[2], y[3]);
             *reinterpret_cast<uint4*>(sm.q[1] + bf) = x;
-            if (i == 0) sm.unit[r] = pow2(e) * a.scale_log2;
+            if (i == 0) {
+                sm.unit[r] = fmaxf(pow2(e) * fabsf(a.scale_log2), kLeast);
+                sm.inv[r] = inv;
+            }
         } else {
             *reinterpret_cast<uint4*>(sm.q[0] + bf) = x;
         }
     }
 
-    State<D, NT> st;
-    unsigned token[NT][2];  // of this lane's columns, as a bit
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            st.m[n][i] = -INFINITY;
-            st.l[n][i] = 0.0f;
-            const int r = n * 8 + 2 * c + i;
-            token[n][i] = r < rows ? 1u << (r / per_token) : 0u;
-        }
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st.o[n][d][i] = 0.0f;
-    }
-    int sref = kNoScale;  // 8-bit cache: accumulators are in units of 2^(sref - kLift)
+    Unit u;
+    u.b = b;
+    u.hk = hk;
+    u.nt = nt;
+    u.per_token = per_token;
+    u.rows = rows;
+    u.n_entries = n_entries;
+    u.step = S * kWarps;
+    u.turn = rank * kWarps + warp;
     __syncthreads();
-
-    // ---- pages
-    const int per_page = a.P / kTile, shift = __ffs(per_page) - 1;
-    const int tiles = n_entries << shift;
-    const int step = S * kWarps;
-    const int w0 = rank * kWarps + warp;
-    // Tile i: its first row in the pools, its keys, and who sees them.
-    int live = 0, at = 0;
-    unsigned who = 0;
-    size_t first = 0;
-    auto next = [&](int from) {
-        live = 0;
-        for (at = from; at < tiles; at += step) {
-            const Entry e = sm.entries[at >> shift];
-            const int off = (at & (per_page - 1)) * kTile;
-            live = min(max(static_cast<int>(e.live_who & 255u) - off, 0), kTile);
-            who = e.live_who >> 8;
-            first = (static_cast<size_t>(e.page) * a.Hkv + hk) * a.P + off;
-            if (live > 0) break;  // (tiles without keys are passed over)
-        }
-    };
-    next(w0);
-    if (!FP8) {
-        uint4 k[2][D / 32], v[4][D / 64];
-        auto load_k = [&] {
-            const uint16_t* base = static_cast<const uint16_t*>(a.kv[0]) + first * D;
-            load_keys_bf16<D>(k, [&](int r) { return base + r * D; }, g, c, a.wide);
-        };
-        auto load_v = [&] {
-            const uint16_t* base = static_cast<const uint16_t*>(a.kv[1]) + first * D;
-            load_values_bf16<D>(v, [&](int r) { return base + r * D; }, g, c);
-        };
-        if (live > 0) {
-            load_k();
-            load_v();
-        }
-        while (live > 0) {
-            float x[NT][4];
-            scores_bf16<D, NT>(x, k, sm.q[0], g, c);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[n][j] *= a.scale_log2;
-            const int now = live;
-            const unsigned seers = who;
-            next(at + step);
-            if (live > 0) load_k();
-            if (now < kTile) {
-                hide<NT>(x, now, g);
-                clear_values(v, now, c);
-            }
-            bool mine[NT][2], careful = false;
-            if (seers != everyone) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) mine[n][i] = (token[n][i] & seers) != 0;
-                hide_others<NT>(x, mine);
-                careful = not_finite<false>(v);
-            }
-            follow(st, x);
-            exponents(st, x);
-            add_values_bf16<D, NT>(st, x, v, 1.0f, mine, careful);
-            if (live > 0) load_v();
-        }
-    } else {
-        constexpr int NC = D / 64;  // 16-byte vectors of a lane
-        uint4 k[2][NC];
-        uint4 v[4][1];
-        uint32_t s[2][2];  // [K, V] scale bytes of keys g and g + 8
-        auto load_k = [&] {
-            const uint8_t* base = static_cast<const uint8_t*>(a.kv[0]) + first * D + c * (D / 4);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if (D == 128)
-                    load32(k[r][0], k[r][NC - 1], base + (g + 8 * r) * D, a.wide);
-                else
-                    k[r][0] = ptx::ld_stream(base + (g + 8 * r) * D);
-                s[0][r] = a.scales[0][first + g + 8 * r];
-            }
-        };
-        auto load_v = [&] {
-            const uint8_t* base = static_cast<const uint8_t*>(a.kv[1]) + first * D + g * (D / 8);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint8_t* p = base + (2 * c + (r & 1) + 8 * (r >> 1)) * D;
-                if (D == 128) {
-                    v[r][0] = ptx::ld_stream(p);
-                } else {
-                    const uint2 y = ptx::ld_stream8(p);
-                    v[r][0] = make_uint4(y.x, y.y, 0u, 0u);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) s[1][r] = a.scales[1][first + g + 8 * r];
-        };
-        float rf[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) rf[n][i] = sm.unit[n * 8 + 2 * c + i];
-        if (live > 0) {
-            load_k();
-            load_v();
-        }
-        while (live > 0) {
-            float x[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[n][j] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NC; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {  // eight codes of a lane
-                    uint32_t f[2][4];
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        f16x2_of_e4m3x4(word(k[0][j], 2 * h + w), f[w][0], f[w][2]);
-                        f16x2_of_e4m3x4(word(k[1][j], 2 * h + w), f[w][1], f[w][3]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint4 y = query<D>(sm.q[0], n * 8 + g, 2 * j + h, c);
-                        ptx::mma_sync_f16(x[n], f[0][0], f[0][1], f[0][2], f[0][3], y.x, y.y);
-                        ptx::mma_sync_f16(x[n], f[1][0], f[1][1], f[1][2], f[1][3], y.z, y.w);
-                    }
-                }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[n][j] = x[n][j] * scale_of(s[0][j >> 1]) * rf[n][j & 1];
-            const int now = live;
-            const unsigned seers = who;
-            next(at + step);
-            if (live > 0) load_k();
-            int sv[2] = {static_cast<int>(s[1][0]) - 127, static_cast<int>(s[1][1]) - 127};
-            if (now < kTile) {
-                hide<NT>(x, now, g);
-                if (g >= now) sv[0] = kNoScale;
-                if (g + 8 >= now) sv[1] = kNoScale;
-                clear_values(v, now, c);
-            }
-            bool mine[NT][2], careful = false;
-            if (seers != everyone) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) mine[n][i] = (token[n][i] & seers) != 0;
-                hide_others<NT>(x, mine);
-                careful = not_finite<true>(v);
-            }
-            follow(st, x);
-            exponents(st, x);
-            // The unit of the accumulators follows the largest value scale.
-            const int top = __reduce_max_sync(kFull, max(sv[0], sv[1]));
-            if (top > sref) {
-                const float f = sref == kNoScale ? 1.0f : pow2(sref - top);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) st.o[n][d][j] *= f;
-                sref = top;
-            }
-            const float pf[2] = {pow2(sv[0] - sref + kLift), pow2(sv[1] - sref + kLift)};
-            uint32_t p[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    p[n][h] = ptx::transpose8(
-                        pack_f16(x[n][2 * h] * pf[h], x[n][2 * h + 1] * pf[h]));
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                const uint32_t k0 = word(v[0][0], w), k1 = word(v[1][0], w);
-                const uint32_t k2 = word(v[2][0], w), k3 = word(v[3][0], w);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {  // channels 4w + 2h and the next
-                    uint32_t a0, a1, a2, a3;
-                    f16x2_of_e4m3x4(__byte_perm(k0, k1, h ? 0x7362 : 0x5140), a0, a1);
-                    f16x2_of_e4m3x4(__byte_perm(k2, k3, h ? 0x7362 : 0x5140), a2, a3);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        add_tile(st.o[n][2 * w + h], mine[n], careful, [&](float (&o)[4]) {
-                            ptx::mma_sync_f16(o, a0, a1, a2, a3, p[n][0], p[n][1]);
-                        });
-                }
-            }
-            if (live > 0) load_v();
-        }
-    }
-
-    // ---- tree tokens (bf16 in either cache): tiles of one token each, behind the pages'
-    {
-        const size_t stride = static_cast<size_t>(a.Hkv) * D;
-        const size_t base = (static_cast<size_t>(b) * a.T * a.Hkv + hk) * D;
-        int turn = tiles;
-        for (int t = 0; t < nt; ++t) {
-            for (int i = 0; i < sm.n_seen[t]; i += kTile, ++turn) {
-                if (turn % step != w0) continue;
-                const int here = min(sm.n_seen[t] - i, kTile);
-                auto from = [&](const uint16_t* p, int r) {
-                    return p + base + sm.seen[t][i + min(r, here - 1)] * stride;
-                };
-                uint4 k[2][D / 32], v[4][D / 64];
-                load_keys_bf16<D>(k, [&](int r) { return from(a.tree[0], r); }, g, c, a.wide);
-                // The value operand's channels follow the accumulators' order.
-                if (FP8) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint16_t* p =
-                            from(a.tree[1], 2 * c + (r & 1) + 8 * (r >> 1)) + g * (D / 8);
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h) v[r][h] = ptx::ld_stream(p + 8 * h);
-                    }
-                } else {
-                    load_values_bf16<D>(v, [&](int r) { return from(a.tree[1], r); }, g, c);
-                }
-                float x[NT][4];
-                scores_bf16<D, NT>(x, k, sm.q[FP8 ? 1 : 0], g, c);
-                bool mine[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[n][j] *= a.scale_log2;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) mine[n][j] = (token[n][j] >> t & 1u) != 0;
-                }
-                hide<NT>(x, here, g);
-                hide_others<NT>(x, mine);
-                clear_values(v, here, c);
-                follow(st, x);
-                exponents(st, x);
-                if (FP8 && sref == kNoScale) sref = 0;
-                add_values_bf16<D, NT>(st, x, v, FP8 ? pow2(kLift - sref) : 1.0f, mine,
-                                       nt > 1 && not_finite<false>(v));
-            }
-        }
-    }
-
-    // ---- this warp's rows to shared memory
-    const float unit_of = FP8 && sref != kNoScale ? pow2(sref - kLift) : 1.0f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float l = st.l[n][i];
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(kFull, l, off);
-            const int r = n * 8 + 2 * c + i;
-            if (g == 0) {
-                sm.part_m[warp][r] = st.m[n][i];
-                sm.part_l[warp][r] = l;
-            }
-#pragma unroll
-            for (int d = 0; d < D / 16; d += 2) {
-                const int ch = FP8 ? channel_fp8<D>(d, g) : channel_bf16<D>(d, g);
-                *reinterpret_cast<float4*>(&sm.part[warp][r][ch]) =
-                    make_float4(st.o[n][d][i] * unit_of, st.o[n][d][i + 2] * unit_of,
-                                st.o[n][d + 1][i] * unit_of, st.o[n][d + 1][i + 2] * unit_of);
-            }
-        }
+    if (!warp_rows<D, FP8, NT, false>(a, sm, u)) warp_rows_again<D, FP8, NT>(a, sm, u);
     __syncthreads();
     // ---- the CTA's rows, then (S > 1) the cluster's: four channels to a thread
     constexpr int kQuads = D / 4;
     for (int i = tid; i < rows * kQuads; i += kThreads) {
         const int r = i / kQuads, d = i % kQuads * 4;
-        float m = -INFINITY;
+        float m = kLow;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.part_m[w][r]);
         float l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float mw = sm.part_m[w][r];
-            if (mw == -INFINITY) continue;
-            const float f = ex2(mw - m);
+            const float f = ex2(sm.part_m[w][r] - m);
             l += f * sm.part_l[w][r];
-            const float4 y = *reinterpret_cast<const float4*>(&sm.part[w][r][d]);
+            const float4 y = *reinterpret_cast<const float4*>(&sm.warp[w].rows[r][d]);
             o.x += f * y.x;
             o.y += f * y.y;
             o.z += f * y.z;
@@ -861,13 +905,11 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kResident)
         const int r = i / kQuads, d = i % kQuads * 4;
         const uint32_t at_m = ptx::smem_u32(&sm.mine_m[r]), at_l = ptx::smem_u32(&sm.mine_l[r]);
         const uint32_t at_o = ptx::smem_u32(&sm.mine[r][d]);
-        float m = -INFINITY, l = 0.0f;
+        float m = kLow, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int s = 0; s < S; ++s) m = fmaxf(m, ptx::ld_cluster(ptx::map_rank(at_m, s)));
         for (int s = 0; s < S; ++s) {
-            const float ms = ptx::ld_cluster(ptx::map_rank(at_m, s));
-            if (ms == -INFINITY) continue;
-            const float f = ex2(ms - m);
+            const float f = ex2(ptx::ld_cluster(ptx::map_rank(at_m, s)) - m);
             l += f * ptx::ld_cluster(ptx::map_rank(at_l, s));
             const float4 y = ptx::ld_cluster_v4(ptx::map_rank(at_o, s));
             o.x += f * y.x;
@@ -875,7 +917,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kResident)
             o.z += f * y.z;
             o.w += f * y.w;
         }
-        const bool none = m == -INFINITY;
+        const bool none = l == 0.0f;  // no key at all
         const float inv = none ? 0.0f : 1.0f / l;
         const size_t row = row_of(r);
         *reinterpret_cast<uint2*>(a.out + row * D + d) =
@@ -889,8 +931,7 @@ int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ER
 
 template <int D, bool FP8, int NT>
 int launch(const Args& a, long long units, int sms, cudaStream_t stream) {
-    using Sh = Shape<NT>;
-    const size_t smem = sizeof(Smem<D, NT>) +
+    const size_t smem = sizeof(Smem<D, FP8, NT>) +
                         static_cast<size_t>(a.tokens) * a.n_blocks * sizeof(Entry);
     const auto kernel = blocks_kernel<D, FP8, NT>;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -899,15 +940,24 @@ int launch(const Args& a, long long units, int sms, cudaStream_t stream) {
         cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return TREE_ATTN_ERR_CUDA;
-    // CTAs of a cluster: as many as the SMs hold at once, while each warp has a tile.
+    // CTAs of a cluster: those that take the least time when the SMs take all CTAs in
+    // waves, and a CTA its tiles and kFixed tiles' worth of beginning and end.
     const long long most = a.n_blocks < a.max_pages ? a.n_blocks : a.max_pages;
-    const long long tiles = most * (a.P / kTile) + (a.T + kTile - 1) / kTile;
+    const long long tiles = most * (a.P / kTile) * (a.tokens + 1) / 2 + a.tokens;
+    const long long slots = static_cast<long long>(kResident) * sms;
     int S = 1;
-    while (S < 16 && 2 * S * units <= static_cast<long long>(Sh::kResident) * sms &&
-           tiles >= 2LL * S * Sh::kWarps)
-        S *= 2;
+    long long best = -1;
+    for (int s = 1; s <= 16; s *= 2) {
+        const long long waves = (units * s + slots - 1) / slots;
+        const long long each = (tiles + s * kWarps - 1) / (s * kWarps);
+        const long long cost = waves * (each + kFixed);
+        if (best < 0 || cost < best) {
+            best = cost;
+            S = s;
+        }
+    }
     return rc_of(launch_cluster(kernel, dim3(static_cast<unsigned>(units * S)),
-                                dim3(Sh::kThreads), smem, S, stream, a));
+                                dim3(kThreads), smem, S, stream, a));
 }
 
 }  // namespace
@@ -984,7 +1034,6 @@ extern "C" int tree_attn_verify_blocks(
     a.row_blocks = row_blocks;
     a.tokens = tokens;
     a.groups = groups;
-    a.wide = ptr_aligned(k_pages, 32) && ptr_aligned(tree_k, 32);
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
     a.status = status;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
