@@ -23,6 +23,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/tree_attn.h"
 #include "cluster.cuh"
@@ -41,7 +42,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kResident = 2;  // CTAs of an SM: 128 registers, and half of the shared memory
 constexpr int kTile = 16;        // keys
-constexpr int kWindow = 8192;    // pages of a sequence that are marked at a time
+constexpr int kWindow = 4096;    // pages of a sequence that are marked at a time
 constexpr int kMostEntries = 4096;
 constexpr int kFixed = 4;
 constexpr float kMove = 8.0f;    // binades a score may exceed its row's reference by
@@ -70,6 +71,8 @@ struct Args {
     float* lse;
     int n_blocks, max_pages, mask_stride, parents_stride, Hq, Hkv, T, P, num_pages, row_blocks;
     int tokens, groups;  // of a unit, and units of a sequence's tokens
+    int B;
+    bool longest_first;
     float scale_log2;
     int32_t* status;
 };
@@ -278,7 +281,11 @@ __device__ __forceinline__ void load_values(uint4 (&v)[4], uint32_t at, int ch, 
     for (int r = 0; r < 4; ++r) {
         const int row = 2 * c + (r & 1) + 8 * (r >> 1);
         v[r] = ptx::ld_shared_v4(at + chunk_at<RB, true>(row, ch));
-        if (row >= live) v[r] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (live < kTile) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (2 * c + (r & 1) + 8 * (r >> 1) >= live) v[r] = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -377,10 +384,10 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
     return before + x - v;
 }
 
-// One page of a unit's list: its row of the pools, its committed tokens, and (from
-// bit 8 on) the tokens of the unit that list it.
+// One page of a unit's list: its first row of the pools (for the unit's KV head), its
+// committed tokens, and (from bit 8 on) the tokens of the unit that list it.
 struct Entry {
-    int page;
+    int row;
     uint32_t live_who;
 };
 
@@ -407,9 +414,9 @@ struct Smem {
     int sums[kWarps];
     alignas(16) Entry entries[1];            // [tokens * n_blocks]
 
-    // Tokens that list a page, 16 bits each, while the list is made.
+    // Tokens that list a page, 16 bits each, and the pages' rows, while the list is made.
     __device__ __forceinline__ uint32_t* marks() {
-        static_assert(sizeof(warp) >= kWindow * 2, "a window's marks");
+        static_assert(sizeof(warp) >= kWindow * (2 + 4), "a window's marks and rows");
         static_assert(sizeof(Warp::ring) >= 2 * kTile * 2 * D, "a tile of tree tokens");
         return reinterpret_cast<uint32_t*>(&warp[0]);
     }
@@ -460,55 +467,56 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
     int sref = kNoScale;  // 8-bit cache: accumulators are in units of 2^(sref - kLift)
 
     // ---- pages
+    // Tile i is rows i % (P / 16) * 16 of page i / (P / 16); a warp takes every step-th,
+    // step being a multiple of 8 and so of a page's tiles: the same rows of all its pages.
     const int per_page = a.P / kTile, shift = __ffs(per_page) - 1;
     const int tiles = u.n_entries << shift;
-    // Tile i: its first row in the pools, its keys, and who sees them.
+    const int off = (u.turn & (per_page - 1)) * kTile;
+    const int e0 = u.turn >> shift, e_step = u.step >> shift;
     using Sm = Smem<D, FP8, NT>;
     constexpr int RB = Sm::RB;
     const uint32_t ring = ptx::smem_u32(sm.warp[warp].ring);
     // Tiles without keys are passed over.
-    auto live_at = [&](int i) {
-        return min(static_cast<int>(sm.entries[i >> shift].live_who & 255u) -
-                       (i & (per_page - 1)) * kTile,
-                   kTile);
-    };
-    auto skip = [&](int i) {
-        while (i < tiles && live_at(i) <= 0) i += u.step;
-        return i;
+    auto live_at = [&](int e) { return static_cast<int>(sm.entries[e].live_who & 255u) - off; };
+    auto skip = [&](int e) {
+        while (e < u.n_entries && live_at(e) <= 0) e += e_step;
+        return e;
     };
     // The copies run ahead by the ring's slots: K of a tile, V of it, K of the next.
-    int ahead = skip(u.turn);
-    bool values = false;
-    auto copy_next = [&](uint32_t slot) {
-        if (ahead < tiles) {
-            const int page = sm.entries[ahead >> shift].page;
-            const size_t first = (static_cast<size_t>(page) * a.Hkv + u.hk) * a.P +
-                                 (ahead & (per_page - 1)) * kTile;
-            const uint8_t* base = static_cast<const uint8_t*>(a.kv[values]) + first * RB;
-            if (values)
-                copy_tile<RB, true>(slot, [&](int r) { return base + r * RB; });
-            else
-                copy_tile<RB, false>(slot, [&](int r) { return base + r * RB; });
-            if (FP8 && lane == 0) copy16(slot + kTile * RB, a.scales[values] + first);
-            if (values) ahead = skip(ahead + u.step);
-            values = !values;
+    int ahead = skip(e0);
+    auto copy_next = [&](uint32_t slot, auto values) {
+        constexpr bool V = decltype(values)::value;
+        if (ahead < u.n_entries) {
+            const int first = sm.entries[ahead].row + off;
+            const uint8_t* base =
+                static_cast<const uint8_t*>(a.kv[V ? 1 : 0]) + static_cast<size_t>(first) * RB;
+            copy_tile<RB, V>(slot, [&](int r) { return base + r * RB; });
+            if (FP8 && lane == 0) copy16(slot + kTile * RB, a.scales[V ? 1 : 0] + first);
+            if (V) ahead = skip(ahead + e_step);
         }
         copies_commit();
     };
+    using std::bool_constant;
 #pragma unroll
-    for (int i = 0; i < Sm::kSlots; ++i) copy_next(ring + i * Sm::kSlot);
+    for (int i = 0; i < Sm::kSlots; i += 2) {
+        copy_next(ring + i * Sm::kSlot, bool_constant<false>());
+        if (i + 1 < Sm::kSlots) copy_next(ring + (i + 1) * Sm::kSlot, bool_constant<true>());
+    }
+    // What is kSlots further on than K: K again, or V.
+    using AfterK = bool_constant<Sm::kSlots % 2 != 0>;
+    using AfterV = bool_constant<Sm::kSlots % 2 == 0>;
     uint32_t slot = ring;
     // The slot's copies have arrived; it has been read and is filled again.
     auto arrive = [&] { copies_wait<Sm::kSlots - 1>(); };
-    auto refill = [&] {
+    auto refill = [&](auto values) {
         __syncwarp();
-        copy_next(slot);
+        copy_next(slot, values);
         slot += Sm::kSlot;
         if (slot == ring + Sm::kSlots * Sm::kSlot) slot = ring;
     };
-    for (int i = skip(u.turn); i < tiles; i = skip(i + u.step)) {
-        const int live = live_at(i);
-        const unsigned seers = sm.entries[i >> shift].live_who >> 8;
+    for (int e = skip(e0); e < u.n_entries; e = skip(e + e_step)) {
+        const int live = min(live_at(e), kTile);
+        const unsigned seers = sm.entries[e].live_who >> 8;
         float x[NT][4];
         arrive();
         if (!FP8) {
@@ -546,7 +554,7 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[n][j] *= j < 2 ? f0 : f1;
         }
-        refill();
+        refill(AfterK());
         if (live < kTile) hide<NT>(x, live, g);
         bool mine[NT][2];
         if (CAREFUL || seers != everyone) {
@@ -612,7 +620,7 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
                 }
             }
         }
-        refill();
+        refill(AfterV());
     }
 
     // ---- tree tokens (bf16 in either cache): tiles of one token each, behind the pages'
@@ -705,7 +713,27 @@ __global__ void __launch_bounds__(kThreads, kResident)
     unit /= a.row_blocks;
     const int t0 = unit % a.groups * a.tokens;
     unit /= a.groups;
-    const int hk = unit % a.Hkv, b = unit / a.Hkv;
+    const int hk = unit % a.Hkv;
+    int b = unit / a.Hkv;
+    if (a.longest_first) {  // b-th by length (units that come late should end soon)
+        int* lens = reinterpret_cast<int*>(sm.entries);
+        int* found = sm.sums;
+        const int mine = tid < a.B ? a.lens[tid] : 0;
+        if (tid < a.B) lens[tid] = mine;
+        __syncthreads();
+        if (tid < a.B) {
+            int before = 0;
+#pragma unroll 8
+            for (int i = 0; i < a.B; ++i) {
+                const int other = lens[i];
+                before += other > mine || (other == mine && i < tid);
+            }
+            if (before == b) *found = tid;
+        }
+        __syncthreads();
+        b = *found;
+        __syncthreads();
+    }
     const int G = a.Hq / a.Hkv;
     const int nt = min(a.tokens, a.T - t0);
     const int per_token = min(G - rb * R, R);  // rows
@@ -716,40 +744,59 @@ __global__ void __launch_bounds__(kThreads, kResident)
                static_cast<size_t>(hk) * G + rb * R + r % per_token;
     };
 
+    // ---- all that can be asked for at once: the sequence's length, this thread's part of
+    // the lists, of the queries and of the tree
+    const int n_listed = nt * a.n_blocks;
+    auto listed = [&](int i) {  // entry i of the unit's lists, token by token
+        const int t = i / a.n_blocks;
+        return a.blocks[((static_cast<size_t>(b) * a.T + t0 + t) * a.Hkv + hk) * a.n_blocks + i -
+                        t * a.n_blocks];
+    };
+    const int L_raw = a.lens[b];
+    const int j_mine = tid < n_listed ? listed(tid) : -1;
+    const int j_then = nt == 1 && tid + 1 < n_listed ? listed(tid + 1) : -1;
+    constexpr int kVecs = D / 8;  // 16-byte vectors of a row, one to a lane
+    static_assert(R * kVecs <= kThreads, "one vector of the queries to a thread");
+    const int q_row = tid / kVecs;
+    uint4 q_mine = make_uint4(0u, 0u, 0u, 0u);
+    if (q_row < rows)
+        q_mine = *reinterpret_cast<const uint4*>(a.q + row_of(q_row) * D + tid % kVecs * 8);
+    const int32_t* up = a.parents + static_cast<size_t>(b) * a.parents_stride;
+    const int p0 = a.mask == nullptr && lane < a.T ? up[lane] : -1;
+    const int p1 = a.mask == nullptr && lane + 32 < a.T ? up[lane + 32] : -1;
+
     // ---- the list of pages
     bool bad;
-    const int L = clamp_seq_len(a.lens[b], a.P, a.max_pages, bad);
+    const int L = clamp_seq_len(L_raw, a.P, a.max_pages, bad);
     if (bad && tid == 0) report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
     const int nb = (L + a.P - 1) / a.P;
     const int32_t* table = a.table + static_cast<size_t>(b) * a.max_pages;
-    auto list_of = [&](int t) {
-        return a.blocks +
-               ((static_cast<size_t>(b) * a.T + t0 + t) * a.Hkv + hk) * a.n_blocks;
+    // First row of logical page j of the sequence, -1 where there is none.
+    auto page_row = [&](int j) {
+        const int page = table[j];
+        if (page >= 0 && page < a.num_pages) return (page * a.Hkv + hk) * a.P;  // (below 2^31)
+        report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+        return -1;
     };
-    auto entry = [&](int j, unsigned who) {
+    auto entry = [&](int j, int row, unsigned who) {
         Entry e;
-        e.page = table[j];
-        if (e.page < 0 || e.page >= a.num_pages) {
-            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-            e.page = 0;
-            who = 0;
-        }
-        e.live_who = static_cast<uint32_t>(who == 0 ? 0 : min(a.P, L - j * a.P)) | who << 8;
+        e.row = max(row, 0);
+        e.live_who = row < 0 ? 0u : static_cast<uint32_t>(min(a.P, L - j * a.P)) | who << 8;
         return e;
     };
     // One token whose list ascends (as it comes from the selection) is taken as it is.
     int n_entries = 0;
     bool as_is = nt == 1;
     if (as_is) {
-        const int32_t* list = list_of(0);
         bool ascends = true;
         int n = 0;
-        for (int i = tid; i < a.n_blocks; i += kThreads) {
-            const int j = list[i], then = i + 1 < a.n_blocks ? list[i + 1] : -1;
+        for (int i = tid; i < n_listed; i += kThreads) {
+            const int j = i == tid ? j_mine : listed(i);
+            const int then = i == tid ? j_then : i + 1 < n_listed ? listed(i + 1) : -1;
             ascends &= then < 0 || (j >= 0 && j < then);
             if (j < -1 || j >= nb) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
             const bool ok = j >= 0 && j < nb;
-            if (ok) sm.entries[i] = entry(j, 1u);
+            if (ok) sm.entries[i] = entry(j, page_row(j), 1u);
             n += ok;
         }
         as_is = __syncthreads_and(ascends);
@@ -757,30 +804,31 @@ __global__ void __launch_bounds__(kThreads, kResident)
     }
     if (!as_is) {
         n_entries = 0;
+        uint32_t* marks = sm.marks();  // and behind them the pages' rows
+        int* row_at = reinterpret_cast<int*>(marks + kWindow / 2);
         for (int w0 = 0; w0 < nb; w0 += kWindow) {
             const int width = min(kWindow, nb - w0);
-            uint32_t* marks = sm.marks();
             __syncthreads();
             for (int i = tid; i < (width + 1) / 2; i += kThreads) marks[i] = 0;
             __syncthreads();
-            for (int t = 0; t < nt; ++t) {
-                const int32_t* list = list_of(t);
-                for (int i = tid; i < a.n_blocks; i += kThreads) {
-                    const int j = list[i];
-                    if (j < -1 || j >= nb) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-                    if (j >= w0 && j < w0 + width)
-                        atomicOr(marks + ((j - w0) >> 1), 1u << (t + 16 * ((j - w0) & 1)));
+            for (int i = tid; i < n_listed; i += kThreads) {
+                const int j = i == tid ? j_mine : listed(i);
+                if (j < -1 || j >= nb) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                if (j >= w0 && j < w0 + width) {
+                    const int at = j - w0;
+                    atomicOr(marks + (at >> 1), 1u << (i / a.n_blocks + 16 * (at & 1)));
+                    row_at[at] = page_row(j);  // (the same from all)
                 }
             }
             __syncthreads();
             for (int i0 = 0; i0 < (width + 1) / 2; i0 += kThreads) {
-                const uint32_t m = i0 + tid < (width + 1) / 2 ? marks[i0 + tid] : 0u;
+                const int i = i0 + tid;
+                const uint32_t m = i < (width + 1) / 2 ? marks[i] : 0u;
                 const unsigned lo = m & 0xffffu, hi = m >> 16;
                 int total;
                 int at = n_entries + block_scan((lo != 0) + (hi != 0), sm.sums, total);
-                const int j = w0 + 2 * (i0 + tid);
-                if (lo != 0) sm.entries[at++] = entry(j, lo);
-                if (hi != 0) sm.entries[at] = entry(j + 1, hi);
+                if (lo != 0) sm.entries[at++] = entry(w0 + 2 * i, row_at[2 * i], lo);
+                if (hi != 0) sm.entries[at] = entry(w0 + 2 * i + 1, row_at[2 * i + 1], hi);
                 n_entries += total;
             }
         }
@@ -793,8 +841,6 @@ __global__ void __launch_bounds__(kThreads, kResident)
             bits = a.mask[static_cast<size_t>(b) * a.mask_stride + t0 + t];
             if (a.T < 64) bits &= (1ull << a.T) - 1ull;
         } else {
-            const int32_t* up = a.parents + static_cast<size_t>(b) * a.parents_stride;
-            const int p0 = lane < a.T ? up[lane] : -1, p1 = lane + 32 < a.T ? up[lane + 32] : -1;
             if (p0 < -1 || (p0 >= lane && lane < a.T) || p1 < -1 ||
                 (p1 >= lane + 32 && lane + 32 < a.T))
                 report(a.status, TREE_ATTN_STATUS_BAD_PARENT);
@@ -818,11 +864,9 @@ __global__ void __launch_bounds__(kThreads, kResident)
     // ---- queries, as the product's second operand (8-bit cache: in fp16, scaled so that
     // the row's largest lies in [2^14, 2^15): exact down to 2^-28 of it, and to 2^-39 of
     // it below; and in bf16 for the tree)
-    constexpr int kVecs = D / 8;  // 16-byte vectors of a row, one to a lane
-    for (int r = tid / kVecs; r < R; r += kThreads / kVecs) {
-        const int i = tid % kVecs;
-        uint4 x = r < rows ? *reinterpret_cast<const uint4*>(a.q + row_of(r) * D + i * 8)
-                           : make_uint4(0u, 0u, 0u, 0u);
+    if (q_row < R) {
+        const int r = q_row, i = tid % kVecs;
+        uint4 x = q_mine;
         if (a.scale_log2 < 0.0f) {  // score units are positive
             x.x ^= 0x80008000u;
             x.y ^= 0x80008000u;
@@ -872,8 +916,16 @@ __global__ void __launch_bounds__(kThreads, kResident)
     __syncthreads();
     if (!warp_rows<D, FP8, NT, false>(a, sm, u)) warp_rows_again<D, FP8, NT>(a, sm, u);
     __syncthreads();
-    // ---- the CTA's rows, then (S > 1) the cluster's: four channels to a thread
+    // ---- the CTA's rows, and (S > 1) the cluster's: four channels to a thread
     constexpr int kQuads = D / 4;
+    auto write = [&](int r, int d, float m, float l, const float4& o) {
+        const bool none = l == 0.0f;  // no key at all
+        const float inv = none ? 0.0f : 1.0f / l;
+        const size_t row = row_of(r);
+        *reinterpret_cast<uint2*>(a.out + row * D + d) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (d == 0) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+    };
     for (int i = tid; i < rows * kQuads; i += kThreads) {
         const int r = i / kQuads, d = i % kQuads * 4;
         float m = kLow;
@@ -891,47 +943,65 @@ __global__ void __launch_bounds__(kThreads, kResident)
             o.z += f * y.z;
             o.w += f * y.w;
         }
-        *reinterpret_cast<float4*>(&sm.mine[r][d]) = o;
-        if (d == 0) {
-            sm.mine_m[r] = m;
-            sm.mine_l[r] = l;
+        if (S == 1) {
+            write(r, d, m, l, o);
+        } else {
+            *reinterpret_cast<float4*>(&sm.mine[r][d]) = o;
+            if (d == 0) {
+                sm.mine_m[r] = m;
+                sm.mine_l[r] = l;
+            }
         }
     }
-    if (S > 1)
-        ptx::cluster_sync();
-    else
-        __syncthreads();
+    if (S == 1) return;
+    ptx::cluster_sync();
     for (int i = rank * kThreads + tid; i < rows * kQuads; i += S * kThreads) {
         const int r = i / kQuads, d = i % kQuads * 4;
         const uint32_t at_m = ptx::smem_u32(&sm.mine_m[r]), at_l = ptx::smem_u32(&sm.mine_l[r]);
         const uint32_t at_o = ptx::smem_u32(&sm.mine[r][d]);
         float m = kLow, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int s = 0; s < S; ++s) m = fmaxf(m, ptx::ld_cluster(ptx::map_rank(at_m, s)));
-        for (int s = 0; s < S; ++s) {
-            const float f = ex2(ptx::ld_cluster(ptx::map_rank(at_m, s)) - m);
-            l += f * ptx::ld_cluster(ptx::map_rank(at_l, s));
-            const float4 y = ptx::ld_cluster_v4(ptx::map_rank(at_o, s));
-            o.x += f * y.x;
-            o.y += f * y.y;
-            o.z += f * y.z;
-            o.w += f * y.w;
+        for (int s0 = 0; s0 < S; s0 += 4) {  // (four CTAs' at a time: one round trip)
+            float ms[4], ls[4];
+            float4 y[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t from = min(s0 + s, S - 1);
+                ms[s] = ptx::ld_cluster(ptx::map_rank(at_m, from));
+                ls[s] = ptx::ld_cluster(ptx::map_rank(at_l, from));
+                y[s] = ptx::ld_cluster_v4(ptx::map_rank(at_o, from));
+            }
+            float top = m;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) top = fmaxf(top, ms[s]);
+            const float f0 = ex2(m - top);
+            m = top;
+            l *= f0;
+            o.x *= f0;
+            o.y *= f0;
+            o.z *= f0;
+            o.w *= f0;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (s0 + s >= S) break;
+                const float f = ex2(ms[s] - top);
+                l += f * ls[s];
+                o.x += f * y[s].x;
+                o.y += f * y[s].y;
+                o.z += f * y[s].z;
+                o.w += f * y[s].w;
+            }
         }
-        const bool none = l == 0.0f;  // no key at all
-        const float inv = none ? 0.0f : 1.0f / l;
-        const size_t row = row_of(r);
-        *reinterpret_cast<uint2*>(a.out + row * D + d) =
-            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (d == 0) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+        write(r, d, m, l, o);
     }
-    if (S > 1) ptx::cluster_sync();  // (other CTAs may still read this one's rows)
+    ptx::cluster_sync();  // (other CTAs may still read this one's rows)
 }
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
 
 template <int D, bool FP8, int NT>
-int launch(const Args& a, long long units, int sms, cudaStream_t stream) {
-    const size_t smem = sizeof(Smem<D, FP8, NT>) +
+int launch(Args a, long long units, int sms, cudaStream_t stream) {
+    const size_t smem = sizeof(Smem<D, FP8, NT>) + kThreads * sizeof(int) +
                         static_cast<size_t>(a.tokens) * a.n_blocks * sizeof(Entry);
     const auto kernel = blocks_kernel<D, FP8, NT>;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -956,6 +1026,7 @@ int launch(const Args& a, long long units, int sms, cudaStream_t stream) {
             S = s;
         }
     }
+    a.longest_first = a.B > 1 && a.B <= kThreads && units * S > slots;
     return rc_of(launch_cluster(kernel, dim3(static_cast<unsigned>(units * S)),
                                 dim3(kThreads), smem, S, stream, a));
 }
@@ -1032,6 +1103,7 @@ extern "C" int tree_attn_verify_blocks(
     a.P = page_size;
     a.num_pages = num_pages;
     a.row_blocks = row_blocks;
+    a.B = B;
     a.tokens = tokens;
     a.groups = groups;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
