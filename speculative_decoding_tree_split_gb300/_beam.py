@@ -5,8 +5,8 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import load
-from ._serving import _F32, _I32, _NOT_SO, _Place, _device_of, _tensor
+from ._pages import _workspace
+from ._serving import _DEVICES, _F32, _I32, _NOT_SO, _Place, _device_of, _tensor
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _FLAGS = (torch.bool, torch.uint8)
@@ -25,6 +25,15 @@ def _check(logits, scores, finished, dev: int):
         _tensor(finished, "finished", _FLAGS, 2, dev)
         if tuple(finished.shape) != (B, W):
             raise ValueError(f"finished must have shape {(B, W)}")
+
+
+def _out(t, name: str, dtype, shape, at: _Place) -> torch.Tensor:
+    if t is None:
+        return at.empty(shape, dtype)
+    _tensor(t, name, (dtype,), 2, at.dev)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}")
+    return t
 
 
 def beam_select(logits, scores, n_select: int, *, finished=None, eos: Optional[int] = None,
@@ -61,24 +70,19 @@ def beam_select(logits, scores, n_select: int, *, finished=None, eos: Optional[i
     if finished is not None and eos is None:
         raise ValueError("finished beams need eos")
     at = _Place(dev, stream)
-    outs = []
-    for t, name, dtype in ((scores_out, "scores_out", _F32), (rows_out, "rows_out", _I32),
-                           (tokens_out, "tokens_out", _I32)):
-        if t is None:
-            t = at.empty((B, k), dtype)
-        else:
-            _tensor(t, name, (dtype,), 2, dev)
-            if tuple(t.shape) != (B, k):
-                raise ValueError(f"{name} must have shape {(B, k)}")
-        outs.append(t)
-    if workspace is None:
-        need = load().tree_beam_workspace_size(B, W, V, k)
-        workspace = at.empty(max(need, 256), torch.uint8)
+    if scores_out is None and rows_out is None and tokens_out is None and at.stream is None and k > 0:
+        d = _DEVICES[dev]
+        scores_out = torch.empty((B, k), dtype=_F32, device=d)
+        rows_out = torch.empty((B, k), dtype=_I32, device=d)
+        tokens_out = torch.empty((B, k), dtype=_I32, device=d)
     else:
-        _tensor(workspace, "workspace", (torch.uint8,), 1, dev)
+        scores_out = _out(scores_out, "scores_out", _F32, (B, max(k, 0)), at)
+        rows_out = _out(rows_out, "rows_out", _I32, (B, max(k, 0)), at)
+        tokens_out = _out(tokens_out, "tokens_out", _I32, (B, max(k, 0)), at)
+    workspace = _workspace(workspace, at, "tree_beam_workspace_size", B, W, V, k)
     at.run("tree_beam_select", logits.data_ptr(), _DTYPES[logits.dtype], bs if B > 1 else 0,
            ws if W > 1 else 0, scores.data_ptr(),
            None if finished is None else finished.data_ptr(), -1 if eos is None else int(eos),
-           outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), B, W, V, k,
+           scores_out.data_ptr(), rows_out.data_ptr(), tokens_out.data_ptr(), B, W, V, k,
            workspace.data_ptr(), workspace.numel())
-    return outs[0], outs[1], outs[2]
+    return scores_out, rows_out, tokens_out

@@ -9,8 +9,8 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import _BITS64
-from ._serving import (_BF16, _CODES, _F32, _I32, _NOT_SO, _U8, _Place, _device_of, _tensor,
-                       _vector, _status)
+from ._serving import (_BF16, _CODES, _DEVICES, _F32, _I32, _NOT_SO, _U8, _Place, _device_of,
+                       _status, _tensor, _vector)
 
 _I8 = torch.int8
 
@@ -58,12 +58,22 @@ def kv_block_bounds(k_pages, block_table, seq_lens, *, k_scales=None, starts=Non
     bounds_exp uint8 [num_pages][Hkv]); rows of other pages keep what they held
     (are uninitialised when the call makes them).
     """
-    dev = _device_of(k_pages, "k_pages")
+    try:
+        dev = k_pages.get_device()
+        B, width = block_table.shape
+        sound = (dev >= 0 and block_table.dtype is _I32 and seq_lens.dtype is _I32
+                 and seq_lens.shape == (B,) and block_table.get_device() == dev
+                 and seq_lens.get_device() == dev and block_table.is_contiguous()
+                 and seq_lens.is_contiguous())
+    except _NOT_SO:
+        sound = False
+    if not sound:
+        dev = _device_of(k_pages, "k_pages")
+        _tensor(block_table, "block_table", (_I32,), 2, dev)
+        B, width = block_table.shape
+        _vector(seq_lens, "seq_lens", B, dev)
     _cache_arg(k_pages, k_scales, "k", dev)
     n, H, P, d = k_pages.shape
-    _tensor(block_table, "block_table", (_I32,), 2, dev)
-    B, width = block_table.shape
-    _vector(seq_lens, "seq_lens", B, dev)
     if starts is not None:
         _vector(starts, "starts", B, dev)
     if (bounds is None) != (bounds_exp is None):
@@ -75,7 +85,7 @@ def kv_block_bounds(k_pages, block_table, seq_lens, *, k_scales=None, starts=Non
         _check_bounds(bounds, bounds_exp, n, H, d, dev)
     at.run("tree_kv_block_bounds", k_pages.data_ptr(), _ptr(k_scales), block_table.data_ptr(),
            width, _ptr(starts), seq_lens.data_ptr(), bounds.data_ptr(), bounds_exp.data_ptr(), B,
-           H, d, P, n, _status(status, dev))
+           H, d, P, n, None if status is None else _status(status, dev))
     return bounds, bounds_exp
 
 
@@ -88,27 +98,46 @@ def select_blocks(q, bounds, bounds_exp, block_table, seq_lens, n_select: int, p
     n_first and the last n_last pages of a sequence are always among them.  Returns
     int32 [B][T][Hkv][n_select]: pages of the sequence in ascending order, then -1.
     """
-    dev = _device_of(q, "q")
-    _tensor(q, "q", (_BF16,), 4, dev)
-    B, T, Hq, d = q.shape
-    _tensor(bounds, "bounds", (_I8,), 4, dev)
-    n, H = bounds.shape[:2]
-    _check_bounds(bounds, bounds_exp, n, H, d, dev)
-    _tensor(block_table, "block_table", (_I32,), 2, dev)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
-    _vector(seq_lens, "seq_lens", B, dev)
-    k = int(n_select)
+    k = n_select
+    try:
+        dev = q.get_device()
+        B, T, Hq, d = q.shape
+        n, H = bounds_exp.shape
+        width = block_table.shape[1]
+        sound = (dev >= 0 and q.dtype is _BF16 and bounds.dtype is _I8 and bounds_exp.dtype is _U8
+                 and block_table.dtype is _I32 and seq_lens.dtype is _I32
+                 and bounds.shape == (n, H, 2, d) and block_table.shape == (B, width)
+                 and seq_lens.shape == (B,) and bounds.get_device() == dev
+                 and bounds_exp.get_device() == dev and block_table.get_device() == dev
+                 and seq_lens.get_device() == dev and q.is_contiguous()
+                 and bounds.is_contiguous() and bounds_exp.is_contiguous()
+                 and block_table.is_contiguous() and seq_lens.is_contiguous())
+    except (*_NOT_SO, IndexError):
+        sound = False
+    if not sound:
+        dev = _device_of(q, "q")
+        _tensor(q, "q", (_BF16,), 4, dev)
+        B, T, Hq, d = q.shape
+        _tensor(bounds, "bounds", (_I8,), 4, dev)
+        n, H = bounds.shape[:2]
+        _check_bounds(bounds, bounds_exp, n, H, d, dev)
+        _tensor(block_table, "block_table", (_I32,), 2, dev)
+        if block_table.shape[0] != B:
+            raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
+        _vector(seq_lens, "seq_lens", B, dev)
+        width = block_table.shape[1]
     at = _Place(dev, stream)
-    if out is None:
+    if out is None and at.stream is None and k > 0:
+        out = torch.empty((B, T, H, k), dtype=_I32, device=_DEVICES[dev])
+    elif out is None:
         out = at.empty((B, T, H, max(k, 0)), _I32)
     else:
         _tensor(out, "out", (_I32,), 4, dev)
         if tuple(out.shape) != (B, T, H, k):
             raise ValueError(f"out must have shape {(B, T, H, k)}")
     at.run("tree_select_blocks", q.data_ptr(), bounds.data_ptr(), bounds_exp.data_ptr(),
-           block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), out.data_ptr(), B,
-           Hq, H, d, T, page_size, n, k, n_first, n_last, _status(status, dev))
+           block_table.data_ptr(), width, seq_lens.data_ptr(), out.data_ptr(), B, Hq, H, d, T,
+           page_size, n, k, n_first, n_last, None if status is None else _status(status, dev))
     return out
 
 
@@ -173,16 +202,20 @@ def verify_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, tree_k, tr
         B, T, Hq, _ = q.shape
     stride = T if tree.dim() == 2 else 0
     at = _Place(dev, stream)
-    if out is None:
-        out = at.empty(q.shape, _BF16)
+    if out is None and lse is None and at.stream is None:
+        out = torch.empty_like(q)
+        lse = torch.empty((B, T, Hq), dtype=_F32, device=_DEVICES[dev])
     else:
-        _tensor(out, "out", (_BF16,), 4, dev)
-    if lse is None:
-        lse = at.empty((B, T, Hq), _F32)
-    else:
-        _tensor(lse, "lse", (_F32,), 3, dev)
-    if out.shape != q.shape or tuple(lse.shape) != (B, T, Hq):
-        raise ValueError("out and lse must have shapes [B][T][Hq][d] and [B][T][Hq]")
+        if out is None:
+            out = at.empty(q.shape, _BF16)
+        else:
+            _tensor(out, "out", (_BF16,), 4, dev)
+        if lse is None:
+            lse = at.empty((B, T, Hq), _F32)
+        else:
+            _tensor(lse, "lse", (_F32,), 3, dev)
+        if out.shape != q.shape or tuple(lse.shape) != (B, T, Hq):
+            raise ValueError("out and lse must have shapes [B][T][Hq][d] and [B][T][Hq]")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
     at.run("tree_attn_verify_blocks", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
@@ -190,5 +223,5 @@ def verify_blocks(q, k_pages, v_pages, block_table, seq_lens, blocks, tree_k, tr
            seq_lens.data_ptr(), blocks.data_ptr(), blocks.shape[3], tree_k.data_ptr(),
            tree_v.data_ptr(), _ptr(mask), stride if parents is None else 0, _ptr(parents),
            0 if parents is None else stride, out.data_ptr(), lse.data_ptr(), B, Hq, H, d, T, P, n,
-           float(softmax_scale), _status(status, dev))
+           float(softmax_scale), None if status is None else _status(status, dev))
     return out, lse

@@ -13,41 +13,54 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from ._lib import load
-from ._serving import _I32, _NOT_SO, _Place, _device_of, _status, _tensor, _vector
+from ._serving import (_DEVICES, _I32, _NOT_SO, _U8, _Place, _device_of, _status, _tensor,
+                       _vector)
+
+
+def _check_pools(pools, num_pages: Optional[int], dev: int):
+    """The pools one by one."""
+    for i, t in enumerate(pools):
+        name = f"pools[{i}]"
+        if _device_of(t, name) != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the other tensors on "
+                             f"cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.dim() < 2:
+            raise ValueError(f"{name} must have pages of some size")
+        if t.shape[0] != num_pages and num_pages is not None or t.shape[0] == 0:
+            raise ValueError(f"{name} has {t.shape[0]} pages, expected {num_pages}")
+        num_pages = t.shape[0]
 
 
 def _pool_args(pools: Sequence[torch.Tensor], num_pages: Optional[int], dev: int):
     """(pointers, bytes of a page, how many, pages) of the pools, as arrays for the
     library (to be kept until the call returns)."""
-    ptrs, sizes = array("Q"), array("Q")
-    for i, t in enumerate(pools):
-        try:
-            sound = (t.get_device() == dev and t.is_contiguous() and t.dim() >= 2
-                     and (num_pages is None or t.shape[0] == num_pages) and t.shape[0] > 0)
-        except _NOT_SO:
-            sound = False
-        if not sound:
-            name = f"pools[{i}]"
-            if _device_of(t, name) != dev:
-                raise ValueError(f"{name} is on cuda:{t.get_device()}, the other tensors on "
-                                 f"cuda:{dev}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-            if t.dim() < 2:
-                raise ValueError(f"{name} must have pages of some size")
-            raise ValueError(f"{name} has {t.shape[0]} pages, expected {num_pages}")
-        num_pages = t.shape[0]
-        ptrs.append(t.data_ptr())
-        sizes.append(t.nbytes // num_pages)
-    return ptrs, sizes, len(ptrs), num_pages
+    try:
+        n = num_pages if num_pages is not None or not pools else pools[0].shape[0]
+        sizes = array("Q", [t.nbytes // n for t in pools if t.shape[0] == n and t.dim() > 1
+                            and t.is_contiguous() and t.get_device() == dev])
+        if len(sizes) == len(pools):
+            return array("Q", [t.data_ptr() for t in pools]), sizes, len(pools), n
+    except (*_NOT_SO, ZeroDivisionError, IndexError):
+        pass
+    _check_pools(pools, num_pages, dev)
+    raise ValueError("pools must be a sequence of tensors of the same number of pages")
 
 
-def _workspace(workspace, need: int, dev: int, at: _Place) -> torch.Tensor:
-    if workspace is None:
-        return at.empty(max(need, 256), torch.uint8)
-    _tensor(workspace, "workspace", (torch.uint8,), 1, dev)
-    return workspace
+_SIZES: dict = {}  # workspace bytes, by function and sizes
+
+
+def _workspace(given, at: _Place, name: str, *sizes: int) -> torch.Tensor:
+    if given is not None:
+        _tensor(given, "workspace", (_U8,), 1, at.dev)
+        return given
+    need = _SIZES.get((name, sizes))
+    if need is None:
+        need = _SIZES[name, sizes] = max(at.call(name, *sizes), 256)
+    if at.stream is None:
+        return torch.empty(need, dtype=_U8, device=_DEVICES[at.dev])
+    return at.empty(need, _U8)
 
 
 def kv_copy_pages(pools, src, dst, *, count=None, status=None, stream=None) -> None:
@@ -72,7 +85,10 @@ def kv_copy_pages(pools, src, dst, *, count=None, status=None, stream=None) -> N
 
 
 def _out(t, name: str, like: torch.Tensor, shape, at: _Place) -> torch.Tensor:
+    """An output given by the caller (not the input of its kind), or a new one."""
     if t is None:
+        if at.stream is None:
+            return torch.empty(shape, dtype=_I32, device=_DEVICES[at.dev])
         return at.empty(shape, _I32)
     _tensor(t, name, (_I32,), len(shape), at.dev)
     if tuple(t.shape) != tuple(shape):
@@ -97,33 +113,45 @@ def kv_fork(pools, block_table, seq_lens, page_refs, src, page_size: int, *, res
     Returns (block_table, seq_lens, page_refs) of the new rows; status 6: there
     were not enough free pages.
     """
-    dev = _device_of(block_table, "block_table")
-    _tensor(block_table, "block_table", (_I32,), 2, dev)
-    rows, width = block_table.shape
-    _vector(seq_lens, "seq_lens", rows, dev)
-    _tensor(page_refs, "page_refs", (_I32,), 1, dev)
-    _tensor(src, "src", (_I32,), 1, dev)
-    n = src.shape[0]
-    num_pages = page_refs.shape[0]
+    try:
+        dev = block_table.get_device()
+        rows, width = block_table.shape
+        (n,), (num_pages,) = src.shape, page_refs.shape
+        sound = (dev >= 0 and block_table.dtype is _I32 and seq_lens.dtype is _I32
+                 and page_refs.dtype is _I32 and src.dtype is _I32 and seq_lens.shape == (rows,)
+                 and seq_lens.get_device() == dev and page_refs.get_device() == dev
+                 and src.get_device() == dev and block_table.is_contiguous()
+                 and seq_lens.is_contiguous() and page_refs.is_contiguous()
+                 and src.is_contiguous())
+    except _NOT_SO:
+        sound = False
+    if not sound:
+        dev = _device_of(block_table, "block_table")
+        _tensor(block_table, "block_table", (_I32,), 2, dev)
+        rows, width = block_table.shape
+        _vector(seq_lens, "seq_lens", rows, dev)
+        _tensor(page_refs, "page_refs", (_I32,), 1, dev)
+        _tensor(src, "src", (_I32,), 1, dev)
+        n, num_pages = src.shape[0], page_refs.shape[0]
     more, each = 0, None
-    if isinstance(reserve, torch.Tensor):
-        _vector(reserve, "reserve", n, dev)
-        each = reserve.data_ptr()
-    else:
-        more = int(reserve)
+    if type(reserve) is int:
+        more = reserve
         if more < 0:
             raise ValueError("reserve must not be negative")
+    else:
+        _vector(reserve, "reserve", n, dev)
+        each = reserve.data_ptr()
     ptrs, sizes, n_pools, _ = _pool_args(pools, num_pages, dev)
     at = _Place(dev, stream)
     table = _out(block_table_out, "block_table_out", block_table, (n, width), at)
     lens = _out(seq_lens_out, "seq_lens_out", seq_lens, (n,), at)
     refs = _out(page_refs_out, "page_refs_out", page_refs, (num_pages,), at)
-    workspace = _workspace(workspace, load().tree_kv_fork_workspace_size(rows, n, num_pages), dev,
-                           at)
+    workspace = _workspace(workspace, at, "tree_kv_fork_workspace_size", rows, n, num_pages)
     at.run("tree_kv_fork", ptrs.buffer_info()[0], sizes.buffer_info()[0], n_pools,
            block_table.data_ptr(), width, seq_lens.data_ptr(), page_refs.data_ptr(),
            src.data_ptr(), each, more, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rows, n,
-           page_size, num_pages, workspace.data_ptr(), workspace.numel(), _status(status, dev))
+           page_size, num_pages, workspace.data_ptr(), workspace.numel(),
+           None if status is None else _status(status, dev))
     return table, lens, refs
 
 
@@ -136,27 +164,34 @@ def kv_compact(pools, block_table, page_refs, *, block_table_out=None, page_refs
     int32 [num_pages].  Returns (block_table, page_refs, n_used): pages n_used ..
     num_pages - 1 are free then (n_used: int32 tensor of one element).
     """
-    dev = _device_of(block_table, "block_table")
-    _tensor(block_table, "block_table", (_I32,), 2, dev)
-    _tensor(page_refs, "page_refs", (_I32,), 1, dev)
-    rows, width = block_table.shape
-    num_pages = page_refs.shape[0]
+    try:
+        dev = block_table.get_device()
+        rows, width = block_table.shape
+        (num_pages,) = page_refs.shape
+        sound = (dev >= 0 and block_table.dtype is _I32 and page_refs.dtype is _I32
+                 and page_refs.get_device() == dev and block_table.is_contiguous()
+                 and page_refs.is_contiguous())
+    except _NOT_SO:
+        sound = False
+    if not sound:
+        dev = _device_of(block_table, "block_table")
+        _tensor(block_table, "block_table", (_I32,), 2, dev)
+        _tensor(page_refs, "page_refs", (_I32,), 1, dev)
+        rows, width = block_table.shape
+        num_pages = page_refs.shape[0]
     ptrs, sizes, n_pools, _ = _pool_args(pools, num_pages, dev)
     at = _Place(dev, stream)
     if block_table_out is None:
-        block_table_out = at.empty((rows, width), _I32)
-    else:
+        block_table_out = _out(None, "", block_table, (rows, width), at)
+    else:  # (may be block_table)
         _tensor(block_table_out, "block_table_out", (_I32,), 2, dev)
         if block_table_out.shape != block_table.shape:
             raise ValueError("block_table_out must have block_table's shape")
     refs = _out(page_refs_out, "page_refs_out", page_refs, (num_pages,), at)
-    if n_used is None:
-        n_used = at.empty((1,), _I32)
-    else:
-        _vector(n_used, "n_used", 1, dev)
-    workspace = _workspace(workspace, load().tree_kv_compact_workspace_size(num_pages), dev, at)
+    n_used = _out(n_used, "n_used", page_refs, (1,), at)
+    workspace = _workspace(workspace, at, "tree_kv_compact_workspace_size", num_pages)
     at.run("tree_kv_compact", ptrs.buffer_info()[0], sizes.buffer_info()[0], n_pools,
            block_table.data_ptr(), width, page_refs.data_ptr(), block_table_out.data_ptr(),
            refs.data_ptr(), n_used.data_ptr(), rows, num_pages, workspace.data_ptr(),
-           workspace.numel(), _status(status, dev))
+           workspace.numel(), None if status is None else _status(status, dev))
     return block_table_out, refs, n_used
