@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/tree_attn.h"
 #include "cluster.cuh"
@@ -231,12 +232,16 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs
 // some of its tokens.  With p = max(c, 0) and m = min(c, 0) a score is
 // p . hi + m . lo: a product of the pages' bounds (16 pages to a tile, 2 d deep)
 // with the query codes, on the tensor cores in fp16, whose products and fp32 sums
-// of such whole numbers are exact.  The highest scores are then found by their
-// bits, eight at a time from the top, and written in the order of the pages.
+// of such whole numbers are exact.
 //
 // The bounds of a page are contiguous and each is used once, so they go from
 // memory straight into the product's registers: the order of channels within a
 // product is free, and is chosen so that a lane's 16 bytes are its operand.
+//
+// The k-th highest score is found by counting: the keys (ordered bits of the scores)
+// between the lowest and the highest fall into 256 equal ranges, the one with the k-th
+// is divided again, until it holds no more than are wanted of it; two counts as a rule.
+// The pages are then written in their order.
 // ---------------------------------------------------------------------------
 struct SelectArgs {
     const uint16_t* q;
@@ -249,14 +254,15 @@ struct SelectArgs {
     int TC, chunks;  // tokens of a CTA, and CTAs' worth of tokens
     int cols;        // columns of a token: a power of two up to 8, or a multiple of 8
     int per_most;    // scores of a token that one CTA holds at most
+    int B;
+    bool longest_first;
     int32_t* status;
 };
 
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kTilesAtOnce = 4;  // column tiles that share one conversion of the bounds
 
-// Order-preserving bits of a score; 0 for a page that scores nothing.
+// Order-preserving bits of a score (above 1, the key of a page that scores nothing).
 __device__ __forceinline__ uint32_t score_key(float x) {
     const uint32_t b = __float_as_uint(x);
     return (b >> 31) != 0 ? ~b : b | 0x80000000u;
@@ -272,17 +278,6 @@ __device__ __forceinline__ void f16x2_of_s8x4(uint32_t x, uint32_t& h0, uint32_t
     __half2 y1 = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
     h0 = *reinterpret_cast<uint32_t*>(&y0);
     h1 = *reinterpret_cast<uint32_t*>(&y1);
-}
-
-__device__ __forceinline__ uint32_t max0_f16x2(uint32_t x) {
-    uint32_t r;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0u));
-    return r;
-}
-__device__ __forceinline__ uint32_t min0_f16x2(uint32_t x) {
-    uint32_t r;
-    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0u));
-    return r;
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -307,111 +302,184 @@ struct Keys {
     }
 };
 
-// By NW warps (all of the CTA, or each warp for itself): the k highest of n keys,
-// as ascending indices to out[0 .. k).
+// Barrier of the NW warps that work on one token: all of the CTA's, some, or one.
 template <int NW>
-__device__ __forceinline__ void take_highest(const Keys& key, int n, int k, int32_t* out,
-                                             int* hist, int* counts, int t) {
-    constexpr int GS = 32 * NW;
-    auto sync = [] {
-        if (NW > 1)
-            __syncthreads();
-        else
-            __syncwarp();
-    };
-    const int lane = t & 31, w = t >> 5;
-    uint32_t prefix = 0, known = 0;
-    int left = k;  // still to be found among the keys that share the prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = t; i < 256; i += GS) hist[i] = 0;
-        sync();
-        for (int i = t; i < n; i += GS) {
-            const uint32_t v = key(i);
-            if ((v & known) == prefix) atomicAdd(hist + ((v >> shift) & 255u), 1);
-        }
-        sync();
-        // The bin that holds the left-th from the top; every warp finds it.
-        int own = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) own += hist[255 - (lane * 8 + j)];
-        int upto = own;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(kFull, upto, off);
-            if (lane >= off) upto += y;
-        }
-        const int src = __ffs(__ballot_sync(kFull, upto >= left)) - 1;
-        int above = upto - own, bin = 0;
-        if (lane == src) {
-            int j = 0;
-            for (; j < 7; ++j) {
-                const int c = hist[255 - (lane * 8 + j)];
-                if (above + c >= left) break;
-                above += c;
-            }
-            bin = 255 - (lane * 8 + j);
-        }
-        bin = __shfl_sync(kFull, bin, src);
-        left -= __shfl_sync(kFull, above, src);
-        prefix |= static_cast<uint32_t>(bin) << shift;
-        known |= 255u << shift;
-        sync();  // (hist is read)
-    }
-    // Keys above the prefix, and the first `left` that equal it.
-    const int seg = ((n + GS - 1) / GS) * 32;  // of one warp
-    const int lo = min(w * seg, n), hi = min(lo + seg, n);
-    int more = 0, same = 0;
-    if (NW > 1) {
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const uint32_t v = i0 + lane < hi ? key(i0 + lane) : 0u;
-            more += __popc(__ballot_sync(kFull, i0 + lane < hi && v > prefix));
-            same += __popc(__ballot_sync(kFull, i0 + lane < hi && v == prefix));
-        }
-        if (lane == 0) {
-            counts[2 * w] = more;
-            counts[2 * w + 1] = same;
-        }
-        sync();
-        more = same = 0;
-        for (int i = 0; i < w; ++i) {
-            more += counts[2 * i];
-            same += counts[2 * i + 1];
-        }
-    }
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const uint32_t v = i0 + lane < hi ? key(i0 + lane) : 0u;
-        const unsigned gt = __ballot_sync(kFull, i0 + lane < hi && v > prefix);
-        const unsigned eq = __ballot_sync(kFull, i0 + lane < hi && v == prefix);
-        const unsigned below = (1u << lane) - 1u;
-        const int eq_rank = same + __popc(eq & below);
-        const bool take = ((gt >> lane) & 1u) != 0 || (((eq >> lane) & 1u) != 0 && eq_rank < left);
-        if (take) out[more + __popc(gt & below) + min(eq_rank, left)] = i0 + lane;
-        more += __popc(gt);
-        same += __popc(eq);
-    }
-    sync();
+__device__ __forceinline__ void group_sync(int id) {
+    if (NW == kSelWarps)
+        __syncthreads();
+    else if (NW > 1)
+        asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "n"(32 * NW) : "memory");
+    else
+        __syncwarp();
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+struct Scratch {  // of the warps that work on one token
+    int hist[256];
+    uint32_t low[kSelWarps], high[kSelWarps];
+    int counts[2 * kSelWarps];
+};
+
+constexpr int kHeld = 16;  // keys that a lane may hold in registers
+
+// By NW warps: of keys lo .. hi - 1 (none of them 0), the k highest (ties: the lowest
+// indices), together with all indices of [0, lo) and [hi, n), as ascending indices to out.
+// HELD: n <= 32 NW kHeld, so that each key is read once and stays in a register.
+template <int NW, bool HELD>
+__device__ __forceinline__ void take_highest(const Keys& key, int n, int lo, int hi, int k,
+                                             int32_t* out, Scratch& sc, int id, int t) {
+    constexpr int GS = 32 * NW;
+    const int lane = t & 31, w = t >> 5;
+    const int seg = ((n + GS - 1) / GS) * 32;  // keys of one warp, in a row
+    const int a0 = min(w * seg, n), a1 = min(a0 + seg, n);
+    uint32_t held[HELD ? kHeld : 1];
+    auto read = [&](int i) { return i >= max(lo, a0) && i < min(hi, a1) ? key(i) : 0u; };
+    if (HELD) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) held[HELD ? j : 0] = read(a0 + 32 * j + lane);
+    }
+    // f(index, key) for each of this lane's keys, 0 for what is not a candidate.
+    auto each = [&](auto f) {
+        if (HELD) {
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) {
+                if (a0 + 32 * j >= a1) break;
+                f(a0 + 32 * j + lane, held[HELD ? j : 0]);
+            }
+        } else {
+#pragma unroll 4
+            for (int i0 = a0; i0 < a1; i0 += 32) f(i0 + lane, read(i0 + lane));
+        }
+    };
+    uint32_t bound = 0xffffffffu;  // keys above it are taken, and the first `left` equal to it
+    int left = 0;
+    if (k > 0) {
+        uint32_t low = 0xffffffffu, high = 0;  // (low: less one, so that 0 is the largest)
+        each([&](int, uint32_t v) {
+            low = min(low, v - 1u);
+            high = max(high, v);
+        });
+        low = __reduce_min_sync(kFull, low);
+        high = __reduce_max_sync(kFull, high);
+        if (NW > 1) {
+            if (lane == 0) {
+                sc.low[w] = low;
+                sc.high[w] = high;
+            }
+            group_sync<NW>(id);
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                low = min(low, sc.low[i]);
+                high = max(high, sc.high[i]);
+            }
+        }
+        low += 1;
+        left = k;  // still to be found among keys low .. high
+        for (;;) {
+            const uint32_t range = high - low;
+            const int shift = max(0, 24 - __clz(range));
+            for (int i = t; i < 256; i += GS) sc.hist[i] = 0;
+            group_sync<NW>(id);
+            each([&](int, uint32_t v) {  // (0 - low is above every range)
+                if (v - low <= range) atomicAdd(sc.hist + ((v - low) >> shift), 1);
+            });
+            group_sync<NW>(id);
+            // The range that holds the left-th from the top; every warp finds it.
+            // Of the 256 counts, which 32 first, then which of them.
+            int eighth = 0, above = 0;
+            {
+                int part[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    part[j] = __reduce_add_sync(kFull, sc.hist[255 - (lane + 32 * j)]);
+#pragma unroll
+                for (int j = 0; j < 7; ++j) {
+                    const bool on = eighth == j && above + part[j] < left;
+                    above += on ? part[j] : 0;
+                    eighth += on;
+                }
+            }
+            const int mine = sc.hist[255 - (32 * eighth + lane)];
+            int upto = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(kFull, upto, off);
+                if (lane >= off) upto += y;
+            }
+            const int src = __ffs(__ballot_sync(kFull, above + upto >= left)) - 1;
+            const int in = __shfl_sync(kFull, mine, src);
+            left -= above + __shfl_sync(kFull, upto, src) - in;
+            low += static_cast<uint32_t>(255 - (32 * eighth + src)) << shift;
+            if (in == left || shift == 0) {  // all of the range, or keys that are all equal
+                bound = low;
+                break;
+            }
+            high = min(high, low + ((1u << shift) - 1u));
+            group_sync<NW>(id);  // (hist has been read)
+        }
+    }
+    // Keys above the bound, and the first `left` that equal it (all of those, where the
+    // whole range is taken).
+    auto taken = [&](int i, uint32_t v) {
+        return i < a1 && (i < lo || i >= hi || v > bound);
+    };
+    int more = 0, same = 0;
+    if (NW > 1) {
+        each([&](int i, uint32_t v) {
+            more += __popc(__ballot_sync(kFull, taken(i, v)));
+            same += __popc(__ballot_sync(kFull, v == bound));
+        });
+        if (lane == 0) {
+            sc.counts[2 * w] = more;
+            sc.counts[2 * w + 1] = same;
+        }
+        group_sync<NW>(id);
+        more = same = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            more += i < w ? sc.counts[2 * i] : 0;
+            same += i < w ? sc.counts[2 * i + 1] : 0;
+        }
+    }
+    const unsigned below = (1u << lane) - 1u;
+    each([&](int i, uint32_t v) {
+        const bool over = taken(i, v);
+        const unsigned gt = __ballot_sync(kFull, over);
+        const unsigned eq = __ballot_sync(kFull, v == bound);
+        const int eq_rank = same + __popc(eq & below);
+        if (over || (v == bound && eq_rank < left))
+            out[more + __popc(gt & below) + min(eq_rank, left)] = i;
+        more += __popc(gt);
+        same += __popc(eq);
+    });
+    group_sync<NW>(id);
+}
+
+// TILES: column tiles that share one conversion of the bounds (the last of several such
+// turns may work on columns that nobody wants).
+template <int D, int TILES>
+__global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int kStride = D + 4;  // halves: lanes g of a fragment load fall on banks of their own
+    // Query codes: [column][16-byte vectors of codes as (p, p, m, m) pairs], columns 64
+    // bytes apart beyond their length: two rows' reads fall on different banks.
+    constexpr int kStride = 4 * D + 64;  // bytes
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int S = static_cast<int>(ptx::cluster_size());
     const int rank = static_cast<int>(ptx::cluster_rank());
     const int unit = blockIdx.x / S;
-    const int hk = unit / a.chunks % a.Hkv, b = unit / (a.chunks * a.Hkv);
+    const int hk = unit / a.chunks % a.Hkv;
+    int b = unit / (a.chunks * a.Hkv);
+    if (a.longest_first) b = by_length(a.lens, a.B, b, reinterpret_cast<int*>(smem));
     const int t0 = unit % a.chunks * a.TC;
     const int nt = min(a.TC, a.T - t0);  // tokens
     const int G = a.Hq / a.Hkv;
-    const int tiles = (a.TC * a.cols + 7) / 8;
-    uint32_t* scores = reinterpret_cast<uint32_t*>(smem);  // [TC][per_most]
-    int* hist = reinterpret_cast<int*>(scores + static_cast<size_t>(a.TC) * a.per_most);
-    int* counts = hist + 256 * kSelWarps;
-    __half* codes = reinterpret_cast<__half*>(counts + 2 * kSelWarps);  // [tiles * 8][kStride]
+    const int tiles = ((a.TC * a.cols + 7) / 8 + TILES - 1) / TILES * TILES;
+    uint8_t* codes = smem;                                                // [tiles * 8][kStride]
+    Scratch* scratch = reinterpret_cast<Scratch*>(codes + tiles * 8 * kStride);  // [kSelWarps]
+    uint32_t* scores = reinterpret_cast<uint32_t*>(scratch + kSelWarps);  // [TC][per_most]
+    int* pages = reinterpret_cast<int*>(scores + static_cast<size_t>(a.TC) * a.per_most);  // [per_most]
 
     bool bad;
     const int L = clamp_seq_len(a.lens[b], a.P, a.max_pages, bad);
@@ -421,6 +489,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     const int lo = min(rank * per, nb), hi = min(lo + per, nb);
 
     if (nb > a.n_select) {
+        const int32_t* table = a.table + static_cast<size_t>(b) * a.max_pages;
+        for (int i = lo + tid; i < hi; i += kSelThreads) pages[i - lo] = table[i];
         // Query codes: a warp takes a token's heads.
         for (int t = warp; t < tiles * 8 / a.cols; t += kSelWarps) {
             const uint16_t* q =
@@ -434,27 +504,47 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
             }
             top = __reduce_max_sync(kFull, top);
             const float inv = pow2(-exponent_for(__uint_as_float(top << 16)));
-            for (int i = lane; i < a.cols * D; i += 32) {
-                const int col = i / D, d = i % D;  // columns past the group repeat its first head
-                const float x = __uint_as_float(
-                    static_cast<uint32_t>(q[(col < G ? col : 0) * D + d]) << 16);
-                const float y = x != x ? 0.0f : fminf(fmaxf(rintf(x * inv), -127.0f), 127.0f);
-                codes[static_cast<size_t>(t * a.cols + col) * kStride + d] = __float2half_rn(y);
+            // Four codes at a time: vector j, word w of lane c is channels 64 j + 16 c + 4 w.
+            for (int i = lane; i < a.cols * D / 4; i += 32) {
+                const int col = i / (D / 4), d = i % (D / 4) * 4;
+                const uint2 raw = *reinterpret_cast<const uint2*>(
+                    q + (col < G ? col : 0) * D + d);  // columns past the group repeat its first
+                __half2 p[2], m[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = h == 0 ? raw.x : raw.y;
+                    float y[2] = {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        y[e] = y[e] != y[e] ? 0.0f
+                                            : fminf(fmaxf(rintf(y[e] * inv), -127.0f), 127.0f);
+                    p[h] = __floats2half2_rn(fmaxf(y[0], 0.0f), fmaxf(y[1], 0.0f));
+                    m[h] = __floats2half2_rn(fminf(y[0], 0.0f), fminf(y[1], 0.0f));
+                }
+                const int j = d / 64, lane_c = d / 16 % 4, w = d / 4 % 4;
+                uint4 v;
+                v.x = *reinterpret_cast<uint32_t*>(&p[0]);
+                v.y = *reinterpret_cast<uint32_t*>(&p[1]);
+                v.z = *reinterpret_cast<uint32_t*>(&m[0]);
+                v.w = *reinterpret_cast<uint32_t*>(&m[1]);
+                *reinterpret_cast<uint4*>(codes + (t * a.cols + col) * kStride + (j * 4 + w) * 64 +
+                                          lane_c * 16) = v;
             }
         }
         __syncthreads();
         constexpr int NC = D / 64;  // 16-byte vectors of a row of bounds, to a lane
-        const int32_t* table = a.table + static_cast<size_t>(b) * a.max_pages;
-        for (int p0 = lo + warp * 16; p0 < hi; p0 += kSelWarps * 16) {
-            uint4 x[2][2][NC];  // [page g, g + 8][hi, lo]
-            float size[2];
-            bool none[2];
+        // A tile's loads: the bounds of pages g and g + 8, their exponents.
+        uint4 x[2][2][NC];  // [page g, g + 8][hi, lo]
+        uint8_t exps[2];
+        unsigned missing = 0;  // bits of pages that are not in the pool
+        auto fetch = [&](int p0) {
+            missing = 0;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                int page = table[min(p0 + g + 8 * r, hi - 1)];
-                none[r] = page < 0 || page >= a.num_pages;
-                if (none[r]) {
+                int page = pages[min(p0 + g + 8 * r, hi - 1) - lo];
+                if (page < 0 || page >= a.num_pages) {
                     report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                    missing |= 1u << r;
                     page = 0;
                 }
                 const size_t at = static_cast<size_t>(page) * a.Hkv + hk;
@@ -463,13 +553,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
 #pragma unroll
                     for (int j = 0; j < NC; ++j)
                         x[r][h][j] = ptx::ld_stream(a.bounds + at * 2 * D + h * D + j * 64 + c * 16);
-                size[r] = scale_of(a.exps[at]);
+                exps[r] = a.exps[at];
             }
+        };
+        if (lo + warp * 16 < hi) fetch(lo + warp * 16);
+        for (int p0 = lo + warp * 16; p0 < hi; p0 += kSelWarps * 16) {
+            const float size[2] = {scale_of(exps[0]), scale_of(exps[1])};
+            const bool none[2] = {(missing & 1u) != 0, (missing & 2u) != 0};
             __syncwarp();
-            for (int n0 = 0; n0 < tiles; n0 += kTilesAtOnce) {
-                float acc[kTilesAtOnce][4];
+            for (int n0 = 0; n0 < tiles; n0 += TILES) {
+                float acc[TILES][4];
 #pragma unroll
-                for (int n = 0; n < kTilesAtOnce; ++n)
+                for (int n = 0; n < TILES; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
 #pragma unroll
@@ -486,22 +581,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
                                               f[h][r], f[h][r + 2]);
                             }
 #pragma unroll
-                        for (int n = 0; n < kTilesAtOnce; ++n) {
-                            if (n0 + n >= tiles) break;
-                            const uint2 q = *reinterpret_cast<const uint2*>(
-                                codes + static_cast<size_t>((n0 + n) * 8 + g) * kStride + j * 64 +
-                                c * 16 + w * 4);
-                            ptx::mma_sync_f16(acc[n], f[0][0], f[0][1], f[0][2], f[0][3],
-                                              max0_f16x2(q.x), max0_f16x2(q.y));
-                            ptx::mma_sync_f16(acc[n], f[1][0], f[1][1], f[1][2], f[1][3],
-                                              min0_f16x2(q.x), min0_f16x2(q.y));
+                        for (int n = 0; n < TILES; ++n) {
+                            const uint4 q = *reinterpret_cast<const uint4*>(
+                                codes + ((n0 + n) * 8 + g) * kStride + (j * 4 + w) * 64 + c * 16);
+                            ptx::mma_sync_f16(acc[n], f[0][0], f[0][1], f[0][2], f[0][3], q.x, q.y);
+                            ptx::mma_sync_f16(acc[n], f[1][0], f[1][1], f[1][2], f[1][3], q.z, q.w);
                         }
                     }
                 }
+                // The next tile's loads, once this one's bounds have been used.
+                if (n0 + TILES >= tiles && p0 + kSelWarps * 16 < hi) fetch(p0 + kSelWarps * 16);
                 // The largest of each token's columns.
 #pragma unroll
-                for (int n = 0; n < kTilesAtOnce; ++n) {
-                    if (n0 + n >= tiles) break;
+                for (int n = 0; n < TILES; ++n) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float y0 = acc[n][2 * r], y1 = acc[n][2 * r + 1];
@@ -509,12 +601,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
                         if (a.cols > 2) y0 = fmaxf(y0, __shfl_xor_sync(kFull, y0, 1));
                         if (a.cols > 4) y0 = fmaxf(y0, __shfl_xor_sync(kFull, y0, 2));
                         const int i = p0 + g + 8 * r;
-                        const bool forced = i < a.n_first || i >= nb - a.n_last;
                         auto put = [&](int t, float y, bool again) {
                             if (i >= hi || t >= nt) return;
                             uint32_t* to = scores + static_cast<size_t>(t) * a.per_most + (i - lo);
-                            const uint32_t k =
-                                forced ? 0xffffffffu : none[r] ? 0u : score_key(y * size[r]);
+                            const uint32_t k = none[r] ? 1u : score_key(y * size[r]);
                             *to = again ? max(*to, k) : k;
                         };
                         const int col = (n0 + n) * 8 + 2 * c;
@@ -533,8 +623,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
         ptx::cluster_sync();
     else
         __syncthreads();
-    // Tokens are shared out over the cluster's CTAs, and within a CTA over its
-    // warps where there are several.
+    // Tokens are shared out over the cluster's CTAs, and a CTA's over its warps.
     Keys key;
     key.per = per;
     key.remote = S > 1;
@@ -548,16 +637,30 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
         for (int i = tid; i < a.n_select; i += kSelThreads)
             if (i >= k || nb == k) out[i] = i < k ? i : -1;
     }
-    if (nb > a.n_select) {
-        if (nt > S) {
-            for (int t = rank + S * warp; t < nt; t += S * kSelWarps) {
+    if (nb > a.n_select) {  // (so the first and the last ones do not meet)
+        const int here = (nt - rank + S - 1) / S;  // tokens of this CTA
+        auto take = [&](auto warps, auto in_registers) {
+            constexpr int NW = decltype(warps)::value;
+            const int group = warp / NW;
+            for (int t = rank + S * group; t < nt; t += S * (kSelWarps / NW)) {
                 key.at = ptx::smem_u32(scores + static_cast<size_t>(t) * a.per_most);
-                take_highest<1>(key, nb, k, row_of(t), hist + 256 * warp, counts, lane);
+                take_highest<NW, decltype(in_registers)::value>(
+                    key, nb, a.n_first, nb - a.n_last, k - a.n_first - a.n_last, row_of(t),
+                    scratch[group], group, tid % (32 * NW));
             }
-        } else if (rank < nt) {
-            key.at = ptx::smem_u32(scores + static_cast<size_t>(rank) * a.per_most);
-            take_highest<kSelWarps>(key, nb, k, row_of(rank), hist, counts, tid);
-        }
+        };
+        using std::integral_constant;
+        constexpr int kOf = 32 * kHeld;  // keys that a warp holds
+        if (here >= 8 && nb <= kOf)
+            take(integral_constant<int, 1>(), std::true_type());
+        else if (here >= 3 && nb <= 2 * kOf)
+            take(integral_constant<int, 2>(), std::true_type());
+        else if (here >= 2 && nb <= 4 * kOf)
+            take(integral_constant<int, 4>(), std::true_type());
+        else if (nb <= 8 * kOf)
+            take(integral_constant<int, 8>(), std::true_type());
+        else
+            take(integral_constant<int, 8>(), std::false_type());
     }
     if (S > 1) ptx::cluster_sync();  // (other CTAs may still read this one's scores)
 }
@@ -580,6 +683,13 @@ bool cache_shape_ok(int B, int Hkv, int d, int max_pages, int P, int num_pages) 
 }
 
 constexpr int kMaxSelectPages = 262144;
+
+// Column tiles of so many columns that share a conversion, and how many there are then.
+int tiles_at_once(int columns) { return columns <= 8 ? 1 : columns <= 16 ? 2 : 4; }
+int padded_tiles(int columns) {
+    const int n = tiles_at_once(columns);
+    return ((columns + 7) / 8 + n - 1) / n * n;
+}
 
 }  // namespace
 }  // namespace treeattn
@@ -670,14 +780,14 @@ int tree_select_blocks(const uint16_t* q, const int8_t* bounds, const uint8_t* b
     int S = 1;
     while (S < 8 && 2LL * S * B * Hkv <= 2LL * sms && max_pages_per_seq >= 2 * S * 64) S *= 2;
     // Tokens of a CTA: all, unless its scores or its query codes get too large.
-    const size_t code_row = static_cast<size_t>(d + 4) * 2;
+    const size_t code_row = static_cast<size_t>(4 * d + 64);
     int TC = T;
     size_t need = 0;
     for (;; TC = (TC + 1) / 2) {
         a.per_most = ((max_pages_per_seq + S - 1) / S + 3) / 4 * 4;
-        need = static_cast<size_t>(TC) * a.per_most * 4 + (256 + 2) * kSelWarps * 4 +
-               static_cast<size_t>((TC * a.cols + 7) / 8 * 8) * code_row;
-        if (need <= (TC == 1 ? 200u * 1024u : 100u * 1024u)) break;
+        need = static_cast<size_t>(TC + 1) * a.per_most * 4 + kSelWarps * sizeof(Scratch) +
+               static_cast<size_t>(padded_tiles(TC * a.cols) * 8) * code_row;
+        if (need <= (TC == 1 ? 200u * 1024u : 72u * 1024u)) break;  // (three CTAs to an SM)
         if (TC == 1) {  // one token of a very long sequence: more CTAs share its pages
             if (S == 8) return TREE_ATTN_ERR_SHAPE;
             S *= 2;
@@ -685,11 +795,21 @@ int tree_select_blocks(const uint16_t* q, const int8_t* bounds, const uint8_t* b
         }
     }
     a.TC = TC;
+    a.B = B;
+    a.longest_first = B > 1 && B <= kSelThreads &&
+                      static_cast<long long>(B) * Hkv * ((T + TC - 1) / TC) > 2LL * sms;
     a.chunks = (T + TC - 1) / TC;
     const long long grid = static_cast<long long>(B) * Hkv * a.chunks * S;
     if (grid >= (1LL << 31)) return TREE_ATTN_ERR_SHAPE;
     using Kernel = void (*)(SelectArgs);
-    const Kernel kernel = d == 128 ? select_kernel<128> : select_kernel<64>;
+    const int at_once = tiles_at_once(TC * a.cols);
+    const Kernel kernel =
+        d == 128 ? (at_once == 1   ? select_kernel<128, 1>
+                    : at_once == 2 ? select_kernel<128, 2>
+                                   : select_kernel<128, 4>)
+                 : (at_once == 1   ? select_kernel<64, 1>
+                    : at_once == 2 ? select_kernel<64, 2>
+                                   : select_kernel<64, 4>);
     if (need > 48 * 1024 &&
         cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                              cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -72,4 +72,28 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
 }
 
 }  // namespace ptx
+
+// The sequence that is `rank`-th by length, longest first (equal ones in order): units
+// that begin late should end soon.  For n <= blockDim.x sequences, by all threads;
+// `scratch` holds n + 1 ints and is free again afterwards.
+__device__ __forceinline__ int by_length(const int32_t* lens, int n, int rank, int* scratch) {
+    const int tid = static_cast<int>(threadIdx.x);
+    const int mine = tid < n ? lens[tid] : 0;
+    if (tid < n) scratch[tid] = mine;
+    __syncthreads();
+    if (tid < n) {
+        int before = 0;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const int other = scratch[i];
+            before += other > mine || (other == mine && i < tid);
+        }
+        if (before == rank) scratch[n] = tid;
+    }
+    __syncthreads();
+    const int found = scratch[n];
+    __syncthreads();
+    return found;
+}
+
 }  // namespace treeattn

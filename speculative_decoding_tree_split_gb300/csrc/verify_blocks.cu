@@ -715,25 +715,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     unit /= a.groups;
     const int hk = unit % a.Hkv;
     int b = unit / a.Hkv;
-    if (a.longest_first) {  // b-th by length (units that come late should end soon)
-        int* lens = reinterpret_cast<int*>(sm.entries);
-        int* found = sm.sums;
-        const int mine = tid < a.B ? a.lens[tid] : 0;
-        if (tid < a.B) lens[tid] = mine;
-        __syncthreads();
-        if (tid < a.B) {
-            int before = 0;
-#pragma unroll 8
-            for (int i = 0; i < a.B; ++i) {
-                const int other = lens[i];
-                before += other > mine || (other == mine && i < tid);
-            }
-            if (before == b) *found = tid;
-        }
-        __syncthreads();
-        b = *found;
-        __syncthreads();
-    }
+    if (a.longest_first) b = by_length(a.lens, a.B, b, reinterpret_cast<int*>(sm.entries));
     const int G = a.Hq / a.Hkv;
     const int nt = min(a.tokens, a.T - t0);
     const int per_token = min(G - rb * R, R);  // rows
@@ -1001,7 +983,7 @@ int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ER
 
 template <int D, bool FP8, int NT>
 int launch(Args a, long long units, int sms, cudaStream_t stream) {
-    const size_t smem = sizeof(Smem<D, FP8, NT>) + kThreads * sizeof(int) +
+    const size_t smem = sizeof(Smem<D, FP8, NT>) + (kThreads + 1) * sizeof(int) +
                         static_cast<size_t>(a.tokens) * a.n_blocks * sizeof(Entry);
     const auto kernel = blocks_kernel<D, FP8, NT>;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
