@@ -34,83 +34,6 @@ __device__ __forceinline__ void report(int32_t* status, int code) {
 }
 
 // ---------------------------------------------------------------------------
-// Copies: page src[k] of every pool to its page dst[k].  A warp moves 4 KB at a
-// time, eight 16-byte vectors to a lane, all loaded before the first is stored.
-// ---------------------------------------------------------------------------
-constexpr int kPoolsMost = 120;  // of one launch
-constexpr int kPiece = 4096;     // bytes a warp moves at a time
-constexpr int kCopyThreads = 256;
-
-struct CopyArgs {
-    uint8_t* pool[kPoolsMost];
-    long long bytes[kPoolsMost];  // of one page
-    int first[kPoolsMost + 1];    // first piece of each pool within a page's
-    const int32_t* src;
-    const int32_t* dst;
-    const int32_t* count;  // nullable: n
-    int n, n_pools, num_pages;
-    int32_t* status;
-};
-
-__device__ __forceinline__ uint4 ld_once(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    const int lane = threadIdx.x & 31;
-    const int n = a.count != nullptr ? min(max(*a.count, 0), a.n) : a.n;
-    const int per = a.first[a.n_pools];
-    const int warps = gridDim.x * (kCopyThreads / 32);
-    const int step_k = warps / per, step_c = warps % per;
-    const int w0 = blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32;
-    int k = w0 / per, c = w0 % per;
-    while (k < n) {
-        const int s = a.src[k], d = a.dst[k];
-        if (s >= 0 && d >= 0 && s < a.num_pages && d < a.num_pages) {
-            int lo = 0, hi = a.n_pools - 1;  // the pool that piece c belongs to
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (a.first[mid] <= c)
-                    lo = mid;
-                else
-                    hi = mid - 1;
-            }
-            const long long page = a.bytes[lo];
-            const long long at = static_cast<long long>(c - a.first[lo]) * kPiece;
-            const int m = static_cast<int>(min(page - at, static_cast<long long>(kPiece)));
-            const uint8_t* from = a.pool[lo] + s * page + at;
-            uint8_t* to = a.pool[lo] + d * page + at;
-            if (((page | reinterpret_cast<uintptr_t>(a.pool[lo])) & 15) == 0) {
-                uint4 v[kPiece / 512];
-#pragma unroll
-                for (int i = 0; i < kPiece / 512; ++i)
-                    if (i * 512 + lane * 16 < m) v[i] = ld_once(from + i * 512 + lane * 16);
-#pragma unroll
-                for (int i = 0; i < kPiece / 512; ++i)
-                    if (i * 512 + lane * 16 < m)
-                        *reinterpret_cast<uint4*>(to + i * 512 + lane * 16) = v[i];
-            } else {
-                for (int i = lane; i < m; i += 32) to[i] = from[i];
-            }
-        } else if (lane == 0 && (s < -1 || d < -1 || s >= a.num_pages || d >= a.num_pages)) {
-            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-        }
-        k += step_k;
-        c += step_c;
-        if (c >= per) {
-            c -= per;
-            ++k;
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
 // What both plans use: prefix sums of one CTA, and runs over the page counts.
 // ---------------------------------------------------------------------------
 
@@ -169,6 +92,7 @@ struct ForkArgs {
     int32_t* copy_src;  // [rows_out]
     int32_t* copy_dst;  // [rows_out]
     int32_t* count;     // [1]
+    int32_t* free_all;  // [1] free pages
     int32_t* free_of;   // [kMaxCtas] free pages of each CTA's part
     int32_t* children;  // [rows_in]
     int32_t* eldest;    // [rows_in]
@@ -187,7 +111,7 @@ struct Row {
 
 __device__ __forceinline__ bool entry_ok(int e, int num_pages) { return e >= 0 && e < num_pages; }
 
-__device__ __forceinline__ Row row_of(const ForkArgs& a, int i) {
+__device__ __forceinline__ Row row_of(const ForkArgs& a, int i, const int32_t* eldest) {
     Row r;
     r.parent = a.src[i];
     r.L = r.full = r.need = 0;
@@ -200,7 +124,7 @@ __device__ __forceinline__ Row row_of(const ForkArgs& a, int i) {
     bool bad = false;
     if (r.parent >= 0) {
         r.L = clamp_seq_len(a.lens[r.parent], a.P, a.max_pages, bad);
-        r.eldest = __ldcg(a.eldest + r.parent) == i;
+        r.eldest = eldest[r.parent] == i;
     }
     if (bad) {
         report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
@@ -220,10 +144,16 @@ __device__ __forceinline__ bool keeps(const ForkArgs& a, const Row& r, int e) {
     return r.eldest && entry_ok(e, a.num_pages) && a.refs[e] == 1;
 }
 
+// Rows whose children and eldest child a CTA keeps in shared memory.
+constexpr int kHeldRows = 4096;
+
+// The plan: new pages of every row, and which pages are copied.  The table itself is made
+// beside the copies (fork_row, fork_release).
 __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     __shared__ int sums[kPlanWarps];
+    __shared__ int children[kHeldRows], eldest[kHeldRows];
     const int tid = threadIdx.x, lane = tid & 31;
     const int ctas = static_cast<int>(ptx::cluster_size());
     const int rank = static_cast<int>(ptx::cluster_rank());
@@ -232,34 +162,56 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
     int lo, hi;
     my_pages(a.num_pages, lo, hi);
 
-    // Counts carried over, free pages counted, rows' children reset.
+    // Counts carried over, free pages counted; every row's children.  Where rows are not
+    // too many, each CTA finds all of them for itself.
+    const bool held = a.rows_in <= kHeldRows;
+    if (held) {
+        for (int p = tid; p < a.rows_in; p += kPlanThreads) {
+            children[p] = 0;
+            eldest[p] = 0x7fffffff;
+        }
+        __syncthreads();
+        for (int i = tid; i < a.rows_out; i += kPlanThreads) {
+            const int p = a.src[i];
+            if (p >= 0 && p < a.rows_in) {
+                atomicAdd(children + p, 1);
+                atomicMin(eldest + p, i);
+            }
+        }
+    } else {
+        for (int p = gtid; p < a.rows_in; p += gthreads) {
+            a.children[p] = 0;
+            a.eldest[p] = 0x7fffffff;
+        }
+        ptx::cluster_sync();
+        for (int i = gtid; i < a.rows_out; i += gthreads) {
+            const int p = a.src[i];
+            if (p >= 0 && p < a.rows_in) {
+                atomicAdd(a.children + p, 1);
+                atomicMin(a.eldest + p, i);
+            }
+        }
+        ptx::cluster_sync();
+    }
     int mine = 0;
+#pragma unroll 4
     for (int p = lo + tid; p < hi; p += kPlanThreads) {
         const int c = a.refs[p];
         a.refs_out[p] = c;
         mine += c == 0;
     }
     int free_here;
-    block_scan(mine, sums, free_here);
+    block_scan(mine, sums, free_here);  // (and all threads are past the atomics)
     if (tid == 0) a.free_of[rank] = free_here;
-    for (int p = gtid; p < a.rows_in; p += gthreads) {
-        a.children[p] = 0;
-        a.eldest[p] = 0x7fffffff;
-    }
-    ptx::cluster_sync();
-
-    for (int i = gtid; i < a.rows_out; i += gthreads) {
-        const int p = a.src[i];
-        if (p >= 0 && p < a.rows_in) {
-            atomicAdd(a.children + p, 1);
-            atomicMin(a.eldest + p, i);
+    if (held) {
+        for (int p = gtid; p < a.rows_in; p += gthreads) {
+            a.children[p] = children[p];
+            a.eldest[p] = eldest[p];
         }
     }
-    ptx::cluster_sync();
-
     // New pages that each row wants.
     for (int i = gwarp; i < a.rows_out; i += gwarps) {
-        const Row r = row_of(a, i);
+        const Row r = row_of(a, i, held ? eldest : a.eldest);
         int n = 0;
         bool copy = false;
         for (int s0 = r.full; s0 < r.need; s0 += 32) {
@@ -321,65 +273,170 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
     }
     if (gtid == 0) {
         *a.count = copies;
+        *a.free_all = free_all;
         if (total > free_all) report(a.status, TREE_ATTN_STATUS_NO_PAGE);
     }
     ptx::cluster_sync();
 
-    // The new table, and the counts of entries that come and go.
-    for (int i = gwarp; i < a.rows_out; i += gwarps) {
-        const Row r = row_of(a, i);
-        const int32_t* from = a.table + static_cast<size_t>(max(r.parent, 0)) * a.max_pages;
-        int32_t* to = a.table_out + static_cast<size_t>(i) * a.max_pages;
-        int next = __ldcg(a.base + i);
+    // Lengths, and the pages that are copied.
+    for (int i = gtid; i < a.rows_out; i += gthreads) {
+        const Row r = row_of(a, i, held ? eldest : a.eldest);
         int L = r.L;
-        for (int s0 = 0; s0 < a.max_pages; s0 += 32) {
-            const int s = s0 + lane;
-            int e = -1;
-            bool fresh = false;
-            if (s < r.need) {
-                e = r.parent >= 0 ? from[s] : -1;
-                if (s < r.full) {
-                    if (!entry_ok(e, a.num_pages)) {
-                        report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-                        e = -1;
-                    }
-                } else {
-                    fresh = !keeps(a, r, e);
-                }
-            }
-            const unsigned who = __ballot_sync(kFull, fresh);
-            if (fresh) {
-                const int k = next + __popc(who & ((1u << lane) - 1u));
-                const int page = k < free_all ? __ldcg(a.list + k) : -1;
-                if (s == r.full && r.L % a.P != 0) {
-                    const int c = __ldcg(a.copies + i);
-                    if (!entry_ok(e, a.num_pages)) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-                    a.copy_src[c] = page >= 0 && entry_ok(e, a.num_pages) ? e : -1;
-                    a.copy_dst[c] = page;
-                    if (page < 0) L = r.full * a.P;  // the tokens that found no page
-                }
-                e = page;
-            }
-            if (s >= r.full && e >= 0) atomicAdd(a.refs_out + e, 1);
-            if (s < a.max_pages) to[s] = e;
-            next += __popc(who);
+        if (__ldcg(a.wants + i) >> 30 != 0) {  // its first new page takes tokens
+            const int k = __ldcg(a.base + i), c = __ldcg(a.copies + i);
+            const int to = k < free_all ? __ldcg(a.list + k) : -1;
+            const int from = a.table[static_cast<size_t>(r.parent) * a.max_pages + r.full];
+            const bool ok = entry_ok(from, a.num_pages);
+            if (!ok) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+            a.copy_src[c] = ok && to >= 0 ? from : -1;
+            a.copy_dst[c] = to;
+            if (to < 0) L = r.full * a.P;  // the tokens that found no page
         }
-        L = __reduce_min_sync(kFull, L);
-        if (lane == 0) a.lens_out[i] = L;
+        a.lens_out[i] = L;
     }
-    for (int p = gwarp; p < a.rows_in; p += gwarps) {
-        bool bad;
-        const int L = clamp_seq_len(a.lens[p], a.P, a.max_pages, bad);
-        const int full = bad ? 0 : L / a.P;
-        const int kept = __ldcg(a.children + p) - 1;  // for shared pages
-        const int32_t* from = a.table + static_cast<size_t>(p) * a.max_pages;
-        for (int s = (kept == 0 ? full : 0) + lane; s < a.max_pages; s += 32) {
-            const int e = from[s];
-            const int more = s < full ? kept : -1;
-            if (entry_ok(e, a.num_pages))
-                atomicAdd(a.refs_out + e, more);
-            else if (e != -1)
-                report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+}
+
+// One warp: row i of the new table, and the counts of its own pages.
+__device__ __forceinline__ void fork_row(const ForkArgs& a, int i) {
+    const int lane = threadIdx.x & 31;
+    const Row r = row_of(a, i, a.eldest);
+    const int32_t* from = a.table + static_cast<size_t>(max(r.parent, 0)) * a.max_pages;
+    int32_t* to = a.table_out + static_cast<size_t>(i) * a.max_pages;
+    int next = a.base[i];
+    const int free_all = *a.free_all;
+#pragma unroll 4
+    for (int s = lane; s < a.max_pages; s += 32) {  // the shared ones
+        if (s >= r.full && s < r.need) continue;
+        int e = s < r.full ? from[s] : -1;
+        if (s < r.full && !entry_ok(e, a.num_pages)) {
+            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+            e = -1;
+        }
+        to[s] = e;
+    }
+    __syncwarp();
+    for (int s0 = r.full; s0 < r.need; s0 += 32) {
+        const int s = s0 + lane;
+        int e = s < r.need && r.parent >= 0 ? from[s] : -1;
+        const bool fresh = s < r.need && !keeps(a, r, e);
+        const unsigned who = __ballot_sync(kFull, fresh);
+        if (fresh) {
+            const int k = next + __popc(who & ((1u << lane) - 1u));
+            e = k < free_all ? a.list[k] : -1;
+        }
+        if (s < r.need) {
+            if (e >= 0) atomicAdd(a.refs_out + e, 1);
+            to[s] = e;
+        }
+        next += __popc(who);
+    }
+}
+
+// One warp: the counts of what row p had.
+__device__ __forceinline__ void fork_release(const ForkArgs& a, int p) {
+    bool bad;
+    const int L = clamp_seq_len(a.lens[p], a.P, a.max_pages, bad);
+    const int full = bad ? 0 : L / a.P;
+    const int kept = a.children[p] - 1;  // for shared pages
+    const int32_t* from = a.table + static_cast<size_t>(p) * a.max_pages;
+#pragma unroll 4
+    for (int s = (kept == 0 ? full : 0) + (threadIdx.x & 31); s < a.max_pages; s += 32) {
+        const int e = from[s];
+        if (entry_ok(e, a.num_pages))
+            atomicAdd(a.refs_out + e, s < full ? kept : -1);
+        else if (e != -1)
+            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Copies: page src[k] of every pool to its page dst[k].  A warp moves 4 KB at a
+// time, eight 16-byte vectors to a lane, all loaded before the first is stored.
+// ---------------------------------------------------------------------------
+constexpr int kPoolsMost = 120;  // of one launch
+constexpr int kPiece = 4096;     // bytes a warp moves at a time
+constexpr int kCopyThreads = 256;
+
+struct CopyArgs {
+    uint8_t* pool[kPoolsMost];
+    long long bytes[kPoolsMost];  // of one page
+    int first[kPoolsMost + 1];    // first piece of each pool within a page's
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* count;  // nullable: n
+    int n, n_pools, num_pages;
+    int32_t* status;
+};
+
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// FORK: the first warps make the rows of a fork's table as well.
+template <bool FORK>
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ ForkArgs f) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    if (FORK) {
+        const int warps = gridDim.x * (kCopyThreads / 32);
+        // (from the last warp on: the first ones have the most copies)
+        for (int i = warps - 1 - (blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32);
+             i < f.rows_out + f.rows_in; i += warps) {
+            if (i < f.rows_out)
+                fork_row(f, i);
+            else
+                fork_release(f, i - f.rows_out);
+        }
+        if (a.n_pools == 0) return;
+    }
+    const int n = a.count != nullptr ? min(max(*a.count, 0), a.n) : a.n;
+    const int per = a.first[a.n_pools];
+    const int warps = gridDim.x * (kCopyThreads / 32);
+    const int step_k = warps / per, step_c = warps % per;
+    const int w0 = blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32;
+    int k = w0 / per, c = w0 % per;
+    while (k < n) {
+        const int s = a.src[k], d = a.dst[k];
+        if (s >= 0 && d >= 0 && s < a.num_pages && d < a.num_pages) {
+            int lo = 0, hi = a.n_pools - 1;  // the pool that piece c belongs to
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (a.first[mid] <= c)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const long long page = a.bytes[lo];
+            const long long at = static_cast<long long>(c - a.first[lo]) * kPiece;
+            const int m = static_cast<int>(min(page - at, static_cast<long long>(kPiece)));
+            const uint8_t* from = a.pool[lo] + s * page + at;
+            uint8_t* to = a.pool[lo] + d * page + at;
+            if (((page | reinterpret_cast<uintptr_t>(a.pool[lo])) & 15) == 0) {
+                uint4 v[kPiece / 512];
+#pragma unroll
+                for (int i = 0; i < kPiece / 512; ++i)
+                    if (i * 512 + lane * 16 < m) v[i] = ld_once(from + i * 512 + lane * 16);
+#pragma unroll
+                for (int i = 0; i < kPiece / 512; ++i)
+                    if (i * 512 + lane * 16 < m)
+                        *reinterpret_cast<uint4*>(to + i * 512 + lane * 16) = v[i];
+            } else {
+                for (int i = lane; i < m; i += 32) to[i] = from[i];
+            }
+        } else if (lane == 0 && (s < -1 || d < -1 || s >= a.num_pages || d >= a.num_pages)) {
+            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+        }
+        k += step_k;
+        c += step_c;
+        if (c >= per) {
+            c -= per;
+            ++k;
         }
     }
 }
@@ -519,8 +576,10 @@ int check_pools(void* const* pools, const size_t* page_bytes, int n_pools) {
 // Pools in launches of at most kPoolsMost.
 int enqueue_copies(void* const* pools, const size_t* page_bytes, int n_pools, const int32_t* src,
                    const int32_t* dst, const int32_t* count, int n, int num_pages,
-                   int32_t* status, cudaStream_t stream) {
-    if (n == 0) return TREE_ATTN_OK;
+                   int32_t* status, cudaStream_t stream, const ForkArgs* fork = nullptr) {
+    const long long rows =
+        fork != nullptr ? static_cast<long long>(fork->rows_in) + fork->rows_out : 0;
+    if (n == 0 && rows == 0) return TREE_ATTN_OK;
     const int sms = sm_count();
     if (sms == 0) return TREE_ATTN_ERR_CUDA;
     CopyArgs a;
@@ -530,7 +589,7 @@ int enqueue_copies(void* const* pools, const size_t* page_bytes, int n_pools, co
     a.n = n;
     a.num_pages = num_pages;
     a.status = status;
-    for (int i = 0; i < n_pools;) {
+    for (int i = 0; i < n_pools || fork != nullptr;) {
         long long pieces = 0;
         int m = 0;
         for (; i < n_pools && m < kPoolsMost; ++i, ++m) {
@@ -544,12 +603,19 @@ int enqueue_copies(void* const* pools, const size_t* page_bytes, int n_pools, co
         a.first[m] = static_cast<int>(pieces);
         a.n_pools = m;
         // As many CTAs as the SMs hold at once: they take the pieces in turn.
-        const long long warps = pieces * n;
+        long long warps = pieces * n;
+        if (fork != nullptr && warps < rows) warps = rows;
         const long long ctas = (warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
         const int grid = static_cast<int>(ctas < 8LL * sms ? ctas : 8LL * sms);
-        const int rc = rc_of(launch_dependent(copy_kernel, dim3(grid), dim3(kCopyThreads), 0,
-                                              stream, a));
+        if (grid == 0) return TREE_ATTN_OK;
+        const int rc =
+            fork != nullptr
+                ? rc_of(launch_dependent(copy_kernel<true>, dim3(grid), dim3(kCopyThreads), 0,
+                                         stream, a, *fork))
+                : rc_of(launch_dependent(copy_kernel<false>, dim3(grid), dim3(kCopyThreads), 0,
+                                         stream, a, ForkArgs()));
         if (rc != TREE_ATTN_OK) return rc;
+        fork = nullptr;  // (its rows are made once)
     }
     return TREE_ATTN_OK;
 }
@@ -640,6 +706,7 @@ int tree_kv_fork(void* const* pools, const size_t* page_bytes, int n_pools,
     a.num_pages = num_pages;
     int32_t* w = static_cast<int32_t*>(workspace);
     a.count = w;
+    a.free_all = w + 1;
     a.free_of = w + 32;
     w += 64;
     a.children = w;
@@ -659,9 +726,9 @@ int tree_kv_fork(void* const* pools, const size_t* page_bytes, int n_pools,
     const int ctas = plan_ctas(work);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int rp = rc_of(launch_cluster(fork_kernel, dim3(ctas), dim3(kPlanThreads), 0, ctas, s, a));
-    if (rp != TREE_ATTN_OK || n_pools == 0) return rp;
+    if (rp != TREE_ATTN_OK) return rp;
     return enqueue_copies(pools, page_bytes, n_pools, a.copy_src, a.copy_dst, a.count, rows_out,
-                          num_pages, status, s);
+                          num_pages, status, s, &a);
 }
 
 size_t tree_kv_compact_workspace_size(int num_pages) {
