@@ -237,9 +237,25 @@ __device__ __forceinline__ void copies_wait() {
     __syncwarp();
 }
 
-// One warp copies a tile, row r from row(r).
+// One warp copies a tile of rows next to one another, 512 bytes at a time.  Where a
+// lane's chunk goes changes in few bits from one time to the next.
+template <int RB, bool V>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* src) {
+    constexpr int kChunks = RB / 16;
+    const int lane = threadIdx.x & 31;
+    const int at = chunk_at<RB, V>(lane / kChunks, lane % kChunks);
+    src += lane * 16;
+#pragma unroll
+    for (int i = 0; i < RB * kTile / 512; ++i) {
+        // Row lane / kChunks + 32 / kChunks * i: what that adds to (row / 2) % 4.
+        const int turn = !V || RB < 128 ? 0 : RB == 128 ? (i & 1) * 64 : (i & 3) * 32;
+        copy16(dst + (at ^ turn) + i * 512, src + i * 512);
+    }
+}
+
+// The same with row r from row(r).
 template <int RB, bool V, typename Row>
-__device__ __forceinline__ void copy_tile(uint32_t dst, Row row) {
+__device__ __forceinline__ void copy_rows(uint32_t dst, Row row) {
     constexpr int kChunks = RB / 16;
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -490,7 +506,7 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
             const int first = sm.entries[ahead].row + off;
             const uint8_t* base =
                 static_cast<const uint8_t*>(a.kv[V ? 1 : 0]) + static_cast<size_t>(first) * RB;
-            copy_tile<RB, V>(slot, [&](int r) { return base + r * RB; });
+            copy_tile<RB, V>(slot, base);
             if (FP8 && lane == 0) copy16(slot + kTile * RB, a.scales[V ? 1 : 0] + first);
             if (V) ahead = skip(ahead + e_step);
         }
@@ -637,8 +653,8 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
                 };
                 const uint32_t v_at = ring + kTile * 2 * D;
                 __syncwarp();  // (the ring has been read)
-                copy_tile<2 * D, false>(ring, [&](int r) { return from(a.tree[0], r); });
-                copy_tile<2 * D, true>(v_at, [&](int r) { return from(a.tree[1], r); });
+                copy_rows<2 * D, false>(ring, [&](int r) { return from(a.tree[0], r); });
+                copy_rows<2 * D, true>(v_at, [&](int r) { return from(a.tree[1], r); });
                 copies_commit();
                 copies_wait<0>();
                 float x[NT][4];
@@ -738,11 +754,15 @@ __global__ void __launch_bounds__(kThreads, kResident)
     const int j_mine = tid < n_listed ? listed(tid) : -1;
     const int j_then = nt == 1 && tid + 1 < n_listed ? listed(tid + 1) : -1;
     constexpr int kVecs = D / 8;  // 16-byte vectors of a row, one to a lane
-    static_assert(R * kVecs <= kThreads, "one vector of the queries to a thread");
-    const int q_row = tid / kVecs;
-    uint4 q_mine = make_uint4(0u, 0u, 0u, 0u);
-    if (q_row < rows)
-        q_mine = *reinterpret_cast<const uint4*>(a.q + row_of(q_row) * D + tid % kVecs * 8);
+    constexpr int kTurns = (R * kVecs + kThreads - 1) / kThreads;
+    uint4 q_mine[kTurns];
+#pragma unroll
+    for (int h = 0; h < kTurns; ++h) {
+        const int r = (tid + h * kThreads) / kVecs;
+        q_mine[h] = r < rows
+                        ? *reinterpret_cast<const uint4*>(a.q + row_of(r) * D + tid % kVecs * 8)
+                        : make_uint4(0u, 0u, 0u, 0u);
+    }
     const int32_t* up = a.parents + static_cast<size_t>(b) * a.parents_stride;
     const int p0 = a.mask == nullptr && lane < a.T ? up[lane] : -1;
     const int p1 = a.mask == nullptr && lane + 32 < a.T ? up[lane + 32] : -1;
@@ -846,9 +866,11 @@ __global__ void __launch_bounds__(kThreads, kResident)
     // ---- queries, as the product's second operand (8-bit cache: in fp16, scaled so that
     // the row's largest lies in [2^14, 2^15): exact down to 2^-28 of it, and to 2^-39 of
     // it below; and in bf16 for the tree)
-    if (q_row < R) {
-        const int r = q_row, i = tid % kVecs;
-        uint4 x = q_mine;
+#pragma unroll
+    for (int h = 0; h < kTurns; ++h) {
+        const int r = (tid + h * kThreads) / kVecs, i = tid % kVecs;
+        if (r >= R) break;
+        uint4 x = q_mine[h];
         if (a.scale_log2 < 0.0f) {  // score units are positive
             x.x ^= 0x80008000u;
             x.y ^= 0x80008000u;
