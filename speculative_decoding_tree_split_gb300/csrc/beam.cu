@@ -14,9 +14,9 @@
 // four lanes is known after the maximum; the K-th largest of those 64 is a bound
 // that at least K logits reach and few exceed.  Only logits above it are kept from
 // then on (one comparison per tile and thread as a rule).  Where more are kept than
-// there is room for -- logits that ascend, a first tile of -inf -- the piece is read
-// again with the bound of all its threads' largest logits, under which there is
-// always room.  Keys (logit, -index) are all different, so ties need no extra rule.
+// there is room for -- logits that ascend or are all equal, a first tile of -inf -- the
+// piece is read again with the bound of all its threads' largest logits, under which
+// there is always room, keys (logit, -index) being all different.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -25,6 +25,7 @@
 
 #include "../../include/tree_attn.h"
 #include "launch.cuh"
+#include "mma_sync.cuh"
 #include "ptx.cuh"
 
 namespace treeattn {
@@ -85,23 +86,45 @@ __device__ __forceinline__ unsigned long long full_key(float x, uint32_t index) 
                : (static_cast<unsigned long long>(key_of(x)) << 32) | (0xffffffffu - index);
 }
 
-// The K-th largest of the CTA's NT keys (0: none) in `tops`, 1 where there are
-// fewer; to be called by all threads, kThreads / NT of which look at one key.
-template <int NT>
-__device__ __forceinline__ void find_bound(const unsigned long long* tops, int K,
-                                           unsigned long long* bound) {
-    constexpr int P = kThreads / NT;
+// The K-th largest of the CTA's keys (0: none), one to a thread, 1 where there are fewer;
+// to be called by all threads.
+__device__ __forceinline__ unsigned long long find_bound(unsigned long long mine, int K,
+                                                         unsigned long long* tops,
+                                                         unsigned long long* bound) {
     const int tid = threadIdx.x;
+    tops[tid] = mine;
     if (tid == 0) *bound = 1;
     __syncthreads();
-    const unsigned long long t = tops[tid / P];
     int above = 0;
-#pragma unroll 16
-    for (int i = tid % P; i < NT; i += P) above += tops[i] > t;
-#pragma unroll
-    for (int off = 1; off < P; off <<= 1) above += __shfl_xor_sync(kFull, above, off);
-    if (t != 0 && above == K - 1) *bound = t;  // (one of P threads' equal stores)
+#pragma unroll 8
+    for (int i = 0; i < kThreads; ++i) above += tops[i] > mine;
+    if (mine != 0 && above == K - 1) *bound = mine;
     __syncthreads();
+    return *bound;
+}
+
+// The K-th largest of the largest numbers of the CTA's groups of four threads (K <= 64), by
+// all threads; -inf where fewer groups have any.
+__device__ __forceinline__ float group_bound(float top, int K, float* tops, uint32_t* bound) {
+    const int tid = threadIdx.x;
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+    if (tid % 4 == 0) tops[tid / 4] = top;
+    if (tid == 0) *bound = 0xffffffffu;
+    __syncthreads();
+    // (each thread of a group looks at a quarter of the others)
+    int above = 0;
+    const float4* quarter = reinterpret_cast<const float4*>(tops) + tid % 4 * (kThreads / 64);
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; ++i) {
+        const float4 t = quarter[i];
+        above += (t.x > top) + (t.y > top) + (t.z > top) + (t.w > top);
+    }
+    above += __shfl_xor_sync(kFull, above, 1);
+    above += __shfl_xor_sync(kFull, above, 2);
+    if (tid % 4 == 0 && above < K) atomicMin(bound, key_of(top + 0.0f));
+    __syncthreads();
+    return logit_of(*bound);
 }
 
 template <typename T>
@@ -123,7 +146,7 @@ struct Row {
     __device__ __forceinline__ void fetch(int first, uint4 (&raw)[kVecs]) const {
 #pragma unroll
         for (int u = 0; u < kVecs; ++u)
-            raw[u] = __ldcs(reinterpret_cast<const uint4*>(x + index(first, u * N)));
+            raw[u] = ptx::ld_stream(x + index(first, u * N));  // (volatile: asked for here)
     }
     __device__ __forceinline__ void unpack(const uint4 (&raw)[kVecs], float (&v)[kEach]) const {
 #pragma unroll
@@ -135,12 +158,6 @@ struct Row {
     }
     // Any tile; -inf for what is not in the row.
     __device__ __forceinline__ void load(int first, float (&v)[kEach]) const {
-        if (inside(first)) {
-            uint4 raw[kVecs];
-            fetch(first, raw);
-            unpack(raw, v);
-            return;
-        }
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int i = index(first, e);
@@ -153,13 +170,12 @@ struct Row {
         int at = 0;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            const float y = clean(v[e]);
-            if (y > top) {
-                top = y;
+            if (v[e] > top) {
+                top = v[e];
                 at = e;
             }
         }
-        return full_key(top, static_cast<uint32_t>(index(first, at)));
+        return full_key(clean(top), static_cast<uint32_t>(index(first, at)));
     }
 };
 
@@ -181,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
     __shared__ unsigned long long tops[kThreads];
     __shared__ float red[2][kWarps];
     __shared__ unsigned long long bound;
+    __shared__ uint32_t group_least;
     __shared__ int n_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.y, piece = blockIdx.x;
@@ -192,14 +209,24 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
     r.skew = static_cast<int>((reinterpret_cast<uintptr_t>(r.x) & 15) / sizeof(T));
     const int first = piece * a.tiles * kTile;
     if (tid == 0) n_kept = 0;
-    // Keeps those of a thread's logits (bits of `which`) that reach `least`: few, read
-    // again rather than held for it.
-    auto keep = [&](unsigned which, int at, unsigned long long least) {
+    // Keeps those of a thread's logits that exceed `above` (and reach `least`).
+    auto keep = [&](const float (&v)[kEach], int at, float above, unsigned long long least) {
+        unsigned which = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            if (v[e] > above) which |= 1u << e;
         while (which != 0) {
-            const int i = r.index(at, __ffs(which) - 1);
+            const int e = __ffs(which) - 1;
             which &= which - 1;
-            const unsigned long long k =
-                full_key(clean(as_float<T>(r.x[i])), static_cast<uint32_t>(i));
+            float y[kEach / 2];  // v[e], by halves
+#pragma unroll
+            for (int i = 0; i < kEach / 2; ++i) y[i] = (e & 1) != 0 ? v[2 * i + 1] : v[2 * i];
+#pragma unroll
+            for (int i = 0; i < kEach / 4; ++i) y[i] = (e & 2) != 0 ? y[2 * i + 1] : y[2 * i];
+#pragma unroll
+            for (int i = 0; i < kEach / 8; ++i) y[i] = (e & 4) != 0 ? y[2 * i + 1] : y[2 * i];
+            const unsigned long long k = full_key(clean((e & 8) != 0 ? y[1] : y[0]),
+                                                  static_cast<uint32_t>(r.index(at, e)));
             if (k >= least) {
                 const int place = atomicAdd(&n_kept, 1);
                 if (place < a.room) kept[place] = k;
@@ -222,35 +249,29 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
         float top = -INFINITY;  // (the number, of a number and a NaN)
 #pragma unroll
         for (int e = 0; e < kEach; ++e) top = fmaxf(top, v[e]);
-        unsigned long long least = 1;
-        bool some;
         if (t == 0) {
-            unsigned long long mine = r.largest(at, v);
-            // Groups of four lanes where 64 of them are enough, else every lane its own.
-            if (a.K <= 16) {
-#pragma unroll
-                for (int off = 1; off < 4; off <<= 1) {
-                    const unsigned long long o = __shfl_xor_sync(kFull, mine, off);
-                    mine = o > mine ? o : mine;
-                }
-                if ((lane & 3) == 0) tops[tid >> 2] = mine;
-                find_bound<kThreads / 4>(tops, a.K, &bound);
-            } else {
-                tops[tid] = mine;
-                find_bound<kThreads>(tops, a.K, &bound);
-            }
-            least = bound;
-            lim = least == 1 ? -INFINITY : logit_of(static_cast<uint32_t>(least >> 32));
-            some = top >= lim;
-        } else {
-            some = top > lim;  // (an equal one further on is worse than K others)
+            lim = group_bound(top, a.K, reinterpret_cast<float*>(tops), &group_least);
+            // (the bound itself is kept: a number below it, and the rest by the keys)
+            if (top >= lim)
+                keep(v, at, lim == -INFINITY ? lim : lim - fabsf(lim) * 1e-6f - 1e-30f,
+                     static_cast<unsigned long long>(key_of(lim)) << 32);
+        } else if (top > lim) {  // (an equal one further on is worse than K others)
+            keep(v, at, lim, 1);
         }
-        if (some) {
-            unsigned which = 0;  // (never what lies outside the row: that is -inf)
-#pragma unroll
-            for (int e = 0; e < kEach; ++e)
-                if (v[e] > lim || (least != 1 && v[e] == lim)) which |= 1u << e;
-            keep(which, at, least);
+        // What has been kept by then gives a better bound, twice.
+        if ((t == 1 || t == 3) && t + 1 < a.tiles) {
+            __syncthreads();
+            const int n = n_kept;
+            if (n >= a.K && n <= min(kThreads, a.room)) {
+                const unsigned long long mine = tid < n ? kept[tid] : 0;
+                int above = 0;
+                if (tid < n)
+                    for (int i = 0; i < n; ++i) above += kept[i] > mine;
+                if (tid < n && above == a.K - 1) bound = mine;
+                __syncthreads();
+                lim = logit_of(static_cast<uint32_t>(bound >> 32));
+            }
+            __syncthreads();  // (nothing is kept before all have the bound)
         }
         if (top > m) {
             s = m == -INFINITY ? 0.0f : s * ex2((m - top) * kLog2e);
@@ -299,19 +320,13 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
             const unsigned long long k = r.largest(first + t * kTile, v);
             mine = k > mine ? k : mine;
         }
-        tops[tid] = mine;
-        find_bound<kThreads>(tops, a.K, &bound);
-        const unsigned long long least = bound;
+        const unsigned long long least = find_bound(mine, a.K, tops, &bound);
         if (tid == 0) n_kept = 0;
         __syncthreads();
         for (int t = 0; t < a.tiles; ++t) {
             float v[kEach];
             r.load(first + t * kTile, v);
-            unsigned which = 0;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e)
-                if (v[e] > -INFINITY) which |= 1u << e;
-            keep(which, first + t * kTile, least);
+            keep(v, first + t * kTile, -INFINITY, least);
         }
         __syncthreads();
         n = n_kept;
@@ -571,8 +586,11 @@ size_t join_smem(int all, int K) {
     const int most = all <= 64 ? all : K * ((all + n - 1) / n) * join_group(all, K);
     return static_cast<size_t>(most) * sizeof(Cand);
 }
-// Logits a piece keeps: K groups' worth of its first tile, or K threads' of all.
-int piece_room(int K, int tiles) { return K * kEach * (tiles > 4 ? tiles : 4); }
+// Logits a piece keeps: those of K threads, where it comes to that.
+int piece_room(int K, int tiles) {
+    const int n = K * kEach * tiles;
+    return n < 512 ? 512 : n;
+}
 
 // (For pieces of one tile, the most that there can be, whatever the device.)
 size_t beam_bytes(int B, int W, int V, int K) {
