@@ -545,14 +545,6 @@ __global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
 // Tiles of a row (one more than V asks for, for rows that start inside a vector).
 int tiles_of(int V) { return (V + 7 + kTile - 1) / kTile; }
 
@@ -598,12 +590,6 @@ size_t beam_bytes(int B, int W, int V, int K) {
     return (n * K * 8 + n * 8 + 255) / 256 * 256;
 }
 
-bool allow_smem(const void* kernel, size_t bytes) {
-    return bytes <= 32 * 1024 ||
-           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(bytes)) == cudaSuccess;
-}
-
 }  // namespace
 }  // namespace treeattn
 
@@ -629,7 +615,9 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
         return TREE_ATTN_ERR_ALIGN;
     if (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < beam_bytes(B, W, V, K))
         return TREE_ATTN_ERR_WORKSPACE;
-    const int sms = sm_count();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
+    const int sms = sms_of(dev);
     if (sms == 0) return TREE_ATTN_ERR_CUDA;
     const int tiles = piece_tiles(static_cast<long long>(B) * W, V, sms);
     const int pieces = (tiles_of(V) + tiles - 1) / tiles;
@@ -655,8 +643,10 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     const int all = W * pieces * K;
     using Join = void (*)(JoinArgs);
     const Join join = join_threads(all) == 256 ? join_kernel<256> : join_kernel<1024>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), smem) ||
-        !allow_smem(reinterpret_cast<const void*>(join), join_smem(all, K)))
+    static std::atomic<unsigned long long> piece_ready[3], join_ready[2];
+    if ((smem > 32 * 1024 && !opt_in(reinterpret_cast<const void*>(kernel), dev, piece_ready[dtype])) ||
+        (join_smem(all, K) > 24 * 1024 &&
+         !opt_in(reinterpret_cast<const void*>(join), dev, join_ready[join_threads(all) != 256])))
         return TREE_ATTN_ERR_CUDA;
     const int rc = rc_of(launch_dependent(kernel, dim3(pieces, B * W), dim3(kThreads),
                                           smem, s, p));

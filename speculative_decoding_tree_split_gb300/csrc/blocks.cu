@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs
     constexpr int LPR = D / V;          // lanes per row
     constexpr int RW = 32 / LPR;        // rows per load of a warp
     constexpr int STEP = RW * kBoundsWarps;
-    constexpr int U = 8;
+    constexpr int U = FP8 ? 4 : 8;      // (all of a page of 64 tokens)
     __shared__ float part[kBoundsWarps][2][D];
     __shared__ float red[kBoundsWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -667,14 +667,6 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
 bool cache_shape_ok(int B, int Hkv, int d, int max_pages, int P, int num_pages) {
     return B >= 0 && B <= 65535 && Hkv >= 1 && Hkv <= 65535 && (d == 64 || d == 128) &&
            max_pages >= 1 && num_pages >= 1 && page_size_ok(P) &&
@@ -709,7 +701,9 @@ int tree_kv_block_bounds(const void* k_pages, const uint8_t* k_scales, const int
     if (!ptr_aligned(k_pages, 16) || !ptr_aligned(bounds, 16) || !ptr_aligned(block_table, 4) ||
         !ptr_aligned(starts, 4) || !ptr_aligned(seq_lens, 4) || !ptr_aligned(status, 4))
         return TREE_ATTN_ERR_ALIGN;
-    const int sms = sm_count();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
+    const int sms = sms_of(dev);
     if (sms == 0) return TREE_ATTN_ERR_CUDA;
     BoundsArgs a;
     a.k_pages = k_pages;
@@ -753,7 +747,9 @@ int tree_select_blocks(const uint16_t* q, const int8_t* bounds, const uint8_t* b
     if (!ptr_aligned(q, 16) || !ptr_aligned(bounds, 16) || !ptr_aligned(block_table, 4) ||
         !ptr_aligned(seq_lens, 4) || !ptr_aligned(blocks, 4) || !ptr_aligned(status, 4))
         return TREE_ATTN_ERR_ALIGN;
-    const int sms = sm_count();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
+    const int sms = sms_of(dev);
     if (sms == 0) return TREE_ATTN_ERR_CUDA;
     const int G = Hq / Hkv;
     SelectArgs a;
@@ -810,10 +806,9 @@ int tree_select_blocks(const uint16_t* q, const int8_t* bounds, const uint8_t* b
                  : (at_once == 1   ? select_kernel<64, 1>
                     : at_once == 2 ? select_kernel<64, 2>
                                    : select_kernel<64, 4>);
-    if (need > 48 * 1024 &&
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(need)) != cudaSuccess)
+    static std::atomic<unsigned long long> ready[2][3];
+    if (need > 48 * 1024 && !opt_in(reinterpret_cast<const void*>(kernel), dev,
+                                    ready[d == 128][at_once == 4 ? 2 : at_once - 1]))
         return TREE_ATTN_ERR_CUDA;
     return rc_of(launch_cluster(kernel, dim3(static_cast<unsigned>(grid)), dim3(kSelThreads), need,
                                 S, static_cast<cudaStream_t>(stream), a));

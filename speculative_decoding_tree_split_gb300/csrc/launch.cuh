@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 namespace treeattn {
@@ -23,6 +24,39 @@ inline cudaError_t launch_dependent(Kernel kernel, dim3 grid, dim3 block, size_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// SMs of a device (asked for once), 0 if it cannot be told.
+inline int sms_of(int dev) {
+    static std::atomic<int> known[64];
+    if (dev < 0) return 0;
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Lets a kernel have all of an SM's shared memory, and clusters of 16 CTAs where
+// `wide` (asked for once per device; `configured` has a bit for each).
+inline bool opt_in(const void* kernel, int dev, std::atomic<unsigned long long>& configured,
+                   bool wide = false) {
+    const unsigned long long bit = 1ull << (dev & 63);
+    if ((configured.load(std::memory_order_relaxed) & bit) != 0) return true;
+    int most = 0;
+    cudaFuncAttributes fixed;
+    if (cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
+            cudaSuccess ||
+        cudaFuncGetAttributes(&fixed, kernel) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             most - static_cast<int>(fixed.sharedSizeBytes)) != cudaSuccess)
+        return false;
+    if (wide && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                    cudaSuccess)
+        return false;
+    configured.fetch_or(bit);
+    return true;
 }
 
 inline bool ptr_aligned(const void* p, uintptr_t a) {

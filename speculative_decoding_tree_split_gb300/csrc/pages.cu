@@ -553,14 +553,6 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
 int check_pools(void* const* pools, const size_t* page_bytes, int n_pools) {
     if (n_pools < 0) return TREE_ATTN_ERR_SHAPE;
     if (n_pools == 0) return TREE_ATTN_OK;
@@ -580,7 +572,9 @@ int enqueue_copies(void* const* pools, const size_t* page_bytes, int n_pools, co
     const long long rows =
         fork != nullptr ? static_cast<long long>(fork->rows_in) + fork->rows_out : 0;
     if (n == 0 && rows == 0) return TREE_ATTN_OK;
-    const int sms = sm_count();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
+    const int sms = sms_of(dev);
     if (sms == 0) return TREE_ATTN_ERR_CUDA;
     CopyArgs a;
     a.src = src;

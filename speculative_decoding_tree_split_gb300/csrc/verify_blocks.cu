@@ -1004,16 +1004,12 @@ __global__ void __launch_bounds__(kThreads, kResident)
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
 
 template <int D, bool FP8, int NT>
-int launch(Args a, long long units, int sms, cudaStream_t stream) {
+int launch(Args a, long long units, int dev, int sms, cudaStream_t stream) {
     const size_t smem = sizeof(Smem<D, FP8, NT>) + (kThreads + 1) * sizeof(int) +
                         static_cast<size_t>(a.tokens) * a.n_blocks * sizeof(Entry);
     const auto kernel = blocks_kernel<D, FP8, NT>;
-    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return TREE_ATTN_ERR_CUDA;
+    static std::atomic<unsigned long long> ready{0};
+    if (!opt_in(reinterpret_cast<const void*>(kernel), dev, ready, true)) return TREE_ATTN_ERR_CUDA;
     // CTAs of a cluster: those that take the least time when the SMs take all CTAs in
     // waves, and a CTA its tiles and kFixed tiles' worth of beginning and end.
     const long long most = a.n_blocks < a.max_pages ? a.n_blocks : a.max_pages;
@@ -1078,10 +1074,10 @@ extern "C" int tree_attn_verify_blocks(
         !ptr_aligned(lse, 4) || !ptr_aligned(mask, 8) || !ptr_aligned(parents, 4) ||
         !ptr_aligned(status, 4))
         return TREE_ATTN_ERR_ALIGN;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return TREE_ATTN_ERR_CUDA;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
+    const int sms = sms_of(dev);
+    if (sms == 0) return TREE_ATTN_ERR_CUDA;
     Args a;
     a.q = q;
     a.kv[0] = k_pages;
@@ -1115,9 +1111,9 @@ extern "C" int tree_attn_verify_blocks(
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f = k_scales != nullptr;
     if (d == 128) {
-        if (NT == 1) return f ? launch<128, true, 1>(a, units, sms, s) : launch<128, false, 1>(a, units, sms, s);
-        return f ? launch<128, true, 2>(a, units, sms, s) : launch<128, false, 2>(a, units, sms, s);
+        if (NT == 1) return f ? launch<128, true, 1>(a, units, dev, sms, s) : launch<128, false, 1>(a, units, dev, sms, s);
+        return f ? launch<128, true, 2>(a, units, dev, sms, s) : launch<128, false, 2>(a, units, dev, sms, s);
     }
-    if (NT == 1) return f ? launch<64, true, 1>(a, units, sms, s) : launch<64, false, 1>(a, units, sms, s);
-    return f ? launch<64, true, 2>(a, units, sms, s) : launch<64, false, 2>(a, units, sms, s);
+    if (NT == 1) return f ? launch<64, true, 1>(a, units, dev, sms, s) : launch<64, false, 1>(a, units, dev, sms, s);
+    return f ? launch<64, true, 2>(a, units, dev, sms, s) : launch<64, false, 2>(a, units, dev, sms, s);
 }
