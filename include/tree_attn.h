@@ -648,7 +648,7 @@ TREE_ATTN_API int tree_attn_prefill(const uint16_t *q, const uint16_t *k, const 
  *   pools        HOST array of n_pools device pointers, page_bytes (host) the
  *                bytes of one page of each, 1 .. 2^31 (fastest where pool and
  *                size are multiples of 16)
- *   src, dst     int32 [n]; a pair with a -1 is skipped.  No page may be a dst
+ *   src, dst     int32 [n], n below 2^30; a pair with a -1 is skipped.  No page may be a dst
  *                twice, or a src and a dst.
  *   count        nullable device int32: only the first min(*count, n) pairs
  *   status       nullable: TREE_ATTN_STATUS_BAD_PAGE (that pair is skipped).
@@ -684,7 +684,8 @@ TREE_ATTN_API int tree_kv_copy_pages(void *const *pools, const size_t *page_byte
  *                -1; a row whose copied page is among them ends at that page:
  *                seq_lens_out says where), _BAD_SEQ_LEN (a length, or a length
  *                and reserve, outside the table), _BAD_PAGE, _BAD_ROW.
- * rows_in and rows_out below 2^24, num_pages and max_pages_per_seq below 2^30.
+ * rows_in and rows_out below 2^24, num_pages and max_pages_per_seq below 2^30, tables
+ * below 2^31 entries.
  * n_pools = 0 makes the tables only.  Returns 0, -1, -2, -3, -4, -5.
  */
 TREE_ATTN_API size_t tree_kv_fork_workspace_size(int rows_in, int rows_out, int num_pages);
@@ -764,7 +765,7 @@ TREE_ATTN_API int tree_beam_select(const void *logits, int dtype, long long batc
  *                k_scales as for the 8-bit cache
  *   starts       nullable int32 [B] (NULL: 0): the lengths before the tokens came
  *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN, _BAD_PAGE.
- * A page that two sequences of the call share gets the bounds of one of them.
+ * A page that several sequences of the call share has the same committed tokens in all.
  * Sizes as for the 8-bit cache; bounds and k_pages 16-byte aligned.  Returns 0,
  * -1, -2, -3, -5.
  */

@@ -479,7 +479,9 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
     uint8_t* codes = smem;                                                // [tiles * 8][kStride]
     Scratch* scratch = reinterpret_cast<Scratch*>(codes + tiles * 8 * kStride);  // [kSelWarps]
     uint32_t* scores = reinterpret_cast<uint32_t*>(scratch + kSelWarps);  // [TC][per_most]
-    int* pages = reinterpret_cast<int*>(scores + static_cast<size_t>(a.TC) * a.per_most);  // [per_most]
+    // The pages' numbers stand where the first token's scores will: a warp has read those
+    // of a tile, and of its next, before it writes the tile's scores.
+    int* pages = reinterpret_cast<int*>(scores);
 
     bool bad;
     const int L = clamp_seq_len(a.lens[b], a.P, a.max_pages, bad);
@@ -781,7 +783,7 @@ int tree_select_blocks(const uint16_t* q, const int8_t* bounds, const uint8_t* b
     size_t need = 0;
     for (;; TC = (TC + 1) / 2) {
         a.per_most = ((max_pages_per_seq + S - 1) / S + 3) / 4 * 4;
-        need = static_cast<size_t>(TC + 1) * a.per_most * 4 + kSelWarps * sizeof(Scratch) +
+        need = static_cast<size_t>(TC) * a.per_most * 4 + kSelWarps * sizeof(Scratch) +
                static_cast<size_t>(padded_tiles(TC * a.cols) * 8) * code_row;
         if (need <= (TC == 1 ? 200u * 1024u : 72u * 1024u)) break;  // (three CTAs to an SM)
         if (TC == 1) {  // one token of a very long sequence: more CTAs share its pages

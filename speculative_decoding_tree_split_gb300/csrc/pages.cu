@@ -620,7 +620,7 @@ int plan_ctas(long long work) { return work <= 8192 ? 1 : kMaxCtas; }
 bool pages_shape_ok(int rows, int max_pages, int num_pages) {
     return rows >= 0 && rows < (1 << 24) && max_pages >= 1 && num_pages >= 1 &&
            max_pages < (1 << 30) && num_pages < (1 << 30) &&
-           static_cast<long long>(rows) * max_pages < (1LL << 40);
+           static_cast<long long>(rows) * max_pages < (1LL << 31);  // (new pages are counted in ints)
 }
 
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -641,7 +641,8 @@ extern "C" {
 int tree_kv_copy_pages(void* const* pools, const size_t* page_bytes, int n_pools,
                        const int32_t* src, const int32_t* dst, const int32_t* count, int n,
                        int num_pages, int32_t* status, void* stream) {
-    if (n < 0 || num_pages < 1) return TREE_ATTN_ERR_SHAPE;
+    if (n < 0 || n >= (1 << 30) || num_pages < 1 || num_pages >= (1 << 30))
+        return TREE_ATTN_ERR_SHAPE;
     const int rc = check_pools(pools, page_bytes, n_pools);
     if (rc != TREE_ATTN_OK) return rc;
     if (n == 0 || n_pools == 0) return TREE_ATTN_OK;

@@ -1071,7 +1071,8 @@ extern "C" int tree_attn_verify_blocks(
     if (!ptr_aligned(q, 16) || !ptr_aligned(k_pages, 16) || !ptr_aligned(v_pages, 16) ||
         !ptr_aligned(tree_k, 16) || !ptr_aligned(tree_v, 16) || !ptr_aligned(out, 16) ||
         !ptr_aligned(block_table, 4) || !ptr_aligned(seq_lens, 4) || !ptr_aligned(blocks, 4) ||
-        !ptr_aligned(lse, 4) || !ptr_aligned(mask, 8) || !ptr_aligned(parents, 4) ||
+        !ptr_aligned(k_scales, 16) || !ptr_aligned(v_scales, 16) || !ptr_aligned(lse, 4) ||
+        !ptr_aligned(mask, 8) || !ptr_aligned(parents, 4) ||
         !ptr_aligned(status, 4))
         return TREE_ATTN_ERR_ALIGN;
     int dev = 0;

@@ -28,7 +28,7 @@ def copy(lib, ptrs=(A,), size=64, **kw):
 
 
 def test_copy_pages(lib):
-    for kw in (dict(n=-1), dict(pages=0), dict(n_pools=-1), dict(size=0), dict(size=(1 << 31) + 1)):
+    for kw in (dict(n=-1), dict(n=1 << 30), dict(pages=1 << 30), dict(pages=0), dict(n_pools=-1), dict(size=0), dict(size=(1 << 31) + 1)):
         assert copy(lib, **kw) == -2
     for kw in (dict(src=None), dict(dst=None), dict(pools=None), dict(bytes=None), dict(ptrs=(A, None))):
         assert copy(lib, **kw) == -1
@@ -54,7 +54,7 @@ def test_fork(lib):
     need = lib.tree_kv_fork_workspace_size(2, 3, 8)
     assert need > 0 and lib.tree_kv_fork_workspace_size(-1, 3, 8) == 0
     assert lib.tree_kv_fork_workspace_size(2, 3, 0) == 0
-    for kw in (dict(rows_in=-1), dict(rows_out=1 << 24), dict(maxp=0), dict(pages=0), dict(P=24),
+    for kw in (dict(rows_in=-1), dict(rows_out=1 << 24), dict(rows_out=1 << 16, maxp=1 << 15), dict(maxp=0), dict(pages=0), dict(P=24),
                dict(all=-1), dict(bt_out=A), dict(lens_out=A), dict(refs_out=A), dict(n_pools=-1)):
         assert fork(lib, **kw) == -2, kw
     for name in ("bt", "lens", "refs", "src", "bt_out", "lens_out", "refs_out", "pools"):
@@ -181,7 +181,7 @@ def test_verify_blocks(lib):
     for name in ("q", "k", "v", "bt", "lens", "blocks", "tk", "tv", "mask", "out", "lse"):
         assert attend(lib, **{name: None}) == -1, name
     for kw in (dict(q=A + 8), dict(k=A + 8), dict(v=A + 2), dict(bt=A + 2), dict(lens=A + 1),
-               dict(blocks=A + 2), dict(tk=A + 8), dict(tv=A + 8), dict(mask=A + 4),
+               dict(blocks=A + 2), dict(ks=A + 8, vs=A), dict(ks=A, vs=A + 4), dict(tk=A + 8), dict(tv=A + 8), dict(mask=A + 4),
                dict(mask=None, par=A + 2), dict(out=A + 8), dict(lse=A + 2), dict(status=A + 2)):
         assert attend(lib, **kw) == -3, kw
     assert attend(lib, B=0, q=None) == 0

@@ -202,7 +202,8 @@ def test_select_queries_that_are_no_numbers():
     check_select(q.bfloat16(), bounds, exps, rows, lens, P, 9, 0, 0)
 
 
-@pytest.mark.parametrize("nb,T,k", [(3000, 1, 64), (9001, 3, 200), (40000, 2, 4096), (70000, 1, 5)])
+@pytest.mark.parametrize("nb,T,k", [(3000, 1, 64), (9001, 3, 200), (40000, 2, 4096), (70000, 1, 5),
+                                    (262144, 1, 33)])
 def test_select_from_many_pages(nb, T, k):
     P = 16
     g = torch.Generator("cuda").manual_seed(nb)

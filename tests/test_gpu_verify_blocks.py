@@ -173,6 +173,21 @@ def test_scores_far_apart_and_a_first_key_that_draws_most(fp8):
     c.check(scale=-0.3)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_scale_of_zero_gives_the_mean(fp8):
+    c = Case([70], 1, 4, 64, 16, 2, 3, fp8, seed=17)
+    out, lse = c.call(softmax_scale=0.0)
+    for t in range(2):
+        vs = [c.tv[0, c.sees(0, t), 0].double().cpu()]
+        for j in c.blocks[0, t, 0].tolist():
+            if j >= 0:
+                vs.append(c.values(c.v, c.vs, c.rows[0][j], 0, min(16, 70 - 16 * j)))
+        vs = torch.cat(vs)
+        assert float((out[0, t].double().cpu() - vs.mean(0)).abs().max()) <= float(
+            vs.mean(0).abs().max()) * 2.0 ** -8 + float(vs.abs().max()) * 2.0 ** -11
+        assert float((lse[0, t] - math.log(vs.shape[0])).abs().max()) <= 1e-5
+
+
 def test_value_scales_far_apart():
     c = Case([640], 2, 4, 128, 64, 2, 10, True, seed=8)
     for j, page in enumerate(c.rows[0]):
