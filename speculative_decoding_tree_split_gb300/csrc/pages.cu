@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/tree_attn.h"
 #include "cluster.cuh"
@@ -350,98 +351,6 @@ __device__ __forceinline__ void fork_release(const ForkArgs& a, int p) {
 }
 
 // ---------------------------------------------------------------------------
-// Copies: page src[k] of every pool to its page dst[k].  A warp moves 4 KB at a
-// time, eight 16-byte vectors to a lane, all loaded before the first is stored.
-// ---------------------------------------------------------------------------
-constexpr int kPoolsMost = 120;  // of one launch
-constexpr int kPiece = 4096;     // bytes a warp moves at a time
-constexpr int kCopyThreads = 256;
-
-struct CopyArgs {
-    uint8_t* pool[kPoolsMost];
-    long long bytes[kPoolsMost];  // of one page
-    int first[kPoolsMost + 1];    // first piece of each pool within a page's
-    const int32_t* src;
-    const int32_t* dst;
-    const int32_t* count;  // nullable: n
-    int n, n_pools, num_pages;
-    int32_t* status;
-};
-
-__device__ __forceinline__ uint4 ld_once(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-// FORK: the first warps make the rows of a fork's table as well.
-template <bool FORK>
-__global__ void __launch_bounds__(kCopyThreads)
-    copy_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ ForkArgs f) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    const int lane = threadIdx.x & 31;
-    if (FORK) {
-        const int warps = gridDim.x * (kCopyThreads / 32);
-        // (from the last warp on: the first ones have the most copies)
-        for (int i = warps - 1 - (blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32);
-             i < f.rows_out + f.rows_in; i += warps) {
-            if (i < f.rows_out)
-                fork_row(f, i);
-            else
-                fork_release(f, i - f.rows_out);
-        }
-        if (a.n_pools == 0) return;
-    }
-    const int n = a.count != nullptr ? min(max(*a.count, 0), a.n) : a.n;
-    const int per = a.first[a.n_pools];
-    const int warps = gridDim.x * (kCopyThreads / 32);
-    const int step_k = warps / per, step_c = warps % per;
-    const int w0 = blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32;
-    int k = w0 / per, c = w0 % per;
-    while (k < n) {
-        const int s = a.src[k], d = a.dst[k];
-        if (s >= 0 && d >= 0 && s < a.num_pages && d < a.num_pages) {
-            int lo = 0, hi = a.n_pools - 1;  // the pool that piece c belongs to
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (a.first[mid] <= c)
-                    lo = mid;
-                else
-                    hi = mid - 1;
-            }
-            const long long page = a.bytes[lo];
-            const long long at = static_cast<long long>(c - a.first[lo]) * kPiece;
-            const int m = static_cast<int>(min(page - at, static_cast<long long>(kPiece)));
-            const uint8_t* from = a.pool[lo] + s * page + at;
-            uint8_t* to = a.pool[lo] + d * page + at;
-            if (((page | reinterpret_cast<uintptr_t>(a.pool[lo])) & 15) == 0) {
-                uint4 v[kPiece / 512];
-#pragma unroll
-                for (int i = 0; i < kPiece / 512; ++i)
-                    if (i * 512 + lane * 16 < m) v[i] = ld_once(from + i * 512 + lane * 16);
-#pragma unroll
-                for (int i = 0; i < kPiece / 512; ++i)
-                    if (i * 512 + lane * 16 < m)
-                        *reinterpret_cast<uint4*>(to + i * 512 + lane * 16) = v[i];
-            } else {
-                for (int i = lane; i < m; i += 32) to[i] = from[i];
-            }
-        } else if (lane == 0 && (s < -1 || d < -1 || s >= a.num_pages || d >= a.num_pages)) {
-            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-        }
-        k += step_k;
-        c += step_c;
-        if (c >= per) {
-            c -= per;
-            ++k;
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
 // Compact.  With u(p) = used pages before p and n the used pages in all, the
 // k-th used page at or past n goes to the k-th free page before n:
 //   page p >= n is mover u(p) - u(n), page p < n is hole p - u(p).
@@ -533,19 +442,122 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(const CompactArgs
         *a.count = moves;
         *a.n_used = n;
     }
-    ptx::cluster_sync();
+}
 
-    for (long long i = gtid; i < a.entries; i += gthreads) {
+// The pages' new places in the table, by all warps of the copies' grid.
+__device__ __forceinline__ void compact_table(const CompactArgs& a, long long thread,
+                                              long long threads) {
+    if (thread >= a.entries) return;
+    const int n = *a.n_used;
+    for (long long i = thread; i < a.entries; i += threads) {
         int e = a.table[i];
         if (e != -1) {
             if (!entry_ok(e, a.num_pages) || a.refs[e] <= 0) {
                 report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
                 e = -1;
             } else if (e >= n) {
-                e = __ldcg(a.to + e);
+                e = a.to[e];
             }
         }
         a.table_out[i] = e;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Copies: page src[k] of every pool to its page dst[k].  A warp moves 4 KB at a
+// time, eight 16-byte vectors to a lane, all loaded before the first is stored.
+// ---------------------------------------------------------------------------
+constexpr int kPoolsMost = 120;  // of one launch
+constexpr int kPiece = 4096;     // bytes a warp moves at a time
+constexpr int kCopyThreads = 256;
+
+struct CopyArgs {
+    uint8_t* pool[kPoolsMost];
+    long long bytes[kPoolsMost];  // of one page
+    int first[kPoolsMost + 1];    // first piece of each pool within a page's
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* count;  // nullable: n
+    int n, n_pools, num_pages;
+    int32_t* status;
+};
+
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// What is done beside the copies: nothing, or the table of a fork or a compaction.
+struct NoTable {};
+
+template <typename Table>
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ Table f) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    if constexpr (std::is_same<Table, CompactArgs>::value) {
+        compact_table(f, static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x,
+                      static_cast<long long>(gridDim.x) * kCopyThreads);
+    }
+    if constexpr (std::is_same<Table, ForkArgs>::value) {
+        const int warps = gridDim.x * (kCopyThreads / 32);
+        // (from the last warp on: the first ones have the most copies)
+        for (int i = warps - 1 - (blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32);
+             i < f.rows_out + f.rows_in; i += warps) {
+            if (i < f.rows_out)
+                fork_row(f, i);
+            else
+                fork_release(f, i - f.rows_out);
+        }
+    }
+    if (a.n_pools == 0) return;
+    const int n = a.count != nullptr ? min(max(*a.count, 0), a.n) : a.n;
+    const int per = a.first[a.n_pools];
+    const int warps = gridDim.x * (kCopyThreads / 32);
+    const int step_k = warps / per, step_c = warps % per;
+    const int w0 = blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32;
+    int k = w0 / per, c = w0 % per;
+    while (k < n) {
+        const int s = a.src[k], d = a.dst[k];
+        if (s >= 0 && d >= 0 && s < a.num_pages && d < a.num_pages) {
+            int lo = 0, hi = a.n_pools - 1;  // the pool that piece c belongs to
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (a.first[mid] <= c)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const long long page = a.bytes[lo];
+            const long long at = static_cast<long long>(c - a.first[lo]) * kPiece;
+            const int m = static_cast<int>(min(page - at, static_cast<long long>(kPiece)));
+            const uint8_t* from = a.pool[lo] + s * page + at;
+            uint8_t* to = a.pool[lo] + d * page + at;
+            if (((page | reinterpret_cast<uintptr_t>(a.pool[lo])) & 15) == 0) {
+                uint4 v[kPiece / 512];
+#pragma unroll
+                for (int i = 0; i < kPiece / 512; ++i)
+                    if (i * 512 + lane * 16 < m) v[i] = ld_once(from + i * 512 + lane * 16);
+#pragma unroll
+                for (int i = 0; i < kPiece / 512; ++i)
+                    if (i * 512 + lane * 16 < m)
+                        *reinterpret_cast<uint4*>(to + i * 512 + lane * 16) = v[i];
+            } else {
+                for (int i = lane; i < m; i += 32) to[i] = from[i];
+            }
+        } else if (lane == 0 && (s < -1 || d < -1 || s >= a.num_pages || d >= a.num_pages)) {
+            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+        }
+        k += step_k;
+        c += step_c;
+        if (c >= per) {
+            c -= per;
+            ++k;
+        }
     }
 }
 
@@ -565,13 +577,13 @@ int check_pools(void* const* pools, const size_t* page_bytes, int n_pools) {
     return TREE_ATTN_OK;
 }
 
-// Pools in launches of at most kPoolsMost.
+// Pools in launches of at most kPoolsMost; the first also makes a table (whose rows,
+// or entries, take `more` warps).
+template <typename Table>
 int enqueue_copies(void* const* pools, const size_t* page_bytes, int n_pools, const int32_t* src,
                    const int32_t* dst, const int32_t* count, int n, int num_pages,
-                   int32_t* status, cudaStream_t stream, const ForkArgs* fork = nullptr) {
-    const long long rows =
-        fork != nullptr ? static_cast<long long>(fork->rows_in) + fork->rows_out : 0;
-    if (n == 0 && rows == 0) return TREE_ATTN_OK;
+                   int32_t* status, cudaStream_t stream, const Table& table, long long more) {
+    if (n == 0 && more == 0) return TREE_ATTN_OK;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     const int sms = sms_of(dev);
@@ -583,7 +595,7 @@ int enqueue_copies(void* const* pools, const size_t* page_bytes, int n_pools, co
     a.n = n;
     a.num_pages = num_pages;
     a.status = status;
-    for (int i = 0; i < n_pools || fork != nullptr;) {
+    for (int i = 0; i < n_pools || more > 0;) {
         long long pieces = 0;
         int m = 0;
         for (; i < n_pools && m < kPoolsMost; ++i, ++m) {
@@ -598,18 +610,17 @@ int enqueue_copies(void* const* pools, const size_t* page_bytes, int n_pools, co
         a.n_pools = m;
         // As many CTAs as the SMs hold at once: they take the pieces in turn.
         long long warps = pieces * n;
-        if (fork != nullptr && warps < rows) warps = rows;
+        if (warps < more) warps = more;
         const long long ctas = (warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
         const int grid = static_cast<int>(ctas < 8LL * sms ? ctas : 8LL * sms);
         if (grid == 0) return TREE_ATTN_OK;
         const int rc =
-            fork != nullptr
-                ? rc_of(launch_dependent(copy_kernel<true>, dim3(grid), dim3(kCopyThreads), 0,
-                                         stream, a, *fork))
-                : rc_of(launch_dependent(copy_kernel<false>, dim3(grid), dim3(kCopyThreads), 0,
-                                         stream, a, ForkArgs()));
+            more > 0 ? rc_of(launch_dependent(copy_kernel<Table>, dim3(grid), dim3(kCopyThreads), 0,
+                                              stream, a, table))
+                     : rc_of(launch_dependent(copy_kernel<NoTable>, dim3(grid), dim3(kCopyThreads),
+                                              0, stream, a, NoTable()));
         if (rc != TREE_ATTN_OK) return rc;
-        fork = nullptr;  // (its rows are made once)
+        more = 0;  // (it is made once)
     }
     return TREE_ATTN_OK;
 }
@@ -651,7 +662,7 @@ int tree_kv_copy_pages(void* const* pools, const size_t* page_bytes, int n_pools
         !ptr_aligned(status, 4))
         return TREE_ATTN_ERR_ALIGN;
     return enqueue_copies(pools, page_bytes, n_pools, src, dst, count, n, num_pages, status,
-                          static_cast<cudaStream_t>(stream));
+                          static_cast<cudaStream_t>(stream), NoTable(), 0);
 }
 
 size_t tree_kv_fork_workspace_size(int rows_in, int rows_out, int num_pages) {
@@ -723,7 +734,7 @@ int tree_kv_fork(void* const* pools, const size_t* page_bytes, int n_pools,
     const int rp = rc_of(launch_cluster(fork_kernel, dim3(ctas), dim3(kPlanThreads), 0, ctas, s, a));
     if (rp != TREE_ATTN_OK) return rp;
     return enqueue_copies(pools, page_bytes, n_pools, a.copy_src, a.copy_dst, a.count, rows_out,
-                          num_pages, status, s, &a);
+                          num_pages, status, s, a, static_cast<long long>(rows_in) + rows_out);
 }
 
 size_t tree_kv_compact_workspace_size(int num_pages) {
@@ -770,9 +781,9 @@ int tree_kv_compact(void* const* pools, const size_t* page_bytes, int n_pools,
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int rp =
         rc_of(launch_cluster(compact_kernel, dim3(ctas), dim3(kPlanThreads), 0, ctas, s, a));
-    if (rp != TREE_ATTN_OK || n_pools == 0) return rp;
+    if (rp != TREE_ATTN_OK) return rp;
     return enqueue_copies(pools, page_bytes, n_pools, a.copy_src, a.copy_dst, a.count,
-                          num_pages / 2, num_pages, status, s);
+                          num_pages / 2, num_pages, status, s, a, (a.entries + 127) / 128);
 }
 
 }  // extern "C"
