@@ -49,7 +49,7 @@ constexpr float kMove = 8.0f;    // binades a score may exceed its row's referen
 // 8-bit cache: P's largest at a fresh reference is 2^kLift (2^8 above it is still
 // below fp16's 2^16).
 constexpr int kLift = 6;
-constexpr int kNoScale = -1000;  // no key has been seen
+constexpr int kNoScale = -1000;  // no key has been seen, so no scale byte
 constexpr float kLeast = 1.17549435e-38f;  // of a score unit: never 0, which would lose -inf
 constexpr float kLow = -3.0e38f; // a reference before the first key
 
@@ -480,7 +480,7 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
 #pragma unroll
             for (int i = 0; i < 4; ++i) st.o[n][d][i] = 0.0f;
     }
-    int sref = kNoScale;  // 8-bit cache: accumulators are in units of 2^(sref - kLift)
+    int sref = kNoScale;  // 8-bit cache: accumulators are in units of 2^(sref - 127 - kLift)
 
     // ---- pages
     // Tile i is rows i % (P / 16) * 16 of page i / (P / 16); a warp takes every step-th,
@@ -492,23 +492,26 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
     using Sm = Smem<D, FP8, NT>;
     constexpr int RB = Sm::RB;
     const uint32_t ring = ptx::smem_u32(sm.warp[warp].ring);
-    // Tiles without keys are passed over.
-    auto live_at = [&](int e) { return static_cast<int>(sm.entries[e].live_who & 255u) - off; };
-    auto skip = [&](int e) {
-        while (e < u.n_entries && live_at(e) <= 0) e += e_step;
+    // The next entry from e on whose tile has keys (others are passed over), and what it says.
+    auto find = [&](int e, Entry& en) {
+        for (; e < u.n_entries; e += e_step) {
+            en = sm.entries[e];
+            if (static_cast<int>(en.live_who & 255u) > off) break;
+        }
         return e;
     };
     // The copies run ahead by the ring's slots: K of a tile, V of it, K of the next.
-    int ahead = skip(e0);
+    Entry next;
+    int ahead = find(e0, next);
     auto copy_next = [&](uint32_t slot, auto values) {
         constexpr bool V = decltype(values)::value;
         if (ahead < u.n_entries) {
-            const int first = sm.entries[ahead].row + off;
+            const int first = next.row + off;
             const uint8_t* base =
                 static_cast<const uint8_t*>(a.kv[V ? 1 : 0]) + static_cast<size_t>(first) * RB;
             copy_tile<RB, V>(slot, base);
             if (FP8 && lane == 0) copy16(slot + kTile * RB, a.scales[V ? 1 : 0] + first);
-            if (V) ahead = skip(ahead + e_step);
+            if (V) ahead = find(ahead + e_step, next);
         }
         copies_commit();
     };
@@ -530,9 +533,10 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
         slot += Sm::kSlot;
         if (slot == ring + Sm::kSlots * Sm::kSlot) slot = ring;
     };
-    for (int e = skip(e0); e < u.n_entries; e = skip(e + e_step)) {
-        const int live = min(live_at(e), kTile);
-        const unsigned seers = sm.entries[e].live_who >> 8;
+    Entry here;
+    for (int e = find(e0, here); e < u.n_entries; e = find(e + e_step, here)) {
+        const int live = min(static_cast<int>(here.live_who & 255u) - off, kTile);
+        const unsigned seers = here.live_who >> 8;
         float x[NT][4];
         arrive();
         if (!FP8) {
@@ -586,8 +590,14 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
             add_values_bf16<CAREFUL, true>(st, x, slot, live, 1.0f, mine, g, c);
         } else {
             const uint32_t s = slot + kTile * RB;
-            const int sv0 = g < live ? static_cast<int>(ld_shared_u8(s + g)) - 127 : kNoScale;
-            const int sv1 = g + 8 < live ? static_cast<int>(ld_shared_u8(s + g + 8)) - 127 : kNoScale;
+            // Scale bytes of keys g and g + 8; of keys that are not there, one in use.
+            int sv0 = static_cast<int>(ld_shared_u8(s + g));
+            int sv1 = static_cast<int>(ld_shared_u8(s + g + 8));
+            if (live < kTile) {
+                const int some = static_cast<int>(ld_shared_u8(s));
+                if (g >= live) sv0 = some;
+                if (g + 8 >= live) sv1 = some;
+            }
             // The unit of the accumulators follows the largest value scale.
             const int top = __reduce_max_sync(kFull, max(sv0, sv1));
             if (top > sref) {
@@ -600,7 +610,9 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
                         for (int j = 0; j < 4; ++j) st.o[n][d][j] *= f;
                 sref = top;
             }
-            const float pf0 = pow2(sv0 - sref + kLift), pf1 = pow2(sv1 - sref + kLift);
+            // 2^(byte - sref + kLift): 2^-90 at the least for the bytes that caches hold.
+            const float pf0 = __int_as_float(max(sv0 - sref + kLift + 127, 0) << 23);
+            const float pf1 = __int_as_float(max(sv1 - sref + kLift + 127, 0) << 23);
             uint32_t p[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -672,9 +684,9 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
                 hide<NT>(x, here, g);
                 hide_others<NT>(x, mine);
                 exponents(st, x);
-                if (FP8 && sref == kNoScale) sref = 0;
+                if (FP8 && sref == kNoScale) sref = 127;
                 // (the accumulators' order of channels)
-                add_values_bf16<CAREFUL, !FP8>(st, x, v_at, here, FP8 ? pow2(kLift - sref) : 1.0f,
+                add_values_bf16<CAREFUL, !FP8>(st, x, v_at, here, FP8 ? pow2(kLift + 127 - sref) : 1.0f,
                                                mine, g, c);
             }
         }
@@ -683,7 +695,7 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
 
     // ---- this warp's rows to shared memory, where its ring was
     copies_wait<0>();
-    const float unit_of = FP8 && sref != kNoScale ? pow2(sref - kLift) : 1.0f;
+    const float unit_of = FP8 && sref != kNoScale ? pow2(sref - 127 - kLift) : 1.0f;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
