@@ -42,8 +42,9 @@ __device__ __forceinline__ int exponent_for(float x) {
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 // ---------------------------------------------------------------------------
-// Bounds.  One CTA per (page, KV head); a page is at most 32 KB and is read in
-// one go, so that all of its loads are in flight at once.
+// Bounds.  A page of one KV head is contiguous and is read in one go.  Large bf16 pages
+// (16 KB and more) have a CTA of four warps each, so that few pages fill the GPU; others a
+// warp each, which needs no barrier.
 // ---------------------------------------------------------------------------
 struct BoundsArgs {
     const void* k_pages;
@@ -60,152 +61,160 @@ struct BoundsArgs {
 constexpr int kBoundsWarps = 4;
 constexpr int kBoundsThreads = 32 * kBoundsWarps;
 
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+// The codes of one (page, KV head): bounds h and l of channels `ch` .. ch + N - 1 (with
+// h >= l where there is any number), all of them by the threads that share `top`, the
+// largest magnitude.
+template <int D, int N>
+__device__ __forceinline__ void store_bounds(const BoundsArgs& a, size_t at, int ch,
+                                             const float (&h)[N], const float (&l)[N], int e) {
+    const float inv = pow2(-e);
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int x = static_cast<int>(fminf(fmaxf(ceilf(h[i] * inv), -127.0f), 127.0f));
+        const int y = static_cast<int>(fminf(fmaxf(floorf(l[i] * inv), -127.0f), 127.0f));
+        hi |= (static_cast<uint32_t>(x) & 255u) << (8 * i);
+        lo |= (static_cast<uint32_t>(y) & 255u) << (8 * i);
+    }
+    int8_t* to = a.bounds + at * 2 * D + ch;
+    if (N == 4) {
+        *reinterpret_cast<uint32_t*>(to) = hi;
+        *reinterpret_cast<uint32_t*>(to + D) = lo;
+    } else if (N == 2) {
+        *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(hi);
+        *reinterpret_cast<uint16_t*>(to + D) = static_cast<uint16_t>(lo);
+    } else {
+        to[0] = static_cast<int8_t>(hi);
+        to[D] = static_cast<int8_t>(lo);
+    }
 }
 
-template <int D, bool FP8>
+// Infinities as the largest finite number, 0 where there is no number at all.
+__device__ __forceinline__ void finite_bounds(float& h, float& l) {
+    const float most = __uint_as_float(0x7f7f0000u);
+    if (!(h >= l)) h = l = 0.0f;
+    h = fminf(fmaxf(h, -most), most);
+    l = fminf(fmaxf(l, -most), most);
+}
+
+// The pages of sequence b that are to be done, and its length; false where there are none.
+__device__ __forceinline__ bool pages_of(const BoundsArgs& a, int b, int& first, int& end, int& L) {
+    bool bad;
+    const int start = a.starts != nullptr ? a.starts[b] : 0;
+    L = clamp_seq_len(a.lens[b], a.P, a.max_pages, bad);
+    if (bad || start < 0) {
+        report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
+        return false;
+    }
+    first = start / a.P;
+    end = start < L ? (L + a.P - 1) / a.P : 0;
+    return first < end;
+}
+
+// Larger and smaller halves of pairs of bf16 (fp16) numbers; the number, of a number and
+// a NaN.
+template <bool FP8>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (FP8)
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool FP8>
+__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (FP8)
+        asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool FP8>
+__device__ __forceinline__ float half_of(uint32_t pair, int i) {
+    if (!FP8) return __uint_as_float(i == 0 ? pair << 16 : pair & 0xffff0000u);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(i == 0 ? pair : pair >> 16)));
+}
+
+// Four warps to a page: bf16 only.
+template <int D>
 __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    constexpr int V = FP8 ? 16 : 8;     // values of a 16-byte vector
-    constexpr int LPR = D / V;          // lanes per row
+    constexpr int LPR = D / 8;          // lanes per row
     constexpr int RW = 32 / LPR;        // rows per load of a warp
     constexpr int STEP = RW * kBoundsWarps;
-    constexpr int U = FP8 ? 4 : 8;      // (all of a page of 64 tokens)
-    __shared__ float part[kBoundsWarps][2][D];
+    constexpr int U = 8;
+    __shared__ uint32_t part[kBoundsWarps][2][D / 2];
     __shared__ float red[kBoundsWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hk = blockIdx.y, b = blockIdx.z;
-    bool bad;
-    const int L = clamp_seq_len(a.lens[b], a.P, a.max_pages, bad);
-    const int start = a.starts != nullptr ? a.starts[b] : 0;
-    if (bad || start < 0) {
-        if (tid == 0) report(a.status, TREE_ATTN_STATUS_BAD_SEQ_LEN);
-        return;
-    }
-    const int end = start < L ? (L + a.P - 1) / a.P : 0;
+    int from, end, L;
+    if (!pages_of(a, b, from, end, L)) return;
     const int sub = lane % LPR, row0 = warp * RW + lane / LPR;
-    for (int j = start / a.P + blockIdx.x; j < end; j += gridDim.x) {
+    for (int j = from + blockIdx.x; j < end; j += gridDim.x) {
         const int page = a.table[static_cast<size_t>(b) * a.max_pages + j];
         if (page < 0 || page >= a.num_pages) {
             if (tid == 0) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
             continue;
         }
         const int n = min(a.P, L - j * a.P);
-        const size_t first = (static_cast<size_t>(page) * a.Hkv + hk) * a.P;  // row of the pool
-        float hi[V], lo[V];
-        if (FP8) {
-            const uint8_t* base = static_cast<const uint8_t*>(a.k_pages) + first * D + sub * 16;
+        const size_t at = static_cast<size_t>(page) * a.Hkv + hk;
+        const uint16_t* base = static_cast<const uint16_t*>(a.k_pages) + at * a.P * D + sub * 8;
+        uint32_t h[4], l[4];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                hi[i] = -INFINITY;
-                lo[i] = INFINITY;
-            }
-            for (int r0 = row0; r0 < n + row0; r0 += U * STEP) {
-                uint4 x[U];
-                uint8_t s[U];
+        for (int i = 0; i < 4; ++i) {
+            h[i] = 0xff80ff80u;
+            l[i] = 0x7f807f80u;
+        }
+        for (int r0 = row0; r0 < n + row0; r0 += U * STEP) {
+            uint4 x[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * STEP;
-                    if (r < n) {
-                        x[u] = ptx::ld_stream(base + static_cast<size_t>(r) * D);
-                        s[u] = a.k_scales[first + r];
-                    }
+            for (int u = 0; u < U; ++u)
+                if (r0 + u * STEP < n)
+                    x[u] = ptx::ld_stream(base + static_cast<size_t>(r0 + u * STEP) * D);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r0 + u * STEP >= n) break;
+                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = max_pair<false>(h[i], w[i]);
+                    l[i] = min_pair<false>(l[i], w[i]);
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (r0 + u * STEP >= n) break;
-                    const float f = scale_of(s[u]);
-                    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t h[2];
-                        f16x2_of_e4m3x4(w[i], h[0], h[1]);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float2 y = __half22float2(*reinterpret_cast<__half2*>(&h[k]));
-                            const int at = i * 4 + k * 2;
-                            hi[at] = fmaxf(hi[at], y.x * f);
-                            lo[at] = fminf(lo[at], y.x * f);
-                            hi[at + 1] = fmaxf(hi[at + 1], y.y * f);
-                            lo[at + 1] = fminf(lo[at + 1], y.y * f);
-                        }
-                    }
-                }
-            }
-        } else {
-            const uint16_t* base = static_cast<const uint16_t*>(a.k_pages) + first * D + sub * 8;
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[i] = 0xff80ff80u;
-                l[i] = 0x7f807f80u;
-            }
-            for (int r0 = row0; r0 < n + row0; r0 += U * STEP) {
-                uint4 x[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (r0 + u * STEP < n)
-                        x[u] = ptx::ld_stream(base + static_cast<size_t>(r0 + u * STEP) * D);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (r0 + u * STEP >= n) break;
-                    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // (the number, of a number and a NaN)
-                        h[i] = max_bf16x2(h[i], w[i]);
-                        l[i] = min_bf16x2(l[i], w[i]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                hi[2 * i] = __uint_as_float(h[i] << 16);
-                hi[2 * i + 1] = __uint_as_float(h[i] & 0xffff0000u);
-                lo[2 * i] = __uint_as_float(l[i] << 16);
-                lo[2 * i + 1] = __uint_as_float(l[i] & 0xffff0000u);
             }
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int off = LPR; off < 32; off <<= 1) {
-                hi[i] = fmaxf(hi[i], __shfl_xor_sync(kFull, hi[i], off));
-                lo[i] = fminf(lo[i], __shfl_xor_sync(kFull, lo[i], off));
+                h[i] = max_pair<false>(h[i], __shfl_xor_sync(kFull, h[i], off));
+                l[i] = min_pair<false>(l[i], __shfl_xor_sync(kFull, l[i], off));
             }
         }
         __syncthreads();  // (the page before has been read from `part`)
         if (lane < LPR) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                part[warp][0][sub * V + i] = hi[i];
-                part[warp][1][sub * V + i] = lo[i];
+            for (int i = 0; i < 4; ++i) {
+                part[warp][0][sub * 4 + i] = h[i];
+                part[warp][1][sub * 4 + i] = l[i];
             }
         }
         __syncthreads();
-        float h = 0.0f, l = 0.0f;
+        float hi[1] = {0.0f}, lo[1] = {0.0f};
         if (tid < D) {
-            h = part[0][0][tid];
-            l = part[0][1][tid];
+            uint32_t x = part[0][0][tid / 2], y = part[0][1][tid / 2];
 #pragma unroll
             for (int w = 1; w < kBoundsWarps; ++w) {
-                h = fmaxf(h, part[w][0][tid]);
-                l = fminf(l, part[w][1][tid]);
+                x = max_pair<false>(x, part[w][0][tid / 2]);
+                y = min_pair<false>(y, part[w][1][tid / 2]);
             }
-            if (!(h >= l)) h = l = 0.0f;  // no number at all
-            const float most = __uint_as_float(0x7f7f0000u);
-            h = fminf(fmaxf(h, -most), most);
-            l = fminf(fmaxf(l, -most), most);
+            hi[0] = half_of<false>(x, tid & 1);
+            lo[0] = half_of<false>(y, tid & 1);
+            finite_bounds(hi[0], lo[0]);
         }
-        float top = fmaxf(fabsf(h), fabsf(l));
+        float top = fmaxf(fabsf(hi[0]), fabsf(lo[0]));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
@@ -215,15 +224,155 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs
 #pragma unroll
         for (int w = 1; w < kBoundsWarps; ++w) top = fmaxf(top, red[w]);
         const int e = exponent_for(top);
-        const float inv = pow2(-e);
-        const size_t at = static_cast<size_t>(page) * a.Hkv + hk;
-        if (tid < D) {
-            a.bounds[at * 2 * D + tid] =
-                static_cast<int8_t>(fminf(fmaxf(ceilf(h * inv), -127.0f), 127.0f));
-            a.bounds[at * 2 * D + D + tid] =
-                static_cast<int8_t>(fminf(fmaxf(floorf(l * inv), -127.0f), 127.0f));
-        }
+        if (tid < D) store_bounds<D, 1>(a, at, tid, hi, lo, e);
         if (tid == 0) a.exps[at] = static_cast<uint8_t>(e + 127);
+    }
+}
+
+// A warp to a page.  8-bit rows: with t the largest scale of the page, values are held in
+// fp16 in units of 2^t, where a code times 2^(s - t) is exact down to s - t = -15.  Rows
+// below that take part with 2^-15: their values, at most 448 * 2^-15 < 2^-6 then, have
+// bounds' codes of -1, 0 or 1 by their sign alone as long as the codes' unit is 2^(t - 6)
+// at least; where it is not (rows whose largest code is small), the page is done again
+// in fp32.
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kBoundsThreads) bounds_warp_kernel(const BoundsArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    constexpr int V = FP8 ? 16 : 8;     // values of a 16-byte vector
+    constexpr int LPR = D / V;          // lanes per row
+    constexpr int RW = 32 / LPR;        // rows per load of the warp
+    constexpr int U = 8;
+    constexpr int N = D / 32;           // channels whose codes a lane writes
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.y;
+    int from, end, L;
+    if (!pages_of(a, b, from, end, L)) return;
+    const int sub = lane % LPR, group = lane / LPR;
+    const int items = (end - from) * a.Hkv;
+    for (int item = blockIdx.x * kBoundsWarps + warp; item < items;
+         item += gridDim.x * kBoundsWarps) {
+        const int j = from + item / a.Hkv, hk = item % a.Hkv;
+        const int page = a.table[static_cast<size_t>(b) * a.max_pages + j];
+        if (page < 0 || page >= a.num_pages) {
+            if (lane == 0) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+            continue;
+        }
+        const int n = min(a.P, L - j * a.P);
+        const size_t at = static_cast<size_t>(page) * a.Hkv + hk;
+        const uint8_t* base = static_cast<const uint8_t*>(a.k_pages) +
+                              at * a.P * D * (FP8 ? 1 : 2) + sub * 16;
+        constexpr int RB = FP8 ? D : 2 * D;
+        const uint8_t* scales = FP8 ? a.k_scales + at * a.P : nullptr;
+        int t = 0;  // 8-bit rows: the largest scale byte
+        if (FP8) {
+            for (int r = lane; r < n; r += 32) t = max(t, static_cast<int>(scales[r]));
+            t = __reduce_max_sync(kFull, t);
+        }
+        uint32_t h[V / 2], l[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            h[i] = FP8 ? 0xfc00fc00u : 0xff80ff80u;
+            l[i] = FP8 ? 0x7c007c00u : 0x7f807f80u;
+        }
+        for (int r0 = group; r0 < n + group; r0 += U * RW) {
+            uint4 x[U];
+            uint8_t s[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * RW;
+                if (r < n) {
+                    x[u] = ptx::ld_stream(base + static_cast<size_t>(r) * RB);
+                    if (FP8) s[u] = scales[r];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r0 + u * RW >= n) break;
+                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                if (FP8) {
+                    const __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(
+                        max(static_cast<int>(s[u]) - t, -15) + 15 > 0
+                            ? (max(static_cast<int>(s[u]) - t, -14) + 15) << 10
+                            : 0x0200)));  // 2^-15 is subnormal
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t y[2];
+                        f16x2_of_e4m3x4(w[i], y[0], y[1]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y[k]), f);
+                            const uint32_t v = *reinterpret_cast<uint32_t*>(&z);
+                            h[2 * i + k] = max_pair<FP8>(h[2 * i + k], v);
+                            l[2 * i + k] = min_pair<FP8>(l[2 * i + k], v);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h[i] = max_pair<FP8>(h[i], w[i]);
+                        l[i] = min_pair<FP8>(l[i], w[i]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+#pragma unroll
+            for (int off = LPR; off < 32; off <<= 1) {
+                h[i] = max_pair<FP8>(h[i], __shfl_xor_sync(kFull, h[i], off));
+                l[i] = min_pair<FP8>(l[i], __shfl_xor_sync(kFull, l[i], off));
+            }
+        }
+        // This lane's channels: N of its vector's.
+        float hi[N], lo[N];
+        const float unit = FP8 ? scale_of(t) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t x = 0, y = 0;
+#pragma unroll
+            for (int k = 0; k < 32 / LPR; ++k) {
+                if (k == group) {
+                    x = h[(k * N + i) / 2];
+                    y = l[(k * N + i) / 2];
+                }
+            }
+            hi[i] = half_of<FP8>(x, i & 1) * unit;
+            lo[i] = half_of<FP8>(y, i & 1) * unit;
+            finite_bounds(hi[i], lo[i]);
+        }
+        auto exponent = [&] {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) top = fmaxf(top, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
+            // (bits of numbers >= 0 are in the numbers' order)
+            return exponent_for(__uint_as_float(
+                __reduce_max_sync(kFull, __float_as_uint(top))));
+        };
+        int e = exponent();
+        const int ch = sub * V + group * N;
+        if (FP8 && e < t - 127 - 6) {  // (rare) the same in fp32
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                hi[i] = -INFINITY;
+                lo[i] = INFINITY;
+            }
+            for (int r = 0; r < n; ++r) {
+                const float f = scale_of(scales[r]);
+                const uint8_t* row = static_cast<const uint8_t*>(a.k_pages) + (at * a.P + r) * D + ch;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float y = half_of<true>(f16x2_of_e4m3x2(row[i]), 0) * f;
+                    hi[i] = fmaxf(hi[i], y);
+                    lo[i] = fminf(lo[i], y);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) finite_bounds(hi[i], lo[i]);
+            e = exponent();
+        }
+        store_bounds<D, N>(a, at, ch, hi, lo, e);
+        if (lane == 0) a.exps[at] = static_cast<uint8_t>(e + 127);
     }
 }
 
@@ -254,6 +403,7 @@ struct SelectArgs {
     int TC, chunks;  // tokens of a CTA, and CTAs' worth of tokens
     int cols;        // columns of a token: a power of two up to 8, or a multiple of 8
     int per_most;    // scores of a token that one CTA holds at most
+    bool gather;     // whether a CTA has room for all scores of a token of the cluster
     int B;
     bool longest_first;
     int32_t* status;
@@ -646,6 +796,20 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
             const int group = warp / NW;
             for (int t = rank + S * group; t < nt; t += S * (kSelWarps / NW)) {
                 key.at = ptx::smem_u32(scores + static_cast<size_t>(t) * a.per_most);
+                if (!decltype(in_registers)::value && key.remote && a.gather) {
+                    // (NW is all warps here) One round of reads from the others, not five.
+                    uint32_t* all = scores + static_cast<size_t>(a.TC) * a.per_most;
+#pragma unroll 8
+                    for (int i = tid; i < nb; i += kSelThreads) all[i] = key(i);
+                    __syncthreads();
+                    Keys near = key;
+                    near.remote = false;
+                    near.at = ptx::smem_u32(all);
+                    take_highest<NW, false>(near, nb, a.n_first, nb - a.n_last,
+                                            k - a.n_first - a.n_last, row_of(t), scratch[group],
+                                            group, tid);
+                    continue;
+                }
                 take_highest<NW, decltype(in_registers)::value>(
                     key, nb, a.n_first, nb - a.n_last, k - a.n_first - a.n_last, row_of(t),
                     scratch[group], group, tid % (32 * NW));
@@ -720,17 +884,25 @@ int tree_kv_block_bounds(const void* k_pages, const uint8_t* k_scales, const int
     a.P = page_size;
     a.num_pages = num_pages;
     a.status = status;
-    // The host does not know how many pages a sequence has: its CTAs take them in
-    // turn, twelve to an SM where there are that many.
-    const long long rows = static_cast<long long>(B) * Hkv;
-    const long long fill = (12LL * sms + rows - 1) / rows;
-    const int nx = static_cast<int>(fill < max_pages_per_seq ? fill : max_pages_per_seq);
+    // The host does not know how many pages a sequence has: its CTAs take them in turn,
+    // eight to an SM where there are that many.
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (k_scales == nullptr && page_size * d >= 64 * 128) {
+        const long long rows = static_cast<long long>(B) * Hkv;
+        const long long fill = (8LL * sms + rows - 1) / rows;
+        const int nx = static_cast<int>(fill < max_pages_per_seq ? fill : max_pages_per_seq);
+        return rc_of(launch_dependent(d == 128 ? bounds_kernel<128> : bounds_kernel<64>,
+                                      dim3(nx, Hkv, B), dim3(kBoundsThreads), 0, s, a));
+    }
+    const long long fill = (8LL * sms + B - 1) / B;
+    const long long most =
+        (static_cast<long long>(max_pages_per_seq) * Hkv + kBoundsWarps - 1) / kBoundsWarps;
+    const int nx = static_cast<int>(fill < most ? fill : most);
     using Kernel = void (*)(BoundsArgs);
-    const Kernel kernel = k_scales ? (d == 128 ? bounds_kernel<128, true> : bounds_kernel<64, true>)
-                                   : (d == 128 ? bounds_kernel<128, false>
-                                               : bounds_kernel<64, false>);
-    return rc_of(launch_dependent(kernel, dim3(nx, Hkv, B), dim3(kBoundsThreads), 0,
-                                  static_cast<cudaStream_t>(stream), a));
+    const Kernel kernel =
+        k_scales ? (d == 128 ? bounds_warp_kernel<128, true> : bounds_warp_kernel<64, true>)
+                 : (d == 128 ? bounds_warp_kernel<128, false> : bounds_warp_kernel<64, false>);
+    return rc_of(launch_dependent(kernel, dim3(nx, B), dim3(kBoundsThreads), 0, s, a));
 }
 
 int tree_select_blocks(const uint16_t* q, const int8_t* bounds, const uint8_t* bounds_exp,
@@ -792,6 +964,9 @@ int tree_select_blocks(const uint16_t* q, const int8_t* bounds, const uint8_t* b
             TC = 2;  // (1 again)
         }
     }
+    a.gather = S > 1 && max_pages_per_seq > 32 * kHeld * kSelWarps &&
+               need + static_cast<size_t>(max_pages_per_seq) * 4 <= 200u * 1024u;
+    if (a.gather) need += static_cast<size_t>(max_pages_per_seq) * 4;
     a.TC = TC;
     a.B = B;
     a.longest_first = B > 1 && B <= kSelThreads &&

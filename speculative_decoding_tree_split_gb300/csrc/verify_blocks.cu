@@ -44,7 +44,7 @@ constexpr int kResident = 2;  // CTAs of an SM: 128 registers, and half of the s
 constexpr int kTile = 16;        // keys
 constexpr int kWindow = 4096;    // pages of a sequence that are marked at a time
 constexpr int kMostEntries = 4096;
-constexpr int kFixed = 4;
+constexpr int kFixed = 8;
 constexpr float kMove = 8.0f;    // binades a score may exceed its row's reference by
 // 8-bit cache: P's largest at a fresh reference is 2^kLift (2^8 above it is still
 // below fp16's 2^16).
@@ -1022,23 +1022,23 @@ int launch(Args a, long long units, int dev, int sms, cudaStream_t stream) {
     const auto kernel = blocks_kernel<D, FP8, NT>;
     static std::atomic<unsigned long long> ready{0};
     if (!opt_in(reinterpret_cast<const void*>(kernel), dev, ready, true)) return TREE_ATTN_ERR_CUDA;
-    // CTAs of a cluster: those that take the least time when the SMs take all CTAs in
-    // waves, and a CTA its tiles and kFixed tiles' worth of beginning and end.
+    // CTAs of a cluster: those that take the least time, a CTA taking as long as a warp's
+    // tiles and kFixed tiles' worth of beginning and end, and an SM with c of them c times
+    // 0.62 of that (measured: two go on beside each other at 1.6 times the pace of one).
     const long long most = a.n_blocks < a.max_pages ? a.n_blocks : a.max_pages;
     const long long tiles = most * (a.P / kTile) * (a.tokens + 1) / 2 + a.tokens;
-    const long long slots = static_cast<long long>(kResident) * sms;
     int S = 1;
     long long best = -1;
     for (int s = 1; s <= 16; s *= 2) {
-        const long long waves = (units * s + slots - 1) / slots;
-        const long long each = (tiles + s * kWarps - 1) / (s * kWarps);
-        const long long cost = waves * (each + kFixed);
+        const long long on_sm = (units * s + sms - 1) / sms;
+        const long long each = (tiles + s * kWarps - 1) / (s * kWarps) + kFixed;
+        const long long cost = each * (on_sm == 1 ? 100 : 62 * on_sm);
         if (best < 0 || cost < best) {
             best = cost;
             S = s;
         }
     }
-    a.longest_first = a.B > 1 && a.B <= kThreads && units * S > slots;
+    a.longest_first = a.B > 1 && a.B <= kThreads && units * S > kResident * sms;
     return rc_of(launch_cluster(kernel, dim3(static_cast<unsigned>(units * S)),
                                 dim3(kThreads), smem, S, stream, a));
 }
