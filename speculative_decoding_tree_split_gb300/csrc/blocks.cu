@@ -249,11 +249,14 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_warp_kernel(const Bound
     int from, end, L;
     if (!pages_of(a, b, from, end, L)) return;
     const int sub = lane % LPR, group = lane / LPR;
-    const int items = (end - from) * a.Hkv;
-    for (int item = blockIdx.x * kBoundsWarps + warp; item < items;
-         item += gridDim.x * kBoundsWarps) {
+    const int items = (end - from) * a.Hkv, step = gridDim.x * kBoundsWarps;
+    const int32_t* table = a.table + static_cast<size_t>(b) * a.max_pages + from;
+    int item = blockIdx.x * kBoundsWarps + warp;
+    int page_next = item < items ? table[item / a.Hkv] : 0;
+    for (; item < items; item += step) {
         const int j = from + item / a.Hkv, hk = item % a.Hkv;
-        const int page = a.table[static_cast<size_t>(b) * a.max_pages + j];
+        const int page = page_next;
+        if (item + step < items) page_next = table[(item + step) / a.Hkv];
         if (page < 0 || page >= a.num_pages) {
             if (lane == 0) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
             continue;
@@ -316,29 +319,25 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_warp_kernel(const Bound
                 }
             }
         }
+        // The lanes of a row's vector share it out as they join it: half of what a lane
+        // has goes to the other one at each step, N channels are left.
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
+        for (int off = 16, m = V / 4; off >= LPR; off >>= 1, m >>= 1) {
+            const bool upper = (lane & off) != 0;
 #pragma unroll
-            for (int off = LPR; off < 32; off <<= 1) {
-                h[i] = max_pair<FP8>(h[i], __shfl_xor_sync(kFull, h[i], off));
-                l[i] = min_pair<FP8>(l[i], __shfl_xor_sync(kFull, l[i], off));
+            for (int i = 0; i < m; ++i) {
+                const uint32_t x = __shfl_xor_sync(kFull, upper ? h[i] : h[i + m], off);
+                const uint32_t y = __shfl_xor_sync(kFull, upper ? l[i] : l[i + m], off);
+                h[i] = max_pair<FP8>(upper ? h[i + m] : h[i], x);
+                l[i] = min_pair<FP8>(upper ? l[i + m] : l[i], y);
             }
         }
-        // This lane's channels: N of its vector's.
         float hi[N], lo[N];
         const float unit = FP8 ? scale_of(t) : 1.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            uint32_t x = 0, y = 0;
-#pragma unroll
-            for (int k = 0; k < 32 / LPR; ++k) {
-                if (k == group) {
-                    x = h[(k * N + i) / 2];
-                    y = l[(k * N + i) / 2];
-                }
-            }
-            hi[i] = half_of<FP8>(x, i & 1) * unit;
-            lo[i] = half_of<FP8>(y, i & 1) * unit;
+            hi[i] = half_of<FP8>(h[i / 2], i & 1) * unit;
+            lo[i] = half_of<FP8>(l[i / 2], i & 1) * unit;
             finite_bounds(hi[i], lo[i]);
         }
         auto exponent = [&] {
