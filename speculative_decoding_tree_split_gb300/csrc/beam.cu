@@ -6,9 +6,9 @@
 // and the K highest are taken, ties to the lowest (w, v).  Within a beam that
 // is the order of x itself, so one pass over the logits suffices: a CTA streams a
 // piece of a row and leaves the piece's maximum, its sum of exponentials (fp32)
-// and its K largest logits.  A second, small kernel joins the sums, scores the few
-// candidates in fp64 (so that the order of two beams' candidates is not that of a
-// rounding) and takes the best K.
+// and its K largest logits.  A second, small kernel joins the sums, finds with error
+// bounds in fp32 which candidates may be among the best K, scores those few in fp64 (so
+// that the order of two beams' candidates is not that of a rounding) and ranks them.
 //
 // The K largest of a piece: of its first tile the largest logit of every group of
 // four lanes is known after the maximum; the K-th largest of those 64 is a bound
@@ -351,7 +351,7 @@ struct JoinArgs {
     float* scores_out;        // [B][K]
     int32_t* rows_out;        // [B][K]
     int32_t* tokens_out;      // [B][K]
-    int W, V, K, pieces, eos, group;
+    int W, V, K, pieces, eos, group, room;
 };
 
 constexpr int kMaxBeams = 64;
@@ -405,12 +405,13 @@ template <int NT>
 __global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    extern __shared__ Cand kept_of[];     // join_smem
+    extern __shared__ Cand kept_of[];     // [room]
     __shared__ Cand tops[NT];
     __shared__ double less[kMaxBeams];    // what is taken off a beam's logits, after its maximum
     __shared__ float row_max[kMaxBeams], start[kMaxBeams];
     __shared__ uint8_t done[kMaxBeams];
     __shared__ Cand bound;
+    __shared__ uint32_t least_bound;
     __shared__ int n_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x;
@@ -484,23 +485,87 @@ __global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
         a.tokens_out[out + above] =
             static_cast<int>(flat - static_cast<unsigned long long>(w) * a.V);
     };
-    Cand held[kHeld];
+    // What a score is at least and at most, by fp32 (in units of 2^8, which leaves room
+    // for numbers of any size): three sums, and start and less rounded once each.
+    auto about = [&](int i, unsigned long long k, float& least, float& most) {
+        const int w = min(static_cast<int>((static_cast<float>(i) + 0.5f) * per_inv), a.W - 1);
+        const float from = start[w] * 0.00390625f;
+        float y = 0.0f, off = 0.0f;
+        bool some = k != 0;
+        if (done[w]) {
+            some = i == w * per_row;
+        } else if (some) {
+            const float x = logit_of(static_cast<uint32_t>(k >> 32)), top = row_max[w];
+            y = x == top ? 0.0f : x * 0.00390625f - top * 0.00390625f;
+            off = static_cast<float>(less[w]) * 0.00390625f;
+        }
+        const float s = from + (y - off);
+        const float e = (fabsf(from) + fabsf(y) + fabsf(off)) * 4.8e-7f + 1e-37f;  // > 2^-22 of each
+        some &= s > -INFINITY;
+        least = some ? s - e : -INFINITY;
+        most = some ? s + e : -INFINITY;
+    };
+    // Candidates that may be among the K best, their scores in fp64.
+    bool slow = false;
+    if (all <= 64) {
+        if (tid < all) {
+            const Cand c = cand(tid, key[0]);
+            if (c.s != 0) kept_of[atomicAdd(&n_kept, 1)] = c;
+        }
+    } else {
+        // The K-th largest of what the best of groups of four threads are at least is a bound.
+        float best = -INFINITY, top[kHeld];
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-        held[h].s = held[h].place = 0;
-        if (tid + h * NT < all) held[h] = cand(tid + h * NT, key[h]);
-    }
-    Cand lim;
-    lim.s = 1;
-    lim.place = 0;
-    if (all > 64) {
-        // The K-th best of the best ones of groups of four threads (of threads, where
-        // that might keep too many) is a bound.
-        Cand mine = held[0];
-#pragma unroll
-        for (int h = 1; h < kHeld; ++h)
-            if (better(held[h], mine)) mine = held[h];
+        for (int h = 0; h < kHeld; ++h) {
+            float least;
+            top[h] = -INFINITY;
+            if (tid + h * NT < all) {
+                about(tid + h * NT, key[h], least, top[h]);
+                best = fmaxf(best, least);
+            }
+        }
         for (int i = tid + kHeld * NT; i < all; i += NT) {
+            float least, most;
+            about(i, keys[i], least, most);
+            best = fmaxf(best, least);
+        }
+        best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
+        best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
+        float* bests = reinterpret_cast<float*>(tops);
+        if (tid % 4 == 0) bests[tid / 4] = best;
+        if (tid == 0) least_bound = 0xffffffffu;
+        __syncthreads();
+        int above = 0;
+#pragma unroll 8
+        for (int i = tid % 4; i < NT / 4; i += 4) above += bests[i] > best;
+        above += __shfl_xor_sync(kFull, above, 1);
+        above += __shfl_xor_sync(kFull, above, 2);
+        if (tid % 4 == 0 && above < a.K) atomicMin(&least_bound, key_of(best + 0.0f));
+        __syncthreads();
+        const float lim = logit_of(least_bound);  // (-inf where fewer groups have any)
+        auto keep = [&](int i, unsigned long long k) {
+            const Cand c = cand(i, k);
+            if (c.s == 0) return;
+            const int at = atomicAdd(&n_kept, 1);
+            if (at < a.room) kept_of[at] = c;
+        };
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (top[h] >= lim && top[h] > -INFINITY) keep(tid + h * NT, key[h]);
+        for (int i = tid + kHeld * NT; i < all; i += NT) {
+            const unsigned long long k = keys[i];
+            float least, most;
+            about(i, k, least, most);
+            if (most >= lim && most > -INFINITY) keep(i, k);
+        }
+        __syncthreads();
+        slow = n_kept > a.room;
+    }
+    if (slow) {  // (rare: many scores that fp32 does not tell apart) all of it in fp64
+        __syncthreads();
+        Cand mine;
+        mine.s = mine.place = 0;
+        for (int i = tid; i < all; i += NT) {
             const Cand c = cand(i, keys[i]);
             if (better(c, mine)) mine = c;
         }
@@ -518,20 +583,21 @@ __global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
         } else {
             tops[tid] = mine;
         }
-        if (tid == 0) bound = lim;
+        if (tid == 0) {
+            bound.s = 1;
+            bound.place = 0;
+            n_kept = 0;
+        }
         __syncthreads();
         rank_all<NT>(tops, n_tops, [&](int, const Cand& c, int above) {
             if (c.s != 0 && above == a.K - 1) bound = c;
         });
         __syncthreads();
-        lim = bound;
-    }
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-        if (held[h].s != 0 && !better(lim, held[h])) kept_of[atomicAdd(&n_kept, 1)] = held[h];
-    for (int i = tid + kHeld * NT; i < all; i += NT) {
-        const Cand c = cand(i, keys[i]);
-        if (c.s != 0 && !better(lim, c)) kept_of[atomicAdd(&n_kept, 1)] = c;
+        const Cand lim = bound;
+        for (int i = tid; i < all; i += NT) {
+            const Cand c = cand(i, keys[i]);
+            if (c.s != 0 && !better(lim, c)) kept_of[atomicAdd(&n_kept, 1)] = c;
+        }
     }
     __syncthreads();
     const int n = n_kept;
@@ -573,10 +639,10 @@ int join_group(int all, int K) {
 }
 
 // Candidates the join may have to keep: all where they are few, else K groups'.
-size_t join_smem(int all, int K) {
+int join_room(int all, int K) {
     const int n = join_threads(all);
-    const int most = all <= 64 ? all : K * ((all + n - 1) / n) * join_group(all, K);
-    return static_cast<size_t>(most) * sizeof(Cand);
+    const int most = K * ((all + n - 1) / n) * join_group(all, K);
+    return all <= 64 ? all : most < 256 ? 256 : most;
 }
 // Logits a piece keeps: those of K threads, where it comes to that.
 int piece_room(int K, int tiles) {
@@ -641,11 +707,12 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
                                        : piece_kernel<__nv_bfloat16>;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int all = W * pieces * K;
+    const size_t join_bytes = static_cast<size_t>(join_room(all, K)) * sizeof(Cand);
     using Join = void (*)(JoinArgs);
     const Join join = join_threads(all) == 256 ? join_kernel<256> : join_kernel<1024>;
     static std::atomic<unsigned long long> piece_ready[3], join_ready[2];
     if ((smem > 32 * 1024 && !opt_in(reinterpret_cast<const void*>(kernel), dev, piece_ready[dtype])) ||
-        (join_smem(all, K) > 24 * 1024 &&
+        (join_bytes > 24 * 1024 &&
          !opt_in(reinterpret_cast<const void*>(join), dev, join_ready[join_threads(all) != 256])))
         return TREE_ATTN_ERR_CUDA;
     const int rc = rc_of(launch_dependent(kernel, dim3(pieces, B * W), dim3(kThreads),
@@ -665,7 +732,8 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     j.pieces = pieces;
     j.eos = eos;
     j.group = join_group(all, K);
-    return rc_of(launch_dependent(join, dim3(B), dim3(join_threads(all)), join_smem(all, K), s, j));
+    j.room = join_room(all, K);
+    return rc_of(launch_dependent(join, dim3(B), dim3(join_threads(all)), join_bytes, s, j));
 }
 
 }  // extern "C"

@@ -159,3 +159,32 @@ def test_refusals():
         with pytest.raises(ta.TreeAttnError):
             bad()
     assert [t.shape for t in ta.beam_select(x[:0], s[:0], 3)] == [(0, 3)] * 3
+
+
+@pytest.mark.parametrize("W,V,k", [(16, 70000, 16), (8, 200001, 40), (64, 9000, 30)])
+def test_many_candidates_and_scores_that_are_nearly_equal(W, V, k):
+    """Joins of thousands of candidates, apart by little or by nothing, and far off."""
+    g = torch.Generator("cuda").manual_seed(V)
+    x = torch.randn(3, W, V, generator=g, device="cuda")
+    x[0] = 0.0                                    # all equal in every beam
+    x[0, 1] += 1.0
+    x[1] = 1e-6 * torch.randint(0, 3, (W, V), generator=g, device="cuda")
+    x[2, :, ::7] = torch.finfo(torch.float32).min
+    x[2, 3] = 3e38
+    s = torch.zeros(3, W, device="cuda")
+    s[1] = -1e-6 * torch.arange(W, device="cuda")
+    s[2] = -1e30 * torch.arange(W, device="cuda")
+    got = ta.beam_select(x, s, k)
+    for b in range(3):
+        # (the plain one takes too long in Python: its order by sorting)
+        y = x[b].double()
+        y = y - y.amax(1, keepdim=True)
+        y = y - y.exp().sum(1, keepdim=True).log() + s[b].double()[:, None]
+        best, at = torch.sort(y.view(-1), descending=True, stable=True)
+        rows, tokens = got[1][b].long() - b * W, got[2][b].long()
+        mine = y[rows, tokens]
+        # scores in order, the same as the best ones to the precision of the sums
+        assert float((mine - best[:k]).abs().max()) <= 2.0 ** -20 + float(best[:k].abs().max()) * 2.0 ** -22
+        assert len(set(zip(rows.tolist(), tokens.tolist()))) == k
+        if b == 0:
+            assert rows.tolist() == (at[:k] // V).tolist() and tokens.tolist() == (at[:k] % V).tolist()
