@@ -36,7 +36,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kEach = 16;                  // logits of one thread in a tile
 constexpr int kTile = kThreads * kEach;
-constexpr int kMostTiles = 8;              // of a piece
+constexpr int kMostTiles = 16;             // of a piece
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Order-preserving bits of a logit (-0 as +0, NaN as -inf: no candidate).
@@ -614,12 +614,32 @@ int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ER
 // Tiles of a row (one more than V asks for, for rows that start inside a vector).
 int tiles_of(int V) { return (V + 7 + kTile - 1) / kTile; }
 
-// Tiles of a piece: one where the tiles do not fill the SMs with the twelve CTAs
-// that they have at work or waiting, more where they do, since every piece costs a
-// bound, two reductions and K candidates for the join.
-int piece_tiles(long long rows, int V, int sms) {
-    const long long n = rows * tiles_of(V) / (12LL * sms);
-    return n < 1 ? 1 : n > kMostTiles ? kMostTiles : static_cast<int>(n);
+// Logits a piece keeps: those of K threads, where it comes to that.
+int piece_room(int K, int tiles) {
+    const int n = K * kEach * tiles;
+    return n < 512 ? 512 : n;
+}
+
+// Tiles of a piece: those that take the least time when the SMs take the pieces in waves
+// of four to an SM, a piece taking as long as its tiles and two more (measured, a warp's
+// instructions: 203 to a tile and 264 to a piece; 256 rows of 50257 logits in bf16: 13
+// pieces of one tile 25 us, two of seven 14).  Pieces of fp32 are bound by memory and end
+// at eight tiles, of which more then fit between the last (512 rows of 128000: 52 us with
+// eight, 56 with sixteen).
+int piece_tiles(long long rows, int V, int K, int sms, bool fp32) {
+    const int all = tiles_of(V), most = fp32 ? kMostTiles / 2 : kMostTiles;
+    int best = 1;
+    long long least = -1;
+    for (int t = 1; t <= most && t <= all; ++t) {
+        if (t > 1 && piece_room(K, t) * sizeof(unsigned long long) > 48 * 1024) break;
+        const long long ctas = rows * ((all + t - 1) / t);
+        const long long cost = (ctas + 4LL * sms - 1) / (4LL * sms) * (t + 2);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = t;
+        }
+    }
+    return best;
 }
 
 bool beam_shape_ok(int B, int W, int V, int K) {
@@ -628,8 +648,9 @@ bool beam_shape_ok(int B, int W, int V, int K) {
            static_cast<long long>(W) * tiles_of(V) * K <= 131072;
 }
 
-// Threads of the join: sixteen candidates to each at most, as far as that goes.
-int join_threads(int all) { return all <= 4096 ? 256 : 1024; }
+// Threads of the join: four candidates to each at most, which stay with it, as far as that
+// goes (2560 candidates: 256 threads 25 us, 1024 threads 9).
+int join_threads(int all) { return all <= 1024 ? 256 : 1024; }
 
 // Threads of a group whose best candidate counts: four, unless K groups' candidates
 // would not fit.
@@ -644,12 +665,6 @@ int join_room(int all, int K) {
     const int most = K * ((all + n - 1) / n) * join_group(all, K);
     return all <= 64 ? all : most < 256 ? 256 : most;
 }
-// Logits a piece keeps: those of K threads, where it comes to that.
-int piece_room(int K, int tiles) {
-    const int n = K * kEach * tiles;
-    return n < 512 ? 512 : n;
-}
-
 // (For pieces of one tile, the most that there can be, whatever the device.)
 size_t beam_bytes(int B, int W, int V, int K) {
     const size_t n = static_cast<size_t>(B) * W * tiles_of(V);
@@ -685,7 +700,7 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     if (cudaGetDevice(&dev) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     const int sms = sms_of(dev);
     if (sms == 0) return TREE_ATTN_ERR_CUDA;
-    const int tiles = piece_tiles(static_cast<long long>(B) * W, V, sms);
+    const int tiles = piece_tiles(static_cast<long long>(B) * W, V, K, sms, dtype == 2);
     const int pieces = (tiles_of(V) + tiles - 1) / tiles;
     const size_t smem = static_cast<size_t>(piece_room(K, tiles)) * sizeof(unsigned long long);
     PieceArgs p;
