@@ -251,9 +251,11 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
         for (int e = 0; e < kEach; ++e) top = fmaxf(top, v[e]);
         if (t == 0) {
             lim = group_bound(top, a.K, reinterpret_cast<float*>(tops), &group_least);
-            // (the bound itself is kept: a number below it, and the rest by the keys)
+            // (the bound itself is kept: a number below it, finite where the bound is +inf, and
+            // the rest by the keys)
+            const float near = fminf(lim, 3.0e38f);
             if (top >= lim)
-                keep(v, at, lim == -INFINITY ? lim : lim - fabsf(lim) * 1e-6f - 1e-30f,
+                keep(v, at, lim == -INFINITY ? lim : near - fabsf(near) * 1e-6f - 1e-30f,
                      static_cast<unsigned long long>(key_of(lim)) << 32);
         } else if (top > lim) {  // (an equal one further on is worse than K others)
             keep(v, at, lim, 1);

@@ -86,6 +86,21 @@ def test_values_that_are_no_numbers():
     check(x, s, 3, finished=done, eos=0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_many_logits_of_the_largest_value(dtype):
+    """As many as there are wanted, and more, in the first tile: +inf, and the type's largest."""
+    g = torch.Generator("cuda").manual_seed(6)
+    x = torch.randn(4, 2, 9000, generator=g, device="cuda").to(dtype)
+    x[0] = INF
+    x[1, 0] = INF
+    x[2, 1, ::3] = INF
+    x[3, :, 40:] = torch.finfo(dtype).max
+    s = torch.tensor([[0.0, -1.0]], device="cuda").expand(4, 2).contiguous()
+    for k in (1, 8, 64):
+        check(x, s, k)
+    check(-x, s, 8)
+
+
 @pytest.mark.parametrize("order", ["up", "down", "one thread", "one group"])
 def test_logits_whose_largest_lie_together(order):
     """The largest logits where one thread or one group of lanes holds all of them."""
