@@ -766,8 +766,8 @@ TREE_ATTN_API int tree_beam_select(const void *logits, int dtype, long long batc
  *   starts       nullable int32 [B] (NULL: 0): the lengths before the tokens came
  *   status       nullable: TREE_ATTN_STATUS_BAD_SEQ_LEN, _BAD_PAGE.
  * A page that several sequences of the call share has the same committed tokens in all.
- * Sizes as for the 8-bit cache; bounds and k_pages 16-byte aligned.  Returns 0,
- * -1, -2, -3, -5.
+ * Sizes as for the 8-bit cache, max_pages_per_seq * Hkv < 2^30; bounds and k_pages
+ * 16-byte aligned.  Returns 0, -1, -2, -3, -5.
  */
 TREE_ATTN_API int tree_kv_block_bounds(const void *k_pages, const uint8_t *k_scales,
                                        const int32_t *block_table, int max_pages_per_seq,

@@ -859,7 +859,8 @@ int tree_kv_block_bounds(const void* k_pages, const uint8_t* k_scales, const int
                          int max_pages_per_seq, const int32_t* starts, const int32_t* seq_lens,
                          int8_t* bounds, uint8_t* bounds_exp, int B, int Hkv, int d,
                          int page_size, int num_pages, int32_t* status, void* stream) {
-    if (!cache_shape_ok(B, Hkv, d, max_pages_per_seq, page_size, num_pages))
+    if (!cache_shape_ok(B, Hkv, d, max_pages_per_seq, page_size, num_pages) ||
+        static_cast<long long>(max_pages_per_seq) * Hkv >= (1LL << 30))
         return TREE_ATTN_ERR_SHAPE;
     if (B == 0) return TREE_ATTN_OK;
     if (!k_pages || !block_table || !seq_lens || !bounds || !bounds_exp) return TREE_ATTN_ERR_NULL;

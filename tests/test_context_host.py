@@ -128,7 +128,7 @@ def bounds(lib, **kw):
 
 def test_bounds(lib):
     for kw in (dict(B=-1), dict(B=65536), dict(H=0), dict(d=96), dict(P=8), dict(maxp=0), dict(pages=0),
-               dict(pages=1 << 27), dict(maxp=1 << 28)):
+               dict(pages=1 << 27), dict(maxp=1 << 28), dict(maxp=1 << 20, H=1 << 10, pages=1)):
         assert bounds(lib, **kw) == -2, kw
     for name in ("k", "bt", "lens", "out", "exps"):
         assert bounds(lib, **{name: None}) == -1, name

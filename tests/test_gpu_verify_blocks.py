@@ -275,6 +275,12 @@ def test_lists_over_many_pages_and_cache_rows_off_32_byte_boundaries(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,G", [(1, 1), (5, 4)])
+def test_the_longest_lists(T, G, fp8):
+    Case([16 * 4100, 31], 1, G, 128, 16, T, 4096, fp8, seed=23).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_all_pages_are_the_whole_cache_and_twice_counts_once(fp8):
     c = Case([300, 17], 2, 4, 128, 16, 5, 19, fp8, seed=10)
     for b, L in enumerate(c.lens):
