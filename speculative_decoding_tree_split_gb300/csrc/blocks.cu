@@ -642,8 +642,42 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
     if (nb > a.n_select) {
         const int32_t* table = a.table + static_cast<size_t>(b) * a.max_pages;
         for (int i = lo + tid; i < hi; i += kSelThreads) pages[i - lo] = table[i];
-        // Query codes: a warp takes a token's heads.
-        for (int t = warp; t < tiles * 8 / a.cols; t += kSelWarps) {
+        __syncthreads();
+        constexpr int NC = D / 64;  // 16-byte vectors of a row of bounds, to a lane
+        // Columns: one, two, four or eight to a token, or `wide` tiles.
+        const int log_cols = 31 - __clz(min(a.cols, 8)), per_tile = 8 >> log_cols;
+        const int t_lane = 2 * c >> log_cols, wide = a.cols >> 3;
+        const bool writes = (2 * c & ((1 << log_cols) - 1)) == 0;
+        // A tile's loads: the bounds of pages g and g + 8, their exponents.
+        uint4 x[2][2][NC];  // [page g, g + 8][hi, lo]
+        uint8_t exps[2];
+        unsigned missing = 0;  // bits of pages that are not in the pool
+        auto fetch = [&](int p0) {
+            missing = 0;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                int page = pages[min(p0 + g + 8 * r, hi - 1) - lo];
+                if (page < 0 || page >= a.num_pages) {
+                    report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                    missing |= 1u << r;
+                    page = 0;
+                }
+                const size_t at = static_cast<size_t>(page) * a.Hkv + hk;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < NC; ++j)
+                        x[r][h][j] = ptx::ld_stream(a.bounds + at * 2 * D + h * D + j * 64 + c * 16);
+                exps[r] = a.exps[at];
+            }
+        };
+        if (lo + warp * 16 < hi) fetch(lo + warp * 16);
+        // Query codes, while the first bounds are on their way: a token's heads by one warp,
+        // or by `parts` of them.
+        const int tokens = tiles * 8 / a.cols;
+        const int parts = tokens <= 1 ? kSelWarps : tokens <= 2 ? kSelWarps / 2
+                          : tokens <= kSelWarps / 2 ? 2 : 1;
+        for (int t = warp / parts; t < tokens; t += kSelWarps / parts) {
             const uint16_t* q =
                 a.q + ((static_cast<size_t>(b) * a.T + min(t0 + t, a.T - 1)) * a.Hq + hk * G) * D;
             uint32_t top = 0;
@@ -656,7 +690,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
             top = __reduce_max_sync(kFull, top);
             const float inv = pow2(-exponent_for(__uint_as_float(top << 16)));
             // Four codes at a time: vector j, word w of lane c is channels 64 j + 16 c + 4 w.
-            for (int i = lane; i < a.cols * D / 4; i += 32) {
+            for (int i = warp % parts * 32 + lane; i < a.cols * D / 4; i += 32 * parts) {
                 const int col = i / (D / 4), d = i % (D / 4) * 4;
                 const uint2 raw = *reinterpret_cast<const uint2*>(
                     q + (col < G ? col : 0) * D + d);  // columns past the group repeat its first
@@ -683,31 +717,6 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
             }
         }
         __syncthreads();
-        constexpr int NC = D / 64;  // 16-byte vectors of a row of bounds, to a lane
-        // A tile's loads: the bounds of pages g and g + 8, their exponents.
-        uint4 x[2][2][NC];  // [page g, g + 8][hi, lo]
-        uint8_t exps[2];
-        unsigned missing = 0;  // bits of pages that are not in the pool
-        auto fetch = [&](int p0) {
-            missing = 0;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                int page = pages[min(p0 + g + 8 * r, hi - 1) - lo];
-                if (page < 0 || page >= a.num_pages) {
-                    report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-                    missing |= 1u << r;
-                    page = 0;
-                }
-                const size_t at = static_cast<size_t>(page) * a.Hkv + hk;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < NC; ++j)
-                        x[r][h][j] = ptx::ld_stream(a.bounds + at * 2 * D + h * D + j * 64 + c * 16);
-                exps[r] = a.exps[at];
-            }
-        };
-        if (lo + warp * 16 < hi) fetch(lo + warp * 16);
         for (int p0 = lo + warp * 16; p0 < hi; p0 += kSelWarps * 16) {
             const float size[2] = {scale_of(exps[0]), scale_of(exps[1])};
             const bool none[2] = {(missing & 1u) != 0, (missing & 2u) != 0};
@@ -745,26 +754,22 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const SelectArgs
                 // The largest of each token's columns.
 #pragma unroll
                 for (int n = 0; n < TILES; ++n) {
+                    // Token of this lane's first column (of `wide` tiles, the same of all).
+                    const int t = wide > 1 ? (n0 + n) / wide : (n0 + n) * per_tile + t_lane;
+                    const bool again = wide > 1 && (n0 + n) % wide != 0;
+                    uint32_t* to = scores + t * a.per_most + (p0 + g - lo);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float y0 = acc[n][2 * r], y1 = acc[n][2 * r + 1];
                         if (a.cols > 1) y0 = fmaxf(y0, y1);
                         if (a.cols > 2) y0 = fmaxf(y0, __shfl_xor_sync(kFull, y0, 1));
                         if (a.cols > 4) y0 = fmaxf(y0, __shfl_xor_sync(kFull, y0, 2));
-                        const int i = p0 + g + 8 * r;
-                        auto put = [&](int t, float y, bool again) {
-                            if (i >= hi || t >= nt) return;
-                            uint32_t* to = scores + static_cast<size_t>(t) * a.per_most + (i - lo);
-                            const uint32_t k = none[r] ? 1u : score_key(y * size[r]);
-                            *to = again ? max(*to, k) : k;
-                        };
-                        const int col = (n0 + n) * 8 + 2 * c;
-                        if (a.cols == 1) {
-                            put(col, y0, false);
-                            put(col + 1, y1, false);
-                        } else if (2 * c % (a.cols < 8 ? a.cols : 8) == 0) {
-                            put(col / a.cols, y0, col % a.cols != 0);
-                        }
+                        if (!writes || p0 + g + 8 * r >= hi || t >= nt) continue;
+                        uint32_t k = none[r] ? 1u : score_key(y0 * size[r]);
+                        if (again) k = max(k, to[8 * r]);
+                        to[8 * r] = k;
+                        if (a.cols == 1 && t + 1 < nt)
+                            to[a.per_most + 8 * r] = none[r] ? 1u : score_key(y1 * size[r]);
                     }
                 }
             }
