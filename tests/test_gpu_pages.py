@@ -230,6 +230,40 @@ def test_compact_against_loops(n, share, rows, width):
     assert t0.tolist() == want_t and same(again, pools)
 
 
+@pytest.mark.parametrize("n,holes", [(31, [0]), (32, [31]), (33, [32]), (33, [0, 31]), (8191, [5, 8190]),
+                                     (8192, [0, 4096, 8191]), (8192, []), (8193, [1, 8192]),
+                                     (8192, range(8191)), (8192, range(1, 8192)),
+                                     (8193, range(0, 8193, 2)), (2047, [2046]), (2048, []),
+                                     (2048, [0, 2047]), (2048, range(1, 2048)),
+                                     (2048, range(0, 2048, 3)), (2049, [7])])
+def test_compact_of_few_and_many_holes(n, holes):
+    g = torch.Generator("cuda").manual_seed(n)
+    refs = [p % 3 + 1 for p in range(n)]
+    for p in holes:
+        refs[p] = 0
+    table = [[p if c else -1 for p, c in enumerate(refs)]]
+    pools = [torch.randint(0, 99, (n, 48), dtype=torch.uint8, device="cuda", generator=g),
+             torch.randint(0, 99, (n, 5), dtype=torch.uint8, device="cuda", generator=g)]
+    want_t, want_r, want_n, moves = context.compact(table, refs)
+    want = moved(pools, moves)
+    got = ta.kv_compact(pools, ints(table), ints(refs))
+    assert got[0].tolist() == want_t and got[1].tolist() == want_r and got[2].tolist() == [want_n]
+    assert same(pools, want)
+
+
+def test_compact_of_more_pools_than_one_launch_takes():
+    g = torch.Generator("cuda").manual_seed(8)
+    pools = [torch.randint(0, 99, (40, 16), dtype=torch.uint8, device="cuda", generator=g)
+             for _ in range(250)]
+    refs = [p % 2 for p in range(40)]
+    table = [list(range(1, 40, 2))]
+    want_t, want_r, want_n, moves = context.compact(table, refs)
+    want = moved(pools, moves)
+    got = ta.kv_compact(pools, ints(table), ints(refs))
+    assert got[0].tolist() == want_t and got[1].tolist() == want_r and got[2].tolist() == [want_n]
+    assert same(pools, want)
+
+
 def test_compact_reports_entries_without_a_page():
     pools = [torch.zeros(8, 32, dtype=torch.uint8, device="cuda")]
     status = ints([0])
