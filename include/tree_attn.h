@@ -706,7 +706,8 @@ TREE_ATTN_API int tree_kv_fork(void *const *pools, const size_t *page_bytes, int
  *   block_table_out  the table with the pages' new places (may be block_table)
  *   page_refs_out    their counts (not page_refs: -2)
  *   n_used           int32 [1]: n; pages n .. num_pages - 1 are free
- *   workspace        tree_kv_compact_workspace_size(...) bytes, 256-byte aligned
+ *   workspace        tree_kv_compact_workspace_size(...) bytes, 256-byte aligned (none
+ *                    where that is 0: for 2048 pages and fewer)
  *   status           nullable: TREE_ATTN_STATUS_BAD_PAGE (an entry without a used
  *                    page becomes -1).
  * Sizes, n_pools = 0 and return codes as tree_kv_fork.
@@ -733,7 +734,8 @@ TREE_ATTN_API int tree_kv_compact(void *const *pools, const size_t *page_bytes, 
  *                eos) with its score unchanged (its logits are not read)
  *   scores_out   fp32 [B][K];  rows_out int32 [B][K]: b * W + w;  tokens_out int32
  *                [B][K].  Where there are fewer than K candidates: -inf, -1, -1.
- *   workspace    tree_beam_workspace_size(...) bytes, 256-byte aligned
+ *   workspace    tree_beam_workspace_size(...) bytes, 256-byte aligned (none where that
+ *                is 0, as for the smallest sizes)
  * 1 <= W, K <= 64, B * W <= 65535, V <= 2^30, W * K * ceil((V + 7) / 4096) <=
  * 131072.  Scores are summed in fp64 over fp32 sums of exponentials.
  * Returns 0, -1, -2, -3, -4, -5.

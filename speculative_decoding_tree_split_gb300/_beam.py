@@ -84,5 +84,6 @@ def beam_select(logits, scores, n_select: int, *, finished=None, eos: Optional[i
            ws if W > 1 else 0, scores.data_ptr(),
            None if finished is None else finished.data_ptr(), -1 if eos is None else int(eos),
            scores_out.data_ptr(), rows_out.data_ptr(), tokens_out.data_ptr(), B, W, V, k,
-           workspace.data_ptr(), workspace.numel())
+           None if workspace is None else workspace.data_ptr(),
+           0 if workspace is None else workspace.numel())
     return scores_out, rows_out, tokens_out

@@ -51,13 +51,17 @@ def _pool_args(pools: Sequence[torch.Tensor], num_pages: Optional[int], dev: int
 _SIZES: dict = {}  # workspace bytes, by function and sizes
 
 
-def _workspace(given, at: _Place, name: str, *sizes: int) -> torch.Tensor:
+def _workspace(given, at: _Place, name: str, *sizes: int) -> Optional[torch.Tensor]:
+    """The caller's workspace or a new one; None where none is needed (or the sizes are
+    wrong, which the call itself says)."""
     if given is not None:
         _tensor(given, "workspace", (_U8,), 1, at.dev)
         return given
     need = _SIZES.get((name, sizes))
     if need is None:
-        need = _SIZES[name, sizes] = max(at.call(name, *sizes), 256)
+        need = _SIZES[name, sizes] = at.call(name, *sizes)
+    if need == 0:
+        return None
     if at.stream is None:
         return torch.empty(need, dtype=_U8, device=_DEVICES[at.dev])
     return at.empty(need, _U8)
@@ -150,8 +154,8 @@ def kv_fork(pools, block_table, seq_lens, page_refs, src, page_size: int, *, res
     at.run("tree_kv_fork", ptrs.buffer_info()[0], sizes.buffer_info()[0], n_pools,
            block_table.data_ptr(), width, seq_lens.data_ptr(), page_refs.data_ptr(),
            src.data_ptr(), each, more, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rows, n,
-           page_size, num_pages, workspace.data_ptr(), workspace.numel(),
-           None if status is None else _status(status, dev))
+           page_size, num_pages, None if workspace is None else workspace.data_ptr(),
+           0 if workspace is None else workspace.numel(), None if status is None else _status(status, dev))
     return table, lens, refs
 
 
@@ -192,6 +196,7 @@ def kv_compact(pools, block_table, page_refs, *, block_table_out=None, page_refs
     workspace = _workspace(workspace, at, "tree_kv_compact_workspace_size", num_pages)
     at.run("tree_kv_compact", ptrs.buffer_info()[0], sizes.buffer_info()[0], n_pools,
            block_table.data_ptr(), width, page_refs.data_ptr(), block_table_out.data_ptr(),
-           refs.data_ptr(), n_used.data_ptr(), rows, num_pages, workspace.data_ptr(),
-           workspace.numel(), None if status is None else _status(status, dev))
+           refs.data_ptr(), n_used.data_ptr(), rows, num_pages,
+           None if workspace is None else workspace.data_ptr(),
+           0 if workspace is None else workspace.numel(), None if status is None else _status(status, dev))
     return block_table_out, refs, n_used

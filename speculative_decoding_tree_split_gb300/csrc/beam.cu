@@ -24,6 +24,7 @@
 #include <cstdint>
 
 #include "../../include/tree_attn.h"
+#include "cluster.cuh"
 #include "launch.cuh"
 #include "mma_sync.cuh"
 #include "ptx.cuh"
@@ -38,6 +39,11 @@ constexpr int kEach = 16;                  // logits of one thread in a tile
 constexpr int kTile = kThreads * kEach;
 constexpr int kMostTiles = 16;             // of a piece
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Bytes of what the pieces of a sequence leave to be joined.
+__host__ __device__ constexpr int whole_bytes(int pieces, int K) {
+    return (pieces * (K * 8 + 8) + 15) / 16 * 16;
+}
 
 // Order-preserving bits of a logit (-0 as +0, NaN as -inf: no candidate).
 __device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : x + 0.0f; }
@@ -189,20 +195,19 @@ __device__ __forceinline__ float exp_sum(const float (&v)[kEach], float m) {
     return ((s[0] + s[1]) + (s[2] + s[3])) * ex2(fmaf(-m, kLog2e, r));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    extern __shared__ unsigned long long kept[];  // [room]
-    __shared__ unsigned long long tops[kThreads];
+// One piece of one row, by a CTA, what is found going to keys [K] and sums once ready() has
+// returned; kept: room for `a.room` keys in shared memory.
+template <typename T, typename Ready>
+__device__ __forceinline__ void take_piece(const PieceArgs& a, int row, int piece,
+                                           unsigned long long* kept, unsigned long long* keys,
+                                           float2* sums, Ready ready) {
+    __shared__ __align__(16) unsigned long long tops[kThreads];  // (read by vectors of four floats)
     __shared__ float red[2][kWarps];
     __shared__ unsigned long long bound;
     __shared__ uint32_t group_least;
     __shared__ int n_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.y, piece = blockIdx.x;
     const int b = row / a.W, w = row % a.W;
-    if (a.finished != nullptr && a.finished[row] != 0) return;  // (not read for it either)
     Row<T> r;
     r.x = static_cast<const T*>(a.logits) + b * a.batch_stride + w * a.beam_stride;
     r.V = a.V;
@@ -306,12 +311,12 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
     if (lane == 0) red[1][warp] = s;
     __syncthreads();
-    const size_t out = static_cast<size_t>(row) * a.pieces + piece;
+    ready();
     if (tid == 0) {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) sum += red[1][i];
-        a.sums[out] = make_float2(all, sum);
+        *sums = make_float2(all, sum);
     }
     int n = n_kept;
     if (n > a.room) {  // (rare) the piece again
@@ -337,13 +342,26 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
         const unsigned long long k = kept[i];
         int above = 0;
         for (int j = 0; j < n; ++j) above += kept[j] > k;
-        if (above < a.K) a.keys[out * a.K + above] = k;
+        if (above < a.K) keys[above] = k;
     }
-    for (int i = n + tid; i < a.K; i += kThreads) a.keys[out * a.K + i] = 0;
+    for (int i = n + tid; i < a.K; i += kThreads) keys[i] = 0;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int row = blockIdx.y, piece = blockIdx.x;
+    if (a.finished != nullptr && a.finished[row] != 0) return;  // (not read for it either)
+    const size_t out = static_cast<size_t>(row) * a.pieces + piece;
+    take_piece<T>(a, row, piece, reinterpret_cast<unsigned long long*>(smem), a.keys + out * a.K,
+                  a.sums + out, [] {});
 }
 
 // ---------------------------------------------------------------------------
-// Joining: one CTA per sequence.
+// Joining: one CTA per sequence, of a kernel of its own, or (few pieces) of the cluster that
+// took them.
 // ---------------------------------------------------------------------------
 struct JoinArgs {
     const unsigned long long* keys;
@@ -403,11 +421,12 @@ __device__ __forceinline__ void rank_all(const Cand* c, int n, F n_of) {
     }
 }
 
+// Sequence b by NT threads from its pieces' keys [W][pieces][K] and sums [W][pieces]; kept_of:
+// room for `a.room` candidates in shared memory.
 template <int NT>
-__global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    extern __shared__ Cand kept_of[];     // [room]
+__device__ __forceinline__ void join_pieces(const JoinArgs& a, int b,
+                                            const unsigned long long* keys, const float2* sums,
+                                            Cand* kept_of) {
     __shared__ Cand tops[NT];
     __shared__ double less[kMaxBeams];    // what is taken off a beam's logits, after its maximum
     __shared__ float row_max[kMaxBeams], start[kMaxBeams];
@@ -416,11 +435,9 @@ __global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
     __shared__ uint32_t least_bound;
     __shared__ int n_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x;
     const int row0 = b * a.W;
     const int per_row = a.pieces * a.K;
     const int all = a.W * per_row;
-    const unsigned long long* keys = a.keys + static_cast<size_t>(row0) * per_row;
     // The first few candidates of a thread stay with it; their loads come first.
     constexpr int kHeld = 4;
     unsigned long long key[kHeld];
@@ -428,7 +445,7 @@ __global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
     for (int h = 0; h < kHeld; ++h) key[h] = tid + h * NT < all ? keys[tid + h * NT] : 0ull;
     for (int w = warp; w < a.W; w += NT / 32) {
         const bool over = a.finished != nullptr && a.finished[row0 + w] != 0;
-        const float2* s = a.sums + static_cast<size_t>(row0 + w) * a.pieces;
+        const float2* s = sums + w * a.pieces;
         float m = -INFINITY, sum = 0.0f;
         for (int i = lane; i < a.pieces; i += 32) {
             const float2 y = s[i];
@@ -611,6 +628,45 @@ __global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
     }
 }
 
+template <int NT>
+__global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    extern __shared__ __align__(16) uint8_t smem[];
+    const size_t row0 = static_cast<size_t>(blockIdx.x) * a.W;
+    join_pieces<NT>(a, blockIdx.x, a.keys + row0 * a.pieces * a.K, a.sums + row0 * a.pieces,
+                    reinterpret_cast<Cand*>(smem));
+}
+
+// A sequence whose pieces are few, by one cluster: they leave what they find in the shared
+// memory of its first CTA, which joins them.  (A cluster's size is a power of two: CTAs
+// past the pieces have none.)
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4)
+    whole_kernel(const PieceArgs a, const JoinArgs j) {
+    ptx::cluster_arrive();
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int size = static_cast<int>(ptx::cluster_size());
+    const int rank = static_cast<int>(ptx::cluster_rank());
+    const int b = blockIdx.x / size;
+    const int found = a.W * a.pieces * a.K;
+    unsigned long long* keys = reinterpret_cast<unsigned long long*>(smem);
+    float2* sums = reinterpret_cast<float2*>(keys + found);
+    uint8_t* room = smem + whole_bytes(a.W * a.pieces, a.K);
+    const int row = b * a.W + rank / a.pieces;
+    const bool has = rank < a.W * a.pieces && (a.finished == nullptr || a.finished[row] == 0);
+    if (has)
+        take_piece<T>(a, row, rank % a.pieces, reinterpret_cast<unsigned long long*>(room),
+                      ptx::map_generic(keys + rank * a.K, 0), ptx::map_generic(sums + rank, 0),
+                      [] { ptx::cluster_wait(); });  // (the first CTA is there)
+    else
+        ptx::cluster_wait();
+    ptx::cluster_sync();
+    if (rank == 0) join_pieces<kThreads>(j, b, keys, sums, reinterpret_cast<Cand*>(room));
+}
+
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
 
 // Tiles of a row (one more than V asks for, for rows that start inside a vector).
@@ -644,31 +700,44 @@ int piece_tiles(long long rows, int V, int K, int sms, bool fp32) {
     return best;
 }
 
+// Tiles of a piece where a sequence's pieces go to one cluster, 0 where they do not: where
+// sixteen CTAs make pieces of at most two tiles, and the clusters of all sequences run at
+// once.  That takes the GPU as long as two kernels do (4 beams of 32000: 6.2 us), but the
+// host less, and no workspace; with pieces of four tiles it would take longer (8 beams
+// of 32000: 8.4 us for 6.3).
+constexpr int kMostCluster = 16, kWholeTiles = 2, kMostWhole = 16;
+int whole_tiles(int B, int W, int V) {
+    if (W > kMostCluster || B > kMostWhole) return 0;
+    const int all = tiles_of(V), pieces = kMostCluster / W;
+    const int t = (all + pieces - 1) / pieces;
+    return t <= kWholeTiles ? t : 0;
+}
+
 bool beam_shape_ok(int B, int W, int V, int K) {
     return B >= 0 && W >= 1 && W <= kMaxBeams && V >= 1 && K >= 1 && K <= kMaxBeams &&
            V <= (1 << 30) && static_cast<long long>(B) * W <= 65535 &&
            static_cast<long long>(W) * tiles_of(V) * K <= 131072;
 }
 
-// Threads of the join: four candidates to each at most, which stay with it, as far as that
-// goes (2560 candidates: 256 threads 25 us, 1024 threads 9).
-int join_threads(int all) { return all <= 1024 ? 256 : 1024; }
+// Threads of the join (for one sequence with 832 candidates 256 threads are 2 us faster than
+// 1024, for 32 with 1024 candidates, 32 taken, 7 us slower, for one with 8192 14 us slower:
+// four candidates stay with a thread, the others are read again).
+int join_threads(int all) { return all < 1024 ? 256 : 1024; }
 
-// Threads of a group whose best candidate counts: four, unless K groups' candidates
+// Threads of a group, of n, whose best candidate counts: four, unless K groups' candidates
 // would not fit.
-int join_group(int all, int K) {
-    const int n = join_threads(all);
+int join_group(int all, int K, int n) {
     return static_cast<size_t>(K) * ((all + n - 1) / n) * 4 * sizeof(Cand) <= 128 * 1024 ? 4 : 1;
 }
 
 // Candidates the join may have to keep: all where they are few, else K groups'.
-int join_room(int all, int K) {
-    const int n = join_threads(all);
-    const int most = K * ((all + n - 1) / n) * join_group(all, K);
+int join_room(int all, int K, int n) {
+    const int most = K * ((all + n - 1) / n) * join_group(all, K, n);
     return all <= 64 ? all : most < 256 ? 256 : most;
 }
 // (For pieces of one tile, the most that there can be, whatever the device.)
 size_t beam_bytes(int B, int W, int V, int K) {
+    if (whole_tiles(B, W, V) > 0) return 0;
     const size_t n = static_cast<size_t>(B) * W * tiles_of(V);
     return (n * K * 8 + n * 8 + 255) / 256 * 256;
 }
@@ -696,13 +765,16 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     if (!ptr_aligned(logits, dtype == 2 ? 4 : 2) || !ptr_aligned(scores, 4) ||
         !ptr_aligned(scores_out, 4) || !ptr_aligned(rows_out, 4) || !ptr_aligned(tokens_out, 4))
         return TREE_ATTN_ERR_ALIGN;
-    if (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < beam_bytes(B, W, V, K))
+    const size_t need = beam_bytes(B, W, V, K);
+    if (need > 0 && (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < need))
         return TREE_ATTN_ERR_WORKSPACE;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return TREE_ATTN_ERR_CUDA;
     const int sms = sms_of(dev);
     if (sms == 0) return TREE_ATTN_ERR_CUDA;
-    const int tiles = piece_tiles(static_cast<long long>(B) * W, V, K, sms, dtype == 2);
+    const int whole = whole_tiles(B, W, V);
+    const int tiles = whole > 0 ? whole
+                                : piece_tiles(static_cast<long long>(B) * W, V, K, sms, dtype == 2);
     const int pieces = (tiles_of(V) + tiles - 1) / tiles;
     const size_t smem = static_cast<size_t>(piece_room(K, tiles)) * sizeof(unsigned long long);
     PieceArgs p;
@@ -718,23 +790,6 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     p.pieces = pieces;
     p.tiles = tiles;
     p.room = piece_room(K, tiles);
-    using Kernel = void (*)(PieceArgs);
-    const Kernel kernel = dtype == 2   ? piece_kernel<float>
-                          : dtype == 1 ? piece_kernel<__half>
-                                       : piece_kernel<__nv_bfloat16>;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int all = W * pieces * K;
-    const size_t join_bytes = static_cast<size_t>(join_room(all, K)) * sizeof(Cand);
-    using Join = void (*)(JoinArgs);
-    const Join join = join_threads(all) == 256 ? join_kernel<256> : join_kernel<1024>;
-    static std::atomic<unsigned long long> piece_ready[3], join_ready[2];
-    if ((smem > 32 * 1024 && !opt_in(reinterpret_cast<const void*>(kernel), dev, piece_ready[dtype])) ||
-        (join_bytes > 24 * 1024 &&
-         !opt_in(reinterpret_cast<const void*>(join), dev, join_ready[join_threads(all) != 256])))
-        return TREE_ATTN_ERR_CUDA;
-    const int rc = rc_of(launch_dependent(kernel, dim3(pieces, B * W), dim3(kThreads),
-                                          smem, s, p));
-    if (rc != TREE_ATTN_OK) return rc;
     JoinArgs j;
     j.keys = p.keys;
     j.sums = p.sums;
@@ -748,9 +803,40 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     j.K = K;
     j.pieces = pieces;
     j.eos = eos;
-    j.group = join_group(all, K);
-    j.room = join_room(all, K);
-    return rc_of(launch_dependent(join, dim3(B), dim3(join_threads(all)), join_bytes, s, j));
+    const int all = W * pieces * K;
+    const int threads = whole > 0 ? kThreads : join_threads(all);
+    j.group = join_group(all, K, threads);
+    j.room = join_room(all, K, threads);
+    const size_t join_bytes = static_cast<size_t>(j.room) * sizeof(Cand);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    static std::atomic<unsigned long long> piece_ready[3], join_ready[2], whole_ready[3];
+    if (whole > 0) {
+        using Kernel = void (*)(PieceArgs, JoinArgs);
+        const Kernel kernel = dtype == 2   ? whole_kernel<float>
+                              : dtype == 1 ? whole_kernel<__half>
+                                           : whole_kernel<__nv_bfloat16>;
+        if (!opt_in(reinterpret_cast<const void*>(kernel), dev, whole_ready[dtype], true))
+            return TREE_ATTN_ERR_CUDA;
+        int size = 1;
+        while (size < W * pieces) size *= 2;
+        return rc_of(launch_cluster(
+            kernel, dim3(static_cast<unsigned>(B) * size), dim3(kThreads),
+            whole_bytes(W * pieces, K) + (smem > join_bytes ? smem : join_bytes), size, s, p, j));
+    }
+    using Kernel = void (*)(PieceArgs);
+    const Kernel kernel = dtype == 2   ? piece_kernel<float>
+                          : dtype == 1 ? piece_kernel<__half>
+                                       : piece_kernel<__nv_bfloat16>;
+    using Join = void (*)(JoinArgs);
+    const Join join = threads == 256 ? join_kernel<256> : join_kernel<1024>;
+    if ((smem > 32 * 1024 && !opt_in(reinterpret_cast<const void*>(kernel), dev, piece_ready[dtype])) ||
+        (join_bytes > 24 * 1024 &&
+         !opt_in(reinterpret_cast<const void*>(join), dev, join_ready[threads != 256])))
+        return TREE_ATTN_ERR_CUDA;
+    const int rc = rc_of(launch_dependent(kernel, dim3(pieces, B * W), dim3(kThreads),
+                                          smem, s, p));
+    if (rc != TREE_ATTN_OK) return rc;
+    return rc_of(launch_dependent(join, dim3(B), dim3(threads), join_bytes, s, j));
 }
 
 }  // extern "C"

@@ -743,7 +743,9 @@ size_t fork_bytes(int rows_in, int rows_out, int num_pages) {
     return padded((64 + 2 * static_cast<size_t>(rows_in) + 5 * static_cast<size_t>(rows_out) +
                    static_cast<size_t>(num_pages)) * 4);
 }
-size_t compact_bytes(int num_pages) { return padded((64 + 4 * static_cast<size_t>(num_pages)) * 4); }
+size_t compact_bytes(int num_pages) {
+    return num_pages <= kFewPages ? 0 : padded((64 + 4 * static_cast<size_t>(num_pages)) * 4);
+}
 
 }  // namespace
 }  // namespace treeattn
@@ -870,9 +872,10 @@ int tree_kv_compact(void* const* pools, const size_t* page_bytes, int n_pools,
     const void* ints[] = {block_table, page_refs, block_table_out, page_refs_out, n_used, status};
     for (const void* p : ints)
         if (!ptr_aligned(p, 4)) return TREE_ATTN_ERR_ALIGN;
-    if (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < compact_bytes(num_pages))
+    const size_t need = compact_bytes(num_pages);
+    if (need > 0 && (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < need))
         return TREE_ATTN_ERR_WORKSPACE;
-    CompactArgs a;
+    CompactArgs a = {};
     a.table = block_table;
     a.refs = page_refs;
     a.table_out = block_table_out;
@@ -880,16 +883,6 @@ int tree_kv_compact(void* const* pools, const size_t* page_bytes, int n_pools,
     a.n_used = n_used;
     a.entries = static_cast<long long>(rows) * max_pages_per_seq;
     a.num_pages = num_pages;
-    int32_t* w = static_cast<int32_t*>(workspace);
-    a.count = w;
-    a.before_n = w + 1;
-    a.used_of = w + 32;
-    w += 64;
-    a.copy_src = w;
-    a.copy_dst = w + num_pages;
-    w += 2 * static_cast<size_t>(num_pages);
-    a.movers = w;
-    a.to = w + num_pages;
     a.status = status;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const long long more = (a.entries + 127) / 128;
@@ -901,6 +894,16 @@ int tree_kv_compact(void* const* pools, const size_t* page_bytes, int n_pools,
                                   return launch_dependent(compact_few_kernel, grid,
                                                           dim3(kCopyThreads), 0, s, c, a);
                               });
+    int32_t* w = static_cast<int32_t*>(workspace);
+    a.count = w;
+    a.before_n = w + 1;
+    a.used_of = w + 32;
+    w += 64;
+    a.copy_src = w;
+    a.copy_dst = w + num_pages;
+    w += 2 * static_cast<size_t>(num_pages);
+    a.movers = w;
+    a.to = w + num_pages;
     const int ctas = plan_ctas(num_pages + a.entries);
     const int rp =
         rc_of(launch_cluster(compact_kernel, dim3(ctas), dim3(kPlanThreads), 0, ctas, s, a));

@@ -76,8 +76,9 @@ def compact(lib, **kw):
 
 
 def test_compact(lib):
-    need = lib.tree_kv_compact_workspace_size(8)
-    assert need > 0 and lib.tree_kv_compact_workspace_size(0) == 0
+    need = lib.tree_kv_compact_workspace_size(2049)
+    assert need > 0 and lib.tree_kv_compact_workspace_size(2048) == 0
+    assert lib.tree_kv_compact_workspace_size(0) == 0
     for kw in (dict(rows=-1), dict(maxp=0), dict(pages=0), dict(refs_out=A), dict(n_pools=-1)):
         assert compact(lib, **kw) == -2, kw
     for name in ("bt", "refs", "bt_out", "refs_out", "n", "pools"):
@@ -85,12 +86,12 @@ def test_compact(lib):
     for name in ("bt", "refs", "bt_out", "refs_out", "n", "status"):
         assert compact(lib, **{name: 3 * A + 2}) == -3, name
     for kw in (dict(ws=None), dict(ws=A + 16), dict(ws_bytes=need - 1)):
-        assert compact(lib, **kw) == -4
+        assert compact(lib, **dict(dict(pages=2049, ws_bytes=need), **kw)) == -4
 
 
 def beam(lib, **kw):
-    a = dict(x=A, dtype=0, bs=400, ws=100, scores=A, done=None, eos=-1, so=A, ro=A, to=A, B=2, W=4,
-             V=100, K=4, work=A, bytes=lib.tree_beam_workspace_size(2, 4, 100, 4))
+    a = dict(x=A, dtype=0, bs=400, ws=100, scores=A, done=None, eos=-1, so=A, ro=A, to=A, B=20, W=4,
+             V=100, K=4, work=A, bytes=lib.tree_beam_workspace_size(20, 4, 100, 4))
     a.update(kw)
     return lib.tree_beam_select(a["x"], a["dtype"], a["bs"], a["ws"], a["scores"], a["done"], a["eos"],
                                 a["so"], a["ro"], a["to"], a["B"], a["W"], a["V"], a["K"], a["work"],
@@ -98,8 +99,9 @@ def beam(lib, **kw):
 
 
 def test_beam(lib):
-    need = lib.tree_beam_workspace_size(2, 4, 100, 4)
-    assert need > 0
+    need = lib.tree_beam_workspace_size(20, 4, 100, 4)
+    assert need > 0 and lib.tree_beam_workspace_size(2, 4, 100, 4) == 0
+    assert lib.tree_beam_workspace_size(1, 4, 40000, 4) > 0
     for sizes in ((2, 0, 100, 4), (2, 65, 100, 4), (2, 4, 0, 4), (2, 4, 100, 65), (2, 4, 100, 0),
                   (20000, 4, 100, 4), (1, 64, 1 << 20, 64)):
         assert lib.tree_beam_workspace_size(*sizes) == 0
