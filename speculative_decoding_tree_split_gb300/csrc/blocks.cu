@@ -44,7 +44,11 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // ---------------------------------------------------------------------------
 // Bounds.  A page of one KV head is contiguous and is read in one go.  Large bf16 pages
 // (16 KB and more) have a CTA of four warps each, so that few pages fill the GPU; others a
-// warp each, which needs no barrier.
+// warp each, which needs no barrier.  Bound by memory with bf16 rows, by the conversions of
+// 8-bit ones, by a page's chain (its number, its rows, the join) where pages are small.
+// Measured, 64 sequences with 0.26 M tokens in all and 8 heads of 128, pages of 64: bf16
+// 94 us (5.6 TB/s), 8-bit 62 (4.3 TB/s; by four warps a page and in fp32 150); 8-bit in
+// pages of 16 121 (512).
 // ---------------------------------------------------------------------------
 struct BoundsArgs {
     const void* k_pages;
@@ -390,6 +394,12 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_warp_kernel(const Bound
 // between the lowest and the highest fall into 256 equal ranges, the one with the k-th
 // is divided again, until it holds no more than are wanted of it; two counts as a rule.
 // The pages are then written in their order.
+//
+// Measured, 64 sequences of 512 to 16384 tokens, 4 tokens each, 32 heads on 8 of 128, 64
+// pages of 16 tokens taken: 31 us (67 MB of bounds, 2.1 TB/s).  Bound by the rate of
+// instructions and their latency -- 400 to a tile of 16 pages, of which 160 widen the codes;
+// a third of the time is the choice -- with three CTAs to an SM (two: 37 us, four, which
+// spill: 63).  One token of 512 pages takes 6 us, latency alone.
 // ---------------------------------------------------------------------------
 struct SelectArgs {
     const uint16_t* q;
