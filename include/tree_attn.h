@@ -679,7 +679,8 @@ TREE_ATTN_API int tree_kv_copy_pages(void *const *pools, const size_t *page_byte
  *   outputs      block_table_out [rows_out][max_pages_per_seq], seq_lens_out
  *                [rows_out], page_refs_out [num_pages], none of them the input
  *                of its kind (-2)
- *   workspace    tree_kv_fork_workspace_size(...) bytes, 256-byte aligned
+ *   workspace    tree_kv_fork_workspace_size(...) bytes, 256-byte aligned (none where
+ *                that is 0: for 16 rows before and after, 2048 pages, and fewer)
  *   status       nullable: TREE_ATTN_STATUS_NO_PAGE (entries without a page are
  *                -1; a row whose copied page is among them ends at that page:
  *                seq_lens_out says where), _BAD_SEQ_LEN (a length, or a length

@@ -299,25 +299,39 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
     }
 }
 
-// One warp: row i of the new table, and the counts of its own pages.
-__device__ __forceinline__ void fork_row(const ForkArgs& a, int i) {
+// The plan as the first kernel left it in the workspace.
+struct Stored {
+    const ForkArgs& a;
+    const int32_t* eldest;
+    __device__ __forceinline__ explicit Stored(const ForkArgs& args) : a(args), eldest(args.eldest) {}
+    __device__ __forceinline__ int base(int i) const { return a.base[i]; }
+    __device__ __forceinline__ int free_all() const { return *a.free_all; }
+    __device__ __forceinline__ int free_at(int k) const { return a.list[k]; }
+    __device__ __forceinline__ int children(int p) const { return a.children[p]; }
+};
+
+// One warp: row i of the new table (TABLE), and the counts of its own pages in refs (REFS).
+template <bool TABLE, bool REFS, typename Plan>
+__device__ __forceinline__ void fork_row(const ForkArgs& a, const Plan& plan, int i, int32_t* refs) {
     const int lane = threadIdx.x & 31;
-    const Row r = row_of(a, i, a.eldest);
+    const Row r = row_of(a, i, plan.eldest);
     const int32_t* from = a.table + static_cast<size_t>(max(r.parent, 0)) * a.max_pages;
     int32_t* to = a.table_out + static_cast<size_t>(i) * a.max_pages;
-    int next = a.base[i];
-    const int free_all = *a.free_all;
+    int next = plan.base(i);
+    const int free_all = plan.free_all();
+    if (TABLE) {
 #pragma unroll 4
-    for (int s = lane; s < a.max_pages; s += 32) {  // the shared ones
-        if (s >= r.full && s < r.need) continue;
-        int e = s < r.full ? from[s] : -1;
-        if (s < r.full && !entry_ok(e, a.num_pages)) {
-            report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
-            e = -1;
+        for (int s = lane; s < a.max_pages; s += 32) {  // the shared ones
+            if (s >= r.full && s < r.need) continue;
+            int e = s < r.full ? from[s] : -1;
+            if (s < r.full && !entry_ok(e, a.num_pages)) {
+                report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                e = -1;
+            }
+            to[s] = e;
         }
-        to[s] = e;
+        __syncwarp();
     }
-    __syncwarp();
     for (int s0 = r.full; s0 < r.need; s0 += 32) {
         const int s = s0 + lane;
         int e = s < r.need && r.parent >= 0 ? from[s] : -1;
@@ -325,28 +339,30 @@ __device__ __forceinline__ void fork_row(const ForkArgs& a, int i) {
         const unsigned who = __ballot_sync(kFull, fresh);
         if (fresh) {
             const int k = next + __popc(who & ((1u << lane) - 1u));
-            e = k < free_all ? a.list[k] : -1;
+            e = k < free_all ? plan.free_at(k) : -1;
         }
         if (s < r.need) {
-            if (e >= 0) atomicAdd(a.refs_out + e, 1);
-            to[s] = e;
+            if (REFS && e >= 0) atomicAdd(refs + e, 1);
+            if (TABLE) to[s] = e;
         }
         next += __popc(who);
     }
 }
 
-// One warp: the counts of what row p had.
-__device__ __forceinline__ void fork_release(const ForkArgs& a, int p) {
+// One warp: the counts, in refs, of what row p had.
+template <typename Plan>
+__device__ __forceinline__ void fork_release(const ForkArgs& a, const Plan& plan, int p,
+                                             int32_t* refs) {
     bool bad;
     const int L = clamp_seq_len(a.lens[p], a.P, a.max_pages, bad);
     const int full = bad ? 0 : L / a.P;
-    const int kept = a.children[p] - 1;  // for shared pages
+    const int kept = plan.children(p) - 1;  // for shared pages
     const int32_t* from = a.table + static_cast<size_t>(p) * a.max_pages;
 #pragma unroll 4
     for (int s = (kept == 0 ? full : 0) + (threadIdx.x & 31); s < a.max_pages; s += 32) {
         const int e = from[s];
         if (entry_ok(e, a.num_pages))
-            atomicAdd(a.refs_out + e, s < full ? kept : -1);
+            atomicAdd(refs + e, s < full ? kept : -1);
         else if (e != -1)
             report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
     }
@@ -561,9 +577,9 @@ __global__ void __launch_bounds__(kCopyThreads)
         for (int i = warps - 1 - (blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32);
              i < f.rows_out + f.rows_in; i += warps) {
             if (i < f.rows_out)
-                fork_row(f, i);
+                fork_row<true, true>(f, Stored(f), i, f.refs_out);
             else
-                fork_release(f, i - f.rows_out);
+                fork_release(f, Stored(f), i - f.rows_out, f.refs_out);
         }
     }
     copy_pairs(a, a.count != nullptr ? min(max(*a.count, 0), a.n) : a.n, [&](int k, int& s, int& d) {
@@ -573,14 +589,16 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 
 // ---------------------------------------------------------------------------
-// Compact, of few pages: which are used fits into one bit each, and any CTA finds from
-// those bits and the counts before each 32 of them where a page goes, by bisection.  So
-// every CTA of the copies makes the whole plan for itself, and nothing waits for another
-// (256 pages of 128 KB, 100 used: 10.3 us for 14.4 with a plan of its own; 2048 pages,
-// 262 MB moved, 52 for 56; 4096 pages, whose counts take every CTA longer to read, 95 for 91).
+// Few pages: which of them are used (free) fits into one bit each, and any CTA finds from
+// those bits and the counts before each 32 of them, by bisection, the k-th of them.  So
+// every CTA of the copies makes the whole plan for itself, and nothing waits for another.
+// Compaction: 256 pages of 128 KB, 100 used, 10.3 us for 14.4 with a plan of its own; 2048
+// pages, 262 MB moved, 52 for 56; 4096 pages, whose counts take every CTA longer to read,
+// 95 for 91.
 // ---------------------------------------------------------------------------
 constexpr int kFewWords = 64;
 constexpr int kFewPages = 32 * kFewWords;
+constexpr int kCopyWarps = kCopyThreads / 32;
 static_assert(kFewWords <= kCopyThreads, "a thread counts a word");
 
 // Place of the r-th set bit of w.
@@ -598,45 +616,59 @@ __device__ __forceinline__ int nth_bit(uint32_t w, int r) {
     return at;
 }
 
-__global__ void __launch_bounds__(kCopyThreads, 4)
-    compact_few_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ CompactArgs f) {
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    __shared__ uint32_t bits[kFewWords];
-    __shared__ int before[kFewWords];  // used pages before those of a word
-    __shared__ int sums[kCopyThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int words = (f.num_pages + 31) / 32;
+struct Bitmap {  // in shared memory
+    uint32_t bits[kFewWords];
+    int before[kFewWords];  // marked pages before those of a word
+    int sums[kCopyWarps];
+    int words;
+
+    // By all threads: marks the pages that `is` says; how many there are.
+    template <typename Is>
+    __device__ __forceinline__ int make(int num_pages, Is is) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        const int n_words = (num_pages + 31) / 32;
 #pragma unroll 8
-    for (int w = warp; w < words; w += kCopyThreads / 32) {
-        const int p = 32 * w + lane;
-        const unsigned m = __ballot_sync(kFull, p < f.num_pages && f.refs[p] > 0);
-        if (lane == 0) bits[w] = m;
+        for (int w = tid >> 5; w < n_words; w += kCopyWarps) {
+            const int p = 32 * w + lane;
+            const unsigned m = __ballot_sync(kFull, p < num_pages && is(p));
+            if (lane == 0) bits[w] = m;
+        }
+        __syncthreads();
+        int n;
+        const int earlier = block_scan<kCopyWarps>(tid < n_words ? __popc(bits[tid]) : 0, sums, n);
+        if (tid < kFewWords) before[tid] = earlier;
+        if (tid == 0) words = n_words;
+        __syncthreads();
+        return n;
     }
-    __syncthreads();
-    int n;
-    const int earlier =
-        block_scan<kCopyThreads / 32>(tid < words ? __popc(bits[tid]) : 0, sums, n);
-    if (tid < kFewWords) before[tid] = earlier;
-    __syncthreads();
-    auto used_before = [&](int p) {
+    __device__ __forceinline__ bool has(int p) const { return (bits[p / 32] >> p % 32 & 1u) != 0; }
+    __device__ __forceinline__ int marked_before(int p) const {
         return before[p / 32] + __popc(bits[p / 32] & ((1u << p % 32) - 1u));
-    };
-    auto used_at = [&](int r) {  // the r-th used page
+    }
+    __device__ __forceinline__ int marked_at(int r) const {  // the r-th marked page
         int w = 0;
 #pragma unroll
         for (int step = kFewWords / 2; step > 0; step >>= 1)
             if (w + step < words && before[w + step] <= r) w += step;
         return 32 * w + nth_bit(bits[w], r - before[w]);
-    };
-    auto free_at = [&](int r) {  // the r-th free page
+    }
+    __device__ __forceinline__ int unmarked_at(int r) const {  // the r-th other page
         int w = 0;
 #pragma unroll
         for (int step = kFewWords / 2; step > 0; step >>= 1)
             if (w + step < words && 32 * (w + step) - before[w + step] <= r) w += step;
         return 32 * w + nth_bit(~bits[w], r - (32 * w - before[w]));
-    };
-    const int un = n == f.num_pages ? n : used_before(n);
+    }
+};
+
+__global__ void __launch_bounds__(kCopyThreads, 4)
+    compact_few_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ CompactArgs f) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    __shared__ Bitmap used;
+    const int tid = threadIdx.x;
+    const int n = used.make(f.num_pages, [&](int p) { return f.refs[p] > 0; });
+    const int un = n == f.num_pages ? n : used.marked_before(n);
     if (f.refs_out != nullptr) {  // (the first of several launches)
         const long long thread = static_cast<long long>(blockIdx.x) * kCopyThreads + tid;
         const long long threads = static_cast<long long>(gridDim.x) * kCopyThreads;
@@ -644,26 +676,141 @@ __global__ void __launch_bounds__(kCopyThreads, 4)
         for (long long i = thread; i < f.num_pages; i += threads) {
             const int p = static_cast<int>(i);
             int from = p;
-            if (p < n && (bits[p / 32] >> p % 32 & 1u) == 0)
-                from = used_at(un + p - used_before(p));
+            if (p < n && !used.has(p)) from = used.marked_at(un + p - used.marked_before(p));
             f.refs_out[p] = p < n ? f.refs[from] : 0;
         }
         for (long long i = thread; i < f.entries; i += threads) {
             int e = f.table[i];
             if (e != -1) {
-                if (!entry_ok(e, f.num_pages) || (bits[e / 32] >> e % 32 & 1u) == 0) {
+                if (!entry_ok(e, f.num_pages) || !used.has(e)) {
                     report(f.status, TREE_ATTN_STATUS_BAD_PAGE);
                     e = -1;
                 } else if (e >= n) {
-                    e = free_at(used_before(e) - un);
+                    e = used.unmarked_at(used.marked_before(e) - un);
                 }
             }
             f.table_out[i] = e;
         }
     }
     copy_pairs(a, n - un, [&](int k, int& s, int& d) {
-        s = used_at(un + k);
-        d = free_at(k);
+        s = used.marked_at(un + k);
+        d = used.unmarked_at(k);
+    });
+}
+
+// Fork, of few rows and pages: the last CTA also keeps the counts, in shared memory (16 rows
+// of 128 pages: 6.3 us for 10.3 with a plan of its own, of 2048 pages 14.5 for 18.6; 32
+// rows of 128 pages 10.4 for 10.3, of 2048 pages 24.7 for 18.7).
+constexpr int kFewRows = 16;
+
+struct FewRows {
+    int children_of[kFewRows], eldest[kFewRows], base_of[kFewRows];
+    int wants[kFewRows], tokens[kFewRows];
+    int src_of[kFewRows];  // the page that holds the last tokens of a row's parent
+    int src[kFewRows], dst[kFewRows];
+    int n_free, n_copies;
+    int refs[kFewPages];
+    Bitmap free;
+    __device__ __forceinline__ int base(int i) const { return base_of[i]; }
+    __device__ __forceinline__ int free_all() const { return n_free; }
+    __device__ __forceinline__ int free_at(int k) const { return free.marked_at(k); }
+    __device__ __forceinline__ int children(int p) const { return children_of[p]; }
+};
+
+__global__ void __launch_bounds__(kCopyThreads, 4)
+    fork_few_kernel(const __grid_constant__ CopyArgs c, const __grid_constant__ ForkArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    __shared__ FewRows sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool first = a.table_out != nullptr || a.rows_out == 0;  // (of several launches)
+    if (tid < kFewRows) {
+        sm.children_of[tid] = 0;
+        sm.eldest[tid] = 0x7fffffff;
+    }
+    __syncthreads();
+    if (tid < a.rows_out) {
+        const int p = a.src[tid];
+        if (p >= 0 && p < a.rows_in) {
+            atomicAdd(sm.children_of + p, 1);
+            atomicMin(sm.eldest + p, tid);
+        }
+    }
+    const int n_free = sm.free.make(a.num_pages, [&](int p) { return a.refs[p] == 0; });
+    if (tid == 0) sm.n_free = n_free;
+    // New pages of each row, and whether one is a copy.
+    for (int i = warp; i < a.rows_out; i += kCopyWarps) {
+        const Row r = row_of(a, i, sm.eldest);
+        const int32_t* from = a.table + static_cast<size_t>(max(r.parent, 0)) * a.max_pages;
+        int n = 0, e_full = -1;
+        bool copy = false;
+        for (int s0 = r.full; s0 < r.need; s0 += 32) {
+            const int s = s0 + lane;
+            const int e = s < r.need && r.parent >= 0 ? from[s] : -1;
+            const bool fresh = s < r.need && !keeps(a, r, e);
+            n += __popc(__ballot_sync(kFull, fresh));
+            if (s == r.full) {  // (lane 0)
+                copy = fresh && r.L % a.P != 0;
+                e_full = e;
+            }
+        }
+        if (lane == 0) {
+            sm.wants[i] = n | (copy ? 1 << 30 : 0);
+            sm.tokens[i] = r.L;
+            sm.src_of[i] = e_full;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int wants = lane < a.rows_out ? sm.wants[lane] : 0;
+        const int n = wants & 0x3fffffff;
+        const bool copy = wants >> 30 != 0;
+        int upto = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(kFull, upto, off);
+            if (lane >= off) upto += y;
+        }
+        const int total = __shfl_sync(kFull, upto, 31);
+        const unsigned who = __ballot_sync(kFull, copy);
+        if (lane < a.rows_out) {
+            const int k = upto - n;
+            int L = sm.tokens[lane];
+            sm.base_of[lane] = k;
+            if (copy) {  // its first new page takes tokens
+                const int at = __popc(who & ((1u << lane) - 1u)), e = sm.src_of[lane];
+                const int to = k < n_free ? sm.free.marked_at(k) : -1;
+                const bool ok = entry_ok(e, a.num_pages);
+                if (!ok) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+                sm.src[at] = ok && to >= 0 ? e : -1;
+                sm.dst[at] = to;
+                if (to < 0) L -= L % a.P;  // the tokens that found no page
+            }
+            if (first && blockIdx.x == 0) a.lens_out[lane] = L;
+        }
+        if (lane == 0) {
+            sm.n_copies = __popc(who);
+            if (total > n_free) report(a.status, TREE_ATTN_STATUS_NO_PAGE);
+        }
+    }
+    __syncthreads();
+    if (first) {
+        const int warps = gridDim.x * kCopyWarps;
+        for (int i = blockIdx.x * kCopyWarps + warp; i < a.rows_out; i += warps)
+            fork_row<true, false>(a, sm, i, nullptr);
+        if (blockIdx.x == gridDim.x - 1) {
+            for (int p = tid; p < a.num_pages; p += kCopyThreads) sm.refs[p] = a.refs[p];
+            __syncthreads();
+            for (int i = warp; i < a.rows_out; i += kCopyWarps)
+                fork_row<false, true>(a, sm, i, sm.refs);
+            for (int p = warp; p < a.rows_in; p += kCopyWarps) fork_release(a, sm, p, sm.refs);
+            __syncthreads();
+            for (int p = tid; p < a.num_pages; p += kCopyThreads) a.refs_out[p] = sm.refs[p];
+        }
+    }
+    copy_pairs(c, sm.n_copies, [&](int k, int& s, int& d) {
+        s = sm.src[k];
+        d = sm.dst[k];
     });
 }
 
@@ -739,7 +886,12 @@ bool pages_shape_ok(int rows, int max_pages, int num_pages) {
 
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
+bool few_rows(int rows_in, int rows_out, int num_pages) {
+    return rows_in <= kFewRows && rows_out <= kFewRows && num_pages <= kFewPages;
+}
+
 size_t fork_bytes(int rows_in, int rows_out, int num_pages) {
+    if (few_rows(rows_in, rows_out, num_pages)) return 0;
     return padded((64 + 2 * static_cast<size_t>(rows_in) + 5 * static_cast<size_t>(rows_out) +
                    static_cast<size_t>(num_pages)) * 4);
 }
@@ -802,10 +954,10 @@ int tree_kv_fork(void* const* pools, const size_t* page_bytes, int n_pools,
                           status,      seq_lens_out, page_refs_out, block_table_out};
     for (const void* p : ints)
         if (!ptr_aligned(p, 4)) return TREE_ATTN_ERR_ALIGN;
-    if (!workspace || !ptr_aligned(workspace, 256) ||
-        workspace_bytes < fork_bytes(rows_in, rows_out, num_pages))
+    const size_t bytes = fork_bytes(rows_in, rows_out, num_pages);
+    if (bytes > 0 && (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < bytes))
         return TREE_ATTN_ERR_WORKSPACE;
-    ForkArgs a;
+    ForkArgs a = {};
     a.table = block_table;
     a.lens = seq_lens;
     a.refs = page_refs;
@@ -820,6 +972,17 @@ int tree_kv_fork(void* const* pools, const size_t* page_bytes, int n_pools,
     a.max_pages = max_pages_per_seq;
     a.P = page_size;
     a.num_pages = num_pages;
+    a.status = status;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const long long more = static_cast<long long>(rows_in) + rows_out;
+    if (few_rows(rows_in, rows_out, num_pages))
+        return enqueue_copies(pools, page_bytes, n_pools, nullptr, nullptr, nullptr, rows_out,
+                              num_pages, status, 4, more > 0 ? more : 1,
+                              [&](dim3 grid, const CopyArgs& c, bool first) {
+                                  if (!first) a.table_out = nullptr;
+                                  return launch_dependent(fork_few_kernel, grid,
+                                                          dim3(kCopyThreads), 0, s, c, a);
+                              });
     int32_t* w = static_cast<int32_t*>(workspace);
     a.count = w;
     a.free_all = w + 1;
@@ -836,16 +999,14 @@ int tree_kv_fork(void* const* pools, const size_t* page_bytes, int n_pools,
     w += 2 * static_cast<size_t>(rows_out);
     a.copies = w;
     a.list = w + rows_out;
-    a.status = status;
     const long long work =
         num_pages + static_cast<long long>(rows_in + rows_out) * max_pages_per_seq;
     const int ctas = plan_ctas(work);
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int rp = rc_of(launch_cluster(fork_kernel, dim3(ctas), dim3(kPlanThreads), 0, ctas, s, a));
     if (rp != TREE_ATTN_OK) return rp;
     return enqueue_copies(
         pools, page_bytes, n_pools, a.copy_src, a.copy_dst, a.count, rows_out, num_pages, status, 8,
-        static_cast<long long>(rows_in) + rows_out, [&](dim3 grid, const CopyArgs& c, bool first) {
+        more, [&](dim3 grid, const CopyArgs& c, bool first) {
             return first ? launch_dependent(copy_kernel<ForkArgs>, grid, dim3(kCopyThreads), 0, s,
                                             c, a)
                          : launch_dependent(copy_kernel<NoTable>, grid, dim3(kCopyThreads), 0, s, c,

@@ -39,9 +39,9 @@ def test_copy_pages(lib):
 
 def fork(lib, **kw):
     p, s = pools(A)
-    need = lib.tree_kv_fork_workspace_size(2, 3, 8)
+    need = lib.tree_kv_fork_workspace_size(2, 3, 2049)
     a = dict(pools=p, bytes=s, n_pools=1, bt=A, maxp=4, lens=A, refs=A, src=A, reserve=None, all=0,
-             bt_out=2 * A, lens_out=2 * A, refs_out=2 * A, rows_in=2, rows_out=3, P=16, pages=8, ws=A,
+             bt_out=2 * A, lens_out=2 * A, refs_out=2 * A, rows_in=2, rows_out=3, P=16, pages=2049, ws=A,
              ws_bytes=need, status=None)
     a.update(kw)
     return lib.tree_kv_fork(a["pools"], a["bytes"], a["n_pools"], a["bt"], a["maxp"], a["lens"],
@@ -51,9 +51,11 @@ def fork(lib, **kw):
 
 
 def test_fork(lib):
-    need = lib.tree_kv_fork_workspace_size(2, 3, 8)
+    need = lib.tree_kv_fork_workspace_size(2, 3, 2049)
     assert need > 0 and lib.tree_kv_fork_workspace_size(-1, 3, 8) == 0
     assert lib.tree_kv_fork_workspace_size(2, 3, 0) == 0
+    assert lib.tree_kv_fork_workspace_size(16, 16, 2048) == 0
+    assert lib.tree_kv_fork_workspace_size(17, 3, 8) > 0 and lib.tree_kv_fork_workspace_size(2, 17, 8) > 0
     for kw in (dict(rows_in=-1), dict(rows_out=1 << 24), dict(rows_out=1 << 16, maxp=1 << 15), dict(maxp=0), dict(pages=0), dict(P=24),
                dict(all=-1), dict(bt_out=A), dict(lens_out=A), dict(refs_out=A), dict(n_pools=-1)):
         assert fork(lib, **kw) == -2, kw

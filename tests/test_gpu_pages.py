@@ -134,7 +134,8 @@ def check_fork(table, lens, refs, src, reserve, P, pools, one=None):
 @pytest.mark.parametrize("seed", range(8))
 @pytest.mark.parametrize("rows,out,P,width,num_pages",
                          [(1, 4, 16, 6, 64), (9, 23, 32, 9, 200), (70, 300, 16, 70, 20000),
-                          (5, 0, 64, 5, 40), (33, 65, 128, 33, 1000)])
+                          (5, 0, 64, 5, 40), (33, 65, 128, 33, 1000), (16, 16, 16, 90, 2048),
+                          (16, 16, 16, 90, 2049), (3, 16, 32, 40, 33), (16, 5, 128, 2, 31)])
 def test_fork_against_loops(rows, out, P, width, num_pages, seed):
     r = random.Random(seed * 100 + rows)
     g = torch.Generator("cuda").manual_seed(seed)
@@ -149,6 +150,18 @@ def test_fork_against_loops(rows, out, P, width, num_pages, seed):
     else:
         one = min([r.choice([0, 1, P])] + [width * P - (lens[p] if p >= 0 else 0) for p in src])
         check_fork(table, lens, refs, src, [one] * out, P, pools, one=one)
+
+
+@pytest.mark.parametrize("num_pages", [500, 3000])
+def test_fork_of_more_pools_than_one_launch_takes_and_long_reserves(num_pages):
+    g = torch.Generator("cuda").manual_seed(12)
+    table = [list(range(10, 110)) + [-1] * 100, list(range(110, 113)) + [-1] * 197]
+    lens, refs = [16 * 20 + 3, 47], [0] * num_pages
+    for p in range(10, 113):
+        refs[p] = 1
+    pools = [torch.randint(0, 99, (num_pages, 16), dtype=torch.uint8, device="cuda", generator=g)
+             for _ in range(250)]
+    check_fork(table, lens, refs, [0, 1, 0, -2], [16 * 150, 1, 40, 16 * 33], 16, pools)
 
 
 def test_fork_identity_release_and_new_rows():
@@ -323,7 +336,7 @@ def test_refusals():
     with pytest.raises(ValueError):
         ta.kv_fork([pools[0].t()], t, l, c, s, 16)
     with pytest.raises(ta.TreeAttnError):
-        ta.kv_fork(pools, t, l, c, s, 16,
+        ta.kv_fork(pools, t, l, c, ints([-1] * 17), 16,
                    workspace=torch.empty(256, dtype=torch.uint8, device="cuda")[:16])
     with pytest.raises(ValueError):
         ta.kv_compact(pools, t, c, page_refs_out=c)
