@@ -54,9 +54,9 @@ def kv_block_bounds(k_pages, block_table, seq_lens, *, k_scales=None, starts=Non
     k_pages [num_pages][Hkv][P][d], bf16 or (with k_scales) 8-bit codes.  Writes the
     pages that hold positions starts[b] (None: 0) .. seq_lens[b] - 1, over their
     committed tokens (the same ones in all sequences that share a page); call it after
-    tokens were appended or committed, with the lengths before as ``starts``.  Returns (bounds int8 [num_pages][Hkv][2][d],
-    bounds_exp uint8 [num_pages][Hkv]); rows of other pages keep what they held
-    (are uninitialised when the call makes them).
+    tokens were appended or committed, with the lengths before as ``starts``.  Returns
+    (bounds int8 [num_pages][Hkv][2][d], bounds_exp uint8 [num_pages][Hkv]); rows of
+    other pages keep what they held (are uninitialised when the call makes them).
     """
     try:
         dev = k_pages.get_device()
