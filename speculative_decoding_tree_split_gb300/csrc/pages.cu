@@ -212,21 +212,24 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const ForkArgs a) {
             a.eldest[p] = eldest[p];
         }
     }
-    // New pages that each row wants.
-    for (int i = gwarp; i < a.rows_out; i += gwarps) {
+    // New pages that each row wants: all it needs, a thread to a row; a parent's first row
+    // keeps what it can, a warp to a parent.
+    for (int i = gtid; i < a.rows_out; i += gthreads) {
+        const Row r = row_of(a, i, held ? eldest : a.eldest);
+        const int n = max(r.need - r.full, 0);
+        if (!r.eldest) a.wants[i] = n | (n > 0 && r.L % a.P != 0 ? 1 << 30 : 0);
+    }
+    for (int p = gwarp; p < a.rows_in; p += gwarps) {
+        const int i = held ? eldest[p] : __ldcg(a.eldest + p);
+        if (i >= a.rows_out) continue;  // (nobody continues it)
         const Row r = row_of(a, i, held ? eldest : a.eldest);
         int n = 0;
         bool copy = false;
         for (int s0 = r.full; s0 < r.need; s0 += 32) {
             const int s = s0 + lane;
-            bool fresh = false;
-            if (s < r.need) {
-                const int e = r.parent >= 0
-                                  ? a.table[static_cast<size_t>(r.parent) * a.max_pages + s]
-                                  : -1;
-                fresh = !keeps(a, r, e);
-                copy |= fresh && s == r.full && r.L % a.P != 0;
-            }
+            const bool fresh =
+                s < r.need && !keeps(a, r, a.table[static_cast<size_t>(p) * a.max_pages + s]);
+            copy |= fresh && s == r.full && r.L % a.P != 0;
             n += __popc(__ballot_sync(kFull, fresh));
         }
         copy = __any_sync(kFull, copy);
@@ -699,8 +702,8 @@ __global__ void __launch_bounds__(kCopyThreads, 4)
 }
 
 // Fork, of few rows and pages: the last CTA also keeps the counts, in shared memory (16 rows
-// of 128 pages: 6.3 us for 10.3 with a plan of its own, of 2048 pages 14.5 for 18.6; 32
-// rows of 128 pages 10.4 for 10.3, of 2048 pages 24.7 for 18.7).
+// of 128 pages: 6.3 us for 8.3 and more with a plan of its own, of 2048 pages 14.4 for 18.6;
+// 32 rows of 128 pages 10.4 for 8.4, of 2048 pages 24.7 for 18.6).
 constexpr int kFewRows = 16;
 
 struct FewRows {

@@ -285,16 +285,17 @@ def test_compact_reports_entries_without_a_page():
     assert got[0].tolist() == [[0, -1, -1, -1, -1]] and int(status) == ta.STATUS_BAD_PAGE
 
 
-def test_captured_and_replayed_on_two_streams_at_once():
+@pytest.mark.parametrize("rows,out,n", [(40, 100, 4000), (9, 16, 600)])
+def test_captured_and_replayed_on_two_streams_at_once(rows, out, n):
     """Two captured forks with workspaces of their own, replayed at once, twice."""
     states = []
     for seed in range(2):
         r = random.Random(seed)
-        table, lens, refs = random_state(r, 40, 16, 40, 4000)
-        src = [r.randrange(-1, 40) for _ in range(100)]
+        table, lens, refs = random_state(r, rows, 16, 40, n)
+        src = [r.randrange(-1, rows) for _ in range(out)]
         g = torch.Generator("cuda").manual_seed(seed)
-        pool = torch.randint(0, 256, (4000, 4096), dtype=torch.uint8, device="cuda", generator=g)
-        want = context.fork(table, lens, refs, src, [0] * 100, 16)
+        pool = torch.randint(0, 256, (n, 4096), dtype=torch.uint8, device="cuda", generator=g)
+        want = context.fork(table, lens, refs, src, [0] * out, 16)
         states.append((ints(table), ints(lens), ints(refs), ints(src), pool, pool.clone(), want))
     graphs = []
     for t, l, c, s, pool, _, _ in states:
@@ -302,8 +303,8 @@ def test_captured_and_replayed_on_two_streams_at_once():
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            out = ta.kv_fork([pool], t, l, c, s, 16)
-        graphs.append((graph, out))
+            got = ta.kv_fork([pool], t, l, c, s, 16)
+        graphs.append((graph, got))
     streams = [torch.cuda.Stream() for _ in states]
     for (t, l, c, s, pool, first, _) in states:
         pool.copy_(first)
@@ -313,9 +314,9 @@ def test_captured_and_replayed_on_two_streams_at_once():
             with torch.cuda.stream(stream):
                 graph.replay()
     torch.cuda.synchronize()
-    for (_, out), (_, _, _, _, pool, first, want) in zip(graphs, states):
-        assert out[0].tolist() == want[0] and out[1].tolist() == want[1]
-        assert out[2].tolist() == want[2] and same([pool], moved([first], want[3]))
+    for (_, got), (_, _, _, _, pool, first, want) in zip(graphs, states):
+        assert got[0].tolist() == want[0] and got[1].tolist() == want[1]
+        assert got[2].tolist() == want[2] and same([pool], moved([first], want[3]))
 
 
 def test_refusals():
