@@ -702,8 +702,8 @@ __global__ void __launch_bounds__(kCopyThreads, 4)
 }
 
 // Fork, of few rows and pages: the last CTA also keeps the counts, in shared memory (16 rows
-// of 128 pages: 6.3 us for 8.3 and more with a plan of its own, of 2048 pages 14.4 for 18.6;
-// 32 rows of 128 pages 10.4 for 8.4, of 2048 pages 24.7 for 18.6).
+// of 128 pages: 6.3 us, with a plan of its own 8.4 to 10.4; of 2048 pages 14.5 and 18.6; 32
+// rows of 128 pages 10.4 either way, of 2048 pages 24.7 and 20.5).
 constexpr int kFewRows = 16;
 
 struct FewRows {
