@@ -51,11 +51,15 @@ constexpr int kTile = 16;        // keys
 constexpr int kWindow = 4096;    // pages of a sequence that are marked at a time
 constexpr int kMostEntries = 4096;
 constexpr int kFixed = 8;
-constexpr float kMove = 8.0f;    // binades a score may exceed its row's reference by
-// 8-bit cache: P's largest at a fresh reference is 2^kLift (2^8 above it is still
-// below fp16's 2^16).
-constexpr int kLift = 6;
-constexpr int kNoScale = -1000;  // no key has been seen, so no scale byte
+// References.  With a bf16 cache a row's is the largest score that it had when it last
+// moved, which it does where a score exceeds it by more than kMove binades.  With an 8-bit
+// one the scale of a key's value joins its exponent, e = x + s, p = 2^(e - reference): o
+// sums p times the value's codes, the row's sum takes p 2^-s.  So a large scale costs only
+// rows that see it, and those no more than their own largest p max|v| says.  p goes to
+// the product as fp16 and may reach 2^kMost; a new reference, a whole number so that s less
+// it is exact, leaves the largest at 2^kFresh or above.
+constexpr float kMove = 8.0f;
+constexpr float kMost = 15.0f, kFresh = 7.0f;
 constexpr float kLeast = 1.17549435e-38f;  // of a score unit: never 0, which would lose -inf
 constexpr float kLow = -3.0e38f; // a reference before the first key
 
@@ -116,13 +120,24 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// 8-bit cache: exponents s of the value scales of a lane's two keys, and 2^-s.  (With s in
+// [-56, 40] a p that fp32 does not hold takes less than 2^-70 from the row's sum, of which
+// the largest p has 2^-33 or more.)
+struct ValueScales {
+    float s[2] = {0.0f, 0.0f}, inv[2] = {1.0f, 1.0f};
+    __device__ __forceinline__ void set(int i, uint32_t byte) {
+        s[i] = static_cast<float>(static_cast<int>(byte) - 127);
+        inv[i] = __int_as_float(max(254 - static_cast<int>(byte), 0) << 23);
+    }
+};
+
 // One warp's running state for NT * 8 query rows; a lane holds columns 2c and
 // 2c + 1 of every column tile.  Scores x come in units that make a logarithm to base 2
 // of them by a factor (> 0), a column's own (8-bit cache) or one for all.
 template <int D, bool FP8, int NT>
 struct State {
     float unit[FP8 ? NT : 1][FP8 ? 2 : 1];
-    float m[NT][2];           // references, logarithms to base 2
+    float m[NT][2];           // references, logarithms to base 2 (kLow: of no key yet)
     float l[NT][2];           // this lane's part of the sums
     float o[NT][D / 16][4];   // [column tile][channel tile]
 
@@ -130,36 +145,42 @@ struct State {
         return FP8 ? unit[FP8 ? n : 0][FP8 ? i : 0] : unit[0][0];
     }
     // Logarithms above the references.
-    __device__ __forceinline__ void above(float (&y)[NT][4], const float (&x)[NT][4]) const {
+    __device__ __forceinline__ void above(float (&y)[NT][4], const float (&x)[NT][4],
+                                          const ValueScales& v) const {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[n][i] = fmaf(x[n][i], factor(n, i & 1), -m[n][i & 1]);
+            for (int i = 0; i < 4; ++i)
+                y[n][i] = fmaf(x[n][i], factor(n, i & 1),
+                               FP8 ? v.s[i >> 1] - m[n][i & 1] : -m[n][i & 1]);
     }
 };
 
-// Scores to probabilities (in place), summed; the references are moved where a score
-// exceeds one by more than kMove.
+// Scores to probabilities (in place), summed; the references are moved where one is
+// exceeded by too much.
 template <int D, bool FP8, int NT>
-__device__ __forceinline__ void exponents(State<D, FP8, NT>& st, float (&x)[NT][4]) {
+__device__ __forceinline__ void exponents(State<D, FP8, NT>& st, float (&x)[NT][4],
+                                          const ValueScales& v) {
     float y[NT][4];
-    st.above(y, x);
+    st.above(y, x, v);
     float top = -INFINITY;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, y[n][i]);
-    if (__any_sync(kFull, top > kMove)) {
+    if (__any_sync(kFull, top > (FP8 ? kMost : kMove))) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float t = fmaxf(x[n][i], x[n][i + 2]);
+                float t = FP8 ? fmaxf(fmaf(x[n][i], st.factor(n, i), v.s[0]),
+                                      fmaf(x[n][i + 2], st.factor(n, i), v.s[1]))
+                              : fmaxf(x[n][i], x[n][i + 2]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     t = fmaxf(t, __shfl_xor_sync(kFull, t, off));
-                t = fmaxf(t * st.factor(n, i), st.m[n][i]);
+                t = fmaxf(FP8 ? floorf(t) - kFresh : t * st.factor(n, i), st.m[n][i]);
                 f[i] = ex2(st.m[n][i] - t);
                 st.m[n][i] = t;
                 st.l[n][i] *= f[i];
@@ -169,14 +190,15 @@ __device__ __forceinline__ void exponents(State<D, FP8, NT>& st, float (&x)[NT][
 #pragma unroll
                 for (int i = 0; i < 4; ++i) st.o[n][d][i] *= f[i & 1];
         }
-        st.above(y, x);
+        st.above(y, x, v);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[n][i] = ex2(y[n][i]);
-            st.l[n][i & 1] += x[n][i];
+            st.l[n][i & 1] = FP8 ? fmaf(x[n][i], v.inv[i >> 1], st.l[n][i & 1])
+                                 : st.l[n][i & 1] + x[n][i];
         }
 }
 
@@ -311,20 +333,19 @@ __device__ __forceinline__ void load_values(uint4 (&v)[4], uint32_t at, int ch, 
     }
 }
 
-// O^T += V^T P^T for 16 keys of bf16 values, the probabilities (times f) as two
-// bf16 numbers: what one leaves out (2^-9) would be the largest error before the
+// O^T += V^T P^T for 16 keys of bf16 values, the probabilities as two bf16 numbers: what one leaves out (2^-9) would be the largest error before the
 // result is rounded, and the product is not what bounds the kernel.  SPREAD: a lane's
 // channels are 8 of every 64, else D / 8 in a row.
 template <bool CAREFUL, bool SPREAD, int D, bool FP8, int NT>
 __device__ __forceinline__ void add_values_bf16(State<D, FP8, NT>& st, const float (&p)[NT][4],
-                                                uint32_t v_at, int live, float f,
+                                                uint32_t v_at, int live,
                                                 const bool (&mine)[NT][2], int g, int c) {
     uint32_t b[NT][2][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float y0 = p[n][2 * h] * f, y1 = p[n][2 * h + 1] * f;
+            const float y0 = p[n][2 * h], y1 = p[n][2 * h + 1];
             const uint32_t hi = pack_bf16(y0, y1);
             const uint32_t lo =
                 pack_bf16(y0 - __uint_as_float(hi << 16), y1 - __uint_as_float(hi & 0xffff0000u));
@@ -418,7 +439,8 @@ struct Smem {
     static constexpr int R = 8 * NT;         // query rows
     static constexpr int kStride = D + 4;    // floats of a partial row
     static constexpr int RB = FP8 ? D : 2 * D;       // bytes of a cache row
-    static constexpr int kSlot = kTile * RB + (FP8 ? 16 : 0);  // K or V of a tile, and its scales
+    // K or V of a tile; 8-bit cache: behind K the scales of its keys and of their values.
+    static constexpr int kSlot = kTile * RB + (FP8 ? 32 : 0);
     // Slots of a warp's ring: 8 and 12 KB (d = 128), which also hold a tile of tree tokens.
     static constexpr int kSlots = FP8 ? 4 : 3;
     union alignas(16) Warp {
@@ -486,7 +508,6 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
 #pragma unroll
             for (int i = 0; i < 4; ++i) st.o[n][d][i] = 0.0f;
     }
-    int sref = kNoScale;  // 8-bit cache: accumulators are in units of 2^(sref - 127 - kLift)
 
     // ---- pages
     // Tile i is rows i % (P / 16) * 16 of page i / (P / 16); a warp takes every step-th,
@@ -516,7 +537,7 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
             const uint8_t* base =
                 static_cast<const uint8_t*>(a.kv[V ? 1 : 0]) + static_cast<size_t>(first) * RB;
             copy_tile<RB, V>(slot, base);
-            if (FP8 && lane == 0) copy16(slot + kTile * RB, a.scales[V ? 1 : 0] + first);
+            if (FP8 && !V && lane < 2) copy16(slot + kTile * RB + 16 * lane, a.scales[lane] + first);
             if (V) ahead = find(ahead + e_step, next);
         }
         copies_commit();
@@ -544,6 +565,7 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
         const int live = min(static_cast<int>(here.live_who & 255u) - off, kTile);
         const unsigned seers = here.live_who >> 8;
         float x[NT][4];
+        ValueScales vs;
         arrive();
         if (!FP8) {
             scores_bf16<D, NT>(x, slot, sm.q[0], g, c);
@@ -579,6 +601,8 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[n][j] *= j < 2 ? f0 : f1;
+            vs.set(0, ld_shared_u8(slot + kTile * RB + 16 + g));
+            vs.set(1, ld_shared_u8(slot + kTile * RB + 16 + g + 8));
         }
         refill(AfterK());
         if (live < kTile) hide<NT>(x, live, g);
@@ -590,40 +614,16 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
                 for (int j = 0; j < 2; ++j) mine[n][j] = (token[n][j] & seers) != 0;
             hide_others<NT>(x, mine);
         }
-        exponents(st, x);
+        exponents(st, x, vs);
         arrive();
         if (!FP8) {
-            add_values_bf16<CAREFUL, true>(st, x, slot, live, 1.0f, mine, g, c);
+            add_values_bf16<CAREFUL, true>(st, x, slot, live, mine, g, c);
         } else {
-            const uint32_t s = slot + kTile * RB;
-            // Scale bytes of keys g and g + 8; of keys that are not there, one in use.
-            int sv0 = static_cast<int>(ld_shared_u8(s + g));
-            int sv1 = static_cast<int>(ld_shared_u8(s + g + 8));
-            if (live < kTile) {
-                const int some = static_cast<int>(ld_shared_u8(s));
-                if (g >= live) sv0 = some;
-                if (g + 8 >= live) sv1 = some;
-            }
-            // The unit of the accumulators follows the largest value scale.
-            const int top = __reduce_max_sync(kFull, max(sv0, sv1));
-            if (top > sref) {
-                const float f = sref == kNoScale ? 1.0f : pow2(sref - top);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) st.o[n][d][j] *= f;
-                sref = top;
-            }
-            // 2^(byte - sref + kLift): 2^-90 at the least for the bytes that caches hold.
-            const float pf0 = __int_as_float(max(sv0 - sref + kLift + 127, 0) << 23);
-            const float pf1 = __int_as_float(max(sv1 - sref + kLift + 127, 0) << 23);
             uint32_t p[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                p[n][0] = ptx::transpose8(pack_f16(x[n][0] * pf0, x[n][1] * pf0));
-                p[n][1] = ptx::transpose8(pack_f16(x[n][2] * pf1, x[n][3] * pf1));
+                p[n][0] = ptx::transpose8(pack_f16(x[n][0], x[n][1]));
+                p[n][1] = ptx::transpose8(pack_f16(x[n][2], x[n][3]));
             }
             uint4 v[4];
             if (D == 128) {
@@ -689,11 +689,9 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
                 }
                 hide<NT>(x, here, g);
                 hide_others<NT>(x, mine);
-                exponents(st, x);
-                if (FP8 && sref == kNoScale) sref = 127;
+                exponents(st, x, ValueScales());
                 // (the accumulators' order of channels)
-                add_values_bf16<CAREFUL, !FP8>(st, x, v_at, here, FP8 ? pow2(kLift + 127 - sref) : 1.0f,
-                                               mine, g, c);
+                add_values_bf16<CAREFUL, !FP8>(st, x, v_at, here, mine, g, c);
             }
         }
     }
@@ -701,7 +699,6 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
 
     // ---- this warp's rows to shared memory, where its ring was
     copies_wait<0>();
-    const float unit_of = FP8 && sref != kNoScale ? pow2(sref - 127 - kLift) : 1.0f;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -718,8 +715,8 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
             for (int d = 0; d < D / 16; d += 2) {
                 const int ch = FP8 ? channel_fp8<D>(d, g) : channel_bf16<D>(d, g);
                 *reinterpret_cast<float4*>(&sm.warp[warp].rows[r][ch]) =
-                    make_float4(st.o[n][d][i] * unit_of, st.o[n][d][i + 2] * unit_of,
-                                st.o[n][d + 1][i] * unit_of, st.o[n][d + 1][i + 2] * unit_of);
+                    make_float4(st.o[n][d][i], st.o[n][d][i + 2], st.o[n][d + 1][i],
+                                st.o[n][d + 1][i + 2]);
             }
         }
     return true;
