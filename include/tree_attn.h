@@ -737,8 +737,11 @@ TREE_ATTN_API int tree_kv_compact(void *const *pools, const size_t *page_bytes, 
  *                [B][K].  Where there are fewer than K candidates: -inf, -1, -1.
  *   workspace    tree_beam_workspace_size(...) bytes, 256-byte aligned (none where that
  *                is 0, as for the smallest sizes)
- * 1 <= W, K <= 64, B * W <= 65535, V <= 2^30, W * K * ceil((V + 7) / 4096) <=
- * 131072.  Scores are summed in fp64 over fp32 sums of exponentials.
+ * 1 <= W, K <= 64, B * W <= 65535, V <= 2^30, W * K * ceil(V / 4096) <= 131072.
+ * Scores are in fp64 past fp32 sums of exponentials, whose terms are taken by their
+ * places in the row: beams with the same logits and scores tie wherever their rows lie.
+ * Candidates of beams with other logits whose scores are within the sums' rounding
+ * (about 2^-21) of each other may stand in either order.
  * Returns 0, -1, -2, -3, -4, -5.
  */
 TREE_ATTN_API size_t tree_beam_workspace_size(int B, int W, int V, int K);

@@ -47,7 +47,9 @@ def beam_select(logits, scores, n_select: int, *, finished=None, eos: Optional[i
     ``eos``) stands for itself alone, as (w, eos) with its score unchanged.
     Returns (scores fp32, rows int32, tokens int32), each [B][n_select], best first,
     ties to the lowest (w, v); rows are b * W + w, the ``src`` of ``kv_fork``.  NaN and
-    -inf logits are never taken; where nothing is left: -inf, -1, -1.
+    -inf logits are never taken; where nothing is left: -inf, -1, -1.  Beams with the same
+    logits and scores tie wherever they lie in memory; scores of other beams are told apart
+    to fp32's rounding of the sums (about 2^-21).
     """
     k = int(n_select)
     try:

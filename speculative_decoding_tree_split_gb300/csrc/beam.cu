@@ -8,7 +8,9 @@
 // piece of a row and leaves the piece's maximum, its sum of exponentials (fp32)
 // and its K largest logits.  A second, small kernel joins the sums, finds with error
 // bounds in fp32 which candidates may be among the best K, scores those few in fp64 (so
-// that the order of two beams' candidates is not that of a rounding) and ranks them.
+// that no rounding but the sums' own comes into the order of two beams' candidates) and
+// ranks them.  The sums' terms go by their places in the row, not by its address: beams with
+// the same logits have the same sums, and tie.
 //
 // The K largest of a piece: of its first tile the largest logit of every group of
 // four lanes is known after the maximum; the K-th largest of those 64 is a bound
@@ -133,33 +135,83 @@ __device__ __forceinline__ float group_bound(float top, int K, float* tops, uint
     return logit_of(*bound);
 }
 
-template <typename T>
+// A row of logits.  Which thread takes a logit, and when, goes by its index in the row
+// alone, so that rows of the same logits have the same sums, bit for bit, wherever they
+// begin.  A row that begins inside a 16-byte vector (SKEWED: it may) is read by whole
+// vectors all the same, a lane's and the next one's making up what is the lane's.
+template <typename T, bool SKEWED>
 struct Row {
     const T* x;
-    int V, skew;  // `skew` logits before the row's first share its first vector, unread
+    int V, skew;  // `skew` logits before the row's first share its first vector
     static constexpr int N = 16 / sizeof(T);
+    static constexpr int kVecs = kEach / N;
+
+    // What a thread asks for of a tile: its vectors; lane 0 also the one behind its warp's.
+    struct Raw {
+        uint4 own[kVecs];
+        uint4 behind;
+    };
 
     // Index of logit e of a thread in the tile that begins at `first`.
     __device__ __forceinline__ int index(int first, int e) const {
-        return first + ((e / N) * kThreads + static_cast<int>(threadIdx.x)) * N - skew + e % N;
+        return first + static_cast<int>(threadIdx.x >> 5) * (32 * kEach) + (e / N) * (32 * N) +
+               static_cast<int>(threadIdx.x & 31) * N + e % N;
     }
-    static constexpr int kVecs = kEach / N;
-
-    // Whether a tile lies inside the row, so that its vectors can be read whole.
+    // Whether a tile's vectors lie inside the row, so that they can be read whole.
     __device__ __forceinline__ bool inside(int first) const {
-        return first >= skew && first + kTile - skew <= V;
+        if (!SKEWED || skew == 0) return first + kTile <= V;
+        return first >= skew && first + kTile + N - skew <= V;
     }
-    __device__ __forceinline__ void fetch(int first, uint4 (&raw)[kVecs]) const {
+    __device__ __forceinline__ void fetch(int first, Raw& raw) const {
+        const T* from = SKEWED ? x - skew : x;
 #pragma unroll
         for (int u = 0; u < kVecs; ++u)
-            raw[u] = ptx::ld_stream(x + index(first, u * N));  // (volatile: asked for here)
+            raw.own[u] = ptx::ld_stream(from + index(first, u * N));  // (volatile: asked for here)
+        if (SKEWED && skew != 0 && (threadIdx.x & 31) == 0)
+            raw.behind = ptx::ld_stream(from + index(first, 0) + 32 * kEach);
     }
-    __device__ __forceinline__ void unpack(const uint4 (&raw)[kVecs], float (&v)[kEach]) const {
+    static __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+        return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    }
+    // The logits of a thread's vectors, WORDS (and a half: HALF) of them from the next lane's.
+    template <int WORDS, bool HALF>
+    __device__ __forceinline__ void unpack_as(const Raw& raw, float (&v)[kEach]) const {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) {
-            const T* t = reinterpret_cast<const T*>(&raw[u]);
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = word(raw.own[u], i);
+                if (i < WORDS + HALF) {
+                    // (behind lane 31's vector lies lane 0's of the next turn, or what is
+                    // behind the warp's)
+                    const uint32_t after =
+                        word(u + 1 < kVecs ? raw.own[(u + 1) % kVecs] : raw.behind, i);
+                    w[i + 4] = __shfl_sync(kFull, lane == 0 ? after : w[i], (lane + 1) & 31);
+                }
+            }
+            uint32_t mine[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mine[i] = HALF ? __funnelshift_r(w[i + WORDS], w[i + WORDS + 1], 16) : w[i + WORDS];
+            const T* t = reinterpret_cast<const T*>(mine);
 #pragma unroll
             for (int j = 0; j < N; ++j) v[u * N + j] = as_float<T>(t[j]);
+        }
+    }
+    __device__ __forceinline__ void unpack(const Raw& raw, float (&v)[kEach]) const {
+        if (!SKEWED) return unpack_as<0, false>(raw, v);
+        constexpr bool H = sizeof(T) == 2;
+        switch (skew * static_cast<int>(sizeof(T)) / 2) {  // (the same for all of the CTA)
+            case 0: return unpack_as<0, false>(raw, v);
+            case 1: return unpack_as<0, H>(raw, v);
+            case 2: return unpack_as<1, false>(raw, v);
+            case 3: return unpack_as<1, H>(raw, v);
+            case 4: return unpack_as<2, false>(raw, v);
+            case 5: return unpack_as<2, H>(raw, v);
+            case 6: return unpack_as<3, false>(raw, v);
+            default: return unpack_as<3, H>(raw, v);
         }
     }
     // Any tile; -inf for what is not in the row.
@@ -167,7 +219,7 @@ struct Row {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int i = index(first, e);
-            v[e] = i >= 0 && i < V ? as_float<T>(x[i]) : -INFINITY;
+            v[e] = i < V ? as_float<T>(x[i]) : -INFINITY;
         }
     }
     // The largest of a thread's logits; of equal ones the first.
@@ -197,7 +249,7 @@ __device__ __forceinline__ float exp_sum(const float (&v)[kEach], float m) {
 
 // One piece of one row, by a CTA, what is found going to keys [K] and sums once ready() has
 // returned; kept: room for `a.room` keys in shared memory.
-template <typename T, typename Ready>
+template <typename T, bool SKEWED, typename Ready>
 __device__ __forceinline__ void take_piece(const PieceArgs& a, int row, int piece,
                                            unsigned long long* kept, unsigned long long* keys,
                                            float2* sums, Ready ready) {
@@ -208,10 +260,10 @@ __device__ __forceinline__ void take_piece(const PieceArgs& a, int row, int piec
     __shared__ int n_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = row / a.W, w = row % a.W;
-    Row<T> r;
+    Row<T, SKEWED> r;
     r.x = static_cast<const T*>(a.logits) + b * a.batch_stride + w * a.beam_stride;
     r.V = a.V;
-    r.skew = static_cast<int>((reinterpret_cast<uintptr_t>(r.x) & 15) / sizeof(T));
+    r.skew = SKEWED ? static_cast<int>((reinterpret_cast<uintptr_t>(r.x) & 15) / sizeof(T)) : 0;
     const int first = piece * a.tiles * kTile;
     if (tid == 0) n_kept = 0;
     // Keeps those of a thread's logits that exceed `above` (and reach `least`).
@@ -239,11 +291,11 @@ __device__ __forceinline__ void take_piece(const PieceArgs& a, int row, int piec
         }
     };
     float m = -INFINITY, s = 0.0f, lim = INFINITY;
-    uint4 raw[Row<T>::kVecs];
+    typename Row<T, SKEWED>::Raw raw;
     if (r.inside(first)) r.fetch(first, raw);
     for (int t = 0; t < a.tiles; ++t) {
         const int at = first + t * kTile;
-        if (at - r.skew >= a.V) break;
+        if (at >= a.V) break;
         float v[kEach];
         if (r.inside(at))
             r.unpack(raw, v);
@@ -347,7 +399,7 @@ __device__ __forceinline__ void take_piece(const PieceArgs& a, int row, int piec
     for (int i = n + tid; i < a.K; i += kThreads) keys[i] = 0;
 }
 
-template <typename T>
+template <typename T, bool SKEWED>
 __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -355,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, 4) piece_kernel(const PieceArgs a) {
     const int row = blockIdx.y, piece = blockIdx.x;
     if (a.finished != nullptr && a.finished[row] != 0) return;  // (not read for it either)
     const size_t out = static_cast<size_t>(row) * a.pieces + piece;
-    take_piece<T>(a, row, piece, reinterpret_cast<unsigned long long*>(smem), a.keys + out * a.K,
-                  a.sums + out, [] {});
+    take_piece<T, SKEWED>(a, row, piece, reinterpret_cast<unsigned long long*>(smem), a.keys + out * a.K,
+                          a.sums + out, [] {});
 }
 
 // ---------------------------------------------------------------------------
@@ -641,7 +693,7 @@ __global__ void __launch_bounds__(NT) join_kernel(const JoinArgs a) {
 // A sequence whose pieces are few, by one cluster: they leave what they find in the shared
 // memory of its first CTA, which joins them.  (A cluster's size is a power of two: CTAs
 // past the pieces have none.)
-template <typename T>
+template <typename T, bool SKEWED>
 __global__ void __launch_bounds__(kThreads, 4)
     whole_kernel(const PieceArgs a, const JoinArgs j) {
     ptx::cluster_arrive();
@@ -658,9 +710,10 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int row = b * a.W + rank / a.pieces;
     const bool has = rank < a.W * a.pieces && (a.finished == nullptr || a.finished[row] == 0);
     if (has)
-        take_piece<T>(a, row, rank % a.pieces, reinterpret_cast<unsigned long long*>(room),
-                      ptx::map_generic(keys + rank * a.K, 0), ptx::map_generic(sums + rank, 0),
-                      [] { ptx::cluster_wait(); });  // (the first CTA is there)
+        take_piece<T, SKEWED>(a, row, rank % a.pieces, reinterpret_cast<unsigned long long*>(room),
+                              ptx::map_generic(keys + rank * a.K, 0),
+                              ptx::map_generic(sums + rank, 0),
+                              [] { ptx::cluster_wait(); });  // (the first CTA is there)
     else
         ptx::cluster_wait();
     ptx::cluster_sync();
@@ -669,8 +722,8 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TREE_ATTN_OK : TREE_ATTN_ERR_CUDA; }
 
-// Tiles of a row (one more than V asks for, for rows that start inside a vector).
-int tiles_of(int V) { return (V + 7 + kTile - 1) / kTile; }
+// Tiles of a row.
+int tiles_of(int V) { return (V + kTile - 1) / kTile; }
 
 // Logits a piece keeps: those of K threads, where it comes to that.
 int piece_room(int K, int tiles) {
@@ -809,27 +862,37 @@ int tree_beam_select(const void* logits, int dtype, long long batch_stride, long
     j.room = join_room(all, K, threads);
     const size_t join_bytes = static_cast<size_t>(j.room) * sizeof(Cand);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    static std::atomic<unsigned long long> piece_ready[3], join_ready[2], whole_ready[3];
+    // Whether some row may begin inside a vector.
+    const size_t size = dtype == 2 ? 4 : 2;
+    const bool skewed = !ptr_aligned(logits, 16) || batch_stride * size % 16 != 0 ||
+                        beam_stride * size % 16 != 0;
+    static std::atomic<unsigned long long> piece_ready[2][3], join_ready[2], whole_ready[2][3];
     if (whole > 0) {
         using Kernel = void (*)(PieceArgs, JoinArgs);
-        const Kernel kernel = dtype == 2   ? whole_kernel<float>
-                              : dtype == 1 ? whole_kernel<__half>
-                                           : whole_kernel<__nv_bfloat16>;
-        if (!opt_in(reinterpret_cast<const void*>(kernel), dev, whole_ready[dtype], true))
+        static const Kernel of[2][3] = {
+            {whole_kernel<__nv_bfloat16, false>, whole_kernel<__half, false>,
+             whole_kernel<float, false>},
+            {whole_kernel<__nv_bfloat16, true>, whole_kernel<__half, true>,
+             whole_kernel<float, true>}};
+        const Kernel kernel = of[skewed][dtype];
+        if (!opt_in(reinterpret_cast<const void*>(kernel), dev, whole_ready[skewed][dtype], true))
             return TREE_ATTN_ERR_CUDA;
-        int size = 1;
-        while (size < W * pieces) size *= 2;
+        int ctas = 1;
+        while (ctas < W * pieces) ctas *= 2;
         return rc_of(launch_cluster(
-            kernel, dim3(static_cast<unsigned>(B) * size), dim3(kThreads),
-            whole_bytes(W * pieces, K) + (smem > join_bytes ? smem : join_bytes), size, s, p, j));
+            kernel, dim3(static_cast<unsigned>(B) * ctas), dim3(kThreads),
+            whole_bytes(W * pieces, K) + (smem > join_bytes ? smem : join_bytes), ctas, s, p, j));
     }
     using Kernel = void (*)(PieceArgs);
-    const Kernel kernel = dtype == 2   ? piece_kernel<float>
-                          : dtype == 1 ? piece_kernel<__half>
-                                       : piece_kernel<__nv_bfloat16>;
+    static const Kernel of[2][3] = {
+        {piece_kernel<__nv_bfloat16, false>, piece_kernel<__half, false>,
+         piece_kernel<float, false>},
+        {piece_kernel<__nv_bfloat16, true>, piece_kernel<__half, true>, piece_kernel<float, true>}};
+    const Kernel kernel = of[skewed][dtype];
     using Join = void (*)(JoinArgs);
     const Join join = threads == 256 ? join_kernel<256> : join_kernel<1024>;
-    if ((smem > 32 * 1024 && !opt_in(reinterpret_cast<const void*>(kernel), dev, piece_ready[dtype])) ||
+    if ((smem > 32 * 1024 && !opt_in(reinterpret_cast<const void*>(kernel), dev,
+                                  piece_ready[skewed][dtype])) ||
         (join_bytes > 24 * 1024 &&
          !opt_in(reinterpret_cast<const void*>(join), dev, join_ready[threads != 256])))
         return TREE_ATTN_ERR_CUDA;
