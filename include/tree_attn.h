@@ -820,7 +820,9 @@ TREE_ATTN_API int tree_select_blocks(const uint16_t *q, const int8_t *bounds,
  *                _BAD_PARENT.
  * 0 <= n_blocks <= 4096.  In the 8-bit form a query element is held to 2^-38 of its row's
  * largest or to bf16's precision, probabilities as for tree_attn_verify_fp8; with
- * a bf16 cache they enter the product as two bf16 numbers.  No workspace.
+ * a bf16 cache they enter the product as two bf16 numbers.  A value that is infinite or NaN
+ * reaches the rows that see its key, as the formula has it, and no others (an infinite one
+ * whose probability fp32 holds as 0 gives NaN).  No workspace.
  * Returns 0, -1, -2, -3, -5.
  */
 TREE_ATTN_API int tree_attn_verify_blocks(

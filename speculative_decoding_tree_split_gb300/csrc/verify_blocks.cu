@@ -333,9 +333,17 @@ __device__ __forceinline__ void load_values(uint4 (&v)[4], uint32_t at, int ch, 
     }
 }
 
+// A pair of bf16 numbers with 0 for those that are infinite.
+__device__ __forceinline__ uint32_t without_infinities(uint32_t pair) {
+    if ((pair & 0x7fffu) == 0x7f80u) pair &= 0xffff0000u;
+    if ((pair & 0x7fff0000u) == 0x7f800000u) pair &= 0xffffu;
+    return pair;
+}
+
 // O^T += V^T P^T for 16 keys of bf16 values, the probabilities as two bf16 numbers: what one leaves out (2^-9) would be the largest error before the
 // result is rounded, and the product is not what bounds the kernel.  SPREAD: a lane's
-// channels are 8 of every 64, else D / 8 in a row.
+// channels are 8 of every 64, else D / 8 in a row.  CAREFUL: an infinite value goes with
+// the first number alone, since the second may be 0 or below.
 template <bool CAREFUL, bool SPREAD, int D, bool FP8, int NT>
 __device__ __forceinline__ void add_values_bf16(State<D, FP8, NT>& st, const float (&p)[NT][4],
                                                 uint32_t v_at, int live,
@@ -367,7 +375,12 @@ __device__ __forceinline__ void add_values_bf16(State<D, FP8, NT>& st, const flo
             for (int n = 0; n < NT; ++n)
                 add_tile<CAREFUL>(st.o[n][h * 4 + w], mine[n], [&](float (&o)[4]) {
                     ptx::mma_sync_bf16(o, a0, a1, a2, a3, b[n][0][0], b[n][0][1]);
-                    ptx::mma_sync_bf16(o, a0, a1, a2, a3, b[n][1][0], b[n][1][1]);
+                    if (CAREFUL)
+                        ptx::mma_sync_bf16(o, without_infinities(a0), without_infinities(a1),
+                                           without_infinities(a2), without_infinities(a3),
+                                           b[n][1][0], b[n][1][1]);
+                    else
+                        ptx::mma_sync_bf16(o, a0, a1, a2, a3, b[n][1][0], b[n][1][1]);
                 });
         }
     }
@@ -472,10 +485,11 @@ struct Unit {
     int turn, step;  // of the tiles it takes
 };
 
-// One warp's tiles, its rows left in shared memory.  A value that is no number must not
-// reach tokens that do not see it, but a product gives it to all.  So that the tiles need
-// not look, the warp looks at what it has in the end: if that is no number, it leaves
-// nothing (false) and takes its tiles again, CAREFUL.
+// One warp's tiles, its rows left in shared memory.  A value that is no finite number must
+// not reach tokens that do not see it, but a product gives it to all, and an infinite one
+// must not meet both parts of a probability.  So that the tiles need not look, the warp
+// looks at what it has in the end: if that is not finite, it leaves nothing (false) and
+// takes its tiles again, CAREFUL.
 template <int D, bool FP8, int NT, bool CAREFUL>
 __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, const Unit& u) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -695,7 +709,7 @@ __device__ __forceinline__ bool warp_rows(const Args& a, Smem<D, FP8, NT>& sm, c
             }
         }
     }
-    if (!CAREFUL && u.nt > 1 && not_finite(st)) return false;
+    if (!CAREFUL && not_finite(st)) return false;
 
     // ---- this warp's rows to shared memory, where its ring was
     copies_wait<0>();
