@@ -972,7 +972,9 @@ int tree_select_blocks(const uint16_t* q, const int8_t* bounds, const uint8_t* b
         a.per_most = ((max_pages_per_seq + S - 1) / S + 3) / 4 * 4;
         need = static_cast<size_t>(TC) * a.per_most * 4 + kSelWarps * sizeof(Scratch) +
                static_cast<size_t>(padded_tiles(TC * a.cols) * 8) * code_row;
-        if (need <= (TC == 1 ? 200u * 1024u : 72u * 1024u)) break;  // (three CTAs to an SM)
+        // (72 KB: three CTAs to an SM; 227 KB: all that a CTA can have, which the widest tables
+        // with 97 heads and more to a group take)
+        if (need <= (TC > 1 ? 72u * 1024u : S < 8 ? 200u * 1024u : 227u * 1024u)) break;
         if (TC == 1) {  // one token of a very long sequence: more CTAs share its pages
             if (S == 8) return TREE_ATTN_ERR_SHAPE;
             S *= 2;
