@@ -837,6 +837,10 @@ __global__ void __launch_bounds__(kThreads, kResident)
         n_entries = 0;
         uint32_t* marks = sm.marks();  // and behind them the pages' rows
         int* row_at = reinterpret_cast<int*>(marks + kWindow / 2);
+        if (nb == 0) {  // (no window looks at the lists then)
+            for (int i = tid; i < n_listed; i += kThreads)
+                if (listed(i) != -1) report(a.status, TREE_ATTN_STATUS_BAD_PAGE);
+        }
         for (int w0 = 0; w0 < nb; w0 += kWindow) {
             const int width = min(kWindow, nb - w0);
             __syncthreads();
