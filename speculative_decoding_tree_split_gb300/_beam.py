@@ -6,7 +6,7 @@ from typing import Optional, Tuple
 import torch
 
 from ._pages import _workspace
-from ._serving import _DEVICES, _F32, _I32, _NOT_SO, _Place, _device_of, _tensor
+from ._serving import _DEVICES, _F32, _I32, _NOT_SO, _Place, _device_of, _int32, _tensor
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _FLAGS = (torch.bool, torch.uint8)
@@ -69,8 +69,11 @@ def beam_select(logits, scores, n_select: int, *, finished=None, eos: Optional[i
         _check(logits, scores, finished, dev)
         B, W, V = logits.shape
         bs, ws, _ = logits.stride()
-    if finished is not None and eos is None:
+    if finished is None:
+        eos = -1
+    elif eos is None:
         raise ValueError("finished beams need eos")
+    _int32(k, eos)
     at = _Place(dev, stream)
     if scores_out is None and rows_out is None and tokens_out is None and at.stream is None and k > 0:
         d = _DEVICES[dev]
@@ -84,7 +87,7 @@ def beam_select(logits, scores, n_select: int, *, finished=None, eos: Optional[i
     workspace = _workspace(workspace, at, "tree_beam_workspace_size", B, W, V, k)
     at.run("tree_beam_select", logits.data_ptr(), _DTYPES[logits.dtype], bs if B > 1 else 0,
            ws if W > 1 else 0, scores.data_ptr(),
-           None if finished is None else finished.data_ptr(), -1 if eos is None else int(eos),
+           None if finished is None else finished.data_ptr(), int(eos),
            scores_out.data_ptr(), rows_out.data_ptr(), tokens_out.data_ptr(), B, W, V, k,
            None if workspace is None else workspace.data_ptr(),
            0 if workspace is None else workspace.numel())

@@ -10,7 +10,7 @@ import torch
 
 from ._lib import _BITS64
 from ._serving import (_BF16, _CODES, _DEVICES, _F32, _I32, _NOT_SO, _U8, _Place, _device_of,
-                       _status, _tensor, _vector)
+                       _int32, _status, _tensor, _vector)
 
 _I8 = torch.int8
 
@@ -126,6 +126,7 @@ def select_blocks(q, bounds, bounds_exp, block_table, seq_lens, n_select: int, p
             raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
         _vector(seq_lens, "seq_lens", B, dev)
         width = block_table.shape[1]
+    _int32(k, page_size, n_first, n_last)
     at = _Place(dev, stream)
     if out is None and at.stream is None and k > 0:
         out = torch.empty((B, T, H, k), dtype=_I32, device=_DEVICES[dev])

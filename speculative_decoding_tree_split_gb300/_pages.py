@@ -13,8 +13,8 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from ._serving import (_DEVICES, _I32, _NOT_SO, _U8, _Place, _device_of, _status, _tensor,
-                       _vector)
+from ._serving import (_DEVICES, _I32, _NOT_SO, _U8, _Place, _device_of, _int32, _status,
+                       _tensor, _vector)
 
 
 def _check_pools(pools, num_pages: Optional[int], dev: int):
@@ -145,6 +145,7 @@ def kv_fork(pools, block_table, seq_lens, page_refs, src, page_size: int, *, res
     else:
         _vector(reserve, "reserve", n, dev)
         each = reserve.data_ptr()
+    _int32(page_size, more)
     ptrs, sizes, n_pools, _ = _pool_args(pools, num_pages, dev)
     at = _Place(dev, stream)
     table = _out(block_table_out, "block_table_out", block_table, (n, width), at)

@@ -48,6 +48,13 @@ def _tensor(t, name: str, dtypes, ndim: int, dev: int, dense: bool = True):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _int32(*numbers: int) -> None:
+    """Refuses what 32 bits do not hold (the call would take its last 32)."""
+    for x in numbers:
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{x} does not fit 32 bits")
+
+
 def _device_of(t, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
