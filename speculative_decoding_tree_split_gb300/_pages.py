@@ -48,7 +48,8 @@ def _pool_args(pools: Sequence[torch.Tensor], num_pages: Optional[int], dev: int
     raise ValueError("pools must be a sequence of tensors of the same number of pages")
 
 
-_SIZES: dict = {}  # workspace bytes, by function and sizes
+_SIZES: dict = {}  # workspace bytes, by function and sizes: the last few hundred asked for
+_SIZES_MOST = 256
 
 
 def _workspace(given, at: _Place, name: str, *sizes: int) -> Optional[torch.Tensor]:
@@ -59,7 +60,10 @@ def _workspace(given, at: _Place, name: str, *sizes: int) -> Optional[torch.Tens
         return given
     need = _SIZES.get((name, sizes))
     if need is None:
-        need = _SIZES[name, sizes] = at.call(name, *sizes)
+        need = at.call(name, *sizes)
+        if len(_SIZES) >= _SIZES_MOST:
+            _SIZES.clear()
+        _SIZES[name, sizes] = need
     if need == 0:
         return None
     if at.stream is None:
