@@ -56,10 +56,12 @@ constexpr int kFixed = 8;
 // one the scale of a key's value joins its exponent, e = x + s, p = 2^(e - reference): o
 // sums p times the value's codes, the row's sum takes p 2^-s.  So a large scale costs only
 // rows that see it, and those no more than their own largest p max|v| says.  p goes to
-// the product as fp16 and may reach 2^kMost; a new reference, a whole number so that s less
-// it is exact, leaves the largest at 2^kFresh or above.
+// the product as fp16 and may reach 2^kMost; a new reference leaves the largest at
+// 2^kFresh, or as near as fp16 does not tell apart: a key that has most of its row is then
+// rounded by less than 2^-15, not 2^-12.  (A reference is a multiple of 1 / kGrid, so that
+// s less it is exact.)
 constexpr float kMove = 8.0f;
-constexpr float kMost = 15.0f, kFresh = 7.0f;
+constexpr float kMost = 15.0f, kFresh = 7.0f, kGrid = 16384.0f;
 constexpr float kLeast = 1.17549435e-38f;  // of a score unit: never 0, which would lose -inf
 constexpr float kLow = -3.0e38f; // a reference before the first key
 
@@ -156,6 +158,11 @@ struct State {
     }
 };
 
+// The multiple of 1 / kGrid nearest to t; t itself where fp32 has few finer steps or none.
+__device__ __forceinline__ float on_grid(float t) {
+    return fabsf(t) < 1024.0f ? rintf(t * kGrid) * (1.0f / kGrid) : t;
+}
+
 // Scores to probabilities (in place), summed; the references are moved where one is
 // exceeded by too much.
 template <int D, bool FP8, int NT>
@@ -180,7 +187,7 @@ __device__ __forceinline__ void exponents(State<D, FP8, NT>& st, float (&x)[NT][
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     t = fmaxf(t, __shfl_xor_sync(kFull, t, off));
-                t = fmaxf(FP8 ? floorf(t) - kFresh : t * st.factor(n, i), st.m[n][i]);
+                t = fmaxf(FP8 ? on_grid(t) - kFresh : t * st.factor(n, i), st.m[n][i]);
                 f[i] = ex2(st.m[n][i] - t);
                 st.m[n][i] = t;
                 st.l[n][i] *= f[i];
