@@ -711,7 +711,8 @@ TREE_ATTN_API int tree_kv_fork(void *const *pools, const size_t *page_bytes, int
  *                    where that is 0: for 2048 pages and fewer)
  *   status           nullable: TREE_ATTN_STATUS_BAD_PAGE (an entry without a used
  *                    page becomes -1).
- * Sizes, n_pools = 0 and return codes as tree_kv_fork.
+ * Pages that the caller holds beside the table move like all others: give them a row of
+ * it.  Sizes, n_pools = 0 and return codes as tree_kv_fork.
  */
 TREE_ATTN_API size_t tree_kv_compact_workspace_size(int num_pages);
 
@@ -729,7 +730,7 @@ TREE_ATTN_API int tree_kv_compact(void *const *pools, const size_t *page_bytes, 
  *   logits       [B][W][V] of type `dtype` (0 bf16, 1 fp16, 2 fp32); batch and
  *                beam strides in elements, not negative, the V logits contiguous.
  *                NaN and -inf are no candidates; where some are +inf, those share
-                the beam's whole probability.
+ *                the beam's whole probability.
  *   scores       fp32 [B][W]; a beam at -inf or NaN has no candidates
  *   finished     nullable uint8 [B][W]: a non-zero beam's only candidate is (w,
  *                eos) with its score unchanged (its logits are not read)
@@ -788,7 +789,9 @@ TREE_ATTN_API int tree_kv_block_bounds(const void *k_pages, const uint8_t *k_sca
  * codes c = rint(q * 2^-f) in [-127, 127], f the smallest integer of [-100, 100] with
  * max|q| <= 127 * 2^f over the group's finite values (NaN is 0), a page scores
  *   2^e * max over the group's heads of sum_i max(c_i * hi_i, c_i * lo_i),
- * a whole number times a power of two, so that the choice is exact.  The first
+ * a whole number times a power of two, so that the choice is exact.  (The codes of the
+ * queries are rounded to nearest, so a score bounds the codes' products with a page's keys,
+ * those of the queries themselves to half a code.)  The first
  * n_first and the last n_last pages of a sequence are always taken; ties go to
  * the lowest page.
  *   q            bf16 [B][T][Hq][d]; bounds, bounds_exp as above

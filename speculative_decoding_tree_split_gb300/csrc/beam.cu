@@ -733,10 +733,12 @@ int piece_room(int K, int tiles) {
 
 // Tiles of a piece: those that take the least time when the SMs take the pieces in waves
 // of four to an SM, a piece taking as long as its tiles and two more (measured, a warp's
-// instructions: 203 to a tile and 264 to a piece; 256 rows of 50257 logits in bf16: 13
-// pieces of one tile 25 us, two of seven 14).  Pieces of fp32 are bound by memory and end
-// at eight tiles, of which more then fit between the last (512 rows of 128000: 52 us with
-// eight, 56 with sixteen).
+// instructions: about 200 to a tile and 264 to a piece; 256 rows of 50256 logits in bf16: 13
+// pieces of one tile 22 us, two of seven 15).  Both types are bound by the rate of
+// instructions (two a clock of an SM) and the wait for loads, DRAM at 59 % in fp32.  Pieces
+// of fp32 end at eight tiles, of which more then fit between the last where finished beams
+// leave gaps: 512 rows of 128000, a fifth of them finished, 47 us with eight and 50
+// with sixteen (none finished: 56 and 53).
 int piece_tiles(long long rows, int V, int K, int sms, bool fp32) {
     const int all = tiles_of(V), most = fp32 ? kMostTiles / 2 : kMostTiles;
     int best = 1;

@@ -10,7 +10,7 @@
 //
 // A plan is a few KB to a few MB of integers with four dependent phases: one
 // cluster of CTAs runs them with hardware barriers in between, in one launch; it is
-// bound by their latency (about 8 us from cold caches).  The copies, with the new table
+// bound by their latency (9 to 14 us from cold caches).  The copies, with the new table
 // made beside them, are bound by memory traffic (515 MB moved in 77 us, 6.7 TB/s).
 #include <cuda_runtime.h>
 
@@ -701,9 +701,10 @@ __global__ void __launch_bounds__(kCopyThreads, 4)
     });
 }
 
-// Fork, of few rows and pages: the last CTA also keeps the counts, in shared memory (16 rows
-// of 128 pages: 6.3 us, with a plan of its own 8.4 to 10.4; of 2048 pages 14.5 and 18.6; 32
-// rows of 128 pages 10.4 either way, of 2048 pages 24.7 and 20.5).
+// Fork, of few rows and pages: the last CTA also keeps the counts, in shared memory.  Against
+// a plan of its own, three runs of each, 2048 pages in all: 16 rows with tables of 128
+// entries 7.0 to 8.3 us and 8.4 to 10.4, of 2048 entries 14.5 and 18.6; 32 rows of 64 entries
+// 12.3 and 10.4, of 128 entries 10.4 to 10.8 and 10.4, of 2048 entries 24.7 and 20.6.
 constexpr int kFewRows = 16;
 
 struct FewRows {

@@ -19,10 +19,10 @@
 // put together by byte permutes, P turns from result to operand by movmatrix.
 //
 // Measured, 64 sequences of 512 to 16384 tokens, 32 heads on 8 of 128, 32 pages of 64
-// tokens: one token bf16 81 us (6.0 TB/s), 8-bit 54 (4.5 TB/s); four tokens with lists of
-// their own, 8-bit, 428 MB, 105 us (4.1 TB/s).  The bf16 form is bound by memory, the
-// 8-bit one by the rate of instructions: 490 to a tile of 16 keys and 16 rows, most of
-// them conversions of codes, at 2.1 a clock of an SM, whose registers hold two CTAs.
+// tokens: one token bf16 82 us (5.9 TB/s), 8-bit 53 (4.6 TB/s); four tokens with lists of
+// their own, bf16 150 (5.6 TB/s), 8-bit, 428 MB, 98 (4.4 TB/s).  The bf16 form is bound by
+// memory, the 8-bit one by the rate of instructions: 475 to a tile of 16 keys and 16 rows,
+// most of them conversions of codes, at 2.1 a clock of an SM, whose registers hold two CTAs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
