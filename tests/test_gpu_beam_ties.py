@@ -84,3 +84,22 @@ def test_largest_logits_with_one_thread_and_numbers_beside_the_rows(dtype, skip)
         want = context.beams(y[b].cpu(), scores[b].cpu(), None, None, 40)
         assert got[1][b].tolist() == [b * 3 + w for _, w, _ in want]
         assert got[2][b].tolist() == [v for _, _, v in want]
+
+
+def test_the_most_candidates():
+    """W, K and V at their joint limit, and one token past it."""
+    W = k = 64
+    V = 131072
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.randn(1, W, V, generator=g, device="cuda")
+    s = -torch.rand(1, W, generator=g, device="cuda")
+    got, rows, tokens = ta.beam_select(x, s, k)
+    y = torch.log_softmax(x[0].double(), -1) + s[0].double()[:, None]
+    best, at = torch.sort(y.view(-1), descending=True, stable=True)
+    assert float((got[0].double() - best[:k]).abs().max()) <= 2.0 ** -20 + 2.0 ** -23 * float(
+        best[:k].abs().max())
+    mine = y[rows[0].long(), tokens[0].long()]
+    # (order to the rounding of the sums)
+    assert float((mine - best[:k]).abs().max()) <= 2.0 ** -20
+    with pytest.raises(ta.TreeAttnError):
+        ta.beam_select(torch.zeros(1, W, V + 1, device="cuda"), s, k)
